@@ -41,7 +41,8 @@
  *   - Calls are asynchronous on `stream` (NULL = legacy default stream).
  *     Argument errors are found on the host and returned before any launch.
  *     Errors that only the device can see (malformed cu_seqlens, a bounded
- *     wait that ran out) are recorded in a per-device error word; the
+ *     wait that ran out, a state slot outside its cache) are recorded in a
+ *     per-device error word; the
  *     affected blocks write nothing.  Read and clear it with
  *     gdn_get_last_device_error().
  *   - Results are deterministic: the same inputs give bitwise-identical
@@ -74,7 +75,8 @@ typedef enum {
     GDN_ERR_MISALIGNED = 3,    /* a tensor pointer is not 16-byte aligned */
     GDN_ERR_BAD_SEQLENS = 4,   /* device found cu_seqlens not 0 .. T non-decreasing */
     GDN_ERR_TIMEOUT = 5,       /* device: a bounded wait gave up (kernel returned early) */
-    GDN_ERR_CUDA = 6           /* a CUDA runtime call failed (launch, sync, copy) */
+    GDN_ERR_CUDA = 6,          /* a CUDA runtime call failed (launch, sync, copy) */
+    GDN_ERR_BAD_SLOT = 7       /* device found a state slot outside the cache */
 } gdn_status;
 
 /* Chunk length used by the library (tokens per chunk). */
@@ -337,8 +339,8 @@ GDN_API gdn_status gdn_chunk_bwd_saved(const gdn_bf16* q, const gdn_bf16* k, con
 
 /*
  * Synchronises `stream`, then returns and clears the device error word of
- * the current device: GDN_OK, GDN_ERR_BAD_SEQLENS or GDN_ERR_TIMEOUT
- * (GDN_ERR_CUDA if the synchronisation or the read itself failed).
+ * the current device: GDN_OK, GDN_ERR_BAD_SEQLENS, GDN_ERR_TIMEOUT or
+ * GDN_ERR_BAD_SLOT (GDN_ERR_CUDA if the synchronisation or the read itself failed).
  * The word is one per device, not one per stream: with library calls in
  * flight on several streams of the same device, the code returned (and
  * cleared) may come from another stream's call.  Callers that need to tell
@@ -476,6 +478,140 @@ GDN_API gdn_status gdn_chunk_bwd_saved_wait_limit(const gdn_bf16* q, const gdn_b
                                           const void* saved, size_t saved_bytes,
                                           void* workspace, size_t workspace_bytes, uint32_t wait_limit,
                                           int stall_first_wait, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Mixer operators: what stands around the delta rule in a layer, and the
+ * diagonal state space recurrence that uses the same neighbours.
+ *
+ * Conventions beyond those above.  Activations are bf16 or fp32 (`dtype`),
+ * channels last: (B, T, C), or packed (1, T, C) with cu_seqlens and N = B
+ * sequences.  Every parameter and every state of the scan is fp32.  An
+ * activation input marked (strided) may be a slice of a wider tensor: rows
+ * `*_stride` elements apart (at least the row's own length; batch rows T rows
+ * apart), each row dense, the address aligned to its element only.  Everything
+ * else is dense and 16-byte aligned.  Widths and strides that 16-byte accesses
+ * cannot take are read in narrower ones.  All arithmetic is fp32, rounded once
+ * on output; sums run in a fixed order (no atomics).  T <= 2^30, D <= 65536,
+ * B <= 65535; outputs must not overlap inputs except where said.
+ * ------------------------------------------------------------------------ */
+typedef enum { GDN_BF16 = 0, GDN_F32 = 1 } gdn_dtype;
+typedef enum { GDN_ACT_NONE = 0, GDN_ACT_SILU = 1, GDN_ACT_SIGMOID = 2 } gdn_activation;
+
+/*
+ * Short causal convolution per channel ("Research Sprint Day 2 - Rooflines",
+ * GDN layer pseudocode: the convolution and SiLU on q, k and v), W in {2, 3, 4}:
+ *     y_t = act(bias + sum_{j < W} weight[:, j] x_{t - (W-1) + j})
+ *   x             (B,T,D) (strided)          weight (D,W)   bias (D) or NULL
+ *   initial_state (N,W-1,D), the inputs before each sequence, oldest first, or
+ *                 NULL (zeros); in x's dtype
+ *   y             (B,T,D)
+ *   final_state   (N,W-1,D) or NULL: the last W-1 inputs (of initial_state
+ *                 where a sequence is shorter); not initial_state's memory
+ *   activation    GDN_ACT_NONE or GDN_ACT_SILU
+ */
+GDN_API gdn_status gdn_conv_fwd(const void* x, int64_t x_stride, const float* weight, const float* bias,
+                                const void* initial_state, const int32_t* cu_seqlens, void* y, void* final_state,
+                                int B, int T, int D, int W, int activation, int dtype, cudaStream_t stream);
+
+/* Bytes of workspace gdn_conv_bwd needs (partial weight gradients). */
+GDN_API size_t gdn_conv_bwd_workspace_size(int B, int T, int D, int W, int varlen);
+
+/*
+ * Reverse mode of gdn_conv_fwd (the pre-activation is recomputed).  d_out
+ * (B,T,D) and d_final_state (N,W-1,D) or NULL in; dx (B,T,D), dweight (D,W),
+ * dbias (D) or NULL and d_initial_state (N,W-1,D) or NULL out.
+ */
+GDN_API gdn_status gdn_conv_bwd(const void* x, int64_t x_stride, const float* weight, const float* bias,
+                                const void* initial_state, const int32_t* cu_seqlens, const void* d_out,
+                                const void* d_final_state, void* dx, float* dweight, float* dbias,
+                                void* d_initial_state, int B, int T, int D, int W, int activation, int dtype,
+                                void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * One token per row, for decode: y (B,D) from x (B,D) (strided) and `state`
+ * (S,W-1,D), whose rows move up by one into out_state (may be `state`).
+ *   slots   NULL (row b uses state row b; S >= B) or device int32 (B): the
+ *           state row of each batch row.  A negative slot is an idle row: y is
+ *           zero and no state changes.  A slot >= S records GDN_ERR_BAD_SLOT
+ *           and is treated as idle.  Two rows of one call may not share a slot.
+ */
+GDN_API gdn_status gdn_conv_step(const void* x, int64_t x_stride, const float* weight, const float* bias,
+                                 const void* state, void* out_state, const int32_t* slots, void* y, int B, int S,
+                                 int D, int W, int activation, int dtype, cudaStream_t stream);
+
+/*
+ * Selective state space scan: per channel d of group g(d) = d / (D / G), with N
+ * states,
+ *     dt  = softplus(dt + dt_bias) if dt_softplus, else dt + dt_bias
+ *     h_n <- exp(dt A[d,n]) h_n + dt u B[g,n]
+ *     y   = sum_n C[g,n] h_n + D_skip u;    out = y silu(z)   (y without z)
+ *   u, dt, z      (B,T,D) (strided); z may be NULL (no gate)
+ *   A             (D,N), documented domain A <= 0;  D_skip, dt_bias (D) or NULL
+ *   Bm, Cm        (B,T,G,N) (strided, a row being G*N);  D a multiple of G
+ *   initial_state (nseq,D,N) or NULL;  final_state (nseq,D,N) or NULL
+ *   out           (B,T,D)
+ *   saved         NULL, or gdn_ssm_saved_size() bytes that the backward reads:
+ *                 the state before every 16 tokens
+ *   N in {8, 16, 32, 64, 128}
+ */
+GDN_API size_t gdn_ssm_saved_size(int B, int T, int D, int N, int varlen);
+GDN_API size_t gdn_ssm_fwd_workspace_size(int B, int T, int D, int G, int N, int varlen);
+GDN_API gdn_status gdn_ssm_fwd(const void* u, int64_t u_stride, const void* dt, int64_t dt_stride, const float* A,
+                               const void* Bm, int64_t B_stride, const void* Cm, int64_t C_stride,
+                               const float* D_skip, const void* z, int64_t z_stride, const float* dt_bias,
+                               int dt_softplus, const float* initial_state, const int32_t* cu_seqlens, void* out,
+                               float* final_state, void* saved, size_t saved_bytes, int B, int T, int D, int G, int N,
+                               int dtype, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Reverse mode of gdn_ssm_fwd from the same inputs and the `saved` buffer it
+ * filled.  d_out (B,T,D) and d_final_state (nseq,D,N) or NULL in; du, ddt, dz
+ * (B,T,D; dz exactly when z is given), dB, dC (B,T,G,N), dA (D,N), dD and
+ * ddt_bias (D, each may be NULL), d_initial_state (nseq,D,N) or NULL out.
+ */
+GDN_API size_t gdn_ssm_bwd_workspace_size(int B, int T, int D, int G, int N, int varlen);
+GDN_API gdn_status gdn_ssm_bwd(const void* u, int64_t u_stride, const void* dt, int64_t dt_stride, const float* A,
+                               const void* Bm, int64_t B_stride, const void* Cm, int64_t C_stride,
+                               const float* D_skip, const void* z, int64_t z_stride, const float* dt_bias,
+                               int dt_softplus, const int32_t* cu_seqlens, const void* d_out,
+                               const float* d_final_state, const void* saved, size_t saved_bytes, void* du, void* ddt,
+                               void* dz, void* dB, void* dC, float* dA, float* dD, float* ddt_bias,
+                               float* d_initial_state, int B, int T, int D, int G, int N, int dtype, void* workspace,
+                               size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * One token per row, for decode: u, dt, z, out (B,D), Bm, Cm (B,G,N), the
+ * state (S,D,N) into out_state (may be `state`); slots as in gdn_conv_step.
+ */
+GDN_API gdn_status gdn_ssm_step(const void* u, int64_t u_stride, const void* dt, int64_t dt_stride, const float* A,
+                                const void* Bm, int64_t B_stride, const void* Cm, int64_t C_stride,
+                                const float* D_skip, const void* z, int64_t z_stride, const float* dt_bias,
+                                int dt_softplus, const float* state, float* out_state, const int32_t* slots,
+                                void* out, int B, int S, int D, int G, int N, int dtype, cudaStream_t stream);
+
+/*
+ * Group norm with an activation ("Research Sprint Day 2 - Rooflines", GDN layer
+ * pseudocode: RMSNorm of the output times SiLU of the gate), rows of C channels
+ * in `groups` equal groups of at most 8192:
+ *     x' = x act(gate) if gate_first, else x
+ *     v  = (x' - m) (mean((x' - m)^2) + eps)^-1/2 weight + bias,
+ *          m = mean(x') if center, else 0 (RMS norm), means over the group
+ *     y  = v act(gate) | v (gate_first) | act(v) (no gate)
+ *   x, gate (rows,C) (strided), gate may be NULL;  weight, bias (C) or NULL
+ */
+GDN_API gdn_status gdn_norm_fwd(const void* x, int64_t x_stride, const void* gate, int64_t gate_stride,
+                                const float* weight, const float* bias, void* y, int64_t rows, int C, int groups,
+                                float eps, int activation, int center, int gate_first, int dtype, cudaStream_t stream);
+
+/* Reverse mode of gdn_norm_fwd: d_out (rows,C) in; dx, dgate (rows,C; dgate
+ * exactly when gate is given), dweight and dbias (C; each exactly when its
+ * parameter is given) out. */
+GDN_API size_t gdn_norm_bwd_workspace_size(int64_t rows, int C, int groups, int dtype);
+GDN_API gdn_status gdn_norm_bwd(const void* x, int64_t x_stride, const void* gate, int64_t gate_stride,
+                                const float* weight, const float* bias, const void* d_out, void* dx, void* dgate,
+                                float* dweight, float* dbias, int64_t rows, int C, int groups, float eps,
+                                int activation, int center, int gate_first, int dtype, void* workspace,
+                                size_t workspace_bytes, cudaStream_t stream);
 
 /*
  * Number of CUDA kernels this library has launched in this process so far

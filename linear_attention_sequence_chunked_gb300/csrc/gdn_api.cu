@@ -310,6 +310,11 @@ gdn_status recurrent(const gdn_bf16* q, const gdn_bf16* k, const gdn_bf16* v, co
 
 }  // namespace
 
+namespace gdn {
+int* device_error_word() { return error_word(); }
+bool count_launch(cudaError_t e, int kernels) { return launched(e, kernels); }
+}  // namespace gdn
+
 extern "C" {
 
 const char* gdn_status_string(gdn_status status) {
@@ -321,6 +326,7 @@ const char* gdn_status_string(gdn_status status) {
         case GDN_ERR_BAD_SEQLENS: return "GDN_ERR_BAD_SEQLENS: malformed cu_seqlens";
         case GDN_ERR_TIMEOUT: return "GDN_ERR_TIMEOUT: a bounded device wait gave up";
         case GDN_ERR_CUDA: return "GDN_ERR_CUDA: CUDA runtime error";
+        case GDN_ERR_BAD_SLOT: return "GDN_ERR_BAD_SLOT: a state slot outside the cache";
     }
     return "GDN_ERR_UNKNOWN";
 }

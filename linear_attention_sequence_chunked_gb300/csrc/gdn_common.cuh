@@ -33,6 +33,7 @@ constexpr int kChunk = 64;
 // Codes written to the per-device error word (match gdn_status values).
 constexpr int kErrBadSeqlens = 4;
 constexpr int kErrTimeout = 5;
+constexpr int kErrBadSlot = 7;
 
 __device__ __forceinline__ float bf16_to_f32(uint16_t b) {
     return __uint_as_float(static_cast<uint32_t>(b) << 16);

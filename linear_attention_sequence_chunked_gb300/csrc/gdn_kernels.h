@@ -317,4 +317,153 @@ cudaError_t launch_fwd_ws(const FwdArgs& a, uint32_t wait_limit, cudaStream_t st
 cudaError_t launch_fwd_ws_f32(const FwdArgs& a, uint32_t wait_limit, cudaStream_t stream);
 constexpr uint32_t kDefaultWaitLimit = 4000000u;
 
+// ---------------------------------------------------------------------------
+// Mixer operators (activations bf16, dtype 0, or fp32, dtype 1; void* below)
+// ---------------------------------------------------------------------------
+
+// Short causal convolution.  Rows of x are x_stride elements apart; everything
+// else is dense.  slots: time blocks of tb tokens (find_block).
+struct ConvArgs {
+    const void* x;
+    long long x_stride;
+    const float* weight;          // (D, W)
+    const float* bias;            // (D) or null
+    const void* initial_state;    // (N, W - 1, D) or null
+    const int32_t* cu_seqlens;
+    void* y;                      // forward
+    void* final_state;            // (N, W - 1, D) or null
+    const void* d_out;            // backward, from here
+    const void* d_final_state;    // (N, W - 1, D) or null
+    void* dx;
+    void* d_initial_state;        // (N, W - 1, D) or null
+    float* partial;               // [conv_partial_rows(slots)][W + 1][D]
+    int N, T, D, W;
+    int activation;               // 0 none, 1 SiLU
+    int dtype;
+    int tb;
+    long long slots;
+    int* err;
+};
+struct ConvStepArgs {
+    const void* x;                // (B, D), rows x_stride apart
+    long long x_stride;
+    const float* weight;
+    const float* bias;
+    const void* state;            // (S, W - 1, D)
+    void* out_state;              // may be `state`
+    const int32_t* slots;         // (B) rows of the state, or null (row b)
+    void* y;                      // (B, D)
+    int B, S, D, W, activation, dtype;
+    int* err;
+};
+int conv_block_tokens(int B, int T, int D, int backward);
+long long conv_partial_rows(long long slots);
+cudaError_t launch_conv_fwd(const ConvArgs& a, cudaStream_t stream);
+cudaError_t launch_conv_bwd(const ConvArgs& a, cudaStream_t stream);
+cudaError_t launch_conv_step(const ConvStepArgs& a, cudaStream_t stream);
+
+// Column sums of partial[rows][stride], of its first cols columns, in a fixed order: the first c0 columns to
+// out[0], the next c1 to out[1], the rest to out[2] (null: dropped).  W > 0:
+// cols = (W + 1) c1, out[0] is (c1, W) and out[1] (c1).
+struct ColumnSumArgs {
+    const float* partial;
+    long long stride, cols, c0, c1;
+    int rows, W;
+    float* out[3];
+};
+cudaError_t launch_column_sum(const ColumnSumArgs& a, cudaStream_t stream);
+
+// Selective state space scan.
+struct SsmArgs {
+    const void* u;                // (rows, D), rows u_stride apart; dt, z likewise
+    const void* dt;
+    const void* z;                // or null
+    const void* Bm;               // (rows, G, N), rows B_stride apart, a row dense; Cm likewise
+    const void* Cm;
+    long long u_stride, dt_stride, z_stride, B_stride, C_stride;
+    const float* A;               // (D, N)
+    const float* D_skip;          // (D) or null
+    const float* dt_bias;         // (D) or null
+    int softplus;
+    const float* initial_state;   // (nseq, D, N) or null
+    const int32_t* cu_seqlens;
+    void* out;                    // forward
+    float* final_state;           // (nseq, D, N) or null
+    float* saved;                 // chunk start states [slot][D][N]; written by the forward (or null), read by the backward
+    const void* d_out;            // backward, from here
+    const float* d_final_state;   // (nseq, D, N) or null
+    void* du;
+    void* ddt;
+    void* dz;
+    float* d_initial_state;       // (nseq, D, N) or null
+    float* bc_part;               // [channel blocks][rows][2 N]
+    float* par_part;              // [nseq][ssm_par_stride]: dA (D N), dD (D), ddt_bias (D)
+    int nseq, T, D, G, N, dtype;
+    int* err;
+};
+struct SsmStepArgs {
+    const void* u;
+    const void* dt;
+    const void* z;
+    const void* Bm;
+    const void* Cm;
+    long long u_stride, dt_stride, z_stride, B_stride, C_stride;
+    const float* A;
+    const float* D_skip;
+    const float* dt_bias;
+    int softplus;
+    const float* state;           // (S, D, N)
+    float* out_state;             // may be `state`
+    const int32_t* slots;         // (B) rows of the state, or null
+    void* out;                    // (B, D)
+    int B, S, D, G, N, dtype;
+    int* err;
+};
+// dB and dC from the channel blocks' partial sums
+struct SsmBcArgs {
+    const float* bc_part;
+    void* dB;
+    void* dC;
+    long long rows;
+    int G, N, blocks;             // blocks per group
+    int dtype;
+};
+constexpr int kSsmChunk = 16;
+// a partial row's length, so that every row's dA takes 16-byte stores
+__host__ __device__ inline long long ssm_par_stride(int D, int N) { return (static_cast<long long>(D) * (N + 2) + 3) / 4 * 4; }
+int ssm_group_blocks(int D, int G, int N);  // channel blocks of the backward, per group
+cudaError_t launch_ssm_fwd(const SsmArgs& a, cudaStream_t stream);
+cudaError_t launch_ssm_bwd(const SsmArgs& a, cudaStream_t stream);
+cudaError_t launch_ssm_bc(const SsmBcArgs& a, cudaStream_t stream);
+cudaError_t launch_ssm_step(const SsmStepArgs& a, cudaStream_t stream);
+
+// Group norm with an activation, rows of C channels.
+struct NormArgs {
+    const void* x;                // (rows, C), rows x_stride apart
+    const void* gate;             // (rows, C), rows gate_stride apart, or null
+    long long x_stride, gate_stride;
+    const float* weight;          // (C) or null
+    const float* bias;            // (C) or null
+    void* y;                      // forward
+    const void* d_out;            // backward, from here
+    void* dx;
+    void* dgate;
+    float* partial;               // [teams][C] for dweight, then as much for dbias; or null
+    long long rows;
+    int C, groups;
+    float eps;
+    int activation;               // 0 none, 1 SiLU, 2 sigmoid
+    int center, gate_first;
+    int dtype;
+};
+int norm_partial_rows(long long rows, int C, int groups, int dtype);
+constexpr int kNormMaxGroup = 8192;
+cudaError_t launch_norm_fwd(const NormArgs& a, cudaStream_t stream);
+cudaError_t launch_norm_bwd(const NormArgs& a, cudaStream_t stream);
+
+// The library's per-device error word and its count of launched kernels
+// (gdn_api.cu), for the other files of the C ABI.
+int* device_error_word();
+bool count_launch(cudaError_t e, int kernels = 1);
+
 }  // namespace gdn

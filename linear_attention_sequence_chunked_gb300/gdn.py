@@ -26,6 +26,7 @@ GDN_OK = 0
 STATUS_NAMES = {
     0: "GDN_OK", 1: "GDN_ERR_INVALID_ARG", 2: "GDN_ERR_UNSUPPORTED", 3: "GDN_ERR_MISALIGNED",
     4: "GDN_ERR_BAD_SEQLENS", 5: "GDN_ERR_TIMEOUT", 6: "GDN_ERR_CUDA",
+    7: "GDN_ERR_BAD_SLOT",
 }
 HEADER = os.path.join(_build.ROOT, "include", "gdn.h")
 
@@ -109,6 +110,35 @@ def load():
         lib.gdn_chunk_bwd_noalloc.restype = i
         lib.gdn_chunk_fwd_wait_limit.argtypes = [vp] * 5 + [f] + [vp] * 4 + [i] * 5 + [vp, sz, ctypes.c_uint32, i, vp]
         lib.gdn_chunk_fwd_wait_limit.restype = i
+        i64 = ctypes.c_int64
+        row = [vp, i64]  # an activation and the distance of its rows
+        lib.gdn_conv_fwd.argtypes = row + [vp] * 6 + [i] * 6 + [vp]
+        lib.gdn_conv_fwd.restype = i
+        lib.gdn_conv_bwd_workspace_size.argtypes = [i] * 5
+        lib.gdn_conv_bwd_workspace_size.restype = sz
+        lib.gdn_conv_bwd.argtypes = row + [vp] * 10 + [i] * 6 + [vp, sz, vp]
+        lib.gdn_conv_bwd.restype = i
+        lib.gdn_conv_step.argtypes = row + [vp] * 6 + [i] * 6 + [vp]
+        lib.gdn_conv_step.restype = i
+        scan = row + row + [vp] + row + row + [vp] + row + [vp, i]
+        lib.gdn_ssm_saved_size.argtypes = [i] * 5
+        lib.gdn_ssm_saved_size.restype = sz
+        lib.gdn_ssm_fwd_workspace_size.argtypes = [i] * 6
+        lib.gdn_ssm_fwd_workspace_size.restype = sz
+        lib.gdn_ssm_fwd.argtypes = scan + [vp] * 5 + [sz] + [i] * 6 + [vp, sz, vp]
+        lib.gdn_ssm_fwd.restype = i
+        lib.gdn_ssm_bwd_workspace_size.argtypes = [i] * 6
+        lib.gdn_ssm_bwd_workspace_size.restype = sz
+        lib.gdn_ssm_bwd.argtypes = scan + [vp] * 4 + [sz] + [vp] * 9 + [i] * 6 + [vp, sz, vp]
+        lib.gdn_ssm_bwd.restype = i
+        lib.gdn_ssm_step.argtypes = scan + [vp] * 4 + [i] * 6 + [vp]
+        lib.gdn_ssm_step.restype = i
+        lib.gdn_norm_fwd.argtypes = row + row + [vp] * 3 + [i64, i, i, f, i, i, i, i, vp]
+        lib.gdn_norm_fwd.restype = i
+        lib.gdn_norm_bwd_workspace_size.argtypes = [i64, i, i, i]
+        lib.gdn_norm_bwd_workspace_size.restype = sz
+        lib.gdn_norm_bwd.argtypes = row + row + [vp] * 7 + [i64, i, i, f, i, i, i, i, vp, sz, vp]
+        lib.gdn_norm_bwd.restype = i
         lib.gdn_kernel_launches.argtypes = []
         lib.gdn_kernel_launches.restype = ctypes.c_uint64
         _lib = lib
