@@ -42,7 +42,7 @@ template <typename T, int W, int E>
 __device__ __forceinline__ void load_state_row(const T* state, long long seq, int r, long long D, long long d0,
                                                float* x) {
     if (state) {
-        unpack<T, E>(load_raw<T, E>(state + (seq * (W - 1) + r) * D + d0, true, E), x);
+        unpack<T, E>(load_raw<T, E>(state + (seq * (W - 1) + r) * D + d0, E), x);
     } else {
 #pragma unroll
         for (int e = 0; e < E; ++e) x[e] = 0.f;
@@ -74,10 +74,10 @@ __global__ void __launch_bounds__(kThreads) conv_fwd_kernel(const ConvArgs p) {
             const int t = t1 - (W - 1) + r;
             float v[E];
             if (t >= t0)
-                unpack<T, E>(load_raw<T, E>(x + t * p.x_stride, true, E), v);
+                unpack<T, E>(load_raw<T, E>(x + t * p.x_stride, E), v);
             else
                 load_state_row<T, W, E>(s0, n, t - t0 + (W - 1), p.D, d0, v);
-            store_raw<T, E>(fs + (static_cast<long long>(n) * (W - 1) + r) * p.D + d0, pack<T, E>(v), true, E);
+            store_raw<T, E>(fs + (static_cast<long long>(n) * (W - 1) + r) * p.D + d0, pack<T, E>(v), E);
         }
     }
     if (tb >= te) return;
@@ -87,14 +87,14 @@ __global__ void __launch_bounds__(kThreads) conv_fwd_kernel(const ConvArgs p) {
     for (int r = 0; r < W - 1; ++r) {
         const int t = tb - (W - 1) + r;
         if (t >= t0)
-            unpack<T, E>(load_raw<T, E>(x + t * p.x_stride, true, E), win[r]);
+            unpack<T, E>(load_raw<T, E>(x + t * p.x_stride, E), win[r]);
         else
             load_state_row<T, W, E>(s0, n, t - t0 + (W - 1), p.D, d0, win[r]);
     }
     for (int t = tb; t < te; t += U) {
         Raw<T, E> in[U];
 #pragma unroll
-        for (int k = 0; k < U; ++k) in[k] = load_raw<T, E>(x + (t + k) * p.x_stride, true, t + k < te ? E : 0);
+        for (int k = 0; k < U; ++k) in[k] = load_raw<T, E>(x + (t + k) * p.x_stride, t + k < te ? E : 0);
 #pragma unroll
         for (int k = 0; k < U; ++k) {
             if (t + k >= te) break;
@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(kThreads) conv_fwd_kernel(const ConvArgs p) {
                 for (int j = 0; j < W; ++j) acc = fmaf(w[j][e], win[j][e], acc);
                 o[e] = p.activation ? acc * sigmoid(acc) : acc;
             }
-            store_raw<T, E>(y + (t + k) * static_cast<long long>(p.D), pack<T, E>(o), true, E);
+            store_raw<T, E>(y + (t + k) * static_cast<long long>(p.D), pack<T, E>(o), E);
 #pragma unroll
             for (int j = 0; j < W - 1; ++j)
 #pragma unroll
@@ -158,15 +158,15 @@ __global__ void __launch_bounds__(kThreads) conv_bwd_kernel(const ConvArgs p) {
             for (int r = 0; r < W - 1; ++r) {
                 const int t = tb - (W - 1) + r;
                 if (t >= t0)
-                    unpack<T, E>(load_raw<T, E>(x + t * p.x_stride, true, E), win[r]);
+                    unpack<T, E>(load_raw<T, E>(x + t * p.x_stride, E), win[r]);
                 else
                     load_state_row<T, W, E>(s0, n, t - t0 + (W - 1), p.D, d0, win[r]);
             }
             for (int t = tb; t < te + W - 1; ++t) {
                 const bool in = t < t1;
                 float g[E];
-                unpack<T, E>(load_raw<T, E>(x + t * p.x_stride, true, in ? E : 0), win[W - 1]);
-                unpack<T, E>(load_raw<T, E>(dy + t * static_cast<long long>(p.D), true, in ? E : 0), g);
+                unpack<T, E>(load_raw<T, E>(x + t * p.x_stride, in ? E : 0), win[W - 1]);
+                unpack<T, E>(load_raw<T, E>(dy + t * static_cast<long long>(p.D), in ? E : 0), g);
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
                     float acc = bs[e];
@@ -192,13 +192,13 @@ __global__ void __launch_bounds__(kThreads) conv_bwd_kernel(const ConvArgs p) {
                     }
                     if (dfs && s >= t1 - (W - 1)) {  // one of the rows the final state holds
                         float v[E];
-                        unpack<T, E>(load_raw<T, E>(dfs + (static_cast<long long>(n) * (W - 1) + s - t1 + (W - 1)) * p.D + d0, true, E), v);
+                        unpack<T, E>(load_raw<T, E>(dfs + (static_cast<long long>(n) * (W - 1) + s - t1 + (W - 1)) * p.D + d0, E), v);
 #pragma unroll
                         for (int e = 0; e < E; ++e) o[e] += v[e];
                     }
                     T* to = s >= tb ? dx + s * static_cast<long long>(p.D)
                                     : ds0 + (static_cast<long long>(n) * (W - 1) + s - t0 + (W - 1)) * p.D + d0;
-                    store_raw<T, E>(to, pack<T, E>(o), true, E);
+                    store_raw<T, E>(to, pack<T, E>(o), E);
                 }
 #pragma unroll
                 for (int j = 0; j < W - 1; ++j)
@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(kThreads) conv_step_kernel(const ConvStepArgs 
         if (slot < 0 || slot >= p.S) {  // an idle row, or one outside the cache
             if (slot >= p.S) record_error(p.err, kErrBadSlot);
             const float zero[E] = {};
-            store_raw<T, E>(y, pack<T, E>(zero), true, E);
+            store_raw<T, E>(y, pack<T, E>(zero), E);
             return;
         }
     }
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kThreads) conv_step_kernel(const ConvStepArgs 
     for (int r = 0; r < W - 1; ++r) {  // not the read-only path: out_state may be the same memory
         in[r] = *reinterpret_cast<const Raw<T, E>*>(st + r * static_cast<long long>(p.D));
     }
-    in[W - 1] = load_raw<T, E>(static_cast<const T*>(p.x) + b * p.x_stride + d0, true, E);
+    in[W - 1] = load_raw<T, E>(static_cast<const T*>(p.x) + b * p.x_stride + d0, E);
     float w[W][E], o[E];
     load_weights<W, E>(p.weight, p.bias, d0, w, o);
 #pragma unroll
@@ -260,11 +260,11 @@ __global__ void __launch_bounds__(kThreads) conv_step_kernel(const ConvStepArgs 
         unpack<T, E>(in[j], v);
 #pragma unroll
         for (int e = 0; e < E; ++e) o[e] = fmaf(w[j][e], v[e], o[e]);
-        if (j > 0) store_raw<T, E>(so + (j - 1) * static_cast<long long>(p.D), in[j], true, E);
+        if (j > 0) store_raw<T, E>(so + (j - 1) * static_cast<long long>(p.D), in[j], E);
     }
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = p.activation ? o[e] * sigmoid(o[e]) : o[e];
-    store_raw<T, E>(y, pack<T, E>(o), true, E);
+    store_raw<T, E>(y, pack<T, E>(o), E);
 }
 
 // Sums of a [rows][cols] partial array over its rows, in a fixed order.

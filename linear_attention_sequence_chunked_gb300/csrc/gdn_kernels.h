@@ -398,9 +398,18 @@ struct SsmArgs {
     float* d_initial_state;       // (nseq, D, N) or null
     float* bc_part;               // [channel blocks][rows][2 N]
     float* par_part;              // [nseq][ssm_par_stride]: dA (D N), dD (D), ddt_bias (D)
+    // A long scan over few channels runs as segments of `seg` tokens (a multiple
+    // of kSsmChunk; slots in all, as find_block counts): carry [slot][D][N] and
+    // carry_dt [slot][D] join them.  Unsplit: seg 2^30, slots nseq, carry null.
+    float* carry;
+    float* carry_dt;
+    int seg;
+    long long slots;
     int nseq, T, D, G, N, dtype;
     int* err;
 };
+// Tokens per segment of a scan of these sizes.
+int ssm_segment(int nseq, int T, int D, int G, int N, bool varlen);
 struct SsmStepArgs {
     const void* u;
     const void* dt;
@@ -434,6 +443,7 @@ __host__ __device__ inline long long ssm_par_stride(int D, int N) { return (stat
 int ssm_group_blocks(int D, int G, int N);  // channel blocks of the backward, per group
 cudaError_t launch_ssm_fwd(const SsmArgs& a, cudaStream_t stream);
 cudaError_t launch_ssm_bwd(const SsmArgs& a, cudaStream_t stream);
+cudaError_t launch_ssm_compose(const SsmArgs& a, bool reverse, cudaStream_t stream);
 cudaError_t launch_ssm_bc(const SsmBcArgs& a, cudaStream_t stream);
 cudaError_t launch_ssm_step(const SsmStepArgs& a, cudaStream_t stream);
 

@@ -26,33 +26,91 @@ struct alignas(sizeof(T) * E >= 16 ? 16 : sizeof(T) * E) Raw {
     T v[E];
 };
 
+// Read-only loads under a predicate, zero where it is false.  Written as
+// volatile assembly so that a prefetch stays where it is issued and nothing
+// that uses the value is folded into the branch around it.
+__device__ __forceinline__ uint4 load_16(const void* p, bool on) {
+    uint4 r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %5, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\t"
+        "mov.b32 %3, 0;\n\t@p ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+        : "=&r"(r.x), "=&r"(r.y), "=&r"(r.z), "=&r"(r.w)
+        : "l"(p), "r"(static_cast<int>(on)));
+    return r;
+}
+__device__ __forceinline__ uint2 load_8(const void* p, bool on) {
+    uint2 r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %3, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\t"
+        "@p ld.global.nc.v2.b32 {%0, %1}, [%2];\n\t}"
+        : "=&r"(r.x), "=&r"(r.y)
+        : "l"(p), "r"(static_cast<int>(on)));
+    return r;
+}
+__device__ __forceinline__ uint32_t load_4(const void* p, bool on) {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %2, 0;\n\tmov.b32 %0, 0;\n\t@p ld.global.nc.b32 %0, [%1];\n\t}"
+                 : "=&r"(r)
+                 : "l"(p), "r"(static_cast<int>(on)));
+    return r;
+}
+__device__ __forceinline__ uint16_t load_2(const void* p, bool on) {
+    uint16_t r;
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %2, 0;\n\tmov.b16 %0, 0;\n\t@p ld.global.nc.b16 %0, [%1];\n\t}"
+                 : "=&h"(r)
+                 : "l"(p), "r"(static_cast<int>(on)));
+    return r;
+}
+
+// One element where it lies; `on` false: zero.
+template <typename T, bool PRED = true>
+__device__ __forceinline__ T load_one(const T* p, bool on = true) {
+    if constexpr (PRED) {
+        if constexpr (sizeof(T) == 2)
+            return load_2(p, on);
+        else
+            return __uint_as_float(load_4(p, on));
+    } else if constexpr (sizeof(T) == 2) {
+        uint16_t r;
+        asm volatile("ld.global.nc.b16 %0, [%1];" : "=h"(r) : "l"(p));
+        return r;
+    } else {
+        float r;
+        asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(r) : "l"(p));
+        return r;
+    }
+}
+
 // Elements [0, n) of the E at p (n < E at the right edge of a row; 0: none).
-// `vec`: p is aligned to the vector, so a full one moves in wide accesses.
-template <typename T, int E>
-__device__ __forceinline__ Raw<T, E> load_raw(const T* p, bool vec, int n) {
+// VEC: p is aligned to the vector and n is 0 or E, one access of up to 16
+// bytes each; else element by element.
+template <typename T, int E, bool VEC = true>
+__device__ __forceinline__ Raw<T, E> load_raw(const T* p, int n) {
     Raw<T, E> r;
-    if (vec && n >= E) {
-        if constexpr (sizeof(r) % 16 == 0) {
-            uint4* d = reinterpret_cast<uint4*>(&r);
+    if constexpr (VEC && sizeof(r) % 16 == 0) {
 #pragma unroll
-            for (int i = 0; i < static_cast<int>(sizeof(r) / 16); ++i) d[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
-        } else if constexpr (sizeof(r) == 8) {
-            *reinterpret_cast<uint2*>(&r) = __ldg(reinterpret_cast<const uint2*>(p));
-        } else if constexpr (sizeof(r) == 4) {
-            *reinterpret_cast<uint32_t*>(&r) = __ldg(reinterpret_cast<const uint32_t*>(p));
-        } else {
-            r.v[0] = __ldg(p);
-        }
+        for (int i = 0; i < static_cast<int>(sizeof(r) / 16); ++i)
+            reinterpret_cast<uint4*>(&r)[i] = load_16(reinterpret_cast<const uint4*>(p) + i, n > 0);
+    } else if constexpr (VEC && sizeof(r) == 8) {
+        *reinterpret_cast<uint2*>(&r) = load_8(p, n > 0);
+    } else if constexpr (VEC && sizeof(r) == 4) {
+        *reinterpret_cast<uint32_t*>(&r) = load_4(p, n > 0);
     } else {
 #pragma unroll
-        for (int i = 0; i < E; ++i) r.v[i] = i < n ? __ldg(p + i) : from_f32<T>(0.f);
+        for (int i = 0; i < E; ++i) {
+            if constexpr (sizeof(T) == 2)
+                r.v[i] = load_2(p + i, i < n);
+            else
+                r.v[i] = __uint_as_float(load_4(p + i, i < n));
+        }
     }
     return r;
 }
 
-template <typename T, int E>
-__device__ __forceinline__ void store_raw(T* p, const Raw<T, E>& r, bool vec, int n) {
-    if (vec && n >= E) {
+template <typename T, int E, bool VEC = true>
+__device__ __forceinline__ void store_raw(T* p, const Raw<T, E>& r, int n) {
+    if constexpr (VEC) {
+        if (n <= 0) return;
         if constexpr (sizeof(r) % 16 == 0) {
             const uint4* s = reinterpret_cast<const uint4*>(&r);
 #pragma unroll
@@ -94,11 +152,58 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+// 1 / x in one instruction (relative error about 2^-23; 0 for huge x)
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float sigmoid(float x) { return rcp(1.f + ex2(-kLog2e * x)); }
 
 // softplus without overflow and with a relative error of a few ulp where it
-// is small: log1p(e), e = exp(-|x|) in (0, 1]
-__device__ __forceinline__ float softplus(float x) { return fmaxf(x, 0.f) + log1pf(__expf(-fabsf(x))); }
+// is small: max(x, 0) + log1p(e), e = exp(-|x|) in (0, 1], by the series of
+// log1p(e) = 2 atanh(s), s = e / (2 + e) <= 1/3, up to s^13 (the next term is
+// below 2^-25 of the sum).  A third of log1pf's instructions and no branch.
+__device__ __forceinline__ float softplus(float x) {
+    const float e = ex2(-kLog2e * fabsf(x));
+    const float s = e * rcp(2.f + e), q = s * s;
+    float r = fmaf(q, 1.f / 13.f, 1.f / 11.f);
+    r = fmaf(q, r, 1.f / 9.f);
+    r = fmaf(q, r, 1.f / 7.f);
+    r = fmaf(q, r, 1.f / 5.f);
+    r = fmaf(q, r, 1.f / 3.f);
+    r = fmaf(q, r, 1.f);
+    return fmaf(2.f * s, r, fmaxf(x, 0.f));
+}
+
+// Two fp32 values in a register pair: one instruction works on both.
+struct Two {
+    unsigned long long v;
+};
+__device__ __forceinline__ Two two(float lo, float hi) {
+    Two r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void split(Two a, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.v));
+}
+__device__ __forceinline__ Two mul2(Two a, Two b) {
+    Two r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+    Two r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ Two ex2_2(Two a) {
+    float lo, hi;
+    split(a, lo, hi);
+    return two(ex2(lo), ex2(hi));
+}
 
 // d silu(x) / dx with s = sigmoid(x)
 __device__ __forceinline__ float dsilu(float x, float s) { return s * (1.f + x * (1.f - s)); }

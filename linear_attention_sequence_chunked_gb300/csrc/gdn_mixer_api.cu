@@ -84,6 +84,31 @@ size_t ssm_saved(int B, int T, int D, int N, bool varlen) {
     return round_up(sizeof(float) * slots * D * N);
 }
 
+// Segments of a scan, and the workspace that joins them.
+struct SsmSplit {
+    int seg;
+    long long slots;
+    size_t dt, total;  // carry_dt's offset (carry is at 0); 0 bytes: not split
+};
+SsmSplit ssm_split(int B, int T, int D, int G, int N, bool varlen) {
+    SsmSplit s{};
+    s.seg = gdn::ssm_segment(B, T, D, G, N, varlen);
+    s.slots = block_slots(B, T, s.seg, varlen);
+    if (s.seg < T) {
+        s.dt = round_up(sizeof(float) * s.slots * D * N);
+        s.total = s.dt + round_up(sizeof(float) * s.slots * D);
+    }
+    return s;
+}
+void set_split(gdn::SsmArgs& a, const SsmSplit& s, void* workspace) {
+    a.seg = s.seg;
+    a.slots = s.slots;
+    if (s.total) {
+        a.carry = static_cast<float*>(workspace);
+        a.carry_dt = reinterpret_cast<float*>(static_cast<char*>(workspace) + s.dt);
+    }
+}
+
 struct SsmBwdLayout {
     size_t bc, par, total;
 };
@@ -185,8 +210,8 @@ size_t gdn_ssm_saved_size(int B, int T, int D, int N, int varlen) {
 }
 
 size_t gdn_ssm_fwd_workspace_size(int B, int T, int D, int G, int N, int varlen) {
-    (void)B, (void)T, (void)D, (void)G, (void)N, (void)varlen;
-    return 0;
+    if (check_ssm(B, T, D, G, N, 0) != GDN_OK) return 0;
+    return ssm_split(B, T, D, G, N, varlen != 0).total;
 }
 
 gdn_status gdn_ssm_fwd(const void* u, int64_t u_stride, const void* dt, int64_t dt_stride, const float* A,
@@ -208,7 +233,8 @@ gdn_status gdn_ssm_fwd(const void* u, int64_t u_stride, const void* dt, int64_t 
     GDN_TRY(check_cu(cu_seqlens));
     const bool varlen = cu_seqlens != nullptr;
     if (saved) GDN_TRY(check_ws(saved, saved_bytes, ssm_saved(B, T, D, N, varlen)));
-    GDN_TRY(check_ws(workspace, workspace_bytes, gdn_ssm_fwd_workspace_size(B, T, D, G, N, varlen)));
+    const SsmSplit split = ssm_split(B, T, D, G, N, varlen);
+    GDN_TRY(check_ws(workspace, workspace_bytes, split.total));
     if (T == 0 && !final_state) return GDN_OK;
     int* err = gdn::device_error_word();
     if (!err) return GDN_ERR_CUDA;
@@ -219,7 +245,8 @@ gdn_status gdn_ssm_fwd(const void* u, int64_t u_stride, const void* dt, int64_t 
     a.initial_state = initial_state; a.cu_seqlens = cu_seqlens; a.out = out; a.final_state = final_state;
     a.saved = static_cast<float*>(saved);
     a.nseq = B; a.T = T; a.D = D; a.G = G; a.N = N; a.dtype = dtype; a.err = err;
-    return gdn::count_launch(gdn::launch_ssm_fwd(a, stream)) ? GDN_OK : GDN_ERR_CUDA;
+    set_split(a, split, workspace);
+    return gdn::count_launch(gdn::launch_ssm_fwd(a, stream), split.total ? 3 : 1) ? GDN_OK : GDN_ERR_CUDA;
 }
 
 size_t gdn_ssm_bwd_workspace_size(int B, int T, int D, int G, int N, int varlen) {

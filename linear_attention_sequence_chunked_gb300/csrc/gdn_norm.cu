@@ -61,7 +61,7 @@ struct Row {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int j = lane + i * LANES;
-            r[i] = load_raw<T, E>(p + static_cast<long long>(j) * E, true, on && j < nv ? E : 0);
+            r[i] = load_raw<T, E>(p + static_cast<long long>(j) * E, on && j < nv ? E : 0);
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) unpack<T, E>(r[i], v[i]);
@@ -70,7 +70,7 @@ struct Row {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int j = lane + i * LANES;
-            if (on && j < nv) store_raw<T, E>(p + static_cast<long long>(j) * E, pack<T, E>(v[i]), true, E);
+            if (on && j < nv) store_raw<T, E>(p + static_cast<long long>(j) * E, pack<T, E>(v[i]), E);
         }
     }
 };
@@ -111,7 +111,7 @@ __device__ __forceinline__ void load_param(const float* p, float missing, int la
         const int j = lane + i * LANES;
 #pragma unroll
         for (int e = 0; e < E; ++e) w[i][e] = missing;
-        if (p && j < nv) unpack<float, E>(load_raw<float, E>(p + static_cast<long long>(j) * E, true, E), w[i]);
+        if (p && j < nv) unpack<float, E>(load_raw<float, E>(p + static_cast<long long>(j) * E, E), w[i]);
     }
 }
 

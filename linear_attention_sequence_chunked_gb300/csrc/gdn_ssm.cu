@@ -9,123 +9,226 @@ namespace {
 
 using namespace ssm;
 
+constexpr int kWarps = 4;
+constexpr int kTile = 8;  // tokens whose inputs are held at a time; divides kSsmChunk
+
+// A lane holds NL = min(N, 16) states of one channel, four at a time: group j
+// of lane q of a channel's LPC = N / NL lanes is states 4 (j LPC + q) .. + 3, so
+// that those lanes read neighbouring 16 bytes of a row of B.  CH channels per
+// warp; with N <= 16 a lane is a channel and a row of 32 channels one access.
 template <int N>
-constexpr int kWarps = N >= 64 ? 2 : 4;
+struct Lanes {
+    static constexpr int NL = N < 16 ? N : 16;
+    static constexpr int LPC = N / NL;
+    static constexpr int CH = 32 / LPC;
+    static constexpr int GR = NL / 4;
+};
 
-template <typename T, int N>
-__global__ void __launch_bounds__(32 * kWarps<N>) ssm_fwd_kernel(const SsmArgs p, int seg, long long slots, int blocks) {
-    using G = Geo<N>;
-    constexpr int CH = G::CH, EPL = G::EPL;
-    struct Tile {
-        float2 dtx[K][CH];
-        float B[K][N];
-        float C[K][N];
-        float y[K][CH];
-    };
-    __shared__ __align__(16) Tile tiles[kWarps<N>];
-    if (blockIdx.x == 0) check_offsets(p.cu_seqlens, p.nseq, p.T, p.err);
-    const int lane = threadIdx.x & 31;
-    const long long unit = static_cast<long long>(blockIdx.x) * kWarps<N> + (threadIdx.x >> 5);
-    const int nblk = blocks * p.G;
-    if (unit >= slots * nblk) return;
-    Place w;
-    if (!find_place<CH>(p, unit / nblk, static_cast<int>(unit % nblk), seg, blocks, w)) return;
-    Tile& tile = tiles[threadIdx.x >> 5];
-
-    // this lane's states
-    const int ch = lane / G::LPC, q = lane % G::LPC;
-    const bool mine = ch < w.nd;
-    const long long so = (static_cast<long long>(w.n) * p.D + w.d0 + ch) * N + 4 * q;
-    float A2[4], h[4];
-    {
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f), s = a;
-        if (mine) {
-            a = *reinterpret_cast<const float4*>(p.A + static_cast<long long>(w.d0 + ch) * N + 4 * q);
-            if (w.first && p.initial_state) s = *reinterpret_cast<const float4*>(p.initial_state + so);
-        }
-        A2[0] = a.x * kLog2e; A2[1] = a.y * kLog2e; A2[2] = a.z * kLog2e; A2[3] = a.w * kLog2e;
-        h[0] = s.x; h[1] = s.y; h[2] = s.z; h[3] = s.w;
-    }
-    // its share of a tile's elements
-    const int tok = lane / G::PARTS, c0 = lane % G::PARTS * EPL;
-    const int ne = tok < K ? max(0, min(EPL, w.nd - c0)) : 0;
-    float dskip[EPL], bias[EPL];
+// B or C rows of a tile, [kTile][N] as fp32 in shared memory: read from global
+// a tile ahead (16 bytes per access where VEC), put there when its turn comes.
+template <typename T, int N, bool VEC>
+struct Rows {
+    static constexpr int PE = VEC ? (N * kTile / 32 < 16 / static_cast<int>(sizeof(T)) ? N * kTile / 32 : 16 / static_cast<int>(sizeof(T))) : 1;
+    static constexpr int NP = N * kTile / 32 / PE;
+    Raw<T, PE> v[NP];
+    __device__ __forceinline__ void load(const T* rows, long long stride, int nt, int lane) {
 #pragma unroll
-    for (int e = 0; e < EPL; ++e) {
-        dskip[e] = (p.D_skip && e < ne) ? p.D_skip[w.d0 + c0 + e] : 0.f;
-        bias[e] = (p.dt_bias && e < ne) ? p.dt_bias[w.d0 + c0 + e] : 0.f;
+        for (int i = 0; i < NP; ++i) {
+            const int id = i * 32 + lane, tok = id / (N / PE), n0 = id % (N / PE) * PE;
+            v[i] = load_raw<T, PE>(rows + tok * stride + n0, tok < nt ? PE : 0);
+        }
     }
+    __device__ __forceinline__ void store(float* dst, int lane) const {
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            float x[PE];
+            unpack<T, PE>(v[i], x);
+#pragma unroll
+            for (int e = 0; e < PE; ++e) dst[(i * 32 + lane) * PE + e] = x[e];
+        }
+    }
+};
+
+// The states of a lane, as register pairs, from or to a channel's N floats.
+template <int N>
+__device__ __forceinline__ void load_states(const float* p, int q, Two (&v)[Lanes<N>::NL / 2]) {
+#pragma unroll
+    for (int j = 0; j < Lanes<N>::GR; ++j) {
+        const float4 x = *reinterpret_cast<const float4*>(p + 4 * (j * Lanes<N>::LPC + q));
+        v[2 * j] = two(x.x, x.y);
+        v[2 * j + 1] = two(x.z, x.w);
+    }
+}
+template <int N>
+__device__ __forceinline__ void store_states(float* p, int q, const Two (&v)[Lanes<N>::NL / 2]) {
+#pragma unroll
+    for (int j = 0; j < Lanes<N>::GR; ++j) {
+        float4 x;
+        split(v[2 * j], x.x, x.y);
+        split(v[2 * j + 1], x.z, x.w);
+        *reinterpret_cast<float4*>(p + 4 * (j * Lanes<N>::LPC + q)) = x;
+    }
+}
+
+// kOut: the whole forward.  Without it, only the segment's end state from a
+// zero start and the sum of its dt (the first pass of a split scan).
+template <typename T, int N, bool kOut, bool VEC>
+__global__ void __launch_bounds__(32 * kWarps) ssm_fwd_kernel(const SsmArgs p, int blocks) {
+    using L = Lanes<N>;
+    constexpr int LPC = L::LPC, CH = L::CH, NL = L::NL;
+    __shared__ __align__(16) float tile_B[kWarps][kTile][N];
+    __shared__ __align__(16) float tile_C[kWarps][kOut ? kTile : 1][N];
+    if (blockIdx.x == 0) check_offsets(p.cu_seqlens, p.nseq, p.T, p.err);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long unit = static_cast<long long>(blockIdx.x) * kWarps + warp;
+    const int nblk = blocks * p.G;
+    if (unit >= p.slots * nblk) return;
+    Place w;
+    if (!find_place<CH>(p, unit / nblk, static_cast<int>(unit % nblk), p.seg, blocks, w)) return;
+    if (!kOut && w.last) return;  // nothing starts after it
+
+    const int ch = lane / LPC, q = lane % LPC;
+    const bool mine = ch < w.nd;
+    const int d = w.d0 + (mine ? ch : 0);
+    const long long so = (static_cast<long long>(w.n) * p.D + d) * N;
+    const long long co = (w.slot * p.D + d) * N;
+    Two A2[NL / 2], h[NL / 2];
+    load_states<N>(p.A + static_cast<long long>(d) * N, q, A2);
+#pragma unroll
+    for (int i = 0; i < NL / 2; ++i) {
+        A2[i] = mul2(A2[i], two(kLog2e, kLog2e));
+        h[i] = two(0.f, 0.f);
+    }
+    if (kOut && !w.first)
+        load_states<N>(p.carry + co, q, h);
+    else if (kOut && p.initial_state)
+        load_states<N>(p.initial_state + so, q, h);
+    const float dskip = kOut && p.D_skip && q == 0 ? p.D_skip[d] : 0.f;
+    const float bias = p.dt_bias ? p.dt_bias[d] : 0.f;
+    float sum = 0.f;
     const long long row0 = static_cast<long long>(w.b) * p.T;
-    const T* u = static_cast<const T*>(p.u) + row0 * p.u_stride + w.d0 + c0;
-    const T* dt = static_cast<const T*>(p.dt) + row0 * p.dt_stride + w.d0 + c0;
-    const T* z = p.z ? static_cast<const T*>(p.z) + row0 * p.z_stride + w.d0 + c0 : nullptr;
+    const T* u = static_cast<const T*>(p.u) + row0 * p.u_stride + d;
+    const T* dt = static_cast<const T*>(p.dt) + row0 * p.dt_stride + d;
+    const T* z = kOut && p.z ? static_cast<const T*>(p.z) + row0 * p.z_stride + d : nullptr;
     const T* Bm = static_cast<const T*>(p.Bm) + row0 * p.B_stride + w.g * N;
     const T* Cm = static_cast<const T*>(p.Cm) + row0 * p.C_stride + w.g * N;
-    T* out = static_cast<T*>(p.out) + row0 * p.D + w.d0 + c0;
-    const bool vec_u = can_vec<T>(u, p.u_stride, EPL), vec_dt = can_vec<T>(dt, p.dt_stride, EPL);
-    const bool vec_z = z && can_vec<T>(z, p.z_stride, EPL), vec_o = can_vec<T>(out, p.D, EPL);
-    using Rows = RowTile<T, N>;
-    const bool vec_B = can_vec<T>(Bm, p.B_stride, Rows::PE), vec_C = can_vec<T>(Cm, p.C_stride, Rows::PE);
-
-    for (int t = w.s0; t < w.s1; t += K) {
-        const int nt = min(K, w.s1 - t);
-        const int n_in = tok < nt ? ne : 0;
-        if (p.saved && mine)
-            *reinterpret_cast<float4*>(p.saved + ((w.chunk0 + (t - w.s0) / K) * p.D + w.d0 + ch) * N + 4 * q) =
-                make_float4(h[0], h[1], h[2], h[3]);
-        float ux[EPL], zx[EPL];
-        {
-            float dx[EPL];
-            unpack<T, EPL>(load_raw<T, EPL>(u + (t + tok) * p.u_stride, vec_u, n_in), ux);
-            unpack<T, EPL>(load_raw<T, EPL>(dt + (t + tok) * p.dt_stride, vec_dt, n_in), dx);
-            if (z) unpack<T, EPL>(load_raw<T, EPL>(z + (t + tok) * p.z_stride, vec_z, n_in), zx);
-            Rows r;
-            r.load(Bm + t * p.B_stride, p.B_stride, vec_B, nt, lane);
-            r.store(&tile.B[0][0], lane);
-            r.load(Cm + t * p.C_stride, p.C_stride, vec_C, nt, lane);
-            r.store(&tile.C[0][0], lane);
-            if (tok < K) {
+    T* out = kOut ? static_cast<T*>(p.out) + row0 * p.D + d : nullptr;
+    // per-thread row pointers move a tile at a time; the rows in between are
+    // uniform offsets
+    u += w.s0 * p.u_stride;
+    dt += w.s0 * p.dt_stride;
+    Bm += w.s0 * p.B_stride;
+    Cm += w.s0 * p.C_stride;
+    if (kOut) {
+        out += w.s0 * static_cast<long long>(p.D);
+        if (z) z += w.s0 * p.z_stride;
+    }
+    T u_in[kTile], dt_in[kTile];
+    Rows<T, N, VEC> b_in, c_in;
+    // the next tile's inputs; `left` tokens remain (none: nothing is read)
+    auto load = [&](int left) {
+        b_in.load(Bm, p.B_stride, left, lane);
+        if (kOut) c_in.load(Cm, p.C_stride, left, lane);
+        if (left >= kTile) {
 #pragma unroll
-                for (int e = 0; e < EPL; ++e) {
-                    float d = dx[e] + bias[e];
-                    if (p.softplus) d = softplus(d);
-                    d = e < n_in ? d : 0.f;
-                    tile.dtx[tok][c0 + e] = make_float2(d, d * ux[e]);
+            for (int k = 0; k < kTile; ++k) {
+                u_in[k] = load_one<T, false>(u + k * p.u_stride);
+                dt_in[k] = load_one<T, false>(dt + k * p.dt_stride);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < kTile; ++k) {
+                u_in[k] = load_one(u + k * p.u_stride, k < left);
+                dt_in[k] = load_one(dt + k * p.dt_stride, k < left);
+            }
+        }
+        u += kTile * p.u_stride;
+        dt += kTile * p.dt_stride;
+        Bm += kTile * p.B_stride;
+        Cm += kTile * p.C_stride;
+    };
+
+    load(w.s1 - w.s0);
+    for (int left = w.s1 - w.s0, done = 0; left > 0; left -= kTile, done += kTile) {
+        if (kOut && p.saved && mine && done % kSsmChunk == 0)
+            store_states<N>(p.saved + ((w.chunk0 + done / kSsmChunk) * p.D + d) * N, q, h);
+        b_in.store(&tile_B[warp][0][0], lane);
+        if (kOut) c_in.store(&tile_C[warp][0][0], lane);
+        T z_in[kTile];
+        if (z) {
+            if (left >= kTile) {
+#pragma unroll
+                for (int k = 0; k < kTile; ++k) z_in[k] = load_one<T, false>(z + k * p.z_stride);
+            } else {
+#pragma unroll
+                for (int k = 0; k < kTile; ++k) z_in[k] = load_one(z + k * p.z_stride, k < left);
+            }
+            z += kTile * p.z_stride;
+        }
+        Two d2[kTile], x2[kTile], y2[kTile];
+#pragma unroll
+        for (int k = 0; k < kTile; ++k) {
+            const float uk = to_f32(u_in[k]);
+            float dk = to_f32(dt_in[k]) + bias;
+            if (p.softplus) dk = softplus(dk);
+            if (left < kTile) dk = k < left ? dk : 0.f;
+            if (!kOut) sum += dk;
+            d2[k] = two(dk, dk);
+            x2[k] = two(dk * uk, dk * uk);
+            if (kOut) y2[k] = two(dskip * uk, 0.f);
+        }
+        load(left - kTile);
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < L::GR; ++j) {
+#pragma unroll
+            for (int k = 0; k < kTile; ++k) {
+                const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(&tile_B[warp][k][4 * (j * LPC + q)]);
+                h[2 * j] = fma2(ex2_2(mul2(d2[k], A2[2 * j])), h[2 * j], mul2(x2[k], Two{b.x}));
+                h[2 * j + 1] = fma2(ex2_2(mul2(d2[k], A2[2 * j + 1])), h[2 * j + 1], mul2(x2[k], Two{b.y}));
+                if (kOut) {
+                    const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(&tile_C[warp][k][4 * (j * LPC + q)]);
+                    y2[k] = fma2(h[2 * j], Two{c.x}, y2[k]);
+                    y2[k] = fma2(h[2 * j + 1], Two{c.y}, y2[k]);
                 }
             }
         }
-        __syncwarp();
-        float y[K];
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const float2 d = tile.dtx[k][ch];
-            const float4 b = *reinterpret_cast<const float4*>(&tile.B[k][4 * q]);
-            const float4 c = *reinterpret_cast<const float4*>(&tile.C[k][4 * q]);
-            h[0] = fmaf(ex2(d.x * A2[0]), h[0], d.y * b.x);
-            h[1] = fmaf(ex2(d.x * A2[1]), h[1], d.y * b.y);
-            h[2] = fmaf(ex2(d.x * A2[2]), h[2], d.y * b.z);
-            h[3] = fmaf(ex2(d.x * A2[3]), h[3], d.y * b.w);
-            y[k] = fmaf(c.x, h[0], c.y * h[1]) + fmaf(c.z, h[2], c.w * h[3]);
-        }
-        put_channel_sums<G::LPC, CH>(y, q, ch, &tile.y[0][0]);
-        __syncwarp();
-        if (n_in > 0) {
-            float o[EPL];
-#pragma unroll
-            for (int e = 0; e < EPL; ++e) {
-                o[e] = fmaf(dskip[e], ux[e], tile.y[tok][c0 + e]);
-                if (z) o[e] *= zx[e] * sigmoid(zx[e]);
-            }
-            store_raw<T, EPL>(out + (t + tok) * static_cast<long long>(p.D), pack<T, EPL>(o), vec_o, n_in);
-        }
         __syncwarp();  // the next tile overwrites this one
+        if (kOut) {
+            float y[kTile];
+#pragma unroll
+            for (int k = 0; k < kTile; ++k) {
+                float lo, hi;
+                split(y2[k], lo, hi);
+                lo += hi;
+#pragma unroll
+                for (int m = 1; m < LPC; m *= 2) lo += __shfl_xor_sync(0xffffffffu, lo, m);
+                if (z) {
+                    const float zk = to_f32(z_in[k]);
+                    lo *= zk * sigmoid(zk);
+                }
+                y[k] = lo;
+            }
+            if (mine) {
+#pragma unroll
+                for (int k = 0; k < kTile; ++k)
+                    if (k < left && (LPC == 1 || q == k % LPC)) out[k * static_cast<long long>(p.D)] = from_f32<T>(y[k]);
+            }
+            out += kTile * static_cast<long long>(p.D);
+        }
     }
-    if (w.last && p.final_state && mine) *reinterpret_cast<float4*>(p.final_state + so) = make_float4(h[0], h[1], h[2], h[3]);
+    if (!mine) return;
+    if constexpr (kOut) {
+        if (w.last && p.final_state) store_states<N>(p.final_state + so, q, h);
+    } else {
+        store_states<N>(p.carry + co, q, h);
+        if (q == 0) p.carry_dt[w.slot * p.D + d] = sum;
+    }
 }
 
 // One token: lane q of a channel updates four of its states where they lie.
 // Bound by HBM: the state is read and written once.
-template <typename T, int N>
+template <typename T, int N, bool VEC>
 __global__ void __launch_bounds__(256) ssm_step_kernel(const SsmStepArgs p) {
     constexpr int LPC = N / 4;
     const long long id = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
@@ -150,8 +253,8 @@ __global__ void __launch_bounds__(256) ssm_step_kernel(const SsmStepArgs p) {
         const T* Bm = static_cast<const T*>(p.Bm) + b * p.B_stride + g * N + 4 * q;
         const T* Cm = static_cast<const T*>(p.Cm) + b * p.C_stride + g * N + 4 * q;
         float bv[4], cv[4], h[4];
-        unpack<T, 4>(load_raw<T, 4>(Bm, can_vec<T>(Bm, 4, 4), 4), bv);
-        unpack<T, 4>(load_raw<T, 4>(Cm, can_vec<T>(Cm, 4, 4), 4), cv);
+        unpack<T, 4>(VEC ? load_raw<T, 4>(Bm, 4) : load_raw<T, 4, false>(Bm, 4), bv);
+        unpack<T, 4>(VEC ? load_raw<T, 4>(Cm, 4) : load_raw<T, 4, false>(Cm, 4), cv);
         uu = to_f32(static_cast<const T*>(p.u)[b * p.u_stride + d]);
         float dt = to_f32(static_cast<const T*>(p.dt)[b * p.dt_stride + d]) + (p.dt_bias ? __ldg(p.dt_bias + d) : 0.f);
         if (p.softplus) dt = softplus(dt);
@@ -175,19 +278,96 @@ __global__ void __launch_bounds__(256) ssm_step_kernel(const SsmStepArgs p) {
     }
 }
 
+// The states between the segments of a split scan: carry holds every segment's
+// own contribution and receives the state it starts from (reverse: the
+// gradient that reaches its end), four states per thread, segment after segment
+// with the loads of eight in flight.
+__global__ void __launch_bounds__(256) ssm_compose_kernel(const SsmArgs p, int reverse) {
+    const long long id = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+    const long long per = static_cast<long long>(p.D) * p.N / 4;
+    if (id >= per * p.nseq) return;
+    const int n = static_cast<int>(id / per);
+    const long long i4 = id % per;  // float4 of a state
+    const long long d = i4 * 4 / p.N;
+    int b, t0, t1;
+    if (!token_range(p.cu_seqlens, n, p.nseq, p.T, p.err, b, t0, t1)) return;
+    const int segs = max(1, (t1 - t0 + p.seg - 1) / p.seg);
+    const long long base = p.cu_seqlens ? static_cast<long long>(t0 / p.seg) + n
+                                        : static_cast<long long>(n) * max(1, (p.T + p.seg - 1) / p.seg);
+    const float* start = reverse ? p.d_final_state : p.initial_state;
+    float4 h = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (start) h = *reinterpret_cast<const float4*>(start + (n * per + i4) * 4);
+    float4 a = *reinterpret_cast<const float4*>(p.A + i4 * 4);
+    a.x *= kLog2e; a.y *= kLog2e; a.z *= kLog2e; a.w *= kLog2e;
+    constexpr int U = 8;
+    for (int c = 0; c < segs; c += U) {
+        float4 e[U];
+        float s[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int j = c + k;
+            // the last segment in walking order contributes to nothing
+            if (j < segs - 1) {
+                const long long slot = base + (reverse ? segs - 1 - j : j);
+                e[k] = *reinterpret_cast<const float4*>(p.carry + (slot * per + i4) * 4);
+                s[k] = p.carry_dt[slot * p.D + d];
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int j = c + k;
+            if (j < segs) {
+                const long long slot = base + (reverse ? segs - 1 - j : j);
+                *reinterpret_cast<float4*>(p.carry + (slot * per + i4) * 4) = h;
+                if (j < segs - 1) {
+                    h.x = fmaf(ex2(a.x * s[k]), h.x, e[k].x);
+                    h.y = fmaf(ex2(a.y * s[k]), h.y, e[k].y);
+                    h.z = fmaf(ex2(a.z * s[k]), h.z, e[k].z);
+                    h.w = fmaf(ex2(a.w * s[k]), h.w, e[k].w);
+                }
+            }
+        }
+    }
+}
+
+cudaError_t launch_compose(const SsmArgs& a, bool reverse, cudaStream_t stream) {
+    const long long threads = static_cast<long long>(a.nseq) * a.D * a.N / 4;
+    ssm_compose_kernel<<<static_cast<unsigned>((threads + 255) / 256), 256, 0, stream>>>(a, reverse);
+    return cudaGetLastError();
+}
+
+template <typename T, int N, bool VEC>
+cudaError_t fwd_v(const SsmArgs& a, cudaStream_t stream) {
+    const int blocks = (a.D / a.G + Lanes<N>::CH - 1) / Lanes<N>::CH;
+    const long long units = a.slots * blocks * a.G;
+    const unsigned grid = static_cast<unsigned>((units + kWarps - 1) / kWarps);
+    if (a.carry) {
+        ssm_fwd_kernel<T, N, false, VEC><<<grid, 32 * kWarps, 0, stream>>>(a, blocks);
+        const cudaError_t e = launch_compose(a, false, stream);
+        if (e != cudaSuccess) return e;
+    }
+    ssm_fwd_kernel<T, N, true, VEC><<<grid, 32 * kWarps, 0, stream>>>(a, blocks);
+    return cudaGetLastError();
+}
+
 template <typename T, int N>
 cudaError_t fwd_n(const SsmArgs& a, cudaStream_t stream) {
-    const int blocks = (a.D / a.G + Geo<N>::CH - 1) / Geo<N>::CH;
-    const long long units = static_cast<long long>(a.nseq) * blocks * a.G;
-    ssm_fwd_kernel<T, N><<<static_cast<unsigned>((units + kWarps<N> - 1) / kWarps<N>), 32 * kWarps<N>, 0, stream>>>(
-        a, 1 << 30, a.nseq, blocks);
-    return cudaGetLastError();
+    constexpr int bytes = Rows<T, N, true>::PE * static_cast<int>(sizeof(T));
+    auto ok = [](const void* p, long long stride) {
+        return reinterpret_cast<uintptr_t>(p) % bytes == 0 && stride * static_cast<long long>(sizeof(T)) % bytes == 0;
+    };
+    return ok(a.Bm, a.B_stride) && ok(a.Cm, a.C_stride) ? fwd_v<T, N, true>(a, stream) : fwd_v<T, N, false>(a, stream);
 }
 
 template <typename T, int N>
 cudaError_t step_n(const SsmStepArgs& a, cudaStream_t stream) {
     const long long threads = static_cast<long long>(a.B) * a.D * (N / 4);
-    ssm_step_kernel<T, N><<<static_cast<unsigned>((threads + 255) / 256), 256, 0, stream>>>(a);
+    const unsigned grid = static_cast<unsigned>((threads + 255) / 256);
+    auto ok = [](const void* p, long long stride) { return reinterpret_cast<uintptr_t>(p) % (4 * sizeof(T)) == 0 && stride % 4 == 0; };
+    if (ok(a.Bm, a.B_stride) && ok(a.Cm, a.C_stride))
+        ssm_step_kernel<T, N, true><<<grid, 256, 0, stream>>>(a);
+    else
+        ssm_step_kernel<T, N, false><<<grid, 256, 0, stream>>>(a);
     return cudaGetLastError();
 }
 
@@ -207,6 +387,18 @@ cudaError_t step_n(const SsmStepArgs& a, cudaStream_t stream) {
     }                                     \
     GDN_SSM_N(fn, float)
 
+int ssm_segment(int nseq, int T, int D, int G, int N, bool varlen) {
+    const int ch = N <= 16 ? 32 : 512 / N;
+    const long long warps = static_cast<long long>(varlen ? 1 : nseq) * G * ((D / G + ch - 1) / ch);
+    if (warps >= 456 || T < 256) return 1 << 30;
+    const long long segs = 1824 / warps;  // one wave of 12 warps per SM
+    const int seg = static_cast<int>(((T + segs - 1) / segs + kSsmChunk - 1) / kSsmChunk * kSsmChunk);
+    return seg < 64 ? 64 : seg;
+}
+
+cudaError_t launch_ssm_compose(const SsmArgs& a, bool reverse, cudaStream_t stream) {
+    return launch_compose(a, reverse, stream);
+}
 cudaError_t launch_ssm_fwd(const SsmArgs& a, cudaStream_t stream) { GDN_SSM_DISPATCH(fwd_n) }
 cudaError_t launch_ssm_step(const SsmStepArgs& a, cudaStream_t stream) { GDN_SSM_DISPATCH(step_n) }
 

@@ -45,20 +45,12 @@ __device__ __forceinline__ void across_channels(float (&v)[8], int ch) {
     }
 }
 
-// Sum over the token lanes that share a channel share (same lane % PARTS).
-template <int PARTS>
-__device__ __forceinline__ float over_tokens(float x) {
-#pragma unroll
-    for (int m = PARTS; m < 32; m *= 2) x += __shfl_xor_sync(0xffffffffu, x, m);
-    return x;
-}
-
-template <typename T, int N>
+template <typename T, int N, bool VEC>
 __global__ void __launch_bounds__(32 * kWarps<N>) ssm_bwd_kernel(const SsmArgs p, int seg, long long slots, int blocks) {
-    using G = Geo<N>;
+    using G = Geo<N, 4>;
     constexpr int CH = G::CH, EPL = G::EPL, LPC = G::LPC;
     constexpr int M8 = CH < 8 ? CH : 8;
-    struct Tile {
+    struct alignas(16) Tile {
         float2 dtx[K][CH];
         float dy[K][CH];
         float B[K][N];
@@ -114,11 +106,7 @@ __global__ void __launch_bounds__(32 * kWarps<N>) ssm_bwd_kernel(const SsmArgs p
     T* dz = z ? static_cast<T*>(p.dz) + dense : nullptr;
     const T* Bm = static_cast<const T*>(p.Bm) + row0 * p.B_stride + w.g * N;
     const T* Cm = static_cast<const T*>(p.Cm) + row0 * p.C_stride + w.g * N;
-    const bool vec_u = can_vec<T>(u, p.u_stride, EPL), vec_dt = can_vec<T>(dt, p.dt_stride, EPL);
-    const bool vec_z = z && can_vec<T>(z, p.z_stride, EPL);
-    const bool vec_g = can_vec<T>(d_out, p.D, EPL), vec_o = can_vec<T>(du, p.D, EPL);
-    using Rows = RowTile<T, N>;
-    const bool vec_B = can_vec<T>(Bm, p.B_stride, Rows::PE), vec_C = can_vec<T>(Cm, p.C_stride, Rows::PE);
+    using Rows = RowTile<T, N, VEC>;
     const long long rows = p.cu_seqlens ? p.T : static_cast<long long>(p.nseq) * p.T;
     float* bc = p.bc_part + (static_cast<long long>(block) * rows + row0) * 2 * N;
 
@@ -130,15 +118,15 @@ __global__ void __launch_bounds__(32 * kWarps<N>) ssm_bwd_kernel(const SsmArgs p
         float4 hs = make_float4(0.f, 0.f, 0.f, 0.f);
         if (mine) hs = *reinterpret_cast<const float4*>(p.saved + ((w.chunk0 + it) * p.D + w.d0 + ch) * N + 4 * q);
         float ux[EPL], rx[EPL], zx[EPL], gx[EPL];
-        unpack<T, EPL>(load_raw<T, EPL>(u + (t + tok) * p.u_stride, vec_u, n_in), ux);
-        unpack<T, EPL>(load_raw<T, EPL>(dt + (t + tok) * p.dt_stride, vec_dt, n_in), rx);
-        if (z) unpack<T, EPL>(load_raw<T, EPL>(z + (t + tok) * p.z_stride, vec_z, n_in), zx);
-        unpack<T, EPL>(load_raw<T, EPL>(d_out + (t + tok) * static_cast<long long>(p.D), vec_g, n_in), gx);
+        unpack<T, EPL>(load_raw<T, EPL, VEC>(u + (t + tok) * p.u_stride, n_in), ux);
+        unpack<T, EPL>(load_raw<T, EPL, VEC>(dt + (t + tok) * p.dt_stride, n_in), rx);
+        if (z) unpack<T, EPL>(load_raw<T, EPL, VEC>(z + (t + tok) * p.z_stride, n_in), zx);
+        unpack<T, EPL>(load_raw<T, EPL, VEC>(d_out + (t + tok) * static_cast<long long>(p.D), n_in), gx);
         {
             Rows r;
-            r.load(Bm + t * p.B_stride, p.B_stride, vec_B, nt, lane);
+            r.load(Bm + t * p.B_stride, p.B_stride, nt, lane);
             r.store(&tile.B[0][0], lane);
-            r.load(Cm + t * p.C_stride, p.C_stride, vec_C, nt, lane);
+            r.load(Cm + t * p.C_stride, p.C_stride, nt, lane);
             r.store(&tile.C[0][0], lane);
         }
         if (tok < K) {
@@ -221,9 +209,9 @@ __global__ void __launch_bounds__(32 * kWarps<N>) ssm_bwd_kernel(const SsmArgs p
                 }
             }
             const long long at = (t + tok) * static_cast<long long>(p.D);
-            store_raw<T, EPL>(du + at, pack<T, EPL>(o1), vec_o, n_in);
-            store_raw<T, EPL>(ddt + at, pack<T, EPL>(o2), vec_o, n_in);
-            if (z) store_raw<T, EPL>(dz + at, pack<T, EPL>(o3), vec_o, n_in);
+            store_raw<T, EPL, VEC>(du + at, pack<T, EPL>(o1), n_in);
+            store_raw<T, EPL, VEC>(ddt + at, pack<T, EPL>(o2), n_in);
+            if (z) store_raw<T, EPL, VEC>(dz + at, pack<T, EPL>(o3), n_in);
         }
         __syncwarp();
     }
@@ -263,8 +251,12 @@ template <typename T, int N>
 cudaError_t bwd_n(const SsmArgs& a, cudaStream_t stream) {
     const int blocks = ssm_group_blocks(a.D, a.G, N);
     const long long units = static_cast<long long>(a.nseq) * blocks * a.G;
-    ssm_bwd_kernel<T, N><<<static_cast<unsigned>((units + kWarps<N> - 1) / kWarps<N>), 32 * kWarps<N>, 0, stream>>>(
-        a, 1 << 30, a.nseq, blocks);
+    const unsigned grid = static_cast<unsigned>((units + kWarps<N> - 1) / kWarps<N>);
+    // out is not written here; d_out, du, ddt and dz are dense rows of D as it is, 16-byte aligned all
+    if (all_vec<T, N, 4>(a))
+        ssm_bwd_kernel<T, N, true><<<grid, 32 * kWarps<N>, 0, stream>>>(a, 1 << 30, a.nseq, blocks);
+    else
+        ssm_bwd_kernel<T, N, false><<<grid, 32 * kWarps<N>, 0, stream>>>(a, 1 << 30, a.nseq, blocks);
     return cudaGetLastError();
 }
 

@@ -4,13 +4,13 @@
 //   dt_t = softplus(dt_raw_t + dt_bias_d)          (or without the softplus)
 //   h_t  = exp(dt_t A_dn) h_{t-1} + dt_t u_t B_tn,   y_t = sum_n C_tn h_tn + D_d u_t,
 //   out_t = y_t silu(z_t)                           (or y_t without a gate).
-// One warp walks a run of tokens for CH = 128 / N channels: lane
-// ch * LPC + q holds states 4q .. 4q+3 of channel ch in registers, so a token
-// costs four exponentials and about 16 fp32 operations per lane.  Tokens come in
-// tiles of kSsmChunk = 16: lane l first takes the l-th share of the tile's
-// (token, channel) elements, forms dt and x = dt u once per element and puts
-// them, B and C into the warp's shared memory as fp32; the 16 tokens then run
-// from there without a branch (a token after the end has dt = x = 0, which
+// One warp walks a run of tokens for CH = 32 NS / N channels: lane
+// ch * LPC + q holds states NS q .. NS q + NS - 1 of channel ch in registers, so
+// a token costs NS exponentials and about 4 NS fp32 operations per lane.  Tokens
+// come in tiles of kSsmChunk = 16: lane l first takes the l-th share of the
+// tile's (token, channel) elements, forms dt and x = dt u once per element and
+// puts them, B and C into the warp's shared memory as fp32; the 16 tokens then
+// run from there without a branch (a token after the end has dt = x = 0, which
 // leaves the state as it is).
 #pragma once
 
@@ -26,28 +26,28 @@ constexpr int K = kSsmChunk;
 
 // K tokens x CH channels over 32 lanes: token lane / PARTS, EPL channels from
 // (lane % PARTS) * EPL.
-template <int N>
+template <int N, int NS>
 struct Geo {
-    static constexpr int LPC = N / 4;
+    static constexpr int LPC = N / NS;
     static constexpr int CH = 32 / LPC;
     static constexpr int EPL = CH >= 2 ? CH / 2 : 1;
     static constexpr int PARTS = CH >= 2 ? 2 : 1;
 };
 
 // B or C rows of a tile: K x N elements in pieces of PE, NP pieces per lane.
-template <typename T, int N>
+template <typename T, int N, bool VEC>
 struct RowTile {
     static constexpr int PE = (N / 2 < 16 / static_cast<int>(sizeof(T))) ? N / 2 : 16 / static_cast<int>(sizeof(T));
     static constexpr int NP = N / 2 / PE;
     Raw<T, PE> v[NP];
 
     // rows: the tile's first row at this group's column 0; nt rows are valid
-    __device__ __forceinline__ void load(const T* rows, long long stride, bool vec, int nt, int lane) {
+    __device__ __forceinline__ void load(const T* rows, long long stride, int nt, int lane) {
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
             const int id = p * 32 + lane;
             const int tok = id / (N / PE), n0 = id % (N / PE) * PE;
-            v[p] = load_raw<T, PE>(rows + tok * stride + n0, vec, tok < nt ? PE : 0);
+            v[p] = load_raw<T, PE, VEC>(rows + tok * stride + n0, tok < nt ? PE : 0);
         }
     }
     __device__ __forceinline__ void store(float* dst, int lane) const {  // [K][N]
@@ -62,10 +62,18 @@ struct RowTile {
     }
 };
 
-// Whether rows at p can be read E elements at a time.
-template <typename T>
-__device__ __forceinline__ bool can_vec(const void* p, long long stride, int E) {
-    return reinterpret_cast<uintptr_t>(p) % (E * sizeof(T)) == 0 && stride % E == 0;
+// Whether every activation of the scan can be accessed in the vectors of this
+// geometry (decided on the host: the kernels have no branch on it).
+template <typename T, int N, int NS>
+bool all_vec(const SsmArgs& a) {
+    constexpr int EPL = Geo<N, NS>::EPL, PE = RowTile<T, N, true>::PE;
+    auto ok = [](const void* p, long long stride, int e) {
+        const int bytes = e * static_cast<int>(sizeof(T)) < 16 ? e * static_cast<int>(sizeof(T)) : 16;
+        return reinterpret_cast<uintptr_t>(p) % bytes == 0 && stride * static_cast<long long>(sizeof(T)) % bytes == 0;
+    };
+    return a.D / a.G % EPL == 0 && ok(a.u, a.u_stride, EPL) && ok(a.dt, a.dt_stride, EPL) &&
+           (!a.z || ok(a.z, a.z_stride, EPL)) && ok(a.out, a.D, EPL) && ok(a.Bm, a.B_stride, PE) &&
+           ok(a.Cm, a.C_stride, PE);
 }
 
 // Sums over the LPC lanes of a channel of v[t], t < K: value i of lane q is
@@ -99,6 +107,14 @@ __device__ __forceinline__ void put_channel_sums(float (&v)[K], int q, int ch, f
     for (int i = 0; i < K / M; ++i) out[(i * M + q % M) * CH + ch] = v[i];
 }
 
+// Sum over the token lanes that share a channel share (same lane % PARTS).
+template <int PARTS>
+__device__ __forceinline__ float over_tokens(float x) {
+#pragma unroll
+    for (int m = PARTS; m < 32; m *= 2) x += __shfl_xor_sync(0xffffffffu, x, m);
+    return x;
+}
+
 // Where a warp works: segment `slot` of the tokens, one block of CH channels.
 struct Place {
     int n, b, t0, t1;         // sequence, batch row, its token range
@@ -106,6 +122,7 @@ struct Place {
     bool first, last;         // segment of its sequence
     int g, d0, nd;            // group, first channel, channels (<= CH)
     long long chunk0;         // the segment's first slot of the saved chunk states
+    long long slot;           // the segment itself
 };
 
 template <int CH>
@@ -115,6 +132,7 @@ __device__ __forceinline__ bool find_place(const SsmArgs& p, long long slot, int
     if (!token_range(p.cu_seqlens, w.n, p.nseq, p.T, p.err, w.b, w.t0, w.t1)) return false;
     const long long begin = w.t0 + c * seg;
     w.first = c == 0;
+    w.slot = slot;
     if (begin >= w.t1 && !w.first) return false;  // no such segment
     w.s0 = static_cast<int>(begin);
     w.s1 = static_cast<int>(min(begin + seg, static_cast<long long>(w.t1)));

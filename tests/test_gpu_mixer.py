@@ -209,6 +209,24 @@ def test_scan(case, dtype):
     _scan_check(case, dtype)
 
 
+# Few channels and many tokens: the scan runs in segments joined afterwards.
+LONG = [
+    (1, 1100, 20, 1, 16, None, True, False, True, True),
+    (2, 700, 9, 1, 8, None, False, True, False, True),
+    (1, 1500, 18, 2, 32, [0, 700, 700, 701, 1400, 1500], True, False, True, True),
+    (1, 640, 3, 1, 64, [0, 1, 640], True, True, True, False),
+    (1, 520, 4, 1, 128, None, True, False, True, True),
+]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("case", LONG, ids=str)
+def test_long_scan(case, dtype):
+    B, T, D, G, N, cu = case[:6]
+    assert gdn.load().gdn_ssm_fwd_workspace_size(len(cu) - 1 if cu else B, T, D, G, N, int(cu is not None)) > 0
+    _scan_check(case, dtype)
+
+
 def test_scan_without_skip_or_bias():
     a, t = _scan_inputs(SCAN[4], F32)
     args = (t["u"], t["dt"], t["A"], t["B"], t["C"])
