@@ -551,7 +551,7 @@ GDN_API gdn_status gdn_conv_step(const void* x, int64_t x_stride, const float* w
  *   initial_state (nseq,D,N) or NULL;  final_state (nseq,D,N) or NULL
  *   out           (B,T,D)
  *   saved         NULL, or gdn_ssm_saved_size() bytes that the backward reads:
- *                 the state before every 16 tokens
+ *                 the state before every 8 tokens
  *   N in {8, 16, 32, 64, 128}
  */
 GDN_API size_t gdn_ssm_saved_size(int B, int T, int D, int N, int varlen);

@@ -249,7 +249,11 @@ __global__ void __launch_bounds__(kThreads) conv_step_kernel(const ConvStepArgs 
     Raw<T, E> in[W];
 #pragma unroll
     for (int r = 0; r < W - 1; ++r) {  // not the read-only path: out_state may be the same memory
-        in[r] = *reinterpret_cast<const Raw<T, E>*>(st + r * static_cast<long long>(p.D));
+        const T* row = st + r * static_cast<long long>(p.D);
+        if constexpr (E * sizeof(T) >= 4)
+            in[r] = *reinterpret_cast<const Raw<T, E>*>(row);
+        else
+            in[r].w[0] = *row;
     }
     in[W - 1] = load_raw<T, E>(static_cast<const T*>(p.x) + b * p.x_stride + d0, E);
     float w[W][E], o[E];

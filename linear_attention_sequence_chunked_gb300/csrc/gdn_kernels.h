@@ -397,7 +397,7 @@ struct SsmArgs {
     void* dz;
     float* d_initial_state;       // (nseq, D, N) or null
     float* bc_part;               // [channel blocks][rows][2 N]
-    float* par_part;              // [nseq][ssm_par_stride]: dA (D N), dD (D), ddt_bias (D)
+    float* par_part;              // [slots][ssm_par_stride]: dA (D N), dD (D), ddt_bias (D)
     // A long scan over few channels runs as segments of `seg` tokens (a multiple
     // of kSsmChunk; slots in all, as find_block counts): carry [slot][D][N] and
     // carry_dt [slot][D] join them.  Unsplit: seg 2^30, slots nseq, carry null.
@@ -437,7 +437,7 @@ struct SsmBcArgs {
     int G, N, blocks;             // blocks per group
     int dtype;
 };
-constexpr int kSsmChunk = 16;
+constexpr int kSsmChunk = 8;  // tokens between saved states
 // a partial row's length, so that every row's dA takes 16-byte stores
 __host__ __device__ inline long long ssm_par_stride(int D, int N) { return (static_cast<long long>(D) * (N + 2) + 3) / 4 * 4; }
 int ssm_group_blocks(int D, int G, int N);  // channel blocks of the backward, per group

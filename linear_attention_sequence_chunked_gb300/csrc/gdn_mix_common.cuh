@@ -19,11 +19,16 @@ __device__ __forceinline__ T from_f32(float x) {
         return x;
 }
 
-// E consecutive elements as they lie in memory.  Alignment lets load_raw and
-// store_raw move them in accesses of up to 16 bytes.
+// E consecutive elements as they lie in memory, held as the 32-bit words that
+// wide loads fill, so that nothing touches them before they are unpacked.
 template <typename T, int E>
-struct alignas(sizeof(T) * E >= 16 ? 16 : sizeof(T) * E) Raw {
-    T v[E];
+struct alignas(sizeof(T) * E >= 16 ? 16 : (sizeof(T) * E + 3) / 4 * 4) Raw {
+    static constexpr int kWords = (static_cast<int>(sizeof(T)) * E + 3) / 4;
+    uint32_t w[kWords];
+    __device__ __forceinline__ float get(int i) const {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+        return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+    }
 };
 
 // Read-only loads under a predicate, zero where it is false.  Written as
@@ -54,31 +59,27 @@ __device__ __forceinline__ uint32_t load_4(const void* p, bool on) {
                  : "l"(p), "r"(static_cast<int>(on)));
     return r;
 }
-__device__ __forceinline__ uint16_t load_2(const void* p, bool on) {
-    uint16_t r;
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %2, 0;\n\tmov.b16 %0, 0;\n\t@p ld.global.nc.b16 %0, [%1];\n\t}"
-                 : "=&h"(r)
-                 : "l"(p), "r"(static_cast<int>(on)));
+
+// One element where it lies, as the 32-bit register that the load fills (no
+// conversion before its use); `on` false: zero.
+template <typename T, bool PRED = true>
+__device__ __forceinline__ uint32_t load_one(const T* p, bool on = true) {
+    uint32_t r;
+    if constexpr (PRED && sizeof(T) == 2)
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %2, 0;\n\tmov.b32 %0, 0;\n\t@p ld.global.nc.u16 %0, [%1];\n\t}"
+                     : "=&r"(r)
+                     : "l"(p), "r"(static_cast<int>(on)));
+    else if constexpr (PRED)
+        r = load_4(p, on);
+    else if constexpr (sizeof(T) == 2)
+        asm volatile("ld.global.nc.u16 %0, [%1];" : "=r"(r) : "l"(p));
+    else
+        asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(r) : "l"(p));
     return r;
 }
-
-// One element where it lies; `on` false: zero.
-template <typename T, bool PRED = true>
-__device__ __forceinline__ T load_one(const T* p, bool on = true) {
-    if constexpr (PRED) {
-        if constexpr (sizeof(T) == 2)
-            return load_2(p, on);
-        else
-            return __uint_as_float(load_4(p, on));
-    } else if constexpr (sizeof(T) == 2) {
-        uint16_t r;
-        asm volatile("ld.global.nc.b16 %0, [%1];" : "=h"(r) : "l"(p));
-        return r;
-    } else {
-        float r;
-        asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(r) : "l"(p));
-        return r;
-    }
+template <typename T>
+__device__ __forceinline__ float one_f32(uint32_t r) {
+    return __uint_as_float(sizeof(T) == 2 ? r << 16 : r);
 }
 
 // Elements [0, n) of the E at p (n < E at the right edge of a row; 0: none).
@@ -87,21 +88,26 @@ __device__ __forceinline__ T load_one(const T* p, bool on = true) {
 template <typename T, int E, bool VEC = true>
 __device__ __forceinline__ Raw<T, E> load_raw(const T* p, int n) {
     Raw<T, E> r;
-    if constexpr (VEC && sizeof(r) % 16 == 0) {
+    constexpr int bytes = static_cast<int>(sizeof(T)) * E;
+    if constexpr (VEC && bytes % 16 == 0) {
 #pragma unroll
-        for (int i = 0; i < static_cast<int>(sizeof(r) / 16); ++i)
-            reinterpret_cast<uint4*>(&r)[i] = load_16(reinterpret_cast<const uint4*>(p) + i, n > 0);
-    } else if constexpr (VEC && sizeof(r) == 8) {
-        *reinterpret_cast<uint2*>(&r) = load_8(p, n > 0);
-    } else if constexpr (VEC && sizeof(r) == 4) {
-        *reinterpret_cast<uint32_t*>(&r) = load_4(p, n > 0);
+        for (int i = 0; i < bytes / 16; ++i) {
+            const uint4 x = load_16(reinterpret_cast<const uint4*>(p) + i, n > 0);
+            r.w[4 * i] = x.x; r.w[4 * i + 1] = x.y; r.w[4 * i + 2] = x.z; r.w[4 * i + 3] = x.w;
+        }
+    } else if constexpr (VEC && bytes == 8) {
+        const uint2 x = load_8(p, n > 0);
+        r.w[0] = x.x; r.w[1] = x.y;
+    } else if constexpr (VEC && bytes == 4) {
+        r.w[0] = load_4(p, n > 0);
+    } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < E; ++i) r.w[i] = load_4(p + i, i < n);
     } else {
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-            if constexpr (sizeof(T) == 2)
-                r.v[i] = load_2(p + i, i < n);
-            else
-                r.v[i] = __uint_as_float(load_4(p + i, i < n));
+        for (int i = 0; i < E; i += 2) {
+            r.w[i / 2] = load_one(p + i, i < n);
+            if (i + 1 < E) r.w[i / 2] |= load_one(p + i + 1, i + 1 < n) << 16;
         }
     }
     return r;
@@ -109,36 +115,47 @@ __device__ __forceinline__ Raw<T, E> load_raw(const T* p, int n) {
 
 template <typename T, int E, bool VEC = true>
 __device__ __forceinline__ void store_raw(T* p, const Raw<T, E>& r, int n) {
-    if constexpr (VEC) {
+    constexpr int bytes = static_cast<int>(sizeof(T)) * E;
+    if constexpr (VEC && bytes >= 4) {
         if (n <= 0) return;
-        if constexpr (sizeof(r) % 16 == 0) {
-            const uint4* s = reinterpret_cast<const uint4*>(&r);
+        if constexpr (bytes % 16 == 0) {
 #pragma unroll
-            for (int i = 0; i < static_cast<int>(sizeof(r) / 16); ++i) reinterpret_cast<uint4*>(p)[i] = s[i];
-        } else if constexpr (sizeof(r) == 8) {
-            *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(&r);
-        } else if constexpr (sizeof(r) == 4) {
-            *reinterpret_cast<uint32_t*>(p) = *reinterpret_cast<const uint32_t*>(&r);
+            for (int i = 0; i < bytes / 16; ++i)
+                reinterpret_cast<uint4*>(p)[i] = make_uint4(r.w[4 * i], r.w[4 * i + 1], r.w[4 * i + 2], r.w[4 * i + 3]);
+        } else if constexpr (bytes == 8) {
+            *reinterpret_cast<uint2*>(p) = make_uint2(r.w[0], r.w[1]);
         } else {
-            p[0] = r.v[0];
+            *reinterpret_cast<uint32_t*>(p) = r.w[0];
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < E; ++i)
-            if (i < n) p[i] = r.v[i];
+        for (int i = 0; i < E; ++i) {
+            if (i >= n) continue;
+            if constexpr (sizeof(T) == 4)
+                p[i] = __uint_as_float(r.w[i]);
+            else
+                p[i] = static_cast<uint16_t>(i & 1 ? r.w[i / 2] >> 16 : r.w[i / 2]);
+        }
     }
 }
 
 template <typename T, int E>
 __device__ __forceinline__ void unpack(const Raw<T, E>& r, float* x) {
 #pragma unroll
-    for (int i = 0; i < E; ++i) x[i] = to_f32(r.v[i]);
+    for (int i = 0; i < E; ++i) x[i] = r.get(i);
 }
 template <typename T, int E>
 __device__ __forceinline__ Raw<T, E> pack(const float* x) {
     Raw<T, E> r;
 #pragma unroll
-    for (int i = 0; i < E; ++i) r.v[i] = from_f32<T>(x[i]);
+    for (int i = 0; i < E; ++i) {
+        if constexpr (sizeof(T) == 4)
+            r.w[i] = __float_as_uint(x[i]);
+        else if (i & 1)
+            r.w[i / 2] |= static_cast<uint32_t>(f32_to_bf16(x[i])) << 16;
+        else
+            r.w[i / 2] = f32_to_bf16(x[i]);
+    }
     return r;
 }
 

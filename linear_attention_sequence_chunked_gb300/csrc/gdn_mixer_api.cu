@@ -110,14 +110,16 @@ void set_split(gdn::SsmArgs& a, const SsmSplit& s, void* workspace) {
 }
 
 struct SsmBwdLayout {
-    size_t bc, par, total;
+    size_t bc, par, carry, total;
 };
 SsmBwdLayout ssm_bwd_layout(int B, int T, int D, int G, int N, bool varlen) {
     SsmBwdLayout L{};
     const long long rows = varlen ? T : static_cast<long long>(B) * T;
     L.bc = 0;
     L.par = round_up(sizeof(float) * gdn::ssm_group_blocks(D, G, N) * static_cast<long long>(G) * rows * 2 * N);
-    L.total = L.par + round_up(sizeof(float) * B * gdn::ssm_par_stride(D, N));
+    const SsmSplit split = ssm_split(B, T, D, G, N, varlen);
+    L.carry = L.par + round_up(sizeof(float) * split.slots * gdn::ssm_par_stride(D, N));
+    L.total = L.carry + split.total;
     return L;
 }
 
@@ -289,7 +291,9 @@ gdn_status gdn_ssm_bwd(const void* u, int64_t u_stride, const void* dt, int64_t 
     a.d_initial_state = d_initial_state;
     a.bc_part = reinterpret_cast<float*>(ws + L.bc); a.par_part = reinterpret_cast<float*>(ws + L.par);
     a.nseq = B; a.T = T; a.D = D; a.G = G; a.N = N; a.dtype = dtype; a.err = err;
-    if (!gdn::count_launch(gdn::launch_ssm_bwd(a, stream))) return GDN_ERR_CUDA;
+    const SsmSplit split = ssm_split(B, T, D, G, N, varlen);
+    set_split(a, split, ws + L.carry);
+    if (!gdn::count_launch(gdn::launch_ssm_bwd(a, stream), split.total ? 3 : 1)) return GDN_ERR_CUDA;
     gdn::SsmBcArgs bc{};
     bc.bc_part = a.bc_part; bc.dB = dB; bc.dC = dC; bc.rows = varlen ? T : static_cast<long long>(B) * T;
     bc.G = G; bc.N = N; bc.blocks = gdn::ssm_group_blocks(D, G, N); bc.dtype = dtype;
@@ -297,7 +301,7 @@ gdn_status gdn_ssm_bwd(const void* u, int64_t u_stride, const void* dt, int64_t 
     gdn::ColumnSumArgs c{};
     c.partial = a.par_part; c.c0 = static_cast<long long>(D) * N; c.c1 = D; c.cols = c.c0 + 2LL * D;
     c.stride = gdn::ssm_par_stride(D, N);
-    c.rows = B; c.out[0] = dA; c.out[1] = dD; c.out[2] = ddt_bias;
+    c.rows = static_cast<int>(split.slots); c.out[0] = dA; c.out[1] = dD; c.out[2] = ddt_bias;
     return gdn::count_launch(gdn::launch_column_sum(c, stream)) ? GDN_OK : GDN_ERR_CUDA;
 }
 

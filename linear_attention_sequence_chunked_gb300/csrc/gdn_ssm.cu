@@ -9,77 +9,32 @@ namespace {
 
 using namespace ssm;
 
-constexpr int kWarps = 4;
-constexpr int kTile = 8;  // tokens whose inputs are held at a time; divides kSsmChunk
-
-// A lane holds NL = min(N, 16) states of one channel, four at a time: group j
-// of lane q of a channel's LPC = N / NL lanes is states 4 (j LPC + q) .. + 3, so
-// that those lanes read neighbouring 16 bytes of a row of B.  CH channels per
-// warp; with N <= 16 a lane is a channel and a row of 32 channels one access.
-template <int N>
-struct Lanes {
-    static constexpr int NL = N < 16 ? N : 16;
-    static constexpr int LPC = N / NL;
-    static constexpr int CH = 32 / LPC;
-    static constexpr int GR = NL / 4;
+// A warp's tiles: what is on its way from global memory, and B and C as fp32.
+template <typename T, int N, bool kOut>
+struct alignas(16) FwdStage {
+    static constexpr int CH = Lanes<N>::CH;
+    T u[kTile][CH], dt[kTile][CH];
+    T B[kTile][N];
+    T z[kOut ? kTile : 0][CH];
+    T C[kOut ? kTile : 0][N];
 };
-
-// B or C rows of a tile, [kTile][N] as fp32 in shared memory: read from global
-// a tile ahead (16 bytes per access where VEC), put there when its turn comes.
-template <typename T, int N, bool VEC>
-struct Rows {
-    static constexpr int PE = VEC ? (N * kTile / 32 < 16 / static_cast<int>(sizeof(T)) ? N * kTile / 32 : 16 / static_cast<int>(sizeof(T))) : 1;
-    static constexpr int NP = N * kTile / 32 / PE;
-    Raw<T, PE> v[NP];
-    __device__ __forceinline__ void load(const T* rows, long long stride, int nt, int lane) {
-#pragma unroll
-        for (int i = 0; i < NP; ++i) {
-            const int id = i * 32 + lane, tok = id / (N / PE), n0 = id % (N / PE) * PE;
-            v[i] = load_raw<T, PE>(rows + tok * stride + n0, tok < nt ? PE : 0);
-        }
-    }
-    __device__ __forceinline__ void store(float* dst, int lane) const {
-#pragma unroll
-        for (int i = 0; i < NP; ++i) {
-            float x[PE];
-            unpack<T, PE>(v[i], x);
-#pragma unroll
-            for (int e = 0; e < PE; ++e) dst[(i * 32 + lane) * PE + e] = x[e];
-        }
-    }
+template <typename T, int N, bool kOut>
+struct alignas(16) FwdShared {
+    FwdStage<T, N, kOut> stage[kStages];
+    float B[kTile][N];
+    float C[kOut ? kTile : 0][N];
 };
-
-// The states of a lane, as register pairs, from or to a channel's N floats.
-template <int N>
-__device__ __forceinline__ void load_states(const float* p, int q, Two (&v)[Lanes<N>::NL / 2]) {
-#pragma unroll
-    for (int j = 0; j < Lanes<N>::GR; ++j) {
-        const float4 x = *reinterpret_cast<const float4*>(p + 4 * (j * Lanes<N>::LPC + q));
-        v[2 * j] = two(x.x, x.y);
-        v[2 * j + 1] = two(x.z, x.w);
-    }
-}
-template <int N>
-__device__ __forceinline__ void store_states(float* p, int q, const Two (&v)[Lanes<N>::NL / 2]) {
-#pragma unroll
-    for (int j = 0; j < Lanes<N>::GR; ++j) {
-        float4 x;
-        split(v[2 * j], x.x, x.y);
-        split(v[2 * j + 1], x.z, x.w);
-        *reinterpret_cast<float4*>(p + 4 * (j * Lanes<N>::LPC + q)) = x;
-    }
-}
 
 // kOut: the whole forward.  Without it, only the segment's end state from a
 // zero start and the sum of its dt (the first pass of a split scan).
 template <typename T, int N, bool kOut, bool VEC>
-__global__ void __launch_bounds__(32 * kWarps) ssm_fwd_kernel(const SsmArgs p, int blocks) {
+__global__ void __launch_bounds__(32 * kWarps, 3) ssm_fwd_kernel(const SsmArgs p, int blocks) {
     using L = Lanes<N>;
     constexpr int LPC = L::LPC, CH = L::CH, NL = L::NL;
-    __shared__ __align__(16) float tile_B[kWarps][kTile][N];
-    __shared__ __align__(16) float tile_C[kWarps][kOut ? kTile : 1][N];
+    extern __shared__ __align__(16) unsigned char smem[];
     if (blockIdx.x == 0) check_offsets(p.cu_seqlens, p.nseq, p.T, p.err);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    FwdShared<T, N, kOut>& sm = reinterpret_cast<FwdShared<T, N, kOut>*>(smem)[warp];
     const long long unit = static_cast<long long>(blockIdx.x) * kWarps + warp;
     const int nblk = blocks * p.G;
     if (unit >= p.slots * nblk) return;
@@ -106,70 +61,43 @@ __global__ void __launch_bounds__(32 * kWarps) ssm_fwd_kernel(const SsmArgs p, i
     const float dskip = kOut && p.D_skip && q == 0 ? p.D_skip[d] : 0.f;
     const float bias = p.dt_bias ? p.dt_bias[d] : 0.f;
     float sum = 0.f;
-    const long long row0 = static_cast<long long>(w.b) * p.T;
-    const T* u = static_cast<const T*>(p.u) + row0 * p.u_stride + d;
-    const T* dt = static_cast<const T*>(p.dt) + row0 * p.dt_stride + d;
-    const T* z = kOut && p.z ? static_cast<const T*>(p.z) + row0 * p.z_stride + d : nullptr;
+    const long long row0 = static_cast<long long>(w.b) * p.T + w.s0;
+    const T* u = static_cast<const T*>(p.u) + row0 * p.u_stride + w.d0;
+    const T* dt = static_cast<const T*>(p.dt) + row0 * p.dt_stride + w.d0;
+    const T* z = kOut && p.z ? static_cast<const T*>(p.z) + row0 * p.z_stride + w.d0 : nullptr;
     const T* Bm = static_cast<const T*>(p.Bm) + row0 * p.B_stride + w.g * N;
     const T* Cm = static_cast<const T*>(p.Cm) + row0 * p.C_stride + w.g * N;
     T* out = kOut ? static_cast<T*>(p.out) + row0 * p.D + d : nullptr;
-    // per-thread row pointers move a tile at a time; the rows in between are
-    // uniform offsets
-    u += w.s0 * p.u_stride;
-    dt += w.s0 * p.dt_stride;
-    Bm += w.s0 * p.B_stride;
-    Cm += w.s0 * p.C_stride;
-    if (kOut) {
-        out += w.s0 * static_cast<long long>(p.D);
-        if (z) z += w.s0 * p.z_stride;
-    }
-    T u_in[kTile], dt_in[kTile];
-    Rows<T, N, VEC> b_in, c_in;
-    // the next tile's inputs; `left` tokens remain (none: nothing is read)
-    auto load = [&](int left) {
-        b_in.load(Bm, p.B_stride, left, lane);
-        if (kOut) c_in.load(Cm, p.C_stride, left, lane);
-        if (left >= kTile) {
-#pragma unroll
-            for (int k = 0; k < kTile; ++k) {
-                u_in[k] = load_one<T, false>(u + k * p.u_stride);
-                dt_in[k] = load_one<T, false>(dt + k * p.dt_stride);
-            }
-        } else {
-#pragma unroll
-            for (int k = 0; k < kTile; ++k) {
-                u_in[k] = load_one(u + k * p.u_stride, k < left);
-                dt_in[k] = load_one(dt + k * p.dt_stride, k < left);
+    const int len = w.s1 - w.s0;
+    auto fetch = [&](int t) {  // the tile at token t, if there is one
+        if (t < len) {
+            FwdStage<T, N, kOut>& st = sm.stage[t / kTile % kStages];
+            fill_tile<T, CH, VEC>(&st.u[0][0], u + t * p.u_stride, p.u_stride, len - t, w.nd, lane);
+            fill_tile<T, CH, VEC>(&st.dt[0][0], dt + t * p.dt_stride, p.dt_stride, len - t, w.nd, lane);
+            fill_tile<T, N, VEC>(&st.B[0][0], Bm + t * p.B_stride, p.B_stride, len - t, N, lane);
+            if constexpr (kOut) {
+                if (z) fill_tile<T, CH, VEC>(&st.z[0][0], z + t * p.z_stride, p.z_stride, len - t, w.nd, lane);
+                fill_tile<T, N, VEC>(&st.C[0][0], Cm + t * p.C_stride, p.C_stride, len - t, N, lane);
             }
         }
-        u += kTile * p.u_stride;
-        dt += kTile * p.dt_stride;
-        Bm += kTile * p.B_stride;
-        Cm += kTile * p.C_stride;
+        commit_copies();
     };
-
-    load(w.s1 - w.s0);
-    for (int left = w.s1 - w.s0, done = 0; left > 0; left -= kTile, done += kTile) {
-        if (kOut && p.saved && mine && done % kSsmChunk == 0)
-            store_states<N>(p.saved + ((w.chunk0 + done / kSsmChunk) * p.D + d) * N, q, h);
-        b_in.store(&tile_B[warp][0][0], lane);
-        if (kOut) c_in.store(&tile_C[warp][0][0], lane);
-        T z_in[kTile];
-        if (z) {
-            if (left >= kTile) {
 #pragma unroll
-                for (int k = 0; k < kTile; ++k) z_in[k] = load_one<T, false>(z + k * p.z_stride);
-            } else {
-#pragma unroll
-                for (int k = 0; k < kTile; ++k) z_in[k] = load_one(z + k * p.z_stride, k < left);
-            }
-            z += kTile * p.z_stride;
-        }
+    for (int i = 0; i < kStages - 1; ++i) fetch(i * kTile);
+    for (int t = 0; t < len; t += kTile) {
+        if (kOut && p.saved && mine) store_states<N>(p.saved + ((w.chunk0 + t / kTile) * p.D + d) * N, q, h);
+        wait_copies<kStages - 2>();
+        __syncwarp();  // the tile is there, and everyone is through with the one before
+        fetch(t + (kStages - 1) * kTile);
+        const FwdStage<T, N, kOut>& st = sm.stage[t / kTile % kStages];
+        widen_rows<T, N>(&st.B[0][0], &sm.B[0][0], lane);
+        if constexpr (kOut) widen_rows<T, N>(&st.C[0][0], &sm.C[0][0], lane);
+        const int left = len - t;
         Two d2[kTile], x2[kTile], y2[kTile];
 #pragma unroll
         for (int k = 0; k < kTile; ++k) {
-            const float uk = to_f32(u_in[k]);
-            float dk = to_f32(dt_in[k]) + bias;
+            const float uk = to_f32(st.u[k][ch]);
+            float dk = to_f32(st.dt[k][ch]) + bias;
             if (p.softplus) dk = softplus(dk);
             if (left < kTile) dk = k < left ? dk : 0.f;
             if (!kOut) sum += dk;
@@ -177,37 +105,34 @@ __global__ void __launch_bounds__(32 * kWarps) ssm_fwd_kernel(const SsmArgs p, i
             x2[k] = two(dk * uk, dk * uk);
             if (kOut) y2[k] = two(dskip * uk, 0.f);
         }
-        load(left - kTile);
         __syncwarp();
 #pragma unroll
         for (int j = 0; j < L::GR; ++j) {
 #pragma unroll
             for (int k = 0; k < kTile; ++k) {
-                const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(&tile_B[warp][k][4 * (j * LPC + q)]);
+                const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(&sm.B[k][4 * (j * LPC + q)]);
                 h[2 * j] = fma2(ex2_2(mul2(d2[k], A2[2 * j])), h[2 * j], mul2(x2[k], Two{b.x}));
                 h[2 * j + 1] = fma2(ex2_2(mul2(d2[k], A2[2 * j + 1])), h[2 * j + 1], mul2(x2[k], Two{b.y}));
-                if (kOut) {
-                    const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(&tile_C[warp][k][4 * (j * LPC + q)]);
+                if constexpr (kOut) {
+                    const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(&sm.C[k][4 * (j * LPC + q)]);
                     y2[k] = fma2(h[2 * j], Two{c.x}, y2[k]);
                     y2[k] = fma2(h[2 * j + 1], Two{c.y}, y2[k]);
                 }
             }
         }
-        __syncwarp();  // the next tile overwrites this one
-        if (kOut) {
+        if constexpr (kOut) {
             float y[kTile];
 #pragma unroll
             for (int k = 0; k < kTile; ++k) {
-                float lo, hi;
-                split(y2[k], lo, hi);
-                lo += hi;
+                float hi;
+                split(y2[k], y[k], hi);
+                y[k] += hi;
 #pragma unroll
-                for (int m = 1; m < LPC; m *= 2) lo += __shfl_xor_sync(0xffffffffu, lo, m);
+                for (int m = 1; m < LPC; m *= 2) y[k] += __shfl_xor_sync(0xffffffffu, y[k], m);
                 if (z) {
-                    const float zk = to_f32(z_in[k]);
-                    lo *= zk * sigmoid(zk);
+                    const float zk = to_f32(st.z[k][ch]);
+                    y[k] *= zk * sigmoid(zk);
                 }
-                y[k] = lo;
             }
             if (mine) {
 #pragma unroll
@@ -340,23 +265,21 @@ template <typename T, int N, bool VEC>
 cudaError_t fwd_v(const SsmArgs& a, cudaStream_t stream) {
     const int blocks = (a.D / a.G + Lanes<N>::CH - 1) / Lanes<N>::CH;
     const long long units = a.slots * blocks * a.G;
-    const unsigned grid = static_cast<unsigned>((units + kWarps - 1) / kWarps);
     if (a.carry) {
-        ssm_fwd_kernel<T, N, false, VEC><<<grid, 32 * kWarps, 0, stream>>>(a, blocks);
-        const cudaError_t e = launch_compose(a, false, stream);
+        cudaError_t e = launch_warps(ssm_fwd_kernel<T, N, false, VEC>, units, sizeof(FwdShared<T, N, false>), a, blocks, stream);
+        if (e == cudaSuccess) e = launch_compose(a, false, stream);
         if (e != cudaSuccess) return e;
     }
-    ssm_fwd_kernel<T, N, true, VEC><<<grid, 32 * kWarps, 0, stream>>>(a, blocks);
-    return cudaGetLastError();
+    return launch_warps(ssm_fwd_kernel<T, N, true, VEC>, units, sizeof(FwdShared<T, N, true>), a, blocks, stream);
 }
 
 template <typename T, int N>
 cudaError_t fwd_n(const SsmArgs& a, cudaStream_t stream) {
-    constexpr int bytes = Rows<T, N, true>::PE * static_cast<int>(sizeof(T));
-    auto ok = [](const void* p, long long stride) {
-        return reinterpret_cast<uintptr_t>(p) % bytes == 0 && stride * static_cast<long long>(sizeof(T)) % bytes == 0;
-    };
-    return ok(a.Bm, a.B_stride) && ok(a.Cm, a.C_stride) ? fwd_v<T, N, true>(a, stream) : fwd_v<T, N, false>(a, stream);
+    constexpr int CH = Lanes<N>::CH;
+    const bool vec = a.D / a.G * sizeof(T) % piece_bytes<T, CH> == 0 && takes_pieces<T, CH>(a.u, a.u_stride) &&
+                     takes_pieces<T, CH>(a.dt, a.dt_stride) && (!a.z || takes_pieces<T, CH>(a.z, a.z_stride)) &&
+                     takes_pieces<T, N>(a.Bm, a.B_stride) && takes_pieces<T, N>(a.Cm, a.C_stride);
+    return vec ? fwd_v<T, N, true>(a, stream) : fwd_v<T, N, false>(a, stream);
 }
 
 template <typename T, int N>
@@ -391,7 +314,7 @@ int ssm_segment(int nseq, int T, int D, int G, int N, bool varlen) {
     const int ch = N <= 16 ? 32 : 512 / N;
     const long long warps = static_cast<long long>(varlen ? 1 : nseq) * G * ((D / G + ch - 1) / ch);
     if (warps >= 456 || T < 256) return 1 << 30;
-    const long long segs = 1824 / warps;  // one wave of 12 warps per SM
+    const long long segs = 152 * 12 / warps;  // one wave of 12 warps per SM
     const int seg = static_cast<int>(((T + segs - 1) / segs + kSsmChunk - 1) / kSsmChunk * kSsmChunk);
     return seg < 64 ? 64 : seg;
 }

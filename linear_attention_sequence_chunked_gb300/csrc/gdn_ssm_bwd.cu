@@ -6,12 +6,17 @@
 //   q_t  = a_t e_t h_{t-1}:  ddt_t = u_t dx_t + sum_n A q_t,   dA = sum_t dt_t q_t
 //   du_t = dt_t dx_t + D dy_t,   dD = sum_t dy_t u_t,   dz_t = d_out_t y_t silu'(z_t)
 //   ddt_raw = ddt sigmoid(dt_raw + bias),   ddt_bias = sum_t ddt_raw.
-// A warp walks its tokens from the last tile to the first.  It reads the tile's
-// start state that the forward kept, runs the tile forward once more with the
-// 16 decays and states in registers, then back.  Sums over a channel's lanes
-// and over the warp's channels halve the values with each shuffle.  dB and dC
-// of a warp's CH channels go out as partial rows, dA, dD and ddt_bias as one
-// partial row per sequence; two small kernels add those up in a fixed order.
+// A warp walks its tokens from the last tile to the first.  Four states at a
+// time it takes the state before the tile, which the forward kept, runs the
+// tile forward once more with the decays and states in registers, then back.
+// The eight sums over channels per token (dB and dC of four states) halve with
+// each of the first three shuffles; a warp's sums for its 32 channels go out as
+// partial rows, dA, dD and ddt_bias as one partial row per segment, and two
+// small kernels add those up in a fixed order.  A long scan over few channels
+// runs in segments: a pass that only carries the state gradient back, the
+// composition, then this.  Bound by instruction issue: about 16 paired
+// operations, 4 exponentials and 32 instructions of the sums over channels per
+// token and four states.
 #include "gdn_ssm_common.cuh"
 
 namespace gdn {
@@ -19,9 +24,6 @@ namespace gdn {
 namespace {
 
 using namespace ssm;
-
-template <int N>
-constexpr int kWarps = N >= 64 ? 2 : 4;
 
 // Sums of v[0..7] over the CH channels of a warp (lanes LPC apart): value i of
 // channel lane ch is then the sum of v[i * min(CH, 8) + ch mod 8].
@@ -45,186 +47,275 @@ __device__ __forceinline__ void across_channels(float (&v)[8], int ch) {
     }
 }
 
-template <typename T, int N, bool VEC>
-__global__ void __launch_bounds__(32 * kWarps<N>) ssm_bwd_kernel(const SsmArgs p, int seg, long long slots, int blocks) {
-    using G = Geo<N, 4>;
-    constexpr int CH = G::CH, EPL = G::EPL, LPC = G::LPC;
+// kFull: the whole reverse mode.  Without it, only the state gradient that a
+// segment sends to the one before it, from a zero one at its end, and the sum
+// of its dt.
+template <typename T, int N, bool kFull>
+struct alignas(16) BwdStage {
+    static constexpr int CH = Lanes<N>::CH;
+    T dt[kTile][CH], z[kTile][CH], d_out[kTile][CH];
+    T C[kTile][N];
+    T u[kFull ? kTile : 0][CH];
+    T B[kFull ? kTile : 0][N];
+    float saved[kFull ? CH : 0][N];
+};
+template <typename T, int N, bool kFull>
+struct alignas(16) BwdShared {
+    static constexpr int GR = Lanes<N>::GR;
+    BwdStage<T, N, kFull> stage[2];
+    float C[kTile][N];
+    float B[kFull ? kTile : 0][N];
+    // a lane's own: A log2(e), the state gradient, the sum for dA
+    float4 A2[GR][32], g[GR][32];
+    float4 dA[kFull ? GR : 0][32];
+    float bc[kFull ? kTile : 0][2 * N];
+};
+
+struct Four {
+    Two lo, hi;
+};
+__device__ __forceinline__ Four get4(const float* p) {
+    const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(p);
+    return Four{Two{x.x}, Two{x.y}};
+}
+__device__ __forceinline__ Four get4(const float4& p) { return get4(&p.x); }
+__device__ __forceinline__ void put4(float4& p, Four v) {
+    *reinterpret_cast<ulonglong2*>(&p) = make_ulonglong2(v.lo.v, v.hi.v);
+}
+__device__ __forceinline__ Four mul4(Four a, Two b) { return Four{mul2(a.lo, b), mul2(a.hi, b)}; }
+__device__ __forceinline__ Four mul4(Four a, Four b) { return Four{mul2(a.lo, b.lo), mul2(a.hi, b.hi)}; }
+__device__ __forceinline__ Four fma4(Four a, Two b, Four c) { return Four{fma2(a.lo, b, c.lo), fma2(a.hi, b, c.hi)}; }
+__device__ __forceinline__ Four fma4(Four a, Four b, Four c) { return Four{fma2(a.lo, b.lo, c.lo), fma2(a.hi, b.hi, c.hi)}; }
+__device__ __forceinline__ Two dot4(Four a, Four b, Two c) { return fma2(a.hi, b.hi, fma2(a.lo, b.lo, c)); }
+__device__ __forceinline__ Four ex2_4(Four a) { return Four{ex2_2(a.lo), ex2_2(a.hi)}; }
+// the sum of both halves, over a channel's LPC lanes
+template <int LPC>
+__device__ __forceinline__ float channel_sum(Two v) {
+    float lo, hi;
+    split(v, lo, hi);
+    lo += hi;
+#pragma unroll
+    for (int m = 1; m < LPC; m *= 2) lo += __shfl_xor_sync(0xffffffffu, lo, m);
+    return lo;
+}
+
+template <typename T, int N, bool kFull, bool VEC>
+__global__ void __launch_bounds__(32 * kWarps, 2) ssm_bwd_kernel(const SsmArgs p, int blocks) {
+    using L = Lanes<N>;
+    constexpr int CH = L::CH, LPC = L::LPC, GR = L::GR;
     constexpr int M8 = CH < 8 ? CH : 8;
-    struct alignas(16) Tile {
-        float2 dtx[K][CH];
-        float dy[K][CH];
-        float B[K][N];
-        float C[K][N];
-        float y[K][CH];
-        float dx[K][CH];
-        float da[K][CH];
-    };
-    __shared__ __align__(16) Tile tiles[kWarps<N>];
+    extern __shared__ __align__(16) unsigned char smem[];
     if (blockIdx.x == 0) check_offsets(p.cu_seqlens, p.nseq, p.T, p.err);
-    const int lane = threadIdx.x & 31;
-    const long long unit = static_cast<long long>(blockIdx.x) * kWarps<N> + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    BwdShared<T, N, kFull>& sm = reinterpret_cast<BwdShared<T, N, kFull>*>(smem)[warp];
+    const long long unit = static_cast<long long>(blockIdx.x) * kWarps + warp;
     const int nblk = blocks * p.G;
-    if (unit >= slots * nblk) return;
+    if (unit >= p.slots * nblk) return;
     const long long slot = unit / nblk;
     const int block = static_cast<int>(unit % nblk);
-    float* par = p.par_part + slot * ssm_par_stride(p.D, N);
-    Place w;
-    if (!find_place<CH>(p, slot, block, seg, blocks, w)) return;
-    Tile& tile = tiles[threadIdx.x >> 5];
-
     const int ch = lane / LPC, q = lane % LPC;
-    const bool mine = ch < w.nd;
-    const long long so = (static_cast<long long>(w.n) * p.D + w.d0 + ch) * N + 4 * q;
-    const long long ao = static_cast<long long>(w.d0 + ch) * N + 4 * q;
-    float A2[4], g[4], dA[4] = {0.f, 0.f, 0.f, 0.f};
-    {
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f), s = a;
-        if (mine) {
-            a = *reinterpret_cast<const float4*>(p.A + ao);
-            if (w.last && p.d_final_state) s = *reinterpret_cast<const float4*>(p.d_final_state + so);
+    Place w;
+    const bool found = find_place<CH>(p, slot, block, p.seg, blocks, w);
+    if (!kFull && (!found || w.first)) return;  // nothing comes before it
+    if (!found) {  // its row of the parameters' partial sums is read all the same
+        const int per = p.D / p.G, off = block % blocks * CH;
+        if (kFull && ch < min(CH, per - off)) {
+            const int d = block / blocks * per + off + ch;
+            float* par = p.par_part + slot * ssm_par_stride(p.D, N);
+            for (int j = 0; j < GR; ++j)
+                *reinterpret_cast<float4*>(par + static_cast<long long>(d) * N + 4 * (j * LPC + q)) = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (q == 0) par[static_cast<long long>(p.D) * N + d] = par[static_cast<long long>(p.D) * N + p.D + d] = 0.f;
         }
-        A2[0] = a.x * kLog2e; A2[1] = a.y * kLog2e; A2[2] = a.z * kLog2e; A2[3] = a.w * kLog2e;
-        g[0] = s.x; g[1] = s.y; g[2] = s.z; g[3] = s.w;
+        return;
     }
-    const int tok = lane / G::PARTS, c0 = lane % G::PARTS * EPL;
-    const int ne = tok < K ? max(0, min(EPL, w.nd - c0)) : 0;
-    float dskip[EPL], bias[EPL], s_dD[EPL], s_db[EPL];
+    const bool mine = ch < w.nd;
+    const int d = w.d0 + (mine ? ch : 0);
+    const float* start = !kFull ? nullptr : p.carry ? p.carry + (slot * p.D + d) * N
+                         : p.d_final_state ? p.d_final_state + (static_cast<long long>(w.n) * p.D + d) * N : nullptr;
 #pragma unroll
-    for (int e = 0; e < EPL; ++e) {
-        dskip[e] = (p.D_skip && e < ne) ? p.D_skip[w.d0 + c0 + e] : 0.f;
-        bias[e] = (p.dt_bias && e < ne) ? p.dt_bias[w.d0 + c0 + e] : 0.f;
-        s_dD[e] = s_db[e] = 0.f;
+    for (int j = 0; j < GR; ++j) {
+        const int at = 4 * (j * LPC + q);
+        float4 a = *reinterpret_cast<const float4*>(p.A + static_cast<long long>(d) * N + at);
+        a.x *= kLog2e; a.y *= kLog2e; a.z *= kLog2e; a.w *= kLog2e;
+        sm.A2[j][lane] = a;
+        sm.g[j][lane] = start && mine ? *reinterpret_cast<const float4*>(start + at) : make_float4(0.f, 0.f, 0.f, 0.f);
+        if constexpr (kFull) sm.dA[j][lane] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    const long long row0 = static_cast<long long>(w.b) * p.T;
-    const T* u = static_cast<const T*>(p.u) + row0 * p.u_stride + w.d0 + c0;
-    const T* dt = static_cast<const T*>(p.dt) + row0 * p.dt_stride + w.d0 + c0;
-    const T* z = p.z ? static_cast<const T*>(p.z) + row0 * p.z_stride + w.d0 + c0 : nullptr;
-    const long long dense = row0 * p.D + w.d0 + c0;
-    const T* d_out = static_cast<const T*>(p.d_out) + dense;
-    T* du = static_cast<T*>(p.du) + dense;
-    T* ddt = static_cast<T*>(p.ddt) + dense;
-    T* dz = z ? static_cast<T*>(p.dz) + dense : nullptr;
+    const float dskip = kFull && p.D_skip ? p.D_skip[d] : 0.f;
+    const float bias = p.dt_bias ? p.dt_bias[d] : 0.f;
+    float s_dD = 0.f, s_db = 0.f;
+    const long long row0 = static_cast<long long>(w.b) * p.T + w.s0;
+    const T* u = static_cast<const T*>(p.u) + row0 * p.u_stride + w.d0;
+    const T* dt = static_cast<const T*>(p.dt) + row0 * p.dt_stride + w.d0;
+    const T* z = p.z ? static_cast<const T*>(p.z) + row0 * p.z_stride + w.d0 : nullptr;
+    const T* d_out = static_cast<const T*>(p.d_out) + row0 * p.D + w.d0;
     const T* Bm = static_cast<const T*>(p.Bm) + row0 * p.B_stride + w.g * N;
     const T* Cm = static_cast<const T*>(p.Cm) + row0 * p.C_stride + w.g * N;
-    using Rows = RowTile<T, N, VEC>;
+    const long long dense = row0 * p.D + d;
     const long long rows = p.cu_seqlens ? p.T : static_cast<long long>(p.nseq) * p.T;
-    float* bc = p.bc_part + (static_cast<long long>(block) * rows + row0) * 2 * N;
-
-    const int tiles_n = (w.s1 - w.s0 + K - 1) / K;
-    for (int it = tiles_n - 1; it >= 0; --it) {
-        const int t = w.s0 + it * K;
-        const int nt = min(K, w.s1 - t);
-        const int n_in = tok < nt ? ne : 0;
-        float4 hs = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (mine) hs = *reinterpret_cast<const float4*>(p.saved + ((w.chunk0 + it) * p.D + w.d0 + ch) * N + 4 * q);
-        float ux[EPL], rx[EPL], zx[EPL], gx[EPL];
-        unpack<T, EPL>(load_raw<T, EPL, VEC>(u + (t + tok) * p.u_stride, n_in), ux);
-        unpack<T, EPL>(load_raw<T, EPL, VEC>(dt + (t + tok) * p.dt_stride, n_in), rx);
-        if (z) unpack<T, EPL>(load_raw<T, EPL, VEC>(z + (t + tok) * p.z_stride, n_in), zx);
-        unpack<T, EPL>(load_raw<T, EPL, VEC>(d_out + (t + tok) * static_cast<long long>(p.D), n_in), gx);
-        {
-            Rows r;
-            r.load(Bm + t * p.B_stride, p.B_stride, nt, lane);
-            r.store(&tile.B[0][0], lane);
-            r.load(Cm + t * p.C_stride, p.C_stride, nt, lane);
-            r.store(&tile.C[0][0], lane);
-        }
-        if (tok < K) {
+    float* bc = kFull ? p.bc_part + (block * rows + row0) * 2 * N : nullptr;
+    const int len = w.s1 - w.s0;
+    const int tiles = (len + kTile - 1) / kTile;
+    auto fetch = [&](int it) {  // tile `it`, if there is one
+        if (it >= 0) {
+            BwdStage<T, N, kFull>& st = sm.stage[it & 1];
+            const int t = it * kTile, nt = len - t;
+            fill_tile<T, CH, VEC>(&st.dt[0][0], dt + t * p.dt_stride, p.dt_stride, nt, w.nd, lane);
+            if (z) fill_tile<T, CH, VEC>(&st.z[0][0], z + t * p.z_stride, p.z_stride, nt, w.nd, lane);
+            fill_tile<T, CH, VEC>(&st.d_out[0][0], d_out + t * static_cast<long long>(p.D), p.D, nt, w.nd, lane);
+            fill_tile<T, N, VEC>(&st.C[0][0], Cm + t * p.C_stride, p.C_stride, nt, N, lane);
+            if constexpr (kFull) {
+                fill_tile<T, CH, VEC>(&st.u[0][0], u + t * p.u_stride, p.u_stride, nt, w.nd, lane);
+                fill_tile<T, N, VEC>(&st.B[0][0], Bm + t * p.B_stride, p.B_stride, nt, N, lane);
+                // the channels' states before the tile, 16 bytes at a time
+                const float* from = p.saved + ((w.chunk0 + it) * p.D + w.d0) * N;
 #pragma unroll
-            for (int e = 0; e < EPL; ++e) {
-                float d = rx[e] + bias[e];
-                if (p.softplus) d = softplus(d);
-                d = e < n_in ? d : 0.f;
-                tile.dtx[tok][c0 + e] = make_float2(d, d * ux[e]);
-                tile.dy[tok][c0 + e] = z ? gx[e] * zx[e] * sigmoid(zx[e]) : gx[e];
-            }
-        }
-        __syncwarp();
-        // the tile forward again: decays and the state before every token
-        float a[K][4], h[K + 1][4], s1[K], s2[K];
-        h[0][0] = hs.x; h[0][1] = hs.y; h[0][2] = hs.z; h[0][3] = hs.w;
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const float2 d = tile.dtx[k][ch];
-            const float4 b = *reinterpret_cast<const float4*>(&tile.B[k][4 * q]);
-            const float4 c = *reinterpret_cast<const float4*>(&tile.C[k][4 * q]);
-            const float bv[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                a[k][i] = ex2(d.x * A2[i]);
-                h[k + 1][i] = fmaf(a[k][i], h[k][i], d.y * bv[i]);
-            }
-            s1[k] = fmaf(c.x, h[k + 1][0], c.y * h[k + 1][1]) + fmaf(c.z, h[k + 1][2], c.w * h[k + 1][3]);
-        }
-        put_channel_sums<LPC, CH>(s1, q, ch, &tile.y[0][0]);
-        // and back
-#pragma unroll
-        for (int k = K - 1; k >= 0; --k) {
-            const float2 d = tile.dtx[k][ch];
-            const float dy = tile.dy[k][ch];
-            const float4 b = *reinterpret_cast<const float4*>(&tile.B[k][4 * q]);
-            const float4 c = *reinterpret_cast<const float4*>(&tile.C[k][4 * q]);
-            const float bv[4] = {b.x, b.y, b.z, b.w}, cv[4] = {c.x, c.y, c.z, c.w};
-            float v[8], sx = 0.f, sa = 0.f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float e = fmaf(cv[i], dy, g[i]);
-                v[i] = e * d.y;
-                v[4 + i] = dy * h[k + 1][i];
-                sx = fmaf(e, bv[i], sx);
-                g[i] = a[k][i] * e;
-                const float qq = g[i] * h[k][i];
-                sa = fmaf(A2[i], qq, sa);
-                dA[i] = fmaf(d.x, qq, dA[i]);
-            }
-            s1[k] = sx;
-            s2[k] = sa;
-            across_channels<LPC, CH>(v, ch);
-            if (k < nt && ch < 8) {
-#pragma unroll
-                for (int i = 0; i < 8 / M8; ++i) {
-                    const int idx = i * M8 + ch;
-                    bc[(t + k) * static_cast<long long>(2 * N) + (idx >> 2) * N + 4 * q + (idx & 3)] = v[i];
+                for (int i = 0; i < (CH * N / 4 + 31) / 32; ++i) {
+                    const int id = i * 32 + lane;
+                    const bool ok = id * 4 < w.nd * N;
+                    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(&st.saved[0][0] + id * 4));
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(ok ? from + id * 4 : from),
+                                 "r"(ok ? 16 : 0)
+                                 : "memory");
                 }
             }
         }
-        put_channel_sums<LPC, CH>(s1, q, ch, &tile.dx[0][0]);
-        put_channel_sums<LPC, CH>(s2, q, ch, &tile.da[0][0]);
+        commit_copies();
+    };
+    fetch(tiles - 1);
+    for (int it = tiles - 1; it >= 0; --it) {
+        __syncwarp();  // everyone is through with the tile before
+        fetch(it - 1);
+        wait_copies<1>();
         __syncwarp();
-        if (n_in > 0) {
-            float o1[EPL], o2[EPL], o3[EPL];
+        const BwdStage<T, N, kFull>& st = sm.stage[it & 1];
+        widen_rows<T, N>(&st.C[0][0], &sm.C[0][0], lane);
+        if constexpr (kFull) widen_rows<T, N>(&st.B[0][0], &sm.B[0][0], lane);
+        const int t = it * kTile, left = len - t;
+        float dk[kTile], xk[kTile], yk[kTile];
 #pragma unroll
-            for (int e = 0; e < EPL; ++e) {
-                const float2 d = tile.dtx[tok][c0 + e];
-                const float dy = tile.dy[tok][c0 + e], dx = tile.dx[tok][c0 + e];
-                const float y = fmaf(dskip[e], ux[e], tile.y[tok][c0 + e]);
-                float dr = fmaf(ux[e], dx, tile.da[tok][c0 + e] * (1.f / kLog2e));
-                if (p.softplus) dr *= sigmoid(rx[e] + bias[e]);
-                o1[e] = fmaf(d.x, dx, dskip[e] * dy);
-                o2[e] = dr;
-                o3[e] = z ? gx[e] * y * dsilu(zx[e], sigmoid(zx[e])) : 0.f;
-                if (e < n_in) {
-                    s_dD[e] = fmaf(dy, ux[e], s_dD[e]);
-                    s_db[e] += dr;
-                }
+        for (int k = 0; k < kTile; ++k) {
+            float v = to_f32(st.dt[k][ch]) + bias;
+            if (p.softplus) v = softplus(v);
+            dk[k] = k < left ? v : 0.f;
+            yk[k] = to_f32(st.d_out[k][ch]);
+            if (z) {
+                const float zk = to_f32(st.z[k][ch]);
+                yk[k] *= zk * sigmoid(zk);
             }
-            const long long at = (t + tok) * static_cast<long long>(p.D);
-            store_raw<T, EPL, VEC>(du + at, pack<T, EPL>(o1), n_in);
-            store_raw<T, EPL, VEC>(ddt + at, pack<T, EPL>(o2), n_in);
-            if (z) store_raw<T, EPL, VEC>(dz + at, pack<T, EPL>(o3), n_in);
+            if constexpr (kFull) xk[k] = dk[k] * to_f32(st.u[k][ch]);
+            if (!kFull) s_db += dk[k];
         }
         __syncwarp();
-    }
-    if (mine) {
-        *reinterpret_cast<float4*>(par + ao) = make_float4(dA[0], dA[1], dA[2], dA[3]);
-        if (w.first && p.d_initial_state) *reinterpret_cast<float4*>(p.d_initial_state + so) = make_float4(g[0], g[1], g[2], g[3]);
-    }
+        if constexpr (!kFull) {
 #pragma unroll
-    for (int e = 0; e < EPL; ++e) {
-        const float sd = over_tokens<G::PARTS>(s_dD[e]), sb = over_tokens<G::PARTS>(s_db[e]);
-        if (lane < G::PARTS && e < ne) {
-            par[static_cast<long long>(p.D) * N + w.d0 + c0 + e] = sd;
-            par[static_cast<long long>(p.D) * N + p.D + w.d0 + c0 + e] = sb;
+            for (int j = 0; j < GR; ++j) {
+                const Four A2 = get4(sm.A2[j][lane]);
+                Four g = get4(sm.g[j][lane]);
+#pragma unroll
+                for (int k = kTile - 1; k >= 0; --k)
+                    g = mul4(ex2_4(mul4(A2, two(dk[k], dk[k]))), fma4(get4(&sm.C[k][4 * (j * LPC + q)]), two(yk[k], yk[k]), g));
+                put4(sm.g[j][lane], g);
+            }
+        } else {
+            Two sx[kTile], sa[kTile], sy[kTile];
+#pragma unroll
+            for (int k = 0; k < kTile; ++k) sx[k] = sa[k] = sy[k] = two(0.f, 0.f);
+#pragma unroll 1
+            for (int j = 0; j < GR; ++j) {
+                const int at = 4 * (j * LPC + q);
+                const Four A2 = get4(sm.A2[j][lane]);
+                Four g = get4(sm.g[j][lane]), dA = get4(sm.dA[j][lane]);
+                // the tile forward again: decays, and the state before and after every token
+                Four a[kTile], h[kTile + 1];
+                h[0] = get4(&st.saved[ch][at]);
+#pragma unroll
+                for (int k = 0; k < kTile; ++k) {
+                    a[k] = ex2_4(mul4(A2, two(dk[k], dk[k])));
+                    h[k + 1] = fma4(a[k], h[k], mul4(get4(&sm.B[k][at]), two(xk[k], xk[k])));
+                    sy[k] = dot4(h[k + 1], get4(&sm.C[k][at]), sy[k]);
+                }
+                // and back
+#pragma unroll
+                for (int k = kTile - 1; k >= 0; --k) {
+                    const Two y2 = two(yk[k], yk[k]);
+                    const Four e = fma4(get4(&sm.C[k][at]), y2, g);
+                    float v[8];
+                    {
+                        const Four vb = mul4(e, two(xk[k], xk[k])), vc = mul4(h[k + 1], y2);
+                        split(vb.lo, v[0], v[1]);
+                        split(vb.hi, v[2], v[3]);
+                        split(vc.lo, v[4], v[5]);
+                        split(vc.hi, v[6], v[7]);
+                    }
+                    sx[k] = dot4(e, get4(&sm.B[k][at]), sx[k]);
+                    g = mul4(a[k], e);
+                    const Four qq = mul4(g, h[k]);
+                    sa[k] = dot4(A2, qq, sa[k]);
+                    dA = fma4(qq, two(dk[k], dk[k]), dA);
+                    across_channels<LPC, CH>(v, ch);
+                    if (ch < 8) {
+#pragma unroll
+                        for (int i = 0; i < 8 / M8; ++i) {
+                            const int idx = i * M8 + ch;
+                            sm.bc[k][(idx >> 2) * N + at + (idx & 3)] = v[i];
+                        }
+                    }
+                }
+                put4(sm.g[j][lane], g);
+                put4(sm.dA[j][lane], dA);
+            }
+            __syncwarp();
+            // the warp's share of dB and dC
+            {
+                float4* to = reinterpret_cast<float4*>(bc + t * static_cast<long long>(2 * N));
+                const float4* from = reinterpret_cast<const float4*>(&sm.bc[0][0]);
+                const int n4 = min(kTile, left) * (N / 2);
+#pragma unroll
+                for (int i = 0; i < (kTile * N / 2 + 31) / 32; ++i)
+                    if (i * 32 + lane < n4) to[i * 32 + lane] = from[i * 32 + lane];
+            }
+            const long long at = dense + t * static_cast<long long>(p.D);
+#pragma unroll
+            for (int k = 0; k < kTile; ++k) {
+                const float y = channel_sum<LPC>(sy[k]), dx = channel_sum<LPC>(sx[k]), da = channel_sum<LPC>(sa[k]);
+                const float uk = to_f32(st.u[k][ch]);
+                float dr = fmaf(uk, dx, da * (1.f / kLog2e));
+                if (p.softplus) dr *= sigmoid(to_f32(st.dt[k][ch]) + bias);
+                if (k < left) {
+                    s_dD = fmaf(yk[k], uk, s_dD);
+                    s_db += dr;
+                    if (mine && (LPC == 1 || q == k % LPC)) {
+                        static_cast<T*>(p.du)[at + k * static_cast<long long>(p.D)] = from_f32<T>(fmaf(dk[k], dx, dskip * yk[k]));
+                        static_cast<T*>(p.ddt)[at + k * static_cast<long long>(p.D)] = from_f32<T>(dr);
+                        if (z) {
+                            const float zk = to_f32(st.z[k][ch]);
+                            static_cast<T*>(p.dz)[at + k * static_cast<long long>(p.D)] =
+                                from_f32<T>(to_f32(st.d_out[k][ch]) * fmaf(dskip, uk, y) * dsilu(zk, sigmoid(zk)));
+                        }
+                    }
+                }
+            }
+        }
+    }
+    if (!mine) return;
+    if constexpr (!kFull) {
+#pragma unroll
+        for (int j = 0; j < GR; ++j)
+            *reinterpret_cast<float4*>(p.carry + (slot * p.D + d) * N + 4 * (j * LPC + q)) = sm.g[j][lane];
+        if (q == 0) p.carry_dt[slot * p.D + d] = s_db;
+    } else {
+        float* par = p.par_part + slot * ssm_par_stride(p.D, N);
+#pragma unroll
+        for (int j = 0; j < GR; ++j) {
+            const long long at = static_cast<long long>(d) * N + 4 * (j * LPC + q);
+            *reinterpret_cast<float4*>(par + at) = sm.dA[j][lane];
+            if (w.first && p.d_initial_state)
+                *reinterpret_cast<float4*>(p.d_initial_state + static_cast<long long>(w.n) * p.D * N + at) = sm.g[j][lane];
+        }
+        if (q == 0) {
+            par[static_cast<long long>(p.D) * N + d] = s_dD;
+            par[static_cast<long long>(p.D) * N + p.D + d] = s_db;
         }
     }
 }
@@ -247,23 +338,32 @@ __global__ void __launch_bounds__(256) ssm_bc_kernel(const SsmBcArgs p) {
     out[(row * p.G + g) * p.N + (col < p.N ? col : col - p.N)] = from_f32<T>(s);
 }
 
+template <typename T, int N, bool VEC>
+cudaError_t bwd_v(const SsmArgs& a, cudaStream_t stream) {
+    const int blocks = ssm_group_blocks(a.D, a.G, N);
+    const long long units = a.slots * blocks * a.G;
+    if (a.carry) {
+        cudaError_t e = launch_warps(ssm_bwd_kernel<T, N, false, VEC>, units, sizeof(BwdShared<T, N, false>), a, blocks, stream);
+        if (e == cudaSuccess) e = launch_ssm_compose(a, true, stream);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_warps(ssm_bwd_kernel<T, N, true, VEC>, units, sizeof(BwdShared<T, N, true>), a, blocks, stream);
+}
+
 template <typename T, int N>
 cudaError_t bwd_n(const SsmArgs& a, cudaStream_t stream) {
-    const int blocks = ssm_group_blocks(a.D, a.G, N);
-    const long long units = static_cast<long long>(a.nseq) * blocks * a.G;
-    const unsigned grid = static_cast<unsigned>((units + kWarps<N> - 1) / kWarps<N>);
-    // out is not written here; d_out, du, ddt and dz are dense rows of D as it is, 16-byte aligned all
-    if (all_vec<T, N, 4>(a))
-        ssm_bwd_kernel<T, N, true><<<grid, 32 * kWarps<N>, 0, stream>>>(a, 1 << 30, a.nseq, blocks);
-    else
-        ssm_bwd_kernel<T, N, false><<<grid, 32 * kWarps<N>, 0, stream>>>(a, 1 << 30, a.nseq, blocks);
-    return cudaGetLastError();
+    constexpr int CH = Lanes<N>::CH;
+    // d_out, du, ddt and dz are dense rows of D
+    const bool vec = a.D / a.G * sizeof(T) % piece_bytes<T, CH> == 0 && takes_pieces<T, CH>(a.u, a.u_stride) &&
+                     takes_pieces<T, CH>(a.dt, a.dt_stride) && (!a.z || takes_pieces<T, CH>(a.z, a.z_stride)) &&
+                     takes_pieces<T, N>(a.Bm, a.B_stride) && takes_pieces<T, N>(a.Cm, a.C_stride);
+    return vec ? bwd_v<T, N, true>(a, stream) : bwd_v<T, N, false>(a, stream);
 }
 
 }  // namespace
 
 int ssm_group_blocks(int D, int G, int N) {
-    const int ch = 128 / N;
+    const int ch = N <= 16 ? 32 : 512 / N;
     return (D / G + ch - 1) / ch;
 }
 

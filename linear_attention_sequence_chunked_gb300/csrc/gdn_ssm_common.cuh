@@ -4,14 +4,16 @@
 //   dt_t = softplus(dt_raw_t + dt_bias_d)          (or without the softplus)
 //   h_t  = exp(dt_t A_dn) h_{t-1} + dt_t u_t B_tn,   y_t = sum_n C_tn h_tn + D_d u_t,
 //   out_t = y_t silu(z_t)                           (or y_t without a gate).
-// One warp walks a run of tokens for CH = 32 NS / N channels: lane
-// ch * LPC + q holds states NS q .. NS q + NS - 1 of channel ch in registers, so
-// a token costs NS exponentials and about 4 NS fp32 operations per lane.  Tokens
-// come in tiles of kSsmChunk = 16: lane l first takes the l-th share of the
-// tile's (token, channel) elements, forms dt and x = dt u once per element and
-// puts them, B and C into the warp's shared memory as fp32; the 16 tokens then
-// run from there without a branch (a token after the end has dt = x = 0, which
-// leaves the state as it is).
+// A warp walks a run of tokens for 32 channels (fewer for N > 16), a lane per
+// channel with its states in registers, so that a row of every activation is
+// one 64-byte access and nothing is exchanged between lanes.  Tokens come in
+// tiles of kTile: copied to shared memory a tile or two ahead, B and C widened
+// to fp32 once, dt and x = dt u formed once per element, and then four states
+// at a time over the tile without a branch (a token after the end has
+// dt = x = 0, which leaves the state as it is).  Arithmetic runs on pairs of
+// states in register pairs.  Per token and channel that is N exponentials, 2 N
+// paired operations and about 40 others; measured, it is bound by instruction
+// issue and its latencies (0.67 per cycle and quarter of an SM), not by HBM.
 #pragma once
 
 #include "gdn_kernels.h"
@@ -22,98 +24,9 @@ namespace ssm {
 
 using namespace mix;
 
-constexpr int K = kSsmChunk;
-
-// K tokens x CH channels over 32 lanes: token lane / PARTS, EPL channels from
-// (lane % PARTS) * EPL.
-template <int N, int NS>
-struct Geo {
-    static constexpr int LPC = N / NS;
-    static constexpr int CH = 32 / LPC;
-    static constexpr int EPL = CH >= 2 ? CH / 2 : 1;
-    static constexpr int PARTS = CH >= 2 ? 2 : 1;
-};
-
-// B or C rows of a tile: K x N elements in pieces of PE, NP pieces per lane.
-template <typename T, int N, bool VEC>
-struct RowTile {
-    static constexpr int PE = (N / 2 < 16 / static_cast<int>(sizeof(T))) ? N / 2 : 16 / static_cast<int>(sizeof(T));
-    static constexpr int NP = N / 2 / PE;
-    Raw<T, PE> v[NP];
-
-    // rows: the tile's first row at this group's column 0; nt rows are valid
-    __device__ __forceinline__ void load(const T* rows, long long stride, int nt, int lane) {
-#pragma unroll
-        for (int p = 0; p < NP; ++p) {
-            const int id = p * 32 + lane;
-            const int tok = id / (N / PE), n0 = id % (N / PE) * PE;
-            v[p] = load_raw<T, PE, VEC>(rows + tok * stride + n0, tok < nt ? PE : 0);
-        }
-    }
-    __device__ __forceinline__ void store(float* dst, int lane) const {  // [K][N]
-#pragma unroll
-        for (int p = 0; p < NP; ++p) {
-            float x[PE];
-            unpack<T, PE>(v[p], x);
-            float4* d = reinterpret_cast<float4*>(dst + (p * 32 + lane) * PE);
-#pragma unroll
-            for (int i = 0; i < PE / 4; ++i) d[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-        }
-    }
-};
-
-// Whether every activation of the scan can be accessed in the vectors of this
-// geometry (decided on the host: the kernels have no branch on it).
-template <typename T, int N, int NS>
-bool all_vec(const SsmArgs& a) {
-    constexpr int EPL = Geo<N, NS>::EPL, PE = RowTile<T, N, true>::PE;
-    auto ok = [](const void* p, long long stride, int e) {
-        const int bytes = e * static_cast<int>(sizeof(T)) < 16 ? e * static_cast<int>(sizeof(T)) : 16;
-        return reinterpret_cast<uintptr_t>(p) % bytes == 0 && stride * static_cast<long long>(sizeof(T)) % bytes == 0;
-    };
-    return a.D / a.G % EPL == 0 && ok(a.u, a.u_stride, EPL) && ok(a.dt, a.dt_stride, EPL) &&
-           (!a.z || ok(a.z, a.z_stride, EPL)) && ok(a.out, a.D, EPL) && ok(a.Bm, a.B_stride, PE) &&
-           ok(a.Cm, a.C_stride, PE);
-}
-
-// Sums over the LPC lanes of a channel of v[t], t < K: value i of lane q is
-// then the sum of token i * min(LPC, K) + (q mod K).
-template <int LPC>
-__device__ __forceinline__ void channel_sums(float (&v)[K], int q) {
-#pragma unroll
-    for (int s = 0, m = 1; m < LPC; ++s, m *= 2) {
-        if (m < K) {
-            const bool hi = (q & m) != 0;
-#pragma unroll
-            for (int i = 0; i < K / 2; ++i) {
-                if (i < K / (2 * m)) {
-                    const float send = hi ? v[2 * i] : v[2 * i + 1];
-                    const float keep = hi ? v[2 * i + 1] : v[2 * i];
-                    v[i] = keep + __shfl_xor_sync(0xffffffffu, send, m);
-                }
-            }
-        } else {
-            v[0] += __shfl_xor_sync(0xffffffffu, v[0], m);
-        }
-    }
-}
-
-// This lane's channel_sums into out[token][CH].
-template <int LPC, int CH>
-__device__ __forceinline__ void put_channel_sums(float (&v)[K], int q, int ch, float* out) {
-    channel_sums<LPC>(v, q);
-    constexpr int M = LPC < K ? LPC : K;
-#pragma unroll
-    for (int i = 0; i < K / M; ++i) out[(i * M + q % M) * CH + ch] = v[i];
-}
-
-// Sum over the token lanes that share a channel share (same lane % PARTS).
-template <int PARTS>
-__device__ __forceinline__ float over_tokens(float x) {
-#pragma unroll
-    for (int m = PARTS; m < 32; m *= 2) x += __shfl_xor_sync(0xffffffffu, x, m);
-    return x;
-}
+constexpr int kWarps = 4;
+constexpr int kTile = kSsmChunk;  // tokens worked on at a time
+constexpr int kStages = 3;        // tiles of the forward in shared memory or on their way to it
 
 // Where a warp works: segment `slot` of the tokens, one block of CH channels.
 struct Place {
@@ -142,10 +55,129 @@ __device__ __forceinline__ bool find_place(const SsmArgs& p, long long slot, int
     const int off = block % blocks * CH;
     w.d0 = w.g * per + off;
     w.nd = min(CH, per - off);
-    const long long base = p.cu_seqlens ? static_cast<long long>(w.t0 / K) + w.n
-                                        : static_cast<long long>(w.n) * ((p.T + K - 1) / K);
-    w.chunk0 = base + (w.s0 - w.t0) / K;
+    const long long base = p.cu_seqlens ? static_cast<long long>(w.t0 / kTile) + w.n
+                                        : static_cast<long long>(w.n) * ((p.T + kTile - 1) / kTile);
+    w.chunk0 = base + (w.s0 - w.t0) / kTile;
     return true;
+}
+
+// ---------------------------------------------------------------------------
+// Lanes as channels: the geometry of the forward.
+// ---------------------------------------------------------------------------
+
+
+// A lane holds NL = min(N, 16) states of one channel, four at a time: group j
+// of lane q of a channel's LPC = N / NL lanes is states 4 (j LPC + q) .. + 3, so
+// that those lanes read neighbouring 16 bytes of a row of B.  CH channels per
+// warp; with N <= 16 a lane is a channel, and a row of 32 channels is 64 bytes.
+template <int N>
+struct Lanes {
+    static constexpr int NL = N < 16 ? N : 16;
+    static constexpr int LPC = N / NL;
+    static constexpr int CH = 32 / LPC;
+    static constexpr int GR = NL / 4;
+};
+
+// Copies rows [0, nt) and columns [0, nc) of a kTile x ROW tile to shared
+// memory, zeros elsewhere.  VEC: asynchronously, in pieces of up to 16 bytes
+// (every row's pieces aligned, nc a multiple of a piece); otherwise element by
+// element and at once.
+template <typename T, int ROW, bool VEC>
+__device__ __forceinline__ void fill_tile(T* dst, const T* src, long long stride, int nt, int nc, int lane) {
+    constexpr int row_bytes = ROW * static_cast<int>(sizeof(T));
+    constexpr int CB = row_bytes < 16 ? row_bytes : 16, CE = VEC ? CB / static_cast<int>(sizeof(T)) : 1;
+    constexpr int PER = ROW / CE, TOTAL = kTile * PER;
+#pragma unroll
+    for (int i = 0; i < (TOTAL + 31) / 32; ++i) {
+        const int id = i * 32 + lane, row = id / PER, c = id % PER * CE;
+        if (TOTAL % 32 != 0 && id >= TOTAL) continue;
+        const bool ok = row < nt && c < nc;
+        if constexpr (VEC) {
+            const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(dst + id * CE));
+            const T* from = ok ? src + row * stride + c : src;
+            const int bytes = ok ? CB : 0;
+            if constexpr (CB == 16)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+            else
+                asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(to), "l"(from), "n"(CB), "r"(bytes) : "memory");
+        } else {
+            dst[id] = ok ? __ldg(src + row * stride + c) : T(0);
+        }
+    }
+}
+template <typename T, int ROW>
+constexpr int piece_bytes = ROW * static_cast<int>(sizeof(T)) < 16 ? ROW * static_cast<int>(sizeof(T)) : 16;
+
+// Whether fill_tile can take its pieces of ROW elements from rows at p.
+template <typename T, int ROW>
+bool takes_pieces(const void* p, long long stride) {
+    constexpr int b = piece_bytes<T, ROW>;
+    return reinterpret_cast<uintptr_t>(p) % b == 0 && stride * static_cast<long long>(sizeof(T)) % b == 0;
+}
+
+__device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void wait_copies() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+
+// kTile x N elements of B or C, as fp32.
+template <typename T, int N>
+__device__ __forceinline__ void widen_rows(const T* src, float* dst, int lane) {
+    constexpr int PE = N * kTile / 32 < 16 / static_cast<int>(sizeof(T)) ? N * kTile / 32 : 16 / static_cast<int>(sizeof(T));
+#pragma unroll
+    for (int i = 0; i < N * kTile / 32 / PE; ++i) {
+        const int at = (i * 32 + lane) * PE;
+        Raw<T, PE> r;
+        if constexpr (sizeof(T) * PE == 16)
+            *reinterpret_cast<uint4*>(r.w) = *reinterpret_cast<const uint4*>(src + at);
+        else if constexpr (sizeof(T) * PE == 8)
+            *reinterpret_cast<uint2*>(r.w) = *reinterpret_cast<const uint2*>(src + at);
+        else
+            r.w[0] = *reinterpret_cast<const uint32_t*>(src + at);
+        float x[PE];
+        unpack<T, PE>(r, x);
+        if constexpr (PE >= 4) {
+#pragma unroll
+            for (int e = 0; e < PE; e += 4)
+                *reinterpret_cast<float4*>(dst + at + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+        } else {
+            *reinterpret_cast<float2*>(dst + at) = make_float2(x[0], x[1]);
+        }
+    }
+}
+
+// The states of a lane, as register pairs, from or to a channel's N floats.
+template <int N>
+__device__ __forceinline__ void load_states(const float* p, int q, Two (&v)[Lanes<N>::NL / 2]) {
+#pragma unroll
+    for (int j = 0; j < Lanes<N>::GR; ++j) {
+        const float4 x = *reinterpret_cast<const float4*>(p + 4 * (j * Lanes<N>::LPC + q));
+        v[2 * j] = two(x.x, x.y);
+        v[2 * j + 1] = two(x.z, x.w);
+    }
+}
+template <int N>
+__device__ __forceinline__ void store_states(float* p, int q, const Two (&v)[Lanes<N>::NL / 2]) {
+#pragma unroll
+    for (int j = 0; j < Lanes<N>::GR; ++j) {
+        float4 x;
+        split(v[2 * j], x.x, x.y);
+        split(v[2 * j + 1], x.z, x.w);
+        *reinterpret_cast<float4*>(p + 4 * (j * Lanes<N>::LPC + q)) = x;
+    }
+}
+
+// One launch; shared memory beyond 48 KB is asked for once per kernel.
+template <typename F>
+cudaError_t launch_warps(F kernel, long long units, int bytes_per_warp, const SsmArgs& a, int blocks, cudaStream_t stream) {
+    const int bytes = kWarps * bytes_per_warp;
+    if (bytes > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != cudaSuccess) return e;
+    }
+    kernel<<<static_cast<unsigned>((units + kWarps - 1) / kWarps), 32 * kWarps, bytes, stream>>>(a, blocks);
+    return cudaGetLastError();
 }
 
 }  // namespace ssm

@@ -134,7 +134,7 @@ def test_scan_host_validation(lib):
     assert call(us=63) == 1 and call(bs=31) == 1 and call(zs=10) == 1 and call(z=FAKE + 1) == 3
     assert call(A=FAKE + 4) == 3 and call(b=FAKE + 1) == 3 and call(dtype=7) == 1
     need = lib.gdn_ssm_saved_size(1, 32, 64, 16, 0)
-    assert need == 2 * 64 * 16 * 4 and lib.gdn_ssm_saved_size(3, 32, 64, 16, 1) == (32 // 16 + 3) * 64 * 16 * 4
+    assert need == 4 * 64 * 16 * 4 and lib.gdn_ssm_saved_size(3, 32, 64, 16, 1) == (32 // 8 + 3) * 64 * 16 * 4
     assert lib.gdn_ssm_saved_size(1, 32, 64, 12, 0) == 0
     assert call(saved=FAKE, sbytes=need - 1) == 1 and call(saved=FAKE + 16, sbytes=need) == 3
     wneed = lib.gdn_ssm_bwd_workspace_size(1, 32, 64, 2, 16, 0)
