@@ -11,10 +11,12 @@
 //   dbias_c = sum_t dp_t,
 // and the initial state's gradient is dx at s < 0.
 //
-// All of it is bound by HBM: 2 (forward) or 3 (backward) accesses per element
-// against 2W to 6W operations.  A thread takes E neighbouring channels (16
-// bytes where rows allow it) over a block of consecutive tokens with the
-// window in registers, so every input is read once but for W-1 rows per block.
+// All of it should be bound by HBM: 2 (forward) or 3 (backward) accesses per
+// element against 2W to 6W operations and two or three exponentials or
+// reciprocals.  A thread takes E neighbouring channels over a block of
+// consecutive tokens with the window in registers, so every input is read once
+// but for W-1 rows per block; the next tokens' loads are in flight while these
+// are computed, and the arithmetic runs on pairs of channels.
 #include "gdn_kernels.h"
 #include "gdn_mix_common.cuh"
 
@@ -27,31 +29,42 @@ using namespace mix;
 constexpr int kThreads = 256;
 
 template <int W, int E>
-__device__ __forceinline__ void load_weights(const float* weight, const float* bias, long long d0, float (*w)[E],
-                                             float* bs) {
+__device__ __forceinline__ void load_weights(const float* weight, const float* bias, long long d0, Two (*w)[(E + 1) / 2],
+                                             Two* bs) {
+    float v[W][E + 1], b[E + 1];
 #pragma unroll
     for (int e = 0; e < E; ++e) {
+        const float* row = weight + (d0 + e) * W;
+        if constexpr (W == 4) {
+            const float4 x = __ldg(reinterpret_cast<const float4*>(row));
+            v[0][e] = x.x; v[1][e] = x.y; v[2][e] = x.z; v[3][e] = x.w;
+        } else {
 #pragma unroll
-        for (int j = 0; j < W; ++j) w[j][e] = __ldg(weight + (d0 + e) * W + j);
-        bs[e] = bias ? __ldg(bias + d0 + e) : 0.f;
+            for (int j = 0; j < W; ++j) v[j][e] = __ldg(row + j);
+        }
+        b[e] = bias ? __ldg(bias + d0 + e) : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < (E + 1) / 2; ++i) {
+        const bool both = 2 * i + 1 < E;
+#pragma unroll
+        for (int j = 0; j < W; ++j) w[j][i] = two(v[j][2 * i], both ? v[j][2 * i + 1] : 0.f);
+        bs[i] = two(b[2 * i], both ? b[2 * i + 1] : 0.f);
     }
 }
 
-// Row r of the W-1 inputs before a sequence's start (r = 0 the oldest).
+// The input at token t of a sequence that starts at t0: before it, a row of the
+// W-1 inputs in its initial state (zeros without one).
 template <typename T, int W, int E>
-__device__ __forceinline__ void load_state_row(const T* state, long long seq, int r, long long D, long long d0,
-                                               float* x) {
-    if (state) {
-        unpack<T, E>(load_raw<T, E>(state + (seq * (W - 1) + r) * D + d0, E), x);
-    } else {
-#pragma unroll
-        for (int e = 0; e < E; ++e) x[e] = 0.f;
-    }
+__device__ __forceinline__ Raw<T, E> input_at(const T* x, long long x_stride, const T* state, long long seq, int t, int t0,
+                                              long long D) {
+    if (t >= t0) return load_raw<T, E>(x + t * x_stride, E);
+    return load_raw<T, E>(state ? state + (seq * (W - 1) + t - t0 + (W - 1)) * D : x, state ? E : 0);
 }
 
 template <typename T, int W, int E>
 __global__ void __launch_bounds__(kThreads) conv_fwd_kernel(const ConvArgs p) {
-    constexpr int U = 4;  // tokens whose loads are in flight together
+    constexpr int U = 4, P = (E + 1) / 2;  // tokens whose loads are in flight together, pairs of channels
     if (blockIdx.x == 0) check_offsets(p.cu_seqlens, p.N, p.T, p.err);
     const long long cv = p.D / E;
     const long long id = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
@@ -62,57 +75,53 @@ __global__ void __launch_bounds__(kThreads) conv_fwd_kernel(const ConvArgs p) {
     if (!find_block(p.cu_seqlens, p.N, p.T, p.tb, id / cv, p.err, n, c)) return;
     if (!token_range(p.cu_seqlens, n, p.N, p.T, p.err, b, t0, t1)) return;
     const T* x = static_cast<const T*>(p.x) + static_cast<long long>(b) * p.T * p.x_stride + d0;
-    T* y = static_cast<T*>(p.y) + static_cast<long long>(b) * p.T * p.D + d0;
-    const T* s0 = static_cast<const T*>(p.initial_state);
+    const T* s0 = p.initial_state ? static_cast<const T*>(p.initial_state) + d0 : nullptr;
     const long long begin = t0 + c * p.tb;
     const int tb = static_cast<int>(min(begin, static_cast<long long>(t1)));
     const int te = static_cast<int>(min(begin + p.tb, static_cast<long long>(t1)));
     if (p.final_state && te == t1 && (tb < te || c == 0)) {
-        T* fs = static_cast<T*>(p.final_state);
+        T* fs = static_cast<T*>(p.final_state) + d0;
 #pragma unroll
-        for (int r = 0; r < W - 1; ++r) {
-            const int t = t1 - (W - 1) + r;
-            float v[E];
-            if (t >= t0)
-                unpack<T, E>(load_raw<T, E>(x + t * p.x_stride, E), v);
-            else
-                load_state_row<T, W, E>(s0, n, t - t0 + (W - 1), p.D, d0, v);
-            store_raw<T, E>(fs + (static_cast<long long>(n) * (W - 1) + r) * p.D + d0, pack<T, E>(v), E);
-        }
+        for (int r = 0; r < W - 1; ++r)
+            store_raw<T, E>(fs + (static_cast<long long>(n) * (W - 1) + r) * p.D,
+                            input_at<T, W, E>(x, p.x_stride, s0, n, t1 - (W - 1) + r, t0, p.D), E);
     }
     if (tb >= te) return;
-    float w[W][E], bs[E], win[W][E];
+    Two w[W][P], bs[P], win[W - 1 + U][P];
     load_weights<W, E>(p.weight, p.bias, d0, w, bs);
 #pragma unroll
-    for (int r = 0; r < W - 1; ++r) {
-        const int t = tb - (W - 1) + r;
-        if (t >= t0)
-            unpack<T, E>(load_raw<T, E>(x + t * p.x_stride, E), win[r]);
-        else
-            load_state_row<T, W, E>(s0, n, t - t0 + (W - 1), p.D, d0, win[r]);
-    }
-    for (int t = tb; t < te; t += U) {
-        Raw<T, E> in[U];
+    for (int r = 0; r < W - 1; ++r)
+        unpack_2<T, E>(input_at<T, W, E>(x, p.x_stride, s0, n, tb - (W - 1) + r, t0, p.D), win[r]);
+    x += tb * p.x_stride;
+    T* y = static_cast<T*>(p.y) + (static_cast<long long>(b) * p.T + tb) * p.D + d0;
+    Raw<T, E> in[U];
+    auto load = [&](int left) {
 #pragma unroll
-        for (int k = 0; k < U; ++k) in[k] = load_raw<T, E>(x + (t + k) * p.x_stride, t + k < te ? E : 0);
+        for (int k = 0; k < U; ++k) in[k] = load_raw<T, E>(x + k * p.x_stride, k < left ? E : 0);
+        x += U * p.x_stride;
+    };
+    load(te - tb);
+    for (int left = te - tb; left > 0; left -= U) {
+#pragma unroll
+        for (int k = 0; k < U; ++k) unpack_2<T, E>(in[k], win[W - 1 + k]);
+        load(left - U);
 #pragma unroll
         for (int k = 0; k < U; ++k) {
-            if (t + k >= te) break;
-            unpack<T, E>(in[k], win[W - 1]);
-            float o[E];
+            Two o[P];
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                float acc = bs[e];
+            for (int i = 0; i < P; ++i) {
+                o[i] = bs[i];
 #pragma unroll
-                for (int j = 0; j < W; ++j) acc = fmaf(w[j][e], win[j][e], acc);
-                o[e] = p.activation ? acc * sigmoid(acc) : acc;
+                for (int j = 0; j < W; ++j) o[i] = fma2(w[j][i], win[k + j][i], o[i]);
+                if (p.activation) o[i] = mul2(o[i], sigmoid_2(o[i]));
             }
-            store_raw<T, E>(y + (t + k) * static_cast<long long>(p.D), pack<T, E>(o), E);
-#pragma unroll
-            for (int j = 0; j < W - 1; ++j)
-#pragma unroll
-                for (int e = 0; e < E; ++e) win[j][e] = win[j + 1][e];
+            if (k < left) store_raw<T, E>(y + k * static_cast<long long>(p.D), pack_2<T, E>(o), E);
         }
+        y += U * static_cast<long long>(p.D);
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+            for (int i = 0; i < P; ++i) win[j][i] = win[j + U][i];
     }
 }
 
@@ -124,88 +133,110 @@ constexpr int kRows = kThreads / kLanes;
 
 template <typename T, int W, int E>
 __global__ void __launch_bounds__(kThreads) conv_bwd_kernel(const ConvArgs p) {
+    constexpr int U = 4, P = (E + 1) / 2;
     __shared__ float red[kRows][kLanes][E + 1];
     if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(p.cu_seqlens, p.N, p.T, p.err);
     const int lane = threadIdx.x % kLanes, row = threadIdx.x / kLanes;
     const long long d0 = (static_cast<long long>(blockIdx.y) * kLanes + lane) * E;
     const long long slot = static_cast<long long>(blockIdx.x) * kRows + row;
-    float dw[W + 1][E];
+    const Two zero = two(0.f, 0.f);
+    Two dw[W + 1][P];
 #pragma unroll
     for (int j = 0; j <= W; ++j)
 #pragma unroll
-        for (int e = 0; e < E; ++e) dw[j][e] = 0.f;
+        for (int i = 0; i < P; ++i) dw[j][i] = zero;
     int n, b, t0, t1;
     long long c;
     if (d0 < p.D && slot < p.slots && find_block(p.cu_seqlens, p.N, p.T, p.tb, slot, p.err, n, c) &&
         token_range(p.cu_seqlens, n, p.N, p.T, p.err, b, t0, t1)) {
         const T* x = static_cast<const T*>(p.x) + static_cast<long long>(b) * p.T * p.x_stride + d0;
-        const T* dy = static_cast<const T*>(p.d_out) + static_cast<long long>(b) * p.T * p.D + d0;
-        T* dx = static_cast<T*>(p.dx) + static_cast<long long>(b) * p.T * p.D + d0;
-        const T* s0 = static_cast<const T*>(p.initial_state);
-        const T* dfs = static_cast<const T*>(p.d_final_state);
-        T* ds0 = static_cast<T*>(p.d_initial_state);
+        const T* s0 = p.initial_state ? static_cast<const T*>(p.initial_state) + d0 : nullptr;
+        const T* dfs = p.d_final_state ? static_cast<const T*>(p.d_final_state) + d0 : nullptr;
         const long long begin = t0 + c * p.tb;
         const int tb = static_cast<int>(min(begin, static_cast<long long>(t1)));
         const int te = static_cast<int>(min(begin + p.tb, static_cast<long long>(t1)));
         if (tb < te || c == 0) {
-            float w[W][E], bs[E], win[W][E], dp[W][E];
+            Two w[W][P], bs[P], win[W - 1 + U][P], dp[W - 1 + U][P];
             load_weights<W, E>(p.weight, p.bias, d0, w, bs);
 #pragma unroll
-            for (int j = 0; j < W; ++j)
-#pragma unroll
-                for (int e = 0; e < E; ++e) dp[j][e] = 0.f;
-#pragma unroll
             for (int r = 0; r < W - 1; ++r) {
-                const int t = tb - (W - 1) + r;
-                if (t >= t0)
-                    unpack<T, E>(load_raw<T, E>(x + t * p.x_stride, E), win[r]);
-                else
-                    load_state_row<T, W, E>(s0, n, t - t0 + (W - 1), p.D, d0, win[r]);
+                unpack_2<T, E>(input_at<T, W, E>(x, p.x_stride, s0, n, tb - (W - 1) + r, t0, p.D), win[r]);
+#pragma unroll
+                for (int i = 0; i < P; ++i) dp[r][i] = zero;
             }
-            for (int t = tb; t < te + W - 1; ++t) {
-                const bool in = t < t1;
-                float g[E];
-                unpack<T, E>(load_raw<T, E>(x + t * p.x_stride, in ? E : 0), win[W - 1]);
-                unpack<T, E>(load_raw<T, E>(dy + t * static_cast<long long>(p.D), in ? E : 0), g);
+            const long long base = (static_cast<long long>(b) * p.T + tb) * p.D + d0;
+            const T* dy = static_cast<const T*>(p.d_out) + base;
+            T* dx = static_cast<T*>(p.dx) + base - (W - 1) * static_cast<long long>(p.D);
+            T* ds0 = p.d_initial_state && tb == t0
+                         ? static_cast<T*>(p.d_initial_state) + static_cast<long long>(n) * (W - 1) * p.D + d0 : nullptr;
+            x += tb * p.x_stride;
+            Raw<T, E> in[U], gin[U];
+            auto load = [&](int t) {
 #pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    float acc = bs[e];
+                for (int k = 0; k < U; ++k) {
+                    const int e = t + k < min(t1, te + W - 1) ? E : 0;
+                    in[k] = load_raw<T, E>(x + k * p.x_stride, e);
+                    gin[k] = load_raw<T, E>(dy + k * static_cast<long long>(p.D), e);
+                }
+                x += U * p.x_stride;
+                dy += U * static_cast<long long>(p.D);
+            };
+            load(tb);
+            for (int t = tb; t < te + W - 1; t += U) {
+                Two g[U][P];
 #pragma unroll
-                    for (int j = 0; j < W; ++j) acc = fmaf(w[j][e], win[j][e], acc);
-                    const float d = !in ? 0.f : p.activation ? g[e] * dsilu(acc, sigmoid(acc)) : g[e];
-                    dp[W - 1][e] = d;
-                    if (t < te) {
+                for (int k = 0; k < U; ++k) {
+                    unpack_2<T, E>(in[k], win[W - 1 + k]);
+                    unpack_2<T, E>(gin[k], g[k]);
+                }
+                load(t + U);
 #pragma unroll
-                        for (int j = 0; j < W; ++j) dw[j][e] = fmaf(d, win[j][e], dw[j][e]);
-                        dw[W][e] += d;
+                for (int k = 0; k < U; ++k) {
+#pragma unroll
+                    for (int i = 0; i < P; ++i) {
+                        Two d = g[k][i];
+                        if (p.activation) {
+                            Two acc = bs[i];
+#pragma unroll
+                            for (int j = 0; j < W; ++j) acc = fma2(w[j][i], win[k + j][i], acc);
+                            const Two s = sigmoid_2(acc), one = two(1.f, 1.f), neg = two(-1.f, -1.f);
+                            // silu' = s (1 + p (1 - s))
+                            d = mul2(d, mul2(s, fma2(acc, fma2(s, neg, one), one)));
+                        }
+                        if (t + k >= t1) d = zero;
+                        dp[W - 1 + k][i] = d;
+                        if (t + k >= te) d = zero;  // the next block's
+#pragma unroll
+                        for (int j = 0; j < W; ++j) dw[j][i] = fma2(d, win[k + j][i], dw[j][i]);
+                        dw[W][i] = add2(dw[W][i], d);
+                    }
+                    // input s has now seen every token it feeds
+                    const int s = t + k - (W - 1);
+                    if (s < te && (s >= tb || ds0)) {
+                        Two o[P];
+#pragma unroll
+                        for (int i = 0; i < P; ++i) {
+                            o[i] = zero;
+#pragma unroll
+                            for (int j = 0; j < W; ++j) o[i] = fma2(w[j][i], dp[W - 1 + k - j][i], o[i]);
+                        }
+                        if (dfs && s >= t1 - (W - 1)) {  // one of the rows the final state holds
+                            Two v[P];
+                            unpack_2<T, E>(load_raw<T, E>(dfs + (static_cast<long long>(n) * (W - 1) + s - t1 + (W - 1)) * p.D, E), v);
+#pragma unroll
+                            for (int i = 0; i < P; ++i) o[i] = add2(o[i], v[i]);
+                        }
+                        T* to = s >= tb ? dx + k * static_cast<long long>(p.D) : ds0 + (s - t0 + (W - 1)) * static_cast<long long>(p.D);
+                        store_raw<T, E>(to, pack_2<T, E>(o), E);
                     }
                 }
-                // input s has now seen every token it feeds
-                const int s = t - (W - 1);
-                if (s >= tb || (tb == t0 && ds0)) {
-                    float o[E];
-#pragma unroll
-                    for (int e = 0; e < E; ++e) {
-                        o[e] = 0.f;
-#pragma unroll
-                        for (int j = 0; j < W; ++j) o[e] = fmaf(w[j][e], dp[W - 1 - j][e], o[e]);
-                    }
-                    if (dfs && s >= t1 - (W - 1)) {  // one of the rows the final state holds
-                        float v[E];
-                        unpack<T, E>(load_raw<T, E>(dfs + (static_cast<long long>(n) * (W - 1) + s - t1 + (W - 1)) * p.D + d0, E), v);
-#pragma unroll
-                        for (int e = 0; e < E; ++e) o[e] += v[e];
-                    }
-                    T* to = s >= tb ? dx + s * static_cast<long long>(p.D)
-                                    : ds0 + (static_cast<long long>(n) * (W - 1) + s - t0 + (W - 1)) * p.D + d0;
-                    store_raw<T, E>(to, pack<T, E>(o), E);
-                }
+                dx += U * static_cast<long long>(p.D);
 #pragma unroll
                 for (int j = 0; j < W - 1; ++j)
 #pragma unroll
-                    for (int e = 0; e < E; ++e) {
-                        win[j][e] = win[j + 1][e];
-                        dp[j][e] = dp[j + 1][e];
+                    for (int i = 0; i < P; ++i) {
+                        win[j][i] = win[j + U][i];
+                        dp[j][i] = dp[j + U][i];
                     }
             }
         }
@@ -214,7 +245,12 @@ __global__ void __launch_bounds__(kThreads) conv_bwd_kernel(const ConvArgs p) {
 #pragma unroll
     for (int j = 0; j <= W; ++j) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) red[row][lane][e] = dw[j][e];
+        for (int i = 0; i < P; ++i) {
+            float lo, hi;
+            split(dw[j][i], lo, hi);
+            red[row][lane][2 * i] = lo;
+            if (2 * i + 1 < E) red[row][lane][2 * i + 1] = hi;
+        }
         __syncthreads();
         for (int i = threadIdx.x; i < kLanes * E; i += kThreads) {
             const long long d = static_cast<long long>(blockIdx.y) * kLanes * E + i;
@@ -256,35 +292,39 @@ __global__ void __launch_bounds__(kThreads) conv_step_kernel(const ConvStepArgs 
             in[r].w[0] = *row;
     }
     in[W - 1] = load_raw<T, E>(static_cast<const T*>(p.x) + b * p.x_stride + d0, E);
-    float w[W][E], o[E];
+    constexpr int P = (E + 1) / 2;
+    Two w[W][P], o[P];
     load_weights<W, E>(p.weight, p.bias, d0, w, o);
 #pragma unroll
     for (int j = 0; j < W; ++j) {
-        float v[E];
-        unpack<T, E>(in[j], v);
+        Two v[P];
+        unpack_2<T, E>(in[j], v);
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = fmaf(w[j][e], v[e], o[e]);
+        for (int i = 0; i < P; ++i) o[i] = fma2(w[j][i], v[i], o[i]);
         if (j > 0) store_raw<T, E>(so + (j - 1) * static_cast<long long>(p.D), in[j], E);
     }
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = p.activation ? o[e] * sigmoid(o[e]) : o[e];
-    store_raw<T, E>(y, pack<T, E>(o), E);
+    for (int i = 0; i < P; ++i)
+        if (p.activation) o[i] = mul2(o[i], sigmoid_2(o[i]));
+    store_raw<T, E>(y, pack_2<T, E>(o), E);
 }
 
-// Sums of a [rows][cols] partial array over its rows, in a fixed order.
-// Columns land in up to three outputs of c0, c1 and the rest (null: dropped);
-// with W > 0 the array is [rows][W + 1][D] and the first output (D, W).
-__global__ void __launch_bounds__(kThreads) column_sum_kernel(const ColumnSumArgs p) {
-    __shared__ float red[kRows][kLanes + 1];
-    const int lane = threadIdx.x % kLanes, row = threadIdx.x / kLanes;
-    const long long col = static_cast<long long>(blockIdx.x) * kLanes + lane;
+// Sums of a [rows][cols] partial array over its rows, in a fixed order: 32
+// columns per block, 32 threads down each.  Columns land in up to three outputs
+// of c0, c1 and the rest (null: dropped); with W > 0 the array is
+// [rows][W + 1][D] and the first output (D, W).
+constexpr int kDown = 32;
+__global__ void __launch_bounds__(32 * kDown) column_sum_kernel(const ColumnSumArgs p) {
+    __shared__ float red[kDown][33];
+    const int lane = threadIdx.x % 32, row = threadIdx.x / 32;
+    const long long col = static_cast<long long>(blockIdx.x) * 32 + lane;
     float s[4] = {0.f, 0.f, 0.f, 0.f};
     if (col < p.cols) {
         const float* src = p.partial + col;
-        for (int r = row; r < p.rows; r += 4 * kRows) {
+        for (int r = row; r < p.rows; r += 4 * kDown) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-                if (r + k * kRows < p.rows) s[k] += __ldg(src + (r + k * kRows) * p.stride);
+                if (r + k * kDown < p.rows) s[k] += __ldg(src + (r + k * kDown) * p.stride);
         }
     }
     red[row][lane] = (s[0] + s[1]) + (s[2] + s[3]);
@@ -292,7 +332,7 @@ __global__ void __launch_bounds__(kThreads) column_sum_kernel(const ColumnSumArg
     if (row != 0 || col >= p.cols) return;
     float v = 0.f;
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) v += red[r][lane];
+    for (int r = 0; r < kDown; ++r) v += red[r][lane];
     if (p.W > 0) {
         const long long j = col / p.c1, d = col % p.c1;  // c1 = D
         if (j < p.W)
@@ -320,12 +360,12 @@ cudaError_t conv_fwd_e(const ConvArgs& a, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
-// 16 bytes of a row per thread where its width, stride and address allow it,
-// else 4 bytes (bf16), else one element: neighbouring threads then still read
-// neighbouring elements.
+// Four channels per thread where a row's width, stride and address allow it,
+// else two (bf16), else one: neighbouring threads then still read neighbouring
+// elements.
 template <typename T, int W>
 cudaError_t conv_fwd_w(const ConvArgs& a, cudaStream_t stream) {
-    constexpr int E = 16 / sizeof(T);
+    constexpr int E = 4;
     if (rows_take<T>(a.x, a.x_stride, a.D, E)) return conv_fwd_e<T, W, E>(a, stream);
     if constexpr (sizeof(T) == 2)
         if (rows_take<T>(a.x, a.x_stride, a.D, 2)) return conv_fwd_e<T, W, 2>(a, stream);
@@ -358,12 +398,13 @@ cudaError_t conv_step_w(const ConvStepArgs& a, cudaStream_t stream) {
 }  // namespace
 
 // Tokens per thread: long blocks re-read fewer rows at their edges (W-1 per
-// block), short ones give small inputs enough threads.
+// block) and leave fewer partial rows, short ones give small inputs enough
+// threads (16384 x 2048 backward: 128 tokens and 64 K threads 83 us, 32 tokens
+// 88 us; 16384 x 6144 forward: 64 tokens 77 us, 128 tokens 80 us).
 int conv_block_tokens(int B, int T, int D, int backward) {
-    const long long per_thread = backward ? 4 : 8;
-    const long long work = static_cast<long long>(B) * T * ((D + per_thread - 1) / per_thread);
-    int tb = 64;
-    while (tb > 4 && work / tb < 200000) tb /= 2;
+    const long long work = static_cast<long long>(B) * T * ((D + 3) / 4);
+    int tb = backward ? 128 : 64;
+    while (tb > 4 && work / tb < (backward ? 60000 : 200000)) tb /= 2;
     return tb;
 }
 
@@ -385,7 +426,7 @@ long long conv_partial_rows(long long slots) { return (slots + kRows - 1) / kRow
 
 cudaError_t launch_column_sum(const ColumnSumArgs& a, cudaStream_t stream) {
     if (a.cols == 0) return cudaSuccess;
-    column_sum_kernel<<<static_cast<unsigned>((a.cols + kLanes - 1) / kLanes), kThreads, 0, stream>>>(a);
+    column_sum_kernel<<<static_cast<unsigned>((a.cols + 31) / 32), 32 * kDown, 0, stream>>>(a);
     return cudaGetLastError();
 }
 

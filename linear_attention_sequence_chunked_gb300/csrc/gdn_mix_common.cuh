@@ -151,10 +151,10 @@ __device__ __forceinline__ Raw<T, E> pack(const float* x) {
     for (int i = 0; i < E; ++i) {
         if constexpr (sizeof(T) == 4)
             r.w[i] = __float_as_uint(x[i]);
-        else if (i & 1)
-            r.w[i / 2] |= static_cast<uint32_t>(f32_to_bf16(x[i])) << 16;
-        else
+        else if (i + 1 == E && !(i & 1))
             r.w[i / 2] = f32_to_bf16(x[i]);
+        else if (!(i & 1))
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r.w[i / 2]) : "f"(x[i + 1]), "f"(x[i]));
     }
     return r;
 }
@@ -214,6 +214,11 @@ __device__ __forceinline__ Two mul2(Two a, Two b) {
 __device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
     Two r;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ Two add2(Two a, Two b) {
+    Two r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
     return r;
 }
 __device__ __forceinline__ Two ex2_2(Two a) {
@@ -276,6 +281,30 @@ __device__ __forceinline__ void check_offsets(const int32_t* cu, int N, int T, i
         int b, t0, t1;
         token_range(cu, n, N, T, err, b, t0, t1);
     }
+}
+
+__device__ __forceinline__ Two rcp_2(Two a) {
+    float lo, hi;
+    split(a, lo, hi);
+    return two(rcp(lo), rcp(hi));
+}
+__device__ __forceinline__ Two sigmoid_2(Two x) {
+    return rcp_2(add2(two(1.f, 1.f), ex2_2(mul2(two(-kLog2e, -kLog2e), x))));
+}
+
+// Pairs of elements: E elements are (E + 1) / 2 pairs (an odd one is alone in
+// its pair's low half).
+template <typename T, int E>
+__device__ __forceinline__ void unpack_2(const Raw<T, E>& r, Two* x) {
+#pragma unroll
+    for (int i = 0; i < (E + 1) / 2; ++i) x[i] = two(r.get(2 * i), 2 * i + 1 < E ? r.get(2 * i + 1) : 0.f);
+}
+template <typename T, int E>
+__device__ __forceinline__ Raw<T, E> pack_2(const Two* x) {
+    float v[E + 1];
+#pragma unroll
+    for (int i = 0; i < (E + 1) / 2; ++i) split(x[i], v[2 * i], v[2 * i + 1]);
+    return pack<T, E>(v);
 }
 
 }  // namespace mix

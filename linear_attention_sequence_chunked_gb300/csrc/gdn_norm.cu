@@ -12,9 +12,11 @@
 // and the product and activation rules around it; n is recomputed.
 // Bound by HBM (3 accesses per element gated forward, 5 backward): a team of
 // lanes holds its group's row in registers, so every input is read once; the
-// mean is subtracted before squaring.  In the reverse mode a team keeps one
-// group and walks rows, so the weight gradients accumulate in its registers
-// and leave as one partial row per team, summed afterwards in a fixed order.
+// mean is subtracted before squaring.  In the forward a team takes a few rows
+// with all their loads in flight.  In the reverse mode it keeps one group and
+// walks rows, the next row's loads under way, so the weight gradients
+// accumulate in its registers and leave as one partial row per team, summed
+// afterwards in a fixed order.  Arithmetic runs on pairs of channels.
 #include "gdn_kernels.h"
 #include "gdn_mix_common.cuh"
 
@@ -24,234 +26,323 @@ namespace {
 
 using namespace mix;
 
-constexpr int kThreads = 256;
-
-__device__ __forceinline__ float act(float x, int kind) {
-    return kind == 0 ? x : kind == 1 ? x * sigmoid(x) : sigmoid(x);
+__device__ __forceinline__ Two act_2(Two x, int kind) {
+    return kind == 0 ? x : kind == 1 ? mul2(x, sigmoid_2(x)) : sigmoid_2(x);
 }
-__device__ __forceinline__ float dact(float x, int kind) {
-    if (kind == 0) return 1.f;
-    const float s = sigmoid(x);
-    return kind == 1 ? dsilu(x, s) : s * (1.f - s);
-}
-
-// Sum over the LANES lanes of a team (16 or 32: within a warp; 256: the block).
-template <int LANES>
-__device__ __forceinline__ float team_sum(float x, float* red) {
-    constexpr int M = LANES < 32 ? LANES : 32;
-#pragma unroll
-    for (int m = M / 2; m > 0; m /= 2) x += __shfl_xor_sync(0xffffffffu, x, m);
-    if constexpr (LANES > 32) {
-        __syncthreads();  // the previous sum has been read
-        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
-        __syncthreads();
-        x = red[0];
-#pragma unroll
-        for (int i = 1; i < LANES / 32; ++i) x += red[i];
-    }
-    return x;
+// act'(x)
+__device__ __forceinline__ Two dact_2(Two x, int kind) {
+    const Two one = two(1.f, 1.f);
+    if (kind == 0) return one;
+    const Two s = sigmoid_2(x), r = fma2(s, two(-1.f, -1.f), one);  // r = 1 - s
+    return mul2(s, kind == 1 ? fma2(x, r, one) : r);
 }
 
-// Row of a group: V vectors of E elements per lane, vector v at lane + v LANES.
+// A team: 16 or 32 lanes of a warp, or a whole block of 64 or more.  Its row of
+// a group is V vectors of E elements per lane, vector i at lane + i LANES, held
+// as H pairs of consecutive elements (of vectors 2 h and 2 h + 1 for E = 1).
 template <typename T, int E, int LANES, int V>
-struct Row {
-    float v[V][E];
-    __device__ __forceinline__ void load(const T* p, int lane, int nv, bool on) {
-        Raw<T, E> r[V];
+struct Team {
+    static constexpr int kBlock = LANES < 64 ? 256 : LANES;
+    static constexpr int kTeams = kBlock / LANES;  // per block
+    static constexpr int H = V * E / 2;
+    int lane, nv;
+    float* red;  // shared, 2 x kBlock / 32 floats, for teams of several warps
+
+    __device__ __forceinline__ bool on(int i) const { return lane + i * LANES < nv; }
+    template <typename S>
+    __device__ __forceinline__ void load(const S* p, bool live, Raw<S, E> (&r)[V]) const {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int j = lane + i * LANES;
-            r[i] = load_raw<T, E>(p + static_cast<long long>(j) * E, on && j < nv ? E : 0);
-        }
-#pragma unroll
-        for (int i = 0; i < V; ++i) unpack<T, E>(r[i], v[i]);
+        for (int i = 0; i < V; ++i)
+            r[i] = load_raw<S, E>(p + static_cast<long long>(lane + i * LANES) * E, live && on(i) ? E : 0);
     }
-    __device__ __forceinline__ void store(T* p, int lane, int nv, bool on) const {
+    template <typename S>
+    __device__ __forceinline__ void pairs(const Raw<S, E> (&r)[V], Two (&x)[H]) const {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int j = lane + i * LANES;
-            if (on && j < nv) store_raw<T, E>(p + static_cast<long long>(j) * E, pack<T, E>(v[i]), E);
+        for (int h = 0; h < H; ++h)
+            x[h] = E == 1 ? two(r[2 * h % V].get(0), r[(2 * h + 1) % V].get(0)) : two(r[2 * h / E].get(2 * h % E), r[2 * h / E].get(2 * h % E + (E > 1)));
+    }
+    __device__ __forceinline__ void store(T* p, bool live, const Two (&x)[H]) const {
+        float f[2 * H];
+#pragma unroll
+        for (int h = 0; h < H; ++h) split(x[h], f[2 * h], f[2 * h + 1]);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (live && on(i)) store_raw<T, E>(p + static_cast<long long>(lane + i * LANES) * E, pack<T, E>(f + i * E), E);
+    }
+    // a per-channel parameter, or `missing` everywhere
+    __device__ __forceinline__ void param(const float* p, float missing, Two (&w)[H]) const {
+        if (p) {
+            Raw<float, E> r[V];
+            load(p, true, r);
+            pairs(r, w);
+        } else {
+#pragma unroll
+            for (int h = 0; h < H; ++h) w[h] = two(missing, missing);
         }
+    }
+    // zero where the row has no element
+    __device__ __forceinline__ void clip(Two (&x)[H]) const {
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+            const float lo = on(E == 1 ? 2 * h : 2 * h / E) ? 1.f : 0.f, hi = on(E == 1 ? 2 * h + 1 : 2 * h / E) ? 1.f : 0.f;
+            x[h] = mul2(x[h], two(lo, hi));
+        }
+    }
+    // sums over the team of both arguments
+    __device__ __forceinline__ void sums(Two a, Two b, float& sa, float& sb) const {
+        float lo, hi;
+        split(a, lo, hi);
+        sa = lo + hi;
+        split(b, lo, hi);
+        sb = lo + hi;
+        constexpr int M = LANES < 32 ? LANES : 32;
+#pragma unroll
+        for (int m = M / 2; m > 0; m /= 2) {
+            sa += __shfl_xor_sync(0xffffffffu, sa, m);
+            sb += __shfl_xor_sync(0xffffffffu, sb, m);
+        }
+        if constexpr (LANES > 32) {
+            constexpr int WARPS = LANES / 32;
+            __syncthreads();  // the previous sums have been read
+            if ((threadIdx.x & 31) == 0) {
+                red[threadIdx.x >> 5] = sa;
+                red[WARPS + (threadIdx.x >> 5)] = sb;
+            }
+            __syncthreads();
+            sa = red[0];
+            sb = red[WARPS];
+#pragma unroll
+            for (int i = 1; i < WARPS; ++i) {
+                sa += red[i];
+                sb += red[WARPS + i];
+            }
+        }
+    }
+    // x' -> x' - mean (where centered)
+    __device__ __forceinline__ void center(Two (&x)[H], float inv) const {
+        Two a = two(0.f, 0.f);
+#pragma unroll
+        for (int h = 0; h < H; ++h) a = add2(a, x[h]);
+        float m, unused;
+        sums(a, a, m, unused);
+        m *= -inv;
+#pragma unroll
+        for (int h = 0; h < H; ++h) x[h] = add2(x[h], two(m, m));
+        clip(x);
     }
 };
 
-// x' -> n in place; returns r
-template <int E, int LANES, int V>
-__device__ __forceinline__ float normalise(float (&x)[V][E], int lane, int nv, float inv, float eps, int center,
-                                           float* red) {
-    if (center) {
-        float s = 0.f;
+// A team takes R rows of one group.
+template <typename T, int E, int LANES, int V, int R>
+__global__ void __launch_bounds__(Team<T, E, LANES, V>::kBlock) norm_fwd_kernel(const NormArgs p) {
+    using Tm = Team<T, E, LANES, V>;
+    constexpr int H = Tm::H;
+    __shared__ float red[LANES > 32 ? 2 * LANES / 32 : 1];
+    const int size = p.C / p.groups;
+    const Tm tm{static_cast<int>(threadIdx.x) % LANES, size / E, red};
+    const long long unit = static_cast<long long>(blockIdx.x) * Tm::kTeams + threadIdx.x / LANES;
+    const long long row0 = unit / p.groups * R;  // a team past the last row still meets the others' shuffles
+    const int c0 = static_cast<int>(unit % p.groups) * size;
+    Raw<T, E> xr[R][V], gr[R][V];
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-#pragma unroll
-            for (int e = 0; e < E; ++e) s += x[i][e];
-        const float m = team_sum<LANES>(s, red) * inv;
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-#pragma unroll
-            for (int e = 0; e < E; ++e) x[i][e] = lane + i * LANES < nv ? x[i][e] - m : 0.f;
+    for (int r = 0; r < R; ++r) {
+        const bool live = row0 + r < p.rows;
+        const long long row = live ? row0 + r : 0;
+        tm.load(static_cast<const T*>(p.x) + row * p.x_stride + c0, live, xr[r]);
+        if (p.gate) tm.load(static_cast<const T*>(p.gate) + row * p.gate_stride + c0, live, gr[r]);
     }
-    float s = 0.f;
+    Two w[H], b[H];
+    tm.param(p.weight ? p.weight + c0 : nullptr, 1.f, w);
+    tm.param(p.bias ? p.bias + c0 : nullptr, 0.f, b);
+    const float inv = 1.f / size;
 #pragma unroll
-    for (int i = 0; i < V; ++i)
+    for (int r = 0; r < R; ++r) {
+        Two x[H], g[H];
+        tm.pairs(xr[r], x);
+        if (p.gate) {
+            tm.pairs(gr[r], g);
 #pragma unroll
-        for (int e = 0; e < E; ++e) s = fmaf(x[i][e], x[i][e], s);
-    const float r = 1.f / sqrtf(fmaf(team_sum<LANES>(s, red), inv, eps));
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-#pragma unroll
-        for (int e = 0; e < E; ++e) x[i][e] *= r;
-    return r;
-}
-
-template <int E, int LANES, int V>
-__device__ __forceinline__ void load_param(const float* p, float missing, int lane, int nv, float (&w)[V][E]) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int j = lane + i * LANES;
-#pragma unroll
-        for (int e = 0; e < E; ++e) w[i][e] = missing;
-        if (p && j < nv) unpack<float, E>(load_raw<float, E>(p + static_cast<long long>(j) * E, E), w[i]);
-    }
-}
-
-template <typename T, int E, int LANES, int V>
-__global__ void __launch_bounds__(kThreads) norm_fwd_kernel(const NormArgs p) {
-    __shared__ float red[kThreads / 32];
-    const int size = p.C / p.groups, nv = size / E;
-    const int lane = threadIdx.x % LANES;
-    const long long unit = static_cast<long long>(blockIdx.x) * (kThreads / LANES) + threadIdx.x / LANES;
-    const bool on = unit < p.rows * p.groups;  // whole teams; an idle one still meets the others' shuffles
-    const long long row = on ? unit / p.groups : 0;
-    const int c0 = on ? static_cast<int>(unit % p.groups) * size : 0;
-    Row<T, E, LANES, V> x, gt;
-    x.load(static_cast<const T*>(p.x) + row * p.x_stride + c0, lane, nv, on);
-    if (p.gate) {
-        gt.load(static_cast<const T*>(p.gate) + row * p.gate_stride + c0, lane, nv, on);
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                gt.v[i][e] = act(gt.v[i][e], p.activation);
-                if (p.gate_first) x.v[i][e] = lane + i * LANES < nv ? x.v[i][e] * gt.v[i][e] : 0.f;
+            for (int h = 0; h < H; ++h) {
+                g[h] = act_2(g[h], p.activation);
+                if (p.gate_first) x[h] = mul2(x[h], g[h]);
             }
-    }
-    normalise<E, LANES, V>(x.v, lane, nv, 1.f / size, p.eps, p.center, red);
-    float w[V][E], b[V][E];
-    load_param<E, LANES, V>(p.weight ? p.weight + c0 : nullptr, 1.f, lane, nv, w);
-    load_param<E, LANES, V>(p.bias ? p.bias + c0 : nullptr, 0.f, lane, nv, b);
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const float v = fmaf(x.v[i][e], w[i][e], b[i][e]);
-            x.v[i][e] = p.gate ? (p.gate_first ? v : v * gt.v[i][e]) : act(v, p.activation);
         }
-    x.store(static_cast<T*>(p.y) + row * p.C + c0, lane, nv, on);
+        if (p.center) tm.center(x, inv);
+        Two a = two(0.f, 0.f);
+#pragma unroll
+        for (int h = 0; h < H; ++h) a = fma2(x[h], x[h], a);
+        float ss, unused;
+        tm.sums(a, a, ss, unused);
+        const float rs = 1.f / sqrtf(fmaf(ss, inv, p.eps));
+        const Two r2 = two(rs, rs);
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+            x[h] = fma2(mul2(x[h], r2), w[h], b[h]);
+            if (!p.gate)
+                x[h] = act_2(x[h], p.activation);
+            else if (!p.gate_first)
+                x[h] = mul2(x[h], g[h]);
+        }
+        tm.store(static_cast<T*>(p.y) + (row0 + r) * p.C + c0, row0 + r < p.rows, x);
+    }
 }
 
 // Team `unit` keeps group unit % groups and takes rows unit / groups, + teams, ...
 template <typename T, int E, int LANES, int V>
-__global__ void __launch_bounds__(kThreads) norm_bwd_kernel(const NormArgs p, int teams) {
-    __shared__ float red[kThreads / 32];
-    const int size = p.C / p.groups, nv = size / E;
+__global__ void __launch_bounds__(Team<T, E, LANES, V>::kBlock) norm_bwd_kernel(const NormArgs p, int teams) {
+    using Tm = Team<T, E, LANES, V>;
+    constexpr int H = Tm::H;
+    __shared__ float red[LANES > 32 ? 2 * LANES / 32 : 1];
+    const int size = p.C / p.groups;
     const float inv = 1.f / size;
-    const int lane = threadIdx.x % LANES;
-    const long long unit = static_cast<long long>(blockIdx.x) * (kThreads / LANES) + threadIdx.x / LANES;
+    const Tm tm{static_cast<int>(threadIdx.x) % LANES, size / E, red};
+    const long long unit = static_cast<long long>(blockIdx.x) * Tm::kTeams + threadIdx.x / LANES;
     const bool live = unit < static_cast<long long>(teams) * p.groups;
     const int team = live ? static_cast<int>(unit / p.groups) : 0;
     const int c0 = live ? static_cast<int>(unit % p.groups) * size : 0;
-    float w[V][E], b[V][E], dw[V][E], db[V][E];
-    load_param<E, LANES, V>(p.weight ? p.weight + c0 : nullptr, 1.f, lane, nv, w);
-    load_param<E, LANES, V>(p.bias ? p.bias + c0 : nullptr, 0.f, lane, nv, b);
+    const Two zero = two(0.f, 0.f);
+    Two w[H], dw[H], db[H];
+    tm.param(p.weight ? p.weight + c0 : nullptr, 1.f, w);
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-#pragma unroll
-        for (int e = 0; e < E; ++e) dw[i][e] = db[i][e] = 0.f;
+    for (int h = 0; h < H; ++h) dw[h] = db[h] = zero;
+    Raw<T, E> xr[V], gr[V], dr[V];
+    auto load = [&](long long row) {
+        const bool on = live && row < p.rows;
+        if (!on) row = 0;
+        tm.load(static_cast<const T*>(p.x) + row * p.x_stride + c0, on, xr);
+        tm.load(static_cast<const T*>(p.d_out) + row * p.C + c0, on, dr);
+        if (p.gate) tm.load(static_cast<const T*>(p.gate) + row * p.gate_stride + c0, on, gr);
+    };
+    load(team);
+    const bool first = p.gate && p.gate_first;
     const long long steps = (p.rows + teams - 1) / teams;
     for (long long s = 0; s < steps; ++s) {
         const long long row = team + s * teams;
-        const bool on = live && row < p.rows;
-        Row<T, E, LANES, V> x, gt, dy;
-        float n[V][E];
-        x.load(static_cast<const T*>(p.x) + (on ? row : 0) * p.x_stride + c0, lane, nv, on);
-        dy.load(static_cast<const T*>(p.d_out) + (on ? row : 0) * p.C + c0, lane, nv, on);
-        if (p.gate) gt.load(static_cast<const T*>(p.gate) + (on ? row : 0) * p.gate_stride + c0, lane, nv, on);
+        const bool on = live && row < p.rows;  // a row that is not there is all zeros
+        Two x[H], g[H], dy[H], n[H];
+        tm.pairs(xr, x);
+        tm.pairs(dr, dy);
+        if (p.gate) tm.pairs(gr, g);
+        load(row + teams);
 #pragma unroll
-        for (int i = 0; i < V; ++i)
+        for (int h = 0; h < H; ++h) n[h] = first ? mul2(x[h], act_2(g[h], p.activation)) : x[h];
+        if (p.center) tm.center(n, inv);
+        // With a gate dv does not need the norm, and one exchange gives both sums.
+        const bool early = p.gate;
+        Two a = zero, c = zero;
 #pragma unroll
-            for (int e = 0; e < E; ++e)
-                n[i][e] = p.gate && p.gate_first && lane + i * LANES < nv ? x.v[i][e] * act(gt.v[i][e], p.activation) : x.v[i][e];
-        const float r = normalise<E, LANES, V>(n, lane, nv, inv, p.eps, p.center, red);
-        // dv into dy; with the gate after the norm, its own gradient at once
-        float sn = 0.f, s1 = 0.f;
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const float v = fmaf(n[i][e], w[i][e], b[i][e]);
-                float dv = dy.v[i][e];
-                if (!p.gate) {
-                    dv *= dact(v, p.activation);
-                } else if (!p.gate_first) {
-                    const float ga = gt.v[i][e];
-                    gt.v[i][e] = dv * v * dact(ga, p.activation);
-                    dv *= act(ga, p.activation);
+        for (int h = 0; h < H; ++h) {
+            a = fma2(n[h], n[h], a);
+            if (early) {
+                if (!first) {
+                    // its own gradient wants v = n w + b: kept as dy act'(g), finished below
+                    const Two d = dy[h];
+                    dy[h] = mul2(d, act_2(g[h], p.activation));
+                    g[h] = mul2(d, dact_2(g[h], p.activation));
                 }
-                if (on && lane + i * LANES < nv) {
-                    dw[i][e] = fmaf(dv, n[i][e], dw[i][e]);
-                    db[i][e] += dv;
-                } else {
-                    dv = 0.f;
-                }
-                const float dn = dv * w[i][e];
-                dy.v[i][e] = dn;
-                sn = fmaf(dn, n[i][e], sn);
-                s1 += dn;
+                c = fma2(mul2(dy[h], w[h]), n[h], c);
             }
-        sn = team_sum<LANES>(sn, red) * inv;
-        s1 = p.center ? team_sum<LANES>(s1, red) * inv : 0.f;
+        }
+        float ss, sn;
+        tm.sums(a, c, ss, sn);
+        const float rs = on ? 1.f / sqrtf(fmaf(ss, inv, p.eps)) : 0.f;
+        const Two r2 = two(rs, rs);
+        sn *= rs * inv;
+        if (!early || p.bias) {
+            Two b[H];
+            tm.param(p.bias ? p.bias + c0 : nullptr, 0.f, b);
+            c = zero;
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const float d = r * (dy.v[i][e] - s1 - n[i][e] * sn);
-                if (p.gate && p.gate_first) {
-                    const float ga = gt.v[i][e];
-                    gt.v[i][e] = d * x.v[i][e] * dact(ga, p.activation);
-                    x.v[i][e] = d * act(ga, p.activation);
-                } else {
-                    x.v[i][e] = d;
+            for (int h = 0; h < H; ++h) {
+                n[h] = mul2(n[h], r2);
+                const Two v = fma2(n[h], w[h], b[h]);
+                if (!early) {
+                    dy[h] = mul2(dy[h], dact_2(v, p.activation));
+                    c = fma2(mul2(dy[h], w[h]), n[h], c);
+                } else if (!first) {
+                    g[h] = mul2(g[h], v);
                 }
             }
-        x.store(static_cast<T*>(p.dx) + row * p.C + c0, lane, nv, on);
-        if (p.gate) gt.store(static_cast<T*>(p.dgate) + row * p.C + c0, lane, nv, on);
+            if (!early) {
+                float unused;
+                tm.sums(c, c, sn, unused);
+                sn *= inv;
+            }
+        } else {
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                n[h] = mul2(n[h], r2);
+                if (!first) g[h] = mul2(g[h], mul2(n[h], w[h]));
+            }
+        }
+        Two m1 = zero;
+        if (p.center) {
+            c = zero;
+#pragma unroll
+            for (int h = 0; h < H; ++h) c = fma2(dy[h], w[h], c);
+            float s1, unused;
+            tm.sums(c, c, s1, unused);
+            m1 = two(-s1 * inv, -s1 * inv);
+        }
+        const Two sn2 = two(-sn, -sn);
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+            dw[h] = fma2(dy[h], n[h], dw[h]);
+            db[h] = add2(db[h], dy[h]);
+            const Two d = mul2(r2, add2(fma2(dy[h], w[h], m1), mul2(n[h], sn2)));
+            if (first) {
+                const Two gd = dact_2(g[h], p.activation);
+                const Two ga = act_2(g[h], p.activation);
+                g[h] = mul2(mul2(d, x[h]), gd);
+                x[h] = mul2(d, ga);
+            } else {
+                x[h] = d;
+            }
+        }
+        tm.store(static_cast<T*>(p.dx) + row * p.C + c0, on, x);
+        if (p.gate) tm.store(static_cast<T*>(p.dgate) + row * p.C + c0, on, g);
     }
     if (!p.partial || !live) return;
     float* pw = p.partial + static_cast<long long>(team) * (p.bias ? 2 : 1) * p.C + c0;
+    float fw[2 * H], fb[2 * H];
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+        split(dw[h], fw[2 * h], fw[2 * h + 1]);
+        split(db[h], fb[2 * h], fb[2 * h + 1]);
+    }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int j = lane + i * LANES;
-        if (j >= nv) continue;
+        if (!tm.on(i)) continue;
+        const int at = (tm.lane + i * LANES) * E;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            pw[j * E + e] = dw[i][e];
-            if (p.bias) pw[p.C + j * E + e] = db[i][e];
+            pw[at + e] = fw[i * E + e];
+            if (p.bias) pw[p.C + at + e] = fb[i * E + e];
         }
     }
 }
 
+template <typename T, int E, int LANES, int V, int R>
+cudaError_t norm_fwd_r(const NormArgs& a, cudaStream_t stream) {
+    using Tm = Team<T, E, LANES, V>;
+    const long long units = (a.rows + R - 1) / R * a.groups;
+    norm_fwd_kernel<T, E, LANES, V, R><<<static_cast<unsigned>((units + Tm::kTeams - 1) / Tm::kTeams), Tm::kBlock, 0, stream>>>(a);
+    return cudaGetLastError();
+}
+// Several rows per team once one row each gives the GPU more teams than it
+// holds at a time; before that they would only leave SMs without work.
 template <typename T, int E, int LANES, int V>
 cudaError_t norm_fwd_v(const NormArgs& a, cudaStream_t stream) {
-    const long long units = a.rows * a.groups, per = kThreads / LANES;
-    norm_fwd_kernel<T, E, LANES, V><<<static_cast<unsigned>((units + per - 1) / per), kThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    constexpr int R = V == 1 && E > 1 ? 4 : 1;
+    if (R > 1 && a.rows * a.groups * LANES >= 152LL * 2048) return norm_fwd_r<T, E, LANES, V, R>(a, stream);
+    return norm_fwd_r<T, E, LANES, V, 1>(a, stream);
 }
 template <typename T, int E, int LANES, int V>
 cudaError_t norm_bwd_v(const NormArgs& a, cudaStream_t stream) {
+    using Tm = Team<T, E, LANES, V>;
     const int teams = norm_partial_rows(a.rows, a.C, a.groups, a.dtype);
-    const long long units = static_cast<long long>(teams) * a.groups, per = kThreads / LANES;
-    norm_bwd_kernel<T, E, LANES, V><<<static_cast<unsigned>((units + per - 1) / per), kThreads, 0, stream>>>(a, teams);
+    const long long units = static_cast<long long>(teams) * a.groups;
+    norm_bwd_kernel<T, E, LANES, V><<<static_cast<unsigned>((units + Tm::kTeams - 1) / Tm::kTeams), Tm::kBlock, 0, stream>>>(a, teams);
     return cudaGetLastError();
 }
 
@@ -263,7 +354,7 @@ bool wide_rows(const NormArgs& a) {
 }
 
 // Lanes and registers per group: a half warp or a warp where the group fits
-// its registers, else the block.  Rows that 16-byte accesses cannot take (odd
+// its registers, else a block.  Rows that 16-byte accesses cannot take (odd
 // sizes, strides or addresses) go element by element, neighbouring lanes on
 // neighbouring elements.
 #define GDN_NORM_SIZES(fn, T)                                       \
@@ -274,15 +365,16 @@ bool wide_rows(const NormArgs& a) {
         if (nv <= 16) return fn<T, E, 16, 1>(a, stream);            \
         if (nv <= 32) return fn<T, E, 32, 1>(a, stream);            \
         if (nv <= 64) return fn<T, E, 32, 2>(a, stream);            \
-        if (nv <= 256) return fn<T, E, 256, 1>(a, stream);          \
+        if (nv <= 128) return fn<T, E, 128, 1>(a, stream);          \
+        if (nv <= 256) return fn<T, E, 128, 2>(a, stream);          \
         if (nv <= 512) return fn<T, E, 256, 2>(a, stream);          \
-        if (nv <= 1024) return fn<T, E, 256, 4>(a, stream);         \
-        if constexpr (sizeof(T) == 4) return fn<T, E, 256, 8>(a, stream); \
+        if (nv <= 1024) return fn<T, E, 512, 2>(a, stream);         \
+        if constexpr (sizeof(T) == 4) return fn<T, E, 512, 4>(a, stream); \
     }                                                               \
     if (size <= 128) return fn<T, 1, 32, 4>(a, stream);             \
     if (size <= 512) return fn<T, 1, 32, 16>(a, stream);            \
-    if (size <= 2048) return fn<T, 1, 256, 8>(a, stream);           \
-    return fn<T, 1, 256, 32>(a, stream)
+    if (size <= 2048) return fn<T, 1, 128, 16>(a, stream);          \
+    return fn<T, 1, 512, 16>(a, stream)
 
 template <typename T>
 cudaError_t norm_fwd_t(const NormArgs& a, cudaStream_t stream) {
@@ -295,12 +387,12 @@ cudaError_t norm_bwd_t(const NormArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-// Teams per group in the reverse mode, one partial row each: enough to fill
-// the GPU, few enough that the partial rows cost little beside the inputs.
+// Teams per group in the reverse mode, one partial row each: about 512 threads
+// per SM, few enough that the partial rows cost little beside the inputs.
 int norm_partial_rows(long long rows, int C, int groups, int dtype) {
-    const int size = C / groups;
-    const int lanes = size <= (dtype == 0 ? 512 : 256) ? 16 : 256;
-    long long teams = 152LL * 8 * kThreads / lanes / 2 / groups;
+    const int vectors = C / groups / (dtype == 0 ? 8 : 4);
+    const int lanes = vectors <= 16 ? 16 : vectors <= 64 ? 32 : vectors <= 256 ? 128 : vectors <= 512 ? 256 : 512;
+    long long teams = 152LL * 512 / lanes / groups;
     if (teams < 1) teams = 1;
     return static_cast<int>(rows < teams ? rows : teams);
 }
