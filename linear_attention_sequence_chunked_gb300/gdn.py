@@ -51,6 +51,8 @@ def header_functions():
 def load():
     """Load the built library (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

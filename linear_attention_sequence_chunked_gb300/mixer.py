@@ -16,67 +16,83 @@ and evenly spaced.  Other inputs are contiguous.
 
 from __future__ import annotations
 
-from .gdn import _check, _ptr, _stream, _workspace, load
+import torch
+
+from .gdn import _check, _stream, _workspace, load
 
 _ACTIVATIONS = {None: 0, "none": 0, "silu": 1, "sigmoid": 2}
 STATE_SIZES = (8, 16, 32, 64, 128)
 
-
-def _torch():
-    import torch
-    return torch
-
+# The checks below run on every call, single-token ones too: each looks at a
+# tensor once, and takes its time only when something is wrong.
 
 def _dtype(x, name):
-    torch = _torch()
-    if x.dtype == torch.bfloat16:
+    dt = x.dtype
+    if dt is torch.bfloat16:
         return 0
-    if x.dtype == torch.float32:
+    if dt is torch.float32:
         return 1
-    raise ValueError(f"{name} must be torch.bfloat16 or torch.float32, got {x.dtype}")
+    raise ValueError(f"{name} must be torch.bfloat16 or torch.float32, got {dt}")
 
 
-def _rows(x, inner=1):
-    """(address, row stride) of an activation whose last `inner` dimensions
-    form a dense row and whose rows are evenly spaced."""
-    if x.device.type != "cuda":
-        raise ValueError(f"expected a CUDA tensor, got one on {x.device}")
-    width = 1
-    if not x.is_contiguous():
-        shape, strides = x.shape, x.stride()
-        lead = x.dim() - inner
-        for k in range(x.dim() - 1, lead - 1, -1):
-            if shape[k] != 1 and strides[k] != width:
-                raise ValueError(f"expected dense rows, got shape {tuple(shape)} strides {strides}")
-            width *= shape[k]
-        row = step = None
-        for k in range(lead - 1, -1, -1):
-            if shape[k] == 1:
-                continue
-            if row is None:
-                row = step = strides[k]
-            elif strides[k] != step:
-                raise ValueError(f"expected evenly spaced rows, got shape {tuple(shape)} strides {strides}")
-            step = strides[k] * shape[k]
-        if row is None:
-            row = width
-        if row < width and x.numel():
-            raise ValueError(f"expected rows apart from each other, got shape {tuple(shape)} strides {strides}")
-        return x.data_ptr(), max(row, width)
-    for k in range(1, inner + 1):
-        width *= x.shape[-k]
-    return x.data_ptr(), width
+def _is(name, t, shape, dtype, dev):
+    """Refuses a tensor of another type, shape or device."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        if t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        raise ValueError(f"{name} is on {t.device}: all tensors must share one device")
 
 
-def _same(name, t, shape, dtype, device):
+def _dense(name, t, shape, dtype, dev):
+    """Address of a contiguous tensor of this type and shape (None: None)."""
     if t is None:
-        return
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}: all tensors must share one device ({device})")
+        return None
+    if t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and t.shape == shape:
+        return t.data_ptr()
+    _is(name, t, shape, dtype, dev)
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor, got shape {tuple(t.shape)} strides {t.stride()}")
+    return t.data_ptr()
+
+
+def _on_gpu(dev, x):
+    if dev < 0:
+        raise ValueError(f"expected a CUDA tensor, got one on {x.device}")
+
+
+def _current(stream, dev):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+
+
+def _rows(x, width, inner=1):
+    """(address, row stride) of an activation whose last `inner` dimensions
+    form a dense row of `width` elements and whose rows are evenly spaced."""
+    if x.is_contiguous():
+        return x.data_ptr(), width
+    shape, strides = x.shape, x.stride()
+    if inner == 1 and len(shape) == 2 and strides[1] == 1 and strides[0] >= width:
+        return x.data_ptr(), strides[0]
+    dense = width
+    for k in range(len(shape) - inner, len(shape)):
+        dense //= max(shape[k], 1)
+        if strides[k] != dense and shape[k] != 1:
+            raise ValueError(f"expected dense rows, got shape {tuple(shape)} strides {strides}")
+    row = step = None
+    for k in range(len(shape) - inner - 1, -1, -1):
+        if shape[k] == 1:
+            continue
+        if row is None:
+            row = strides[k]
+        elif strides[k] != step:
+            raise ValueError(f"expected evenly spaced rows, got shape {tuple(shape)} strides {strides}")
+        step = strides[k] * shape[k]
+    if row is None:
+        row = width
+    if row < width:
+        raise ValueError(f"expected rows apart from each other, got shape {tuple(shape)} strides {strides}")
+    return x.data_ptr(), row
 
 
 def _activation(name, allowed=("none", "silu")):
@@ -85,47 +101,56 @@ def _activation(name, allowed=("none", "silu")):
     return _ACTIVATIONS[name]
 
 
-def _sequences(x, cu_seqlens, name):
-    """(N, B of the C ABI) of a (B, T, ...) activation."""
+def _sequences(x, cu_seqlens, dev, name):
+    """(number of sequences, address of the offsets) of a (B, T, ...) activation."""
     if cu_seqlens is None:
-        return x.shape[0]
-    torch = _torch()
-    if cu_seqlens.dtype != torch.int32:
+        return x.shape[0], None
+    if cu_seqlens.dtype is not torch.int32:
         raise ValueError(f"cu_seqlens must be int32, got {cu_seqlens.dtype}")
     if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
         raise ValueError("cu_seqlens must be a 1-D tensor of N + 1 offsets")
-    if cu_seqlens.device != x.device:
-        raise ValueError(f"cu_seqlens is on {cu_seqlens.device}: all tensors must share one device ({x.device})")
     if x.shape[0] != 1:
         raise ValueError(f"packed inputs must have batch extent 1, got {name} of shape {tuple(x.shape)}")
-    return cu_seqlens.numel() - 1
+    return cu_seqlens.numel() - 1, _dense("cu_seqlens", cu_seqlens, cu_seqlens.shape, torch.int32, dev)
 
 
-def _check_slots(slots, batch, device):
-    if slots is not None:
-        _same("slots", slots, (batch,), _torch().int32, device)
+def _state(state, out_state, slots, batch, row, dtype, dev):
+    """Addresses of a state cache, of where it goes, and of the slots; its rows."""
+    if state.dim() != 3 or state.shape[1:] != row or (slots is None and state.shape[0] < batch):
+        raise ValueError(f"state must be (S, {row[0]}, {row[1]}) with a row for each of the {batch}, "
+                         f"got shape {tuple(state.shape)}")
+    shape = state.shape
+    to = state if out_state is None else out_state
+    at = _dense("state", state, shape, dtype, dev)
+    return (at, at if to is state else _dense("out_state", to, shape, dtype, dev),
+            None if slots is None else _dense("slots", slots, (batch,), torch.int32, dev), shape[0])
 
 
 # ----------------------------------------------------------------------------
 # short causal convolution
 # ----------------------------------------------------------------------------
 
-def _conv_args(x, weight, bias, initial_state, cu_seqlens):
-    torch = _torch()
-    if x.dim() != 3:
-        raise ValueError(f"x must be (B, T, D), got shape {tuple(x.shape)}")
-    dtype = _dtype(x, "x")
-    B, T, D = x.shape
+def _taps(weight, D):
     if weight.dim() != 2 or weight.shape[0] != D:
         raise ValueError(f"weight must be (D, W) with D = {D}, got shape {tuple(weight.shape)}")
     W = weight.shape[1]
-    if W not in (2, 3, 4):
+    if not 2 <= W <= 4:
         raise ValueError(f"weight must have 2, 3 or 4 taps, got {W}")
-    N = _sequences(x, cu_seqlens, "x")
-    _same("weight", weight, (D, W), torch.float32, x.device)
-    _same("bias", bias, (D,), torch.float32, x.device)
-    _same("initial_state", initial_state, (N, W - 1, D), x.dtype, x.device)
-    return dtype, N, T, D, W
+    return W
+
+
+def _conv_args(x, weight, bias, activation, initial_state, cu_seqlens):
+    if x.dim() != 3:
+        raise ValueError(f"x must be (B, T, D), got shape {tuple(x.shape)}")
+    dtype, dev = _dtype(x, "x"), x.get_device()
+    act = _activation(activation)
+    T, D = x.shape[1:]
+    W = _taps(weight, D)
+    N, cu = _sequences(x, cu_seqlens, dev, "x")
+    ptrs = (_dense("weight", weight, (D, W), torch.float32, dev), _dense("bias", bias, (D,), torch.float32, dev),
+            _dense("initial_state", initial_state, (N, W - 1, D), x.dtype, dev), cu)
+    _on_gpu(dev, x)
+    return dev, (N, T, D, W, act, dtype), (*_rows(x, D), *ptrs)
 
 
 def short_conv_fwd(x, weight, bias=None, activation="silu", initial_state=None, cu_seqlens=None,
@@ -133,14 +158,11 @@ def short_conv_fwd(x, weight, bias=None, activation="silu", initial_state=None, 
     """Causal convolution of every channel over its last W tokens: x (B, T, D),
     weight (D, W), bias (D), initial_state (N, W - 1, D) in x's dtype (the
     inputs before each sequence).  Returns (y (B, T, D), final_state or None)."""
-    torch = _torch()
-    dtype, N, T, D, W = _conv_args(x, weight, bias, initial_state, cu_seqlens)
-    act = _activation(activation)
-    px, sx = _rows(x)
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    fs = torch.empty((N, W - 1, D), dtype=x.dtype, device=x.device) if output_final_state else None
-    _check(load().gdn_conv_fwd(px, sx, _ptr(weight), _ptr(bias), _ptr(initial_state), _ptr(cu_seqlens), _ptr(y),
-                               _ptr(fs), N, T, D, W, act, dtype, _stream(stream)), "gdn_conv_fwd")
+    dev, dims, args = _conv_args(x, weight, bias, activation, initial_state, cu_seqlens)
+    y = x.new_empty(x.shape)
+    fs = x.new_empty((dims[0], dims[3] - 1, dims[2])) if output_final_state else None
+    _check(load().gdn_conv_fwd(*args, y.data_ptr(), None if fs is None else fs.data_ptr(), *dims, _current(stream, dev)),
+           "gdn_conv_fwd")
     return y, fs
 
 
@@ -148,27 +170,27 @@ def short_conv_bwd(x, weight, d_out, bias=None, activation="silu", initial_state
                    d_final_state=None, stream=None):
     """Gradients of short_conv_fwd: a dict of dx, dweight, dbias (with a bias)
     and d_initial_state (with an initial state)."""
-    torch = _torch()
-    dtype, N, T, D, W = _conv_args(x, weight, bias, initial_state, cu_seqlens)
-    act = _activation(activation)
-    _same("d_out", d_out, x.shape, x.dtype, x.device)
-    _same("d_final_state", d_final_state, (N, W - 1, D), x.dtype, x.device)
-    px, sx = _rows(x)
-    dev = x.device
-    res = {"dx": torch.empty(x.shape, dtype=x.dtype, device=dev),
-           "dweight": torch.empty((D, W), dtype=torch.float32, device=dev)}
+    dev, dims, args = _conv_args(x, weight, bias, activation, initial_state, cu_seqlens)
+    N, T, D, W = dims[:4]
+    d_out = _dense("d_out", d_out, x.shape, x.dtype, dev)
+    dfs = _dense("d_final_state", d_final_state, (N, W - 1, D), x.dtype, dev)
+    res = {"dx": x.new_empty(x.shape), "dweight": weight.new_empty((D, W))}
     if bias is not None:
-        res["dbias"] = torch.empty((D,), dtype=torch.float32, device=dev)
+        res["dbias"] = weight.new_empty((D,))
     if initial_state is not None:
-        res["d_initial_state"] = torch.empty((N, W - 1, D), dtype=x.dtype, device=dev)
+        res["d_initial_state"] = x.new_empty((N, W - 1, D))
     lib = load()
     nbytes = lib.gdn_conv_bwd_workspace_size(N, T, D, W, int(cu_seqlens is not None))
-    ws = _workspace(nbytes, dev)
-    _check(lib.gdn_conv_bwd(px, sx, _ptr(weight), _ptr(bias), _ptr(initial_state), _ptr(cu_seqlens), _ptr(d_out),
-                            _ptr(d_final_state), _ptr(res["dx"]), _ptr(res["dweight"]), _ptr(res.get("dbias")),
-                            _ptr(res.get("d_initial_state")), N, T, D, W, act, dtype, _ptr(ws), nbytes,
-                            _stream(stream)), "gdn_conv_bwd")
+    ws = _workspace(nbytes, x.device)
+    _check(lib.gdn_conv_bwd(*args, d_out, dfs, res["dx"].data_ptr(), res["dweight"].data_ptr(), _out(res, "dbias"),
+                            _out(res, "d_initial_state"), *dims, ws.data_ptr(), nbytes, _current(stream, dev)),
+           "gdn_conv_bwd")
     return res
+
+
+def _out(res, name):
+    t = res.get(name)
+    return None if t is None else t.data_ptr()
 
 
 def short_conv_step(x, state, weight, bias=None, activation="silu", slots=None, out_state=None, stream=None):
@@ -176,66 +198,54 @@ def short_conv_step(x, state, weight, bias=None, activation="silu", slots=None, 
     place or into out_state.  slots (B, int32): the cache row of each batch row
     (negative: an idle row, whose output is zero); by default row b.  Returns y
     (B, D)."""
-    torch = _torch()
     if x.dim() != 2:
         raise ValueError(f"x must be (B, D), got shape {tuple(x.shape)}")
-    dtype = _dtype(x, "x")
-    B, D = x.shape
-    if weight.dim() != 2 or weight.shape[0] != D or weight.shape[1] not in (2, 3, 4):
-        raise ValueError(f"weight must be (D, W) with D = {D} and 2, 3 or 4 taps, got shape {tuple(weight.shape)}")
-    W = weight.shape[1]
-    dev = x.device
-    _same("weight", weight, (D, W), torch.float32, dev)
-    _same("bias", bias, (D,), torch.float32, dev)
-    _check_state(state, out_state, slots, B, (W - 1, D), x.dtype, dev)
+    dtype, dev = _dtype(x, "x"), x.get_device()
     act = _activation(activation)
-    px, sx = _rows(x)
-    y = torch.empty((B, D), dtype=x.dtype, device=dev)
-    _check(load().gdn_conv_step(px, sx, _ptr(weight), _ptr(bias), _ptr(state),
-                                _ptr(state if out_state is None else out_state), _ptr(slots), _ptr(y), B,
-                                state.shape[0], D, W, act, dtype, _stream(stream)), "gdn_conv_step")
+    B, D = x.shape
+    W = _taps(weight, D)
+    w = _dense("weight", weight, (D, W), torch.float32, dev)
+    b = _dense("bias", bias, (D,), torch.float32, dev)
+    at, to, sl, S = _state(state, out_state, slots, B, (W - 1, D), x.dtype, dev)
+    _on_gpu(dev, x)
+    y = x.new_empty((B, D))
+    _check(load().gdn_conv_step(*_rows(x, D), w, b, at, to, sl, y.data_ptr(), B, S, D, W, act, dtype,
+                             _current(stream, dev)), "gdn_conv_step")
     return y
-
-
-def _check_state(state, out_state, slots, batch, row, dtype, device):
-    if state.dim() != 3 or state.shape[1:] != row or (slots is None and state.shape[0] < batch):
-        raise ValueError(f"state must be (S, {row[0]}, {row[1]}) with a row for each of the {batch}, "
-                         f"got shape {tuple(state.shape)}")
-    _same("state", state, state.shape, dtype, device)
-    _same("out_state", out_state, state.shape, dtype, device)
-    _check_slots(slots, batch, device)
 
 
 # ----------------------------------------------------------------------------
 # selective state space scan
 # ----------------------------------------------------------------------------
 
-def _scan_args(u, dt, A, B, C, D, z, dt_bias):
+def _scan_args(u, dt, A, B, C, D, z, dt_bias, softplus):
     """Checks shared by the scan and its step (u of 3 or 2 dimensions)."""
-    torch = _torch()
-    dtype = _dtype(u, "u")
-    lead, width = u.shape[:-1], u.shape[-1]
-    dev = u.device
-    _same("dt", dt, u.shape, u.dtype, dev)
-    _same("z", z, u.shape, u.dtype, dev)
+    dtype, dev, kind = _dtype(u, "u"), u.get_device(), u.dtype
+    shape = u.shape
+    width = shape[-1]
     if A.dim() != 2 or A.shape[0] != width:
         raise ValueError(f"A must be (D, N) with D = {width}, got shape {tuple(A.shape)}")
     N = A.shape[1]
     if N not in STATE_SIZES:
         raise ValueError(f"the state size must be one of {STATE_SIZES}, got {N}")
-    _same("A", A, (width, N), torch.float32, dev)
-    if B.dim() != u.dim() + 1:
-        raise ValueError(f"B must be {tuple(lead)} + (G, N), got shape {tuple(B.shape)}")
+    _is("dt", dt, shape, kind, dev)
+    if z is not None:
+        _is("z", z, shape, kind, dev)
+    if B.dim() != len(shape) + 1:
+        raise ValueError(f"B must be {tuple(shape[:-1])} + (G, N), got shape {tuple(B.shape)}")
     G = B.shape[-2]
     if G < 1 or width % G:
         raise ValueError(f"the {width} channels must divide into the {G} groups of B")
-    _same("B", B, lead + (G, N), u.dtype, dev)
-    _same("C", C, lead + (G, N), u.dtype, dev)
-    _same("D", D, (width,), torch.float32, dev)
-    _same("dt_bias", dt_bias, (width,), torch.float32, dev)
-    pz, sz = (None, 0) if z is None else _rows(z)
-    return (dtype, width, G, N,
-            (*_rows(u), *_rows(dt), _ptr(A), *_rows(B, 2), *_rows(C, 2), _ptr(D), pz, sz, _ptr(dt_bias)))
+    rows = shape[:-1] + (G, N)
+    _is("B", B, rows, kind, dev)
+    _is("C", C, rows, kind, dev)
+    a = _dense("A", A, (width, N), torch.float32, dev)
+    d = _dense("D", D, (width,), torch.float32, dev)
+    b = _dense("dt_bias", dt_bias, (width,), torch.float32, dev)
+    pz, sz = (None, 0) if z is None else _rows(z, width)
+    return (dev, (width, G, N, dtype),
+            (*_rows(u, width), *_rows(dt, width), a, *_rows(B, G * N, 2), *_rows(C, G * N, 2), d, pz, sz, b,
+             int(softplus)))
 
 
 def ssm_scan_fwd(u, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=True, initial_state=None,
@@ -244,26 +254,26 @@ def ssm_scan_fwd(u, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=True,
     (B, T, G, N); D, dt_bias (D); initial_state (N_seq, D, N) fp32.  Returns
     (out, final_state or None), or (out, final_state, saved) with
     save_for_backward (the states ssm_scan_bwd starts from)."""
-    torch = _torch()
     if u.dim() != 3:
         raise ValueError(f"u must be (B, T, D), got shape {tuple(u.shape)}")
-    nseq = _sequences(u, cu_seqlens, "u")
-    dtype, width, G, N, args = _scan_args(u, dt, A, B, C, D, z, dt_bias)
-    dev, T = u.device, u.shape[1]
-    _same("initial_state", initial_state, (nseq, width, N), torch.float32, dev)
-    varlen = int(cu_seqlens is not None)
-    out = torch.empty(u.shape, dtype=u.dtype, device=dev)
-    fs = torch.empty((nseq, width, N), dtype=torch.float32, device=dev) if output_final_state else None
+    dev, dims, args = _scan_args(u, dt, A, B, C, D, z, dt_bias, dt_softplus)
+    nseq, cu = _sequences(u, cu_seqlens, dev, "u")
+    width, G, N, dtype = dims
+    T, varlen = u.shape[1], int(cu_seqlens is not None)
+    h0 = _dense("initial_state", initial_state, (nseq, width, N), torch.float32, dev)
+    _on_gpu(dev, u)
+    out = u.new_empty(u.shape)
+    fs = A.new_empty((nseq, width, N)) if output_final_state else None
     lib = load()
     saved, sbytes = None, 0
     if save_for_backward:
         sbytes = lib.gdn_ssm_saved_size(nseq, T, width, N, varlen)
-        saved = torch.empty(sbytes, dtype=torch.uint8, device=dev)
+        saved = torch.empty(sbytes, dtype=torch.uint8, device=u.device)
     nbytes = lib.gdn_ssm_fwd_workspace_size(nseq, T, width, G, N, varlen)
-    ws = _workspace(nbytes, dev)
-    _check(lib.gdn_ssm_fwd(*args, int(dt_softplus), _ptr(initial_state), _ptr(cu_seqlens), _ptr(out), _ptr(fs),
-                           _ptr(saved), sbytes, nseq, T, width, G, N, dtype, _ptr(ws), nbytes, _stream(stream)),
-           "gdn_ssm_fwd")
+    ws = _workspace(nbytes, u.device)
+    _check(lib.gdn_ssm_fwd(*args, h0, cu, out.data_ptr(), None if fs is None else fs.data_ptr(),
+                           None if saved is None else saved.data_ptr(), sbytes, nseq, T, *dims,
+                           None if ws is None else ws.data_ptr(), nbytes, _current(stream, dev)), "gdn_ssm_fwd")
     return (out, fs, saved) if save_for_backward else (out, fs)
 
 
@@ -272,37 +282,34 @@ def ssm_scan_bwd(u, dt, A, B, C, d_out, saved, D=None, z=None, dt_bias=None, dt_
     """Gradients of ssm_scan_fwd from the same inputs and the `saved` that it
     returned: a dict of du, ddt, dA, dB, dC, and dD, dz, ddt_bias and
     d_initial_state for those that were given."""
-    torch = _torch()
     if u.dim() != 3:
         raise ValueError(f"u must be (B, T, D), got shape {tuple(u.shape)}")
-    nseq = _sequences(u, cu_seqlens, "u")
-    dtype, width, G, N, args = _scan_args(u, dt, A, B, C, D, z, dt_bias)
-    dev, T = u.device, u.shape[1]
-    _same("d_out", d_out, u.shape, u.dtype, dev)
-    _same("initial_state", initial_state, (nseq, width, N), torch.float32, dev)
-    _same("d_final_state", d_final_state, (nseq, width, N), torch.float32, dev)
-    if saved.dtype != torch.uint8 or saved.device != dev:
+    dev, dims, args = _scan_args(u, dt, A, B, C, D, z, dt_bias, dt_softplus)
+    nseq, cu = _sequences(u, cu_seqlens, dev, "u")
+    width, G, N, dtype = dims
+    T, varlen = u.shape[1], int(cu_seqlens is not None)
+    d_out = _dense("d_out", d_out, u.shape, u.dtype, dev)
+    _dense("initial_state", initial_state, (nseq, width, N), torch.float32, dev)
+    dfs = _dense("d_final_state", d_final_state, (nseq, width, N), torch.float32, dev)
+    if saved.dtype is not torch.uint8 or saved.get_device() != dev or not saved.is_contiguous():
         raise ValueError("saved must be the uint8 buffer that the saving forward returned, on u's device")
-    varlen = int(cu_seqlens is not None)
-    f32 = {"dtype": torch.float32, "device": dev}
-    res = {"du": torch.empty(u.shape, dtype=u.dtype, device=dev), "ddt": torch.empty(u.shape, dtype=u.dtype, device=dev),
-           "dA": torch.empty((width, N), **f32), "dB": torch.empty(B.shape, dtype=u.dtype, device=dev),
-           "dC": torch.empty(B.shape, dtype=u.dtype, device=dev)}
+    _on_gpu(dev, u)
+    res = {"du": u.new_empty(u.shape), "ddt": u.new_empty(u.shape), "dA": A.new_empty((width, N)),
+           "dB": u.new_empty(B.shape), "dC": u.new_empty(B.shape)}
     if D is not None:
-        res["dD"] = torch.empty((width,), **f32)
+        res["dD"] = A.new_empty((width,))
     if z is not None:
-        res["dz"] = torch.empty(u.shape, dtype=u.dtype, device=dev)
+        res["dz"] = u.new_empty(u.shape)
     if dt_bias is not None:
-        res["ddt_bias"] = torch.empty((width,), **f32)
+        res["ddt_bias"] = A.new_empty((width,))
     if initial_state is not None:
-        res["d_initial_state"] = torch.empty((nseq, width, N), **f32)
+        res["d_initial_state"] = A.new_empty((nseq, width, N))
     lib = load()
     nbytes = lib.gdn_ssm_bwd_workspace_size(nseq, T, width, G, N, varlen)
-    ws = _workspace(nbytes, dev)
-    out = [_ptr(res.get(k)) for k in ("du", "ddt", "dz", "dB", "dC", "dA", "dD", "ddt_bias", "d_initial_state")]
-    _check(lib.gdn_ssm_bwd(*args, int(dt_softplus), _ptr(cu_seqlens), _ptr(d_out), _ptr(d_final_state), _ptr(saved),
-                           saved.numel(), *out, nseq, T, width, G, N, dtype, _ptr(ws), nbytes, _stream(stream)),
-           "gdn_ssm_bwd")
+    ws = _workspace(nbytes, u.device)
+    out = [_out(res, k) for k in ("du", "ddt", "dz", "dB", "dC", "dA", "dD", "ddt_bias", "d_initial_state")]
+    _check(lib.gdn_ssm_bwd(*args, cu, d_out, dfs, saved.data_ptr(), saved.numel(), *out, nseq, T, *dims,
+                           ws.data_ptr(), nbytes, _current(stream, dev)), "gdn_ssm_bwd")
     return res
 
 
@@ -311,16 +318,14 @@ def ssm_scan_step(u, dt, A, B, C, state, D=None, z=None, dt_bias=None, dt_softpl
     """One token per row: u, dt, z (B, D), B, C (B, G, N) and a state cache
     (S, D, N) fp32, updated in place or into out_state; slots as in
     short_conv_step.  Returns out (B, D)."""
-    torch = _torch()
     if u.dim() != 2:
         raise ValueError(f"u must be (B, D), got shape {tuple(u.shape)}")
-    dtype, width, G, N, args = _scan_args(u, dt, A, B, C, D, z, dt_bias)
-    batch = u.shape[0]
-    _check_state(state, out_state, slots, batch, (width, N), torch.float32, u.device)
-    out = torch.empty((batch, width), dtype=u.dtype, device=u.device)
-    _check(load().gdn_ssm_step(*args, int(dt_softplus), _ptr(state), _ptr(state if out_state is None else out_state),
-                               _ptr(slots), _ptr(out), batch, state.shape[0], width, G, N, dtype, _stream(stream)),
-           "gdn_ssm_step")
+    dev, dims, args = _scan_args(u, dt, A, B, C, D, z, dt_bias, dt_softplus)
+    batch, width = u.shape
+    at, to, sl, S = _state(state, out_state, slots, batch, (width, dims[2]), torch.float32, dev)
+    _on_gpu(dev, u)
+    out = u.new_empty((batch, width))
+    _check(load().gdn_ssm_step(*args, at, to, sl, out.data_ptr(), batch, S, *dims, _current(stream, dev)), "gdn_ssm_step")
     return out
 
 
@@ -328,19 +333,22 @@ def ssm_scan_step(u, dt, A, B, C, state, D=None, z=None, dt_bias=None, dt_softpl
 # group norm with an activation
 # ----------------------------------------------------------------------------
 
-def _norm_args(x, weight, bias, gate, groups):
-    torch = _torch()
-    if x.dim() < 2:
-        raise ValueError(f"x must be (..., C) with at least one row dimension, got shape {tuple(x.shape)}")
-    dtype = _dtype(x, "x")
-    C = x.shape[-1]
-    if groups < 1 or C % groups:
+def _norm_args(x, weight, bias, gate, groups, activation):
+    act = _activation(activation, ("none", "silu", "sigmoid"))
+    shape = x.shape
+    if len(shape) < 2:
+        raise ValueError(f"x must be (..., C) with at least one row dimension, got shape {tuple(shape)}")
+    dtype, dev, C = _dtype(x, "x"), x.get_device(), shape[-1]
+    if groups < 1 or C < 1 or C % groups:
         raise ValueError(f"the {C} channels must divide into the {groups} groups")
-    _same("weight", weight, (C,), torch.float32, x.device)
-    _same("bias", bias, (C,), torch.float32, x.device)
-    _same("gate", gate, x.shape, x.dtype, x.device)
-    pg, sg = (None, 0) if gate is None else _rows(gate)
-    return dtype, x.numel() // C if C else 0, C, (*_rows(x), pg, sg, _ptr(weight), _ptr(bias))
+    w = _dense("weight", weight, (C,), torch.float32, dev)
+    b = _dense("bias", bias, (C,), torch.float32, dev)
+    pg, sg = None, 0
+    if gate is not None:
+        _is("gate", gate, shape, x.dtype, dev)
+        pg, sg = _rows(gate, C)
+    _on_gpu(dev, x)
+    return dev, act, dtype, x.numel() // C, C, (*_rows(x, C), pg, sg, w, b)
 
 
 def group_norm_fwd(x, weight=None, bias=None, gate=None, groups=1, eps=1e-6, activation="silu", center=False,
@@ -349,11 +357,10 @@ def group_norm_fwd(x, weight=None, bias=None, gate=None, groups=1, eps=1e-6, act
     x, gate (..., C), weight, bias (C).  center=False is the RMS norm, True
     subtracts the mean.  With a gate: norm(x) act(gate), or norm(x act(gate))
     with gate_first; without one: act(norm(x)).  Returns y (..., C)."""
-    act = _activation(activation, ("none", "silu", "sigmoid"))
-    dtype, rows, C, args = _norm_args(x, weight, bias, gate, groups)
-    y = _torch().empty(x.shape, dtype=x.dtype, device=x.device)
-    _check(load().gdn_norm_fwd(*args, _ptr(y), rows, C, groups, float(eps), act, int(center), int(gate_first), dtype,
-                               _stream(stream)), "gdn_norm_fwd")
+    dev, act, dtype, rows, C, args = _norm_args(x, weight, bias, gate, groups, activation)
+    y = x.new_empty(x.shape)
+    _check(load().gdn_norm_fwd(*args, y.data_ptr(), rows, C, groups, eps, act, int(center), int(gate_first), dtype,
+                            _current(stream, dev)), "gdn_norm_fwd")
     return y
 
 
@@ -361,26 +368,23 @@ def group_norm_bwd(x, d_out, weight=None, bias=None, gate=None, groups=1, eps=1e
                    gate_first=False, stream=None):
     """Gradients of group_norm_fwd: a dict of dx, and dweight, dbias and dgate
     for those that were given."""
-    torch = _torch()
-    act = _activation(activation, ("none", "silu", "sigmoid"))
-    dtype, rows, C, args = _norm_args(x, weight, bias, gate, groups)
-    _same("d_out", d_out, x.shape, x.dtype, x.device)
-    dev = x.device
-    res = {"dx": torch.empty(x.shape, dtype=x.dtype, device=dev)}
+    dev, act, dtype, rows, C, args = _norm_args(x, weight, bias, gate, groups, activation)
+    d_out = _dense("d_out", d_out, x.shape, x.dtype, dev)
+    res = {"dx": x.new_empty(x.shape)}
     if gate is not None:
-        res["dgate"] = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        res["dgate"] = x.new_empty(x.shape)
     if weight is not None:
-        res["dweight"] = torch.empty((C,), dtype=torch.float32, device=dev)
+        res["dweight"] = weight.new_empty((C,))
     if bias is not None:
-        res["dbias"] = torch.empty((C,), dtype=torch.float32, device=dev)
+        res["dbias"] = bias.new_empty((C,))
     lib = load()
     nbytes = 0
     if weight is not None or bias is not None:
         nbytes = lib.gdn_norm_bwd_workspace_size(rows, C, groups, dtype)
-    ws = _workspace(nbytes, dev)
-    _check(lib.gdn_norm_bwd(*args, _ptr(d_out), _ptr(res["dx"]), _ptr(res.get("dgate")), _ptr(res.get("dweight")),
-                            _ptr(res.get("dbias")), rows, C, groups, float(eps), act, int(center), int(gate_first),
-                            dtype, _ptr(ws), nbytes, _stream(stream)), "gdn_norm_bwd")
+    ws = _workspace(nbytes, x.device)
+    _check(lib.gdn_norm_bwd(*args, d_out, res["dx"].data_ptr(), _out(res, "dgate"), _out(res, "dweight"),
+                            _out(res, "dbias"), rows, C, groups, eps, act, int(center), int(gate_first), dtype,
+                            None if ws is None else ws.data_ptr(), nbytes, _current(stream, dev)), "gdn_norm_bwd")
     return res
 
 
@@ -394,7 +398,6 @@ _FUNCTIONS = {}
 def _functions():
     if _FUNCTIONS:
         return _FUNCTIONS
-    torch = _torch()
 
     def dense(g, like):
         return g.to(like.dtype).contiguous()
