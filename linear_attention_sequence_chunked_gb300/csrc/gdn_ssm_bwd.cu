@@ -99,7 +99,7 @@ __device__ __forceinline__ float channel_sum(Two v) {
     return lo;
 }
 
-template <typename T, int N, bool kFull, bool VEC>
+template <typename T, int N, bool kFull, int PB>
 __global__ void __launch_bounds__(32 * kWarps, 2) ssm_bwd_kernel(const SsmArgs p, int blocks) {
     using L = Lanes<N>;
     constexpr int CH = L::CH, LPC = L::LPC, GR = L::GR;
@@ -160,13 +160,13 @@ __global__ void __launch_bounds__(32 * kWarps, 2) ssm_bwd_kernel(const SsmArgs p
         if (it >= 0) {
             BwdStage<T, N, kFull>& st = sm.stage[it & 1];
             const int t = it * kTile, nt = len - t;
-            fill_tile<T, CH, VEC>(&st.dt[0][0], dt + t * p.dt_stride, p.dt_stride, nt, w.nd, lane);
-            if (z) fill_tile<T, CH, VEC>(&st.z[0][0], z + t * p.z_stride, p.z_stride, nt, w.nd, lane);
-            fill_tile<T, CH, VEC>(&st.d_out[0][0], d_out + t * static_cast<long long>(p.D), p.D, nt, w.nd, lane);
-            fill_tile<T, N, VEC>(&st.C[0][0], Cm + t * p.C_stride, p.C_stride, nt, N, lane);
+            fill_tile<T, CH, PB>(&st.dt[0][0], dt + t * p.dt_stride, p.dt_stride, nt, w.nd, lane);
+            if (z) fill_tile<T, CH, PB>(&st.z[0][0], z + t * p.z_stride, p.z_stride, nt, w.nd, lane);
+            fill_tile<T, CH, PB>(&st.d_out[0][0], d_out + t * static_cast<long long>(p.D), p.D, nt, w.nd, lane);
+            fill_tile<T, N, PB>(&st.C[0][0], Cm + t * p.C_stride, p.C_stride, nt, N, lane);
             if constexpr (kFull) {
-                fill_tile<T, CH, VEC>(&st.u[0][0], u + t * p.u_stride, p.u_stride, nt, w.nd, lane);
-                fill_tile<T, N, VEC>(&st.B[0][0], Bm + t * p.B_stride, p.B_stride, nt, N, lane);
+                fill_tile<T, CH, PB>(&st.u[0][0], u + t * p.u_stride, p.u_stride, nt, w.nd, lane);
+                fill_tile<T, N, PB>(&st.B[0][0], Bm + t * p.B_stride, p.B_stride, nt, N, lane);
                 // the channels' states before the tile, 16 bytes at a time
                 const float* from = p.saved + ((w.chunk0 + it) * p.D + w.d0) * N;
 #pragma unroll
@@ -338,26 +338,26 @@ __global__ void __launch_bounds__(256) ssm_bc_kernel(const SsmBcArgs p) {
     out[(row * p.G + g) * p.N + (col < p.N ? col : col - p.N)] = from_f32<T>(s);
 }
 
-template <typename T, int N, bool VEC>
+template <typename T, int N, int PB>
 cudaError_t bwd_v(const SsmArgs& a, cudaStream_t stream) {
     const int blocks = ssm_group_blocks(a.D, a.G, N);
     const long long units = a.slots * blocks * a.G;
     if (a.carry) {
-        cudaError_t e = launch_warps(ssm_bwd_kernel<T, N, false, VEC>, units, sizeof(BwdShared<T, N, false>), a, blocks, stream);
+        cudaError_t e = launch_warps(ssm_bwd_kernel<T, N, false, PB>, units, sizeof(BwdShared<T, N, false>), a, blocks, stream);
         if (e == cudaSuccess) e = launch_ssm_compose(a, true, stream);
         if (e != cudaSuccess) return e;
     }
-    return launch_warps(ssm_bwd_kernel<T, N, true, VEC>, units, sizeof(BwdShared<T, N, true>), a, blocks, stream);
+    return launch_warps(ssm_bwd_kernel<T, N, true, PB>, units, sizeof(BwdShared<T, N, true>), a, blocks, stream);
 }
 
 template <typename T, int N>
 cudaError_t bwd_n(const SsmArgs& a, cudaStream_t stream) {
-    constexpr int CH = Lanes<N>::CH;
-    // d_out, du, ddt and dz are dense rows of D
-    const bool vec = a.D / a.G * sizeof(T) % piece_bytes<T, CH> == 0 && takes_pieces<T, CH>(a.u, a.u_stride) &&
-                     takes_pieces<T, CH>(a.dt, a.dt_stride) && (!a.z || takes_pieces<T, CH>(a.z, a.z_stride)) &&
-                     takes_pieces<T, N>(a.Bm, a.B_stride) && takes_pieces<T, N>(a.Cm, a.C_stride);
-    return vec ? bwd_v<T, N, true>(a, stream) : bwd_v<T, N, false>(a, stream);
+    switch (scan_pieces<T, N>(a)) {
+        case 16: return bwd_v<T, N, 16>(a, stream);
+        case 4: return bwd_v<T, N, 4>(a, stream);
+    }
+    if constexpr (sizeof(T) == 2) return bwd_v<T, N, 0>(a, stream);
+    return cudaErrorMisalignedAddress;  // fp32 is 4-byte aligned
 }
 
 }  // namespace

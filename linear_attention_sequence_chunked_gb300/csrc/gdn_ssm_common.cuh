@@ -79,20 +79,20 @@ struct Lanes {
 };
 
 // Copies rows [0, nt) and columns [0, nc) of a kTile x ROW tile to shared
-// memory, zeros elsewhere.  VEC: asynchronously, in pieces of up to 16 bytes
-// (every row's pieces aligned, nc a multiple of a piece); otherwise element by
-// element and at once.
-template <typename T, int ROW, bool VEC>
+// memory, zeros elsewhere, asynchronously in pieces of up to PB bytes (every
+// row's pieces aligned, nc a multiple of a piece).  PB = 0: element by element
+// and at once, for 2-byte elements at odd places.
+template <typename T, int ROW, int PB>
 __device__ __forceinline__ void fill_tile(T* dst, const T* src, long long stride, int nt, int nc, int lane) {
     constexpr int row_bytes = ROW * static_cast<int>(sizeof(T));
-    constexpr int CB = row_bytes < 16 ? row_bytes : 16, CE = VEC ? CB / static_cast<int>(sizeof(T)) : 1;
+    constexpr int CB = row_bytes < PB ? row_bytes : PB, CE = PB ? CB / static_cast<int>(sizeof(T)) : 1;
     constexpr int PER = ROW / CE, TOTAL = kTile * PER;
 #pragma unroll
     for (int i = 0; i < (TOTAL + 31) / 32; ++i) {
         const int id = i * 32 + lane, row = id / PER, c = id % PER * CE;
         if (TOTAL % 32 != 0 && id >= TOTAL) continue;
         const bool ok = row < nt && c < nc;
-        if constexpr (VEC) {
+        if constexpr (PB != 0) {
             const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(dst + id * CE));
             const T* from = ok ? src + row * stride + c : src;
             const int bytes = ok ? CB : 0;
@@ -105,14 +105,26 @@ __device__ __forceinline__ void fill_tile(T* dst, const T* src, long long stride
         }
     }
 }
+// Whether fill_tile can take pieces of up to `piece` bytes of ROW elements from
+// rows at p.
 template <typename T, int ROW>
-constexpr int piece_bytes = ROW * static_cast<int>(sizeof(T)) < 16 ? ROW * static_cast<int>(sizeof(T)) : 16;
-
-// Whether fill_tile can take its pieces of ROW elements from rows at p.
-template <typename T, int ROW>
-bool takes_pieces(const void* p, long long stride) {
-    constexpr int b = piece_bytes<T, ROW>;
+bool takes_pieces(const void* p, long long stride, int piece) {
+    const int b = ROW * static_cast<int>(sizeof(T)) < piece ? ROW * static_cast<int>(sizeof(T)) : piece;
     return reinterpret_cast<uintptr_t>(p) % b == 0 && stride * static_cast<long long>(sizeof(T)) % b == 0;
+}
+// The widest pieces that every activation of a scan takes: 16 bytes, 4, or
+// (bf16 at odd places) none.
+template <typename T, int N>
+int scan_pieces(const SsmArgs& a) {
+    constexpr int CH = Lanes<N>::CH;
+    for (const int b : {16, 4}) {
+        const int w = CH * static_cast<int>(sizeof(T)) < b ? CH * static_cast<int>(sizeof(T)) : b;
+        if (a.D / a.G * static_cast<long long>(sizeof(T)) % w == 0 && takes_pieces<T, CH>(a.u, a.u_stride, b) &&
+            takes_pieces<T, CH>(a.dt, a.dt_stride, b) && (!a.z || takes_pieces<T, CH>(a.z, a.z_stride, b)) &&
+            takes_pieces<T, N>(a.Bm, a.B_stride, b) && takes_pieces<T, N>(a.Cm, a.C_stride, b))
+            return b;
+    }
+    return 0;
 }
 
 __device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
