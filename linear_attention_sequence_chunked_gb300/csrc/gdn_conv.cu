@@ -17,6 +17,8 @@
 // consecutive tokens with the window in registers, so every input is read once
 // but for W-1 rows per block; the next tokens' loads are in flight while these
 // are computed, and the arithmetic runs on pairs of channels.
+#include <type_traits>
+
 #include "gdn_kernels.h"
 #include "gdn_mix_common.cuh"
 
@@ -129,10 +131,10 @@ __global__ void __launch_bounds__(kThreads) conv_fwd_kernel(const ConvArgs p) {
 // time block (and the W-1 tokens after it, whose dp reach back into it), then
 // the block's partial weight gradients are summed over its rows in order.
 constexpr int kLanes = 32;
-constexpr int kRows = kThreads / kLanes;
+constexpr int kRows = 4;
 
 template <typename T, int W, int E>
-__global__ void __launch_bounds__(kThreads) conv_bwd_kernel(const ConvArgs p) {
+__global__ void __launch_bounds__(kLanes * kRows, 4) conv_bwd_kernel(const ConvArgs p) {
     constexpr int U = 4, P = (E + 1) / 2;
     __shared__ float red[kRows][kLanes][E + 1];
     if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(p.cu_seqlens, p.N, p.T, p.err);
@@ -181,8 +183,10 @@ __global__ void __launch_bounds__(kThreads) conv_bwd_kernel(const ConvArgs p) {
                 x += U * p.x_stride;
                 dy += U * static_cast<long long>(p.D);
             };
-            load(tb);
-            for (int t = tb; t < te + W - 1; t += U) {
+            // U tokens from t.  kInner: all of them and the inputs whose gradients
+            // they complete lie inside the block, away from the sequence's ends.
+            auto step = [&](int t, auto inner) {
+                constexpr bool kInner = decltype(inner)::value;
                 Two g[U][P];
 #pragma unroll
                 for (int k = 0; k < U; ++k) {
@@ -203,16 +207,16 @@ __global__ void __launch_bounds__(kThreads) conv_bwd_kernel(const ConvArgs p) {
                             // silu' = s (1 + p (1 - s))
                             d = mul2(d, mul2(s, fma2(acc, fma2(s, neg, one), one)));
                         }
-                        if (t + k >= t1) d = zero;
+                        if (!kInner && t + k >= t1) d = zero;
                         dp[W - 1 + k][i] = d;
-                        if (t + k >= te) d = zero;  // the next block's
+                        if (!kInner && t + k >= te) d = zero;  // the next block's
 #pragma unroll
                         for (int j = 0; j < W; ++j) dw[j][i] = fma2(d, win[k + j][i], dw[j][i]);
                         dw[W][i] = add2(dw[W][i], d);
                     }
                     // input s has now seen every token it feeds
                     const int s = t + k - (W - 1);
-                    if (s < te && (s >= tb || ds0)) {
+                    if (kInner || (s < te && (s >= tb || ds0))) {
                         Two o[P];
 #pragma unroll
                         for (int i = 0; i < P; ++i) {
@@ -220,13 +224,16 @@ __global__ void __launch_bounds__(kThreads) conv_bwd_kernel(const ConvArgs p) {
 #pragma unroll
                             for (int j = 0; j < W; ++j) o[i] = fma2(w[j][i], dp[W - 1 + k - j][i], o[i]);
                         }
-                        if (dfs && s >= t1 - (W - 1)) {  // one of the rows the final state holds
-                            Two v[P];
-                            unpack_2<T, E>(load_raw<T, E>(dfs + (static_cast<long long>(n) * (W - 1) + s - t1 + (W - 1)) * p.D, E), v);
+                        T* to = dx + k * static_cast<long long>(p.D);
+                        if constexpr (!kInner) {
+                            if (dfs && s >= t1 - (W - 1)) {  // one of the rows the final state holds
+                                Two v[P];
+                                unpack_2<T, E>(load_raw<T, E>(dfs + (static_cast<long long>(n) * (W - 1) + s - t1 + (W - 1)) * p.D, E), v);
 #pragma unroll
-                            for (int i = 0; i < P; ++i) o[i] = add2(o[i], v[i]);
+                                for (int i = 0; i < P; ++i) o[i] = add2(o[i], v[i]);
+                            }
+                            if (s < tb) to = ds0 + (s - t0 + (W - 1)) * static_cast<long long>(p.D);
                         }
-                        T* to = s >= tb ? dx + k * static_cast<long long>(p.D) : ds0 + (s - t0 + (W - 1)) * static_cast<long long>(p.D);
                         store_raw<T, E>(to, pack_2<T, E>(o), E);
                     }
                 }
@@ -238,7 +245,12 @@ __global__ void __launch_bounds__(kThreads) conv_bwd_kernel(const ConvArgs p) {
                         win[j][i] = win[j + U][i];
                         dp[j][i] = dp[j + U][i];
                     }
-            }
+            };
+            load(tb);
+            int t = tb;
+            step(t, std::false_type{});
+            for (t += U; t + U <= te; t += U) step(t, std::true_type{});
+            for (; t < te + W - 1; t += U) step(t, std::false_type{});
         }
     }
     // partial [block row][W + 1][D]: the weights' gradients, then the bias's
@@ -252,7 +264,7 @@ __global__ void __launch_bounds__(kThreads) conv_bwd_kernel(const ConvArgs p) {
             if (2 * i + 1 < E) red[row][lane][2 * i + 1] = hi;
         }
         __syncthreads();
-        for (int i = threadIdx.x; i < kLanes * E; i += kThreads) {
+        for (int i = threadIdx.x; i < kLanes * E; i += kLanes * kRows) {
             const long long d = static_cast<long long>(blockIdx.y) * kLanes * E + i;
             float s = 0.f;
 #pragma unroll
@@ -376,7 +388,7 @@ template <typename T, int W, int E>
 cudaError_t conv_bwd_e(const ConvArgs& a, cudaStream_t stream) {
     dim3 grid(static_cast<unsigned>((a.slots + kRows - 1) / kRows),
               static_cast<unsigned>((a.D + kLanes * E - 1) / (kLanes * E)));
-    conv_bwd_kernel<T, W, E><<<grid, kThreads, 0, stream>>>(a);
+    conv_bwd_kernel<T, W, E><<<grid, kLanes * kRows, 0, stream>>>(a);
     return cudaGetLastError();
 }
 template <typename T, int W>

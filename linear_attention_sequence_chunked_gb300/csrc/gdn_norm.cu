@@ -17,6 +17,7 @@
 // walks rows, the next row's loads under way, so the weight gradients
 // accumulate in its registers and leave as one partial row per team, summed
 // afterwards in a fixed order.  Arithmetic runs on pairs of channels.
+#include "gdn.h"
 #include "gdn_kernels.h"
 #include "gdn_mix_common.cuh"
 
@@ -26,16 +27,43 @@ namespace {
 
 using namespace mix;
 
-__device__ __forceinline__ Two act_2(Two x, int kind) {
-    return kind == 0 ? x : kind == 1 ? mul2(x, sigmoid_2(x)) : sigmoid_2(x);
+// act(x) of H pairs in place, and act'(x) into d: the kind is asked for once.
+template <int H>
+__device__ __forceinline__ void activate(Two (&x)[H], int kind) {
+    if (kind == GDN_ACT_SILU) {
+#pragma unroll
+        for (int h = 0; h < H; ++h) x[h] = mul2(x[h], sigmoid_2(x[h]));
+    } else if (kind == GDN_ACT_SIGMOID) {
+#pragma unroll
+        for (int h = 0; h < H; ++h) x[h] = sigmoid_2(x[h]);
+    }
 }
-// act'(x)
-__device__ __forceinline__ Two dact_2(Two x, int kind) {
-    const Two one = two(1.f, 1.f);
-    if (kind == 0) return one;
-    const Two s = sigmoid_2(x), r = fma2(s, two(-1.f, -1.f), one);  // r = 1 - s
-    return mul2(s, kind == 1 ? fma2(x, r, one) : r);
+template <int H>
+__device__ __forceinline__ void activate(Two (&x)[H], Two (&d)[H], int kind) {
+    const Two one = two(1.f, 1.f), neg = two(-1.f, -1.f);
+    if (kind == GDN_ACT_NONE) {
+#pragma unroll
+        for (int h = 0; h < H; ++h) d[h] = one;
+    } else if (kind == GDN_ACT_SILU) {
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+            const Two s = sigmoid_2(x[h]), y = mul2(x[h], s);
+            d[h] = fma2(y, fma2(s, neg, one), s);  // s + x s (1 - s)
+            x[h] = y;
+        }
+    } else {
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+            const Two s = sigmoid_2(x[h]);
+            d[h] = mul2(s, fma2(s, neg, one));
+            x[h] = s;
+        }
+    }
 }
+
+// Where the activation stands: on the result, on a gate after the norm, on a
+// gate before it.
+enum Mode { kPlain, kAfter, kFirst };
 
 // A team: 16 or 32 lanes of a warp, or a whole block of 64 or more.  Its row of
 // a group is V vectors of E elements per lane, vector i at lane + i LANES, held
@@ -118,14 +146,29 @@ struct Team {
             }
         }
     }
+    __device__ __forceinline__ float sum(Two a) const {
+        float lo, hi;
+        split(a, lo, hi);
+        lo += hi;
+        constexpr int M = LANES < 32 ? LANES : 32;
+#pragma unroll
+        for (int m = M / 2; m > 0; m /= 2) lo += __shfl_xor_sync(0xffffffffu, lo, m);
+        if constexpr (LANES > 32) {
+            __syncthreads();  // the previous sums have been read
+            if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = lo;
+            __syncthreads();
+            lo = red[0];
+#pragma unroll
+            for (int i = 1; i < LANES / 32; ++i) lo += red[i];
+        }
+        return lo;
+    }
     // x' -> x' - mean (where centered)
     __device__ __forceinline__ void center(Two (&x)[H], float inv) const {
         Two a = two(0.f, 0.f);
 #pragma unroll
         for (int h = 0; h < H; ++h) a = add2(a, x[h]);
-        float m, unused;
-        sums(a, a, m, unused);
-        m *= -inv;
+        const float m = -sum(a) * inv;
 #pragma unroll
         for (int h = 0; h < H; ++h) x[h] = add2(x[h], two(m, m));
         clip(x);
@@ -133,7 +176,7 @@ struct Team {
 };
 
 // A team takes R rows of one group.
-template <typename T, int E, int LANES, int V, int R>
+template <typename T, int E, int LANES, int V, int R, int M>
 __global__ void __launch_bounds__(Team<T, E, LANES, V>::kBlock) norm_fwd_kernel(const NormArgs p) {
     using Tm = Team<T, E, LANES, V>;
     constexpr int H = Tm::H;
@@ -149,46 +192,48 @@ __global__ void __launch_bounds__(Team<T, E, LANES, V>::kBlock) norm_fwd_kernel(
         const bool live = row0 + r < p.rows;
         const long long row = live ? row0 + r : 0;
         tm.load(static_cast<const T*>(p.x) + row * p.x_stride + c0, live, xr[r]);
-        if (p.gate) tm.load(static_cast<const T*>(p.gate) + row * p.gate_stride + c0, live, gr[r]);
+        if (M != kPlain) tm.load(static_cast<const T*>(p.gate) + row * p.gate_stride + c0, live, gr[r]);
     }
-    Two w[H], b[H];
+    Two w[H];
     tm.param(p.weight ? p.weight + c0 : nullptr, 1.f, w);
-    tm.param(p.bias ? p.bias + c0 : nullptr, 0.f, b);
     const float inv = 1.f / size;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         Two x[H], g[H];
         tm.pairs(xr[r], x);
-        if (p.gate) {
+        if (M != kPlain) {
             tm.pairs(gr[r], g);
+            activate(g, p.activation);
+        }
+        if (M == kFirst) {
 #pragma unroll
-            for (int h = 0; h < H; ++h) {
-                g[h] = act_2(g[h], p.activation);
-                if (p.gate_first) x[h] = mul2(x[h], g[h]);
-            }
+            for (int h = 0; h < H; ++h) x[h] = mul2(x[h], g[h]);
         }
         if (p.center) tm.center(x, inv);
         Two a = two(0.f, 0.f);
 #pragma unroll
         for (int h = 0; h < H; ++h) a = fma2(x[h], x[h], a);
-        float ss, unused;
-        tm.sums(a, a, ss, unused);
-        const float rs = 1.f / sqrtf(fmaf(ss, inv, p.eps));
+        const float rs = 1.f / sqrtf(fmaf(tm.sum(a), inv, p.eps));
         const Two r2 = two(rs, rs);
 #pragma unroll
-        for (int h = 0; h < H; ++h) {
-            x[h] = fma2(mul2(x[h], r2), w[h], b[h]);
-            if (!p.gate)
-                x[h] = act_2(x[h], p.activation);
-            else if (!p.gate_first)
-                x[h] = mul2(x[h], g[h]);
+        for (int h = 0; h < H; ++h) x[h] = mul2(mul2(x[h], r2), w[h]);
+        if (p.bias) {
+            Two b[H];
+            tm.param(p.bias + c0, 0.f, b);
+#pragma unroll
+            for (int h = 0; h < H; ++h) x[h] = add2(x[h], b[h]);
+        }
+        if (M == kPlain) activate(x, p.activation);
+        if (M == kAfter) {
+#pragma unroll
+            for (int h = 0; h < H; ++h) x[h] = mul2(x[h], g[h]);
         }
         tm.store(static_cast<T*>(p.y) + (row0 + r) * p.C + c0, row0 + r < p.rows, x);
     }
 }
 
 // Team `unit` keeps group unit % groups and takes rows unit / groups, + teams, ...
-template <typename T, int E, int LANES, int V>
+template <typename T, int E, int LANES, int V, int M>
 __global__ void __launch_bounds__(Team<T, E, LANES, V>::kBlock) norm_bwd_kernel(const NormArgs p, int teams) {
     using Tm = Team<T, E, LANES, V>;
     constexpr int H = Tm::H;
@@ -211,68 +256,62 @@ __global__ void __launch_bounds__(Team<T, E, LANES, V>::kBlock) norm_bwd_kernel(
         if (!on) row = 0;
         tm.load(static_cast<const T*>(p.x) + row * p.x_stride + c0, on, xr);
         tm.load(static_cast<const T*>(p.d_out) + row * p.C + c0, on, dr);
-        if (p.gate) tm.load(static_cast<const T*>(p.gate) + row * p.gate_stride + c0, on, gr);
+        if (M != kPlain) tm.load(static_cast<const T*>(p.gate) + row * p.gate_stride + c0, on, gr);
     };
     load(team);
-    const bool first = p.gate && p.gate_first;
     const long long steps = (p.rows + teams - 1) / teams;
     for (long long s = 0; s < steps; ++s) {
         const long long row = team + s * teams;
         const bool on = live && row < p.rows;  // a row that is not there is all zeros
-        Two x[H], g[H], dy[H], n[H];
+        Two x[H], ga[H], gd[H], dy[H], n[H];
         tm.pairs(xr, x);
         tm.pairs(dr, dy);
-        if (p.gate) tm.pairs(gr, g);
+        if (M != kPlain) tm.pairs(gr, ga);
         load(row + teams);
+        if (M != kPlain) activate(ga, gd, p.activation);
 #pragma unroll
-        for (int h = 0; h < H; ++h) n[h] = first ? mul2(x[h], act_2(g[h], p.activation)) : x[h];
+        for (int h = 0; h < H; ++h) n[h] = M == kFirst ? mul2(x[h], ga[h]) : x[h];
         if (p.center) tm.center(n, inv);
         // With a gate dv does not need the norm, and one exchange gives both sums.
-        const bool early = p.gate;
         Two a = zero, c = zero;
 #pragma unroll
         for (int h = 0; h < H; ++h) {
             a = fma2(n[h], n[h], a);
-            if (early) {
-                if (!first) {
-                    // its own gradient wants v = n w + b: kept as dy act'(g), finished below
-                    const Two d = dy[h];
-                    dy[h] = mul2(d, act_2(g[h], p.activation));
-                    g[h] = mul2(d, dact_2(g[h], p.activation));
-                }
-                c = fma2(mul2(dy[h], w[h]), n[h], c);
+            if (M == kAfter) {  // the gate's own gradient is dy act'(gate) v: v below
+                gd[h] = mul2(dy[h], gd[h]);
+                dy[h] = mul2(dy[h], ga[h]);
             }
+            if (M != kPlain) c = fma2(mul2(dy[h], w[h]), n[h], c);
         }
         float ss, sn;
         tm.sums(a, c, ss, sn);
         const float rs = on ? 1.f / sqrtf(fmaf(ss, inv, p.eps)) : 0.f;
         const Two r2 = two(rs, rs);
         sn *= rs * inv;
-        if (!early || p.bias) {
-            Two b[H];
-            tm.param(p.bias ? p.bias + c0 : nullptr, 0.f, b);
-            c = zero;
 #pragma unroll
-            for (int h = 0; h < H; ++h) {
-                n[h] = mul2(n[h], r2);
-                const Two v = fma2(n[h], w[h], b[h]);
-                if (!early) {
-                    dy[h] = mul2(dy[h], dact_2(v, p.activation));
+        for (int h = 0; h < H; ++h) n[h] = mul2(n[h], r2);
+        if (M != kFirst) {
+            Two v[H];
+#pragma unroll
+            for (int h = 0; h < H; ++h) v[h] = mul2(n[h], w[h]);
+            if (p.bias) {
+                Two b[H];
+                tm.param(p.bias + c0, 0.f, b);
+#pragma unroll
+                for (int h = 0; h < H; ++h) v[h] = add2(v[h], b[h]);
+            }
+            if (M == kAfter) {
+#pragma unroll
+                for (int h = 0; h < H; ++h) gd[h] = mul2(gd[h], v[h]);
+            } else {
+                activate(v, gd, p.activation);
+                c = zero;
+#pragma unroll
+                for (int h = 0; h < H; ++h) {
+                    dy[h] = mul2(dy[h], gd[h]);
                     c = fma2(mul2(dy[h], w[h]), n[h], c);
-                } else if (!first) {
-                    g[h] = mul2(g[h], v);
                 }
-            }
-            if (!early) {
-                float unused;
-                tm.sums(c, c, sn, unused);
-                sn *= inv;
-            }
-        } else {
-#pragma unroll
-            for (int h = 0; h < H; ++h) {
-                n[h] = mul2(n[h], r2);
-                if (!first) g[h] = mul2(g[h], mul2(n[h], w[h]));
+                sn = tm.sum(c) * inv;
             }
         }
         Two m1 = zero;
@@ -280,27 +319,24 @@ __global__ void __launch_bounds__(Team<T, E, LANES, V>::kBlock) norm_bwd_kernel(
             c = zero;
 #pragma unroll
             for (int h = 0; h < H; ++h) c = fma2(dy[h], w[h], c);
-            float s1, unused;
-            tm.sums(c, c, s1, unused);
-            m1 = two(-s1 * inv, -s1 * inv);
+            const float s1 = -tm.sum(c) * inv;
+            m1 = two(s1, s1);
         }
         const Two sn2 = two(-sn, -sn);
 #pragma unroll
         for (int h = 0; h < H; ++h) {
             dw[h] = fma2(dy[h], n[h], dw[h]);
             db[h] = add2(db[h], dy[h]);
-            const Two d = mul2(r2, add2(fma2(dy[h], w[h], m1), mul2(n[h], sn2)));
-            if (first) {
-                const Two gd = dact_2(g[h], p.activation);
-                const Two ga = act_2(g[h], p.activation);
-                g[h] = mul2(mul2(d, x[h]), gd);
-                x[h] = mul2(d, ga);
+            const Two d = mul2(r2, fma2(n[h], sn2, fma2(dy[h], w[h], m1)));
+            if (M == kFirst) {
+                gd[h] = mul2(mul2(d, x[h]), gd[h]);
+                x[h] = mul2(d, ga[h]);
             } else {
                 x[h] = d;
             }
         }
         tm.store(static_cast<T*>(p.dx) + row * p.C + c0, on, x);
-        if (p.gate) tm.store(static_cast<T*>(p.dgate) + row * p.C + c0, on, g);
+        if (M != kPlain) tm.store(static_cast<T*>(p.dgate) + row * p.C + c0, on, gd);
     }
     if (!p.partial || !live) return;
     float* pw = p.partial + static_cast<long long>(team) * (p.bias ? 2 : 1) * p.C + c0;
@@ -326,7 +362,13 @@ template <typename T, int E, int LANES, int V, int R>
 cudaError_t norm_fwd_r(const NormArgs& a, cudaStream_t stream) {
     using Tm = Team<T, E, LANES, V>;
     const long long units = (a.rows + R - 1) / R * a.groups;
-    norm_fwd_kernel<T, E, LANES, V, R><<<static_cast<unsigned>((units + Tm::kTeams - 1) / Tm::kTeams), Tm::kBlock, 0, stream>>>(a);
+    const unsigned grid = static_cast<unsigned>((units + Tm::kTeams - 1) / Tm::kTeams);
+    if (!a.gate)
+        norm_fwd_kernel<T, E, LANES, V, R, kPlain><<<grid, Tm::kBlock, 0, stream>>>(a);
+    else if (a.gate_first)
+        norm_fwd_kernel<T, E, LANES, V, R, kFirst><<<grid, Tm::kBlock, 0, stream>>>(a);
+    else
+        norm_fwd_kernel<T, E, LANES, V, R, kAfter><<<grid, Tm::kBlock, 0, stream>>>(a);
     return cudaGetLastError();
 }
 // Several rows per team once one row each gives the GPU more teams than it
@@ -342,7 +384,13 @@ cudaError_t norm_bwd_v(const NormArgs& a, cudaStream_t stream) {
     using Tm = Team<T, E, LANES, V>;
     const int teams = norm_partial_rows(a.rows, a.C, a.groups, a.dtype);
     const long long units = static_cast<long long>(teams) * a.groups;
-    norm_bwd_kernel<T, E, LANES, V><<<static_cast<unsigned>((units + Tm::kTeams - 1) / Tm::kTeams), Tm::kBlock, 0, stream>>>(a, teams);
+    const unsigned grid = static_cast<unsigned>((units + Tm::kTeams - 1) / Tm::kTeams);
+    if (!a.gate)
+        norm_bwd_kernel<T, E, LANES, V, kPlain><<<grid, Tm::kBlock, 0, stream>>>(a, teams);
+    else if (a.gate_first)
+        norm_bwd_kernel<T, E, LANES, V, kFirst><<<grid, Tm::kBlock, 0, stream>>>(a, teams);
+    else
+        norm_bwd_kernel<T, E, LANES, V, kAfter><<<grid, Tm::kBlock, 0, stream>>>(a, teams);
     return cudaGetLastError();
 }
 
@@ -387,12 +435,13 @@ cudaError_t norm_bwd_t(const NormArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-// Teams per group in the reverse mode, one partial row each: about 512 threads
-// per SM, few enough that the partial rows cost little beside the inputs.
+// Teams per group in the reverse mode, one partial row each: one wave of 384
+// threads per SM (170 registers each), few enough that the partial rows cost
+// little beside the inputs.
 int norm_partial_rows(long long rows, int C, int groups, int dtype) {
     const int vectors = C / groups / (dtype == 0 ? 8 : 4);
     const int lanes = vectors <= 16 ? 16 : vectors <= 64 ? 32 : vectors <= 256 ? 128 : vectors <= 512 ? 256 : 512;
-    long long teams = 152LL * 512 / lanes / groups;
+    long long teams = 152LL * 384 / lanes / groups;
     if (teams < 1) teams = 1;
     return static_cast<int>(rows < teams ? rows : teams);
 }
