@@ -70,7 +70,7 @@ enum Mode { kPlain, kAfter, kFirst };
 // as H pairs of consecutive elements (of vectors 2 h and 2 h + 1 for E = 1).
 template <typename T, int E, int LANES, int V>
 struct Team {
-    static constexpr int kBlock = LANES < 64 ? 256 : LANES;
+    static constexpr int kBlock = LANES < 64 ? 128 : LANES;
     static constexpr int kTeams = kBlock / LANES;  // per block
     static constexpr int H = V * E / 2;
     int lane, nv;
@@ -232,9 +232,15 @@ __global__ void __launch_bounds__(Team<T, E, LANES, V>::kBlock) norm_fwd_kernel(
     }
 }
 
+// Threads per SM in the reverse mode: eight channels per lane keep to the 128
+// registers of 512 threads, sixteen want 168 (16384 x 2048 in one group: 66 us
+// with 384 threads, 111 us with 512).
+template <int E, int LANES, int V>
+constexpr int kBwdThreads = V * E > 8 && LANES <= 128 ? 384 : 512;
+
 // Team `unit` keeps group unit % groups and takes rows unit / groups, + teams, ...
 template <typename T, int E, int LANES, int V, int M>
-__global__ void __launch_bounds__(Team<T, E, LANES, V>::kBlock) norm_bwd_kernel(const NormArgs p, int teams) {
+__global__ void __launch_bounds__(Team<T, E, LANES, V>::kBlock, kBwdThreads<E, LANES, V> / Team<T, E, LANES, V>::kBlock) norm_bwd_kernel(const NormArgs p, int teams) {
     using Tm = Team<T, E, LANES, V>;
     constexpr int H = Tm::H;
     __shared__ float red[LANES > 32 ? 2 * LANES / 32 : 1];
@@ -394,54 +400,68 @@ cudaError_t norm_bwd_v(const NormArgs& a, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
-template <typename T>
-bool wide_rows(const NormArgs& a) {
-    constexpr int E = 16 / sizeof(T);
-    auto ok = [](const void* p, long long stride) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride % E == 0; };
+// Whether rows can be accessed E elements at a time.
+template <typename T, int E>
+bool rows_take(const NormArgs& a) {
+    auto ok = [](const void* p, long long stride) { return reinterpret_cast<uintptr_t>(p) % (E * sizeof(T)) == 0 && stride % E == 0; };
     return (a.C / a.groups) % E == 0 && ok(a.x, a.x_stride) && (!a.gate || ok(a.gate, a.gate_stride));
 }
 
 // Lanes and registers per group: a half warp or a warp where the group fits
 // its registers, else a block.  Rows that 16-byte accesses cannot take (odd
-// sizes, strides or addresses) go element by element, neighbouring lanes on
-// neighbouring elements.
-#define GDN_NORM_SIZES(fn, T)                                       \
-    const int size = a.C / a.groups;                                \
-    constexpr int E = 16 / sizeof(T);                               \
-    if (wide_rows<T>(a)) {                                          \
-        const int nv = size / E;                                    \
-        if (nv <= 16) return fn<T, E, 16, 1>(a, stream);            \
-        if (nv <= 32) return fn<T, E, 32, 1>(a, stream);            \
-        if (nv <= 64) return fn<T, E, 32, 2>(a, stream);            \
-        if (nv <= 128) return fn<T, E, 128, 1>(a, stream);          \
-        if (nv <= 256) return fn<T, E, 128, 2>(a, stream);          \
-        if (nv <= 512) return fn<T, E, 256, 2>(a, stream);          \
-        if (nv <= 1024) return fn<T, E, 512, 2>(a, stream);         \
+// sizes, strides or addresses) go 4 bytes or one element at a time,
+// neighbouring lanes on neighbouring elements.  8192 x 4096 bf16 takes 40 us
+// with 256 lanes forward (512: 65 us), 74 us with 512 lanes in reverse (256: 77
+// to 115 us): L512 and V512.
+#define GDN_NORM_SIZES(fn, T, L512, V512)                               \
+    const int size = a.C / a.groups;                                    \
+    constexpr int E = 16 / sizeof(T);                                   \
+    if (rows_take<T, E>(a)) {                                           \
+        const int nv = size / E;                                        \
+        if (nv <= 16) return fn<T, E, 16, 1>(a, stream);                \
+        if (nv <= 32) return fn<T, E, 32, 1>(a, stream);                \
+        if (nv <= 64) return fn<T, E, 32, 2>(a, stream);                \
+        if (nv <= 128) return fn<T, E, 128, 1>(a, stream);              \
+        if (nv <= 256) return fn<T, E, 128, 2>(a, stream);              \
+        if (nv <= 512) return fn<T, E, L512, V512>(a, stream);          \
+        if (nv <= 1024) return fn<T, E, 512, 2>(a, stream);             \
         if constexpr (sizeof(T) == 4) return fn<T, E, 512, 4>(a, stream); \
-    }                                                               \
-    if (size <= 128) return fn<T, 1, 32, 4>(a, stream);             \
-    if (size <= 512) return fn<T, 1, 32, 16>(a, stream);            \
-    if (size <= 2048) return fn<T, 1, 128, 16>(a, stream);          \
+    }                                                                   \
+    if constexpr (sizeof(T) == 2) {                                     \
+        if (rows_take<T, 2>(a)) {                                       \
+            const int nv = size / 2;                                    \
+            if (nv <= 128) return fn<T, 2, 32, 4>(a, stream);           \
+            if (nv <= 256) return fn<T, 2, 32, 8>(a, stream);           \
+            if (nv <= 512) return fn<T, 2, 128, 4>(a, stream);          \
+            if (nv <= 2048) return fn<T, 2, 512, 4>(a, stream);         \
+            return fn<T, 2, 512, 8>(a, stream);                         \
+        }                                                               \
+    }                                                                   \
+    if (size <= 128) return fn<T, 1, 32, 4>(a, stream);                 \
+    if (size <= 512) return fn<T, 1, 128, 4>(a, stream);                \
+    if (size <= 1024) return fn<T, 1, 128, 8>(a, stream);               \
+    if (size <= 4096) return fn<T, 1, 512, 8>(a, stream);               \
     return fn<T, 1, 512, 16>(a, stream)
 
 template <typename T>
 cudaError_t norm_fwd_t(const NormArgs& a, cudaStream_t stream) {
-    GDN_NORM_SIZES(norm_fwd_v, T);
+    GDN_NORM_SIZES(norm_fwd_v, T, 256, 2);
 }
 template <typename T>
 cudaError_t norm_bwd_t(const NormArgs& a, cudaStream_t stream) {
-    GDN_NORM_SIZES(norm_bwd_v, T);
+    GDN_NORM_SIZES(norm_bwd_v, T, 512, 1);
 }
 
 }  // namespace
 
-// Teams per group in the reverse mode, one partial row each: one wave of 384
-// threads per SM (170 registers each), few enough that the partial rows cost
+// Teams per group in the reverse mode, one partial row each: one wave of the
+// threads that an SM holds at a time, few enough that the partial rows cost
 // little beside the inputs.
 int norm_partial_rows(long long rows, int C, int groups, int dtype) {
-    const int vectors = C / groups / (dtype == 0 ? 8 : 4);
-    const int lanes = vectors <= 16 ? 16 : vectors <= 64 ? 32 : vectors <= 256 ? 128 : vectors <= 512 ? 256 : 512;
-    long long teams = 152LL * 384 / lanes / groups;
+    const int nv = C / groups / (dtype == 0 ? 8 : 4);
+    const int lanes = nv <= 16 ? 16 : nv <= 64 ? 32 : nv <= 256 ? 128 : 512;
+    const bool wide = dtype == 0 && ((nv > 32 && nv <= 64) || (nv > 128 && nv <= 256));  // sixteen channels per lane
+    long long teams = 152LL * (wide ? 384 : 512) / lanes / groups;
     if (teams < 1) teams = 1;
     return static_cast<int>(rows < teams ? rows : teams);
 }

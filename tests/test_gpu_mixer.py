@@ -356,7 +356,7 @@ NORM = [  # rows, C, groups, strided
     (1, 1, 1, False), (0, 64, 1, False), (3, 128, 1, False), (5, 256, 2, False), (9, 2048, 16, False),
     (7, 96, 3, False), (4, 35, 5, False), (6, 130, 1, True), (5, 1000, 1, False), (5, 999, 1, False),
     (3, 4096, 1, False), (2, 8192, 1, False), (3, 2500, 1, True), (2, 8191, 1, False), (700, 64, 4, False),
-    (3, 512, 1, False), (33, 1024, 2, True),
+    (3, 512, 1, False), (33, 1024, 2, True), (4, 500, 1, False), (3, 1998, 2, False), (2, 4098, 1, False), (2, 700, 1, True),
 ]
 
 
