@@ -292,6 +292,22 @@ __device__ __forceinline__ Two sigmoid_2(Two x) {
     return rcp_2(add2(two(1.f, 1.f), ex2_2(mul2(two(-kLog2e, -kLog2e), x))));
 }
 
+// softplus of both halves
+__device__ __forceinline__ Two softplus_2(Two x) {
+    float a, b;
+    split(x, a, b);
+    const Two e = two(ex2(-kLog2e * fabsf(a)), ex2(-kLog2e * fabsf(b)));
+    const Two s = mul2(e, rcp_2(add2(two(2.f, 2.f), e))), q = mul2(s, s);
+    const auto same = [](float c) { return two(c, c); };
+    Two r = fma2(q, same(1.f / 13.f), same(1.f / 11.f));
+    r = fma2(q, r, same(1.f / 9.f));
+    r = fma2(q, r, same(1.f / 7.f));
+    r = fma2(q, r, same(1.f / 5.f));
+    r = fma2(q, r, same(1.f / 3.f));
+    r = fma2(q, r, same(1.f));
+    return fma2(add2(s, s), r, two(fmaxf(a, 0.f), fmaxf(b, 0.f)));
+}
+
 // Pairs of elements: E elements are (E + 1) / 2 pairs (an odd one is alone in
 // its pair's low half).
 template <typename T, int E>

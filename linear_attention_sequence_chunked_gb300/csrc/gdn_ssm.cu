@@ -93,17 +93,30 @@ __global__ void __launch_bounds__(32 * kWarps, 3) ssm_fwd_kernel(const SsmArgs p
         widen_rows<T, N>(&st.B[0][0], &sm.B[0][0], lane);
         if constexpr (kOut) widen_rows<T, N>(&st.C[0][0], &sm.C[0][0], lane);
         const int left = len - t;
+        // two tokens at a time: dt and x = dt u of each, in both halves of a pair
         Two d2[kTile], x2[kTile], y2[kTile];
 #pragma unroll
-        for (int k = 0; k < kTile; ++k) {
-            const float uk = to_f32(st.u[k][ch]);
-            float dk = to_f32(st.dt[k][ch]) + bias;
-            if (p.softplus) dk = softplus(dk);
-            if (left < kTile) dk = k < left ? dk : 0.f;
-            if (!kOut) sum += dk;
-            d2[k] = two(dk, dk);
-            x2[k] = two(dk * uk, dk * uk);
-            if (kOut) y2[k] = two(dskip * uk, 0.f);
+        for (int k = 0; k < kTile; k += 2) {
+            const Two u2 = two(to_f32(st.u[k][ch]), to_f32(st.u[k + 1][ch]));
+            Two v = add2(two(to_f32(st.dt[k][ch]), to_f32(st.dt[k + 1][ch])), two(bias, bias));
+            if (p.softplus) v = softplus_2(v);
+            float v0, v1, x0, x1;
+            if (left < kTile) {
+                split(v, v0, v1);
+                v = two(k < left ? v0 : 0.f, k + 1 < left ? v1 : 0.f);
+            }
+            split(v, v0, v1);
+            split(mul2(v, u2), x0, x1);
+            if (!kOut) sum += v0 + v1;
+            d2[k] = two(v0, v0);
+            d2[k + 1] = two(v1, v1);
+            x2[k] = two(x0, x0);
+            x2[k + 1] = two(x1, x1);
+            if (kOut) {
+                split(mul2(u2, two(dskip, dskip)), x0, x1);
+                y2[k] = two(x0, 0.f);
+                y2[k + 1] = two(x1, 0.f);
+            }
         }
         __syncwarp();
 #pragma unroll
@@ -129,9 +142,12 @@ __global__ void __launch_bounds__(32 * kWarps, 3) ssm_fwd_kernel(const SsmArgs p
                 y[k] += hi;
 #pragma unroll
                 for (int m = 1; m < LPC; m *= 2) y[k] += __shfl_xor_sync(0xffffffffu, y[k], m);
-                if (z) {
-                    const float zk = to_f32(st.z[k][ch]);
-                    y[k] *= zk * sigmoid(zk);
+            }
+            if (z) {
+#pragma unroll
+                for (int k = 0; k < kTile; k += 2) {
+                    const Two z2 = two(to_f32(st.z[k][ch]), to_f32(st.z[k + 1][ch]));
+                    split(mul2(two(y[k], y[k + 1]), mul2(z2, sigmoid_2(z2))), y[k], y[k + 1]);
                 }
             }
             if (mine) {
