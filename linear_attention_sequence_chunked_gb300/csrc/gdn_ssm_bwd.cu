@@ -47,6 +47,10 @@ __device__ __forceinline__ void across_channels(float (&v)[8], int ch) {
     }
 }
 
+// A tile goes back in two halves: decays and states of four tokens fit the
+// registers of twelve warps per SM, those of eight only those of eight warps.
+constexpr int kHalf = kTile / 2;
+
 // kFull: the whole reverse mode.  Without it, only the state gradient that a
 // segment sends to the one before it, from a zero one at its end, and the sum
 // of its dt.
@@ -68,7 +72,8 @@ struct alignas(16) BwdShared {
     // a lane's own: A log2(e), the state gradient, the sum for dA
     float4 A2[GR][32], g[GR][32];
     float4 dA[kFull ? GR : 0][32];
-    float bc[kFull ? kTile : 0][2 * N];
+    float4 mid[kFull ? GR : 0][32];  // its states in the middle of the tile
+    float bc[kFull ? kHalf : 0][2 * N];
 };
 
 struct Four {
@@ -100,7 +105,7 @@ __device__ __forceinline__ float channel_sum(Two v) {
 }
 
 template <typename T, int N, bool kFull, int PB>
-__global__ void __launch_bounds__(32 * kWarps, 2) ssm_bwd_kernel(const SsmArgs p, int blocks) {
+__global__ void __launch_bounds__(32 * kWarps, 3) ssm_bwd_kernel(const SsmArgs p, int blocks) {
     using L = Lanes<N>;
     constexpr int CH = L::CH, LPC = L::LPC, GR = L::GR;
     constexpr int M8 = CH < 8 ? CH : 8;
@@ -192,22 +197,26 @@ __global__ void __launch_bounds__(32 * kWarps, 2) ssm_bwd_kernel(const SsmArgs p
         widen_rows<T, N>(&st.C[0][0], &sm.C[0][0], lane);
         if constexpr (kFull) widen_rows<T, N>(&st.B[0][0], &sm.B[0][0], lane);
         const int t = it * kTile, left = len - t;
-        float dk[kTile], xk[kTile], yk[kTile];
-#pragma unroll
-        for (int k = 0; k < kTile; ++k) {
+        // dt, x = dt u and dy of token k
+        auto token = [&](int k, float& dk, float& xk, float& yk) {
             float v = to_f32(st.dt[k][ch]) + bias;
             if (p.softplus) v = softplus(v);
-            dk[k] = k < left ? v : 0.f;
-            yk[k] = to_f32(st.d_out[k][ch]);
+            dk = k < left ? v : 0.f;
+            yk = to_f32(st.d_out[k][ch]);
             if (z) {
                 const float zk = to_f32(st.z[k][ch]);
-                yk[k] *= zk * sigmoid(zk);
+                yk *= zk * sigmoid(zk);
             }
-            if constexpr (kFull) xk[k] = dk[k] * to_f32(st.u[k][ch]);
-            if (!kFull) s_db += dk[k];
-        }
+            if constexpr (kFull) xk = dk * to_f32(st.u[k][ch]);
+        };
         __syncwarp();
         if constexpr (!kFull) {
+            float dk[kTile], yk[kTile], unused;
+#pragma unroll
+            for (int k = 0; k < kTile; ++k) {
+                token(k, dk[k], unused, yk[k]);
+                s_db += dk[k];
+            }
 #pragma unroll
             for (int j = 0; j < GR; ++j) {
                 const Four A2 = get4(sm.A2[j][lane]);
@@ -218,83 +227,106 @@ __global__ void __launch_bounds__(32 * kWarps, 2) ssm_bwd_kernel(const SsmArgs p
                 put4(sm.g[j][lane], g);
             }
         } else {
-            Two sx[kTile], sa[kTile], sy[kTile];
+            float dk[kHalf], xk[kHalf], yk[kHalf];
 #pragma unroll
-            for (int k = 0; k < kTile; ++k) sx[k] = sa[k] = sy[k] = two(0.f, 0.f);
+            for (int k = 0; k < kHalf; ++k) token(k, dk[k], xk[k], yk[k]);
+            if (left > kHalf) {  // the states in the middle of the tile
+#pragma unroll
+                for (int j = 0; j < GR; ++j) {
+                    const int at = 4 * (j * LPC + q);
+                    const Four A2 = get4(sm.A2[j][lane]);
+                    Four h = get4(&st.saved[ch][at]);
+#pragma unroll
+                    for (int k = 0; k < kHalf; ++k)
+                        h = fma4(ex2_4(mul4(A2, two(dk[k], dk[k]))), h, mul4(get4(&sm.B[k][at]), two(xk[k], xk[k])));
+                    put4(sm.mid[j][lane], h);
+                }
+            }
 #pragma unroll 1
-            for (int j = 0; j < GR; ++j) {
-                const int at = 4 * (j * LPC + q);
-                const Four A2 = get4(sm.A2[j][lane]);
-                Four g = get4(sm.g[j][lane]), dA = get4(sm.dA[j][lane]);
-                // the tile forward again: decays, and the state before and after every token
-                Four a[kTile], h[kTile + 1];
-                h[0] = get4(&st.saved[ch][at]);
+            for (int half = left > kHalf ? 1 : 0; half >= 0; --half) {
+                const int k0 = half * kHalf;
 #pragma unroll
-                for (int k = 0; k < kTile; ++k) {
-                    a[k] = ex2_4(mul4(A2, two(dk[k], dk[k])));
-                    h[k + 1] = fma4(a[k], h[k], mul4(get4(&sm.B[k][at]), two(xk[k], xk[k])));
-                    sy[k] = dot4(h[k + 1], get4(&sm.C[k][at]), sy[k]);
-                }
-                // and back
+                for (int k = 0; k < kHalf; ++k) token(k0 + k, dk[k], xk[k], yk[k]);
+                Two sx[kHalf], sa[kHalf], sy[kHalf];
 #pragma unroll
-                for (int k = kTile - 1; k >= 0; --k) {
-                    const Two y2 = two(yk[k], yk[k]);
-                    const Four e = fma4(get4(&sm.C[k][at]), y2, g);
-                    float v[8];
-                    {
-                        const Four vb = mul4(e, two(xk[k], xk[k])), vc = mul4(h[k + 1], y2);
-                        split(vb.lo, v[0], v[1]);
-                        split(vb.hi, v[2], v[3]);
-                        split(vc.lo, v[4], v[5]);
-                        split(vc.hi, v[6], v[7]);
+                for (int k = 0; k < kHalf; ++k) sx[k] = sa[k] = sy[k] = two(0.f, 0.f);
+#pragma unroll 1
+                for (int j = 0; j < GR; ++j) {
+                    const int at = 4 * (j * LPC + q);
+                    const Four A2 = get4(sm.A2[j][lane]);
+                    Four g = get4(sm.g[j][lane]), dA = get4(sm.dA[j][lane]);
+                    // forward again: decays, and the state before and after every token
+                    Four a[kHalf], h[kHalf + 1];
+                    h[0] = half ? get4(sm.mid[j][lane]) : get4(&st.saved[ch][at]);
+#pragma unroll
+                    for (int k = 0; k < kHalf; ++k) {
+                        a[k] = ex2_4(mul4(A2, two(dk[k], dk[k])));
+                        h[k + 1] = fma4(a[k], h[k], mul4(get4(&sm.B[k0 + k][at]), two(xk[k], xk[k])));
+                        sy[k] = dot4(h[k + 1], get4(&sm.C[k0 + k][at]), sy[k]);
                     }
-                    sx[k] = dot4(e, get4(&sm.B[k][at]), sx[k]);
-                    g = mul4(a[k], e);
-                    const Four qq = mul4(g, h[k]);
-                    sa[k] = dot4(A2, qq, sa[k]);
-                    dA = fma4(qq, two(dk[k], dk[k]), dA);
-                    across_channels<LPC, CH>(v, ch);
-                    if (ch < 8) {
+                    // and back
 #pragma unroll
-                        for (int i = 0; i < 8 / M8; ++i) {
-                            const int idx = i * M8 + ch;
-                            sm.bc[k][(idx >> 2) * N + at + (idx & 3)] = v[i];
+                    for (int k = kHalf - 1; k >= 0; --k) {
+                        const Two y2 = two(yk[k], yk[k]);
+                        const Four e = fma4(get4(&sm.C[k0 + k][at]), y2, g);
+                        float v[8];
+                        {
+                            const Four vb = mul4(e, two(xk[k], xk[k])), vc = mul4(h[k + 1], y2);
+                            split(vb.lo, v[0], v[1]);
+                            split(vb.hi, v[2], v[3]);
+                            split(vc.lo, v[4], v[5]);
+                            split(vc.hi, v[6], v[7]);
+                        }
+                        sx[k] = dot4(e, get4(&sm.B[k0 + k][at]), sx[k]);
+                        g = mul4(a[k], e);
+                        const Four qq = mul4(g, h[k]);
+                        sa[k] = dot4(A2, qq, sa[k]);
+                        dA = fma4(qq, two(dk[k], dk[k]), dA);
+                        across_channels<LPC, CH>(v, ch);
+                        if (ch < 8) {
+#pragma unroll
+                            for (int i = 0; i < 8 / M8; ++i) {
+                                const int idx = i * M8 + ch;
+                                sm.bc[k][(idx >> 2) * N + at + (idx & 3)] = v[i];
+                            }
+                        }
+                    }
+                    put4(sm.g[j][lane], g);
+                    put4(sm.dA[j][lane], dA);
+                }
+                __syncwarp();
+                // the warp's share of dB and dC
+                {
+                    float4* to = reinterpret_cast<float4*>(bc + (t + k0) * static_cast<long long>(2 * N));
+                    const float4* from = reinterpret_cast<const float4*>(&sm.bc[0][0]);
+                    const int n4 = min(kHalf, left - k0) * (N / 2);
+#pragma unroll
+                    for (int i = 0; i < (kHalf * N / 2 + 31) / 32; ++i)
+                        if (i * 32 + lane < n4) to[i * 32 + lane] = from[i * 32 + lane];
+                }
+                const long long at = dense + (t + k0) * static_cast<long long>(p.D);
+#pragma unroll
+                for (int k = 0; k < kHalf; ++k) {
+                    const float y = channel_sum<LPC>(sy[k]), dx = channel_sum<LPC>(sx[k]), da = channel_sum<LPC>(sa[k]);
+                    const float uk = to_f32(st.u[k0 + k][ch]);
+                    float dr = fmaf(uk, dx, da * (1.f / kLog2e));
+                    if (p.softplus) dr *= sigmoid(to_f32(st.dt[k0 + k][ch]) + bias);
+                    if (k0 + k < left) {
+                        s_dD = fmaf(yk[k], uk, s_dD);
+                        s_db += dr;
+                        if (mine && (LPC == 1 || q == k % LPC)) {
+                            const long long to = at + k * static_cast<long long>(p.D);
+                            static_cast<T*>(p.du)[to] = from_f32<T>(fmaf(dk[k], dx, dskip * yk[k]));
+                            static_cast<T*>(p.ddt)[to] = from_f32<T>(dr);
+                            if (z) {
+                                const float zk = to_f32(st.z[k0 + k][ch]);
+                                static_cast<T*>(p.dz)[to] =
+                                    from_f32<T>(to_f32(st.d_out[k0 + k][ch]) * fmaf(dskip, uk, y) * dsilu(zk, sigmoid(zk)));
+                            }
                         }
                     }
                 }
-                put4(sm.g[j][lane], g);
-                put4(sm.dA[j][lane], dA);
-            }
-            __syncwarp();
-            // the warp's share of dB and dC
-            {
-                float4* to = reinterpret_cast<float4*>(bc + t * static_cast<long long>(2 * N));
-                const float4* from = reinterpret_cast<const float4*>(&sm.bc[0][0]);
-                const int n4 = min(kTile, left) * (N / 2);
-#pragma unroll
-                for (int i = 0; i < (kTile * N / 2 + 31) / 32; ++i)
-                    if (i * 32 + lane < n4) to[i * 32 + lane] = from[i * 32 + lane];
-            }
-            const long long at = dense + t * static_cast<long long>(p.D);
-#pragma unroll
-            for (int k = 0; k < kTile; ++k) {
-                const float y = channel_sum<LPC>(sy[k]), dx = channel_sum<LPC>(sx[k]), da = channel_sum<LPC>(sa[k]);
-                const float uk = to_f32(st.u[k][ch]);
-                float dr = fmaf(uk, dx, da * (1.f / kLog2e));
-                if (p.softplus) dr *= sigmoid(to_f32(st.dt[k][ch]) + bias);
-                if (k < left) {
-                    s_dD = fmaf(yk[k], uk, s_dD);
-                    s_db += dr;
-                    if (mine && (LPC == 1 || q == k % LPC)) {
-                        static_cast<T*>(p.du)[at + k * static_cast<long long>(p.D)] = from_f32<T>(fmaf(dk[k], dx, dskip * yk[k]));
-                        static_cast<T*>(p.ddt)[at + k * static_cast<long long>(p.D)] = from_f32<T>(dr);
-                        if (z) {
-                            const float zk = to_f32(st.z[k][ch]);
-                            static_cast<T*>(p.dz)[at + k * static_cast<long long>(p.D)] =
-                                from_f32<T>(to_f32(st.d_out[k][ch]) * fmaf(dskip, uk, y) * dsilu(zk, sigmoid(zk)));
-                        }
-                    }
-                }
+                __syncwarp();  // before the other half's sums go where these were
             }
         }
     }
