@@ -242,8 +242,9 @@ __global__ void __launch_bounds__(32 * kWarps, 3) ssm_bwd_kernel(const SsmArgs p
                     put4(sm.mid[j][lane], h);
                 }
             }
-#pragma unroll 1
-            for (int half = left > kHalf ? 1 : 0; half >= 0; --half) {
+#pragma unroll
+            for (int half = 1; half >= 0; --half) {
+                if (half == 1 && left <= kHalf) continue;
                 const int k0 = half * kHalf;
 #pragma unroll
                 for (int k = 0; k < kHalf; ++k) token(k0 + k, dk[k], xk[k], yk[k]);
