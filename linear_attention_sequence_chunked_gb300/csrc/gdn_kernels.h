@@ -401,9 +401,12 @@ struct SsmArgs {
     // A long scan over few channels runs as segments of `seg` tokens (a multiple
     // of kSsmChunk; slots in all, as find_block counts): carry [slot][D][N] and
     // carry_dt [slot][D] join them.  Unsplit: seg 2^30, slots nseq, carry null.
+    // joined: a kernel has put the segments' start states into carry; otherwise
+    // carry holds what each segment adds by itself, and the few before a segment
+    // are put together where it starts.
     float* carry;
     float* carry_dt;
-    int seg;
+    int seg, joined;
     long long slots;
     int nseq, T, D, G, N, dtype;
     int* err;

@@ -88,13 +88,21 @@ size_t ssm_saved(int B, int T, int D, int N, bool varlen) {
 struct SsmSplit {
     int seg;
     long long slots;
+    int kernels;       // launched by the scan itself
+    bool joined;       // by a kernel of its own
     size_t dt, total;  // carry_dt's offset (carry is at 0); 0 bytes: not split
 };
 SsmSplit ssm_split(int B, int T, int D, int G, int N, bool varlen) {
     SsmSplit s{};
     s.seg = gdn::ssm_segment(B, T, D, G, N, varlen);
     s.slots = block_slots(B, T, s.seg, varlen);
+    s.kernels = 1;
     if (s.seg < T) {
+        // a sequence's segments are joined where they start up to 32 of them
+        // (a few hundred instructions per warp and one kernel less), beyond that
+        // by a kernel that walks them once
+        s.joined = (T - 1) / s.seg >= 32;
+        s.kernels = s.joined ? 3 : 2;
         s.dt = round_up(sizeof(float) * s.slots * D * N);
         s.total = s.dt + round_up(sizeof(float) * s.slots * D);
     }
@@ -103,6 +111,7 @@ SsmSplit ssm_split(int B, int T, int D, int G, int N, bool varlen) {
 void set_split(gdn::SsmArgs& a, const SsmSplit& s, void* workspace) {
     a.seg = s.seg;
     a.slots = s.slots;
+    a.joined = s.joined;
     if (s.total) {
         a.carry = static_cast<float*>(workspace);
         a.carry_dt = reinterpret_cast<float*>(static_cast<char*>(workspace) + s.dt);
@@ -248,7 +257,7 @@ gdn_status gdn_ssm_fwd(const void* u, int64_t u_stride, const void* dt, int64_t 
     a.saved = static_cast<float*>(saved);
     a.nseq = B; a.T = T; a.D = D; a.G = G; a.N = N; a.dtype = dtype; a.err = err;
     set_split(a, split, workspace);
-    return gdn::count_launch(gdn::launch_ssm_fwd(a, stream), split.total ? 3 : 1) ? GDN_OK : GDN_ERR_CUDA;
+    return gdn::count_launch(gdn::launch_ssm_fwd(a, stream), split.kernels) ? GDN_OK : GDN_ERR_CUDA;
 }
 
 size_t gdn_ssm_bwd_workspace_size(int B, int T, int D, int G, int N, int varlen) {
@@ -293,7 +302,7 @@ gdn_status gdn_ssm_bwd(const void* u, int64_t u_stride, const void* dt, int64_t 
     a.nseq = B; a.T = T; a.D = D; a.G = G; a.N = N; a.dtype = dtype; a.err = err;
     const SsmSplit split = ssm_split(B, T, D, G, N, varlen);
     set_split(a, split, ws + L.carry);
-    if (!gdn::count_launch(gdn::launch_ssm_bwd(a, stream), split.total ? 3 : 1)) return GDN_ERR_CUDA;
+    if (!gdn::count_launch(gdn::launch_ssm_bwd(a, stream), split.kernels)) return GDN_ERR_CUDA;
     gdn::SsmBcArgs bc{};
     bc.bc_part = a.bc_part; bc.dB = dB; bc.dC = dC; bc.rows = varlen ? T : static_cast<long long>(B) * T;
     bc.G = G; bc.N = N; bc.blocks = gdn::ssm_group_blocks(D, G, N); bc.dtype = dtype;

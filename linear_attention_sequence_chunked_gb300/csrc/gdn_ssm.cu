@@ -54,10 +54,19 @@ __global__ void __launch_bounds__(32 * kWarps, 3) ssm_fwd_kernel(const SsmArgs p
         A2[i] = mul2(A2[i], two(kLog2e, kLog2e));
         h[i] = two(0.f, 0.f);
     }
-    if (kOut && !w.first)
+    if (kOut && !w.first && p.joined) {
         load_states<N>(p.carry + co, q, h);
-    else if (kOut && p.initial_state)
-        load_states<N>(p.initial_state + so, q, h);
+    } else if (kOut) {
+        if (p.initial_state) load_states<N>(p.initial_state + so, q, h);
+        for (int i = w.before; i > 0; --i) {  // h <- exp(A sum dt) h + own end state, segment by segment
+            const long long sl = (w.slot - i) * p.D + d;
+            const float s = p.carry_dt[sl];
+            Two e[NL / 2];
+            load_states<N>(p.carry + sl * N, q, e);
+#pragma unroll
+            for (int k = 0; k < NL / 2; ++k) h[k] = fma2(ex2_2(mul2(A2[k], two(s, s))), h[k], e[k]);
+        }
+    }
     const float dskip = kOut && p.D_skip && q == 0 ? p.D_skip[d] : 0.f;
     const float bias = p.dt_bias ? p.dt_bias[d] : 0.f;
     float sum = 0.f;
@@ -296,7 +305,7 @@ cudaError_t fwd_v(const SsmArgs& a, cudaStream_t stream) {
     const long long units = a.slots * blocks * a.G;
     if (a.carry) {
         cudaError_t e = launch_warps(ssm_fwd_kernel<T, N, false, PB>, units, sizeof(FwdShared<T, N, false>), a, blocks, stream);
-        if (e == cudaSuccess) e = launch_compose(a, false, stream);
+        if (e == cudaSuccess && a.joined) e = launch_compose(a, false, stream);
         if (e != cudaSuccess) return e;
     }
     return launch_warps(ssm_fwd_kernel<T, N, true, PB>, units, sizeof(FwdShared<T, N, true>), a, blocks, stream);

@@ -135,7 +135,8 @@ __global__ void __launch_bounds__(32 * kWarps, 3) ssm_bwd_kernel(const SsmArgs p
     }
     const bool mine = ch < w.nd;
     const int d = w.d0 + (mine ? ch : 0);
-    const float* start = !kFull ? nullptr : p.carry ? p.carry + (slot * p.D + d) * N
+    const bool composed = kFull && p.carry && p.joined;
+    const float* start = !kFull ? nullptr : composed ? p.carry + (slot * p.D + d) * N
                          : p.d_final_state ? p.d_final_state + (static_cast<long long>(w.n) * p.D + d) * N : nullptr;
 #pragma unroll
     for (int j = 0; j < GR; ++j) {
@@ -143,7 +144,19 @@ __global__ void __launch_bounds__(32 * kWarps, 3) ssm_bwd_kernel(const SsmArgs p
         float4 a = *reinterpret_cast<const float4*>(p.A + static_cast<long long>(d) * N + at);
         a.x *= kLog2e; a.y *= kLog2e; a.z *= kLog2e; a.w *= kLog2e;
         sm.A2[j][lane] = a;
-        sm.g[j][lane] = start && mine ? *reinterpret_cast<const float4*>(start + at) : make_float4(0.f, 0.f, 0.f, 0.f);
+        float4 g = start && mine ? *reinterpret_cast<const float4*>(start + at) : make_float4(0.f, 0.f, 0.f, 0.f);
+        if (kFull && p.carry && !composed && mine) {
+            for (int i = w.after; i > 0; --i) {  // g <- exp(A sum dt) g + own gradient, from the last segment
+                const long long sl = (slot + i) * p.D + d;
+                const float s = p.carry_dt[sl];
+                const float4 e = *reinterpret_cast<const float4*>(p.carry + sl * N + at);
+                g.x = fmaf(ex2(a.x * s), g.x, e.x);
+                g.y = fmaf(ex2(a.y * s), g.y, e.y);
+                g.z = fmaf(ex2(a.z * s), g.z, e.z);
+                g.w = fmaf(ex2(a.w * s), g.w, e.w);
+            }
+        }
+        sm.g[j][lane] = g;
         if constexpr (kFull) sm.dA[j][lane] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
     const float dskip = kFull && p.D_skip ? p.D_skip[d] : 0.f;
@@ -377,7 +390,7 @@ cudaError_t bwd_v(const SsmArgs& a, cudaStream_t stream) {
     const long long units = a.slots * blocks * a.G;
     if (a.carry) {
         cudaError_t e = launch_warps(ssm_bwd_kernel<T, N, false, PB>, units, sizeof(BwdShared<T, N, false>), a, blocks, stream);
-        if (e == cudaSuccess) e = launch_ssm_compose(a, true, stream);
+        if (e == cudaSuccess && a.joined) e = launch_ssm_compose(a, true, stream);
         if (e != cudaSuccess) return e;
     }
     return launch_warps(ssm_bwd_kernel<T, N, true, PB>, units, sizeof(BwdShared<T, N, true>), a, blocks, stream);

@@ -36,6 +36,7 @@ struct Place {
     int g, d0, nd;            // group, first channel, channels (<= CH)
     long long chunk0;         // the segment's first slot of the saved chunk states
     long long slot;           // the segment itself
+    int before, after;        // segments of its sequence before and after it
 };
 
 template <int CH>
@@ -50,6 +51,8 @@ __device__ __forceinline__ bool find_place(const SsmArgs& p, long long slot, int
     w.s0 = static_cast<int>(begin);
     w.s1 = static_cast<int>(min(begin + seg, static_cast<long long>(w.t1)));
     w.last = w.s1 == w.t1;
+    w.before = static_cast<int>(c);
+    w.after = (w.t1 - w.s1 + seg - 1) / seg;
     const int per = p.D / p.G;
     w.g = block / blocks;
     const int off = block % blocks * CH;

@@ -216,6 +216,8 @@ LONG = [
     (1, 1500, 18, 2, 32, [0, 700, 700, 701, 1400, 1500], True, False, True, True),
     (1, 640, 3, 1, 64, [0, 1, 640], True, True, True, False),
     (1, 520, 4, 1, 128, None, True, False, True, True),
+    (1, 2600, 3, 1, 16, None, True, False, True, True),           # more segments than are joined on the way
+    (1, 2700, 5, 1, 8, [0, 2500, 2500, 2700], True, False, True, True),
 ]
 
 
