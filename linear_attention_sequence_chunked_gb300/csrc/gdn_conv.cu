@@ -64,9 +64,51 @@ __device__ __forceinline__ Raw<T, E> input_at(const T* x, long long x_stride, co
     return load_raw<T, E>(state ? state + (seq * (W - 1) + t - t0 + (W - 1)) * D : x, state ? E : 0);
 }
 
+// The next tokens of A arrays, U at a time, on their way to a thread's own part
+// of shared memory, kAhead batches ahead (two, or one of 16-byte items);
+// elements too small to copy (one bf16) wait in registers.
+template <typename T, int E, int U, int A, int THREADS>
+struct Ahead {
+    static constexpr bool kCopies = sizeof(T) * E >= 4;
+    static constexpr int kAhead = sizeof(T) * E == 4 || sizeof(T) * E == 8 ? 2 : 1;
+    static constexpr int kStages = kAhead + 1;
+    using Item = Raw<T, E>;
+    Item (*buf)[U][A][THREADS];
+    Item reg[U][A];
+    int at = 0;  // stage of the batch that get() looks at
+
+    // from(k, a): where item (k, a) of the next batch lies; on(k): whether it does
+    template <typename F, typename G>
+    __device__ __forceinline__ void issue(int ahead, F from, G on) {  // `ahead` batches after that
+        const int st = (at + ahead) % kStages;
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+#pragma unroll
+            for (int a = 0; a < A; ++a) {
+                if constexpr (kCopies)
+                    copy_async<T, E>(&buf[st][k][a][threadIdx.x], from(k, a), on(k));
+                else
+                    reg[k][a] = load_raw<T, E>(from(k, a), on(k) ? E : 0);
+            }
+        if constexpr (kCopies) commit_copies();
+    }
+    __device__ __forceinline__ void wait() {
+        if constexpr (kCopies) wait_copies<kAhead - 1>();
+    }
+    __device__ __forceinline__ Item get(int k, int a) const {
+        if constexpr (kCopies)
+            return buf[at][k][a][threadIdx.x];
+        else
+            return reg[k][a];
+    }
+    __device__ __forceinline__ void next() { at = (at + 1) % kStages; }
+};
+
 template <typename T, int W, int E>
 __global__ void __launch_bounds__(kThreads) conv_fwd_kernel(const ConvArgs p) {
     constexpr int U = 4, P = (E + 1) / 2;  // tokens whose loads are in flight together, pairs of channels
+    using In = Ahead<T, E, U, 1, kThreads>;
+    __shared__ typename In::Item buf[In::kCopies ? In::kStages : 1][U][1][kThreads];
     if (blockIdx.x == 0) check_offsets(p.cu_seqlens, p.N, p.T, p.err);
     const long long cv = p.D / E;
     const long long id = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
@@ -96,17 +138,20 @@ __global__ void __launch_bounds__(kThreads) conv_fwd_kernel(const ConvArgs p) {
         unpack_2<T, E>(input_at<T, W, E>(x, p.x_stride, s0, n, tb - (W - 1) + r, t0, p.D), win[r]);
     x += tb * p.x_stride;
     T* y = static_cast<T*>(p.y) + (static_cast<long long>(b) * p.T + tb) * p.D + d0;
-    Raw<T, E> in[U];
-    auto load = [&](int left) {
-#pragma unroll
-        for (int k = 0; k < U; ++k) in[k] = load_raw<T, E>(x + k * p.x_stride, k < left ? E : 0);
-        x += U * p.x_stride;
+    In in{buf};
+    auto load = [&](int ahead, int left) {
+        in.issue(ahead, [&](int k, int) { return x + (k < left ? k : 0) * p.x_stride; }, [&](int k) { return k < left; });
+        if (left > U) x += U * p.x_stride;  // the last batch stays inside the row
     };
-    load(te - tb);
-    for (int left = te - tb; left > 0; left -= U) {
+    int asked = te - tb;  // tokens not yet asked for
 #pragma unroll
-        for (int k = 0; k < U; ++k) unpack_2<T, E>(in[k], win[W - 1 + k]);
-        load(left - U);
+    for (int i = 0; i < In::kAhead; ++i, asked -= U) load(i, asked);
+    for (int left = te - tb; left > 0; left -= U, asked -= U) {
+        in.wait();
+#pragma unroll
+        for (int k = 0; k < U; ++k) unpack_2<T, E>(in.get(k, 0), win[W - 1 + k]);
+        load(In::kAhead, asked);
+        in.next();
 #pragma unroll
         for (int k = 0; k < U; ++k) {
             Two o[P];
@@ -136,6 +181,8 @@ constexpr int kRows = 4;
 template <typename T, int W, int E>
 __global__ void __launch_bounds__(kLanes * kRows, 4) conv_bwd_kernel(const ConvArgs p) {
     constexpr int U = 4, P = (E + 1) / 2;
+    using In = Ahead<T, E, U, 2, kLanes * kRows>;
+    __shared__ typename In::Item buf[In::kCopies ? In::kStages : 1][U][2][kLanes * kRows];
     __shared__ float red[kRows][kLanes][E + 1];
     if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(p.cu_seqlens, p.N, p.T, p.err);
     const int lane = threadIdx.x % kLanes, row = threadIdx.x / kLanes;
@@ -172,28 +219,35 @@ __global__ void __launch_bounds__(kLanes * kRows, 4) conv_bwd_kernel(const ConvA
             T* ds0 = p.d_initial_state && tb == t0
                          ? static_cast<T*>(p.d_initial_state) + static_cast<long long>(n) * (W - 1) * p.D + d0 : nullptr;
             x += tb * p.x_stride;
-            Raw<T, E> in[U], gin[U];
-            auto load = [&](int t) {
-#pragma unroll
-                for (int k = 0; k < U; ++k) {
-                    const int e = t + k < min(t1, te + W - 1) ? E : 0;
-                    in[k] = load_raw<T, E>(x + k * p.x_stride, e);
-                    gin[k] = load_raw<T, E>(dy + k * static_cast<long long>(p.D), e);
+            In in{buf};
+            const int end = min(t1, te + W - 1);
+            int asked = tb;  // the next token to ask for
+            auto load = [&](int ahead) {
+                in.issue(ahead,
+                         [&](int k, int a) {
+                             const int kk = asked + k < end ? k : 0;
+                             return a ? dy + kk * static_cast<long long>(p.D) : x + kk * p.x_stride;
+                         },
+                         [&](int k) { return asked + k < end; });
+                asked += U;
+                if (asked < end) {  // else: nothing is read there any more
+                    x += U * p.x_stride;
+                    dy += U * static_cast<long long>(p.D);
                 }
-                x += U * p.x_stride;
-                dy += U * static_cast<long long>(p.D);
             };
             // U tokens from t.  kInner: all of them and the inputs whose gradients
             // they complete lie inside the block, away from the sequence's ends.
             auto step = [&](int t, auto inner) {
                 constexpr bool kInner = decltype(inner)::value;
                 Two g[U][P];
+                in.wait();
 #pragma unroll
                 for (int k = 0; k < U; ++k) {
-                    unpack_2<T, E>(in[k], win[W - 1 + k]);
-                    unpack_2<T, E>(gin[k], g[k]);
+                    unpack_2<T, E>(in.get(k, 0), win[W - 1 + k]);
+                    unpack_2<T, E>(in.get(k, 1), g[k]);
                 }
-                load(t + U);
+                load(In::kAhead);
+                in.next();
 #pragma unroll
                 for (int k = 0; k < U; ++k) {
 #pragma unroll
@@ -246,7 +300,8 @@ __global__ void __launch_bounds__(kLanes * kRows, 4) conv_bwd_kernel(const ConvA
                         dp[j][i] = dp[j + U][i];
                     }
             };
-            load(tb);
+#pragma unroll
+            for (int i = 0; i < In::kAhead; ++i) load(i);
             int t = tb;
             step(t, std::false_type{});
             for (t += U; t + U <= te; t += U) step(t, std::true_type{});

@@ -159,6 +159,24 @@ __device__ __forceinline__ Raw<T, E> pack(const float* x) {
     return r;
 }
 
+// A thread's own copies from global to shared memory (it alone reads them, so a
+// wait is all they need): E elements of one row, zeros where `on` is false.
+template <typename T, int E>
+__device__ __forceinline__ void copy_async(void* to, const T* from, bool on) {
+    constexpr int bytes = static_cast<int>(sizeof(T)) * E;
+    static_assert(bytes == 4 || bytes == 8 || bytes == 16, "copy size");
+    const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(to));
+    if constexpr (bytes == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(from), "r"(on ? bytes : 0) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(from), "n"(bytes), "r"(on ? bytes : 0) : "memory");
+}
+__device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void wait_copies() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+
 constexpr float kLog2e = 1.4426950408889634f;
 
 // 2^x in one instruction (relative error about 2^-22, results below the

@@ -130,12 +130,6 @@ int scan_pieces(const SsmArgs& a) {
     return 0;
 }
 
-__device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int LEFT>
-__device__ __forceinline__ void wait_copies() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
-}
-
 // kTile x N elements of B or C, as fp32.
 template <typename T, int N>
 __device__ __forceinline__ void widen_rows(const T* src, float* dst, int lane) {
