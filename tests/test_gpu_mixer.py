@@ -470,3 +470,70 @@ def test_on_another_stream():
     o3, f3 = mixer.ssm_scan_fwd(*args, stream=s)
     s.synchronize()
     assert torch.equal(out, o2) and torch.equal(fs, f2) and torch.equal(out, o3) and torch.equal(fs, f3)
+
+
+# -------------------------------------------------------------- large offsets
+
+def test_offsets_beyond_32_bits():
+    """Rows far apart in a wide tensor and a slot far into a cache: the last
+    rows lie beyond 2^32 elements, and equal those of compact inputs."""
+    T, D, N, wide = 65600, 64, 16, 65664
+    assert (T - 1) * wide > 2 ** 32
+    big = torch.empty(1, T, wide, dtype=BF, device="cuda")
+    u = torch.randn(1, T, D, device="cuda").to(BF)
+    proj = torch.randn(1, T, 2 * N, device="cuda").to(BF)
+    big[..., 64:64 + D] = u
+    big[..., 256:256 + 2 * N] = proj
+    far = big[..., 64:64 + D]
+    B, C = (big[..., 256 + i * N:256 + (i + 1) * N].unflatten(2, (1, N)) for i in range(2))
+    B1, C1 = (proj[..., i * N:(i + 1) * N].unflatten(2, (1, N)) for i in range(2))
+    w = torch.randn(D, 4, device="cuda")
+    y, fs = mixer.short_conv_fwd(far, w, output_final_state=True)
+    y1, fs1 = mixer.short_conv_fwd(u, w, output_final_state=True)
+    assert torch.equal(y, y1) and torch.equal(fs, fs1)
+    g, g1 = mixer.short_conv_bwd(far, w, y), mixer.short_conv_bwd(u, w, y)
+    assert all(torch.equal(g[k], g1[k]) for k in g)
+    A = -torch.rand(D, N, device="cuda")
+    o, h = mixer.ssm_scan_fwd(far, far, A, B, C, z=far)
+    o1, h1 = mixer.ssm_scan_fwd(u, u, A, B1, C1, z=u)
+    assert torch.equal(o, o1) and torch.equal(h, h1)
+    n, n1 = mixer.group_norm_fwd(far, gate=far, groups=2), mixer.group_norm_fwd(u, gate=u, groups=2)
+    assert torch.equal(n, n1)
+    del big, far, B, C
+    S, D, N = 16500, 2048, 128
+    cache = torch.empty(S, D, N, device="cuda")
+    assert (S - 1) * D * N > 2 ** 32
+    row = torch.randn(1, D, N, device="cuda")
+    cache[S - 1] = row[0]
+    x = torch.randn(1, D, device="cuda")
+    Bm, A = torch.randn(1, 1, N, device="cuda"), -torch.rand(D, N, device="cuda")
+    slot = torch.tensor([S - 1], dtype=torch.int32, device="cuda")
+    y = mixer.ssm_scan_step(x, x, A, Bm, Bm, cache, slots=slot)
+    y1 = mixer.ssm_scan_step(x, x, A, Bm, Bm, row)
+    assert torch.equal(y, y1) and torch.equal(cache[S - 1], row[0])
+    _no_device_error()
+
+
+def test_nan_and_infinity_stay_in_their_sequence():
+    """A NaN input of one packed sequence, and infinities in the padding columns
+    beside the rows, touch no other sequence."""
+    cu = [0, 40, 41, 100]
+    a, t = _scan_inputs((1, 100, 24, 1, 16, cu, True, False, True, True), F32)
+    kw = dict(D=t["D"], z=t["z"], dt_bias=t["bias"], initial_state=t["h"], cu_seqlens=t["cu"])
+    args = (t["dt"], t["A"], t["B"], t["C"])
+    out, fs, saved = mixer.ssm_scan_fwd(t["u"], *args, save_for_backward=True, **kw)
+    g = mixer.ssm_scan_bwd(t["u"], *args, t["dout"], saved, **kw)
+    w = torch.randn(24, 4, device="cuda")
+    y, _ = mixer.short_conv_fwd(t["u"], w, cu_seqlens=t["cu"])
+    gy = mixer.short_conv_bwd(t["u"], w, t["dout"], cu_seqlens=t["cu"])
+    u = t["u"].clone()
+    u[0, 40] = float("nan")
+    out2, fs2, saved2 = mixer.ssm_scan_fwd(u, *args, save_for_backward=True, **kw)
+    g2 = mixer.ssm_scan_bwd(u, *args, t["dout"], saved2, **kw)
+    y2, _ = mixer.short_conv_fwd(u, w, cu_seqlens=t["cu"])
+    gy2 = mixer.short_conv_bwd(u, w, t["dout"], cu_seqlens=t["cu"])
+    assert torch.isnan(out2[0, 40]).all() and torch.isnan(y2[0, 40]).all()
+    for rows in (slice(0, 40), slice(41, 100)):
+        for p, q in ((out, out2), (y, y2), (gy["dx"], gy2["dx"])) + tuple((g[k], g2[k]) for k in ("du", "ddt", "dz", "dB", "dC")):
+            assert torch.equal(p[0, rows], q[0, rows])
+    assert torch.equal(fs[0], fs2[0]) and torch.equal(fs[2], fs2[2]) and torch.isnan(fs2[1]).all()
