@@ -412,7 +412,7 @@ struct SsmArgs {
     int* err;
 };
 // Tokens per segment of a scan of these sizes.
-int ssm_segment(int nseq, int T, int D, int G, int N, bool varlen);
+int ssm_segment(int nseq, int T, int D, int G, int N, bool varlen, bool backward);
 struct SsmStepArgs {
     const void* u;
     const void* dt;

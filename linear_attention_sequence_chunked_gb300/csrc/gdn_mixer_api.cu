@@ -92,9 +92,9 @@ struct SsmSplit {
     bool joined;       // by a kernel of its own
     size_t dt, total;  // carry_dt's offset (carry is at 0); 0 bytes: not split
 };
-SsmSplit ssm_split(int B, int T, int D, int G, int N, bool varlen) {
+SsmSplit ssm_split(int B, int T, int D, int G, int N, bool varlen, bool backward) {
     SsmSplit s{};
-    s.seg = gdn::ssm_segment(B, T, D, G, N, varlen);
+    s.seg = gdn::ssm_segment(B, T, D, G, N, varlen, backward);
     s.slots = block_slots(B, T, s.seg, varlen);
     s.kernels = 1;
     if (s.seg < T) {
@@ -126,7 +126,7 @@ SsmBwdLayout ssm_bwd_layout(int B, int T, int D, int G, int N, bool varlen) {
     const long long rows = varlen ? T : static_cast<long long>(B) * T;
     L.bc = 0;
     L.par = round_up(sizeof(float) * gdn::ssm_group_blocks(D, G, N) * static_cast<long long>(G) * rows * 2 * N);
-    const SsmSplit split = ssm_split(B, T, D, G, N, varlen);
+    const SsmSplit split = ssm_split(B, T, D, G, N, varlen, true);
     L.carry = L.par + round_up(sizeof(float) * split.slots * gdn::ssm_par_stride(D, N));
     L.total = L.carry + split.total;
     return L;
@@ -222,7 +222,7 @@ size_t gdn_ssm_saved_size(int B, int T, int D, int N, int varlen) {
 
 size_t gdn_ssm_fwd_workspace_size(int B, int T, int D, int G, int N, int varlen) {
     if (check_ssm(B, T, D, G, N, 0) != GDN_OK) return 0;
-    return ssm_split(B, T, D, G, N, varlen != 0).total;
+    return ssm_split(B, T, D, G, N, varlen != 0, false).total;
 }
 
 gdn_status gdn_ssm_fwd(const void* u, int64_t u_stride, const void* dt, int64_t dt_stride, const float* A,
@@ -244,7 +244,7 @@ gdn_status gdn_ssm_fwd(const void* u, int64_t u_stride, const void* dt, int64_t 
     GDN_TRY(check_cu(cu_seqlens));
     const bool varlen = cu_seqlens != nullptr;
     if (saved) GDN_TRY(check_ws(saved, saved_bytes, ssm_saved(B, T, D, N, varlen)));
-    const SsmSplit split = ssm_split(B, T, D, G, N, varlen);
+    const SsmSplit split = ssm_split(B, T, D, G, N, varlen, false);
     GDN_TRY(check_ws(workspace, workspace_bytes, split.total));
     if (T == 0 && !final_state) return GDN_OK;
     int* err = gdn::device_error_word();
@@ -300,7 +300,7 @@ gdn_status gdn_ssm_bwd(const void* u, int64_t u_stride, const void* dt, int64_t 
     a.d_initial_state = d_initial_state;
     a.bc_part = reinterpret_cast<float*>(ws + L.bc); a.par_part = reinterpret_cast<float*>(ws + L.par);
     a.nseq = B; a.T = T; a.D = D; a.G = G; a.N = N; a.dtype = dtype; a.err = err;
-    const SsmSplit split = ssm_split(B, T, D, G, N, varlen);
+    const SsmSplit split = ssm_split(B, T, D, G, N, varlen, true);
     set_split(a, split, ws + L.carry);
     if (!gdn::count_launch(gdn::launch_ssm_bwd(a, stream), split.kernels)) return GDN_ERR_CUDA;
     gdn::SsmBcArgs bc{};

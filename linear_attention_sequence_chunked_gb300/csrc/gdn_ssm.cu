@@ -20,9 +20,11 @@ struct alignas(16) FwdStage {
 };
 template <typename T, int N, bool kOut>
 struct alignas(16) FwdShared {
-    FwdStage<T, N, kOut> stage[kStages];
+    FwdStage<T, N, kOut> stage[kStages<N>];
     float B[kTile][N];
     float C[kOut ? kTile : 0][N];
+    // dt and x = dt u, where several lanes share a channel
+    float2 dx[Lanes<N>::LPC > 1 ? kTile : 0][Lanes<N>::CH];
 };
 
 // kOut: the whole forward.  Without it, only the segment's end state from a
@@ -67,7 +69,7 @@ __global__ void __launch_bounds__(32 * kWarps, 3) ssm_fwd_kernel(const SsmArgs p
             for (int k = 0; k < NL / 2; ++k) h[k] = fma2(ex2_2(mul2(A2[k], two(s, s))), h[k], e[k]);
         }
     }
-    const float dskip = kOut && p.D_skip && q == 0 ? p.D_skip[d] : 0.f;
+    const float dskip = kOut && p.D_skip ? p.D_skip[d] : 0.f;
     const float bias = p.dt_bias ? p.dt_bias[d] : 0.f;
     float sum = 0.f;
     const long long row0 = static_cast<long long>(w.b) * p.T + w.s0;
@@ -80,7 +82,7 @@ __global__ void __launch_bounds__(32 * kWarps, 3) ssm_fwd_kernel(const SsmArgs p
     const int len = w.s1 - w.s0;
     auto fetch = [&](int t) {  // the tile at token t, if there is one
         if (t < len) {
-            FwdStage<T, N, kOut>& st = sm.stage[t / kTile % kStages];
+            FwdStage<T, N, kOut>& st = sm.stage[t / kTile % kStages<N>];
             fill_tile<T, CH, PB>(&st.u[0][0], u + t * p.u_stride, p.u_stride, len - t, w.nd, lane);
             fill_tile<T, CH, PB>(&st.dt[0][0], dt + t * p.dt_stride, p.dt_stride, len - t, w.nd, lane);
             fill_tile<T, N, PB>(&st.B[0][0], Bm + t * p.B_stride, p.B_stride, len - t, N, lane);
@@ -92,39 +94,60 @@ __global__ void __launch_bounds__(32 * kWarps, 3) ssm_fwd_kernel(const SsmArgs p
         commit_copies();
     };
 #pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) fetch(i * kTile);
+    for (int i = 0; i < kStages<N> - 1; ++i) fetch(i * kTile);
     for (int t = 0; t < len; t += kTile) {
         if (kOut && p.saved && mine) store_states<N>(p.saved + ((w.chunk0 + t / kTile) * p.D + d) * N, q, h);
-        wait_copies<kStages - 2>();
+        wait_copies<kStages<N> - 2>();
         __syncwarp();  // the tile is there, and everyone is through with the one before
-        fetch(t + (kStages - 1) * kTile);
-        const FwdStage<T, N, kOut>& st = sm.stage[t / kTile % kStages];
+        fetch(t + (kStages<N> - 1) * kTile);
+        const FwdStage<T, N, kOut>& st = sm.stage[t / kTile % kStages<N>];
         widen_rows<T, N>(&st.B[0][0], &sm.B[0][0], lane);
         if constexpr (kOut) widen_rows<T, N>(&st.C[0][0], &sm.C[0][0], lane);
         const int left = len - t;
-        // two tokens at a time: dt and x = dt u of each, in both halves of a pair
         Two d2[kTile], x2[kTile], y2[kTile];
+        if constexpr (LPC == 1) {
+            // two tokens at a time: dt and x = dt u of each, in both halves of a pair
 #pragma unroll
-        for (int k = 0; k < kTile; k += 2) {
-            const Two u2 = two(to_f32(st.u[k][ch]), to_f32(st.u[k + 1][ch]));
-            Two v = add2(two(to_f32(st.dt[k][ch]), to_f32(st.dt[k + 1][ch])), two(bias, bias));
-            if (p.softplus) v = softplus_2(v);
-            float v0, v1, x0, x1;
-            if (left < kTile) {
+            for (int k = 0; k < kTile; k += 2) {
+                const Two u2 = two(to_f32(st.u[k][ch]), to_f32(st.u[k + 1][ch]));
+                Two v = add2(two(to_f32(st.dt[k][ch]), to_f32(st.dt[k + 1][ch])), two(bias, bias));
+                if (p.softplus) v = softplus_2(v);
+                float v0, v1, x0, x1;
+                if (left < kTile) {
+                    split(v, v0, v1);
+                    v = two(k < left ? v0 : 0.f, k + 1 < left ? v1 : 0.f);
+                }
                 split(v, v0, v1);
-                v = two(k < left ? v0 : 0.f, k + 1 < left ? v1 : 0.f);
+                split(mul2(v, u2), x0, x1);
+                if (!kOut) sum += v0 + v1;
+                d2[k] = two(v0, v0);
+                d2[k + 1] = two(v1, v1);
+                x2[k] = two(x0, x0);
+                x2[k + 1] = two(x1, x1);
+                if (kOut) {
+                    split(mul2(u2, two(dskip, dskip)), x0, x1);
+                    y2[k] = two(x0, 0.f);
+                    y2[k + 1] = two(x1, 0.f);
+                }
             }
-            split(v, v0, v1);
-            split(mul2(v, u2), x0, x1);
-            if (!kOut) sum += v0 + v1;
-            d2[k] = two(v0, v0);
-            d2[k + 1] = two(v1, v1);
-            x2[k] = two(x0, x0);
-            x2[k + 1] = two(x1, x1);
-            if (kOut) {
-                split(mul2(u2, two(dskip, dskip)), x0, x1);
-                y2[k] = two(x0, 0.f);
-                y2[k + 1] = two(x1, 0.f);
+        } else {
+            // each of a channel's lanes forms its share of the tokens
+#pragma unroll
+            for (int i = 0; i < kTile / LPC; ++i) {
+                const int k = i * LPC + q;
+                float v = to_f32(st.dt[k][ch]) + bias;
+                if (p.softplus) v = softplus(v);
+                v = k < left ? v : 0.f;
+                if (!kOut) sum += v;
+                sm.dx[k][ch] = make_float2(v, v * to_f32(st.u[k][ch]));
+            }
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < kTile; ++k) {
+                const float2 v = sm.dx[k][ch];
+                d2[k] = two(v.x, v.x);
+                x2[k] = two(v.y, v.y);
+                if (kOut) y2[k] = two(0.f, 0.f);
             }
         }
         __syncwarp();
@@ -149,23 +172,39 @@ __global__ void __launch_bounds__(32 * kWarps, 3) ssm_fwd_kernel(const SsmArgs p
                 float hi;
                 split(y2[k], y[k], hi);
                 y[k] += hi;
-#pragma unroll
-                for (int m = 1; m < LPC; m *= 2) y[k] += __shfl_xor_sync(0xffffffffu, y[k], m);
             }
-            if (z) {
+            if constexpr (LPC == 1) {
+                if (z) {
 #pragma unroll
-                for (int k = 0; k < kTile; k += 2) {
-                    const Two z2 = two(to_f32(st.z[k][ch]), to_f32(st.z[k + 1][ch]));
-                    split(mul2(two(y[k], y[k + 1]), mul2(z2, sigmoid_2(z2))), y[k], y[k + 1]);
+                    for (int k = 0; k < kTile; k += 2) {
+                        const Two z2 = two(to_f32(st.z[k][ch]), to_f32(st.z[k + 1][ch]));
+                        split(mul2(two(y[k], y[k + 1]), mul2(z2, sigmoid_2(z2))), y[k], y[k + 1]);
+                    }
                 }
-            }
-            if (mine) {
+                if (mine) {
 #pragma unroll
-                for (int k = 0; k < kTile; ++k)
-                    if (k < left && (LPC == 1 || q == k % LPC)) out[k * static_cast<long long>(p.D)] = from_f32<T>(y[k]);
+                    for (int k = 0; k < kTile; ++k)
+                        if (k < left) out[k * static_cast<long long>(p.D)] = from_f32<T>(y[k]);
+                }
+            } else {
+                share_sums<LPC>(y, q);
+#pragma unroll
+                for (int i = 0; i < kTile / LPC; ++i) {
+                    const int k = i * LPC + q;
+                    float v = fmaf(dskip, to_f32(st.u[k][ch]), y[i]);
+                    if (z) {
+                        const float zk = to_f32(st.z[k][ch]);
+                        v *= zk * sigmoid(zk);
+                    }
+                    if (mine && k < left) out[k * static_cast<long long>(p.D)] = from_f32<T>(v);
+                }
             }
             out += kTile * static_cast<long long>(p.D);
         }
+    }
+    if constexpr (!kOut) {
+#pragma unroll
+        for (int m = 1; m < LPC; m *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, m);
     }
     if (!mine) return;
     if constexpr (kOut) {
@@ -244,7 +283,7 @@ __global__ void __launch_bounds__(256) ssm_step_kernel(const SsmStepArgs p) {
 // The states between the segments of a split scan: carry holds every segment's
 // own contribution and receives the state it starts from (reverse: the
 // gradient that reaches its end), four states per thread, segment after segment
-// with the loads of eight in flight.
+// with the loads of 32 in flight.
 __global__ void __launch_bounds__(256) ssm_compose_kernel(const SsmArgs p, int reverse) {
     const long long id = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
     const long long per = static_cast<long long>(p.D) * p.N / 4;
@@ -262,7 +301,7 @@ __global__ void __launch_bounds__(256) ssm_compose_kernel(const SsmArgs p, int r
     if (start) h = *reinterpret_cast<const float4*>(start + (n * per + i4) * 4);
     float4 a = *reinterpret_cast<const float4*>(p.A + i4 * 4);
     a.x *= kLog2e; a.y *= kLog2e; a.z *= kLog2e; a.w *= kLog2e;
-    constexpr int U = 8;
+    constexpr int U = 32;
     for (int c = 0; c < segs; c += U) {
         float4 e[U];
         float s[U];
@@ -356,11 +395,16 @@ cudaError_t step_n(const SsmStepArgs& a, cudaStream_t stream) {
     }                                     \
     GDN_SSM_N(fn, float)
 
-int ssm_segment(int nseq, int T, int D, int G, int N, bool varlen) {
+// Segments: as many as give one wave of twelve warps per SM, none where the
+// channels alone fill the GPU.  Splitting costs a second pass (0.7 of the forward,
+// 0.2 of the reverse mode), so the forward stays whole from 456 warps (512 warps:
+// 266 us whole, 269 us in segments of the same work), the reverse mode from 1000
+// (512 warps: 1479 us whole, 978 us in segments).
+int ssm_segment(int nseq, int T, int D, int G, int N, bool varlen, bool backward) {
     const int ch = N <= 16 ? 32 : 512 / N;
     const long long warps = static_cast<long long>(varlen ? 1 : nseq) * G * ((D / G + ch - 1) / ch);
-    if (warps >= 456 || T < 256) return 1 << 30;
-    const long long segs = 152 * 12 / warps;  // one wave of 12 warps per SM
+    if (warps >= (backward ? 1000 : 456) || T < 256) return 1 << 30;
+    const long long segs = 152 * 12 / warps;
     const int seg = static_cast<int>(((T + segs - 1) / segs + kSsmChunk - 1) / kSsmChunk * kSsmChunk);
     return seg < 64 ? 64 : seg;
 }

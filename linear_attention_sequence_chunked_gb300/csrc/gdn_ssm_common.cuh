@@ -26,7 +26,10 @@ using namespace mix;
 
 constexpr int kWarps = 4;
 constexpr int kTile = kSsmChunk;  // tokens worked on at a time
-constexpr int kStages = 3;        // tiles of the forward in shared memory or on their way to it
+// Tiles of the forward in shared memory or on their way to it: two where a third
+// would leave room for eight warps per SM only.
+template <int N>
+constexpr int kStages = N >= 64 ? 2 : 3;
 
 // Where a warp works: segment `slot` of the tokens, one block of CH channels.
 struct Place {
@@ -152,6 +155,25 @@ __device__ __forceinline__ void widen_rows(const T* src, float* dst, int lane) {
                 *reinterpret_cast<float4*>(dst + at + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
         } else {
             *reinterpret_cast<float2*>(dst + at) = make_float2(x[0], x[1]);
+        }
+    }
+}
+
+// Sums over the LPC lanes of a channel of v[t], t < kTile: value i of lane q is
+// then the sum of token i LPC + q.  Half as many values after each exchange.
+template <int LPC>
+__device__ __forceinline__ void share_sums(float (&v)[kTile], int q) {
+    static_assert(LPC <= kTile, "a token per lane at least");
+#pragma unroll
+    for (int m = 1; m < LPC; m *= 2) {
+        const bool hi = (q & m) != 0;
+#pragma unroll
+        for (int i = 0; i < kTile / 2; ++i) {
+            if (i < kTile / (2 * m)) {
+                const float send = hi ? v[2 * i] : v[2 * i + 1];
+                const float keep = hi ? v[2 * i + 1] : v[2 * i];
+                v[i] = keep + __shfl_xor_sync(0xffffffffu, send, m);
+            }
         }
     }
 }
