@@ -343,11 +343,11 @@ cudaError_t fwd_v(const SsmArgs& a, cudaStream_t stream) {
     const int blocks = (a.D / a.G + Lanes<N>::CH - 1) / Lanes<N>::CH;
     const long long units = a.slots * blocks * a.G;
     if (a.carry) {
-        cudaError_t e = launch_warps(ssm_fwd_kernel<T, N, false, PB>, units, sizeof(FwdShared<T, N, false>), a, blocks, stream);
+        cudaError_t e = launch_warps<kWarps>(ssm_fwd_kernel<T, N, false, PB>, units, sizeof(FwdShared<T, N, false>), a, blocks, stream);
         if (e == cudaSuccess && a.joined) e = launch_compose(a, false, stream);
         if (e != cudaSuccess) return e;
     }
-    return launch_warps(ssm_fwd_kernel<T, N, true, PB>, units, sizeof(FwdShared<T, N, true>), a, blocks, stream);
+    return launch_warps<kWarps>(ssm_fwd_kernel<T, N, true, PB>, units, sizeof(FwdShared<T, N, true>), a, blocks, stream);
 }
 
 template <typename T, int N>

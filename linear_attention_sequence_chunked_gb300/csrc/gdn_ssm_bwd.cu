@@ -51,9 +51,16 @@ __device__ __forceinline__ void across_channels(float (&v)[8], int ch) {
 // registers of twelve warps per SM, those of eight only those of eight warps.
 constexpr int kHalf = kTile / 2;
 
+// Warps per block: from N = 64 on shared memory holds fewer than twelve warps per
+// SM, and more of them in smaller blocks (1 x 2048 x 1024, N = 128: 612 us by two
+// warps, 657 by four, 646 by one; N = 64: 278, 280, 321).
+template <int N>
+constexpr int kBwdWarps = N >= 64 ? 2 : 4;
+
 // kFull: the whole reverse mode.  Without it, only the state gradient that a
 // segment sends to the one before it, from a zero one at its end, and the sum
 // of its dt.
+
 template <typename T, int N, bool kFull>
 struct alignas(16) BwdStage {
     static constexpr int CH = Lanes<N>::CH;
@@ -74,6 +81,7 @@ struct alignas(16) BwdShared {
     float4 dA[kFull ? GR : 0][32];
     float4 mid[kFull ? GR : 0][32];  // its states in the middle of the tile
     float bc[kFull ? kHalf : 0][2 * N];
+    float4 tok[Lanes<N>::LPC > 1 ? kTile : 0][Lanes<N>::CH];  // dt, x and dy of a token, where lanes share a channel
 };
 
 struct Four {
@@ -93,19 +101,15 @@ __device__ __forceinline__ Four fma4(Four a, Two b, Four c) { return Four{fma2(a
 __device__ __forceinline__ Four fma4(Four a, Four b, Four c) { return Four{fma2(a.lo, b.lo, c.lo), fma2(a.hi, b.hi, c.hi)}; }
 __device__ __forceinline__ Two dot4(Four a, Four b, Two c) { return fma2(a.hi, b.hi, fma2(a.lo, b.lo, c)); }
 __device__ __forceinline__ Four ex2_4(Four a) { return Four{ex2_2(a.lo), ex2_2(a.hi)}; }
-// the sum of both halves, over a channel's LPC lanes
-template <int LPC>
-__device__ __forceinline__ float channel_sum(Two v) {
+// the sum of both halves
+__device__ __forceinline__ float both(Two v) {
     float lo, hi;
     split(v, lo, hi);
-    lo += hi;
-#pragma unroll
-    for (int m = 1; m < LPC; m *= 2) lo += __shfl_xor_sync(0xffffffffu, lo, m);
-    return lo;
+    return lo + hi;
 }
 
 template <typename T, int N, bool kFull, int PB>
-__global__ void __launch_bounds__(32 * kWarps, 3) ssm_bwd_kernel(const SsmArgs p, int blocks) {
+__global__ void __launch_bounds__(32 * kBwdWarps<N>, 12 / kBwdWarps<N>) ssm_bwd_kernel(const SsmArgs p, int blocks) {
     using L = Lanes<N>;
     constexpr int CH = L::CH, LPC = L::LPC, GR = L::GR;
     constexpr int M8 = CH < 8 ? CH : 8;
@@ -113,7 +117,7 @@ __global__ void __launch_bounds__(32 * kWarps, 3) ssm_bwd_kernel(const SsmArgs p
     if (blockIdx.x == 0) check_offsets(p.cu_seqlens, p.nseq, p.T, p.err);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     BwdShared<T, N, kFull>& sm = reinterpret_cast<BwdShared<T, N, kFull>*>(smem)[warp];
-    const long long unit = static_cast<long long>(blockIdx.x) * kWarps + warp;
+    const long long unit = static_cast<long long>(blockIdx.x) * kBwdWarps<N> + warp;
     const int nblk = blocks * p.G;
     if (unit >= p.slots * nblk) return;
     const long long slot = unit / nblk;
@@ -211,7 +215,7 @@ __global__ void __launch_bounds__(32 * kWarps, 3) ssm_bwd_kernel(const SsmArgs p
         if constexpr (kFull) widen_rows<T, N>(&st.B[0][0], &sm.B[0][0], lane);
         const int t = it * kTile, left = len - t;
         // dt, x = dt u and dy of token k
-        auto token = [&](int k, float& dk, float& xk, float& yk) {
+        auto form = [&](int k, float& dk, float& xk, float& yk) {
             float v = to_f32(st.dt[k][ch]) + bias;
             if (p.softplus) v = softplus(v);
             dk = k < left ? v : 0.f;
@@ -221,6 +225,24 @@ __global__ void __launch_bounds__(32 * kWarps, 3) ssm_bwd_kernel(const SsmArgs p
                 yk *= zk * sigmoid(zk);
             }
             if constexpr (kFull) xk = dk * to_f32(st.u[k][ch]);
+        };
+        if constexpr (LPC > 1) {
+#pragma unroll
+            for (int i = 0; i < kTile / LPC; ++i) {
+                float dk, xk = 0.f, yk;
+                form(i * LPC + q, dk, xk, yk);
+                sm.tok[i * LPC + q][ch] = make_float4(dk, xk, yk, 0.f);
+            }
+        }
+        auto token = [&](int k, float& dk, float& xk, float& yk) {
+            if constexpr (LPC > 1) {
+                const float4 v = sm.tok[k][ch];
+                dk = v.x;
+                xk = v.y;
+                yk = v.z;
+            } else {
+                form(k, dk, xk, yk);
+            }
         };
         __syncwarp();
         if constexpr (!kFull) {
@@ -240,9 +262,9 @@ __global__ void __launch_bounds__(32 * kWarps, 3) ssm_bwd_kernel(const SsmArgs p
                 put4(sm.g[j][lane], g);
             }
         } else {
-            float dk[kHalf], xk[kHalf], yk[kHalf];
+            float dts[kHalf], xs[kHalf], dys[kHalf];
 #pragma unroll
-            for (int k = 0; k < kHalf; ++k) token(k, dk[k], xk[k], yk[k]);
+            for (int k = 0; k < kHalf; ++k) token(k, dts[k], xs[k], dys[k]);
             if (left > kHalf) {  // the states in the middle of the tile
 #pragma unroll
                 for (int j = 0; j < GR; ++j) {
@@ -251,7 +273,7 @@ __global__ void __launch_bounds__(32 * kWarps, 3) ssm_bwd_kernel(const SsmArgs p
                     Four h = get4(&st.saved[ch][at]);
 #pragma unroll
                     for (int k = 0; k < kHalf; ++k)
-                        h = fma4(ex2_4(mul4(A2, two(dk[k], dk[k]))), h, mul4(get4(&sm.B[k][at]), two(xk[k], xk[k])));
+                        h = fma4(ex2_4(mul4(A2, two(dts[k], dts[k]))), h, mul4(get4(&sm.B[k][at]), two(xs[k], xs[k])));
                     put4(sm.mid[j][lane], h);
                 }
             }
@@ -260,7 +282,7 @@ __global__ void __launch_bounds__(32 * kWarps, 3) ssm_bwd_kernel(const SsmArgs p
                 if (half == 1 && left <= kHalf) continue;
                 const int k0 = half * kHalf;
 #pragma unroll
-                for (int k = 0; k < kHalf; ++k) token(k0 + k, dk[k], xk[k], yk[k]);
+                for (int k = 0; k < kHalf; ++k) token(k0 + k, dts[k], xs[k], dys[k]);
                 Two sx[kHalf], sa[kHalf], sy[kHalf];
 #pragma unroll
                 for (int k = 0; k < kHalf; ++k) sx[k] = sa[k] = sy[k] = two(0.f, 0.f);
@@ -274,18 +296,18 @@ __global__ void __launch_bounds__(32 * kWarps, 3) ssm_bwd_kernel(const SsmArgs p
                     h[0] = half ? get4(sm.mid[j][lane]) : get4(&st.saved[ch][at]);
 #pragma unroll
                     for (int k = 0; k < kHalf; ++k) {
-                        a[k] = ex2_4(mul4(A2, two(dk[k], dk[k])));
-                        h[k + 1] = fma4(a[k], h[k], mul4(get4(&sm.B[k0 + k][at]), two(xk[k], xk[k])));
+                        a[k] = ex2_4(mul4(A2, two(dts[k], dts[k])));
+                        h[k + 1] = fma4(a[k], h[k], mul4(get4(&sm.B[k0 + k][at]), two(xs[k], xs[k])));
                         sy[k] = dot4(h[k + 1], get4(&sm.C[k0 + k][at]), sy[k]);
                     }
                     // and back
 #pragma unroll
                     for (int k = kHalf - 1; k >= 0; --k) {
-                        const Two y2 = two(yk[k], yk[k]);
+                        const Two y2 = two(dys[k], dys[k]);
                         const Four e = fma4(get4(&sm.C[k0 + k][at]), y2, g);
                         float v[8];
                         {
-                            const Four vb = mul4(e, two(xk[k], xk[k])), vc = mul4(h[k + 1], y2);
+                            const Four vb = mul4(e, two(xs[k], xs[k])), vc = mul4(h[k + 1], y2);
                             split(vb.lo, v[0], v[1]);
                             split(vb.hi, v[2], v[3]);
                             split(vc.lo, v[4], v[5]);
@@ -295,7 +317,7 @@ __global__ void __launch_bounds__(32 * kWarps, 3) ssm_bwd_kernel(const SsmArgs p
                         g = mul4(a[k], e);
                         const Four qq = mul4(g, h[k]);
                         sa[k] = dot4(A2, qq, sa[k]);
-                        dA = fma4(qq, two(dk[k], dk[k]), dA);
+                        dA = fma4(qq, two(dts[k], dts[k]), dA);
                         across_channels<LPC, CH>(v, ch);
                         if (ch < 8) {
 #pragma unroll
@@ -319,18 +341,17 @@ __global__ void __launch_bounds__(32 * kWarps, 3) ssm_bwd_kernel(const SsmArgs p
                         if (i * 32 + lane < n4) to[i * 32 + lane] = from[i * 32 + lane];
                 }
                 const long long at = dense + (t + k0) * static_cast<long long>(p.D);
-#pragma unroll
-                for (int k = 0; k < kHalf; ++k) {
-                    const float y = channel_sum<LPC>(sy[k]), dx = channel_sum<LPC>(sx[k]), da = channel_sum<LPC>(sa[k]);
+                // the outputs of token k0 + k
+                auto finish = [&](int k, float dk, float yk, float y, float dx, float da) {
                     const float uk = to_f32(st.u[k0 + k][ch]);
                     float dr = fmaf(uk, dx, da * (1.f / kLog2e));
                     if (p.softplus) dr *= sigmoid(to_f32(st.dt[k0 + k][ch]) + bias);
                     if (k0 + k < left) {
-                        s_dD = fmaf(yk[k], uk, s_dD);
+                        s_dD = fmaf(yk, uk, s_dD);
                         s_db += dr;
-                        if (mine && (LPC == 1 || q == k % LPC)) {
+                        if (mine) {
                             const long long to = at + k * static_cast<long long>(p.D);
-                            static_cast<T*>(p.du)[to] = from_f32<T>(fmaf(dk[k], dx, dskip * yk[k]));
+                            static_cast<T*>(p.du)[to] = from_f32<T>(fmaf(dk, dx, dskip * yk));
                             static_cast<T*>(p.ddt)[to] = from_f32<T>(dr);
                             if (z) {
                                 const float zk = to_f32(st.z[k0 + k][ch]);
@@ -339,9 +360,38 @@ __global__ void __launch_bounds__(32 * kWarps, 3) ssm_bwd_kernel(const SsmArgs p
                             }
                         }
                     }
+                };
+                if constexpr (LPC == 1) {
+#pragma unroll
+                    for (int k = 0; k < kHalf; ++k) finish(k, dts[k], dys[k], both(sy[k]), both(sx[k]), both(sa[k]));
+                } else {  // a lane takes the tokens whose sums it ends up with
+                    float y[kHalf], dx[kHalf], da[kHalf];
+#pragma unroll
+                    for (int k = 0; k < kHalf; ++k) {
+                        y[k] = both(sy[k]);
+                        dx[k] = both(sx[k]);
+                        da[k] = both(sa[k]);
+                    }
+                    share_sums<LPC>(y, q);
+                    share_sums<LPC>(dx, q);
+                    share_sums<LPC>(da, q);
+                    if (LPC <= kHalf || q < kHalf) {
+#pragma unroll
+                        for (int i = 0; i < (kHalf + LPC - 1) / LPC; ++i) {
+                            const float4 v = sm.tok[k0 + i * LPC + q][ch];
+                            finish(i * LPC + q, v.x, v.z, y[i], dx[i], da[i]);
+                        }
+                    }
                 }
                 __syncwarp();  // before the other half's sums go where these were
             }
+        }
+    }
+    if constexpr (kFull) {  // a channel's lanes took different tokens
+#pragma unroll
+        for (int m = 1; m < LPC; m *= 2) {
+            s_dD += __shfl_xor_sync(0xffffffffu, s_dD, m);
+            s_db += __shfl_xor_sync(0xffffffffu, s_db, m);
         }
     }
     if (!mine) return;
@@ -389,11 +439,11 @@ cudaError_t bwd_v(const SsmArgs& a, cudaStream_t stream) {
     const int blocks = ssm_group_blocks(a.D, a.G, N);
     const long long units = a.slots * blocks * a.G;
     if (a.carry) {
-        cudaError_t e = launch_warps(ssm_bwd_kernel<T, N, false, PB>, units, sizeof(BwdShared<T, N, false>), a, blocks, stream);
+        cudaError_t e = launch_warps<kBwdWarps<N>>(ssm_bwd_kernel<T, N, false, PB>, units, sizeof(BwdShared<T, N, false>), a, blocks, stream);
         if (e == cudaSuccess && a.joined) e = launch_ssm_compose(a, true, stream);
         if (e != cudaSuccess) return e;
     }
-    return launch_warps(ssm_bwd_kernel<T, N, true, PB>, units, sizeof(BwdShared<T, N, true>), a, blocks, stream);
+    return launch_warps<kBwdWarps<N>>(ssm_bwd_kernel<T, N, true, PB>, units, sizeof(BwdShared<T, N, true>), a, blocks, stream);
 }
 
 template <typename T, int N>

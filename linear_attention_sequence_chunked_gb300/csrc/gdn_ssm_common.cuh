@@ -159,21 +159,25 @@ __device__ __forceinline__ void widen_rows(const T* src, float* dst, int lane) {
     }
 }
 
-// Sums over the LPC lanes of a channel of v[t], t < kTile: value i of lane q is
-// then the sum of token i LPC + q.  Half as many values after each exchange.
-template <int LPC>
-__device__ __forceinline__ void share_sums(float (&v)[kTile], int q) {
-    static_assert(LPC <= kTile, "a token per lane at least");
+// Sums over the LPC lanes of a channel of v[t], t < W: value i of lane q is then
+// the sum of token i LPC + q (of token q mod W where LPC > W).  Half as many
+// values after each exchange.
+template <int LPC, int W>
+__device__ __forceinline__ void share_sums(float (&v)[W], int q) {
 #pragma unroll
     for (int m = 1; m < LPC; m *= 2) {
-        const bool hi = (q & m) != 0;
+        if (m < W) {
+            const bool hi = (q & m) != 0;
 #pragma unroll
-        for (int i = 0; i < kTile / 2; ++i) {
-            if (i < kTile / (2 * m)) {
-                const float send = hi ? v[2 * i] : v[2 * i + 1];
-                const float keep = hi ? v[2 * i + 1] : v[2 * i];
-                v[i] = keep + __shfl_xor_sync(0xffffffffu, send, m);
+            for (int i = 0; i < W / 2; ++i) {
+                if (i < W / (2 * m)) {
+                    const float send = hi ? v[2 * i] : v[2 * i + 1];
+                    const float keep = hi ? v[2 * i + 1] : v[2 * i];
+                    v[i] = keep + __shfl_xor_sync(0xffffffffu, send, m);
+                }
             }
+        } else {
+            v[0] += __shfl_xor_sync(0xffffffffu, v[0], m);
         }
     }
 }
@@ -200,14 +204,14 @@ __device__ __forceinline__ void store_states(float* p, int q, const Two (&v)[Lan
 }
 
 // One launch; shared memory beyond 48 KB is asked for once per kernel.
-template <typename F>
+template <int WARPS, typename F>
 cudaError_t launch_warps(F kernel, long long units, int bytes_per_warp, const SsmArgs& a, int blocks, cudaStream_t stream) {
-    const int bytes = kWarps * bytes_per_warp;
+    const int bytes = WARPS * bytes_per_warp;
     if (bytes > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != cudaSuccess) return e;
     }
-    kernel<<<static_cast<unsigned>((units + kWarps - 1) / kWarps), 32 * kWarps, bytes, stream>>>(a, blocks);
+    kernel<<<static_cast<unsigned>((units + WARPS - 1) / WARPS), 32 * WARPS, bytes, stream>>>(a, blocks);
     return cudaGetLastError();
 }
 
