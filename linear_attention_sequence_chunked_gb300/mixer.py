@@ -6,7 +6,8 @@ As in gdn.py, nothing is computed here: arguments are checked and handed to
 the CUDA kernels of ``_build/libgdn.so`` (include/gdn.h has the formulas and
 layouts), without a CPU fallback.  ``*_fwd`` / ``*_bwd`` / ``*_step`` allocate
 their outputs and workspaces with torch; short_conv, ssm_scan and group_norm
-are the same forwards and backwards behind torch.autograd.
+are the same forwards and backwards behind torch.autograd.  The former also
+take `stream=`, in place of the current stream.
 
 Activations are channels last and bf16 or fp32, one type per call; parameters
 and the states of the scan are fp32.  The activation inputs x, gate, u, dt, z,
@@ -18,7 +19,7 @@ from __future__ import annotations
 
 import torch
 
-from .gdn import _check, _stream, _workspace, load
+from .gdn import _check, _workspace, load
 
 _ACTIVATIONS = {None: 0, "none": 0, "silu": 1, "sigmoid": 2}
 STATE_SIZES = (8, 16, 32, 64, 128)
@@ -62,8 +63,24 @@ def _on_gpu(dev, x):
         raise ValueError(f"expected a CUDA tensor, got one on {x.device}")
 
 
-def _current(stream, dev):
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+def _on_stream(fn, args):
+    """fn with its arguments, `stream` among them (a torch.cuda.Stream or its
+    address), on that stream.  Outputs and workspaces are taken from that
+    stream's memory, and outputs stay until the work that the caller's stream
+    has for them is done."""
+    stream = args.pop("stream")
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    caller = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        out = fn(**args)
+    for t in out.values() if isinstance(out, dict) else out if isinstance(out, tuple) else (out,):
+        if t is not None:
+            t.record_stream(caller)
+    return out
+
+
+_current = torch._C._cuda_getCurrentRawStream
 
 
 def _rows(x, width, inner=1):
@@ -158,10 +175,12 @@ def short_conv_fwd(x, weight, bias=None, activation="silu", initial_state=None, 
     """Causal convolution of every channel over its last W tokens: x (B, T, D),
     weight (D, W), bias (D), initial_state (N, W - 1, D) in x's dtype (the
     inputs before each sequence).  Returns (y (B, T, D), final_state or None)."""
+    if stream is not None:
+        return _on_stream(short_conv_fwd, locals())
     dev, dims, args = _conv_args(x, weight, bias, activation, initial_state, cu_seqlens)
     y = x.new_empty(x.shape)
     fs = x.new_empty((dims[0], dims[3] - 1, dims[2])) if output_final_state else None
-    _check(load().gdn_conv_fwd(*args, y.data_ptr(), None if fs is None else fs.data_ptr(), *dims, _current(stream, dev)),
+    _check(load().gdn_conv_fwd(*args, y.data_ptr(), None if fs is None else fs.data_ptr(), *dims, _current(dev)),
            "gdn_conv_fwd")
     return y, fs
 
@@ -170,6 +189,8 @@ def short_conv_bwd(x, weight, d_out, bias=None, activation="silu", initial_state
                    d_final_state=None, stream=None):
     """Gradients of short_conv_fwd: a dict of dx, dweight, dbias (with a bias)
     and d_initial_state (with an initial state)."""
+    if stream is not None:
+        return _on_stream(short_conv_bwd, locals())
     dev, dims, args = _conv_args(x, weight, bias, activation, initial_state, cu_seqlens)
     N, T, D, W = dims[:4]
     d_out = _dense("d_out", d_out, x.shape, x.dtype, dev)
@@ -183,7 +204,7 @@ def short_conv_bwd(x, weight, d_out, bias=None, activation="silu", initial_state
     nbytes = lib.gdn_conv_bwd_workspace_size(N, T, D, W, int(cu_seqlens is not None))
     ws = _workspace(nbytes, x.device)
     _check(lib.gdn_conv_bwd(*args, d_out, dfs, res["dx"].data_ptr(), res["dweight"].data_ptr(), _out(res, "dbias"),
-                            _out(res, "d_initial_state"), *dims, ws.data_ptr(), nbytes, _current(stream, dev)),
+                            _out(res, "d_initial_state"), *dims, ws.data_ptr(), nbytes, _current(dev)),
            "gdn_conv_bwd")
     return res
 
@@ -198,6 +219,8 @@ def short_conv_step(x, state, weight, bias=None, activation="silu", slots=None, 
     place or into out_state.  slots (B, int32): the cache row of each batch row
     (negative: an idle row, whose output is zero); by default row b.  Returns y
     (B, D)."""
+    if stream is not None:
+        return _on_stream(short_conv_step, locals())
     if x.dim() != 2:
         raise ValueError(f"x must be (B, D), got shape {tuple(x.shape)}")
     dtype, dev = _dtype(x, "x"), x.get_device()
@@ -210,7 +233,7 @@ def short_conv_step(x, state, weight, bias=None, activation="silu", slots=None, 
     _on_gpu(dev, x)
     y = x.new_empty((B, D))
     _check(load().gdn_conv_step(*_rows(x, D), w, b, at, to, sl, y.data_ptr(), B, S, D, W, act, dtype,
-                             _current(stream, dev)), "gdn_conv_step")
+                             _current(dev)), "gdn_conv_step")
     return y
 
 
@@ -254,6 +277,8 @@ def ssm_scan_fwd(u, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=True,
     (B, T, G, N); D, dt_bias (D); initial_state (N_seq, D, N) fp32.  Returns
     (out, final_state or None), or (out, final_state, saved) with
     save_for_backward (the states ssm_scan_bwd starts from)."""
+    if stream is not None:
+        return _on_stream(ssm_scan_fwd, locals())
     if u.dim() != 3:
         raise ValueError(f"u must be (B, T, D), got shape {tuple(u.shape)}")
     dev, dims, args = _scan_args(u, dt, A, B, C, D, z, dt_bias, dt_softplus)
@@ -273,7 +298,7 @@ def ssm_scan_fwd(u, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=True,
     ws = _workspace(nbytes, u.device)
     _check(lib.gdn_ssm_fwd(*args, h0, cu, out.data_ptr(), None if fs is None else fs.data_ptr(),
                            None if saved is None else saved.data_ptr(), sbytes, nseq, T, *dims,
-                           None if ws is None else ws.data_ptr(), nbytes, _current(stream, dev)), "gdn_ssm_fwd")
+                           None if ws is None else ws.data_ptr(), nbytes, _current(dev)), "gdn_ssm_fwd")
     return (out, fs, saved) if save_for_backward else (out, fs)
 
 
@@ -282,6 +307,8 @@ def ssm_scan_bwd(u, dt, A, B, C, d_out, saved, D=None, z=None, dt_bias=None, dt_
     """Gradients of ssm_scan_fwd from the same inputs and the `saved` that it
     returned: a dict of du, ddt, dA, dB, dC, and dD, dz, ddt_bias and
     d_initial_state for those that were given."""
+    if stream is not None:
+        return _on_stream(ssm_scan_bwd, locals())
     if u.dim() != 3:
         raise ValueError(f"u must be (B, T, D), got shape {tuple(u.shape)}")
     dev, dims, args = _scan_args(u, dt, A, B, C, D, z, dt_bias, dt_softplus)
@@ -309,7 +336,7 @@ def ssm_scan_bwd(u, dt, A, B, C, d_out, saved, D=None, z=None, dt_bias=None, dt_
     ws = _workspace(nbytes, u.device)
     out = [_out(res, k) for k in ("du", "ddt", "dz", "dB", "dC", "dA", "dD", "ddt_bias", "d_initial_state")]
     _check(lib.gdn_ssm_bwd(*args, cu, d_out, dfs, saved.data_ptr(), saved.numel(), *out, nseq, T, *dims,
-                           ws.data_ptr(), nbytes, _current(stream, dev)), "gdn_ssm_bwd")
+                           ws.data_ptr(), nbytes, _current(dev)), "gdn_ssm_bwd")
     return res
 
 
@@ -318,6 +345,8 @@ def ssm_scan_step(u, dt, A, B, C, state, D=None, z=None, dt_bias=None, dt_softpl
     """One token per row: u, dt, z (B, D), B, C (B, G, N) and a state cache
     (S, D, N) fp32, updated in place or into out_state; slots as in
     short_conv_step.  Returns out (B, D)."""
+    if stream is not None:
+        return _on_stream(ssm_scan_step, locals())
     if u.dim() != 2:
         raise ValueError(f"u must be (B, D), got shape {tuple(u.shape)}")
     dev, dims, args = _scan_args(u, dt, A, B, C, D, z, dt_bias, dt_softplus)
@@ -325,7 +354,7 @@ def ssm_scan_step(u, dt, A, B, C, state, D=None, z=None, dt_bias=None, dt_softpl
     at, to, sl, S = _state(state, out_state, slots, batch, (width, dims[2]), torch.float32, dev)
     _on_gpu(dev, u)
     out = u.new_empty((batch, width))
-    _check(load().gdn_ssm_step(*args, at, to, sl, out.data_ptr(), batch, S, *dims, _current(stream, dev)), "gdn_ssm_step")
+    _check(load().gdn_ssm_step(*args, at, to, sl, out.data_ptr(), batch, S, *dims, _current(dev)), "gdn_ssm_step")
     return out
 
 
@@ -357,10 +386,12 @@ def group_norm_fwd(x, weight=None, bias=None, gate=None, groups=1, eps=1e-6, act
     x, gate (..., C), weight, bias (C).  center=False is the RMS norm, True
     subtracts the mean.  With a gate: norm(x) act(gate), or norm(x act(gate))
     with gate_first; without one: act(norm(x)).  Returns y (..., C)."""
+    if stream is not None:
+        return _on_stream(group_norm_fwd, locals())
     dev, act, dtype, rows, C, args = _norm_args(x, weight, bias, gate, groups, activation)
     y = x.new_empty(x.shape)
     _check(load().gdn_norm_fwd(*args, y.data_ptr(), rows, C, groups, eps, act, int(center), int(gate_first), dtype,
-                            _current(stream, dev)), "gdn_norm_fwd")
+                            _current(dev)), "gdn_norm_fwd")
     return y
 
 
@@ -368,6 +399,8 @@ def group_norm_bwd(x, d_out, weight=None, bias=None, gate=None, groups=1, eps=1e
                    gate_first=False, stream=None):
     """Gradients of group_norm_fwd: a dict of dx, and dweight, dbias and dgate
     for those that were given."""
+    if stream is not None:
+        return _on_stream(group_norm_bwd, locals())
     dev, act, dtype, rows, C, args = _norm_args(x, weight, bias, gate, groups, activation)
     d_out = _dense("d_out", d_out, x.shape, x.dtype, dev)
     res = {"dx": x.new_empty(x.shape)}
@@ -384,7 +417,7 @@ def group_norm_bwd(x, d_out, weight=None, bias=None, gate=None, groups=1, eps=1e
     ws = _workspace(nbytes, x.device)
     _check(lib.gdn_norm_bwd(*args, d_out, res["dx"].data_ptr(), _out(res, "dgate"), _out(res, "dweight"),
                             _out(res, "dbias"), rows, C, groups, eps, act, int(center), int(gate_first), dtype,
-                            None if ws is None else ws.data_ptr(), nbytes, _current(stream, dev)), "gdn_norm_bwd")
+                            None if ws is None else ws.data_ptr(), nbytes, _current(dev)), "gdn_norm_bwd")
     return res
 
 

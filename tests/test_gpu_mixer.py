@@ -472,6 +472,32 @@ def test_on_another_stream():
     assert torch.equal(out, o2) and torch.equal(fs, f2) and torch.equal(out, o3) and torch.equal(fs, f3)
 
 
+@pytest.mark.parametrize("as_address", [False, True])
+def test_memory_of_another_stream(monkeypatch, as_address):
+    """stream= takes outputs and workspaces from that stream's memory: what the
+    current stream gives back or takes meanwhile is not theirs."""
+    a, t = _scan_inputs((1, 700, 24, 1, 16, None, True, False, True, True), F32)
+    args = (t["u"], t["dt"], t["A"], t["B"], t["C"])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    at = []
+    plain = mixer._workspace
+
+    def workspace(nbytes, device):
+        at.append((nbytes, torch.cuda.current_stream().cuda_stream))
+        return plain(nbytes, device)
+
+    monkeypatch.setattr(mixer, "_workspace", workspace)
+    stream = s.cuda_stream if as_address else s
+    out, fs, saved = mixer.ssm_scan_fwd(*args, save_for_backward=True, stream=stream)
+    grads = mixer.ssm_scan_bwd(*args, out, saved, stream=stream)
+    s.synchronize()
+    assert len(at) == 2 and all(n > 0 and where == s.cuda_stream for n, where in at)
+    owner = [(g["address"], g["address"] + g["total_size"], g["stream"]) for g in torch.cuda.memory_snapshot()]
+    for x in (out, fs, saved, *grads.values()):
+        assert [o for lo, hi, o in owner if lo <= x.data_ptr() < hi] == [s.cuda_stream]
+
+
 # -------------------------------------------------------------- large offsets
 
 def test_offsets_beyond_32_bits():
