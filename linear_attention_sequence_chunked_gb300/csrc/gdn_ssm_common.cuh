@@ -203,7 +203,7 @@ __device__ __forceinline__ void store_states(float* p, int q, const Two (&v)[Lan
     }
 }
 
-// One launch; shared memory beyond 48 KB is asked for once per kernel.
+// One launch; shared memory beyond 48 KB has to be asked for.
 template <int WARPS, typename F>
 cudaError_t launch_warps(F kernel, long long units, int bytes_per_warp, const SsmArgs& a, int blocks, cudaStream_t stream) {
     const int bytes = WARPS * bytes_per_warp;

@@ -83,6 +83,11 @@ def _on_stream(fn, args):
 _current = torch._C._cuda_getCurrentRawStream
 
 
+def _new(x):
+    """A contiguous tensor of x's shape and type (the quickest call that gives one)."""
+    return torch.empty_like(x) if x.is_contiguous() else x.new_empty(x.shape)
+
+
 def _rows(x, width, inner=1):
     """(address, row stride) of an activation whose last `inner` dimensions
     form a dense row of `width` elements and whose rows are evenly spaced."""
@@ -178,7 +183,7 @@ def short_conv_fwd(x, weight, bias=None, activation="silu", initial_state=None, 
     if stream is not None:
         return _on_stream(short_conv_fwd, locals())
     dev, dims, args = _conv_args(x, weight, bias, activation, initial_state, cu_seqlens)
-    y = x.new_empty(x.shape)
+    y = _new(x)
     fs = x.new_empty((dims[0], dims[3] - 1, dims[2])) if output_final_state else None
     _check(load().gdn_conv_fwd(*args, y.data_ptr(), None if fs is None else fs.data_ptr(), *dims, _current(dev)),
            "gdn_conv_fwd")
@@ -195,11 +200,11 @@ def short_conv_bwd(x, weight, d_out, bias=None, activation="silu", initial_state
     N, T, D, W = dims[:4]
     d_out = _dense("d_out", d_out, x.shape, x.dtype, dev)
     dfs = _dense("d_final_state", d_final_state, (N, W - 1, D), x.dtype, dev)
-    res = {"dx": x.new_empty(x.shape), "dweight": weight.new_empty((D, W))}
+    res = {"dx": _new(x), "dweight": torch.empty_like(weight)}
     if bias is not None:
-        res["dbias"] = weight.new_empty((D,))
+        res["dbias"] = torch.empty_like(bias)
     if initial_state is not None:
-        res["d_initial_state"] = x.new_empty((N, W - 1, D))
+        res["d_initial_state"] = torch.empty_like(initial_state)
     lib = load()
     nbytes = lib.gdn_conv_bwd_workspace_size(N, T, D, W, int(cu_seqlens is not None))
     ws = _workspace(nbytes, x.device)
@@ -231,7 +236,7 @@ def short_conv_step(x, state, weight, bias=None, activation="silu", slots=None, 
     b = _dense("bias", bias, (D,), torch.float32, dev)
     at, to, sl, S = _state(state, out_state, slots, B, (W - 1, D), x.dtype, dev)
     _on_gpu(dev, x)
-    y = x.new_empty((B, D))
+    y = _new(x)
     _check(load().gdn_conv_step(*_rows(x, D), w, b, at, to, sl, y.data_ptr(), B, S, D, W, act, dtype,
                              _current(dev)), "gdn_conv_step")
     return y
@@ -287,7 +292,7 @@ def ssm_scan_fwd(u, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=True,
     T, varlen = u.shape[1], int(cu_seqlens is not None)
     h0 = _dense("initial_state", initial_state, (nseq, width, N), torch.float32, dev)
     _on_gpu(dev, u)
-    out = u.new_empty(u.shape)
+    out = _new(u)
     fs = A.new_empty((nseq, width, N)) if output_final_state else None
     lib = load()
     saved, sbytes = None, 0
@@ -321,16 +326,16 @@ def ssm_scan_bwd(u, dt, A, B, C, d_out, saved, D=None, z=None, dt_bias=None, dt_
     if saved.dtype is not torch.uint8 or saved.get_device() != dev or not saved.is_contiguous():
         raise ValueError("saved must be the uint8 buffer that the saving forward returned, on u's device")
     _on_gpu(dev, u)
-    res = {"du": u.new_empty(u.shape), "ddt": u.new_empty(u.shape), "dA": A.new_empty((width, N)),
-           "dB": u.new_empty(B.shape), "dC": u.new_empty(B.shape)}
+    res = {"du": _new(u), "ddt": _new(u), "dA": torch.empty_like(A),
+           "dB": _new(B), "dC": _new(C)}
     if D is not None:
-        res["dD"] = A.new_empty((width,))
+        res["dD"] = torch.empty_like(D)
     if z is not None:
-        res["dz"] = u.new_empty(u.shape)
+        res["dz"] = _new(u)
     if dt_bias is not None:
-        res["ddt_bias"] = A.new_empty((width,))
+        res["ddt_bias"] = torch.empty_like(dt_bias)
     if initial_state is not None:
-        res["d_initial_state"] = A.new_empty((nseq, width, N))
+        res["d_initial_state"] = torch.empty_like(initial_state)
     lib = load()
     nbytes = lib.gdn_ssm_bwd_workspace_size(nseq, T, width, G, N, varlen)
     ws = _workspace(nbytes, u.device)
@@ -353,7 +358,7 @@ def ssm_scan_step(u, dt, A, B, C, state, D=None, z=None, dt_bias=None, dt_softpl
     batch, width = u.shape
     at, to, sl, S = _state(state, out_state, slots, batch, (width, dims[2]), torch.float32, dev)
     _on_gpu(dev, u)
-    out = u.new_empty((batch, width))
+    out = _new(u)
     _check(load().gdn_ssm_step(*args, at, to, sl, out.data_ptr(), batch, S, *dims, _current(dev)), "gdn_ssm_step")
     return out
 
@@ -389,7 +394,7 @@ def group_norm_fwd(x, weight=None, bias=None, gate=None, groups=1, eps=1e-6, act
     if stream is not None:
         return _on_stream(group_norm_fwd, locals())
     dev, act, dtype, rows, C, args = _norm_args(x, weight, bias, gate, groups, activation)
-    y = x.new_empty(x.shape)
+    y = _new(x)
     _check(load().gdn_norm_fwd(*args, y.data_ptr(), rows, C, groups, eps, act, int(center), int(gate_first), dtype,
                             _current(dev)), "gdn_norm_fwd")
     return y
@@ -403,13 +408,13 @@ def group_norm_bwd(x, d_out, weight=None, bias=None, gate=None, groups=1, eps=1e
         return _on_stream(group_norm_bwd, locals())
     dev, act, dtype, rows, C, args = _norm_args(x, weight, bias, gate, groups, activation)
     d_out = _dense("d_out", d_out, x.shape, x.dtype, dev)
-    res = {"dx": x.new_empty(x.shape)}
+    res = {"dx": _new(x)}
     if gate is not None:
-        res["dgate"] = x.new_empty(x.shape)
+        res["dgate"] = _new(x)
     if weight is not None:
-        res["dweight"] = weight.new_empty((C,))
+        res["dweight"] = torch.empty_like(weight)
     if bias is not None:
-        res["dbias"] = bias.new_empty((C,))
+        res["dbias"] = torch.empty_like(bias)
     lib = load()
     nbytes = 0
     if weight is not None or bias is not None:
