@@ -1,6 +1,9 @@
 // Selective state space scan: forward, and the single-token step for decode.
 // The layout is described in gdn_ssm_common.cuh; gdn_ssm_bwd.cu holds the
 // reverse mode.
+#include <algorithm>
+#include <cmath>
+
 #include "gdn_ssm_common.cuh"
 
 namespace gdn {
@@ -20,7 +23,7 @@ struct alignas(16) FwdStage {
 };
 template <typename T, int N, bool kOut>
 struct alignas(16) FwdShared {
-    FwdStage<T, N, kOut> stage[kStages<N>];
+    FwdStage<T, N, kOut> stage[kStages];
     float B[kTile][N];
     float C[kOut ? kTile : 0][N];
     // dt and x = dt u, where several lanes share a channel
@@ -82,7 +85,7 @@ __global__ void __launch_bounds__(32 * kWarps, 3) ssm_fwd_kernel(const SsmArgs p
     const int len = w.s1 - w.s0;
     auto fetch = [&](int t) {  // the tile at token t, if there is one
         if (t < len) {
-            FwdStage<T, N, kOut>& st = sm.stage[t / kTile % kStages<N>];
+            FwdStage<T, N, kOut>& st = sm.stage[t / kTile % kStages];
             fill_tile<T, CH, PB>(&st.u[0][0], u + t * p.u_stride, p.u_stride, len - t, w.nd, lane);
             fill_tile<T, CH, PB>(&st.dt[0][0], dt + t * p.dt_stride, p.dt_stride, len - t, w.nd, lane);
             fill_tile<T, N, PB>(&st.B[0][0], Bm + t * p.B_stride, p.B_stride, len - t, N, lane);
@@ -94,13 +97,13 @@ __global__ void __launch_bounds__(32 * kWarps, 3) ssm_fwd_kernel(const SsmArgs p
         commit_copies();
     };
 #pragma unroll
-    for (int i = 0; i < kStages<N> - 1; ++i) fetch(i * kTile);
+    for (int i = 0; i < kStages - 1; ++i) fetch(i * kTile);
     for (int t = 0; t < len; t += kTile) {
         if (kOut && p.saved && mine) store_states<N>(p.saved + ((w.chunk0 + t / kTile) * p.D + d) * N, q, h);
-        wait_copies<kStages<N> - 2>();
+        wait_copies<kStages - 2>();
         __syncwarp();  // the tile is there, and everyone is through with the one before
-        fetch(t + (kStages<N> - 1) * kTile);
-        const FwdStage<T, N, kOut>& st = sm.stage[t / kTile % kStages<N>];
+        fetch(t + (kStages - 1) * kTile);
+        const FwdStage<T, N, kOut>& st = sm.stage[t / kTile % kStages];
         widen_rows<T, N>(&st.B[0][0], &sm.B[0][0], lane);
         if constexpr (kOut) widen_rows<T, N>(&st.C[0][0], &sm.C[0][0], lane);
         const int left = len - t;
@@ -395,18 +398,46 @@ cudaError_t step_n(const SsmStepArgs& a, cudaStream_t stream) {
     }                                     \
     GDN_SSM_N(fn, float)
 
-// Segments: as many as give one wave of twelve warps per SM, none where the
-// channels alone fill the GPU.  Splitting costs a second pass (0.7 of the forward,
-// 0.2 of the reverse mode), so the forward stays whole from 456 warps (512 warps:
-// 266 us whole, 269 us in segments of the same work), the reverse mode from 1000
-// (512 warps: 1479 us whole, 978 us in segments).
+// Segments of 16 tokens or more, none where the channels alone fill the GPU or
+// the sequence is short; of 64 tokens at least, 1 x 256 x 2048 took 20 us and 70
+// us in reverse, of 16 it takes 14 us and 41 us.
+// Forward: as many as give one wave of twelve warps per SM.  Splitting costs a
+// second pass, 0.7 of the first, so it stays whole from 456 warps (512 warps: 266
+// us whole, 269 us in segments of the same work) and below 64 tokens (1 x 64 x
+// 2048: 9.8 us split, 10.8 whole; 32 tokens: 9.0 and 6.8), 96 of packed sequences,
+// which are shorter.
+// Reverse mode: a second pass costs 0.2, and the time of n warps is about that of
+// their whole waves and f^0.4 of one for the part f of a wave that is left (512
+// warps: 1479 us whole, 967 in three segments each, 834 in seven).  Whole below
+// 24 tokens (32 tokens: 29 us split, 35 whole).
 int ssm_segment(int nseq, int T, int D, int G, int N, bool varlen, bool backward) {
     const int ch = N <= 16 ? 32 : 512 / N;
     const long long warps = static_cast<long long>(varlen ? 1 : nseq) * G * ((D / G + ch - 1) / ch);
-    if (warps >= (backward ? 1000 : 456) || T < 256) return 1 << 30;
-    const long long segs = 152 * 12 / warps;
-    const int seg = static_cast<int>(((T + segs - 1) / segs + kSsmChunk - 1) / kSsmChunk * kSsmChunk);
-    return seg < 64 ? 64 : seg;
+    const int whole = 1 << 30;
+    auto tokens = [&](long long segs) {  // of each of `segs` segments
+        return std::max(16, static_cast<int>(((T + segs - 1) / segs + kSsmChunk - 1) / kSsmChunk * kSsmChunk));
+    };
+    if (!backward) return warps >= 456 || T < (varlen ? 96 : 64) ? whole : tokens(152 * 12 / warps);
+    if (T < 24) return whole;
+    const double wave = 152. * (N <= 16 ? 12 : N == 32 ? 10 : N == 64 ? 8 : 6);  // by shared memory
+    auto cost = [&](long long n) {  // per unit of work
+        const double w = n * warps / wave, f = w - std::floor(w);
+        return (std::floor(w) + std::pow(f, 0.4)) / w;
+    };
+    double best = cost(1);
+    int seg = whole;
+    for (int k = 1; k <= 4; ++k) {  // as many segments as k waves hold
+        const long long n = static_cast<long long>(k * wave / warps);
+        if (n < 2) continue;
+        const int len = tokens(n);
+        const long long segs = (T + len - 1) / len;
+        const double c = 1.2 * cost(segs) + 0.0015 * segs;  // and what joins them
+        if (segs > 1 && c < best) {
+            best = c;
+            seg = len;
+        }
+    }
+    return seg;
 }
 
 cudaError_t launch_ssm_compose(const SsmArgs& a, bool reverse, cudaStream_t stream) {

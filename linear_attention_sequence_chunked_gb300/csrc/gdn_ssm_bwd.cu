@@ -51,11 +51,11 @@ __device__ __forceinline__ void across_channels(float (&v)[8], int ch) {
 // registers of twelve warps per SM, those of eight only those of eight warps.
 constexpr int kHalf = kTile / 2;
 
-// Warps per block: from N = 64 on shared memory holds fewer than twelve warps per
-// SM, and more of them in smaller blocks (1 x 2048 x 1024, N = 128: 612 us by two
-// warps, 657 by four, 646 by one; N = 64: 278, 280, 321).
+// Warps per block: from N = 32 on shared memory holds fewer than twelve warps per
+// SM, and more of them in smaller blocks (1 x 2048 x 1024, N = 32: 150 us by two
+// warps, 189 by four; N = 128: 612 and 657, 646 by one).
 template <int N>
-constexpr int kBwdWarps = N >= 64 ? 2 : 4;
+constexpr int kBwdWarps = N >= 32 ? 2 : 4;
 
 // kFull: the whole reverse mode.  Without it, only the state gradient that a
 // segment sends to the one before it, from a zero one at its end, and the sum

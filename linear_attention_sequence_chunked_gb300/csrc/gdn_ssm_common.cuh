@@ -26,10 +26,10 @@ using namespace mix;
 
 constexpr int kWarps = 4;
 constexpr int kTile = kSsmChunk;  // tokens worked on at a time
-// Tiles of the forward in shared memory or on their way to it: two where a third
-// would leave room for eight warps per SM only.
-template <int N>
-constexpr int kStages = N >= 64 ? 2 : 3;
+// Tiles of the forward in shared memory or on their way to it.  A third gains
+// nothing (4 x 4096 x 2048: 263 us against 260) and from N = 128 on would leave
+// room for eight warps per SM only (1 x 2048 x 1024: 224 us against 175).
+constexpr int kStages = 2;
 
 // Where a warp works: segment `slot` of the tokens, one block of CH channels.
 struct Place {
