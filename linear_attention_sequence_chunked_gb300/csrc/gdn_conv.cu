@@ -429,7 +429,9 @@ cudaError_t conv_fwd_e(const ConvArgs& a, cudaStream_t stream) {
 
 // Four channels per thread where a row's width, stride and address allow it,
 // else two (bf16), else one: neighbouring threads then still read neighbouring
-// elements.
+// elements (4 x 4096 x 6144 forward: 68 us by four, 78 by two; 16384 x 2048
+// reverse: 57 by four, 66 by two, 99 by one; 1024 x 6142 step: 17 by two, 27 by
+// one).
 template <typename T, int W>
 cudaError_t conv_fwd_w(const ConvArgs& a, cudaStream_t stream) {
     constexpr int E = 4;
@@ -448,7 +450,10 @@ cudaError_t conv_bwd_e(const ConvArgs& a, cudaStream_t stream) {
 }
 template <typename T, int W>
 cudaError_t conv_bwd_w(const ConvArgs& a, cudaStream_t stream) {
-    return rows_take<T>(a.x, a.x_stride, a.D, 4) ? conv_bwd_e<T, W, 4>(a, stream) : conv_bwd_e<T, W, 1>(a, stream);
+    if (rows_take<T>(a.x, a.x_stride, a.D, 4)) return conv_bwd_e<T, W, 4>(a, stream);
+    if constexpr (sizeof(T) == 2)
+        if (rows_take<T>(a.x, a.x_stride, a.D, 2)) return conv_bwd_e<T, W, 2>(a, stream);
+    return conv_bwd_e<T, W, 1>(a, stream);
 }
 
 template <typename T, int W, int E>
@@ -459,15 +464,18 @@ cudaError_t conv_step_e(const ConvStepArgs& a, cudaStream_t stream) {
 }
 template <typename T, int W>
 cudaError_t conv_step_w(const ConvStepArgs& a, cudaStream_t stream) {
-    return rows_take<T>(a.x, a.x_stride, a.D, 4) ? conv_step_e<T, W, 4>(a, stream) : conv_step_e<T, W, 1>(a, stream);
+    if (rows_take<T>(a.x, a.x_stride, a.D, 4)) return conv_step_e<T, W, 4>(a, stream);
+    if constexpr (sizeof(T) == 2)
+        if (rows_take<T>(a.x, a.x_stride, a.D, 2)) return conv_step_e<T, W, 2>(a, stream);
+    return conv_step_e<T, W, 1>(a, stream);
 }
 
 }  // namespace
 
 // Tokens per thread: long blocks re-read fewer rows at their edges (W-1 per
 // block) and leave fewer partial rows, short ones give small inputs enough
-// threads (16384 x 2048 backward: 128 tokens and 64 K threads 83 us, 32 tokens
-// 88 us; 16384 x 6144 forward: 64 tokens 77 us, 128 tokens 80 us).
+// threads (16384 x 2048 backward: 128 tokens 57 us, 64 tokens 59 us; 16384 x
+// 6144 forward: 64 tokens 68 us, 32 tokens 70 us, 128 tokens 68 us).
 int conv_block_tokens(int B, int T, int D, int backward) {
     const long long work = static_cast<long long>(B) * T * ((D + 3) / 4);
     int tb = backward ? 128 : 64;

@@ -138,6 +138,30 @@ def test_conv_steps_continue_a_prompt(dtype, D, W, strided):
     assert np.array_equal(_np(state), fs_want)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("D", [2, 70])
+def test_conv_of_even_widths(dtype, D):
+    """Widths that two channels per thread fit and four do not: the prompt, its
+    gradients, and steps through slots."""
+    rng = np.random.default_rng(D)
+    T, W, S = 45, 4, 6
+    x, dy = (_round(rng.standard_normal((2, T, D)), dtype) for _ in range(2))
+    w, b = _round(rng.uniform(-0.6, 0.6, (D, W)), F32), _round(rng.uniform(-0.2, 0.2, D), F32)
+    want, fs_want = M.conv_fwd(x, w, b)
+    grads = M.conv_bwd(x, w, dy, b)
+    got = mixer.short_conv_bwd(_dev(x, dtype), _dev(w), _dev(dy, dtype), _dev(b))
+    _close(got["dx"], grads["dx"], _io_tol(dtype, TOL_F32), "dx")
+    for k in ("dweight", "dbias"):
+        _close(got[k], grads[k], TOL_PAR, k)
+    cache = torch.zeros(S, W - 1, D, dtype=dtype, device="cuda")
+    slots = torch.tensor([4, 1], dtype=torch.int32, device="cuda")
+    for t in range(T):
+        y = mixer.short_conv_step(_dev(x[:, t], dtype), cache, _dev(w), _dev(b), slots=slots)
+        _close(y, want[:, t], _io_tol(dtype, TOL_F32), f"step {t}")
+    assert np.array_equal(_np(cache)[[4, 1]], fs_want)
+    assert not _np(cache)[[0, 2, 3, 5]].any()
+
+
 # ------------------------------------------------------------------------ scan
 
 SCAN = [  # B, T, D, G, N, cu, initial state, strided, gated, softplus
