@@ -398,9 +398,11 @@ cudaError_t step_n(const SsmStepArgs& a, cudaStream_t stream) {
     }                                     \
     GDN_SSM_N(fn, float)
 
-// Segments of 16 tokens or more, none where the channels alone fill the GPU or
-// the sequence is short; of 64 tokens at least, 1 x 256 x 2048 took 20 us and 70
-// us in reverse, of 16 it takes 14 us and 41 us.
+// Segments, none where the channels alone fill the GPU or the sequence is short.
+// At least 16 tokens each, and sqrt(T) in the forward of one sequence, half that
+// otherwise: what joins a segment to those before it grows with their number
+// (16384 x 64: 49 us, 103 us with 16 tokens each; reverse mode 97 and 134 us; 256
+// x 2048: 14 and 41 us, 20 and 70 us with 64 each).
 // Forward: as many as give one wave of twelve warps per SM.  Splitting costs a
 // second pass, 0.7 of the first, so it stays whole from 456 warps (512 warps: 266
 // us whole, 269 us in segments of the same work) and below 64 tokens (1 x 64 x
@@ -415,7 +417,9 @@ int ssm_segment(int nseq, int T, int D, int G, int N, bool varlen, bool backward
     const long long warps = static_cast<long long>(varlen ? 1 : nseq) * G * ((D / G + ch - 1) / ch);
     const int whole = 1 << 30;
     auto tokens = [&](long long segs) {  // of each of `segs` segments
-        return std::max(16, static_cast<int>(((T + segs - 1) / segs + kSsmChunk - 1) / kSsmChunk * kSsmChunk));
+        const long long least = static_cast<long long>((backward || varlen ? 0.5 : 1.) * std::sqrt(static_cast<double>(T)));
+        const long long len = std::max((T + segs - 1) / segs, least);
+        return std::max(16, static_cast<int>((len + kSsmChunk - 1) / kSsmChunk * kSsmChunk));
     };
     if (!backward) return warps >= 456 || T < (varlen ? 96 : 64) ? whole : tokens(152 * 12 / warps);
     if (T < 24) return whole;
