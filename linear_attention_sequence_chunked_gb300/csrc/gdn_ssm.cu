@@ -31,7 +31,9 @@ struct alignas(16) FwdShared {
 };
 
 // kOut: the whole forward.  Without it, only the segment's end state from a
-// zero start and the sum of its dt (the first pass of a split scan).
+// zero start and the sum of its dt (the first pass of a split scan).  Twelve
+// warps per SM of 168 registers: 4 x 4096 x 2048 took 275 us, sixteen of 128
+// registers 300, twenty of 96 329.
 template <typename T, int N, bool kOut, int PB>
 __global__ void __launch_bounds__(32 * kWarps, 3) ssm_fwd_kernel(const SsmArgs p, int blocks) {
     using L = Lanes<N>;
@@ -220,7 +222,8 @@ __global__ void __launch_bounds__(32 * kWarps, 3) ssm_fwd_kernel(const SsmArgs p
 
 // One token: lane q of a channel updates four of its states where they lie, for
 // R batch rows whose states are all on their way together.  Bound by HBM: the
-// state is read and written once.
+// state is read and written once (256 x 2048, N = 16: 16 us, 4.4 TB/s; what is
+// left is the start and end of one wave of short threads).
 template <typename T, int N, int R, bool VEC>
 __global__ void __launch_bounds__(256) ssm_step_kernel(const SsmStepArgs p) {
     constexpr int LPC = N / 4;
@@ -411,12 +414,15 @@ cudaError_t step_n(const SsmStepArgs& a, cudaStream_t stream) {
 // Reverse mode: a second pass costs 0.2, and the time of n warps is about that of
 // their whole waves and f^0.4 of one for the part f of a wave that is left (512
 // warps: 1479 us whole, 967 in three segments each, 834 in seven).  Whole below
-// 24 tokens (32 tokens: 29 us split, 35 whole).
+// 24 tokens (32 tokens: 29 us split, 35 whole).  Packed sequences end inside a
+// segment, half of one too many each (1 x 16384 x 2048, 12 sequences: 908 us so,
+// 1065 without; the forward loses by it, 331 and 303 us).
 int ssm_segment(int nseq, int T, int D, int G, int N, bool varlen, bool backward) {
     const int ch = N <= 16 ? 32 : 512 / N;
     const long long warps = static_cast<long long>(varlen ? 1 : nseq) * G * ((D / G + ch - 1) / ch);
     const int whole = 1 << 30;
     auto tokens = [&](long long segs) {  // of each of `segs` segments
+        if (backward && varlen) segs = std::max(segs - nseq / 2, 1LL);  // sequences end inside one
         const long long least = static_cast<long long>((backward || varlen ? 0.5 : 1.) * std::sqrt(static_cast<double>(T)));
         const long long len = std::max((T + segs - 1) / segs, least);
         return std::max(16, static_cast<int>((len + kSsmChunk - 1) / kSsmChunk * kSsmChunk));
