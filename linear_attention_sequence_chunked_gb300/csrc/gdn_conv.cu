@@ -479,11 +479,17 @@ cudaError_t conv_step_w(const ConvStepArgs& a, cudaStream_t stream) {
 // Tokens per thread: long blocks re-read fewer rows at their edges (W-1 per
 // block) and leave fewer partial rows, short ones give small inputs enough
 // threads (16384 x 2048 backward: 128 tokens 57 us, 64 tokens 59 us; 16384 x
-// 6144 forward: 64 tokens 68 us, 32 tokens 70 us, 128 tokens 68 us).
-int conv_block_tokens(int B, int T, int D, int backward) {
-    const long long work = static_cast<long long>(B) * T * ((D + 3) / 4);
+// 6144 forward: 64 tokens 68 us, 32 tokens 70 us).  How many are enough: in
+// reverse 60 thousand (4 x 1024 x 4096 fp32 34 us, 41 with half, 38 with twice as
+// many), forward 50 thousand (2048 x 6144 bf16 11.4 us, 14.6 with 200), 200 where
+// a thread's items of 16 bytes leave room for one batch ahead only (4 x 1024 x
+// 4096 fp32 23.5 us, 25.3 with 50).
+int conv_block_tokens(int B, int T, int D, int backward, int dtype) {
+    const int channels = D % 4 == 0 ? 4 : D % 2 == 0 ? 2 : 1;  // of a thread, if it is aligned
+    const long long work = static_cast<long long>(B) * T * (D / channels);
+    const long long enough = backward ? 60000 : dtype == 1 && channels == 4 ? 200000 : 50000;
     int tb = backward ? 128 : 64;
-    while (tb > 4 && work / tb < (backward ? 60000 : 200000)) tb /= 2;
+    while (tb > 4 && work / tb < enough) tb /= 2;
     return tb;
 }
 

@@ -356,7 +356,7 @@ struct ConvStepArgs {
     int B, S, D, W, activation, dtype;
     int* err;
 };
-int conv_block_tokens(int B, int T, int D, int backward);
+int conv_block_tokens(int B, int T, int D, int backward, int dtype);  // dtype: forward only
 long long conv_partial_rows(long long slots);
 cudaError_t launch_conv_fwd(const ConvArgs& a, cudaStream_t stream);
 cudaError_t launch_conv_bwd(const ConvArgs& a, cudaStream_t stream);

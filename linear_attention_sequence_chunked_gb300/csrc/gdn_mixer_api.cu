@@ -75,7 +75,7 @@ long long block_slots(int B, int T, int tb, bool varlen) {
 
 size_t conv_ws(int B, int T, int D, int W, bool varlen) {
     // packed: T tokens in all
-    const long long slots = block_slots(B, T, gdn::conv_block_tokens(varlen ? 1 : B, T, D, 1), varlen);
+    const long long slots = block_slots(B, T, gdn::conv_block_tokens(varlen ? 1 : B, T, D, 1, 0), varlen);
     return round_up(sizeof(float) * gdn::conv_partial_rows(slots) * (W + 1) * D);
 }
 
@@ -166,7 +166,7 @@ gdn_status gdn_conv_fwd(const void* x, int64_t x_stride, const float* weight, co
     a.x = x; a.x_stride = x_stride; a.weight = weight; a.bias = bias; a.initial_state = initial_state;
     a.cu_seqlens = cu_seqlens; a.y = y; a.final_state = final_state;
     a.N = B; a.T = T; a.D = D; a.W = W; a.activation = activation; a.dtype = dtype; a.err = err;
-    a.tb = gdn::conv_block_tokens(cu_seqlens ? 1 : B, T, D, 0);
+    a.tb = gdn::conv_block_tokens(cu_seqlens ? 1 : B, T, D, 0, dtype);
     a.slots = block_slots(B, T, a.tb, cu_seqlens != nullptr);
     return gdn::count_launch(gdn::launch_conv_fwd(a, stream)) ? GDN_OK : GDN_ERR_CUDA;
 }
@@ -194,7 +194,7 @@ gdn_status gdn_conv_bwd(const void* x, int64_t x_stride, const float* weight, co
     a.cu_seqlens = cu_seqlens; a.d_out = d_out; a.d_final_state = d_final_state; a.dx = dx;
     a.d_initial_state = d_initial_state; a.partial = static_cast<float*>(workspace);
     a.N = B; a.T = T; a.D = D; a.W = W; a.activation = activation; a.dtype = dtype; a.err = err;
-    a.tb = gdn::conv_block_tokens(cu_seqlens ? 1 : B, T, D, 1);
+    a.tb = gdn::conv_block_tokens(cu_seqlens ? 1 : B, T, D, 1, 0);
     a.slots = block_slots(B, T, a.tb, cu_seqlens != nullptr);
     if (!gdn::count_launch(gdn::launch_conv_bwd(a, stream))) return GDN_ERR_CUDA;
     gdn::ColumnSumArgs c{};
