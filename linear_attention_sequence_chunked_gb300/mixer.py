@@ -184,7 +184,9 @@ def short_conv_fwd(x, weight, bias=None, activation="silu", initial_state=None, 
         return _on_stream(short_conv_fwd, locals())
     dev, dims, args = _conv_args(x, weight, bias, activation, initial_state, cu_seqlens)
     y = _new(x)
-    fs = x.new_empty((dims[0], dims[3] - 1, dims[2])) if output_final_state else None
+    fs = None
+    if output_final_state:
+        fs = x.new_empty((dims[0], dims[3] - 1, dims[2])) if initial_state is None else torch.empty_like(initial_state)
     _check(load().gdn_conv_fwd(*args, y.data_ptr(), None if fs is None else fs.data_ptr(), *dims, _current(dev)),
            "gdn_conv_fwd")
     return y, fs
@@ -293,7 +295,9 @@ def ssm_scan_fwd(u, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=True,
     h0 = _dense("initial_state", initial_state, (nseq, width, N), torch.float32, dev)
     _on_gpu(dev, u)
     out = _new(u)
-    fs = A.new_empty((nseq, width, N)) if output_final_state else None
+    fs = None
+    if output_final_state:
+        fs = A.new_empty((nseq, width, N)) if initial_state is None else torch.empty_like(initial_state)
     lib = load()
     saved, sbytes = None, 0
     if save_for_backward:
