@@ -7,7 +7,8 @@ the CUDA kernels of ``_build/libgdn.so`` (include/gdn.h has the formulas and
 layouts), without a CPU fallback.  ``*_fwd`` / ``*_bwd`` / ``*_step`` allocate
 their outputs and workspaces with torch; short_conv, ssm_scan and group_norm
 are the same forwards and backwards behind torch.autograd.  The former also
-take `stream=`, in place of the current stream.
+take `stream=`, in place of the current stream; as with any stream, the caller
+has it wait for what produces the inputs.
 
 Activations are channels last and bf16 or fp32, one type per call; parameters
 and the states of the scan are fp32.  The activation inputs x, gate, u, dt, z,
@@ -66,12 +67,16 @@ def _on_gpu(dev, x):
 def _on_stream(fn, args):
     """fn with its arguments, `stream` among them (a torch.cuda.Stream or its
     address), on that stream.  Outputs and workspaces are taken from that
-    stream's memory, and outputs stay until the work that the caller's stream
-    has for them is done."""
+    stream's memory; outputs stay until the work that the caller's stream has
+    for them is done, and inputs, which a caller may drop when the call returns,
+    until this stream is through with them."""
     stream = args.pop("stream")
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
-    caller = torch.cuda.current_stream()
+    caller = torch.cuda.current_stream(stream.device)
+    for t in args.values():
+        if isinstance(t, torch.Tensor) and t.is_cuda:
+            t.record_stream(stream)
     with torch.cuda.stream(stream):
         out = fn(**args)
     for t in out.values() if isinstance(out, dict) else out if isinstance(out, tuple) else (out,):
