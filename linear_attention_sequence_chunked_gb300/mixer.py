@@ -8,7 +8,7 @@ layouts), without a CPU fallback.  ``*_fwd`` / ``*_bwd`` / ``*_step`` allocate
 their outputs and workspaces with torch; short_conv, ssm_scan and group_norm
 are the same forwards and backwards behind torch.autograd.  The former also
 take `stream=`, in place of the current stream; as with any stream, the caller
-has it wait for what produces the inputs.
+has it wait for what produces the inputs.  All tensors are on the current device.
 
 Activations are channels last and bf16 or fp32, one type per call; parameters
 and the states of the scan are fp32.  The activation inputs x, gate, u, dt, z,
@@ -59,9 +59,16 @@ def _dense(name, t, shape, dtype, dev):
     return t.data_ptr()
 
 
+_device = torch._C._cuda_getDevice
+
+
 def _on_gpu(dev, x):
+    """The library launches on the current device: a tensor of another one is refused."""
     if dev < 0:
         raise ValueError(f"expected a CUDA tensor, got one on {x.device}")
+    if dev != _device():
+        raise ValueError(f"the tensors are on cuda:{dev}, the current device is cuda:{_device()}: "
+                         "call under torch.cuda.device")
 
 
 def _on_stream(fn, args):

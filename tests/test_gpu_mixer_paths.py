@@ -27,3 +27,19 @@ def test_an_input_dropped_during_a_call_on_another_stream():
     assert not s.query() and new.data_ptr() != at
     s.synchronize()
     assert torch.equal(y, want)
+
+
+def test_every_call_refuses_another_device(monkeypatch):
+    """With device 1 said to be current, nothing on device 0 is launched."""
+    x, w, h = torch.ones(2, 8, 16, device="cuda"), torch.ones(16, 4, device="cuda"), torch.ones(2, 3, 16, device="cuda")
+    A, B = -torch.ones(16, 8, device="cuda"), torch.ones(2, 8, 1, 8, device="cuda")
+    state = torch.ones(2, 16, 8, device="cuda")
+    _, _, saved = mixer.ssm_scan_fwd(x, x, A, B, B, save_for_backward=True)
+    monkeypatch.setattr(mixer, "_device", lambda: 1)
+    for call in (lambda: mixer.short_conv_fwd(x, w), lambda: mixer.short_conv_bwd(x, w, x),
+                 lambda: mixer.short_conv_step(x[:, 0], h, w),
+                 lambda: mixer.ssm_scan_fwd(x, x, A, B, B), lambda: mixer.ssm_scan_bwd(x, x, A, B, B, x, saved),
+                 lambda: mixer.ssm_scan_step(x[:, 0], x[:, 0], A, B[:, 0], B[:, 0], state),
+                 lambda: mixer.group_norm_fwd(x), lambda: mixer.group_norm_bwd(x, x)):
+        with pytest.raises(ValueError, match="current device is cuda:1"):
+            call()

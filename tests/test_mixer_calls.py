@@ -43,3 +43,11 @@ def test_tensors_of_a_call_on_another_stream_are_recorded(monkeypatch, kind):
 
     assert mixer._on_stream(call, dict(ins, stream=stream)) is made
     assert outs[0].streams == [("caller", stream.device)]
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    x = torch.zeros(2, 4)
+    monkeypatch.setattr(mixer, "_device", lambda: 0, raising=False)
+    mixer._on_gpu(0, x)
+    with pytest.raises(ValueError, match="tensors are on cuda:1, the current device is cuda:0"):
+        mixer._on_gpu(1, x)
