@@ -147,11 +147,17 @@ def load():
         return lib
 
 
+def _device():
+    """The current device, on which the library launches."""
+    import torch
+    return torch._C._cuda_getDevice()
+
+
 def _ptr(x):
     """Device address of a tensor argument (None and raw integer addresses
-    pass through).  The kernels read every tensor as dense row-major device
-    memory, so a strided view or a host tensor is refused here, before any
-    call into the library."""
+    pass through).  The kernels read every tensor as dense row-major memory of
+    the current device, so a strided view, a host tensor or one of another
+    device is refused here, before any call into the library."""
     if x is None:
         return None
     if isinstance(x, int):
@@ -160,6 +166,9 @@ def _ptr(x):
         raise ValueError(f"expected a contiguous tensor, got shape {tuple(x.shape)} strides {x.stride()}")
     if x.device.type != "cuda":
         raise ValueError(f"expected a CUDA tensor, got one on {x.device}")
+    if x.get_device() != _device():
+        raise ValueError(f"a tensor is on {x.device}, the current device is cuda:{_device()}: "
+                         "call under torch.cuda.device")
     return x.data_ptr()
 
 
