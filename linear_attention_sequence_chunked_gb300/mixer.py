@@ -6,7 +6,8 @@ As in gdn.py, nothing is computed here: arguments are checked and handed to
 the CUDA kernels of ``_build/libgdn.so`` (include/gdn.h has the formulas and
 layouts), without a CPU fallback.  ``*_fwd`` / ``*_bwd`` / ``*_step`` allocate
 their outputs and workspaces with torch; short_conv, ssm_scan and group_norm
-are the same forwards and backwards behind torch.autograd.  The former also
+are the same forwards and backwards behind torch.autograd (first derivatives
+only: a second one raises).  The former also
 take `stream=`, in place of the current stream; as with any stream, the caller
 has it wait for what produces the inputs.  All tensors are on the current device.
 
@@ -20,6 +21,7 @@ from __future__ import annotations
 
 import torch
 
+from ._first_order import first_order
 from .gdn import _check, _workspace, load
 
 _ACTIVATIONS = {None: 0, "none": 0, "silu": 1, "sigmoid": 2}
@@ -466,6 +468,7 @@ def _functions():
             return y, fs
 
         @staticmethod
+        @first_order
         def backward(ctx, d_out, d_fs):
             x, weight, bias, initial_state, cu_seqlens = ctx.saved_tensors
             d_out = torch.zeros(x.shape, dtype=x.dtype, device=x.device) if d_out is None else dense(d_out, x)
@@ -484,6 +487,7 @@ def _functions():
             return out, fs
 
         @staticmethod
+        @first_order
         def backward(ctx, d_out, d_fs):
             u, dt, A, B, C, D, z, dt_bias, initial_state, cu_seqlens, saved = ctx.saved_tensors
             d_out = torch.zeros(u.shape, dtype=u.dtype, device=u.device) if d_out is None else dense(d_out, u)
@@ -501,6 +505,7 @@ def _functions():
             return group_norm_fwd(x, weight, bias, gate, *ctx.rest)
 
         @staticmethod
+        @first_order
         def backward(ctx, d_out):
             x, weight, bias, gate = ctx.saved_tensors
             r = group_norm_bwd(x, dense(d_out, x), weight, bias, gate, *ctx.rest)

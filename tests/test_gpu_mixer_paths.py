@@ -43,3 +43,15 @@ def test_every_call_refuses_another_device(monkeypatch):
                  lambda: mixer.group_norm_fwd(x), lambda: mixer.group_norm_bwd(x, x)):
         with pytest.raises(ValueError, match="current device is cuda:1"):
             call()
+
+
+def test_second_derivatives_are_refused():
+    x = torch.randn(2, 8, 16, device="cuda", requires_grad=True)
+    w, A = torch.randn(16, 4, device="cuda"), -torch.ones(16, 8, device="cuda")
+    B = torch.randn(2, 8, 1, 8, device="cuda")
+    for f in (lambda: mixer.short_conv(x, w)[0], lambda: mixer.ssm_scan(x, x, A, B, B)[0], lambda: mixer.group_norm(x)):
+        g, = torch.autograd.grad(f().sum(), x, create_graph=True)
+        plain, = torch.autograd.grad(f().sum(), x)
+        assert torch.equal(g, plain)
+        with pytest.raises(RuntimeError, match="cannot be differentiated again"):
+            (g.sum() + (x ** 3).sum()).backward()

@@ -51,3 +51,46 @@ def test_tensors_of_another_device_are_refused(monkeypatch):
     mixer._on_gpu(0, x)
     with pytest.raises(ValueError, match="tensors are on cuda:1, the current device is cuda:0"):
         mixer._on_gpu(1, x)
+
+
+def _square(x):
+    """Its gradient 2 x d_out depends on x where d_out is a constant too."""
+    return x * x
+
+
+OPERATORS = {  # the operator as autograd sees it, and x^2 and 2 x d_out in its kernels' place
+    "conv": (lambda x, w: mixer.short_conv(x, w)[0], "short_conv", lambda x, *a, **k: (_square(x), x[:, -3:].clone()),
+             lambda x, w, d, *a, **k: dict(dx=2 * x * d, dweight=torch.zeros_like(w))),
+    "scan": (lambda x, w: mixer.ssm_scan(x, x.detach(), w, x.detach(), x.detach())[0], "ssm_scan",
+             lambda u, *a, **k: (_square(u), u.sum(1), u.new_zeros(4)),
+             lambda u, dt, A, B, C, d, *a, **k: dict(du=2 * u * d, ddt=0 * u, dA=0 * A, dB=0 * B, dC=0 * C)),
+    "norm": (lambda x, w: mixer.group_norm(x, w), "group_norm", lambda x, *a, **k: _square(x),
+             lambda x, d, w, *a, **k: dict(dx=2 * x * d, dweight=torch.zeros_like(w))),
+}
+
+
+@pytest.mark.parametrize("name", list(OPERATORS))
+def test_second_derivatives_are_refused(monkeypatch, name):
+    """Where another path to the same input has a second derivative, only that
+    one would come back."""
+    f, prefix, fwd, bwd = OPERATORS[name]
+    monkeypatch.setattr(mixer, prefix + "_fwd", fwd)
+    monkeypatch.setattr(mixer, prefix + "_bwd", bwd)
+    x, w = torch.randn(2, 5, 4, requires_grad=True), torch.randn(4, 4, requires_grad=True)
+    g, gw = torch.autograd.grad(f(x, w).sum(), (x, w), create_graph=True)
+    assert torch.equal(g, 2 * x) and not gw.any()
+    with pytest.raises(RuntimeError, match="cannot be differentiated again"):
+        (g.sum() + (x ** 3).sum()).backward()
+    f(x, w).sum().backward()  # the first derivative, as before
+    assert torch.equal(x.grad, 2 * x)
+
+
+def test_gradients_of_constants_can_be_used_in_a_graph(monkeypatch):
+    """What does not reach the operator again is not refused."""
+    f, prefix, fwd, bwd = OPERATORS["norm"]
+    monkeypatch.setattr(mixer, prefix + "_fwd", fwd)
+    monkeypatch.setattr(mixer, prefix + "_bwd", bwd)
+    x, s = torch.randn(2, 5, 4, requires_grad=True), torch.tensor(3.0, requires_grad=True)
+    g, = torch.autograd.grad(f(x, torch.ones(4)).sum(), x, create_graph=True)
+    (s * g.detach()).sum().backward()
+    assert torch.allclose(s.grad, (2 * x).sum())
