@@ -584,6 +584,8 @@ def chunk_gated_delta_rule_bwd(q, k, v, g, beta, d_out, scale=None, initial_stat
 def _autograd_function():
     import torch
 
+    from ._first_order import first_order
+
     class _ChunkGatedDeltaRule(torch.autograd.Function):
         """Forward: gdn_chunk_fwd_save (the output, the final state, and every
         chunk's start state and T tiles kept for the backward).  Backward:
@@ -601,6 +603,7 @@ def _autograd_function():
             return out, fs
 
         @staticmethod
+        @first_order
         def backward(ctx, d_out, d_fs):
             q, k, v, g, beta, saved = ctx.saved_tensors
             if d_out is None:
@@ -624,7 +627,8 @@ def chunk_gated_delta_rule(q, k, v, g, beta, scale=None, initial_state=None, cu_
     initial state (N, H, d_k, d_v) and int32 cu_seqlens (packed inputs, B = 1).
     Returns (out (B, T, H, d_v) bf16, final_state (N, H, d_k, d_v) fp32); the
     backward runs from the chunk states the forward kept (gradients w.r.t.
-    q, k, v, g, beta and initial_state, in their dtypes)."""
+    q, k, v, g, beta and initial_state, in their dtypes; differentiating them
+    again raises)."""
     global _AUTOGRAD
     if _AUTOGRAD is None:
         _AUTOGRAD = _autograd_function()
