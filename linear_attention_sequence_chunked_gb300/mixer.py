@@ -14,7 +14,8 @@ has it wait for what produces the inputs.  All tensors are on the current device
 Activations are channels last and bf16 or fp32, one type per call; parameters
 and the states of the scan are fp32.  The activation inputs x, gate, u, dt, z,
 B and C may be slices of a wider projection: any tensor whose rows are dense
-and evenly spaced.  Other inputs are contiguous.
+and evenly spaced.  Other inputs are contiguous, and copied where they do not
+start at a 16-byte boundary; a state cache that a step updates does.
 """
 
 from __future__ import annotations
@@ -59,6 +60,14 @@ def _dense(name, t, shape, dtype, dev):
     if not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous tensor, got shape {tuple(t.shape)} strides {t.stride()}")
     return t.data_ptr()
+
+
+def _aligned(*tensors):
+    """Inputs that the kernels read 16 bytes at a time, those that start
+    elsewhere as copies: a slice of a joined gradient, of a state cache or of a
+    joined weight, with rows of any width, may.  (Held by the caller until its
+    launch.)"""
+    return [t.clone() if t is not None and t.data_ptr() & 15 and t.is_contiguous() else t for t in tensors]
 
 
 _device = torch._C._cuda_getDevice
@@ -196,6 +205,7 @@ def short_conv_fwd(x, weight, bias=None, activation="silu", initial_state=None, 
     inputs before each sequence).  Returns (y (B, T, D), final_state or None)."""
     if stream is not None:
         return _on_stream(short_conv_fwd, locals())
+    weight, bias, initial_state = _aligned(weight, bias, initial_state)
     dev, dims, args = _conv_args(x, weight, bias, activation, initial_state, cu_seqlens)
     y = _new(x)
     fs = None
@@ -212,9 +222,10 @@ def short_conv_bwd(x, weight, d_out, bias=None, activation="silu", initial_state
     and d_initial_state (with an initial state)."""
     if stream is not None:
         return _on_stream(short_conv_bwd, locals())
+    weight, bias, initial_state, d_out, d_final_state = _aligned(weight, bias, initial_state, d_out, d_final_state)
     dev, dims, args = _conv_args(x, weight, bias, activation, initial_state, cu_seqlens)
     N, T, D, W = dims[:4]
-    d_out = _dense("d_out", d_out, x.shape, x.dtype, dev)
+    dout = _dense("d_out", d_out, x.shape, x.dtype, dev)
     dfs = _dense("d_final_state", d_final_state, (N, W - 1, D), x.dtype, dev)
     res = {"dx": _new(x), "dweight": torch.empty_like(weight)}
     if bias is not None:
@@ -224,7 +235,7 @@ def short_conv_bwd(x, weight, d_out, bias=None, activation="silu", initial_state
     lib = load()
     nbytes = lib.gdn_conv_bwd_workspace_size(N, T, D, W, int(cu_seqlens is not None))
     ws = _workspace(nbytes, x.device)
-    _check(lib.gdn_conv_bwd(*args, d_out, dfs, res["dx"].data_ptr(), res["dweight"].data_ptr(), _out(res, "dbias"),
+    _check(lib.gdn_conv_bwd(*args, dout, dfs, res["dx"].data_ptr(), res["dweight"].data_ptr(), _out(res, "dbias"),
                             _out(res, "d_initial_state"), *dims, ws.data_ptr(), nbytes, _current(dev)),
            "gdn_conv_bwd")
     return res
@@ -244,6 +255,7 @@ def short_conv_step(x, state, weight, bias=None, activation="silu", slots=None, 
         return _on_stream(short_conv_step, locals())
     if x.dim() != 2:
         raise ValueError(f"x must be (B, D), got shape {tuple(x.shape)}")
+    weight, bias = _aligned(weight, bias)
     dtype, dev = _dtype(x, "x"), x.get_device()
     act = _activation(activation)
     B, D = x.shape
@@ -302,6 +314,7 @@ def ssm_scan_fwd(u, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=True,
         return _on_stream(ssm_scan_fwd, locals())
     if u.dim() != 3:
         raise ValueError(f"u must be (B, T, D), got shape {tuple(u.shape)}")
+    A, D, dt_bias, initial_state = _aligned(A, D, dt_bias, initial_state)
     dev, dims, args = _scan_args(u, dt, A, B, C, D, z, dt_bias, dt_softplus)
     nseq, cu = _sequences(u, cu_seqlens, dev, "u")
     width, G, N, dtype = dims
@@ -334,11 +347,12 @@ def ssm_scan_bwd(u, dt, A, B, C, d_out, saved, D=None, z=None, dt_bias=None, dt_
         return _on_stream(ssm_scan_bwd, locals())
     if u.dim() != 3:
         raise ValueError(f"u must be (B, T, D), got shape {tuple(u.shape)}")
+    A, D, dt_bias, d_out, d_final_state = _aligned(A, D, dt_bias, d_out, d_final_state)
     dev, dims, args = _scan_args(u, dt, A, B, C, D, z, dt_bias, dt_softplus)
     nseq, cu = _sequences(u, cu_seqlens, dev, "u")
     width, G, N, dtype = dims
     T, varlen = u.shape[1], int(cu_seqlens is not None)
-    d_out = _dense("d_out", d_out, u.shape, u.dtype, dev)
+    dout = _dense("d_out", d_out, u.shape, u.dtype, dev)
     _dense("initial_state", initial_state, (nseq, width, N), torch.float32, dev)
     dfs = _dense("d_final_state", d_final_state, (nseq, width, N), torch.float32, dev)
     if saved.dtype is not torch.uint8 or saved.get_device() != dev or not saved.is_contiguous():
@@ -358,7 +372,7 @@ def ssm_scan_bwd(u, dt, A, B, C, d_out, saved, D=None, z=None, dt_bias=None, dt_
     nbytes = lib.gdn_ssm_bwd_workspace_size(nseq, T, width, G, N, varlen)
     ws = _workspace(nbytes, u.device)
     out = [_out(res, k) for k in ("du", "ddt", "dz", "dB", "dC", "dA", "dD", "ddt_bias", "d_initial_state")]
-    _check(lib.gdn_ssm_bwd(*args, cu, d_out, dfs, saved.data_ptr(), saved.numel(), *out, nseq, T, *dims,
+    _check(lib.gdn_ssm_bwd(*args, cu, dout, dfs, saved.data_ptr(), saved.numel(), *out, nseq, T, *dims,
                            ws.data_ptr(), nbytes, _current(dev)), "gdn_ssm_bwd")
     return res
 
@@ -372,6 +386,7 @@ def ssm_scan_step(u, dt, A, B, C, state, D=None, z=None, dt_bias=None, dt_softpl
         return _on_stream(ssm_scan_step, locals())
     if u.dim() != 2:
         raise ValueError(f"u must be (B, D), got shape {tuple(u.shape)}")
+    A, D, dt_bias = _aligned(A, D, dt_bias)
     dev, dims, args = _scan_args(u, dt, A, B, C, D, z, dt_bias, dt_softplus)
     batch, width = u.shape
     at, to, sl, S = _state(state, out_state, slots, batch, (width, dims[2]), torch.float32, dev)
@@ -411,6 +426,7 @@ def group_norm_fwd(x, weight=None, bias=None, gate=None, groups=1, eps=1e-6, act
     with gate_first; without one: act(norm(x)).  Returns y (..., C)."""
     if stream is not None:
         return _on_stream(group_norm_fwd, locals())
+    weight, bias = _aligned(weight, bias)
     dev, act, dtype, rows, C, args = _norm_args(x, weight, bias, gate, groups, activation)
     y = _new(x)
     _check(load().gdn_norm_fwd(*args, y.data_ptr(), rows, C, groups, eps, act, int(center), int(gate_first), dtype,
@@ -424,8 +440,9 @@ def group_norm_bwd(x, d_out, weight=None, bias=None, gate=None, groups=1, eps=1e
     for those that were given."""
     if stream is not None:
         return _on_stream(group_norm_bwd, locals())
+    weight, bias, d_out = _aligned(weight, bias, d_out)
     dev, act, dtype, rows, C, args = _norm_args(x, weight, bias, gate, groups, activation)
-    d_out = _dense("d_out", d_out, x.shape, x.dtype, dev)
+    dout = _dense("d_out", d_out, x.shape, x.dtype, dev)
     res = {"dx": _new(x)}
     if gate is not None:
         res["dgate"] = _new(x)
@@ -438,7 +455,7 @@ def group_norm_bwd(x, d_out, weight=None, bias=None, gate=None, groups=1, eps=1e
     if weight is not None or bias is not None:
         nbytes = lib.gdn_norm_bwd_workspace_size(rows, C, groups, dtype)
     ws = _workspace(nbytes, x.device)
-    _check(lib.gdn_norm_bwd(*args, d_out, res["dx"].data_ptr(), _out(res, "dgate"), _out(res, "dweight"),
+    _check(lib.gdn_norm_bwd(*args, dout, res["dx"].data_ptr(), _out(res, "dgate"), _out(res, "dweight"),
                             _out(res, "dbias"), rows, C, groups, eps, act, int(center), int(gate_first), dtype,
                             None if ws is None else ws.data_ptr(), nbytes, _current(dev)), "gdn_norm_bwd")
     return res

@@ -55,3 +55,28 @@ def test_second_derivatives_are_refused():
         assert torch.equal(g, plain)
         with pytest.raises(RuntimeError, match="cannot be differentiated again"):
             (g.sum() + (x ** 3).sum()).backward()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_gradients_and_states_at_any_address(dtype):
+    """Joined outputs hand slices of one gradient back, and a state may be a row
+    of a cache: with odd widths neither starts at a 16-byte boundary."""
+    D, N = 1003, 8
+    xs = [torch.randn(1, 5, D, device="cuda").to(dtype).requires_grad_() for _ in range(2)]
+    w = torch.randn(D, 4, device="cuda")
+    A = -torch.rand(D, N, device="cuda")
+    B = torch.randn(1, 5, 1, N, device="cuda").to(dtype)
+    tail = torch.randn(3, 3, D, device="cuda").to(dtype)
+    joined = torch.randn(D + 1, device="cuda")
+    assert tail[1:2].data_ptr() % 16 and joined[1:].data_ptr() % 16
+    for f in (lambda x: mixer.short_conv(x, w, joined[1:], initial_state=tail[1:2])[0],
+              lambda x: mixer.ssm_scan(x, x, A, B, B, D=joined[1:])[0],
+              lambda x: mixer.group_norm(x, joined[1:])):
+        d = torch.randn(1, 10, D, device="cuda").to(dtype)
+        assert d[:, 5:].data_ptr() % 16
+        got = torch.autograd.grad(torch.cat([f(x) for x in xs], 1), xs, d)
+        want = [torch.autograd.grad(f(x), x, d[:, 5 * i:5 * i + 5].clone())[0] for i, x in enumerate(xs)]
+        assert all(torch.equal(p, q) for p, q in zip(got, want))
+    y, _ = mixer.short_conv_fwd(xs[0], w, initial_state=tail[1:2])
+    y1, _ = mixer.short_conv_fwd(xs[0], w, initial_state=tail[1:2].clone())
+    assert torch.equal(y, y1)

@@ -2,6 +2,9 @@
 gradients and addresses, with the kernels and the CUDA runtime replaced."""
 
 import contextlib
+import ctypes
+import math
+import sys
 import types
 
 import pytest
@@ -94,3 +97,76 @@ def test_gradients_of_constants_can_be_used_in_a_graph(monkeypatch):
     g, = torch.autograd.grad(f(x, torch.ones(4)).sum(), x, create_graph=True)
     (s * g.detach()).sum().backward()
     assert torch.allclose(s.grad, (2 * x).sum())
+
+
+class Library:
+    """Notes the addresses that a call hands to the library, and the tensors
+    that its caller holds meanwhile."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        if name.endswith("_size"):
+            return lambda *a: 256
+
+        def call(*args):
+            held = {k: v for k, v in sys._getframe(1).f_locals.items() if isinstance(v, torch.Tensor)}
+            self.calls.append(([a for a in args if isinstance(a, int) and a > 1 << 20], held))
+            return 0
+        return call
+
+
+def _off(*shape):
+    """A contiguous tensor that starts where no 16-byte access fits."""
+    n = math.prod(shape)
+    t = torch.randn(n + 64)[1:1 + n].view(shape)
+    assert t.is_contiguous() and t.data_ptr() % 16
+    return t
+
+
+W3, V = (lambda: _off(5, 3)), (lambda: _off(5))
+AT_ANY_ADDRESS = {  # the call, and the inputs that 16-byte accesses read
+    "conv_fwd": (lambda weight, bias, initial_state: mixer.short_conv_fwd(torch.ones(2, 4, 5), weight, bias, initial_state=initial_state),
+                 dict(weight=W3, bias=V, initial_state=lambda: _off(2, 2, 5))),
+    "conv_bwd": (lambda d_out, weight, bias, initial_state, d_final_state: mixer.short_conv_bwd(
+        torch.ones(2, 4, 5), weight, d_out, bias, initial_state=initial_state, d_final_state=d_final_state),
+        dict(d_out=lambda: _off(2, 4, 5), weight=W3, bias=V, initial_state=lambda: _off(2, 2, 5),
+             d_final_state=lambda: _off(2, 2, 5))),
+    "conv_step": (lambda weight, bias: mixer.short_conv_step(torch.ones(2, 5), torch.ones(2, 2, 5), weight, bias),
+                  dict(weight=W3, bias=V)),
+    "scan_fwd": (lambda A, D, dt_bias, initial_state: mixer.ssm_scan_fwd(
+        torch.ones(2, 4, 5), torch.ones(2, 4, 5), A, torch.ones(2, 4, 1, 8), torch.ones(2, 4, 1, 8), D,
+        dt_bias=dt_bias, initial_state=initial_state),
+        dict(A=lambda: _off(5, 8), D=V, dt_bias=V, initial_state=lambda: _off(2, 5, 8))),
+    "scan_bwd": (lambda A, D, dt_bias, d_out, d_final_state: mixer.ssm_scan_bwd(
+        torch.ones(2, 4, 5), torch.ones(2, 4, 5), A, torch.ones(2, 4, 1, 8), torch.ones(2, 4, 1, 8), d_out,
+        torch.zeros(256, dtype=torch.uint8), D, dt_bias=dt_bias, d_final_state=d_final_state),
+        dict(A=lambda: _off(5, 8), D=V, dt_bias=V, d_out=lambda: _off(2, 4, 5), d_final_state=lambda: _off(2, 5, 8))),
+    "scan_step": (lambda A, D, dt_bias: mixer.ssm_scan_step(
+        torch.ones(2, 5), torch.ones(2, 5), A, torch.ones(2, 1, 8), torch.ones(2, 1, 8), torch.ones(2, 5, 8), D,
+        dt_bias=dt_bias), dict(A=lambda: _off(5, 8), D=V, dt_bias=V)),
+    "norm_fwd": (lambda weight, bias: mixer.group_norm_fwd(torch.ones(3, 5), weight, bias), dict(weight=V, bias=V)),
+    "norm_bwd": (lambda weight, bias, d_out: mixer.group_norm_bwd(torch.ones(3, 5), d_out, weight, bias),
+                 dict(weight=V, bias=V, d_out=lambda: _off(3, 5))),
+}
+
+
+@pytest.mark.parametrize("name", list(AT_ANY_ADDRESS))
+def test_inputs_at_any_address(monkeypatch, name):
+    """Gradients, states and parameters that are slices of others: the library
+    gets their values at a 16-byte boundary."""
+    call, inputs = AT_ANY_ADDRESS[name]
+    inputs = {k: make() for k, make in inputs.items()}
+    lib = Library()
+    monkeypatch.setattr(mixer, "load", lambda: lib)
+    monkeypatch.setattr(mixer, "_on_gpu", lambda dev, x: None)
+    monkeypatch.setattr(mixer, "_current", lambda dev: 0)
+    call(**inputs)
+    (at, held), = lib.calls
+    assert at and not [a for a in at if a % 16]
+    for k, t in inputs.items():
+        assert held[k].data_ptr() in at and torch.equal(held[k], t), k
+    at_16 = {k: t.clone() for k, t in inputs.items()}
+    call(**at_16)  # what is aligned is handed on as it is
+    assert all(lib.calls[1][1][k] is t for k, t in at_16.items())
