@@ -540,7 +540,11 @@ def short_conv(x, weight, bias=None, activation="silu", initial_state=None, cu_s
 
 def ssm_scan(u, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=True, initial_state=None, cu_seqlens=None):
     """ssm_scan_fwd with autograd (every tensor but cu_seqlens).  Returns
-    (out, final_state)."""
+    (out, final_state).  The states for the backward are kept where one can
+    follow: some input needs a gradient and grad mode is on."""
+    if not (torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in
+                                            (u, dt, A, B, C, D, z, dt_bias, initial_state))):
+        return ssm_scan_fwd(u, dt, A, B, C, D, z, dt_bias, dt_softplus, initial_state, cu_seqlens)
     return _functions()["scan"].apply(u, dt, A, B, C, D, z, dt_bias, initial_state, dt_softplus, cu_seqlens)
 
 

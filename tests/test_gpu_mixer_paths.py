@@ -80,3 +80,19 @@ def test_gradients_and_states_at_any_address(dtype):
     y, _ = mixer.short_conv_fwd(xs[0], w, initial_state=tail[1:2])
     y1, _ = mixer.short_conv_fwd(xs[0], w, initial_state=tail[1:2].clone())
     assert torch.equal(y, y1)
+
+
+def test_a_scan_without_gradients_takes_no_memory_for_them():
+    u = torch.randn(1, 256, 64, device="cuda", requires_grad=True)
+    A, B = -torch.rand(64, 128, device="cuda"), torch.randn(1, 256, 1, 128, device="cuda")
+    kept, _ = mixer.ssm_scan(u, u, A, B, B)
+    grown = []
+    for call in (lambda: mixer.ssm_scan_fwd(u, u, A, B, B), lambda: mixer.ssm_scan(u, u, A, B, B)):
+        with torch.no_grad():
+            torch.cuda.reset_peak_memory_stats()
+            before = torch.cuda.memory_allocated()
+            out, _ = call()
+            grown.append(torch.cuda.max_memory_allocated() - before)
+        assert torch.equal(out, kept) and not out.requires_grad
+        del out
+    assert grown[0] == grown[1]

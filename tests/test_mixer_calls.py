@@ -170,3 +170,23 @@ def test_inputs_at_any_address(monkeypatch, name):
     at_16 = {k: t.clone() for k, t in inputs.items()}
     call(**at_16)  # what is aligned is handed on as it is
     assert all(lib.calls[1][1][k] is t for k, t in at_16.items())
+
+
+def test_a_scan_without_gradients_saves_nothing(monkeypatch):
+    """The states for the backward are written only where one can follow."""
+    saves = []
+
+    def fwd(u, *args, save_for_backward=False, **kw):
+        saves.append(save_for_backward)
+        return (u + 0, args[8] if len(args) > 8 else None) + ((u.new_zeros(4),) if save_for_backward else ())
+
+    monkeypatch.setattr(mixer, "ssm_scan_fwd", fwd)
+    names = ("u", "dt", "A", "B", "C", "D", "z", "dt_bias", "initial_state")
+    a = {k: torch.zeros(2) for k in names}
+    out, _ = mixer.ssm_scan(**a)
+    assert saves == [False] and not out.requires_grad
+    for k in names:
+        leaf = {**a, k: torch.zeros(2, requires_grad=True)}
+        assert mixer.ssm_scan(**leaf)[0].requires_grad and saves[-1], k
+        with torch.no_grad():
+            assert not mixer.ssm_scan(**leaf)[0].requires_grad and not saves[-1], k
