@@ -592,7 +592,8 @@ GDN_API gdn_status gdn_ssm_step(const void* u, int64_t u_stride, const void* dt,
 /*
  * Group norm with an activation ("Research Sprint Day 2 - Rooflines", GDN layer
  * pseudocode: RMSNorm of the output times SiLU of the gate), rows of C channels
- * in `groups` equal groups of at most 8192:
+ * in `groups` equal groups of at most 8192 (at most 2^33 - 4 groups of all rows
+ * together, 2^31 - 1 of more than 128 channels):
  *     x' = x act(gate) if gate_first, else x
  *     v  = (x' - m) (mean((x' - m)^2) + eps)^-1/2 weight + bias,
  *          m = mean(x') if center, else 0 (RMS norm), means over the group

@@ -471,6 +471,9 @@ struct NormArgs {
 };
 int norm_partial_rows(long long rows, int C, int groups, int dtype);
 constexpr int kNormMaxGroup = 8192;
+// Groups of all rows together that a grid of 2^31 - 1 blocks covers: at least four
+// per block up to 128 channels, one from there on.
+constexpr long long norm_max_groups(int channels) { return ((1LL << 31) - 1) * (channels <= 128 ? 4 : 1); }
 cudaError_t launch_norm_fwd(const NormArgs& a, cudaStream_t stream);
 cudaError_t launch_norm_bwd(const NormArgs& a, cudaStream_t stream);
 

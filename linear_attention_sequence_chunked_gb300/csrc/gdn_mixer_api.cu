@@ -143,6 +143,7 @@ gdn_status check_norm(int64_t rows, int C, int groups, int activation, int dtype
     if (activation < GDN_ACT_NONE || activation > GDN_ACT_SIGMOID) return GDN_ERR_INVALID_ARG;
     if (dtype != GDN_BF16 && dtype != GDN_F32) return GDN_ERR_INVALID_ARG;
     if (C / groups > gdn::kNormMaxGroup || rows >= (1LL << 40) / C) return GDN_ERR_UNSUPPORTED;
+    if (rows > gdn::norm_max_groups(C / groups) / groups) return GDN_ERR_UNSUPPORTED;
     return GDN_OK;
 }
 

@@ -11,7 +11,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from linear_attention_sequence_chunked_gb300 import mixer  # noqa: E402
+from linear_attention_sequence_chunked_gb300 import build, gdn, mixer  # noqa: E402
 
 
 class OnGpu(torch.Tensor):
@@ -190,3 +190,18 @@ def test_a_scan_without_gradients_saves_nothing(monkeypatch):
         assert mixer.ssm_scan(**leaf)[0].requires_grad and saves[-1], k
         with torch.no_grad():
             assert not mixer.ssm_scan(**leaf)[0].requires_grad and not saves[-1], k
+
+
+def test_more_groups_than_a_grid_covers_are_refused():
+    """Tiny groups in tens of GB: the grid's size, cut to 32 bits, left most of
+    the rows alone.  (Without a GPU a call that is not refused ends with 6.)"""
+    if torch.cuda.is_available():
+        pytest.skip("addresses that are never read, for hosts without a GPU")
+    build.build()
+    lib, at = gdn.load(), 0x10000
+    for channels, groups, limit in ((1, 1, 4 * (2 ** 31 - 1)), (8, 4, 2 ** 31 - 1), (2, 2, 2 ** 32 - 2), (129, 1, 2 ** 31 - 1)):
+        for rows, want in ((limit, 6), (limit + 1, 2), (2 ** 34 // groups + 5, 2)):
+            x = (at, channels, None, 0, None, None, at, rows, channels, groups, 1e-6, 0, 0, 0, 0)
+            assert lib.gdn_norm_fwd(*x, None) == want, (channels, groups, rows)
+            bwd = (at, channels, None, 0, None, None, at, at, None, None, None, rows, channels, groups, 1e-6, 0, 0, 0, 0)
+            assert lib.gdn_norm_bwd(*bwd, None, 0, None) == want, (channels, groups, rows)
