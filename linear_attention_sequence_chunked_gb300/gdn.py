@@ -351,6 +351,8 @@ def chunk_kda_fwd(q, k, v, g, beta, scale=None, initial_state=None, cu_seqlens=N
     gdn_kda_chunk_fwd: q, k (B, T, H, d_k) bf16; v (B, T, H, d_v) bf16;
     g (B, T, H, d_k) fp32 (one log decay per key channel); beta (B, T, H)
     bf16.  Returns (out, final_state)."""
+    if stream is not None:
+        return _on_stream(chunk_kda_fwd, locals())
     import torch
     _validate(q, k, v, g, beta, initial_state, cu_seqlens, per_channel_gate=True)
     B, T, H, d_k, d_v = _dims(q, v, cu_seqlens)
@@ -361,7 +363,7 @@ def chunk_kda_fwd(q, k, v, g, beta, scale=None, initial_state=None, cu_seqlens=N
     nbytes = gdn_kda_chunk_fwd_workspace_size(B, T, H, d_k, d_v, cu_seqlens is not None)
     ws = _workspace(nbytes, v.device)
     gdn_kda_chunk_fwd(q, k, v, g, beta, scale, initial_state, cu_seqlens, out, fs, B, T, H, d_k, d_v,
-                      ws, nbytes, stream)
+                      ws, nbytes)
     return out, fs
 
 
@@ -370,6 +372,8 @@ def chunk_kda_bwd(q, k, v, g, beta, d_out, scale=None, initial_state=None, cu_se
     """Allocate gradients and the workspace and run gdn_kda_chunk_bwd (the
     per-channel-gate backward).  Returns a dict of dq, dk, dv, dg (per key
     channel, fp32), dbeta and d_initial_state."""
+    if stream is not None:
+        return _on_stream(chunk_kda_bwd, locals())
     import torch
     _validate(q, k, v, g, beta, initial_state, cu_seqlens, d_out=d_out, d_final_state=d_final_state,
               per_channel_gate=True)
@@ -387,7 +391,7 @@ def chunk_kda_bwd(q, k, v, g, beta, d_out, scale=None, initial_state=None, cu_se
     ws = _workspace(nbytes, dev)
     gdn_kda_chunk_bwd(q, k, v, g, beta, scale, initial_state, cu_seqlens, d_out, d_final_state,
                       res["dq"], res["dk"], res["dv"], res["dg"], res["dbeta"], res["d_initial_state"],
-                      B, T, H, d_k, d_v, ws, nbytes, stream)
+                      B, T, H, d_k, d_v, ws, nbytes)
     return res
 
 
@@ -434,6 +438,28 @@ def gdn_kernel_launches() -> int:
 # ----------------------------------------------------------------------------
 # convenience wrappers (torch tensors in, torch tensors out)
 # ----------------------------------------------------------------------------
+
+def _on_stream(fn, args):
+    """fn with its arguments, `stream` among them (a torch.cuda.Stream or its
+    address), on that stream.  Outputs and workspaces are taken from that
+    stream's memory; outputs stay until the work that the caller's stream has
+    for them is done, and inputs, which a caller may drop when the call returns,
+    until this stream is through with them."""
+    import torch
+    stream = args.pop("stream")
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    caller = torch.cuda.current_stream(stream.device)
+    for t in args.values():
+        if isinstance(t, torch.Tensor) and t.is_cuda:
+            t.record_stream(stream)
+    with torch.cuda.stream(stream):
+        out = fn(**args)
+    for t in out.values() if isinstance(out, dict) else out if isinstance(out, tuple) else (out,):
+        if t is not None:
+            t.record_stream(caller)
+    return out
+
 
 def _dims(q, v, cu_seqlens):
     Bq, T, H, d_k = q.shape
@@ -502,6 +528,8 @@ def chunk_gated_delta_rule_fwd(q, k, v, g, beta, scale=None, initial_state=None,
     """Allocate outputs and run gdn_chunk_fwd.  Returns (out, final_state), or
     (out, final_state, saved) with save_for_backward: gdn_chunk_fwd_save, whose
     `saved` buffer chunk_gated_delta_rule_bwd(..., saved=saved) reuses."""
+    if stream is not None:
+        return _on_stream(chunk_gated_delta_rule_fwd, locals())
     import torch
     _validate(q, k, v, g, beta, initial_state, cu_seqlens)
     B, T, H, d_k, d_v = _dims(q, v, cu_seqlens)
@@ -514,12 +542,12 @@ def chunk_gated_delta_rule_fwd(q, k, v, g, beta, scale=None, initial_state=None,
         nbytes = gdn_chunk_saved_size(B, T, H, d_k, d_v, cu_seqlens is not None)
         saved = torch.empty(nbytes, dtype=torch.uint8, device=v.device)
         gdn_chunk_fwd_save(q, k, v, g, beta, scale, initial_state, cu_seqlens, out, fs,
-                           B, T, H, d_k, d_v, saved, nbytes, stream)
+                           B, T, H, d_k, d_v, saved, nbytes)
         return out, fs, saved
     nbytes = gdn_chunk_fwd_workspace_size(B, T, H, d_k, d_v, cu_seqlens is not None)
     ws = _workspace(nbytes, v.device)
     gdn_chunk_fwd(q, k, v, g, beta, scale, initial_state, cu_seqlens, out, fs,
-                  B, T, H, d_k, d_v, ws, nbytes, stream)
+                  B, T, H, d_k, d_v, ws, nbytes)
     return out, fs
 
 
@@ -527,6 +555,8 @@ def chunk_gated_delta_rule_fwd_split(q, k, v, g, beta, nseg, scale=None, initial
                                      output_final_state=True, stream=None):
     """Allocate outputs and run gdn_chunk_fwd_split (dense inputs, every
     sequence as nseg segments).  Returns (out, final_state)."""
+    if stream is not None:
+        return _on_stream(chunk_gated_delta_rule_fwd_split, locals())
     import torch
     _validate(q, k, v, g, beta, initial_state)
     B, T, H, d_k, d_v = _dims(q, v, None)
@@ -538,7 +568,7 @@ def chunk_gated_delta_rule_fwd_split(q, k, v, g, beta, nseg, scale=None, initial
     nbytes = gdn_chunk_fwd_split_workspace_size(B, T, H, d_k, d_v, nseg)
     ws = _workspace(nbytes, v.device)
     gdn_chunk_fwd_split(q, k, v, g, beta, scale, initial_state, out, fs, B, T, H, d_k, d_v, nseg,
-                        ws, nbytes, stream)
+                        ws, nbytes)
     return out, fs
 
 
@@ -547,6 +577,8 @@ def chunk_gated_delta_rule_bwd(q, k, v, g, beta, d_out, scale=None, initial_stat
     """Allocate gradients and run gdn_chunk_bwd, or gdn_chunk_bwd_saved when
     `saved` (from chunk_gated_delta_rule_fwd(..., save_for_backward=True) on
     the same inputs) is given.  Returns a dict of tensors."""
+    if stream is not None:
+        return _on_stream(chunk_gated_delta_rule_bwd, locals())
     import torch
     _validate(q, k, v, g, beta, initial_state, cu_seqlens, d_out=d_out, d_final_state=d_final_state)
     if saved is not None and (saved.dtype != torch.uint8 or saved.device != q.device):
@@ -567,13 +599,13 @@ def chunk_gated_delta_rule_bwd(q, k, v, g, beta, d_out, scale=None, initial_stat
         gdn_chunk_bwd_saved(q, k, v, g, beta, scale, cu_seqlens, d_out, d_final_state,
                             res["dq"], res["dk"], res["dv"], res["dg"], res["dbeta"],
                             res["d_initial_state"], B, T, H, d_k, d_v, saved, saved.numel(),
-                            ws, nbytes, stream)
+                            ws, nbytes)
         return res
     nbytes = gdn_chunk_bwd_workspace_size(B, T, H, d_k, d_v, cu_seqlens is not None)
     ws = _workspace(nbytes, dev)
     gdn_chunk_bwd(q, k, v, g, beta, scale, initial_state, cu_seqlens, d_out, d_final_state,
                   res["dq"], res["dk"], res["dv"], res["dg"], res["dbeta"],
-                  res["d_initial_state"], B, T, H, d_k, d_v, ws, nbytes, stream)
+                  res["d_initial_state"], B, T, H, d_k, d_v, ws, nbytes)
     return res
 
 

@@ -23,7 +23,7 @@ from __future__ import annotations
 import torch
 
 from ._first_order import first_order
-from .gdn import _check, _workspace, load
+from .gdn import _check, _on_stream, _workspace, load
 
 _ACTIVATIONS = {None: 0, "none": 0, "silu": 1, "sigmoid": 2}
 STATE_SIZES = (8, 16, 32, 64, 128)
@@ -80,27 +80,6 @@ def _on_gpu(dev, x):
     if dev != _device():
         raise ValueError(f"the tensors are on cuda:{dev}, the current device is cuda:{_device()}: "
                          "call under torch.cuda.device")
-
-
-def _on_stream(fn, args):
-    """fn with its arguments, `stream` among them (a torch.cuda.Stream or its
-    address), on that stream.  Outputs and workspaces are taken from that
-    stream's memory; outputs stay until the work that the caller's stream has
-    for them is done, and inputs, which a caller may drop when the call returns,
-    until this stream is through with them."""
-    stream = args.pop("stream")
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
-    caller = torch.cuda.current_stream(stream.device)
-    for t in args.values():
-        if isinstance(t, torch.Tensor) and t.is_cuda:
-            t.record_stream(stream)
-    with torch.cuda.stream(stream):
-        out = fn(**args)
-    for t in out.values() if isinstance(out, dict) else out if isinstance(out, tuple) else (out,):
-        if t is not None:
-            t.record_stream(caller)
-    return out
 
 
 _current = torch._C._cuda_getCurrentRawStream

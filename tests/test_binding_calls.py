@@ -1,6 +1,7 @@
 """What the binding does around a call, on the CPU: devices, with the CUDA
 runtime replaced."""
 
+import contextlib
 import types
 
 import pytest
@@ -45,3 +46,69 @@ def test_second_derivatives_are_refused(monkeypatch):
         (dx.sum() + (x ** 3).sum()).backward()
     f().backward()
     assert torch.equal(x.grad, 2 * x)
+
+
+class OnGpu(torch.Tensor):
+    """A CPU tensor that says it is a CUDA one."""
+    is_cuda = property(lambda self: True)
+
+
+CALLS = {  # the wrapper, its further arguments, and the library call in it
+    "chunk_gated_delta_rule_fwd": ("g", {}, "gdn_chunk_fwd"),
+    "chunk_gated_delta_rule_fwd (saving)": ("g", dict(save_for_backward=True), "gdn_chunk_fwd_save"),
+    "chunk_gated_delta_rule_fwd_split": ("g", dict(nseg=2), "gdn_chunk_fwd_split"),
+    "chunk_gated_delta_rule_bwd": ("g", dict(d_out="v"), "gdn_chunk_bwd"),
+    "chunk_gated_delta_rule_bwd (saved)": ("g", dict(d_out="v", saved="saved"), "gdn_chunk_bwd_saved"),
+    "chunk_kda_fwd": ("gk", {}, "gdn_kda_chunk_fwd"),
+    "chunk_kda_bwd": ("gk", dict(d_out="v"), "gdn_kda_chunk_bwd"),
+}
+
+
+@pytest.mark.parametrize("name", list(CALLS))
+def test_memory_of_a_call_on_another_stream(monkeypatch, name):
+    """Outputs and workspaces come from the given stream's memory (a workspace
+    is given back when the call returns), inputs stay until it is through with
+    them, outputs until the caller's stream is."""
+    gate, more, inner = CALLS[name]
+    bf = torch.bfloat16
+    t = dict(q=torch.zeros(1, 64, 2, 64, dtype=bf), v=torch.zeros(1, 64, 2, 64, dtype=bf), g=torch.zeros(1, 64, 2),
+             gk=torch.zeros(1, 64, 2, 64), beta=torch.zeros(1, 64, 2, dtype=bf), saved=torch.zeros(64, dtype=torch.uint8))
+    t = {k: v.as_subclass(OnGpu) for k, v in t.items()}
+    stream = types.SimpleNamespace(device=torch.device("cuda", 0), cuda_stream=77)
+    now, recorded, made, empty = ["caller"], [], [], torch.empty
+
+    @contextlib.contextmanager
+    def on(s):
+        now.append(s)
+        yield
+        now.pop()
+
+    def take(*a, **k):
+        x = empty(*a, **k)
+        made.append((x, now[-1]))
+        return x
+
+    def record(x, s):
+        recorded.append((x, s))
+
+    def library(*args, **kw):
+        assert now[-1] is stream and (args[-1] is None or not hasattr(args[-1], "cuda_stream"))
+        assert all(any(x is t[k] and s is stream for x, s in recorded) for k in ("q", "v", gate, "beta"))
+
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: "caller")
+    monkeypatch.setattr(torch.Tensor, "record_stream", record)
+    monkeypatch.setattr(torch, "empty", take)
+    monkeypatch.setattr(gdn, "load", lambda: types.SimpleNamespace(**{f: lambda *a: 256 for f in SIZES}))
+    monkeypatch.setattr(gdn, inner, library)
+    more = {k: t.get(v, v) if isinstance(v, str) else v for k, v in more.items()}
+    out = getattr(gdn, name.split()[0])(t["q"], t["q"], t["v"], t[gate], t["beta"], stream=stream, **more)
+    out = list(out.values()) if isinstance(out, dict) else list(out)
+    assert made and all(s is stream for _, s in made)
+    assert all(any(x is o and s == "caller" for x, s in recorded) for o in out)
+    assert now == ["caller"]
+
+
+SIZES = ("gdn_chunk_fwd_workspace_size", "gdn_chunk_bwd_workspace_size", "gdn_chunk_saved_size",
+         "gdn_chunk_bwd_saved_workspace_size", "gdn_chunk_fwd_split_workspace_size", "gdn_kda_chunk_fwd_workspace_size",
+         "gdn_kda_chunk_bwd_workspace_size")
