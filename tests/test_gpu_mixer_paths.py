@@ -252,3 +252,29 @@ def test_infinities_beside_the_rows(dtype, D, left, right):
     for k, v in r.items():
         G._close(v[0], want[k], tol, k)
     G._no_device_error()
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_nan_stays_in_its_sequence_of_a_segmented_scan(value):
+    """One input of the middle sequence, forward and back, where sequences run
+    over several segments and start inside them."""
+    cu = [0, 411, 700, 1100]
+    case = (1, 1100, 24, 1, 16, cu, True, False, True, True)
+    whole = 4 * (1100 * 2 * 16 + 3 * 24 * 18) + 512  # the reverse mode's partial sums without segments
+    assert gdn.load().gdn_ssm_fwd_workspace_size(3, 1100, 24, 1, 16, 1) > 6 * 4 * 24 * 16
+    assert gdn.load().gdn_ssm_bwd_workspace_size(3, 1100, 24, 1, 16, 1) > whole + 6 * 4 * 24 * 16
+    a, t = G._scan_inputs(case, F32)
+    kw = dict(D=t["D"], z=t["z"], dt_bias=t["bias"], initial_state=t["h"], cu_seqlens=t["cu"])
+    args = (t["dt"], t["A"], t["B"], t["C"])
+    u = t["u"].clone()
+    u[0, 500] = value
+    (out, fs, saved), (out2, fs2, saved2) = (mixer.ssm_scan_fwd(x, *args, save_for_backward=True, **kw) for x in (t["u"], u))
+    g, g2 = (mixer.ssm_scan_bwd(x, *args, t["dout"], s, d_final_state=t["dfs"], **kw) for x, s in ((t["u"], saved), (u, saved2)))
+    assert torch.isnan(out2[0, 500]).all() if value != value else not torch.isfinite(out2[0, 500]).all()
+    for rows in (slice(0, 411), slice(700, 1100)):
+        for p, q in ((out, out2),) + tuple((g[k], g2[k]) for k in ("du", "ddt", "dz", "dB", "dC")):
+            assert torch.equal(p[0, rows], q[0, rows])
+    for n in (0, 2):
+        assert torch.equal(fs[n], fs2[n]) and torch.equal(g["d_initial_state"][n], g2["d_initial_state"][n])
+    assert torch.equal(out[0, 411:500], out2[0, 411:500])
+    G._no_device_error()
