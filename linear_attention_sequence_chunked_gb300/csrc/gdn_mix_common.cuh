@@ -196,8 +196,9 @@ __device__ __forceinline__ float rcp(float x) {
 
 __device__ __forceinline__ float sigmoid(float x) { return rcp(1.f + ex2(-kLog2e * x)); }
 
-// softplus without overflow and with a relative error of a few ulp where it
-// is small: max(x, 0) + log1p(e), e = exp(-|x|) in (0, 1], by the series of
+// softplus without overflow and with a small relative error where it is small
+// (a few ulp near zero, about |x| 2^-24 from the product before the exponential
+// far below it): max(x, 0) + log1p(e), e = exp(-|x|) in (0, 1], by the series of
 // log1p(e) = 2 atanh(s), s = e / (2 + e) <= 1/3, up to s^13 (the next term is
 // below 2^-25 of the sum).  A third of log1pf's instructions and no branch.
 __device__ __forceinline__ float softplus(float x) {

@@ -222,8 +222,9 @@ __global__ void __launch_bounds__(32 * kWarps, 3) ssm_fwd_kernel(const SsmArgs p
 
 // One token: lane q of a channel updates four of its states where they lie, for
 // R batch rows whose states are all on their way together.  Bound by HBM: the
-// state is read and written once (256 x 2048, N = 16: 16 us, 4.4 TB/s; what is
-// left is the start and end of one wave of short threads).
+// state is read and written once (256 x 2048, N = 16: 16 us, 4.4 TB/s, in more
+// than three waves of short threads, each with one round of loads and the stores
+// that wait for it).
 template <typename T, int N, int R, bool VEC>
 __global__ void __launch_bounds__(256) ssm_step_kernel(const SsmStepArgs p) {
     constexpr int LPC = N / 4;

@@ -7,16 +7,19 @@
 // A warp walks a run of tokens for 32 channels (fewer for N > 16), a lane per
 // channel with its states in registers, so that a row of every activation is
 // one 64-byte access and nothing is exchanged between lanes.  Tokens come in
-// tiles of kTile: copied to shared memory a tile or two ahead, B and C widened
+// tiles of kTile: copied to shared memory a tile ahead, B and C widened
 // to fp32 once, dt and x = dt u formed once per element, and then four states
 // at a time over the tile without a branch (a token after the end has
 // dt = x = 0, which leaves the state as it is).  Arithmetic runs on pairs of
 // states in register pairs.  Per token and channel that is N exponentials, 2 N
-// paired operations and about 40 others: bound by the register reads of the
-// paired operations (three different pairs cost an operation 3 cycles, 20 per
-// token and four states of a warp, next to 16 of the exponentials), not by HBM.
-// Measured, 4 x 4096 x 2048 with N = 16: 266 us, 24 cycles per token and four
-// states, 1.0 TB/s.
+// paired operations and about 40 others: bound by instruction issue, not by HBM.
+// Measured, 4 x 4096 x 2048 with N = 16: 266 us, 1.0 TB/s, 156 of them in the
+// pass with the outputs and 110 in the one before it, which joins the segments.
+// 156 us are 43 cycles per token and four states of a warp: 24 in the loop over
+// states (by the 92 us that one group of four instead of four takes; 20 are
+// register reads, since three different pairs cost an operation 3 cycles, next to
+// 16 of the exponentials), the rest work per token and channel (softplus and SiLU
+// 24 us, copies 8, and widening, dt u, the sums' ends and the stores).
 #pragma once
 
 #include "gdn_kernels.h"

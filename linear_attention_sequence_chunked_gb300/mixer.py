@@ -400,7 +400,8 @@ def _norm_args(x, weight, bias, gate, groups, activation):
 def group_norm_fwd(x, weight=None, bias=None, gate=None, groups=1, eps=1e-6, activation="silu", center=False,
                    gate_first=False, stream=None):
     """Norm of every row's groups of channels, with a gate or an activation:
-    x, gate (..., C), weight, bias (C).  center=False is the RMS norm, True
+    x, gate (..., C), weight, bias (C).  The statistics are those of one row
+    (token), not of all positions of a sample as in torch.nn.GroupNorm.  center=False is the RMS norm, True
     subtracts the mean.  With a gate: norm(x) act(gate), or norm(x act(gate))
     with gate_first; without one: act(norm(x)).  Returns y (..., C)."""
     if stream is not None:
