@@ -20,16 +20,18 @@ class _Final(torch.autograd.Function):
 
 
 def first_order(backward):
-    """A backward whose gradients come from kernels and carry no graph.  Where
-    one is asked for (create_graph), differentiating them raises: as constants
-    they would silently drop out of a second derivative."""
+    """backward(ctx, saved tensors, *grads) as an autograd Function's backward,
+    for gradients that come from kernels and carry no graph.  Where one is asked
+    for (create_graph), differentiating them raises: as constants they would
+    silently drop out of a second derivative."""
     @functools.wraps(backward)
     def wrapped(ctx, *grads):
+        saved = ctx.saved_tensors  # once: hooks that recompute them refuse a second time
         with torch.no_grad():
-            out = backward(ctx, *grads)
+            out = backward(ctx, saved, *grads)
         if not torch.is_grad_enabled():
             return out
         made = [g for g in out if g is not None]
-        final = iter(_Final.apply(len(made), *made, *ctx.saved_tensors, *grads))
+        final = iter(_Final.apply(len(made), *made, *saved, *grads))
         return tuple(None if g is None else next(final) for g in out)
     return wrapped

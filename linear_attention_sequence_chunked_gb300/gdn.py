@@ -636,8 +636,8 @@ def _autograd_function():
 
         @staticmethod
         @first_order
-        def backward(ctx, d_out, d_fs):
-            q, k, v, g, beta, saved = ctx.saved_tensors
+        def backward(ctx, saved_tensors, d_out, d_fs):
+            q, k, v, g, beta, saved = saved_tensors
             if d_out is None:
                 d_out = torch.zeros_like(v)
             d_out = d_out.to(torch.bfloat16).contiguous()

@@ -466,8 +466,8 @@ def _functions():
 
         @staticmethod
         @first_order
-        def backward(ctx, d_out, d_fs):
-            x, weight, bias, initial_state, cu_seqlens = ctx.saved_tensors
+        def backward(ctx, saved_tensors, d_out, d_fs):
+            x, weight, bias, initial_state, cu_seqlens = saved_tensors
             d_out = torch.zeros(x.shape, dtype=x.dtype, device=x.device) if d_out is None else dense(d_out, x)
             r = short_conv_bwd(x, weight, d_out, bias, ctx.activation, initial_state, cu_seqlens,
                                None if d_fs is None else dense(d_fs, x))
@@ -485,8 +485,8 @@ def _functions():
 
         @staticmethod
         @first_order
-        def backward(ctx, d_out, d_fs):
-            u, dt, A, B, C, D, z, dt_bias, initial_state, cu_seqlens, saved = ctx.saved_tensors
+        def backward(ctx, saved_tensors, d_out, d_fs):
+            u, dt, A, B, C, D, z, dt_bias, initial_state, cu_seqlens, saved = saved_tensors
             d_out = torch.zeros(u.shape, dtype=u.dtype, device=u.device) if d_out is None else dense(d_out, u)
             d_fs = None if d_fs is None else d_fs.to(torch.float32).contiguous()
             r = ssm_scan_bwd(u, dt, A, B, C, d_out, saved, D, z, dt_bias, ctx.dt_softplus, initial_state, cu_seqlens,
@@ -503,8 +503,8 @@ def _functions():
 
         @staticmethod
         @first_order
-        def backward(ctx, d_out):
-            x, weight, bias, gate = ctx.saved_tensors
+        def backward(ctx, saved_tensors, d_out):
+            x, weight, bias, gate = saved_tensors
             r = group_norm_bwd(x, dense(d_out, x), weight, bias, gate, *ctx.rest)
             return (r["dx"], r.get("dweight"), r.get("dbias"), r.get("dgate")) + (None,) * 5
 

@@ -11,6 +11,8 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
+from torch.utils.checkpoint import checkpoint  # noqa: E402
+
 from linear_attention_sequence_chunked_gb300 import build, gdn, mixer  # noqa: E402
 
 
@@ -205,3 +207,15 @@ def test_more_groups_than_a_grid_covers_are_refused():
             assert lib.gdn_norm_fwd(*x, None) == want, (channels, groups, rows)
             bwd = (at, channels, None, 0, None, None, at, at, None, None, None, rows, channels, groups, 1e-6, 0, 0, 0, 0)
             assert lib.gdn_norm_bwd(*bwd, None, 0, None) == want, (channels, groups, rows)
+
+
+@pytest.mark.parametrize("create_graph", [False, True])
+def test_saved_tensors_that_are_recomputed(monkeypatch, create_graph):
+    """Under activation checkpointing each saved tensor can be asked for once."""
+    f, prefix, fwd, bwd = OPERATORS["norm"]
+    monkeypatch.setattr(mixer, prefix + "_fwd", fwd)
+    monkeypatch.setattr(mixer, prefix + "_bwd", bwd)
+    x, w = torch.randn(2, 5, 4, requires_grad=True), torch.ones(4)
+    y = checkpoint(lambda x: f(x, w) * 2, x, use_reentrant=False)
+    g, = torch.autograd.grad(y.sum(), x, create_graph=create_graph)
+    assert torch.equal(g, 4 * x)
