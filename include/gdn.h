@@ -615,6 +615,85 @@ GDN_API gdn_status gdn_norm_bwd(const void* x, int64_t x_stride, const void* gat
                                 size_t workspace_bytes, cudaStream_t stream);
 
 /*
+ * Gated linear recurrence, one state per channel with gates on the decay and on
+ * the input:
+ *     a_t = exp(-rate softplus(lam) sigmoid(r_t))
+ *     h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(i_t) x_t;    y_t = h_t
+ *   x, r, i       (B,T,D) (strided)          lam (D);  rate > 0
+ *   initial_state (nseq,D) or NULL (zeros);  final_state (nseq,D) or NULL, not
+ *                 initial_state's memory
+ *   y             (B,T,D)
+ *   saved         NULL, or gdn_gated_saved_size() bytes that the backward reads:
+ *                 the state before every 8 tokens
+ */
+GDN_API size_t gdn_gated_saved_size(int B, int T, int D, int varlen);
+GDN_API gdn_status gdn_gated_fwd(const void* x, int64_t x_stride, const void* r, int64_t r_stride, const void* i,
+                                 int64_t i_stride, const float* lam, float rate, const float* initial_state,
+                                 const int32_t* cu_seqlens, void* y, float* final_state, void* saved,
+                                 size_t saved_bytes, int B, int T, int D, int dtype, cudaStream_t stream);
+
+/*
+ * Reverse mode of gdn_gated_fwd from the same inputs and the `saved` buffer it
+ * filled.  d_out (B,T,D) and d_final_state (nseq,D) or NULL in; dx, dr, di
+ * (B,T,D), dlam (D) and d_initial_state (nseq,D; NULL: not wanted) out.
+ */
+GDN_API size_t gdn_gated_bwd_workspace_size(int B, int T, int D, int varlen);
+GDN_API gdn_status gdn_gated_bwd(const void* x, int64_t x_stride, const void* r, int64_t r_stride, const void* i,
+                                 int64_t i_stride, const float* lam, float rate, const float* initial_state,
+                                 const int32_t* cu_seqlens, const void* d_out, const float* d_final_state,
+                                 const void* saved, size_t saved_bytes, void* dx, void* dr, void* di, float* dlam,
+                                 float* d_initial_state, int B, int T, int D, int dtype, void* workspace,
+                                 size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * One token per row, for decode: x, r, i, y (B,D), the state (S,D) into
+ * out_state (may be `state`); slots as in gdn_conv_step.
+ */
+GDN_API gdn_status gdn_gated_step(const void* x, int64_t x_stride, const void* r, int64_t r_stride, const void* i,
+                                  int64_t i_stride, const float* lam, float rate, const float* state,
+                                  float* out_state, const int32_t* slots, void* y, int B, int S, int D, int dtype,
+                                  cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Attention operators: the attention layers that a linear-attention model
+ * puts between its others.  Conventions as for the mixer operators; a token's
+ * row is its heads side by side.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Norm of every query's and key's head and its rotation by position:
+ *     n = x (mean(x^2) + eps)^-1/2 weight          (per head of d channels)
+ *     (u, v) -> (u cos(p f) - v sin(p f), v cos(p f) + u sin(p f))
+ * for pair j of n, frequency f = inv_freq[j] and the token's position p.  Pair
+ * j is channels j and j + pairs, or 2j and 2j + 1 with `interleaved`; channels
+ * from 2 pairs on do not turn.
+ *   q (B,T,H,d), k (B,T,Hk,d) (strided)       q_weight, k_weight (d) or NULL (ones)
+ *   inv_freq  (pairs), radians per token; NULL where pairs is 0 (norm alone)
+ *   positions (B,T) int32 or NULL: a token's place in its sequence
+ *   q_out (B,T,H,d), k_out (B,T,Hk,d), dense
+ *   d in {32, 64, 128, 256}; pairs a multiple of 4, at most d / 2; H, Hk <= 1024;
+ *   B T < 2^31
+ * The angle is exact to about 2^-26 turns at any position: p inv_freq is formed
+ * from the fp32 frequency in 64-bit fixed point.
+ */
+GDN_API gdn_status gdn_rope_fwd(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                const float* q_weight, const float* k_weight, const float* inv_freq,
+                                const int32_t* positions, const int32_t* cu_seqlens, void* q_out, void* k_out, int B,
+                                int T, int H, int Hk, int d, int pairs, int interleaved, float eps, int dtype,
+                                cudaStream_t stream);
+
+/* Reverse mode of gdn_rope_fwd: dq_out (B,T,H,d), dk_out (B,T,Hk,d) in, dense;
+ * dq, dk, and dq_weight, dk_weight (d; each exactly when its weight is given)
+ * out. */
+GDN_API size_t gdn_rope_bwd_workspace_size(int B, int T, int H, int Hk, int d, int varlen);
+GDN_API gdn_status gdn_rope_bwd(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                const float* q_weight, const float* k_weight, const float* inv_freq,
+                                const int32_t* positions, const int32_t* cu_seqlens, const void* dq_out,
+                                const void* dk_out, void* dq, void* dk, float* dq_weight, float* dk_weight, int B,
+                                int T, int H, int Hk, int d, int pairs, int interleaved, float eps, int dtype,
+                                void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
  * Number of CUDA kernels this library has launched in this process so far
  * (all devices, all entry points).  Library bookkeeping with no counterpart
  * on the pages; lets a caller count the kernels inside a timed region.

@@ -477,6 +477,81 @@ constexpr long long norm_max_groups(int channels) { return ((1LL << 31) - 1) * (
 cudaError_t launch_norm_fwd(const NormArgs& a, cudaStream_t stream);
 cudaError_t launch_norm_bwd(const NormArgs& a, cudaStream_t stream);
 
+// Gated linear recurrence: rows of T tokens (packed: one row), D channels.
+constexpr int kGatedStrip = 8;         // tokens of a warp's strip, and between saved states
+constexpr int kGatedMaxCluster = 8;    // blocks side by side on one row
+struct GatedArgs {
+    const void* x;                // (rows T, D), rows x_stride apart; r, i likewise
+    const void* r;
+    const void* i;
+    long long x_stride, r_stride, i_stride;
+    const float* lam;             // (D)
+    float rate;
+    const float* initial_state;   // (nseq, D) or null
+    const int32_t* cu_seqlens;
+    void* y;                      // forward
+    float* final_state;           // (nseq, D) or null
+    float* saved;                 // [rows][strips][D]: the state each strip starts from; written by the forward (or null)
+    const void* d_out;            // backward, from here
+    const float* d_final_state;   // (nseq, D) or null
+    void* dx;
+    void* dr;
+    void* di;
+    float* d_initial_state;       // (nseq, D) or null
+    float* partial;               // [rows cluster][D]: dlam
+    int rows, nseq, T, D, dtype;
+    int cluster;
+    int* err;
+};
+struct GatedStepArgs {
+    const void* x;
+    const void* r;
+    const void* i;
+    long long x_stride, r_stride, i_stride;
+    const float* lam;
+    float rate;
+    const float* state;           // (S, D)
+    float* out_state;             // may be `state`
+    const int32_t* slots;         // (B) rows of the state, or null
+    void* y;                      // (B, D)
+    int B, S, D, dtype;
+    int* err;
+};
+int gated_cluster(int rows, int T, int D);
+cudaError_t launch_gated_fwd(const GatedArgs& a, cudaStream_t stream);
+cudaError_t launch_gated_bwd(const GatedArgs& a, cudaStream_t stream);
+cudaError_t launch_gated_step(const GatedStepArgs& a, cudaStream_t stream);
+
+// Norm and rotation of query and key heads.
+struct RopeArgs {
+    const void* q;                // (tokens, H, d), tokens q_stride apart
+    const void* k;                // (tokens, Hk, d), tokens k_stride apart
+    long long q_stride, k_stride;
+    const float* q_weight;        // (d) or null
+    const float* k_weight;
+    const float* inv_freq;        // (pairs)
+    const int32_t* positions;     // (tokens) or null
+    const int32_t* cu_seqlens;
+    void* q_out;                  // forward
+    void* k_out;
+    const void* dq_out;           // backward, from here
+    const void* dk_out;
+    void* dq;
+    void* dk;
+    float* partial;               // [blocks][2][d] or null
+    long long tokens;
+    int nseq, T, H, Hk, d, pairs;
+    int interleaved, dtype;
+    float eps;
+    int tile;                     // tokens per block
+    unsigned blocks;
+    int* err;
+};
+int rope_tile(long long tokens, int heads);
+long long rope_blocks(long long tokens, int heads, bool backward);
+cudaError_t launch_rope_fwd(const RopeArgs& a, cudaStream_t stream);
+cudaError_t launch_rope_bwd(const RopeArgs& a, cudaStream_t stream);
+
 // The library's per-device error word and its count of launched kernels
 // (gdn_api.cu), for the other files of the C ABI.
 int* device_error_word();

@@ -4,46 +4,14 @@
 #include <stdint.h>
 
 #include <algorithm>
-#include <initializer_list>
 
 #include "gdn.h"
+#include "gdn_checks.h"
 #include "gdn_kernels.h"
 
 namespace {
 
-constexpr size_t kAlign = 256;
-constexpr int kMaxT = 1 << 30;
-
-size_t round_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
-bool off16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
-bool off_elem(const void* p, int dtype) { return reinterpret_cast<uintptr_t>(p) % (dtype == GDN_F32 ? 4 : 2) != 0; }
-
-gdn_status check_dense(std::initializer_list<const void*> ptrs) {
-    for (const void* p : ptrs)
-        if (p && off16(p)) return GDN_ERR_MISALIGNED;
-    return GDN_OK;
-}
-gdn_status check_cu(const int32_t* cu) { return reinterpret_cast<uintptr_t>(cu) & 3u ? GDN_ERR_MISALIGNED : GDN_OK; }
-
-// A strided input: present, aligned to its element, rows at least `row` apart.
-gdn_status check_rows(const void* p, int64_t stride, int64_t row, int dtype) {
-    if (!p || stride < row || stride >= (1LL << 40)) return GDN_ERR_INVALID_ARG;
-    return off_elem(p, dtype) ? GDN_ERR_MISALIGNED : GDN_OK;
-}
-
-gdn_status check_ws(const void* p, size_t bytes, size_t need) {
-    if (need == 0) return GDN_OK;
-    if (!p || bytes < need) return GDN_ERR_INVALID_ARG;
-    return reinterpret_cast<uintptr_t>(p) & (kAlign - 1) ? GDN_ERR_MISALIGNED : GDN_OK;
-}
-
-gdn_status check_sizes(int B, int T, int D, int dtype) {
-    if (B < 1 || T < 0 || D < 1) return GDN_ERR_INVALID_ARG;
-    if (dtype != GDN_BF16 && dtype != GDN_F32) return GDN_ERR_INVALID_ARG;
-    if (B > 65535 || T > kMaxT || D > 65536) return GDN_ERR_UNSUPPORTED;
-    if (static_cast<long long>(B) * T >= (1LL << 40) / D) return GDN_ERR_UNSUPPORTED;
-    return GDN_OK;
-}
+using namespace gdn::checks;
 
 gdn_status check_conv(int B, int T, int D, int W, int activation, int dtype) {
     const gdn_status st = check_sizes(B, T, D, dtype);
@@ -60,12 +28,6 @@ gdn_status check_ssm(int B, int T, int D, int G, int N, int dtype) {
     if (N != 8 && N != 16 && N != 32 && N != 64 && N != 128) return GDN_ERR_UNSUPPORTED;
     return GDN_OK;
 }
-
-#define GDN_TRY(expr)                          \
-    do {                                       \
-        const gdn_status st_ = (expr);         \
-        if (st_ != GDN_OK) return st_;         \
-    } while (0)
 
 // Time blocks (or chunks) of `tb` tokens, as find_block counts them.
 long long block_slots(int B, int T, int tb, bool varlen) {
@@ -137,6 +99,12 @@ SsmBwdLayout ssm_bwd_layout(int B, int T, int D, int G, int N, bool varlen) {
     L.total = L.carry + split.total;
     return L;
 }
+
+size_t gated_saved(int B, int T, int D, bool varlen) {
+    const long long strips = (static_cast<long long>(T) + gdn::kGatedStrip - 1) / gdn::kGatedStrip;
+    return round_up(sizeof(float) * (varlen ? 1 : B) * strips * D);
+}
+size_t gated_ws(int rows, int T, int D) { return round_up(sizeof(float) * rows * gdn::gated_cluster(rows, T, D) * static_cast<size_t>(D)); }
 
 gdn_status check_norm(int64_t rows, int C, int groups, int activation, int dtype) {
     if (rows < 0 || C < 1 || groups < 1 || C % groups != 0) return GDN_ERR_INVALID_ARG;
@@ -393,6 +361,99 @@ gdn_status gdn_norm_bwd(const void* x, int64_t x_stride, const void* gate, int64
     c.rows = gdn::norm_partial_rows(rows, C, groups, dtype);
     c.out[0] = dweight; c.out[1] = dbias;
     return gdn::count_launch(gdn::launch_column_sum(c, stream)) ? GDN_OK : GDN_ERR_CUDA;
+}
+
+size_t gdn_gated_saved_size(int B, int T, int D, int varlen) {
+    if (check_sizes(B, T, D, 0) != GDN_OK) return 0;
+    return gated_saved(B, T, D, varlen != 0);
+}
+
+gdn_status gdn_gated_fwd(const void* x, int64_t x_stride, const void* r, int64_t r_stride, const void* i,
+                         int64_t i_stride, const float* lam, float rate, const float* initial_state,
+                         const int32_t* cu_seqlens, void* y, float* final_state, void* saved, size_t saved_bytes,
+                         int B, int T, int D, int dtype, cudaStream_t stream) {
+    GDN_TRY(check_sizes(B, T, D, dtype));
+    if (!lam || !(rate > 0.f) || (T > 0 && !y)) return GDN_ERR_INVALID_ARG;
+    if (T > 0) {
+        GDN_TRY(check_rows(x, x_stride, D, dtype));
+        GDN_TRY(check_rows(r, r_stride, D, dtype));
+        GDN_TRY(check_rows(i, i_stride, D, dtype));
+    }
+    GDN_TRY(check_dense({lam, initial_state, y, final_state}));
+    GDN_TRY(check_cu(cu_seqlens));
+    if (final_state && final_state == initial_state) return GDN_ERR_INVALID_ARG;
+    const bool varlen = cu_seqlens != nullptr;
+    if (saved) GDN_TRY(check_ws(saved, saved_bytes, gated_saved(B, T, D, varlen)));
+    if (T == 0 && !final_state) return GDN_OK;
+    int* err = gdn::device_error_word();
+    if (!err) return GDN_ERR_CUDA;
+    gdn::GatedArgs a{};
+    a.x = x; a.r = r; a.i = i; a.x_stride = x_stride; a.r_stride = r_stride; a.i_stride = i_stride;
+    a.lam = lam; a.rate = rate; a.initial_state = initial_state; a.cu_seqlens = cu_seqlens; a.y = y;
+    a.final_state = final_state; a.saved = static_cast<float*>(saved);
+    a.rows = varlen ? 1 : B; a.nseq = B; a.T = T; a.D = D; a.dtype = dtype; a.err = err;
+    a.cluster = gdn::gated_cluster(a.rows, T, D);
+    return gdn::count_launch(gdn::launch_gated_fwd(a, stream)) ? GDN_OK : GDN_ERR_CUDA;
+}
+
+size_t gdn_gated_bwd_workspace_size(int B, int T, int D, int varlen) {
+    if (check_sizes(B, T, D, 0) != GDN_OK) return 0;
+    return gated_ws(varlen ? 1 : B, T, D);
+}
+
+gdn_status gdn_gated_bwd(const void* x, int64_t x_stride, const void* r, int64_t r_stride, const void* i,
+                         int64_t i_stride, const float* lam, float rate, const float* initial_state,
+                         const int32_t* cu_seqlens, const void* d_out, const float* d_final_state, const void* saved,
+                         size_t saved_bytes, void* dx, void* dr, void* di, float* dlam, float* d_initial_state, int B,
+                         int T, int D, int dtype, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+    GDN_TRY(check_sizes(B, T, D, dtype));
+    if (!lam || !dlam || !(rate > 0.f)) return GDN_ERR_INVALID_ARG;
+    if (T > 0) {
+        if (!d_out || !dx || !dr || !di) return GDN_ERR_INVALID_ARG;
+        GDN_TRY(check_rows(x, x_stride, D, dtype));
+        GDN_TRY(check_rows(r, r_stride, D, dtype));
+        GDN_TRY(check_rows(i, i_stride, D, dtype));
+    }
+    GDN_TRY(check_dense({lam, initial_state, d_out, d_final_state, dx, dr, di, dlam, d_initial_state}));
+    GDN_TRY(check_cu(cu_seqlens));
+    if (d_initial_state && d_initial_state == d_final_state) return GDN_ERR_INVALID_ARG;
+    const bool varlen = cu_seqlens != nullptr;
+    GDN_TRY(check_ws(saved, saved_bytes, gated_saved(B, T, D, varlen)));
+    const int rows = varlen ? 1 : B;
+    GDN_TRY(check_ws(workspace, workspace_bytes, gated_ws(rows, T, D)));
+    int* err = gdn::device_error_word();
+    if (!err) return GDN_ERR_CUDA;
+    gdn::GatedArgs a{};
+    a.x = x; a.r = r; a.i = i; a.x_stride = x_stride; a.r_stride = r_stride; a.i_stride = i_stride;
+    a.lam = lam; a.rate = rate; a.initial_state = initial_state; a.cu_seqlens = cu_seqlens;
+    a.saved = static_cast<float*>(const_cast<void*>(saved));
+    a.d_out = d_out; a.d_final_state = d_final_state; a.dx = dx; a.dr = dr; a.di = di;
+    a.d_initial_state = d_initial_state; a.partial = static_cast<float*>(workspace);
+    a.rows = rows; a.nseq = B; a.T = T; a.D = D; a.dtype = dtype; a.err = err;
+    a.cluster = gdn::gated_cluster(rows, T, D);
+    if (!gdn::count_launch(gdn::launch_gated_bwd(a, stream))) return GDN_ERR_CUDA;
+    gdn::ColumnSumArgs c{};
+    c.partial = a.partial; c.c0 = c.cols = c.stride = D; c.rows = rows * a.cluster; c.out[0] = dlam;
+    return gdn::count_launch(gdn::launch_column_sum(c, stream)) ? GDN_OK : GDN_ERR_CUDA;
+}
+
+gdn_status gdn_gated_step(const void* x, int64_t x_stride, const void* r, int64_t r_stride, const void* i,
+                          int64_t i_stride, const float* lam, float rate, const float* state, float* out_state,
+                          const int32_t* slots, void* y, int B, int S, int D, int dtype, cudaStream_t stream) {
+    GDN_TRY(check_sizes(B, 1, D, dtype));
+    if (!lam || !state || !out_state || !y || !(rate > 0.f) || S < 1 || (!slots && S < B)) return GDN_ERR_INVALID_ARG;
+    GDN_TRY(check_rows(x, x_stride, D, dtype));
+    GDN_TRY(check_rows(r, r_stride, D, dtype));
+    GDN_TRY(check_rows(i, i_stride, D, dtype));
+    GDN_TRY(check_dense({lam, state, out_state, y}));
+    GDN_TRY(check_cu(slots));
+    int* err = gdn::device_error_word();
+    if (!err) return GDN_ERR_CUDA;
+    gdn::GatedStepArgs a{};
+    a.x = x; a.r = r; a.i = i; a.x_stride = x_stride; a.r_stride = r_stride; a.i_stride = i_stride;
+    a.lam = lam; a.rate = rate; a.state = state; a.out_state = out_state; a.slots = slots; a.y = y;
+    a.B = B; a.S = S; a.D = D; a.dtype = dtype; a.err = err;
+    return gdn::count_launch(gdn::launch_gated_step(a, stream)) ? GDN_OK : GDN_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -141,6 +141,24 @@ def load():
         lib.gdn_norm_bwd_workspace_size.restype = sz
         lib.gdn_norm_bwd.argtypes = row + row + [vp] * 7 + [i64, i, i, f, i, i, i, i, vp, sz, vp]
         lib.gdn_norm_bwd.restype = i
+        gated = row * 3 + [vp, f, vp, vp]
+        lib.gdn_gated_saved_size.argtypes = [i] * 4
+        lib.gdn_gated_saved_size.restype = sz
+        lib.gdn_gated_fwd.argtypes = gated + [vp] * 3 + [sz] + [i] * 4 + [vp]
+        lib.gdn_gated_fwd.restype = i
+        lib.gdn_gated_bwd_workspace_size.argtypes = [i] * 4
+        lib.gdn_gated_bwd_workspace_size.restype = sz
+        lib.gdn_gated_bwd.argtypes = gated + [vp] * 3 + [sz] + [vp] * 5 + [i] * 4 + [vp, sz, vp]
+        lib.gdn_gated_bwd.restype = i
+        lib.gdn_gated_step.argtypes = row * 3 + [vp, f] + [vp] * 4 + [i] * 4 + [vp]
+        lib.gdn_gated_step.restype = i
+        rope = row * 2 + [vp] * 5
+        lib.gdn_rope_fwd.argtypes = rope + [vp] * 2 + [i] * 7 + [f, i, vp]
+        lib.gdn_rope_fwd.restype = i
+        lib.gdn_rope_bwd_workspace_size.argtypes = [i] * 6
+        lib.gdn_rope_bwd_workspace_size.restype = sz
+        lib.gdn_rope_bwd.argtypes = rope + [vp] * 6 + [i] * 7 + [f, i, vp, sz, vp]
+        lib.gdn_rope_bwd.restype = i
         lib.gdn_kernel_launches.argtypes = []
         lib.gdn_kernel_launches.restype = ctypes.c_uint64
         _lib = lib

@@ -1,18 +1,18 @@
 """The operators around the recurrence of a mixer layer: a short causal
-convolution, the selective state space scan, and the group norm with an
-activation; for prompts, for training, and token by token.
+convolution, the selective state space scan, the gated linear recurrence, and
+the group norm with an activation; for prompts, for training, and token by token.
 
 As in gdn.py, nothing is computed here: arguments are checked and handed to
 the CUDA kernels of ``_build/libgdn.so`` (include/gdn.h has the formulas and
 layouts), without a CPU fallback.  ``*_fwd`` / ``*_bwd`` / ``*_step`` allocate
-their outputs and workspaces with torch; short_conv, ssm_scan and group_norm
+their outputs and workspaces with torch; short_conv, ssm_scan, gated_scan and group_norm
 are the same forwards and backwards behind torch.autograd (first derivatives
 only: a second one raises).  The former also
 take `stream=`, in place of the current stream; as with any stream, the caller
 has it wait for what produces the inputs.  All tensors are on the current device.
 
 Activations are channels last and bf16 or fp32, one type per call; parameters
-and the states of the scan are fp32.  The activation inputs x, gate, u, dt, z,
+and the states of the scans are fp32.  The activation inputs x, gate, u, dt, z, r, i,
 B and C may be slices of a wider projection: any tensor whose rows are dense
 and evenly spaced.  Other inputs are contiguous, and copied where they do not
 start at a 16-byte boundary; a state cache that a step updates does.
@@ -376,6 +376,108 @@ def ssm_scan_step(u, dt, A, B, C, state, D=None, z=None, dt_bias=None, dt_softpl
 
 
 # ----------------------------------------------------------------------------
+# gated linear recurrence
+# ----------------------------------------------------------------------------
+
+def _gated_args(x, r, i, lam, rate):
+    """Checks shared by the recurrence and its step (x of 3 or 2 dimensions)."""
+    dtype, dev, shape = _dtype(x, "x"), x.get_device(), x.shape
+    D = shape[-1]
+    _is("r", r, shape, x.dtype, dev)
+    _is("i", i, shape, x.dtype, dev)
+    if not rate > 0:
+        raise ValueError(f"rate must be positive, got {rate}")
+    return dev, dtype, D, (*_rows(x, D), *_rows(r, D), *_rows(i, D), _dense("lam", lam, (D,), torch.float32, dev), rate)
+
+
+def gated_scan_fwd(x, r, i, lam, rate=8.0, initial_state=None, cu_seqlens=None, output_final_state=True,
+                   save_for_backward=False, stream=None):
+    """Gated linear recurrence h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(i_t) x_t
+    with a_t = exp(-rate softplus(lam) sigmoid(r_t)): x, r, i (B, T, D), lam (D),
+    initial_state (N_seq, D) fp32.  Returns (h (B, T, D), final_state or None), or
+    (h, final_state, saved) with save_for_backward (the states gated_scan_bwd
+    starts from)."""
+    if stream is not None:
+        return _on_stream(gated_scan_fwd, locals())
+    if x.dim() != 3:
+        raise ValueError(f"x must be (B, T, D), got shape {tuple(x.shape)}")
+    lam, initial_state = _aligned(lam, initial_state)
+    dev, dtype, D, args = _gated_args(x, r, i, lam, rate)
+    nseq, cu = _sequences(x, cu_seqlens, dev, "x")
+    T, varlen = x.shape[1], int(cu_seqlens is not None)
+    h0 = _dense("initial_state", initial_state, (nseq, D), torch.float32, dev)
+    _on_gpu(dev, x)
+    y = _new(x)
+    fs = None
+    if output_final_state:
+        fs = lam.new_empty((nseq, D)) if initial_state is None else torch.empty_like(initial_state)
+    lib = load()
+    saved, sbytes = None, 0
+    if save_for_backward:
+        sbytes = lib.gdn_gated_saved_size(nseq, T, D, varlen)
+        saved = torch.empty(sbytes, dtype=torch.uint8, device=x.device)
+    _check(lib.gdn_gated_fwd(*args, h0, cu, y.data_ptr(), None if fs is None else fs.data_ptr(),
+                             None if saved is None else saved.data_ptr(), sbytes, nseq, T, D, dtype, _current(dev)),
+           "gdn_gated_fwd")
+    return (y, fs, saved) if save_for_backward else (y, fs)
+
+
+def gated_scan_bwd(x, r, i, lam, d_out, saved, rate=8.0, initial_state=None, cu_seqlens=None, d_final_state=None,
+                   stream=None):
+    """Gradients of gated_scan_fwd from the same inputs and the `saved` that it
+    returned: a dict of dx, dr, di, dlam, and d_initial_state (with an initial
+    state)."""
+    if stream is not None:
+        return _on_stream(gated_scan_bwd, locals())
+    if x.dim() != 3:
+        raise ValueError(f"x must be (B, T, D), got shape {tuple(x.shape)}")
+    lam, initial_state, d_out, d_final_state = _aligned(lam, initial_state, d_out, d_final_state)
+    dev, dtype, D, args = _gated_args(x, r, i, lam, rate)
+    nseq, cu = _sequences(x, cu_seqlens, dev, "x")
+    T, varlen = x.shape[1], int(cu_seqlens is not None)
+    h0 = _dense("initial_state", initial_state, (nseq, D), torch.float32, dev)
+    dout = _dense("d_out", d_out, x.shape, x.dtype, dev)
+    dfs = _dense("d_final_state", d_final_state, (nseq, D), torch.float32, dev)
+    if saved.dtype is not torch.uint8 or saved.get_device() != dev or not saved.is_contiguous():
+        raise ValueError("saved must be the uint8 buffer that the saving forward returned, on x's device")
+    _on_gpu(dev, x)
+    res = {"dx": _new(x), "dr": _new(x), "di": _new(x), "dlam": torch.empty_like(lam)}
+    if initial_state is not None:
+        res["d_initial_state"] = torch.empty_like(initial_state)
+    lib = load()
+    nbytes = lib.gdn_gated_bwd_workspace_size(nseq, T, D, varlen)
+    ws = _workspace(nbytes, x.device)
+    _check(lib.gdn_gated_bwd(*args, h0, cu, dout, dfs, saved.data_ptr(), saved.numel(), res["dx"].data_ptr(),
+                             res["dr"].data_ptr(), res["di"].data_ptr(), res["dlam"].data_ptr(),
+                             _out(res, "d_initial_state"), nseq, T, D, dtype, ws.data_ptr(), nbytes, _current(dev)),
+           "gdn_gated_bwd")
+    return res
+
+
+def gated_scan_step(x, r, i, lam, state, rate=8.0, slots=None, out_state=None, stream=None):
+    """One token per row: x, r, i (B, D) and a state cache (S, D) fp32, updated
+    in place or into out_state; slots as in short_conv_step.  Returns h (B, D)."""
+    if stream is not None:
+        return _on_stream(gated_scan_step, locals())
+    if x.dim() != 2:
+        raise ValueError(f"x must be (B, D), got shape {tuple(x.shape)}")
+    lam, = _aligned(lam)
+    dev, dtype, D, args = _gated_args(x, r, i, lam, rate)
+    B = x.shape[0]
+    if state.dim() != 2 or state.shape[1] != D or (slots is None and state.shape[0] < B):
+        raise ValueError(f"state must be (S, {D}) with a row for each of the {B}, got shape {tuple(state.shape)}")
+    to = state if out_state is None else out_state
+    at = _dense("state", state, state.shape, torch.float32, dev)
+    into = at if to is state else _dense("out_state", to, state.shape, torch.float32, dev)
+    sl = None if slots is None else _dense("slots", slots, (B,), torch.int32, dev)
+    _on_gpu(dev, x)
+    y = _new(x)
+    _check(load().gdn_gated_step(*args, at, into, sl, y.data_ptr(), B, state.shape[0], D, dtype, _current(dev)),
+           "gdn_gated_step")
+    return y
+
+
+# ----------------------------------------------------------------------------
 # group norm with an activation
 # ----------------------------------------------------------------------------
 
@@ -494,6 +596,24 @@ def _functions():
             return (r["du"], r["ddt"], r["dA"], r["dB"], r["dC"], r.get("dD"), r.get("dz"), r.get("ddt_bias"),
                     r.get("d_initial_state"), None, None)
 
+    class GatedScan(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, r, i, lam, initial_state, rate, cu_seqlens):
+            y, fs, saved = gated_scan_fwd(x, r, i, lam, rate, initial_state, cu_seqlens, save_for_backward=True)
+            ctx.save_for_backward(x, r, i, lam, initial_state, cu_seqlens, saved)
+            ctx.rate = rate
+            ctx.set_materialize_grads(False)
+            return y, fs
+
+        @staticmethod
+        @first_order
+        def backward(ctx, saved_tensors, d_out, d_fs):
+            x, r, i, lam, initial_state, cu_seqlens, saved = saved_tensors
+            d_out = torch.zeros(x.shape, dtype=x.dtype, device=x.device) if d_out is None else dense(d_out, x)
+            d_fs = None if d_fs is None else d_fs.to(torch.float32).contiguous()
+            g = gated_scan_bwd(x, r, i, lam, d_out, saved, ctx.rate, initial_state, cu_seqlens, d_fs)
+            return g["dx"], g["dr"], g["di"], g["dlam"], g.get("d_initial_state"), None, None
+
     class GroupNorm(torch.autograd.Function):
         @staticmethod
         def forward(ctx, x, weight, bias, gate, groups, eps, activation, center, gate_first):
@@ -508,7 +628,7 @@ def _functions():
             r = group_norm_bwd(x, dense(d_out, x), weight, bias, gate, *ctx.rest)
             return (r["dx"], r.get("dweight"), r.get("dbias"), r.get("dgate")) + (None,) * 5
 
-    _FUNCTIONS.update(conv=ShortConv, scan=SsmScan, norm=GroupNorm)
+    _FUNCTIONS.update(conv=ShortConv, scan=SsmScan, gated=GatedScan, norm=GroupNorm)
     return _FUNCTIONS
 
 
@@ -526,6 +646,14 @@ def ssm_scan(u, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=True, ini
                                             (u, dt, A, B, C, D, z, dt_bias, initial_state))):
         return ssm_scan_fwd(u, dt, A, B, C, D, z, dt_bias, dt_softplus, initial_state, cu_seqlens)
     return _functions()["scan"].apply(u, dt, A, B, C, D, z, dt_bias, initial_state, dt_softplus, cu_seqlens)
+
+
+def gated_scan(x, r, i, lam, rate=8.0, initial_state=None, cu_seqlens=None):
+    """gated_scan_fwd with autograd (x, r, i, lam, initial_state).  Returns (h,
+    final_state).  The states for the backward are kept where one can follow."""
+    if not (torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, r, i, lam, initial_state))):
+        return gated_scan_fwd(x, r, i, lam, rate, initial_state, cu_seqlens)
+    return _functions()["gated"].apply(x, r, i, lam, initial_state, rate, cu_seqlens)
 
 
 def group_norm(x, weight=None, bias=None, gate=None, groups=1, eps=1e-6, activation="silu", center=False,

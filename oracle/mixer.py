@@ -174,3 +174,64 @@ def norm_bwd(x, dy, w=None, b=None, gate=None, groups=1, eps=1e-6, kind="silu", 
         d = d * act(gate, kind)
     res["dx"] = d
     return res
+
+
+# ----------------------------------------------------------------------------
+# gated linear recurrence
+# ----------------------------------------------------------------------------
+
+def _gated_rows(x, cu):
+    if cu is None:
+        return [(b, 0, x.shape[1]) for b in range(x.shape[0])]
+    return [(0, a, b) for a, b in zip(cu[:-1], cu[1:])]
+
+
+def _sig(x):
+    return np.exp(-np.logaddexp(0.0, -x))
+
+
+def gated_fwd(x, r, i, lam, rate=8.0, h0=None, cu=None):
+    """h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(i_t) x_t, token by token, with
+    a_t = exp(-rate softplus(lam) sigmoid(r_t)).  Returns (h, final states)."""
+    rows = _gated_rows(x, cu)
+    y = np.zeros(x.shape)
+    fs = np.zeros((len(rows), x.shape[2])) if h0 is None else h0.astype(np.float64).copy()
+    L = -rate * np.logaddexp(0.0, lam) * _sig(r)
+    a, m = np.exp(L), np.sqrt(-np.expm1(2 * L))
+    for n, (b, t0, t1) in enumerate(rows):
+        h = fs[n]
+        for t in range(t0, t1):
+            h = a[b, t] * h + m[b, t] * _sig(i[b, t]) * x[b, t]
+            y[b, t] = h
+        fs[n] = h
+    return y, fs
+
+
+def gated_bwd(x, r, i, lam, dy, rate=8.0, h0=None, cu=None, dfs=None):
+    """Its reverse mode, token by token."""
+    y, _ = gated_fwd(x, r, i, lam, rate, h0, cu)
+    sr, si, sp = _sig(r), _sig(i), np.logaddexp(0.0, lam)
+    L = -rate * sp * sr
+    a, m = np.exp(L), np.sqrt(-np.expm1(2 * L))
+    rows = _gated_rows(x, cu)
+    res = {k: np.zeros(x.shape) for k in ("dx", "dr", "di")}
+    res["dlam"] = np.zeros(lam.shape)
+    d0 = np.zeros((len(rows), x.shape[2]))
+    for n, (b, t0, t1) in enumerate(rows):
+        c = np.zeros(x.shape[2]) if dfs is None else dfs[n].astype(np.float64)
+        for t in range(t1 - 1, t0 - 1, -1):
+            dh = dy[b, t] + c
+            past = y[b, t - 1] if t > t0 else (np.zeros(x.shape[2]) if h0 is None else h0[n])
+            at, mt = a[b, t], m[b, t]
+            with np.errstate(divide="ignore", invalid="ignore"):
+                slope = np.where(mt > 0, -at * at / mt, 0.0)
+            dL = dh * (at * past + slope * si[b, t] * x[b, t])
+            res["dx"][b, t] = dh * mt * si[b, t]
+            res["di"][b, t] = dh * mt * x[b, t] * si[b, t] * (1 - si[b, t])
+            res["dr"][b, t] = dL * L[b, t] * (1 - sr[b, t])
+            res["dlam"] += dL * -rate * sr[b, t] * _sig(lam)
+            c = at * dh
+        d0[n] = c
+    if h0 is not None:
+        res["d_initial_state"] = d0
+    return res
