@@ -694,6 +694,68 @@ GDN_API gdn_status gdn_rope_bwd(const void* q, int64_t q_stride, const void* k, 
                                 void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /*
+ * Causal attention with a sliding window and first tokens that stay visible:
+ * token i of a sequence sees j <= i with i - j < window or j < sinks.
+ *     out_i = sum_j softmax_j(scale q_i . k_j) v_j
+ * Query head h reads key head h / (H / Hk).  bf16, fp32 sums and statistics; the
+ * softmax's weights are rounded to bf16 as operands of the second product.
+ *   q (B,T,H,d), k, v (B,T,Hk,d) (strided), here on 16-byte boundaries with
+ *             strides of a multiple of 8 elements
+ *   out       (B,T,H,d)
+ *   lse       NULL, or fp32 (B,H,T) (packed: (1,H,T)): the log of the sum of
+ *             exp(scale q_i . k_j) over the keys that token i sees
+ *   window >= 1, scale > 0, 0 <= sinks <= 128, H a multiple of Hk, H <= 1024,
+ *   d in {64, 128}, B T < 2^31 - 256
+ * A token that another does not see has no part in that one's output, whatever
+ * it holds (NaN and infinities included).
+ */
+GDN_API gdn_status gdn_window_fwd(const gdn_bf16* q, int64_t q_stride, const gdn_bf16* k, int64_t k_stride,
+                                  const gdn_bf16* v, int64_t v_stride, const int32_t* cu_seqlens, gdn_bf16* out,
+                                  float* lse, int B, int T, int H, int Hk, int d, int window, int sinks, float scale,
+                                  cudaStream_t stream);
+
+/*
+ * Reverse mode of gdn_window_fwd from its inputs, its out and its lse: d_out
+ * (B,T,H,d) in; dq (B,T,H,d), dk and dv (B,T,Hk,d) out, dense.  The gradients
+ * of a key head are summed over its query heads in a fixed order.  A NaN or an
+ * infinity stays in its sequence, but may reach tokens of it up to 128 away
+ * that do not see it.
+ */
+GDN_API size_t gdn_window_bwd_workspace_size(int B, int T, int H, int Hk, int d, int window, int sinks, int varlen);
+GDN_API gdn_status gdn_window_bwd(const gdn_bf16* q, int64_t q_stride, const gdn_bf16* k, int64_t k_stride,
+                                  const gdn_bf16* v, int64_t v_stride, const int32_t* cu_seqlens, const gdn_bf16* out,
+                                  const float* lse, const gdn_bf16* d_out, gdn_bf16* dq, gdn_bf16* dk, gdn_bf16* dv,
+                                  int B, int T, int H, int Hk, int d, int window, int sinks, float scale,
+                                  void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * One token per row on a cache of sinks + window rows a sequence: the token at
+ * position p = lengths[b] writes its key and value to row p (p < sinks) or sinks
+ * + (p - sinks) % window, and looks at the min(p + 1, sinks + window) rows that
+ * hold tokens: those that it sees.
+ *   q, out (B,H,d), k, v (B,Hk,d) (q, k, v strided, on 16-byte boundaries)
+ *   k_cache, v_cache (S,sinks + window,Hk,d), updated in place
+ *   lengths   (B) int32: the tokens that each row's sequence has behind it; not
+ *             changed.  Negative: an idle row (out is zero, no cache changes).
+ *   slots     as in gdn_conv_step
+ */
+GDN_API gdn_status gdn_window_step(const gdn_bf16* q, int64_t q_stride, const gdn_bf16* k, int64_t k_stride,
+                                   const gdn_bf16* v, int64_t v_stride, gdn_bf16* k_cache, gdn_bf16* v_cache,
+                                   const int32_t* lengths, const int32_t* slots, gdn_bf16* out, int B, int S, int H,
+                                   int Hk, int d, int window, int sinks, float scale, cudaStream_t stream);
+
+/*
+ * What prompts leave in such caches: of each sequence's keys and values (B,T,
+ * Hk,d) (strided, on 16-byte boundaries) the rows that its next token looks at.
+ * Rows that hold no token keep what they have.  slots (B or, packed, N): the
+ * cache of each sequence, negative for none; NULL: cache n.
+ */
+GDN_API gdn_status gdn_window_fill(const gdn_bf16* k, int64_t k_stride, const gdn_bf16* v, int64_t v_stride,
+                                   const int32_t* cu_seqlens, const int32_t* slots, gdn_bf16* k_cache,
+                                   gdn_bf16* v_cache, int B, int T, int S, int Hk, int d, int window, int sinks,
+                                   cudaStream_t stream);
+
+/*
  * Number of CUDA kernels this library has launched in this process so far
  * (all devices, all entry points).  Library bookkeeping with no counterpart
  * on the pages; lets a caller count the kernels inside a timed region.

@@ -1,5 +1,7 @@
 """The operators of the attention layers that a linear-attention model puts
-between its others: the norm and rotation of queries and keys.
+between its others: the norm and rotation of queries and keys, and attention
+with a sliding window and first tokens that stay visible, for prompts, for
+training, and token by token on a cache of fixed size.
 
 As in mixer.py, nothing is computed here: arguments are checked and handed to
 the CUDA kernels of ``_build/libgdn.so`` (include/gdn.h has the formulas and
@@ -18,6 +20,8 @@ from .gdn import _check, _on_stream, _workspace, load
 from .mixer import _aligned, _current, _dense, _dtype, _is, _on_gpu, _out, _rows, _sequences
 
 HEAD_SIZES = (32, 64, 128, 256)
+WINDOW_HEAD_SIZES = (64, 128)
+MAX_SINKS = 128
 
 
 # ----------------------------------------------------------------------------
@@ -93,6 +97,147 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight=None, k_weight=None, inv_fre
 
 
 # ----------------------------------------------------------------------------
+# attention with a sliding window and first tokens that stay visible
+# ----------------------------------------------------------------------------
+
+def _pieces(x, width):
+    """(tensor, address, row stride) of rows of heads that the kernels copy in
+    16-byte pieces; as a copy where they lie elsewhere."""
+    at, stride = _rows(x, width, 2)
+    if at & 15 or stride & 7:
+        x = x.contiguous() if not x.is_contiguous() else x.clone()
+        at, stride = x.data_ptr(), width
+    return x, at, stride
+
+
+def _window_args(q, k, v, window, sinks, scale, dims):
+    """Checks shared by the attention and its step (q of 4 or 3 dimensions).
+    The tensors of the answer are held until the launch."""
+    if q.dim() != dims or k.dim() != dims:
+        raise ValueError(f"q and k must be {'(B, T, heads, d)' if dims == 4 else '(B, heads, d)'}, "
+                         f"got shapes {tuple(q.shape)} and {tuple(k.shape)}")
+    if q.dtype is not torch.bfloat16:
+        raise ValueError(f"q must be {torch.bfloat16}, got {q.dtype}")
+    dev, shape = q.get_device(), q.shape
+    H, d, Hk = shape[-2], shape[-1], k.shape[-2]
+    kv = shape[:-2] + (Hk, d)
+    _is("k", k, kv, q.dtype, dev)
+    _is("v", v, kv, q.dtype, dev)
+    if d not in WINDOW_HEAD_SIZES:
+        raise ValueError(f"the head size must be one of {WINDOW_HEAD_SIZES}, got {d}")
+    if Hk < 1 or H % Hk or H < 1:
+        raise ValueError(f"the {H} query heads must divide into the {Hk} key heads")
+    _window_sizes(window, sinks)
+    scale = d ** -0.5 if scale is None else float(scale)
+    if not scale > 0:
+        raise ValueError(f"scale must be positive, got {scale}")
+    _on_gpu(dev, q)
+    held = [_pieces(q, H * d), _pieces(k, Hk * d), _pieces(v, Hk * d)]
+    return dev, held, [a for _, *at in held for a in at], H, Hk, d, scale
+
+
+def _window_sizes(window, sinks):
+    if window < 1:
+        raise ValueError(f"window must be at least 1 (a token sees itself), got {window}")
+    if not 0 <= sinks <= MAX_SINKS:
+        raise ValueError(f"sinks must be in 0 .. {MAX_SINKS}, got {sinks}")
+
+
+def window_attention_fwd(q, k, v, window, sinks=0, scale=None, cu_seqlens=None, save_for_backward=False, stream=None):
+    """Causal attention in which token i sees j <= i with i - j < window or
+    j < sinks: q (B, T, H, d), k and v (B, T, Hk, d) bf16, H a multiple of Hk
+    (query head h reads key head h // (H // Hk)), scale by default d^-1/2.  All
+    three may be slices of one projection.  Returns out (B, T, H, d), or (out,
+    lse) with save_for_backward: lse (B, H, T) fp32, the log of each row's sum."""
+    if stream is not None:
+        return _on_stream(window_attention_fwd, locals())
+    dev, held, args, H, Hk, d, scale = _window_args(q, k, v, window, sinks, scale, 4)
+    n, cu = _sequences(q, cu_seqlens, dev, "q")
+    B, T = q.shape[:2]
+    out = q.new_empty(q.shape)
+    lse = torch.empty((B, H, T), dtype=torch.float32, device=q.device) if save_for_backward else None
+    _check(load().gdn_window_fwd(*args, cu, out.data_ptr(), None if lse is None else lse.data_ptr(), n, T, H, Hk, d,
+                                 min(window, max(T, 1)), sinks, scale, _current(dev)), "gdn_window_fwd")
+    return (out, lse) if save_for_backward else out
+
+
+def window_attention_bwd(q, k, v, out, lse, d_out, window, sinks=0, scale=None, cu_seqlens=None, stream=None):
+    """Gradients of window_attention_fwd from its inputs and the (out, lse) that
+    it returned: a dict of dq, dk and dv."""
+    if stream is not None:
+        return _on_stream(window_attention_bwd, locals())
+    out, lse, d_out = _aligned(out, lse, d_out)
+    dev, held, args, H, Hk, d, scale = _window_args(q, k, v, window, sinks, scale, 4)
+    n, cu = _sequences(q, cu_seqlens, dev, "q")
+    B, T = q.shape[:2]
+    o = _dense("out", out, q.shape, q.dtype, dev)
+    s = _dense("lse", lse, (B, H, T), torch.float32, dev)
+    g = _dense("d_out", d_out, q.shape, q.dtype, dev)
+    res = {"dq": q.new_empty(q.shape), "dk": k.new_empty(k.shape), "dv": v.new_empty(v.shape)}
+    window = min(window, max(T, 1))
+    lib = load()
+    nbytes = lib.gdn_window_bwd_workspace_size(n, T, H, Hk, d, window, sinks, int(cu_seqlens is not None))
+    ws = _workspace(nbytes, q.device)
+    _check(lib.gdn_window_bwd(*args, cu, o, s, g, res["dq"].data_ptr(), res["dk"].data_ptr(), res["dv"].data_ptr(), n, T,
+                              H, Hk, d, window, sinks, scale, None if ws is None else ws.data_ptr(), nbytes,
+                              _current(dev)), "gdn_window_bwd")
+    return res
+
+
+def _cache(name, t, like, Hk, d, sinks, dev):
+    if t.dim() != 4 or t.shape[1] <= sinks or (like is not None and t.shape != like.shape):
+        raise ValueError(f"the caches must be (S, sinks + window, {Hk}, {d}) alike, got {name} of shape {tuple(t.shape)}")
+    at = _dense(name, t, (t.shape[0], t.shape[1], Hk, d), torch.bfloat16, dev)
+    if at & 15:
+        raise ValueError(f"{name} must start at a 16-byte boundary: it is updated in place")
+    return at
+
+
+def window_attention_step(q, k, v, k_cache, v_cache, lengths, sinks=0, scale=None, slots=None, stream=None):
+    """One token per row: q (B, H, d), k and v (B, Hk, d), and caches (S, sinks +
+    window, Hk, d) that hold token p in row p, from p = sinks on in row sinks +
+    (p - sinks) % window.  lengths (B, int32): the tokens that each row's sequence
+    has behind it, so the position of this one, whose key and value are written
+    into the caches (lengths stays; negative: an idle row, whose output is zero).
+    slots as in mixer.short_conv_step.  Returns out (B, H, d)."""
+    if stream is not None:
+        return _on_stream(window_attention_step, locals())
+    dev, held, args, H, Hk, d, scale = _window_args(q, k, v, 1, sinks, scale, 3)
+    B = q.shape[0]
+    kc = _cache("k_cache", k_cache, None, Hk, d, sinks, dev)
+    vc = _cache("v_cache", v_cache, k_cache, Hk, d, sinks, dev)
+    S, rows = k_cache.shape[:2]
+    if slots is None and S < B:
+        raise ValueError(f"the caches hold {S} rows for a batch of {B}")
+    ln = _dense("lengths", lengths, (B,), torch.int32, dev)
+    sl = _dense("slots", slots, (B,), torch.int32, dev)
+    out = q.new_empty(q.shape)
+    _check(load().gdn_window_step(*args, kc, vc, ln, sl, out.data_ptr(), B, S, H, Hk, d, rows - sinks, sinks, scale,
+                                  _current(dev)), "gdn_window_step")
+    return out
+
+
+def window_cache_fill(k, v, k_cache, v_cache, sinks=0, cu_seqlens=None, slots=None, stream=None):
+    """Puts what the next token of each prompt looks at into its cache (laid out
+    as in window_attention_step): k, v (B, T, Hk, d), slots (one per sequence,
+    int32; negative: none).  Rows that hold no token keep what they have."""
+    if stream is not None:
+        return _on_stream(window_cache_fill, locals())
+    if k.dim() != 4:
+        raise ValueError(f"k must be (B, T, heads, d), got shape {tuple(k.shape)}")
+    dev, held, args, _, Hk, d, _ = _window_args(k, k, v, 1, sinks, None, 4)
+    n, cu = _sequences(k, cu_seqlens, dev, "k")
+    kc = _cache("k_cache", k_cache, None, Hk, d, sinks, dev)
+    vc = _cache("v_cache", v_cache, k_cache, Hk, d, sinks, dev)
+    S, rows = k_cache.shape[:2]
+    if slots is None and S < n:
+        raise ValueError(f"the caches hold {S} rows for {n} sequences")
+    sl = _dense("slots", slots, (n,), torch.int32, dev)
+    _check(load().gdn_window_fill(*args[2:], cu, sl, kc, vc, n, k.shape[1], S, Hk, d, rows - sinks, sinks,
+                                  _current(dev)), "gdn_window_fill")
+
+
+# ----------------------------------------------------------------------------
 # autograd
 # ----------------------------------------------------------------------------
 
@@ -122,7 +267,22 @@ def _functions():
                                  cu_seqlens, *ctx.rest)
             return (r["dq"], r["dk"], r.get("dq_weight"), r.get("dk_weight")) + (None,) * 5
 
-    _FUNCTIONS.update(rope=QkNormRope)
+    class WindowAttention(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, q, k, v, window, sinks, scale, cu_seqlens):
+            out, lse = window_attention_fwd(q, k, v, window, sinks, scale, cu_seqlens, save_for_backward=True)
+            ctx.save_for_backward(q, k, v, out, lse, cu_seqlens)
+            ctx.rest = (window, sinks, scale)
+            return out
+
+        @staticmethod
+        @first_order
+        def backward(ctx, saved_tensors, d_out):
+            q, k, v, out, lse, cu_seqlens = saved_tensors
+            r = window_attention_bwd(q, k, v, out, lse, dense(d_out, q), *ctx.rest, cu_seqlens)
+            return (r["dq"], r["dk"], r["dv"]) + (None,) * 4
+
+    _FUNCTIONS.update(rope=QkNormRope, window=WindowAttention)
     return _FUNCTIONS
 
 
@@ -133,3 +293,11 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, inv_freq=None, positions=No
     if inv_freq is not None and inv_freq.requires_grad:
         raise ValueError("inv_freq has no gradient here: pass it detached")
     return _functions()["rope"].apply(q, k, q_weight, k_weight, inv_freq, positions, cu_seqlens, eps, interleaved)
+
+
+def window_attention(q, k, v, window, sinks=0, scale=None, cu_seqlens=None):
+    """window_attention_fwd with autograd (q, k, v).  The rows' sums are kept
+    where a backward can follow."""
+    if not (torch.is_grad_enabled() and any(t.requires_grad for t in (q, k, v))):
+        return window_attention_fwd(q, k, v, window, sinks, scale, cu_seqlens)
+    return _functions()["window"].apply(q, k, v, window, sinks, scale, cu_seqlens)

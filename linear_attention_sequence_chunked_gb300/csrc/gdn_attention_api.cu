@@ -46,6 +46,65 @@ gdn_status rope_args(gdn::RopeArgs& a, const void* q, int64_t q_stride, const vo
     return GDN_OK;
 }
 
+gdn_status check_window(int B, int T, int H, int Hk, int d, int window, int sinks, float scale) {
+    if (H < 1 || Hk < 1 || H % Hk != 0 || window < 1 || sinks < 0) return GDN_ERR_INVALID_ARG;
+    if (!(scale > 0.f) || scale > 3e38f) return GDN_ERR_INVALID_ARG;
+    if ((d != 64 && d != 128) || H > 1024 || sinks > gdn::kWindowMaxSinks) return GDN_ERR_UNSUPPORTED;
+    GDN_TRY(check_sizes(B, T, H * d, GDN_BF16));
+    // blocks of a grid, and the copies' row coordinates
+    const long long tokens = static_cast<long long>(B) * T;
+    if (tokens >= (1LL << 31) - 256 || (tokens / 32 + B) * H * (d / 8) >= (1LL << 31) * 8) return GDN_ERR_UNSUPPORTED;
+    return GDN_OK;
+}
+
+// An input that the kernels copy in 16-byte pieces: present, rows at least `row` apart.
+gdn_status check_pieces(const void* p, int64_t stride, int64_t row) {
+    if (!p || stride < row || stride >= (1LL << 38)) return GDN_ERR_INVALID_ARG;
+    return off16(p) || stride % 8 != 0 ? GDN_ERR_MISALIGNED : GDN_OK;
+}
+
+long long tile_slots(int B, int T, int rows, bool varlen) {
+    if (varlen) return static_cast<long long>(T / rows) + B;
+    return static_cast<long long>(B) * (T > rows ? (T + rows - 1) / rows : 1);
+}
+
+// What the backward keeps beside its outputs: delta, and the first tokens' partial sums.
+struct WindowLayout {
+    int window, sinks;  // no longer than the row; no first tokens where the window leaves none out
+    int far_tokens;
+    long long far_slots;
+    size_t far, total;
+};
+WindowLayout window_layout(int B, int T, int H, int Hk, int d, int window, int sinks, bool varlen) {
+    WindowLayout L{};
+    L.window = std::min(window, std::max(T, 1));
+    L.sinks = window >= T ? 0 : sinks;
+    const long long reach = (gdn::kWindowTile - 1 + static_cast<long long>(L.window) - 1) / gdn::kWindowTile + 1;
+    L.far_tokens = static_cast<int>(std::min<long long>(reach * gdn::kWindowTile, 1 << 30));
+    L.far_slots = L.sinks > 0 ? tile_slots(B, T, L.far_tokens, varlen) : 0;
+    L.far = round_up(sizeof(float) * (varlen ? 1 : B) * static_cast<size_t>(H) * T);
+    L.total = L.far + round_up(sizeof(float) * L.far_slots * Hk * 2 * L.sinks * d);
+    return L;
+}
+
+gdn_status window_args(gdn::WindowArgs& a, const WindowLayout& L, const gdn_bf16* q, int64_t q_stride, const gdn_bf16* k,
+                       int64_t k_stride, const gdn_bf16* v, int64_t v_stride, const int32_t* cu_seqlens, int B, int T,
+                       int H, int Hk, int d, float scale) {
+    const bool varlen = cu_seqlens != nullptr;
+    GDN_TRY(check_cu(cu_seqlens));
+    if (T > 0) {
+        GDN_TRY(check_pieces(q, q_stride, static_cast<int64_t>(H) * d));
+        GDN_TRY(check_pieces(k, k_stride, static_cast<int64_t>(Hk) * d));
+        GDN_TRY(check_pieces(v, v_stride, static_cast<int64_t>(Hk) * d));
+    }
+    a.q = q; a.k = k; a.v = v; a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride;
+    a.cu_seqlens = cu_seqlens; a.tokens = varlen ? T : static_cast<long long>(B) * T;
+    a.nseq = B; a.T = T; a.H = H; a.Hk = Hk; a.d = d; a.window = L.window; a.sinks = L.sinks; a.scale = scale;
+    a.far_tokens = L.far_tokens; a.far_slots = L.far_slots;
+    if (T > 0 && !(a.err = gdn::device_error_word())) return GDN_ERR_CUDA;
+    return GDN_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -96,6 +155,94 @@ gdn_status gdn_rope_bwd(const void* q, int64_t q_stride, const void* k, int64_t 
     c.rows = static_cast<int>(a.blocks);
     c.out[0] = dq_weight; c.out[1] = dk_weight;
     return gdn::count_launch(gdn::launch_column_sum(c, stream)) ? GDN_OK : GDN_ERR_CUDA;
+}
+
+gdn_status gdn_window_fwd(const gdn_bf16* q, int64_t q_stride, const gdn_bf16* k, int64_t k_stride, const gdn_bf16* v,
+                          int64_t v_stride, const int32_t* cu_seqlens, gdn_bf16* out, float* lse, int B, int T, int H,
+                          int Hk, int d, int window, int sinks, float scale, cudaStream_t stream) {
+    GDN_TRY(check_window(B, T, H, Hk, d, window, sinks, scale));
+    gdn::WindowArgs a{};
+    const bool varlen = cu_seqlens != nullptr;
+    GDN_TRY(window_args(a, window_layout(B, T, H, Hk, d, window, sinks, varlen), q, q_stride, k, k_stride, v, v_stride,
+                        cu_seqlens, B, T, H, Hk, d, scale));
+    GDN_TRY(check_dense({out, lse}));
+    if (T == 0) return GDN_OK;
+    if (!out) return GDN_ERR_INVALID_ARG;
+    a.out = out; a.lse = lse;
+    a.slots = tile_slots(B, T, gdn::window_fwd_rows(H, Hk), varlen);
+    return gdn::count_launch(gdn::launch_window_fwd(a, stream)) ? GDN_OK : GDN_ERR_CUDA;
+}
+
+size_t gdn_window_bwd_workspace_size(int B, int T, int H, int Hk, int d, int window, int sinks, int varlen) {
+    if (check_window(B, T, H, Hk, d, window, sinks, 1.f) != GDN_OK) return 0;
+    return window_layout(B, T, H, Hk, d, window, sinks, varlen != 0).total;
+}
+
+gdn_status gdn_window_bwd(const gdn_bf16* q, int64_t q_stride, const gdn_bf16* k, int64_t k_stride, const gdn_bf16* v,
+                          int64_t v_stride, const int32_t* cu_seqlens, const gdn_bf16* out, const float* lse,
+                          const gdn_bf16* d_out, gdn_bf16* dq, gdn_bf16* dk, gdn_bf16* dv, int B, int T, int H, int Hk,
+                          int d, int window, int sinks, float scale, void* workspace, size_t workspace_bytes,
+                          cudaStream_t stream) {
+    GDN_TRY(check_window(B, T, H, Hk, d, window, sinks, scale));
+    gdn::WindowArgs a{};
+    const bool varlen = cu_seqlens != nullptr;
+    const WindowLayout L = window_layout(B, T, H, Hk, d, window, sinks, varlen);
+    GDN_TRY(window_args(a, L, q, q_stride, k, k_stride, v, v_stride, cu_seqlens, B, T, H, Hk, d, scale));
+    GDN_TRY(check_dense({out, lse, d_out, dq, dk, dv}));
+    if (T == 0) return GDN_OK;
+    if (!out || !lse || !d_out || !dq || !dk || !dv) return GDN_ERR_INVALID_ARG;
+    GDN_TRY(check_ws(workspace, workspace_bytes, L.total));
+    a.out = const_cast<gdn_bf16*>(out); a.lse = const_cast<float*>(lse); a.d_out = d_out;
+    a.dq = dq; a.dk = dk; a.dv = dv;
+    a.delta = static_cast<float*>(workspace);
+    a.far_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + L.far);
+    a.slots = tile_slots(B, T, gdn::kWindowTile, varlen);
+    return gdn::count_launch(gdn::launch_window_bwd(a, stream), L.sinks > 0 ? 4 : 3) ? GDN_OK : GDN_ERR_CUDA;
+}
+
+gdn_status gdn_window_step(const gdn_bf16* q, int64_t q_stride, const gdn_bf16* k, int64_t k_stride, const gdn_bf16* v,
+                           int64_t v_stride, gdn_bf16* k_cache, gdn_bf16* v_cache, const int32_t* lengths,
+                           const int32_t* slots, gdn_bf16* out, int B, int S, int H, int Hk, int d, int window,
+                           int sinks, float scale, cudaStream_t stream) {
+    GDN_TRY(check_window(B, 1, H, Hk, d, window, sinks, scale));
+    if (window > gdn::checks::kMaxT) return GDN_ERR_UNSUPPORTED;
+    if (!k_cache || !v_cache || !lengths || !out || S < 1 || (!slots && S < B)) return GDN_ERR_INVALID_ARG;
+    GDN_TRY(check_pieces(q, q_stride, static_cast<int64_t>(H) * d));
+    GDN_TRY(check_pieces(k, k_stride, static_cast<int64_t>(Hk) * d));
+    GDN_TRY(check_pieces(v, v_stride, static_cast<int64_t>(Hk) * d));
+    GDN_TRY(check_dense({k_cache, v_cache, out}));
+    GDN_TRY(check_cu(lengths));
+    GDN_TRY(check_cu(slots));
+    gdn::WindowStepArgs a{};
+    if (!(a.err = gdn::device_error_word())) return GDN_ERR_CUDA;
+    a.q = q; a.k = k; a.v = v; a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride;
+    a.k_cache = k_cache; a.v_cache = v_cache; a.lengths = lengths; a.slots = slots; a.out = out;
+    a.B = B; a.S = S; a.H = H; a.Hk = Hk; a.d = d; a.rows = sinks + window; a.window = window; a.sinks = sinks;
+    a.scale = scale;
+    a.cluster = gdn::window_step_cluster(B, Hk, (H / Hk + 15) / 16, a.rows);
+    return gdn::count_launch(gdn::launch_window_step(a, stream)) ? GDN_OK : GDN_ERR_CUDA;
+}
+
+gdn_status gdn_window_fill(const gdn_bf16* k, int64_t k_stride, const gdn_bf16* v, int64_t v_stride,
+                           const int32_t* cu_seqlens, const int32_t* slots, gdn_bf16* k_cache, gdn_bf16* v_cache, int B,
+                           int T, int S, int Hk, int d, int window, int sinks, cudaStream_t stream) {
+    GDN_TRY(check_window(B, T, Hk, Hk, d, window, sinks, 1.f));
+    if (window > gdn::checks::kMaxT) return GDN_ERR_UNSUPPORTED;
+    if (!k_cache || !v_cache || S < 1 || (!slots && S < B)) return GDN_ERR_INVALID_ARG;
+    if (T > 0) {
+        GDN_TRY(check_pieces(k, k_stride, static_cast<int64_t>(Hk) * d));
+        GDN_TRY(check_pieces(v, v_stride, static_cast<int64_t>(Hk) * d));
+    }
+    GDN_TRY(check_dense({k_cache, v_cache}));
+    GDN_TRY(check_cu(cu_seqlens));
+    GDN_TRY(check_cu(slots));
+    if (T == 0) return GDN_OK;
+    gdn::WindowFillArgs a{};
+    if (!(a.err = gdn::device_error_word())) return GDN_ERR_CUDA;
+    a.k = k; a.v = v; a.k_stride = k_stride; a.v_stride = v_stride; a.k_cache = k_cache; a.v_cache = v_cache;
+    a.cu_seqlens = cu_seqlens; a.slots = slots; a.nseq = B; a.T = T; a.S = S; a.Hk = Hk; a.d = d; a.window = window;
+    a.sinks = sinks;
+    return gdn::count_launch(gdn::launch_window_fill(a, stream)) ? GDN_OK : GDN_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -552,6 +552,65 @@ long long rope_blocks(long long tokens, int heads, bool backward);
 cudaError_t launch_rope_fwd(const RopeArgs& a, cudaStream_t stream);
 cudaError_t launch_rope_bwd(const RopeArgs& a, cudaStream_t stream);
 
+// Window attention, bf16 heads of d channels.
+struct WindowArgs {
+    const uint16_t* q;            // (tokens, H, d), tokens q_stride apart
+    const uint16_t* k;            // (tokens, Hk, d); v likewise
+    const uint16_t* v;
+    long long q_stride, k_stride, v_stride;
+    uint16_t* out;                // (tokens, H, d); read by the backward
+    float* lse;                   // (batch rows, H, T) or null; read by the backward
+    const int32_t* cu_seqlens;
+    const uint16_t* d_out;        // backward, from here
+    uint16_t* dq;
+    uint16_t* dk;
+    uint16_t* dv;
+    float* delta;                 // (batch rows, H, T)
+    float* far_part;              // [far_slots][Hk][2][sinks][d]: dV and dK of the first tokens
+    long long tokens, slots;      // slots: tiles of queries (backward: of keys), as find_block counts them
+    long long far_slots;          // stretches of far_tokens queries, likewise
+    int far_tokens;
+    int nseq, T, H, Hk, d;
+    int window, sinks;
+    float scale;
+    int* err;
+};
+int window_fwd_rows(int H, int Hk);  // queries per block of the forward
+constexpr int kWindowTile = 128;
+constexpr int kWindowMaxSinks = 128;
+cudaError_t launch_window_fwd(const WindowArgs& a, cudaStream_t stream);
+cudaError_t launch_window_bwd(const WindowArgs& a, cudaStream_t stream);
+struct WindowStepArgs {
+    const uint16_t* q;            // (B, H, d), rows q_stride apart
+    const uint16_t* k;            // (B, Hk, d); v likewise
+    const uint16_t* v;
+    long long q_stride, k_stride, v_stride;
+    uint16_t* k_cache;            // (S, rows, Hk, d)
+    uint16_t* v_cache;
+    const int32_t* lengths;       // (B)
+    const int32_t* slots;         // (B) or null
+    uint16_t* out;                // (B, H, d)
+    int B, S, H, Hk, d;
+    int rows, window, sinks;
+    float scale;
+    int cluster;
+    int* err;
+};
+int window_step_cluster(int B, int Hk, int sets, int rows);
+cudaError_t launch_window_step(const WindowStepArgs& a, cudaStream_t stream);
+struct WindowFillArgs {
+    const uint16_t* k;            // (tokens, Hk, d), tokens k_stride apart; v likewise
+    const uint16_t* v;
+    long long k_stride, v_stride;
+    uint16_t* k_cache;
+    uint16_t* v_cache;
+    const int32_t* cu_seqlens;
+    const int32_t* slots;         // (nseq) or null
+    int nseq, T, S, Hk, d, window, sinks;
+    int* err;
+};
+cudaError_t launch_window_fill(const WindowFillArgs& a, cudaStream_t stream);
+
 // The library's per-device error word and its count of launched kernels
 // (gdn_api.cu), for the other files of the C ABI.
 int* device_error_word();

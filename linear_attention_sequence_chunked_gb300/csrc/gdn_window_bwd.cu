@@ -1,0 +1,639 @@
+// Attention with a sliding window and first tokens that stay visible: reverse
+// mode.  With delta_i = dout_i . out_i (a kernel of its own),
+//
+//   P = exp(S - lse),  dP = dout V^T,  dS = P (dP - delta)
+//   dV = P^T dout,  dK = scale dS^T Q,  dQ = scale dS K
+//
+// in two kernels, one that owns a tile of keys and one that owns a tile of
+// queries, each of which forms S and dP for itself: seven products instead of
+// five, but every gradient is summed by one block in one order, without atomics.
+// All products run on the tensor cores; P and dS are rounded to bf16 as operands
+// (half a step of 2^-8 each, in random directions) and stay in tensor memory,
+// written over the S and dP that they come from.
+//
+// The first tokens that stay visible are seen by every later query.  Their
+// share beyond the reach of their own tile's window is cut into stretches of
+// queries, one block each, whose fp32 sums a last kernel adds in order.
+#include <cmath>
+
+#include "gdn_window_common.cuh"
+
+namespace gdn {
+
+namespace {
+
+using namespace win;
+
+constexpr int kThreads = 320;  // warps 0-7: elementwise work; 8: copies; 9: products
+
+// A warp's 32 rows of an accumulator (D columns), times `mul`, as bf16 rows of
+// `out`, rows `stride` elements apart, the first `rows` of them; through `mine`,
+// the warp's own shared memory.
+template <int D>
+__device__ __forceinline__ void store_rows(uint32_t t, float mul, uint8_t* mine, uint16_t* out, long long stride, int first,
+                                           int rows, int lane) {
+#pragma unroll
+    for (int g = 0; g < D; g += 32) {
+        uint32_t o[32];
+        tmem_ld32(t + g, o);
+        tmem_ld_wait();
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                w[e] = cvt_bf16x2(__uint_as_float(o[8 * q + 2 * e]) * mul, __uint_as_float(o[8 * q + 2 * e + 1]) * mul);
+            *reinterpret_cast<uint4*>(mine + lane * (D * 2) + (((g / 8 + q) ^ (lane & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+    __syncwarp();
+    constexpr int kChunks = D / 8;
+#pragma unroll 4
+    for (int k = 0; k < kChunks; ++k) {
+        const int r = (k * 32 + lane) / kChunks, ch = (k * 32 + lane) % kChunks;
+        const uint4 w = *reinterpret_cast<const uint4*>(mine + r * (D * 2) + ((ch ^ (r & 7)) * 16));
+        if (r >= first && r < rows) *reinterpret_cast<uint4*>(out + r * stride + ch * 8) = w;
+    }
+}
+
+// ------------------------------------------------------------------ delta
+
+// delta[b][h][t] = dout . out, D / 8 lanes to a row.
+template <int D>
+__global__ void __launch_bounds__(256) window_delta_kernel(const WindowArgs p) {
+    constexpr int LANES = D / 8;
+    const long long row = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) / LANES;  // (token, head)
+    const long long rows = p.tokens * p.H;
+    const bool on = row < rows;
+    const long long o = row * D + (threadIdx.x % LANES) * 8;
+    const mix::Raw<uint16_t, 8> a = mix::load_raw<uint16_t, 8>(p.out + o, on ? 8 : 0), b = mix::load_raw<uint16_t, 8>(p.d_out + o, on ? 8 : 0);
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s = fmaf(a.get(e), b.get(e), s);
+#pragma unroll
+    for (int m = LANES / 2; m > 0; m /= 2) s += __shfl_xor_sync(0xffffffffu, s, m);
+    if (on && threadIdx.x % LANES == 0) {
+        const long long tok = row / p.H, h = row % p.H;
+        p.delta[(tok / p.T * p.H + h) * p.T + tok % p.T] = s;
+    }
+}
+
+// ------------------------------------------------------------------ dK, dV
+
+enum { kvIn = 0, kvQ = 1, kvQFree = 3, kvG = 5, kvGFree = 7, kvS = 9, kvP = 10, kvDP = 11, kvDS = 12, kvDone = 13, kvTail = 14, kvBars = 15 };
+
+template <int D>
+struct KvSmem {
+    static constexpr int kTileBytes = kSlab * (D / 64);
+    static constexpr int k = 0, v = kTileBytes, q = 2 * kTileBytes, g = 4 * kTileBytes, stats = 6 * kTileBytes;
+    static constexpr int bars = stats + 2 * 2 * kTile * 4;
+    static constexpr int misc = bars + kvBars * 8;
+    static constexpr int total = misc + 32 + 1024;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    window_dkv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                      const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_g, const WindowArgs p) {
+    using L = KvSmem<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* sm = smem_raw + smem_align_pad(smem_raw);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::bars);
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + L::misc);
+    volatile int* stop = reinterpret_cast<volatile int*>(sm + L::misc + 4);
+    float* stats = reinterpret_cast<float*>(sm + L::stats);  // [2][lse, delta][kTile]
+    auto bar = [&](int i) { return smem_u32(&bars[i]); };
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (blockIdx.x == 0) mix::check_offsets(p.cu_seqlens, p.nseq, p.T, p.err);
+
+    // a tile of keys and the tiles of queries [qa, qb) that its block looks at:
+    // those in reach of the tile's own window, or a stretch that sees only the
+    // first tokens of block 0
+    const int G = p.H / p.Hk;
+    const int hk = blockIdx.x % p.Hk;
+    long long slot = blockIdx.x / p.Hk;
+    const int reach = (kTile - 1 + p.window - 1) / kTile + 1;  // tiles that a tile's keys reach, its own included
+    const bool far = slot >= p.slots;
+    int n, b, t0, t1;
+    long long c;
+    if (!mix::find_block(p.cu_seqlens, p.nseq, p.T, far ? p.far_tokens : kTile, far ? slot - p.slots : slot, p.err, n, c)) return;
+    if (!mix::token_range(p.cu_seqlens, n, p.nseq, p.T, p.err, b, t0, t1)) return;
+    const int len = t1 - t0, tiles = (len + kTile - 1) / kTile;
+    if (c * (far ? p.far_tokens : kTile) >= len || (far && c == 0)) return;
+    const int j0 = far ? 0 : static_cast<int>(c) * kTile;
+    const int qa = far ? static_cast<int>(c) * reach : j0 / kTile;
+    const int qb = min(tiles, qa + reach), nq = qb - qa;
+    const int steps = nq * G;
+    const long long row0 = static_cast<long long>(b) * p.T + t0;
+    // first tokens, to be joined: where the sums of this block go
+    const int joined = j0 == 0 ? min(p.sinks, len) : 0;
+    float* part = nullptr;
+    if (joined > 0) {
+        const long long base = p.cu_seqlens ? static_cast<long long>(t0 / p.far_tokens) + n
+                                            : static_cast<long long>(n) * (p.T > p.far_tokens ? (p.T + p.far_tokens - 1) / p.far_tokens : 1);
+        part = p.far_part + ((base + (far ? c : 0)) * p.Hk + hk) * 2 * p.sinks * D;
+    }
+
+    if (warp == 9) {
+        tmem_alloc(smem_u32(tslot), 512);
+        tmem_relinquish();
+    }
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kvBars; ++i) mbar_init(bar(i), i == kvP || i == kvDS ? 8 : 1);
+        fence_mbar_init();
+        *stop = 0;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tslot;
+    constexpr uint32_t cS = 0, cDP = 128, cDV = 256, cDK = 384;
+    const auto wait = [&](int i, int parity) {
+        if (*stop) return false;
+        if (mbar_wait(bar(i), parity)) return true;
+        *stop = 1;
+        return false;
+    };
+
+    if (warp == 8) {
+        int tails = 0, lq = 0, lg = 0;
+        if (lane == 0) {
+            mbar_arrive_expect_tx(bar(kvIn), 2 * L::kTileBytes);
+            for (int s = 0; s < D / 64; ++s) {
+                tma_load_3d(smem_u32(sm + L::k + s * kSlab), &map_k, 64 * s, hk, static_cast<int>(row0 + j0), bar(kvIn));
+                tma_load_3d(smem_u32(sm + L::v + s * kSlab), &map_v, 64 * s, hk, static_cast<int>(row0 + j0), bar(kvIn));
+            }
+        }
+        bool ok = true;
+        for (int i = 0; i < steps && ok; ++i) {
+            const int h = hk * G + i / nq, i0 = (qa + i % nq) * kTile, st = i & 1, ph = ((i >> 1) & 1) ^ 1;
+            const int row = static_cast<int>(row0 + i0), valid = min(kTile, len - i0);
+            ok = i < 2 || __all_sync(0xffffffffu, wait(kvQFree + st, ph));
+            if (ok) ok = load_tile<D>(sm + L::q + st * L::kTileBytes, &map_q, h, row, valid, bar(kvQ + st), bar(kvTail), tails, lane);
+            if (!ok) break;
+            lq = i + 1;
+            ok = i < 2 || __all_sync(0xffffffffu, wait(kvGFree + st, ph));
+            if (ok) ok = load_tile<D>(sm + L::g + st * L::kTileBytes, &map_g, h, row, valid, bar(kvG + st), bar(kvTail), tails, lane);
+            if (!ok) break;
+            lg = i + 1;
+        }
+        if (!ok) *stop = 1;
+        // every copy has landed before the block may leave
+        mbar_wait(bar(kvIn), 0);
+        for (int i = max(0, lq - 2); i < lq; ++i) mbar_wait(bar(kvQ + (i & 1)), (i >> 1) & 1);
+        for (int i = max(0, lg - 2); i < lg; ++i) mbar_wait(bar(kvG + (i & 1)), (i >> 1) & 1);
+        __syncwarp();
+    } else if (warp == 9) {
+        if (elect_one()) {
+            constexpr uint32_t id_s = idesc(kFmtBf16, 0, 0, 128, kTile), id_o = idesc(kFmtBf16, 0, 1, 128, D);
+            // D[tmem] = rows (K-major) of `a` times rows of `b`
+            const auto outer = [&](uint32_t d, int a, int bb) {
+                const uint32_t ua = smem_u32(sm + a), ub = smem_u32(sm + bb);
+#pragma unroll
+                for (int s = 0; s < D / 16; ++s) {
+                    const uint32_t o = (s >> 2) * kSlab + (s & 3) * 32;
+                    mma_bf16(tmem + d, desc_sw128(ua + o, 0, 1024), desc_sw128(ub + o, 0, 1024), id_s, s > 0);
+                }
+            };
+            // D[tmem] += bf16 pairs at `a` (two halves of 32 columns, 64 apart) times rows of `b`
+            const auto inner = [&](uint32_t d, uint32_t a, int bb, bool more) {
+                const uint32_t ub = smem_u32(sm + bb);
+#pragma unroll
+                for (int s = 0; s < kTile / 16; ++s)
+                    mma_bf16_ts(tmem + d, tmem + a + (s >> 2) * 64 + (s & 3) * 8, desc_sw128(ub + s * 2048, kSlab, 1024), id_o,
+                                more || s > 0);
+            };
+            bool ok = wait(kvIn, 0) && wait(kvQ, 0);
+            if (ok) {
+                tc_fence_after();
+                outer(cS, L::k, L::q);
+                mma_commit(bar(kvS));
+                ok = wait(kvG, 0);
+            }
+            if (ok) {
+                tc_fence_after();
+                outer(cDP, L::v, L::g);
+                mma_commit(bar(kvDP));
+            }
+            for (int i = 0; i < steps && ok; ++i) {
+                const int st = i & 1, nx = (i + 1) & 1, nph = ((i + 1) >> 1) & 1;
+                ok = wait(kvP, i & 1);
+                if (!ok) break;
+                tc_fence_after();
+                inner(cDV, cS, L::g + st * L::kTileBytes, i > 0);
+                mma_commit(bar(kvGFree + st));
+                if (i + 1 < steps) {
+                    ok = wait(kvQ + nx, nph);
+                    if (!ok) break;
+                    tc_fence_after();
+                    outer(cS, L::k, L::q + nx * L::kTileBytes);
+                    mma_commit(bar(kvS));
+                }
+                ok = wait(kvDS, i & 1);
+                if (!ok) break;
+                tc_fence_after();
+                inner(cDK, cDP, L::q + st * L::kTileBytes, i > 0);
+                mma_commit(bar(kvQFree + st));
+                if (i + 1 < steps) {
+                    ok = wait(kvG + nx, nph);
+                    if (!ok) break;
+                    tc_fence_after();
+                    outer(cDP, L::v, L::g + nx * L::kTileBytes);
+                    mma_commit(bar(kvDP));
+                }
+            }
+            // every product has completed before the tensor memory is read or freed
+            mma_commit(bar(kvDone));
+            mbar_wait(bar(kvDone), 0);
+        }
+        __syncwarp();
+    } else {
+        const int half = warp >> 2;  // which 64 queries of the tile
+        const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+        const uint32_t tS = tmem + lanes + cS + 64 * half, tDP = tmem + lanes + cDP + 64 * half;
+        const int j = j0 + 32 * (warp & 3) + lane;  // this thread's key
+        const float c2 = p.scale * mix::kLog2e;
+        const mix::Two cc = mix::two(c2, c2);
+        const auto stat = [&](int i) {  // the tile's lse, in powers of two, and delta: one value a thread
+            const int e = threadIdx.x & (kTile - 1), t = (qa + i % nq) * kTile + e;
+            if (i >= steps || t >= len) return 0.f;
+            const long long o = (static_cast<long long>(b) * p.H + hk * G + i / nq) * p.T + t0 + t;
+            return half ? p.delta[o] : p.lse[o] * mix::kLog2e;
+        };
+        float next = stat(0);
+        bool ok = true;
+        for (int i = 0; i < steps; ++i) {
+            float* ls = stats + (i & 1) * 2 * kTile;
+            ls[threadIdx.x] = next;
+            tc::named_bar(1, 256);
+            next = stat(i + 1);
+            const float4* lse4 = reinterpret_cast<const float4*>(ls + 64 * half);
+            const float4* del4 = reinterpret_cast<const float4*>(ls + kTile + 64 * half);
+            const int i0 = (qa + i % nq) * kTile;  // the tile's first query
+            // queries that see the key: from it on, up to its window's end or, a first token, the sequence's
+            uint32_t see[2] = {0xffffffffu, 0xffffffffu};
+            const bool masked = i0 < j0 + kTile || (i0 + kTile - 1 - j0 >= p.window) || i0 + kTile > len;
+            if (masked) {
+                const int from = j - i0 - 64 * half;
+                const int to = (j < p.sinks ? len : static_cast<int>(min(static_cast<long long>(len), static_cast<long long>(j) + p.window))) - i0 - 64 * half;
+                const auto below = [](int k) { return k <= 0 ? 0u : k >= 32 ? 0xffffffffu : (1u << k) - 1u; };
+#pragma unroll
+                for (int g = 0; g < 2; ++g) see[g] = below(to - 32 * g) & ~below(from - 32 * g);
+            }
+            ok = ok && __all_sync(0xffffffffu, wait(kvS, i & 1));
+            if (!ok) continue;  // (the named barrier above stays in step)
+            tc_fence_after();
+            uint32_t s[64], pk[32];
+            float pr[64];
+            tmem_ld32(tS, s);
+            tmem_ld32(tS + 32, s + 32);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 64; e += 4) {
+                const float4 l4 = lse4[e / 4];
+                mix::split(mix::ex2_2(mix::fma2(mix::two(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), cc, mix::two(-l4.x, -l4.y))),
+                           pr[e], pr[e + 1]);
+                mix::split(mix::ex2_2(mix::fma2(mix::two(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), cc, mix::two(-l4.z, -l4.w))),
+                           pr[e + 2], pr[e + 3]);
+            }
+            if (masked) {
+#pragma unroll
+                for (int e = 0; e < 64; ++e) pr[e] = (see[e >> 5] >> (e & 31)) & 1 ? pr[e] : 0.f;
+            }
+#pragma unroll
+            for (int e = 0; e < 32; ++e) pk[e] = cvt_bf16x2(pr[2 * e], pr[2 * e + 1]);
+            tmem_st32(tS, pk);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kvP));
+            ok = __all_sync(0xffffffffu, wait(kvDP, i & 1));
+            if (!ok) continue;
+            tc_fence_after();
+            tmem_ld32(tDP, s);
+            tmem_ld32(tDP + 32, s + 32);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 64; e += 4) {
+                const float4 d4 = del4[e / 4];
+                const mix::Two a = mix::mul2(mix::two(pr[e], pr[e + 1]),
+                                             mix::add2(mix::two(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), mix::two(-d4.x, -d4.y)));
+                const mix::Two bb = mix::mul2(mix::two(pr[e + 2], pr[e + 3]),
+                                              mix::add2(mix::two(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), mix::two(-d4.z, -d4.w)));
+                mix::split(a, pr[e], pr[e + 1]);
+                mix::split(bb, pr[e + 2], pr[e + 3]);
+            }
+            if (masked) {
+#pragma unroll
+                for (int e = 0; e < 64; ++e) pr[e] = (see[e >> 5] >> (e & 31)) & 1 ? pr[e] : 0.f;
+            }
+#pragma unroll
+            for (int e = 0; e < 32; ++e) pk[e] = cvt_bf16x2(pr[2 * e], pr[2 * e + 1]);
+            tmem_st32(tDP, pk);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kvDS));
+        }
+        if (ok && __all_sync(0xffffffffu, wait(kvDone, 0))) {
+            tc_fence_after();
+            // the first four warps store dV, the others dK
+            const uint32_t t = tmem + lanes + (half ? cDK : cDV);
+            const float mul = half ? p.scale : 1.f;
+            const int r0 = 32 * (warp & 3);
+            uint8_t* mine = sm + L::q + warp * 32 * (D * 2);
+            if (part && r0 < joined) {
+                float* to = part + static_cast<long long>(half) * p.sinks * D + static_cast<long long>(j) * D;
+#pragma unroll
+                for (int g = 0; g < D; g += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(t + g, o);
+                    tmem_ld_wait();
+                    if (j < joined) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<float4*>(to + g + e) = make_float4(__uint_as_float(o[e]) * mul, __uint_as_float(o[e + 1]) * mul,
+                                                                                 __uint_as_float(o[e + 2]) * mul, __uint_as_float(o[e + 3]) * mul);
+                    }
+                }
+            }
+            if (!far)
+                store_rows<D>(t, mul, mine, (half ? p.dk : p.dv) + ((row0 + j0 + r0) * p.Hk + hk) * D, static_cast<long long>(p.Hk) * D,
+                              joined - r0, min(32, len - j0 - r0), lane);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (*stop && threadIdx.x == 0) record_error(p.err, kErrTimeout);
+    if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+// The first tokens' dK and dV: the sums of their stretches, in order.
+__global__ void __launch_bounds__(256) window_join_kernel(const WindowArgs p) {
+    const long long id = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+    const int d = static_cast<int>(id % p.d);
+    long long rest = id / p.d;
+    const int j = static_cast<int>(rest % p.sinks);
+    rest /= p.sinks;
+    const int which = static_cast<int>(rest % 2);
+    rest /= 2;
+    const int hk = static_cast<int>(rest % p.Hk);
+    const long long n = rest / p.Hk;
+    if (n >= p.nseq) return;
+    int b, t0, t1;
+    if (!mix::token_range(p.cu_seqlens, static_cast<int>(n), p.nseq, p.T, p.err, b, t0, t1)) return;
+    if (j >= t1 - t0) return;
+    const long long base = p.cu_seqlens ? static_cast<long long>(t0 / p.far_tokens) + n
+                                        : n * (p.T > p.far_tokens ? (p.T + p.far_tokens - 1) / p.far_tokens : 1);
+    const int parts = (t1 - t0 + p.far_tokens - 1) / p.far_tokens;
+    float s = 0.f;
+    for (int c = 0; c < parts; ++c) s += p.far_part[((((base + c) * p.Hk + hk) * 2 + which) * p.sinks + j) * p.d + d];
+    (which ? p.dk : p.dv)[((static_cast<long long>(b) * p.T + t0 + j) * p.Hk + hk) * p.d + d] = f32_to_bf16(s);
+}
+
+// ------------------------------------------------------------------ dQ
+
+enum { qIn = 0, qK = 1, qKFree = 3, qV = 5, qVFree = 7, qS = 9, qRead = 10, qDP = 11, qDS = 12, qDone = 13, qTail = 14, qBars = 15 };
+
+template <int D>
+struct QSmem {
+    static constexpr int kTileBytes = kSlab * (D / 64);
+    static constexpr int q = 0, g = kTileBytes, k = 2 * kTileBytes, v = 4 * kTileBytes, bars = 6 * kTileBytes;
+    static constexpr int misc = bars + qBars * 8;
+    static constexpr int total = misc + 32 + 1024;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    window_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                     const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_g, const WindowArgs p) {
+    using L = QSmem<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* sm = smem_raw + smem_align_pad(smem_raw);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::bars);
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + L::misc);
+    volatile int* stop = reinterpret_cast<volatile int*>(sm + L::misc + 4);
+    auto bar = [&](int i) { return smem_u32(&bars[i]); };
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    const int h = blockIdx.x % p.H, hk = h / (p.H / p.Hk);
+    const long long slot = p.slots - 1 - blockIdx.x / p.H;  // late tiles, with the most keys, first
+    int n, b, t0, t1;
+    long long c;
+    if (!mix::find_block(p.cu_seqlens, p.nseq, p.T, kTile, slot, p.err, n, c)) return;
+    if (!mix::token_range(p.cu_seqlens, n, p.nseq, p.T, p.err, b, t0, t1)) return;
+    const int len = t1 - t0;
+    if (c * kTile >= len) return;
+    const int q0 = static_cast<int>(c) * kTile;
+    const Blocks blk = blocks_of(q0, kTile, len, p.window, p.sinks);
+    const int nblk = blk.count();
+    const long long row0 = static_cast<long long>(b) * p.T + t0;
+
+    if (warp == 9) {
+        tmem_alloc(smem_u32(tslot), 512);
+        tmem_relinquish();
+    }
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < qBars; ++i) mbar_init(bar(i), i == qRead || i == qDS ? 8 : 1);
+        fence_mbar_init();
+        *stop = 0;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tslot;
+    constexpr uint32_t cS = 0, cDP = 128, cDQ = 256;
+    const auto wait = [&](int i, int parity) {
+        if (*stop) return false;
+        if (mbar_wait(bar(i), parity)) return true;
+        *stop = 1;
+        return false;
+    };
+
+    if (warp == 8) {
+        int tails = 0, lk = 0, lv = 0;
+        if (lane == 0) {
+            mbar_arrive_expect_tx(bar(qIn), 2 * L::kTileBytes);
+            for (int s = 0; s < D / 64; ++s) {
+                tma_load_3d(smem_u32(sm + L::q + s * kSlab), &map_q, 64 * s, h, static_cast<int>(row0 + q0), bar(qIn));
+                tma_load_3d(smem_u32(sm + L::g + s * kSlab), &map_g, 64 * s, h, static_cast<int>(row0 + q0), bar(qIn));
+            }
+        }
+        bool ok = true;
+        for (int j = 0; j < nblk && ok; ++j) {
+            const int j0 = blk.start(j), st = j & 1, ph = ((j >> 1) & 1) ^ 1;
+            const int row = static_cast<int>(row0 + j0);
+            ok = j < 2 || __all_sync(0xffffffffu, wait(qKFree + st, ph));
+            if (ok) ok = load_tile<D>(sm + L::k + st * L::kTileBytes, &map_k, hk, row, min(kTile, len - j0), bar(qK + st), bar(qTail), tails, lane);
+            if (!ok) break;
+            lk = j + 1;
+            ok = j < 2 || __all_sync(0xffffffffu, wait(qVFree + st, ph));
+            if (ok) ok = load_tile<D>(sm + L::v + st * L::kTileBytes, &map_v, hk, row, kTile, bar(qV + st), bar(qTail), tails, lane);
+            if (!ok) break;
+            lv = j + 1;
+        }
+        if (!ok) *stop = 1;
+        mbar_wait(bar(qIn), 0);
+        for (int j = max(0, lk - 2); j < lk; ++j) mbar_wait(bar(qK + (j & 1)), (j >> 1) & 1);
+        for (int j = max(0, lv - 2); j < lv; ++j) mbar_wait(bar(qV + (j & 1)), (j >> 1) & 1);
+        __syncwarp();
+    } else if (warp == 9) {
+        if (elect_one()) {
+            constexpr uint32_t id_o = idesc(kFmtBf16, 0, 1, 128, D);
+            const auto outer = [&](uint32_t d, int a, int bb, int width) {
+                const uint32_t ua = smem_u32(sm + a), ub = smem_u32(sm + bb), id = idesc(kFmtBf16, 0, 0, 128, width);
+#pragma unroll
+                for (int s = 0; s < D / 16; ++s) {
+                    const uint32_t o = (s >> 2) * kSlab + (s & 3) * 32;
+                    mma_bf16(tmem + d, desc_sw128(ua + o, 0, 1024), desc_sw128(ub + o, 0, 1024), id, s > 0);
+                }
+            };
+            bool ok = wait(qIn, 0) && wait(qK, 0);
+            if (ok) {
+                tc_fence_after();
+                outer(cS, L::q, L::k, blk.width(0));
+                mma_commit(bar(qS));
+                ok = wait(qV, 0);
+            }
+            if (ok) {
+                tc_fence_after();
+                outer(cDP, L::g, L::v, blk.width(0));
+                mma_commit(bar(qDP));
+                mma_commit(bar(qVFree));
+            }
+            for (int j = 0; j < nblk && ok; ++j) {
+                const int st = j & 1, nx = (j + 1) & 1, nph = ((j + 1) >> 1) & 1;
+                if (j + 1 < nblk) {
+                    ok = wait(qRead, j & 1) && wait(qK + nx, nph);
+                    if (!ok) break;
+                    tc_fence_after();
+                    outer(cS, L::q, L::k + nx * L::kTileBytes, blk.width(j + 1));
+                    mma_commit(bar(qS));
+                }
+                ok = wait(qDS, j & 1);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t ub = smem_u32(sm + L::k + st * L::kTileBytes);
+                const int steps = blk.width(j) / 16;
+                for (int s = 0; s < steps; ++s)
+                    mma_bf16_ts(tmem + cDQ, tmem + cDP + (s >> 2) * 64 + (s & 3) * 8, desc_sw128(ub + s * 2048, kSlab, 1024), id_o,
+                                (j | s) != 0);
+                mma_commit(bar(qKFree + st));
+                if (j + 1 < nblk) {
+                    ok = wait(qV + nx, nph);
+                    if (!ok) break;
+                    tc_fence_after();
+                    outer(cDP, L::g, L::v + nx * L::kTileBytes, blk.width(j + 1));
+                    mma_commit(bar(qDP));
+                    mma_commit(bar(qVFree + nx));
+                }
+            }
+            mma_commit(bar(qDone));
+            mbar_wait(bar(qDone), 0);
+        }
+        __syncwarp();
+    } else {
+        const int half = warp >> 2;  // which 64 keys of the block
+        const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+        const uint32_t tS = tmem + lanes + cS + 64 * half, tDP = tmem + lanes + cDP + 64 * half;
+        const int i = q0 + 32 * (warp & 3) + lane;  // this thread's query
+        const float c2 = p.scale * mix::kLog2e;
+        float lse = 0.f, delta = 0.f;
+        if (i < len) {
+            const long long o = (static_cast<long long>(b) * p.H + h) * p.T + t0 + i;
+            lse = p.lse[o] * mix::kLog2e;
+            delta = p.delta[o];
+        }
+        const mix::Two cc = mix::two(c2, c2), ll = mix::two(-lse, -lse), dd = mix::two(-delta, -delta);
+        bool ok = true;
+        for (int j = 0; j < nblk; ++j) {
+            ok = __all_sync(0xffffffffu, wait(qS, j & 1));
+            if (!ok) break;
+            tc_fence_after();
+            const int j0 = blk.start(j) + 64 * half, width = blk.width(j) - 64 * half;  // of this half, 0 or less: none
+            uint32_t s[64], pk[32];
+            float pr[64];
+            if (width > 0) tmem_ld32(tS, s);
+            if (width > 32) tmem_ld32(tS + 32, s + 32);
+            tmem_ld_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(qRead));
+            const bool masked = blk.width(j) < kTile || !all_seen(q0, kTile, blk.start(j), kTile, p.window, p.sinks);
+            uint32_t see[2] = {0xffffffffu, 0xffffffffu};
+            if (masked) {
+                see[0] = width > 0 ? seen_bits(i, j0, p.window, p.sinks) : 0;
+                see[1] = width > 32 ? seen_bits(i, j0 + 32, p.window, p.sinks) : 0;
+            }
+#pragma unroll
+            for (int e = 0; e < 64; e += 2)
+                mix::split(mix::ex2_2(mix::fma2(mix::two(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), cc, ll)), pr[e], pr[e + 1]);
+            ok = __all_sync(0xffffffffu, wait(qDP, j & 1));
+            if (!ok) break;
+            tc_fence_after();
+            if (width > 0) tmem_ld32(tDP, s);
+            if (width > 32) tmem_ld32(tDP + 32, s + 32);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 64; e += 2) {
+                const mix::Two a = mix::mul2(mix::two(pr[e], pr[e + 1]),
+                                             mix::add2(mix::two(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), dd));
+                mix::split(a, pr[e], pr[e + 1]);
+            }
+            if (masked) {
+#pragma unroll
+                for (int e = 0; e < 64; ++e) pr[e] = (see[e >> 5] >> (e & 31)) & 1 ? pr[e] : 0.f;
+            }
+#pragma unroll
+            for (int e = 0; e < 32; ++e) pk[e] = cvt_bf16x2(pr[2 * e], pr[2 * e + 1]);
+            if (width > 0) tmem_st32(tDP, pk);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(qDS));
+        }
+        if (ok && half == 0 && __all_sync(0xffffffffu, wait(qDone, 0))) {
+            tc_fence_after();
+            const int r0 = 32 * warp;
+            store_rows<D>(tmem + lanes + cDQ, p.scale, sm + L::q + warp * 32 * (D * 2), p.dq + ((row0 + q0 + r0) * p.H + h) * D,
+                          static_cast<long long>(p.H) * D, 0, min(32, len - q0 - r0), lane);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (*stop && threadIdx.x == 0) record_error(p.err, kErrTimeout);
+    if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+template <int D>
+cudaError_t launch(const WindowArgs& a, cudaStream_t stream) {
+    CUtensorMap mq, mk, mv, mg;
+    if (!make_heads_map(&mq, a.q, a.tokens, a.q_stride, a.H, D, kTile) ||
+        !make_heads_map(&mk, a.k, a.tokens, a.k_stride, a.Hk, D, kTile) ||
+        !make_heads_map(&mv, a.v, a.tokens, a.v_stride, a.Hk, D, kTile) ||
+        !make_heads_map(&mg, a.d_out, a.tokens, static_cast<long long>(a.H) * D, a.H, D, kTile))
+        return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(window_dkv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, KvSmem<D>::total);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(window_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, QSmem<D>::total);
+    if (e != cudaSuccess) return e;
+    const long long rows = a.tokens * a.H * (D / 8);
+    window_delta_kernel<D><<<static_cast<unsigned>((rows + 255) / 256), 256, 0, stream>>>(a);
+    window_dkv_kernel<D><<<static_cast<unsigned>((a.slots + a.far_slots) * a.Hk), kThreads, KvSmem<D>::total, stream>>>(mq, mk, mv, mg, a);
+    if (a.sinks > 0) {
+        const long long ids = static_cast<long long>(a.nseq) * a.Hk * 2 * a.sinks * D;
+        window_join_kernel<<<static_cast<unsigned>((ids + 255) / 256), 256, 0, stream>>>(a);
+    }
+    window_dq_kernel<D><<<static_cast<unsigned>(a.slots * a.H), kThreads, QSmem<D>::total, stream>>>(mq, mk, mv, mg, a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_window_bwd(const WindowArgs& a, cudaStream_t stream) {
+    return a.d == 64 ? launch<64>(a, stream) : launch<128>(a, stream);
+}
+
+}  // namespace gdn

@@ -1,0 +1,366 @@
+// Attention with a sliding window and first tokens that stay visible: forward.
+//
+//   out_i = sum_j p_ij v_j,  p_ij = exp(s_ij - lse_i),  s_ij = scale q_i . k_j
+//
+// A block of threads holds two tiles of 128 queries that share their keys: two
+// heads of a group, or (groups of odd size) two consecutive tiles of a head.
+// Per 128 keys and tile, S = Q K^T and O += P V are tensor-core products with
+// their accumulators in tensor memory; each tile has a warpgroup, one thread per
+// row, that turns S into P = 2^(S c - m) with a running maximum m and sum, and
+// writes it over S as the bf16 operand of the second product.  P is rounded to
+// bf16 (half a step of 2^-8, in random directions over a row's keys) because
+// that is what the tensor cores multiply; the sum is of the unrounded values.
+// While one tile's warpgroup works, the tensor cores run the other's products.
+// O is rescaled only when a row's maximum has grown by more than 2^8, so most
+// blocks leave it where it is; until then P is at most 2^8.
+//
+// A masked place has P = 0, and 0 times a NaN or an infinity in V would not be
+// zero: rows behind the sequence are cleared in V's tiles, and queries that end up
+// non-finite are computed again from the keys they see.
+#include <cmath>
+
+#include "gdn_window_common.cuh"
+
+namespace gdn {
+
+namespace {
+
+using namespace win;
+
+constexpr int kThreads = 320;  // warps 0-3 and 4-7: a tile's rows each; 8: copies; 9: products
+constexpr float kGrow = 8.f;
+
+// mbarriers
+enum { bQ = 0, bK = 2, bKFree = 4, bV = 6, bVFree = 8, bS = 10, bP = 12, bO = 14, bTail = 16, bDrain = 17, kBars = 18 };
+
+template <int D>
+struct Smem {
+    static constexpr int kTileBytes = kSlab * (D / 64);
+    static constexpr int q = 0, k = 2 * kTileBytes, v = 4 * kTileBytes, bars = 6 * kTileBytes;
+    static constexpr int misc = bars + kBars * 8;
+    static constexpr int total = misc + 32 + 1024;
+};
+
+// One row from the keys that it sees, by a warp: D / 32 channels per lane.
+template <int D>
+__device__ __noinline__ void one_row(const WindowArgs& p, long long row0, int i, int h, float& lse) {
+    constexpr int E = D / 32;
+    const int lane = threadIdx.x & 31, hk = h / (p.H / p.Hk);
+    const uint16_t* q = p.q + (row0 + i) * p.q_stride + h * D + lane * E;
+    float qv[E], o[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        qv[e] = bf16_to_f32(q[e]) * (p.scale * mix::kLog2e);
+        o[e] = 0.f;
+    }
+    float m = -INFINITY, l = 0.f;
+    const int lo = max(0, i - p.window + 1), first = min(p.sinks, lo);
+    for (int c = 0; c < first + i - lo + 1; ++c) {
+        const long long j = row0 + (c < first ? c : lo + c - first);
+        const uint16_t* k = p.k + j * p.k_stride + hk * D + lane * E;
+        float s = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) s = fmaf(qv[e], bf16_to_f32(k[e]), s);
+#pragma unroll
+        for (int x = 16; x > 0; x /= 2) s += __shfl_xor_sync(0xffffffffu, s, x);
+        const float mn = s > m || s != s ? s : m;
+        const float f = m == mn ? 1.f : mix::ex2(m - mn), w = mix::ex2(s - mn);
+        m = mn;
+        l = fmaf(l, f, w);
+        const uint16_t* v = p.v + j * p.v_stride + hk * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = fmaf(o[e], f, w * bf16_to_f32(v[e]));
+    }
+    uint16_t* out = p.out + (row0 + i) * (static_cast<long long>(p.H) * D) + h * D + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; ++e) out[e] = f32_to_bf16(o[e] / l);
+    lse = (m + log2f(l)) * 0.6931471805599453f;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    window_fwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                      const __grid_constant__ CUtensorMap map_v, const WindowArgs p) {
+    using L = Smem<D>;
+    constexpr int kSlabs = D / 64;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* sm = smem_raw + smem_align_pad(smem_raw);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::bars);
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + L::misc);
+    volatile int* stop = reinterpret_cast<volatile int*>(sm + L::misc + 4);
+    auto bar = [&](int i) { return smem_u32(&bars[i]); };
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (blockIdx.x == 0) mix::check_offsets(p.cu_seqlens, p.nseq, p.T, p.err);
+
+    // the two tiles: heads h and h + 1 of one tile, or two tiles of head h
+    const int G = p.H / p.Hk, two_heads = G % 2 == 0;
+    const int units = two_heads ? p.H / 2 : p.H;
+    const long long slot = p.slots - 1 - blockIdx.x / units;  // late tiles, with the most keys, first
+    const int unit = blockIdx.x % units;
+    int n;
+    long long c;
+    int b, t0, t1;
+    // every thread takes the same way out
+    if (!mix::find_block(p.cu_seqlens, p.nseq, p.T, two_heads ? kTile : 2 * kTile, slot, p.err, n, c)) return;
+    if (!mix::token_range(p.cu_seqlens, n, p.nseq, p.T, p.err, b, t0, t1)) return;
+    const int len = t1 - t0;
+    const long long at = c * (two_heads ? kTile : 2 * kTile);
+    if (at >= len) return;
+    const int q0 = static_cast<int>(at);
+    const int h0 = two_heads ? 2 * unit : unit, hk = h0 / G;
+    const int rows = two_heads ? kTile : 2 * kTile;
+    const bool second = two_heads || q0 + kTile < len;
+    const Blocks blk = blocks_of(q0, rows, len, p.window, p.sinks);
+    const int nblk = blk.count();
+    const long long row0 = static_cast<long long>(b) * p.T + t0;  // the sequence's first row
+
+    if (warp == 9) {
+        tmem_alloc(smem_u32(tslot), 512);
+        tmem_relinquish();
+    }
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kBars; ++i) mbar_init(bar(i), i >= bP && i < bO ? 4 : 1);
+        fence_mbar_init();
+        *stop = 0;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tslot;
+    // S (then P) of tile x at column 128 x, O at 256 + 128 x
+    const auto wait = [&](int i, int parity) {
+        if (*stop) return false;
+        if (mbar_wait(bar(i), parity)) return true;
+        *stop = 1;
+        return false;
+    };
+
+    if (warp == 8) {
+        if (lane == 0) {
+            for (int x = 0; x < (second ? 2 : 1); ++x) {
+                mbar_arrive_expect_tx(bar(bQ + x), L::kTileBytes);
+                for (int s = 0; s < kSlabs; ++s)
+                    tma_load_3d(smem_u32(sm + L::q + x * L::kTileBytes + s * kSlab), &map_q, 64 * s, h0 + (two_heads ? x : 0),
+                                static_cast<int>(row0 + q0 + (two_heads ? 0 : x * kTile)), bar(bQ + x));
+            }
+        }
+        int loaded_k = 0, loaded_v = 0, tails = 0;
+        bool ok = true;
+        for (int j = 0; j < nblk; ++j) {
+            const int st = j & 1, ph = ((j >> 1) & 1) ^ 1;
+            const int row = static_cast<int>(row0 + blk.start(j));
+            ok = j < 2 || __all_sync(0xffffffffu, wait(bKFree + st, ph));
+            // K's rows behind the sequence are masked, V's have to be zeros
+            if (ok) ok = load_tile<D>(sm + L::k + st * L::kTileBytes, &map_k, hk, row, kTile, bar(bK + st), bar(bTail), tails, lane);
+            if (!ok) break;
+            loaded_k = j + 1;
+            ok = j < 2 || __all_sync(0xffffffffu, wait(bVFree + st, ph));
+            if (ok) ok = load_tile<D>(sm + L::v + st * L::kTileBytes, &map_v, hk, row, min(kTile, len - blk.start(j)), bar(bV + st),
+                                      bar(bTail), tails, lane);
+            if (!ok) break;
+            loaded_v = j + 1;
+        }
+        if (!ok) *stop = 1;
+        // every copy has landed before the block may leave
+        for (int x = 0; x < (second ? 2 : 1); ++x) mbar_wait(bar(bQ + x), 0);
+        for (int j = max(0, loaded_k - 2); j < loaded_k; ++j) mbar_wait(bar(bK + (j & 1)), (j >> 1) & 1);
+        for (int j = max(0, loaded_v - 2); j < loaded_v; ++j) mbar_wait(bar(bV + (j & 1)), (j >> 1) & 1);
+        __syncwarp();
+    } else if (warp == 9) {
+        if (elect_one()) {
+            const auto scores = [&](int j, int x) {  // S of tile x with block j
+                const uint32_t qa = smem_u32(sm + L::q + x * L::kTileBytes), ka = smem_u32(sm + L::k + (j & 1) * L::kTileBytes);
+                const uint32_t id = idesc(kFmtBf16, 0, 0, 128, blk.width(j));
+#pragma unroll
+                for (int s = 0; s < D / 16; ++s) {
+                    const uint32_t o = (s >> 2) * kSlab + (s & 3) * 32;
+                    mma_bf16(tmem + 128 * x, desc_sw128(qa + o, 0, 1024), desc_sw128(ka + o, 0, 1024), id, s > 0);
+                }
+                mma_commit(bar(bS + x));
+            };
+            const int tiles = second ? 2 : 1;
+            bool ok = true;
+            for (int x = 0; x < tiles && ok; ++x) {
+                ok = wait(bQ + x, 0) && wait(bK, 0);
+                if (!ok) break;
+                tc_fence_after();
+                scores(0, x);
+            }
+            if (ok) mma_commit(bar(bKFree));
+            constexpr uint32_t id_o = idesc(kFmtBf16, 0, 1, 128, D);
+            for (int j = 0; j < nblk && ok; ++j) {
+                const int steps = blk.width(j) / 16;
+                for (int x = 0; x < tiles && ok; ++x) {
+                    ok = wait(bV + (j & 1), (j >> 1) & 1) && wait(bP + x, j & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t va = smem_u32(sm + L::v + (j & 1) * L::kTileBytes);
+                    for (int s = 0; s < steps; ++s)
+                        mma_bf16_ts(tmem + 256 + 128 * x, tmem + 128 * x + 8 * s, desc_sw128(va + s * 2048, kSlab, 1024), id_o,
+                                    (j | s) != 0);
+                    if (j + 1 == nblk) mma_commit(bar(bO + x));
+                    if (x == tiles - 1) mma_commit(bar(bVFree + (j & 1)));
+                    if (j + 1 < nblk) {
+                        ok = wait(bK + ((j + 1) & 1), ((j + 1) >> 1) & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                        scores(j + 1, x);
+                        if (x == tiles - 1) mma_commit(bar(bKFree + ((j + 1) & 1)));
+                    }
+                }
+            }
+            // every product has completed before the tensor memory is freed
+            mma_commit(bar(bDrain));
+            mbar_wait(bar(bDrain), 0);
+        }
+        __syncwarp();
+    } else if (warp < 4 || second) {
+        const int x = warp >> 2;
+        const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+        const uint32_t tS = tmem + lanes + 128 * x, tO = tmem + lanes + 256 + 128 * x;
+        const int qx = q0 + (two_heads ? 0 : x * kTile);  // this tile's first query
+        const int i = qx + 32 * (warp & 3) + lane;        // this thread's
+        const float c2 = p.scale * mix::kLog2e;
+        float m = -INFINITY, l = 0.f;
+        bool ok = true;
+        for (int j = 0; j < nblk; ++j) {
+            ok = __all_sync(0xffffffffu, wait(bS + x, j & 1));
+            if (!ok) break;
+            tc_fence_after();
+            const int j0 = blk.start(j), width = blk.width(j);
+            uint32_t s[kTile];
+#pragma unroll
+            for (int g = 0; g < kTile; g += 32)
+                if (g < width) tmem_ld32(tS + g, s + g);
+            tmem_ld_wait();
+            if (width < kTile || !all_seen(qx, kTile, j0, width, p.window, p.sinks)) {
+#pragma unroll
+                for (int g = 0; g < kTile; g += 32) {
+                    const uint32_t see = g < width ? seen_bits(i, j0 + g, p.window, p.sinks) : 0;
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) s[g + e] = (see >> e) & 1 ? s[g + e] : 0xff800000u;
+                }
+            }
+            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int e = 0; e < kTile; ++e) top[e & 3] = fmaxf(top[e & 3], __uint_as_float(s[e]));
+            const float mb = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c2;
+            if (__any_sync(0xffffffffu, mb > m + kGrow)) {
+                const float mn = fmaxf(m, mb);
+                const float f = m == -INFINITY ? 0.f : mix::ex2(m - mn);
+                m = mn;
+                l *= f;
+                if (j > 0) {  // the scores came behind the last product into O
+#pragma unroll
+                    for (int g = 0; g < D; g += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(tO + g, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        tmem_st32(tO + g, o);
+                    }
+                }
+            }
+            const float ms = m == -INFINITY ? 0.f : -m;
+            const mix::Two cc = mix::two(c2, c2), mm = mix::two(ms, ms);
+            mix::Two sum[2] = {mix::two(0.f, 0.f), mix::two(0.f, 0.f)};
+            uint32_t pk[kTile / 2];
+#pragma unroll
+            for (int e = 0; e < kTile; e += 2) {
+                float a, bb;
+                const mix::Two y = mix::ex2_2(mix::fma2(mix::two(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), cc, mm));
+                sum[(e >> 1) & 1] = mix::add2(sum[(e >> 1) & 1], y);
+                mix::split(y, a, bb);
+                pk[e / 2] = cvt_bf16x2(a, bb);
+            }
+            float a, bb;
+            mix::split(mix::add2(sum[0], sum[1]), a, bb);
+            l += a + bb;
+            tmem_st32(tS, pk);
+            if (width == kTile || width > 64) tmem_st32(tS + 32, pk + 32);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(bP + x));
+        }
+        if (ok && __all_sync(0xffffffffu, wait(bO + x, 0))) {
+            tc_fence_after();
+            const int h = h0 + (two_heads ? x : 0);
+            const float r = 1.f / l;
+            float lse = (m + log2f(l)) * 0.6931471805599453f;
+            // through this warp's own 32 rows of Q's buffer (its products are done):
+            // 16-byte chunks, permuted so that neither side meets a bank twice
+            uint8_t* mine = sm + L::q + x * L::kTileBytes + (warp & 3) * 32 * (D * 2);
+            float bad = 0.f;
+#pragma unroll
+            for (int g = 0; g < D; g += 32) {
+                uint32_t o[32];
+                tmem_ld32(tO + g, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float u = __uint_as_float(o[8 * q + 2 * e]) * r, v = __uint_as_float(o[8 * q + 2 * e + 1]) * r;
+                        bad = fmaf(u, 0.f, fmaf(v, 0.f, bad));
+                        w[e] = cvt_bf16x2(u, v);
+                    }
+                    *reinterpret_cast<uint4*>(mine + lane * (D * 2) + (((g / 8 + q) ^ (lane & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+            __syncwarp();
+            constexpr int kChunks = D / 8;  // of 16 bytes in a row
+#pragma unroll 4
+            for (int k = 0; k < kChunks; ++k) {
+                const int r2 = (k * 32 + lane) / kChunks, ch = (k * 32 + lane) % kChunks;
+                const int t = qx + 32 * (warp & 3) + r2;
+                const uint4 w = *reinterpret_cast<const uint4*>(mine + r2 * (D * 2) + ((ch ^ (r2 & 7)) * 16));
+                if (t < len)
+                    *reinterpret_cast<uint4*>(p.out + (row0 + t) * (static_cast<long long>(p.H) * D) + h * D + ch * 8) = w;
+            }
+            __syncwarp();
+            uint32_t again = __ballot_sync(0xffffffffu, bad != 0.f && i < len);
+            while (again) {
+                const int src = __ffs(again) - 1;
+                again &= again - 1;
+                float v;
+                one_row<D>(p, row0, qx + 32 * (warp & 3) + src, h, v);
+                if (lane == src) lse = v;
+            }
+            if (p.lse && i < len)  // (row of the batch, head, token)
+                p.lse[(static_cast<long long>(b) * p.H + h) * p.T + t0 + i] = lse;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (*stop && threadIdx.x == 0) record_error(p.err, kErrTimeout);
+    if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+template <int D>
+cudaError_t launch(const WindowArgs& a, cudaStream_t stream) {
+    CUtensorMap mq, mk, mv;
+    const long long tokens = a.cu_seqlens ? a.T : static_cast<long long>(a.nseq) * a.T;
+    if (!make_heads_map(&mq, a.q, tokens, a.q_stride, a.H, D, kTile) ||
+        !make_heads_map(&mk, a.k, tokens, a.k_stride, a.Hk, D, kTile) ||
+        !make_heads_map(&mv, a.v, tokens, a.v_stride, a.Hk, D, kTile))
+        return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(window_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::total);
+    if (e != cudaSuccess) return e;
+    const int units = (a.H / a.Hk) % 2 == 0 ? a.H / 2 : a.H;
+    window_fwd_kernel<D><<<static_cast<unsigned>(a.slots * units), kThreads, Smem<D>::total, stream>>>(mq, mk, mv, a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+int window_fwd_rows(int H, int Hk) { return (H / Hk) % 2 == 0 ? win::kTile : 2 * win::kTile; }
+
+cudaError_t launch_window_fwd(const WindowArgs& a, cudaStream_t stream) {
+    return a.d == 64 ? launch<64>(a, stream) : launch<128>(a, stream);
+}
+
+}  // namespace gdn

@@ -159,6 +159,16 @@ def load():
         lib.gdn_rope_bwd_workspace_size.restype = sz
         lib.gdn_rope_bwd.argtypes = rope + [vp] * 6 + [i] * 7 + [f, i, vp, sz, vp]
         lib.gdn_rope_bwd.restype = i
+        lib.gdn_window_fwd.argtypes = row * 3 + [vp] * 3 + [i] * 7 + [f, vp]
+        lib.gdn_window_fwd.restype = i
+        lib.gdn_window_bwd_workspace_size.argtypes = [i] * 8
+        lib.gdn_window_bwd_workspace_size.restype = sz
+        lib.gdn_window_bwd.argtypes = row * 3 + [vp] * 7 + [i] * 7 + [f, vp, sz, vp]
+        lib.gdn_window_bwd.restype = i
+        lib.gdn_window_step.argtypes = row * 3 + [vp] * 5 + [i] * 7 + [f, vp]
+        lib.gdn_window_step.restype = i
+        lib.gdn_window_fill.argtypes = row * 2 + [vp] * 4 + [i] * 7 + [vp]
+        lib.gdn_window_fill.restype = i
         lib.gdn_kernel_launches.argtypes = []
         lib.gdn_kernel_launches.restype = ctypes.c_uint64
         _lib = lib

@@ -150,3 +150,258 @@ def test_a_bad_row_stays_alone():
     same = torch.ones(2, 40, 4, dtype=torch.bool, device="cuda")
     same[1, 3, 2] = same[0, 0, 0] = False
     assert torch.equal(q[same], good[same]) and torch.isnan(q[1, 3, 2]).all()
+
+
+# ------------------------------------------------------------------- window
+#
+# Tolerances of the attention, from its roundings.  P and dS are bf16 operands:
+# each element is off by at most 2^-8 of itself, uniformly distributed, so by
+# about 2^-8 / sqrt(3) x 0.72 in L2 (1.65e-3, as for a bf16 output); summed over
+# keys in random directions the relative error of a sum of like terms stays that
+# of one term, 1.65e-3, and where terms cancel it grows against the sum.  Over
+# iid values the L2 of the sum and of its terms agree, so an output carries
+# sqrt(2) x 1.65e-3 = 2.4e-3 with its own rounding, within the 3e-3 of bf16
+# outputs here.  Gradients of dS carry P's, dS's and the saved output's rounding
+# (delta): sqrt(3) x 1.65e-3 and the final one, 3.3e-3, within this package's
+# bound for gradients, 5e-3.
+TOL_GRAD = 5e-3
+
+WINDOW = [  # B, T, H, Hk, d, window, sinks, cu
+    (1, 1, 1, 1, 64, 1, 0, None),
+    (2, 0, 2, 1, 64, 4, 1, None),
+    (1, 3, 2, 2, 128, 100, 4, None),          # shorter than everything
+    (2, 127, 4, 2, 64, 1, 0, None),           # each token sees itself alone
+    (2, 129, 4, 1, 128, 128, 0, None),
+    (1, 128, 3, 1, 64, 17, 3, None),          # an odd group
+    (1, 300, 5, 5, 128, 129, 0, None),        # a key head to each query head
+    (1, 513, 2, 2, 64, 64, 128, None),        # as many first tokens as there may be
+    (1, 700, 6, 2, 128, 130, 33, None),
+    (2, 1000, 4, 2, 64, 1000, 5, None),       # the window is everything
+    (1, 1200, 8, 1, 128, 300, 4, None),
+    (1, 600, 4, 2, 128, 50, 2, [0, 0, 1, 3, 130, 131, 400, 600]),
+    (1, 900, 3, 3, 64, 200, 64, [0, 256, 512, 640, 900]),
+    (1, 300, 2, 1, 64, 7, 1, [0, 300]),
+    (1, 130, 2, 2, 64, 9, 9, list(range(131))),  # a token each
+]
+
+
+def _window_inputs(case, seed=0):
+    B, T, H, Hk, d, W, S, cu = case
+    rng = np.random.default_rng(T + H + W + seed)
+    a = {n: _round(rng.standard_normal((B, T, h, d)), BF) for n, h in (("q", H), ("k", Hk), ("v", Hk), ("g", H))}
+    t = {n: _dev(x, BF) for n, x in a.items()}
+    # values where a projection left them, behind its queries and keys
+    wide = torch.full((B, T, (H + 2 * Hk) * d), float("nan"), dtype=BF, device="cuda")
+    wide[..., (H + Hk) * d:] = t["v"].flatten(2)
+    t["v"] = wide[..., (H + Hk) * d:].unflatten(2, (Hk, d))
+    return a, t, dict(window=W, sinks=S, cu_seqlens=_ints(cu))
+
+
+@pytest.mark.parametrize("case", WINDOW, ids=lambda c: "-".join(map(str, c[:7])) + ("p" if c[7] else ""))
+def test_window_forward(case):
+    a, t, kw = _window_inputs(case)
+    out, lse = attention.window_attention_fwd(t["q"], t["k"], t["v"], save_for_backward=True, **kw)
+    ref, ref_lse = A.window_fwd(a["q"], a["k"], a["v"], case[5], case[6], cu=case[7])
+    assert gdn.gdn_get_last_device_error() == 0
+    _close(out, ref, TOL_BF16, "out")
+    _close(lse, ref_lse, TOL_PAR, "lse")
+    assert torch.equal(out, attention.window_attention_fwd(t["q"], t["k"], t["v"], **kw))
+
+
+@pytest.mark.parametrize("case", WINDOW, ids=lambda c: "-".join(map(str, c[:7])) + ("p" if c[7] else ""))
+def test_window_gradients(case):
+    a, t, kw = _window_inputs(case)
+    out, lse = attention.window_attention_fwd(t["q"], t["k"], t["v"], save_for_backward=True, **kw)
+    r = attention.window_attention_bwd(t["q"], t["k"], t["v"], out, lse, t["g"], **kw)
+    ref = A.window_bwd(a["q"], a["k"], a["v"], a["g"], case[5], case[6], cu=case[7])
+    assert gdn.gdn_get_last_device_error() == 0
+    # a token that sees itself alone has no gradient but that of its value; what
+    # is left of dP - delta there is the rounding of the output inside delta
+    size = np.linalg.norm(ref["dv"])
+    for n, want in ref.items():
+        if np.linalg.norm(want) <= 1e-2 * size:
+            assert np.linalg.norm(_np(r[n]) - want) <= TOL_GRAD * size, n
+        else:
+            _close(r[n], want, TOL_GRAD, n)
+    again = attention.window_attention_bwd(t["q"], t["k"], t["v"], out, lse, t["g"], **kw)
+    assert all(torch.equal(r[n], again[n]) for n in r)
+
+
+STEP = [  # B, H, Hk, d, window, sinks, lengths
+    (1, 1, 1, 64, 1, 0, [0]),
+    (3, 4, 2, 64, 5, 0, [0, 4, 5]),
+    (4, 8, 2, 128, 16, 4, [3, 4, 19, 20]),
+    (5, 6, 2, 128, 33, 7, [0, 39, 40, 41, 1000000]),
+    (2, 40, 2, 64, 70, 128, [150, 2 ** 31 - 2]),  # twenty heads to a key head
+    (2, 16, 1, 128, 1500, 0, [1499, 4000]),       # several blocks to a row
+    (1, 5, 5, 64, 4096, 3, [4000]),
+]
+
+
+def _step_inputs(case, seed=0):
+    B, H, Hk, d, W, S, lengths = case
+    rng = np.random.default_rng(B + H + W + seed)
+    a = {n: _round(rng.standard_normal(s), BF) for n, s in
+         (("q", (B, H, d)), ("k", (B, Hk, d)), ("v", (B, Hk, d)), ("kc", (B, S + W, Hk, d)), ("vc", (B, S + W, Hk, d)))}
+    return a, {n: _dev(x, BF) for n, x in a.items()}, _ints(lengths)
+
+
+@pytest.mark.parametrize("case", STEP, ids=lambda c: "-".join(map(str, c[:6])))
+def test_window_step(case):
+    a, t, lengths = _step_inputs(case)
+    S = case[5]
+    for b, n in enumerate(case[6]):  # rows that hold no token may hold anything
+        t["kc"][b, n + 1:], t["vc"][b, n + 1:] = float("nan"), float("inf")
+    kc, vc = t["kc"].clone(), t["vc"].clone()
+    out = attention.window_attention_step(t["q"], t["k"], t["v"], kc, vc, lengths, sinks=S)
+    ref, _, _ = A.window_step(a["q"], a["k"], a["v"], a["kc"], a["vc"], case[6], S)
+    assert gdn.gdn_get_last_device_error() == 0
+    _close(out, ref, TOL_BF16, "out")
+    for b, n in enumerate(case[6]):
+        at = A.cache_row(n, case[4], S)
+        t["kc"][b, at], t["vc"][b, at] = t["k"][b], t["v"][b]
+    same = lambda x, y: torch.equal(x.view(torch.int16), y.view(torch.int16))  # noqa: E731  (NaN too)
+    assert same(kc, t["kc"]) and same(vc, t["vc"])
+
+
+def test_window_step_slots_and_idle_rows():
+    case = (5, 4, 2, 64, 12, 2, [3, 100, 7, -1, 13])
+    a, t, lengths = _step_inputs(case)
+    slots = _ints([4, -1, 0, 2, 1])
+    kc, vc = t["kc"].clone(), t["vc"].clone()
+    out = attention.window_attention_step(t["q"], t["k"], t["v"], kc, vc, lengths, sinks=2, slots=slots)
+    ref, kr, vr = A.window_step(a["q"], a["k"], a["v"], a["kc"], a["vc"], case[6], 2, slots=[4, -1, 0, -1, 1])
+    _close(out, ref, TOL_BF16, "out")
+    assert np.array_equal(_np(kc), kr) and np.array_equal(_np(vc), vr)
+    assert out[1].abs().max() == 0 and out[3].abs().max() == 0 and gdn.gdn_get_last_device_error() == 0
+    out = attention.window_attention_step(t["q"], t["k"], t["v"], kc, vc, lengths, sinks=2, slots=_ints([4, 5, 0, 2, 1]))
+    assert out[1].abs().max() == 0 and gdn.gdn_get_last_device_error() == 7
+
+
+@pytest.mark.parametrize("cu", [None, [0, 0, 1, 30, 100, 240]])
+def test_steps_continue_prompts(cu):
+    """A prompt, its cache, and the tokens after it are the longer prompt."""
+    H, Hk, d, W, S, more = 4, 2, 64, 40, 3, 6
+    B, T = (1, cu[-1]) if cu else (3, 61)
+    lens = [T] * B if cu is None else list(np.diff(cu))
+    N = len(lens)
+    rng = np.random.default_rng(7)
+    whole = [{n: _round(rng.standard_normal((1, ln + more, h, d)), BF) for n, h in (("q", H), ("k", Hk), ("v", Hk))}
+             for ln in lens]
+    prompt = {n: np.concatenate([w[n][:, :ln] for w, ln in zip(whole, lens)], 1 if cu else 0) for n in "qkv"}
+    kc, vc = (torch.full((N + 2, S + W, Hk, d), float("nan"), dtype=BF, device="cuda") for _ in range(2))
+    slots = _ints(list(range(N + 1, 1, -1)))
+    attention.window_cache_fill(_dev(prompt["k"], BF), _dev(prompt["v"], BF), kc, vc, sinks=S, cu_seqlens=_ints(cu),
+                                slots=slots)
+    assert torch.isnan(kc[:2]).all()
+    want = [A.window_fwd(w["q"], w["k"], w["v"], W, S)[0] for w in whole]
+    for s in range(more):
+        at = [ln + s for ln in lens]
+        row = {n: _dev(np.stack([w[n][0, p] for w, p in zip(whole, at)]), BF) for n in "qkv"}
+        out = attention.window_attention_step(row["q"], row["k"], row["v"], kc, vc, _ints(at), sinks=S, slots=slots)
+        _close(out, np.stack([w[0, p] for w, p in zip(want, at)]), TOL_BF16, f"step {s}")
+    assert gdn.gdn_get_last_device_error() == 0
+
+
+def test_a_masked_value_has_no_part():
+    """NaN and infinities where a token does not look have no part in its output.
+    (Rows that share a block with one are computed again with unrounded weights:
+    the same to the roundings of the weights, 1.65e-3, that the tolerance has for
+    them, and not bit for bit.)"""
+    case = (1, 400, 4, 2, 64, 60, 2, [0, 150, 400])
+    a, t, kw = _window_inputs(case)
+    good = attention.window_attention_fwd(t["q"], t["k"], t["v"], **kw)
+    k, v = t["k"].clone(), t["v"].clone()
+    for p, x in ((149, float("nan")), (160, float("inf")), (390, float("nan"))):
+        k[0, p, 0, 3] = v[0, p, 1, 5] = x
+    out = attention.window_attention_fwd(t["q"], k, v, **kw)
+    seen = torch.zeros(400, dtype=torch.bool, device="cuda")
+    for p, t0, t1 in ((149, 0, 150), (160, 150, 400), (390, 150, 400)):
+        seen[p:min(p + 60, t1)] = True
+    want = A.window_fwd(a["q"], a["k"], a["v"], 60, 2, cu=case[7])[0]
+    _close(out[0, ~seen], want[0, ~seen.cpu().numpy()], TOL_BF16, "rows that do not look there")
+    # the first sequence's first tile looks at none of the blocks that hold one
+    assert torch.equal(out[0, :128], good[0, :128])
+    lo, hi = torch.isfinite(out[0, seen][:, :2]), torch.isfinite(out[0, seen][:, 2:])
+    assert not lo.all() and not hi.all()
+
+
+def test_a_bad_sequence_leaves_the_others_gradients():
+    case = (1, 400, 4, 2, 64, 60, 2, [0, 150, 290, 400])
+    a, t, kw = _window_inputs(case)
+    def both(q, k, v, g):
+        out, lse = attention.window_attention_fwd(q, k, v, save_for_backward=True, **kw)
+        return attention.window_attention_bwd(q, k, v, out, lse, g, **kw)
+    good = both(t["q"], t["k"], t["v"], t["g"])
+    bad = {n: t[n].clone() for n in "qkvg"}
+    for n in "qkvg":
+        bad[n][0, 150:290] = float("nan")
+    r = both(bad["q"], bad["k"], bad["v"], bad["g"])
+    for n in r:
+        assert torch.equal(r[n][0, :150], good[n][0, :150]) and torch.equal(r[n][0, 290:], good[n][0, 290:]), n
+
+
+def test_large_scores_and_growing_maxima():
+    """Scores up to thousands, the largest last: the running maximum moves often."""
+    case = (1, 500, 2, 2, 64, 400, 4, None)
+    a, t, kw = _window_inputs(case)
+    ramp = np.linspace(0.1, 40, 500)[None, :, None, None]
+    a["k"] = _round(a["k"] * ramp, BF)
+    t["k"] = _dev(a["k"], BF)
+    out, lse = attention.window_attention_fwd(t["q"], t["k"], t["v"], save_for_backward=True, **kw)
+    ref, ref_lse = A.window_fwd(a["q"], a["k"], a["v"], 400, 4)
+    # a score of s has an fp32 error of 2^-22 s (64 products of like size), which is
+    # a relative error of its weight: 400 x 2^-22 = 1e-4
+    _close(out, ref, TOL_BF16 + 1e-4, "out")
+    _close(lse, ref_lse, TOL_PAR, "lse")
+
+
+def test_window_autograd_and_scale():
+    case = (1, 45, 4, 2, 64, 9, 2, [0, 20, 45])
+    a, t, kw = _window_inputs(case)
+    leaves = [t[n].clone().requires_grad_() for n in "qkv"]
+    out = attention.window_attention(*leaves, scale=0.2, **kw)
+    (out.float() * t["g"].float()).sum().backward()
+    ref = A.window_bwd(a["q"], a["k"], a["v"], a["g"], 9, 2, scale=0.2, cu=[0, 20, 45])
+    rng = np.random.default_rng(3)
+    for n, leaf in zip("qkv", leaves):
+        _close(leaf.grad, ref["d" + n], TOL_GRAD, n)
+        # and the definition's own gradient against differences
+        way, h = rng.standard_normal(a[n].shape), 1e-5
+        ends = [(A.window_fwd(*(a[m] + (s * h * way if m == n else 0) for m in "qkv"), 9, 2, 0.2, [0, 20, 45])[0] * a["g"]).sum()
+                for s in (1, -1)]
+        slope = (ends[0] - ends[1]) / (2 * h)
+        assert abs((ref["d" + n] * way).sum() - slope) <= 1e-6 * np.abs(ref["d" + n] * way).sum()
+    with torch.no_grad():
+        assert torch.equal(attention.window_attention(*leaves, scale=0.2, **kw), out)
+    with pytest.raises(RuntimeError, match="cannot be differentiated again"):
+        y = attention.window_attention(*leaves, **kw)
+        d, = torch.autograd.grad(y.float().sum(), leaves[0], create_graph=True)
+        d.float().sum().backward()
+
+
+def test_window_misaligned_slices_and_streams():
+    """Slices that start anywhere, another stream, a captured forward and backward."""
+    case = (2, 200, 4, 2, 64, 70, 3, None)
+    a, t, kw = _window_inputs(case)
+    want, lse = attention.window_attention_fwd(t["q"], t["k"], t["v"], save_for_backward=True, **kw)
+    grads = attention.window_attention_bwd(t["q"], t["k"], t["v"], want, lse, t["g"], **kw)
+    wide = torch.zeros(2, 200, 3 + 8 * 64, dtype=BF, device="cuda")
+    wide[..., 3:3 + 4 * 64], wide[..., 3 + 256:3 + 384], wide[..., 3 + 384:] = (t[n].flatten(2) for n in "qkv")
+    q, k, v = (wide[..., 3 + o:3 + o + h * 64].unflatten(2, (h, 64)) for o, h in ((0, 4), (256, 2), (384, 2)))
+    assert torch.equal(attention.window_attention_fwd(q, k, v, **kw), want)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    out, lse2 = attention.window_attention_fwd(q, k, v, save_for_backward=True, stream=s, **kw)
+    r = attention.window_attention_bwd(q, k, v, out, lse2, t["g"], stream=s, **kw)
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(out, want) and all(torch.equal(r[n], grads[n]) for n in r)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        og, lg = attention.window_attention_fwd(t["q"], t["k"], t["v"], save_for_backward=True, **kw)
+        rg = attention.window_attention_bwd(t["q"], t["k"], t["v"], og, lg, t["g"], **kw)
+    for _ in range(2):
+        og.zero_()
+        graph.replay()
+        assert torch.equal(og, want) and all(torch.equal(rg[n], grads[n]) for n in rg)
+    assert gdn.gdn_get_last_device_error() == 0
