@@ -4,16 +4,17 @@
 //   h_t = a_t h_{t-1} + m_t sigmoid(i_t) x_t
 //
 // per channel.  A token's map h -> a h + b composes with its neighbours', so a
-// row of T tokens is cut into strips of kStrip tokens, one warp to a strip with
-// its channels across the lanes.  A strip's tokens are loaded and its (a, b)
-// formed once, in registers; the warp composes them from a zero state, the
-// strips' products (P, H) meet in shared memory, and each warp then walks its
-// tokens again from the state it really starts from.  Every input is read once
-// and every output written once.  A block is kWarps consecutive strips; where
-// the channels alone do not fill the GPU a cluster of blocks works side by side
-// on consecutive stretches and exchanges one (P, H) per block and channel
-// through distributed shared memory.  The cluster then takes the next stretch,
-// with the state it ended in.  All compositions run in a fixed order.
+// row of T tokens is cut into strips of kStrip tokens.  A warp holds two strips
+// side by side in time, 16 lanes each with two channels a lane; it copies its
+// tokens to shared memory one round ahead, forms their (a, b) in registers and
+// composes them from a zero state, the strips' products (P, H) meet in shared
+// memory, and each lane then walks its tokens again from the state that they
+// really start from.  Every input is read once and every output written once.  A
+// block is kWarps warps on consecutive tokens; where the channels alone do not
+// fill the GPU a cluster of blocks works side by side on consecutive stretches
+// and exchanges one (P, H) per block and channel through distributed shared
+// memory.  The cluster then takes the next stretch, with the state it ended in.
+// All compositions run in a fixed order.
 //
 // Packed sequences are one row: a sequence's first token starts from its own
 // initial state, and a strip that holds such a token ignores what comes in.
@@ -29,7 +30,10 @@ namespace {
 using namespace mix;
 
 constexpr int kWarps = 8;
-constexpr int kStrip = kGatedStrip;
+constexpr int kChannels = 32;  // of a block
+// Tokens of a lane's strip: what a round costs beside its tokens' own arithmetic
+// is shared by more of them, as far as the registers go.
+constexpr int kStripFwd = 2 * kGatedStrip, kStripBwd = kGatedStrip;
 
 // ---------------------------------------------------------------- clusters
 
@@ -42,37 +46,76 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // A store to the same shared variable of block `rank` of the cluster.
-__device__ __forceinline__ void store_remote(float2* p, uint32_t rank, float2 v) {
+__device__ __forceinline__ void store_remote(float4* p, uint32_t rank, float4 v) {
     uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p)), to;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(a), "r"(rank));
-    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(v.x), "f"(v.y) : "memory");
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+}
+__device__ __forceinline__ void store_remote(int* p, uint32_t rank, int v) {
+    uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p)), to;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(a), "r"(rank));
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to), "r"(v) : "memory");
 }
 
 // ---------------------------------------------------------------- the gates
 
-// 1 - exp(y) for y <= 0: the exponential series up to y^9 / 9! for y >= -1/2
-// (relative error below 2^-24), else from the exponential itself (which has lost
-// at most a bit and a half there).
-__device__ __forceinline__ float one_minus_exp(float y, float e) {
-    float s = fmaf(y, 1.f / 362880.f, 1.f / 40320.f);
-    s = fmaf(y, s, 1.f / 5040.f);
-    s = fmaf(y, s, 1.f / 720.f);
-    s = fmaf(y, s, 1.f / 120.f);
-    s = fmaf(y, s, 1.f / 24.f);
-    s = fmaf(y, s, 1.f / 6.f);
-    s = fmaf(y, s, 0.5f);
-    s = fmaf(y, s, 1.f);
-    return y >= -0.5f ? -y * s : 1.f - e;
+__device__ __forceinline__ Two same(float c) { return two(c, c); }
+
+// min(x, 62), a NaN where x is one
+__device__ __forceinline__ float cap(float x) {
+    float y;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(62.f));
+    return y;
+}
+// sigmoid(r) and sigmoid(i) with one reciprocal for both.  The exponentials are
+// cut at 2^62 so that their product stays finite: sigmoids below 2^-62 are that.
+__device__ __forceinline__ void sigmoids(Two r, Two i, Two& sr, Two& si) {
+    float r0, r1, i0, i1;
+    split(mul2(same(-kLog2e), r), r0, r1);
+    split(mul2(same(-kLog2e), i), i0, i1);
+    const Two p = add2(same(1.f), two(ex2(cap(r0)), ex2(cap(r1))));
+    const Two q = add2(same(1.f), two(ex2(cap(i0)), ex2(cap(i1))));
+    const Two w = rcp_2(mul2(p, q));
+    sr = mul2(w, q);
+    si = mul2(w, p);
+}
+// exp(L) - 1 for -1/2 <= L <= 0, by the exponential series up to L^9 / 9!
+// (relative error below 2^-24)
+__device__ __forceinline__ Two expm1_series(Two L) {
+    Two s = fma2(L, same(1.f / 362880.f), same(1.f / 40320.f));
+    s = fma2(L, s, same(1.f / 5040.f));
+    s = fma2(L, s, same(1.f / 720.f));
+    s = fma2(L, s, same(1.f / 120.f));
+    s = fma2(L, s, same(1.f / 24.f));
+    s = fma2(L, s, same(1.f / 6.f));
+    s = fma2(L, s, same(0.5f));
+    s = fma2(L, s, same(1.f));
+    return mul2(L, s);
+}
+// a = exp(L) and 1 - a^2 = -u (2 + u) with u = a - 1.  `small`: no L of this
+// warp's channels is below -1/2, whatever the gate.
+__device__ __forceinline__ void decay(Two L, bool small, Two& a, Two& gap) {
+    Two u = expm1_series(L);
+    if (!small) {
+        float l0, l1, u0, u1;
+        split(L, l0, l1);
+        split(u, u0, u1);
+        if (l0 < -0.5f) u0 = ex2(kLog2e * l0) - 1.f;
+        if (l1 < -0.5f) u1 = ex2(kLog2e * l1) - 1.f;
+        u = two(u0, u1);
+    }
+    a = add2(same(1.f), u);
+    gap = mul2(u, fma2(same(-1.f), u, same(-2.f)));
 }
 __device__ __forceinline__ float root(float x) {
     float y;
     asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// a and m of a token from L (in natural logarithms)
-__device__ __forceinline__ void decay(float L, float& a, float& m) {
-    a = ex2(kLog2e * L);
-    m = root(one_minus_exp(2.f * L, a * a));
+__device__ __forceinline__ Two root_2(Two x) {
+    float a, b;
+    split(x, a, b);
+    return two(root(a), root(b));
 }
 
 // ---------------------------------------------------------------- sequences
@@ -81,8 +124,7 @@ __device__ __forceinline__ void decay(float L, float& a, float& m) {
 struct Seq {
     int n, s0, s1;
 };
-__device__ __forceinline__ Seq find_seq(const GatedArgs& p, int row, int t) {
-    if (p.cu_seqlens == nullptr) return Seq{row, 0, p.T};
+__device__ __forceinline__ Seq find_seq(const GatedArgs& p, int t) {
     int lo = 0, hi = p.nseq - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -94,191 +136,292 @@ __device__ __forceinline__ Seq find_seq(const GatedArgs& p, int row, int t) {
     return Seq{lo, p.cu_seqlens[lo], p.cu_seqlens[lo + 1]};
 }
 
-// The composition of the strips before this warp's: `mine` receives the value
-// that reaches the warp's strip, the return value what leaves the cluster's
-// whole stretch.  P.x is NaN-safe: a strip that ignores what comes in says so
-// by `cut`.
-template <int E>
-struct Exchange {
-    float2 strip[2][kWarps][E][32];   // (P, H) of this block's strips
-    float2 block[2][kGatedMaxCluster][E][32];
-    int cut[2][kWarps];
-    float2 block_cut[2][kGatedMaxCluster];
+// ---------------------------------------------------------------- exchange
+
+// A map of two channels: h -> P h + H, or h -> H where `cut`.
+struct Map {
+    Two P, H;
+    int cut;
 };
+__device__ __forceinline__ Two pass(const Map& m, Two h) {
+    return m.cut ? m.H : fma2(m.P, h, m.H);
+}
+struct Exchange {
+    float4 warp[2][kWarps][kChannels / 2];  // (P, H) of a channel pair: P0, P1, H0, H1
+    float4 block[2][kGatedMaxCluster][kChannels / 2];
+    int cut[2][kWarps], block_cut[2][kGatedMaxCluster];
+};
+__device__ __forceinline__ Map map_of(const float4& v, int cut) { return Map{two(v.x, v.y), two(v.z, v.w), cut}; }
+__device__ __forceinline__ float4 packed(Two P, Two H) {
+    float4 v;
+    split(P, v.x, v.y);
+    split(H, v.z, v.w);
+    return v;
+}
 
-__device__ __forceinline__ float pass(float2 ph, int cut, float h) { return cut ? ph.y : fmaf(ph.x, h, ph.y); }
-
-template <int E>
-__device__ __forceinline__ void exchange(Exchange<E>& sm, int parity, int warp, int lane, uint32_t rank, int C,
-                                         const float* P, const float* H, int cut, float* carry, float* mine) {
-#pragma unroll
-    for (int e = 0; e < E; ++e) sm.strip[parity][warp][e][lane] = make_float2(P[e], H[e]);
-    if (lane == 0) sm.cut[parity][warp] = cut;
+// From each lane's own map (`later`: its strip is the warp's second) to the value
+// that reaches its strip; `carry`, what reaches the cluster's stretch, becomes
+// what leaves it.  CUTS: some maps may ignore what comes in.
+template <bool CUTS>
+__device__ __forceinline__ Two exchange(Exchange& sm, int parity, int warp, int lane, uint32_t rank, int C, const Map& own,
+                                        bool later, Two& carry) {
+    const int pr = lane & 15;
+    const auto strip = [&](int w) { return map_of(sm.warp[parity][w][pr], CUTS ? sm.cut[parity][w] : 0); };
+    Map far;
+    far.P.v = __shfl_xor_sync(0xffffffffu, own.P.v, 16);
+    far.H.v = __shfl_xor_sync(0xffffffffu, own.H.v, 16);
+    far.cut = CUTS ? __shfl_xor_sync(0xffffffffu, own.cut, 16) : 0;
+    if (later == (lane >= 16)) {  // the half that stores holds the pair in order
+        if (lane < 16) sm.warp[parity][warp][pr] = packed(mul2(own.P, far.P), pass(far, own.H));
+    } else {
+        if (lane < 16) sm.warp[parity][warp][pr] = packed(mul2(own.P, far.P), pass(own, far.H));
+    }
+    if (CUTS && lane == 0) sm.cut[parity][warp] = own.cut | far.cut;
     __syncthreads();
+    Two mine = carry;
     if (C > 1) {
-        if (warp < E) {  // the whole block's map, one row of channels per warp
-            float2 s = make_float2(1.f, 0.f);
+        if (threadIdx.x < 16) {  // the whole block's map
+            Two P = same(1.f), H = same(0.f);
             int any = 0;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
-                const float2 ph = sm.strip[parity][w][warp][lane];
-                const int c = sm.cut[parity][w];
-                s.y = pass(ph, c, s.y);
-                s.x *= ph.x;
-                any |= c;
+                const Map m = strip(w);
+                H = pass(m, H);
+                P = mul2(P, m.P);
+                any |= m.cut;
             }
+            const float4 v = packed(P, H);
             for (int c = 0; c < C; ++c) {
-                store_remote(&sm.block[parity][rank][warp][lane], c, s);
-                if (warp == 0 && lane == 0) store_remote(&sm.block_cut[parity][rank], c, make_float2(any ? 1.f : 0.f, 0.f));
+                store_remote(&sm.block[parity][rank][pr], c, v);
+                if (CUTS && lane == 0) store_remote(&sm.block_cut[parity][rank], c, any);
             }
         }
         cluster_sync();
-#pragma unroll
-        for (int e = 0; e < E; ++e) mine[e] = carry[e];
         for (int c = 0; c < C; ++c) {
-            const int ct = sm.block_cut[parity][c].x != 0.f;
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                if (c == static_cast<int>(rank)) mine[e] = carry[e];
-                carry[e] = pass(sm.block[parity][c][e][lane], ct, carry[e]);
-            }
+            if (c == static_cast<int>(rank)) mine = carry;
+            carry = pass(map_of(sm.block[parity][c][pr], CUTS ? sm.block_cut[parity][c] : 0), carry);
         }
-        for (int w = 0; w < warp; ++w) {
-            const int ct = sm.cut[parity][w];
 #pragma unroll
-            for (int e = 0; e < E; ++e) mine[e] = pass(sm.strip[parity][w][e][lane], ct, mine[e]);
-        }
+        for (int w = 0; w < kWarps - 1; ++w)
+            if (w < warp) mine = pass(strip(w), mine);
     } else {
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            const int ct = sm.cut[parity][w];
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                if (w == warp) mine[e] = carry[e];
-                carry[e] = pass(sm.strip[parity][w][e][lane], ct, carry[e]);
-            }
+            if (w == warp) mine = carry;
+            carry = pass(strip(w), carry);
         }
     }
+    return later ? pass(far, mine) : mine;
 }
 
-template <int E>
-__device__ __forceinline__ void load_state(const float* p, int nd, float* h) {
-#pragma unroll
-    for (int e = 0; e < E; ++e) h[e] = p && e < nd ? p[e] : 0.f;
+// ---------------------------------------------------------------- memory
+
+// A state's two channels (nd of them: 0, 1 or 2), zeros where there is none
+__device__ __forceinline__ Two load_state(const float* base, long long n, int D, int d, int nd) {
+    if (!base) return same(0.f);
+    const float* q = base + n * D + d;
+    return two(nd > 0 ? q[0] : 0.f, nd > 1 ? q[1] : 0.f);
 }
-template <int E>
-__device__ __forceinline__ void store_state(float* p, int nd, const float* h) {
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-        if (e < nd) p[e] = h[e];
+__device__ __forceinline__ void store_state(float* base, long long n, int D, int d, int nd, Two h) {
+    float a, b;
+    split(h, a, b);
+    float* q = base + n * D + d;
+    if (nd == 2 && !(D & 1)) {
+        *reinterpret_cast<float2*>(q) = make_float2(a, b);
+        return;
+    }
+    if (nd > 0) q[0] = a;
+    if (nd > 1) q[1] = b;
 }
+template <typename T>
+__device__ __forceinline__ void store_pair(T* q, int D, int nd, Two v) {
+    const Raw<T, 2> r = pack_2<T, 2>(&v);
+    if (!(D & 1))
+        store_raw<T, 2, true>(q, r, nd);
+    else
+        store_raw<T, 2, false>(q, r, nd);
+}
+// A pair of channels of a tile in shared memory
+template <typename T>
+__device__ __forceinline__ Two pair_at(const T* q) {
+    Raw<T, 2> r;
+    if constexpr (sizeof(T) == 2)
+        r.w[0] = *reinterpret_cast<const uint32_t*>(q);
+    else
+        *reinterpret_cast<uint2*>(r.w) = *reinterpret_cast<const uint2*>(q);
+    return two(r.get(0), r.get(1));
+}
+
+// A warp's copies of its SPAN x kChannels tiles of one input to shared memory,
+// zeros behind the row's end and its last channel, in pieces of PB bytes (PB = 0:
+// element by element and at once, for 2-byte elements at odd places).
+template <typename T, int SPAN, int PB>
+struct Copier {
+    static constexpr int CE = PB ? PB / static_cast<int>(sizeof(T)) : 1, PER = kChannels / CE, LINES = 32 / PER > 0 ? 32 / PER : 1;
+    static constexpr int COUNT = SPAN * PER / 32;
+    const T* at;       // this lane's first piece of the row's first tile
+    long long stride;
+    int row, col, nc;
+    __device__ __forceinline__ Copier(const void* base, long long stride_, long long row0, int d0, int nc_, int lane)
+        : stride(stride_), row(lane / PER), col(lane % PER * CE), nc(nc_) {
+        at = static_cast<const T*>(base) + row0 * stride + d0 + row * stride + col;
+    }
+    // the tile of tokens [t, t + SPAN) of T
+    __device__ __forceinline__ void operator()(T* dst, int t, int tokens, int lane) const {
+        const T* src = at + t * stride;
+        const int left = tokens - t - row;
+        T* to = dst + lane * CE;
+#pragma unroll
+        for (int i = 0; i < COUNT; ++i) {
+            // (PER > 32: a line takes several turns)
+            constexpr int turns = PER > 32 ? PER / 32 : 1;
+            const int line = i / turns * LINES, c = i % turns * 32 * CE;
+            const bool ok = line < left && col + c < nc;
+            const T* from = ok ? src + line * stride + c : static_cast<const T*>(at);
+            if constexpr (PB != 0)
+                copy_async<T, CE>(to + i * 32 * CE, from, ok);
+            else
+                to[i * 32 * CE] = ok ? *from : T(0);
+        }
+    }
+};
+
+template <typename T, int N, int SPAN>
+struct alignas(16) Tiles {
+    T v[2][N][SPAN][kChannels];
+};
+
+// What the two kernels share: the warp's place in its row.
+template <typename T>
+struct Place {
+    int warp, lane, sub, row, D, d0, d, nd, nc, C;
+    uint32_t rank;
+    __device__ __forceinline__ Place(const GatedArgs& p) {
+        warp = threadIdx.x >> 5;
+        lane = threadIdx.x & 31;
+        sub = lane >> 4;
+        C = p.cluster;
+        row = blockIdx.y;
+        rank = C > 1 ? cluster_rank() : 0;
+        D = p.D;
+        d0 = blockIdx.x / C * kChannels;
+        nc = min(kChannels, D - d0);
+        d = d0 + (lane & 15) * 2;
+        nd = max(0, min(2, D - d));
+    }
+};
 
 // ---------------------------------------------------------------- forward
 
-template <typename T, int E>
+// SEQS: packed sequences, whose ends may lie anywhere; otherwise a row is one
+// sequence, and its initial state is what reaches its first strip.
+template <typename T, int PB, bool SEQS>
 __global__ void __launch_bounds__(32 * kWarps, 2) gated_fwd_kernel(const GatedArgs p) {
-    __shared__ Exchange<E> sm;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int C = p.cluster, row = blockIdx.y;
-    const uint32_t rank = C > 1 ? cluster_rank() : 0;
-    const int d = (blockIdx.x / C) * (32 * E) + lane * E;
-    const int nd = max(0, min(E, p.D - d));  // this lane's channels
-    if (blockIdx.x == 0 && row == 0) check_offsets(p.cu_seqlens, p.nseq, p.T, p.err);
-    float scale[E];  // -rate softplus(lam)
-#pragma unroll
-    for (int e = 0; e < E; ++e) scale[e] = e < nd ? -p.rate * softplus(p.lam[d + e]) : 0.f;
-    const long long row0 = static_cast<long long>(row) * p.T;
-    const T* x = static_cast<const T*>(p.x) + row0 * p.x_stride + d;
-    const T* r = static_cast<const T*>(p.r) + row0 * p.r_stride + d;
-    const T* gi = static_cast<const T*>(p.i) + row0 * p.i_stride + d;
-    T* y = static_cast<T*>(p.y) + row0 * p.D + d;
-    const int strips = (p.T + kStrip - 1) / kStrip;
-    if (p.final_state && rank == 0) {  // sequences without tokens
-        const int first = p.cu_seqlens ? 0 : row, last = p.cu_seqlens ? p.nseq : row + 1;
-        for (int n = first + warp; n < last; n += kWarps) {
-            if (p.cu_seqlens ? p.cu_seqlens[n] < p.cu_seqlens[n + 1] : p.T > 0) continue;
-            float h[E];
-            load_state<E>(p.initial_state ? p.initial_state + static_cast<long long>(n) * p.D + d : nullptr, nd, h);
-            store_state<E>(p.final_state + static_cast<long long>(n) * p.D + d, nd, h);
+    constexpr int KS = kStripFwd, SPAN = 2 * KS;
+    extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ Exchange sm;
+    const Place<T> w(p);
+    Tiles<T, 3, SPAN>& tile = reinterpret_cast<Tiles<T, 3, SPAN>*>(smem)[w.warp];
+    if (SEQS && blockIdx.x == 0 && w.row == 0) check_offsets(p.cu_seqlens, p.nseq, p.T, p.err);
+    const float s0 = w.nd > 0 ? -p.rate * softplus(p.lam[w.d]) : 0.f, s1 = w.nd > 1 ? -p.rate * softplus(p.lam[w.d + 1]) : 0.f;
+    const Two scale = two(s0, s1);
+    const bool small = __all_sync(0xffffffffu, s0 >= -0.5f && s1 >= -0.5f);
+    const long long row0 = static_cast<long long>(w.row) * p.T;
+    const Copier<T, SPAN, PB> cr(p.r, p.r_stride, row0, w.d0, w.nc, w.lane), ci(p.i, p.i_stride, row0, w.d0, w.nc, w.lane),
+        cx(p.x, p.x_stride, row0, w.d0, w.nc, w.lane);
+    T* y = static_cast<T*>(p.y) + row0 * p.D + w.d;
+    const int spans = (p.T + SPAN - 1) / SPAN, strips = (p.T + kGatedStrip - 1) / kGatedStrip;
+    const auto start_of = [&](int n) { return load_state(p.initial_state, n, w.D, w.d, w.nd); };
+    if (p.final_state && w.rank == 0 && w.sub == 0) {  // sequences without tokens
+        const int first = SEQS ? 0 : w.row, last = SEQS ? p.nseq : w.row + 1;
+        for (int n = first + w.warp; n < last; n += kWarps) {
+            if (SEQS ? p.cu_seqlens[n] < p.cu_seqlens[n + 1] : p.T > 0) continue;
+            store_state(p.final_state, n, w.D, w.d, w.nd, start_of(n));
         }
     }
-    if (C > 1) cluster_sync();  // every block of the cluster is there
-    float carry[E] = {};
-    for (int s0 = 0, round = 0; s0 < strips; s0 += C * kWarps, ++round) {
-        const int s = s0 + rank * kWarps + warp;
-        const int t0 = s * kStrip;  // s < strips + 64: below 2^30 + 2^10
-        const int nk = max(0, min(kStrip, p.T - t0));
-        Raw<T, E> rx[kStrip], rr[kStrip], ri[kStrip];
-#pragma unroll
-        for (int k = 0; k < kStrip; ++k) {
-            const long long t = t0 + k;
-            const int n = k < nk ? nd : 0;
-            rr[k] = load_raw<T, E>(r + t * p.r_stride, n);
-            ri[k] = load_raw<T, E>(gi + t * p.i_stride, n);
-            rx[k] = load_raw<T, E>(x + t * p.x_stride, n);
+    const int mine0 = static_cast<int>(w.rank) * kWarps + w.warp, step = w.C * kWarps;
+    const auto fetch = [&](int s, int stage) {  // the span s, if there is one
+        if (s < spans) {
+            cr(&tile.v[stage][0][0][0], s * SPAN, p.T, w.lane);
+            ci(&tile.v[stage][1][0][0], s * SPAN, p.T, w.lane);
+            cx(&tile.v[stage][2][0][0], s * SPAN, p.T, w.lane);
         }
-        Seq q = nk > 0 ? find_seq(p, row, t0) : Seq{0, -1, 1 << 30};
-        const bool ends = q.s0 == t0 || q.s1 <= t0 + nk;  // a sequence starts or ends here
-        float a[kStrip][E], b[kStrip][E];
+        commit_copies();
+    };
+    fetch(mine0, 0);
+    if (w.C > 1) cluster_sync();  // every block of the cluster is there
+    Two carry = SEQS ? same(0.f) : start_of(w.row);
+    for (int b0 = 0, round = 0; b0 < spans; b0 += step, ++round) {
+        const int s = b0 + mine0;
+        const int t0 = s * SPAN + w.sub * KS;  // this lane's first token: below 2^30 + 2^13
+        const int nk = max(0, min(KS, p.T - t0));
+        fetch(s + step, (round + 1) & 1);
+        Seq q{w.row, 0, p.T};
+        if (SEQS && nk > 0) q = find_seq(p, t0);
+        // the strip holds a sequence's end, or (packed) its beginning
+        const bool ends = q.s1 <= t0 + KS || (SEQS && q.s0 == t0);
+        wait_copies<1>();
+        __syncwarp();
+        Two a[KS], b[KS];
+        Map m{same(1.f), same(0.f), 0};
+        if (s < spans) {
+            const T* v = &tile.v[round & 1][0][w.sub * KS][(w.lane & 15) * 2];
 #pragma unroll
-        for (int k = 0; k < kStrip; ++k) {
+            for (int k = 0; k < KS; ++k) {
+                Two sr, si, gap;
+                sigmoids(pair_at(v + k * kChannels), pair_at(v + (SPAN + k) * kChannels), sr, si);
+                decay(mul2(scale, sr), small, a[k], gap);
+                b[k] = mul2(root_2(gap), mul2(si, pair_at(v + (2 * SPAN + k) * kChannels)));
+                if (!ends) {
+                    m.H = fma2(a[k], m.H, b[k]);
+                    m.P = mul2(m.P, a[k]);
+                }
+            }
+            if (ends) {
+                Seq e = q;
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                float m;
-                decay(scale[e] * sigmoid(rr[k].get(e)), a[k][e], m);
-                b[k][e] = m * (sigmoid(ri[k].get(e)) * rx[k].get(e));
+                for (int k = 0; k < KS; ++k) {
+                    if (k >= nk) continue;
+                    if (SEQS) {
+                        if (t0 + k >= e.s1) e = find_seq(p, t0 + k);
+                        if (t0 + k == e.s0) {
+                            m.cut = 1;
+                            m.H = start_of(e.n);
+                        }
+                    }
+                    m.H = fma2(a[k], m.H, b[k]);
+                    m.P = mul2(m.P, a[k]);
+                }
             }
         }
-        float P[E], H[E];
-        int cut = 0;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            P[e] = 1.f;
-            H[e] = 0.f;
-        }
+        Two h = exchange<SEQS>(sm, round & 1, w.warp, w.lane, w.rank, w.C, m, w.sub != 0, carry);
+        T* to = y + static_cast<long long>(t0) * p.D;
+        float* keep = p.saved ? p.saved + (static_cast<long long>(w.row) * strips + t0 / kGatedStrip) * p.D : nullptr;
         if (!ends) {
 #pragma unroll
-            for (int k = 0; k < kStrip; ++k)
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    H[e] = fmaf(a[k][e], H[e], b[k][e]);
-                    P[e] *= a[k][e];
-                }
+            for (int k = 0; k < KS; ++k) {
+                if (k % kGatedStrip == 0 && keep) store_state(keep, k / kGatedStrip, w.D, w.d, w.nd, h);
+                h = fma2(a[k], h, b[k]);
+                store_pair<T>(to, w.D, w.nd, h);
+                to += p.D;
+            }
         } else {
-            Seq w = q;
 #pragma unroll
-            for (int k = 0; k < kStrip; ++k) {
-                if (k < nk) {
-                    if (t0 + k >= w.s1) w = find_seq(p, row, t0 + k);
-                    if (t0 + k == w.s0) {
-                        cut = 1;
-                        load_state<E>(p.initial_state ? p.initial_state + static_cast<long long>(w.n) * p.D + d : nullptr, nd, H);
-                    }
-#pragma unroll
-                    for (int e = 0; e < E; ++e) H[e] = fmaf(a[k][e], H[e], b[k][e]);
+            for (int k = 0; k < KS; ++k) {
+                if (k >= nk) continue;
+                if (k % kGatedStrip == 0 && keep) store_state(keep, k / kGatedStrip, w.D, w.d, w.nd, h);
+                if (SEQS) {
+                    if (t0 + k >= q.s1) q = find_seq(p, t0 + k);
+                    if (t0 + k == q.s0) h = start_of(q.n);
                 }
-#pragma unroll
-                for (int e = 0; e < E; ++e) P[e] *= a[k][e];
+                h = fma2(a[k], h, b[k]);
+                store_pair<T>(to, w.D, w.nd, h);
+                to += p.D;
+                if (t0 + k == q.s1 - 1 && p.final_state) store_state(p.final_state, q.n, w.D, w.d, w.nd, h);
             }
-        }
-        float h[E];
-        exchange<E>(sm, round & 1, warp, lane, rank, C, P, H, cut, carry, h);
-        if (p.saved && nk > 0) store_state<E>(p.saved + (static_cast<long long>(row) * strips + s) * p.D + d, nd, h);
-#pragma unroll
-        for (int k = 0; k < kStrip; ++k) {
-            if (ends && k < nk) {
-                if (t0 + k >= q.s1) q = find_seq(p, row, t0 + k);
-                if (t0 + k == q.s0)
-                    load_state<E>(p.initial_state ? p.initial_state + static_cast<long long>(q.n) * p.D + d : nullptr, nd, h);
-            }
-#pragma unroll
-            for (int e = 0; e < E; ++e) h[e] = fmaf(a[k][e], h[e], b[k][e]);
-            if (k < nk) store_raw<T, E>(y + static_cast<long long>(t0 + k) * p.D, pack<T, E>(h), nd);
-            if (ends && k < nk && t0 + k == q.s1 - 1 && p.final_state)
-                store_state<E>(p.final_state + static_cast<long long>(q.n) * p.D + d, nd, h);
         }
     }
-    if (C > 1) cluster_sync();  // the others may still write here
+    if (w.C > 1) cluster_sync();  // the others may still write here
 }
 
 // ---------------------------------------------------------------- reverse mode
@@ -289,149 +432,153 @@ __global__ void __launch_bounds__(32 * kWarps, 2) gated_fwd_kernel(const GatedAr
 //   dL = dh (a h_{t-1} - a^2 / m sigmoid(i) x);  dr = dL L (1 - sigmoid(r));
 //   d(sigmoid(i) x) = dh m;  dlam = -rate sigmoid(lam) sum dL sigmoid(r)
 // Where m = 0 (a rounds to 1) a^2 / m L has the limit 0, and the term is left out.
-template <typename T, int E>
-__global__ void __launch_bounds__(32 * kWarps, 2) gated_bwd_kernel(const GatedArgs p) {
-    __shared__ Exchange<E> sm;
-    __shared__ float part[kWarps][E][32];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int C = p.cluster, row = blockIdx.y;
-    const uint32_t rank = C > 1 ? cluster_rank() : 0;
-    const int d = (blockIdx.x / C) * (32 * E) + lane * E;
-    const int nd = max(0, min(E, p.D - d));
-    if (blockIdx.x == 0 && row == 0) check_offsets(p.cu_seqlens, p.nseq, p.T, p.err);
-    float scale[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) scale[e] = e < nd ? -p.rate * softplus(p.lam[d + e]) : 0.f;
-    const long long row0 = static_cast<long long>(row) * p.T;
-    const T* x = static_cast<const T*>(p.x) + row0 * p.x_stride + d;
-    const T* r = static_cast<const T*>(p.r) + row0 * p.r_stride + d;
-    const T* gi = static_cast<const T*>(p.i) + row0 * p.i_stride + d;
-    const T* go = static_cast<const T*>(p.d_out) + row0 * p.D + d;
-    T* dx = static_cast<T*>(p.dx) + row0 * p.D + d;
-    T* dr = static_cast<T*>(p.dr) + row0 * p.D + d;
-    T* di = static_cast<T*>(p.di) + row0 * p.D + d;
-    const int strips = (p.T + kStrip - 1) / kStrip;
-    const auto state_of = [&](const float* s, int n) { return s ? s + static_cast<long long>(n) * p.D + d : nullptr; };
-    if (p.d_initial_state && rank == 0) {  // sequences without tokens pass the final state's gradient on
-        const int first = p.cu_seqlens ? 0 : row, last = p.cu_seqlens ? p.nseq : row + 1;
-        for (int n = first + warp; n < last; n += kWarps) {
-            if (p.cu_seqlens ? p.cu_seqlens[n] < p.cu_seqlens[n + 1] : p.T > 0) continue;
-            float h[E];
-            load_state<E>(state_of(p.d_final_state, n), nd, h);
-            store_state<E>(p.d_initial_state + static_cast<long long>(n) * p.D + d, nd, h);
+template <typename T, int PB, bool SEQS>
+__global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? 2 : 1) gated_bwd_kernel(const GatedArgs p) {
+    constexpr int KS = kStripBwd, SPAN = 2 * KS;
+    extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ Exchange sm;
+    __shared__ float2 part[kWarps][32];
+    const Place<T> w(p);
+    Tiles<T, 4, SPAN>& tile = reinterpret_cast<Tiles<T, 4, SPAN>*>(smem)[w.warp];
+    if (SEQS && blockIdx.x == 0 && w.row == 0) check_offsets(p.cu_seqlens, p.nseq, p.T, p.err);
+    const float s0 = w.nd > 0 ? -p.rate * softplus(p.lam[w.d]) : 0.f, s1 = w.nd > 1 ? -p.rate * softplus(p.lam[w.d + 1]) : 0.f;
+    const Two scale = two(s0, s1);
+    const bool small = __all_sync(0xffffffffu, s0 >= -0.5f && s1 >= -0.5f);
+    const long long row0 = static_cast<long long>(w.row) * p.T;
+    const Copier<T, SPAN, PB> cr(p.r, p.r_stride, row0, w.d0, w.nc, w.lane), ci(p.i, p.i_stride, row0, w.d0, w.nc, w.lane),
+        cx(p.x, p.x_stride, row0, w.d0, w.nc, w.lane), cg(p.d_out, p.D, row0, w.d0, w.nc, w.lane);
+    const long long out0 = row0 * p.D + w.d;
+    const int spans = (p.T + SPAN - 1) / SPAN, strips = (p.T + KS - 1) / KS;
+    const auto start_of = [&](int n) { return load_state(p.initial_state, n, w.D, w.d, w.nd); };
+    const auto end_of = [&](int n) { return load_state(p.d_final_state, n, w.D, w.d, w.nd); };
+    if (p.d_initial_state && w.rank == 0 && w.sub == 0) {  // sequences without tokens pass the final state's gradient on
+        const int first = SEQS ? 0 : w.row, last = SEQS ? p.nseq : w.row + 1;
+        for (int n = first + w.warp; n < last; n += kWarps) {
+            if (SEQS ? p.cu_seqlens[n] < p.cu_seqlens[n + 1] : p.T > 0) continue;
+            store_state(p.d_initial_state, n, w.D, w.d, w.nd, end_of(n));
         }
     }
-    if (C > 1) cluster_sync();  // every block of the cluster is there
-    float carry[E] = {}, dlam[E] = {};
-    for (int j0 = 0, round = 0; j0 < strips; j0 += C * kWarps, ++round) {
-        const int s = strips - 1 - (j0 + static_cast<int>(rank) * kWarps + warp);  // from the last strip on
-        const int t0 = s * kStrip;
-        const int nk = s < 0 ? 0 : min(kStrip, p.T - t0);
-        Raw<T, E> rx[kStrip], rr[kStrip], ri[kStrip], rg[kStrip];
-#pragma unroll
-        for (int k = 0; k < kStrip; ++k) {
-            const long long t = t0 + k;
-            const int n = k < nk ? nd : 0;
-            rr[k] = load_raw<T, E>(r + t * p.r_stride, n);
-            ri[k] = load_raw<T, E>(gi + t * p.i_stride, n);
-            rx[k] = load_raw<T, E>(x + t * p.x_stride, n);
-            rg[k] = load_raw<T, E>(go + t * p.D, n);
+    const int mine0 = static_cast<int>(w.rank) * kWarps + w.warp, step = w.C * kWarps;
+    const auto fetch = [&](int s, int stage) {
+        if (s >= 0) {
+            cr(&tile.v[stage][0][0][0], s * SPAN, p.T, w.lane);
+            ci(&tile.v[stage][1][0][0], s * SPAN, p.T, w.lane);
+            cx(&tile.v[stage][2][0][0], s * SPAN, p.T, w.lane);
+            cg(&tile.v[stage][3][0][0], s * SPAN, p.T, w.lane);
         }
-        float h[E];
-        load_state<E>(nk > 0 ? p.saved + (static_cast<long long>(row) * strips + s) * p.D + d : nullptr, nd, h);
-        const Seq q0 = nk > 0 ? find_seq(p, row, t0) : Seq{0, -1, 1 << 30};
-        const bool ends = q0.s0 == t0 || q0.s1 <= t0 + nk;
+        commit_copies();
+    };
+    fetch(spans - 1 - mine0, 0);
+    if (w.C > 1) cluster_sync();  // every block of the cluster is there
+    Two carry = SEQS ? same(0.f) : end_of(w.row), dlam = same(0.f);
+    for (int b0 = 0, round = 0; b0 < spans; b0 += step, ++round) {
+        const int s = spans - 1 - (b0 + mine0);  // from the last span on
+        const int t0 = s * SPAN + w.sub * KS;
+        const int nk = s < 0 ? 0 : max(0, min(KS, p.T - t0));
+        __syncwarp();  // everyone is through with the tile that this one replaces
+        fetch(s - step, (round + 1) & 1);
+        Two h = same(0.f);
+        if (nk > 0) h = load_state(p.saved, static_cast<long long>(w.row) * strips + 2 * s + w.sub, w.D, w.d, w.nd);
+        Seq q{w.row, 0, p.T};
+        if (SEQS && nk > 0) q = find_seq(p, t0);
+        // the strip holds a sequence's beginning, or (packed) its end, or is not full
+        const bool ends = q.s0 == t0 || nk < KS || (SEQS && q.s1 <= t0 + KS);
+        wait_copies<1>();
+        __syncwarp();
+        const T* v = &tile.v[round & 1][0][w.sub * KS][(w.lane & 15) * 2];
+        const auto at = [&](int which, int k) { return pair_at(v + (which * SPAN + k) * kChannels); };
         // per token: a, sigmoid(r), sigmoid(i) and the state before it
-        float a[kStrip][E], sr[kStrip][E], si[kStrip][E], hp[kStrip][E];
-        Seq q = q0;
+        Two a[KS], sr[KS], si[KS], hp[KS];
+        Map m{same(1.f), same(0.f), 0};
+        if (nk > 0) {
 #pragma unroll
-        for (int k = 0; k < kStrip; ++k) {
-            if (ends && k < nk) {
-                if (t0 + k >= q.s1) q = find_seq(p, row, t0 + k);
-                if (t0 + k == q.s0) load_state<E>(state_of(p.initial_state, q.n), nd, h);
-            }
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                float m;
-                sr[k][e] = sigmoid(rr[k].get(e));
-                si[k][e] = sigmoid(ri[k].get(e));
-                decay(scale[e] * sr[k][e], a[k][e], m);
-                hp[k][e] = h[e];
-                h[e] = fmaf(a[k][e], h[e], m * (si[k][e] * rx[k].get(e)));
-            }
-        }
-        float P[E], Q[E];
-        int cut = 0;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            P[e] = 1.f;
-            Q[e] = 0.f;
-        }
-        Seq w = q;
-#pragma unroll
-        for (int k = kStrip - 1; k >= 0; --k) {
-            if (ends && k < nk) {
-                if (t0 + k < w.s0) w = find_seq(p, row, t0 + k);
-                if (t0 + k == w.s1 - 1) {  // nothing comes from the next sequence
-                    cut = 1;
-                    load_state<E>(state_of(p.d_final_state, w.n), nd, Q);
+            for (int k = 0; k < KS; ++k) {
+                if (SEQS && ends && k < nk) {
+                    if (t0 + k >= q.s1) q = find_seq(p, t0 + k);
+                    if (t0 + k == q.s0) h = start_of(q.n);
                 }
+                Two gap;
+                sigmoids(at(0, k), at(1, k), sr[k], si[k]);
+                decay(mul2(scale, sr[k]), small, a[k], gap);
+                hp[k] = h;
+                h = fma2(a[k], h, mul2(root_2(gap), mul2(si[k], at(2, k))));
             }
+            if (!ends) {
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                if (k < nk) {  // the row's last strip may be short: its other tokens are not there
-                    Q[e] = a[k][e] * (rg[k].get(e) + Q[e]);
-                    P[e] *= a[k][e];
+                for (int k = KS - 1; k >= 0; --k) {
+                    m.H = mul2(a[k], add2(at(3, k), m.H));
+                    m.P = mul2(m.P, a[k]);
+                }
+            } else {
+                Seq e = q;
+#pragma unroll
+                for (int k = KS - 1; k >= 0; --k) {
+                    if (k >= nk) continue;  // the row's last strip may be short: its other tokens are not there
+                    if (SEQS) {
+                        if (t0 + k < e.s0) e = find_seq(p, t0 + k);
+                        if (t0 + k == e.s1 - 1) {  // nothing comes from the next sequence
+                            m.cut = 1;
+                            m.H = end_of(e.n);
+                        }
+                    }
+                    m.H = mul2(a[k], add2(at(3, k), m.H));
+                    m.P = mul2(m.P, a[k]);
                 }
             }
         }
-        float c[E];
-        exchange<E>(sm, round & 1, warp, lane, rank, C, P, Q, cut, carry, c);
-        w = q;
+        __syncwarp();
+        Two c = exchange<SEQS>(sm, round & 1, w.warp, w.lane, w.rank, w.C, m, w.sub == 0, carry);
+        if (nk > 0) {
+            long long o = out0 + static_cast<long long>(t0 + KS - 1) * p.D;
+            const auto token = [&](int k) {
+                const Two dh = add2(at(3, k), c), L = mul2(scale, sr[k]);
+                Two again, gap;
+                decay(L, small, again, gap);
+                const Two mk = root_2(gap), gx = mul2(si[k], at(2, k));
+                float m0, m1;
+                split(mk, m0, m1);
+                const Two inv = two(m0 > 0.f ? rcp(m0) : 0.f, m1 > 0.f ? rcp(m1) : 0.f);
+                // a h_{t-1} - a^2 / m gx = a (h_{t-1} - a / m gx)
+                const Two past = fma2(mul2(mul2(a[k], inv), same(-1.f)), gx, hp[k]);
+                c = mul2(a[k], dh);
+                const Two dL = mul2(c, past), dg = mul2(dh, mk);
+                dlam = fma2(dL, sr[k], dlam);
+                store_pair<T>(static_cast<T*>(p.dx) + o, w.D, w.nd, mul2(dg, si[k]));
+                store_pair<T>(static_cast<T*>(p.dr) + o, w.D, w.nd, mul2(mul2(dL, L), fma2(same(-1.f), sr[k], same(1.f))));
+                store_pair<T>(static_cast<T*>(p.di) + o, w.D, w.nd, mul2(mul2(dg, gx), fma2(same(-1.f), si[k], same(1.f))));
+            };
+            if (!ends) {
 #pragma unroll
-        for (int k = kStrip - 1; k >= 0; --k) {
-            if (k >= nk) continue;
-            if (ends) {
-                if (t0 + k < w.s0) w = find_seq(p, row, t0 + k);
-                if (t0 + k == w.s1 - 1) load_state<E>(state_of(p.d_final_state, w.n), nd, c);
-            }
-            float ox[E], orr[E], oi[E];
+                for (int k = KS - 1; k >= 0; --k, o -= p.D) token(k);
+            } else {
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const float dh = rg[k].get(e) + c[e], xk = rx[k].get(e), ak = a[k][e];
-                const float L = scale[e] * sr[k][e];
-                const float a2 = ak * ak;
-                const float m = root(one_minus_exp(2.f * L, a2));
-                const float through = m > 0.f ? a2 * rcp(m) : 0.f;
-                const float gx = si[k][e] * xk;
-                const float dL = dh * fmaf(ak, hp[k][e], -through * gx);
-                const float dg = dh * m;
-                ox[e] = dg * si[k][e];
-                oi[e] = dg * gx * (1.f - si[k][e]);
-                orr[e] = dL * L * (1.f - sr[k][e]);
-                dlam[e] = fmaf(dL, sr[k][e], dlam[e]);
-                c[e] = ak * dh;
+                for (int k = KS - 1; k >= 0; --k, o -= p.D) {
+                    if (k >= nk) continue;
+                    if (SEQS) {
+                        if (t0 + k < q.s0) q = find_seq(p, t0 + k);
+                        if (t0 + k == q.s1 - 1) c = end_of(q.n);
+                    }
+                    token(k);
+                    if (t0 + k == q.s0 && p.d_initial_state) store_state(p.d_initial_state, q.n, w.D, w.d, w.nd, c);
+                }
             }
-            const long long o = static_cast<long long>(t0 + k) * p.D;
-            store_raw<T, E>(dx + o, pack<T, E>(ox), nd);
-            store_raw<T, E>(dr + o, pack<T, E>(orr), nd);
-            store_raw<T, E>(di + o, pack<T, E>(oi), nd);
-            if (ends && t0 + k == w.s0 && p.d_initial_state)
-                store_state<E>(p.d_initial_state + static_cast<long long>(w.n) * p.D + d, nd, c);
         }
     }
-#pragma unroll
-    for (int e = 0; e < E; ++e) part[warp][e][lane] = dlam[e];
+    float a0, a1;
+    split(dlam, a0, a1);
+    part[w.warp][w.lane] = make_float2(a0, a1);
     __syncthreads();
-    if (warp < E) {  // one row of channels per warp
+    if (threadIdx.x < kChannels) {  // a channel per thread
+        const int pr = threadIdx.x / 2, d = w.d0 + static_cast<int>(threadIdx.x);
         float sum = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) sum += part[w][warp][lane];
-        const int dd = d + warp;
-        if (dd < p.D)
-            p.partial[(static_cast<long long>(row) * C + rank) * p.D + dd] = -p.rate * sigmoid(p.lam[dd]) * sum;
+        for (int k = 0; k < kWarps; ++k) {
+            const float2 u = part[k][pr], v = part[k][16 + pr];
+            sum += threadIdx.x & 1 ? u.y + v.y : u.x + v.x;
+        }
+        if (d < p.D) p.partial[(static_cast<long long>(w.row) * w.C + w.rank) * p.D + d] = -p.rate * sigmoid(p.lam[d]) * sum;
     }
-    if (C > 1) cluster_sync();
+    if (w.C > 1) cluster_sync();
 }
 
 // ---------------------------------------------------------------- one token
@@ -473,9 +620,12 @@ __global__ void __launch_bounds__(256) gated_step_kernel(const GatedStepArgs p) 
     float out[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-        float a, m;
-        decay(-p.rate * softplus(rl.get(e)) * sigmoid(rr.get(e)), a, m);
-        out[e] = on ? fmaf(a, h.get(e), m * (sigmoid(ri.get(e)) * rx.get(e))) : 0.f;
+        Two a, gap;
+        decay(same(-p.rate * softplus(rl.get(e)) * sigmoid(rr.get(e))), false, a, gap);
+        float a0, m0, skip;
+        split(a, a0, skip);
+        split(gap, m0, skip);
+        out[e] = on ? fmaf(a0, h.get(e), root(m0) * (sigmoid(ri.get(e)) * rx.get(e))) : 0.f;
     }
     if (on) store_raw<float, E, VEC>(p.out_state + so, pack<float, E>(out), nd);
     store_raw<T, E, VEC>(static_cast<T*>(p.y) + b * p.D + d, pack<T, E>(out), nd);
@@ -483,50 +633,64 @@ __global__ void __launch_bounds__(256) gated_step_kernel(const GatedStepArgs p) 
 
 // ---------------------------------------------------------------- launches
 
-// E elements per access: every row starts at a multiple of their size
+// Every row of these starts at a multiple of `bytes`
 template <typename T>
-bool fits(int E, int D, std::initializer_list<const void*> ptrs, std::initializer_list<long long> strides) {
+bool fits(int bytes, int D, std::initializer_list<const void*> ptrs, std::initializer_list<long long> strides) {
+    const int E = bytes / static_cast<int>(sizeof(T));
     if (D % E != 0) return false;
     for (const void* q : ptrs)
-        if (q && reinterpret_cast<uintptr_t>(q) % (sizeof(T) * E) != 0) return false;
+        if (q && reinterpret_cast<uintptr_t>(q) % bytes != 0) return false;
     for (long long s : strides)
         if (s % E != 0) return false;
     return true;
 }
 
 template <typename K>
-cudaError_t launch_clusters(K kernel, dim3 grid, int cluster, const GatedArgs& a, cudaStream_t stream) {
+cudaError_t launch_clusters(K kernel, size_t smem, const GatedArgs& a, cudaStream_t stream) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
+    cfg.gridDim = dim3(static_cast<unsigned>((a.D + kChannels - 1) / kChannels * a.cluster), a.rows);
     cfg.blockDim = dim3(32 * kWarps);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = cluster;
+    attr.val.clusterDim.x = a.cluster;
     attr.val.clusterDim.y = 1;
     attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
-    cfg.numAttrs = cluster > 1 ? 1 : 0;
+    cfg.numAttrs = a.cluster > 1 ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
+template <typename T, int PB>
+cudaError_t launch_pieces(const GatedArgs& a, bool backward, cudaStream_t stream) {
+    constexpr size_t bwd = sizeof(Tiles<T, 4, 2 * kStripBwd>) * kWarps, fwd = sizeof(Tiles<T, 3, 2 * kStripFwd>) * kWarps;
+    if (a.cu_seqlens)
+        return backward ? launch_clusters(gated_bwd_kernel<T, PB, true>, bwd, a, stream)
+                        : launch_clusters(gated_fwd_kernel<T, PB, true>, fwd, a, stream);
+    return backward ? launch_clusters(gated_bwd_kernel<T, PB, false>, bwd, a, stream)
+                    : launch_clusters(gated_fwd_kernel<T, PB, false>, fwd, a, stream);
+}
 template <typename T>
 cudaError_t launch(const GatedArgs& a, bool backward, cudaStream_t stream) {
-    const bool pair = fits<T>(2, a.D, {a.x, a.r, a.i}, {a.x_stride, a.r_stride, a.i_stride});
-    const dim3 grid(static_cast<unsigned>((a.D + (pair ? 63 : 31)) / (pair ? 64 : 32) * a.cluster), a.rows);
-    if (backward)
-        return pair ? launch_clusters(gated_bwd_kernel<T, 2>, grid, a.cluster, a, stream)
-                    : launch_clusters(gated_bwd_kernel<T, 1>, grid, a.cluster, a, stream);
-    return pair ? launch_clusters(gated_fwd_kernel<T, 2>, grid, a.cluster, a, stream)
-                : launch_clusters(gated_fwd_kernel<T, 1>, grid, a.cluster, a, stream);
+    const auto ok = [&](int bytes) { return fits<T>(bytes, a.D, {a.x, a.r, a.i}, {a.x_stride, a.r_stride, a.i_stride}); };
+    if (ok(16)) return launch_pieces<T, 16>(a, backward, stream);
+    if constexpr (sizeof(T) == 2) {
+        if (!ok(4)) return launch_pieces<T, 0>(a, backward, stream);
+    }
+    return launch_pieces<T, 4>(a, backward, stream);
 }
 
 }  // namespace
 
-int gated_cluster(int rows, int T, int D) {
-    const long long units = static_cast<long long>(rows) * ((D + 63) / 64);
+// Blocks side by side: as many as are resident together, none without a span.
+int gated_cluster(int rows, int T, int D, int dtype, bool backward) {
+    const long long units = static_cast<long long>(rows) * ((D + kChannels - 1) / kChannels);
+    const int slots = 152 * (dtype == 1 ? 1 : 2), span = 2 * (backward ? kStripBwd : kStripFwd);
     int c = 1;
-    while (c < kGatedMaxCluster && units * c < 3 * 152 && static_cast<long long>(T) > static_cast<long long>(c) * kWarps * kStrip) c *= 2;
+    while (c < kGatedMaxCluster && units * c * 2 <= slots && static_cast<long long>(T) > static_cast<long long>(c) * kWarps * span) c *= 2;
     return c;
 }
 
@@ -540,7 +704,7 @@ cudaError_t launch_gated_bwd(const GatedArgs& a, cudaStream_t stream) {
 namespace {
 template <typename T>
 cudaError_t launch_step(const GatedStepArgs& a, cudaStream_t stream) {
-    const bool vec = fits<T>(4, a.D, {a.x, a.r, a.i}, {a.x_stride, a.r_stride, a.i_stride});
+    const bool vec = fits<T>(4 * static_cast<int>(sizeof(T)), a.D, {a.x, a.r, a.i}, {a.x_stride, a.r_stride, a.i_stride});
     const long long n = static_cast<long long>(a.B) * (vec ? a.D / 4 : a.D);
     const unsigned blocks = static_cast<unsigned>((n + 255) / 256);
     if (vec)

@@ -517,7 +517,7 @@ struct GatedStepArgs {
     int B, S, D, dtype;
     int* err;
 };
-int gated_cluster(int rows, int T, int D);
+int gated_cluster(int rows, int T, int D, int dtype, bool backward);
 cudaError_t launch_gated_fwd(const GatedArgs& a, cudaStream_t stream);
 cudaError_t launch_gated_bwd(const GatedArgs& a, cudaStream_t stream);
 cudaError_t launch_gated_step(const GatedStepArgs& a, cudaStream_t stream);

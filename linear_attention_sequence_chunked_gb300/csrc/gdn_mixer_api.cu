@@ -104,7 +104,11 @@ size_t gated_saved(int B, int T, int D, bool varlen) {
     const long long strips = (static_cast<long long>(T) + gdn::kGatedStrip - 1) / gdn::kGatedStrip;
     return round_up(sizeof(float) * (varlen ? 1 : B) * strips * D);
 }
-size_t gated_ws(int rows, int T, int D) { return round_up(sizeof(float) * rows * gdn::gated_cluster(rows, T, D) * static_cast<size_t>(D)); }
+// partial sums of dlam (enough of them for either type)
+size_t gated_ws(int rows, int T, int D) {
+    const int c = std::max(gdn::gated_cluster(rows, T, D, 0, true), gdn::gated_cluster(rows, T, D, 1, true));
+    return round_up(sizeof(float) * rows * c * static_cast<size_t>(D));
+}
 
 gdn_status check_norm(int64_t rows, int C, int groups, int activation, int dtype) {
     if (rows < 0 || C < 1 || groups < 1 || C % groups != 0) return GDN_ERR_INVALID_ARG;
@@ -392,7 +396,7 @@ gdn_status gdn_gated_fwd(const void* x, int64_t x_stride, const void* r, int64_t
     a.lam = lam; a.rate = rate; a.initial_state = initial_state; a.cu_seqlens = cu_seqlens; a.y = y;
     a.final_state = final_state; a.saved = static_cast<float*>(saved);
     a.rows = varlen ? 1 : B; a.nseq = B; a.T = T; a.D = D; a.dtype = dtype; a.err = err;
-    a.cluster = gdn::gated_cluster(a.rows, T, D);
+    a.cluster = gdn::gated_cluster(a.rows, T, D, dtype, false);
     return gdn::count_launch(gdn::launch_gated_fwd(a, stream)) ? GDN_OK : GDN_ERR_CUDA;
 }
 
@@ -430,7 +434,7 @@ gdn_status gdn_gated_bwd(const void* x, int64_t x_stride, const void* r, int64_t
     a.d_out = d_out; a.d_final_state = d_final_state; a.dx = dx; a.dr = dr; a.di = di;
     a.d_initial_state = d_initial_state; a.partial = static_cast<float*>(workspace);
     a.rows = rows; a.nseq = B; a.T = T; a.D = D; a.dtype = dtype; a.err = err;
-    a.cluster = gdn::gated_cluster(rows, T, D);
+    a.cluster = gdn::gated_cluster(rows, T, D, dtype, true);
     if (!gdn::count_launch(gdn::launch_gated_bwd(a, stream))) return GDN_ERR_CUDA;
     gdn::ColumnSumArgs c{};
     c.partial = a.partial; c.c0 = c.cols = c.stride = D; c.rows = rows * a.cluster; c.out[0] = dlam;
