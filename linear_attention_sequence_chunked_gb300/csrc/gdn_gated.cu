@@ -19,6 +19,7 @@
 // Packed sequences are one row: a sequence's first token starts from its own
 // initial state, and a strip that holds such a token ignores what comes in.
 #include <algorithm>
+#include <type_traits>
 
 #include "gdn_kernels.h"
 #include "gdn_mix_common.cuh"
@@ -61,24 +62,6 @@ __device__ __forceinline__ void store_remote(int* p, uint32_t rank, int v) {
 
 __device__ __forceinline__ Two same(float c) { return two(c, c); }
 
-// min(x, 62), a NaN where x is one
-__device__ __forceinline__ float cap(float x) {
-    float y;
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(62.f));
-    return y;
-}
-// sigmoid(r) and sigmoid(i) with one reciprocal for both.  The exponentials are
-// cut at 2^62 so that their product stays finite: sigmoids below 2^-62 are that.
-__device__ __forceinline__ void sigmoids(Two r, Two i, Two& sr, Two& si) {
-    float r0, r1, i0, i1;
-    split(mul2(same(-kLog2e), r), r0, r1);
-    split(mul2(same(-kLog2e), i), i0, i1);
-    const Two p = add2(same(1.f), two(ex2(cap(r0)), ex2(cap(r1))));
-    const Two q = add2(same(1.f), two(ex2(cap(i0)), ex2(cap(i1))));
-    const Two w = rcp_2(mul2(p, q));
-    sr = mul2(w, q);
-    si = mul2(w, p);
-}
 // exp(L) - 1 for -1/2 <= L <= 0, by the exponential series up to L^9 / 9!
 // (relative error below 2^-24)
 __device__ __forceinline__ Two expm1_series(Two L) {
@@ -92,11 +75,12 @@ __device__ __forceinline__ Two expm1_series(Two L) {
     s = fma2(L, s, same(1.f));
     return mul2(L, s);
 }
-// a = exp(L) and 1 - a^2 = -u (2 + u) with u = a - 1.  `small`: no L of this
+// a = exp(L) and 1 - a^2 = -u (2 + u) with u = a - 1.  SMALL: no L of this
 // warp's channels is below -1/2, whatever the gate.
-__device__ __forceinline__ void decay(Two L, bool small, Two& a, Two& gap) {
+template <bool SMALL>
+__device__ __forceinline__ void decay(Two L, Two& a, Two& gap) {
     Two u = expm1_series(L);
-    if (!small) {
+    if constexpr (!SMALL) {
         float l0, l1, u0, u1;
         split(L, l0, l1);
         split(u, u0, u1);
@@ -106,6 +90,14 @@ __device__ __forceinline__ void decay(Two L, bool small, Two& a, Two& gap) {
     }
     a = add2(same(1.f), u);
     gap = mul2(u, fma2(same(-1.f), u, same(-2.f)));
+}
+// f(std::true_type) where `small`, else f(std::false_type): one branch around a loop
+template <typename F>
+__device__ __forceinline__ void with_size(bool small, F&& f) {
+    if (small)
+        f(std::true_type{});
+    else
+        f(std::false_type{});
 }
 __device__ __forceinline__ float root(float x) {
     float y;
@@ -233,14 +225,13 @@ __device__ __forceinline__ void store_state(float* base, long long n, int D, int
     if (nd > 0) q[0] = a;
     if (nd > 1) q[1] = b;
 }
-template <typename T>
-__device__ __forceinline__ void store_pair(T* q, int D, int nd, Two v) {
-    const Raw<T, 2> r = pack_2<T, 2>(&v);
-    if (!(D & 1))
-        store_raw<T, 2, true>(q, r, nd);
-    else
-        store_raw<T, 2, false>(q, r, nd);
+// EVEN: rows of an even number of channels, so a pair is one access
+template <typename T, bool EVEN>
+__device__ __forceinline__ void store_pair(T* q, int nd, Two v) {
+    store_raw<T, 2, EVEN>(q, pack_2<T, 2>(&v), nd);
 }
+template <typename T, int PB>
+constexpr bool kEven = PB == 16 || (PB == 4 && sizeof(T) == 2);
 // A pair of channels of a tile in shared memory
 template <typename T>
 __device__ __forceinline__ Two pair_at(const T* q) {
@@ -366,13 +357,18 @@ __global__ void __launch_bounds__(32 * kWarps, 2) gated_fwd_kernel(const GatedAr
         Map m{same(1.f), same(0.f), 0};
         if (s < spans) {
             const T* v = &tile.v[round & 1][0][w.sub * KS][(w.lane & 15) * 2];
+            with_size(small, [&](auto size) {
 #pragma unroll
-            for (int k = 0; k < KS; ++k) {
-                Two sr, si, gap;
-                sigmoids(pair_at(v + k * kChannels), pair_at(v + (SPAN + k) * kChannels), sr, si);
-                decay(mul2(scale, sr), small, a[k], gap);
-                b[k] = mul2(root_2(gap), mul2(si, pair_at(v + (2 * SPAN + k) * kChannels)));
-                if (!ends) {
+                for (int k = 0; k < KS; ++k) {
+                    Two gap;
+                    decay<decltype(size)::value>(mul2(scale, sigmoid_2(pair_at(v + k * kChannels))), a[k], gap);
+                    const Two si = sigmoid_2(pair_at(v + (SPAN + k) * kChannels));
+                    b[k] = mul2(root_2(gap), mul2(si, pair_at(v + (2 * SPAN + k) * kChannels)));
+                }
+            });
+            if (!ends) {
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
                     m.H = fma2(a[k], m.H, b[k]);
                     m.P = mul2(m.P, a[k]);
                 }
@@ -402,7 +398,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) gated_fwd_kernel(const GatedAr
             for (int k = 0; k < KS; ++k) {
                 if (k % kGatedStrip == 0 && keep) store_state(keep, k / kGatedStrip, w.D, w.d, w.nd, h);
                 h = fma2(a[k], h, b[k]);
-                store_pair<T>(to, w.D, w.nd, h);
+                store_pair<T, kEven<T, PB>>(to, w.nd, h);
                 to += p.D;
             }
         } else {
@@ -415,7 +411,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) gated_fwd_kernel(const GatedAr
                     if (t0 + k == q.s0) h = start_of(q.n);
                 }
                 h = fma2(a[k], h, b[k]);
-                store_pair<T>(to, w.D, w.nd, h);
+                store_pair<T, kEven<T, PB>>(to, w.nd, h);
                 to += p.D;
                 if (t0 + k == q.s1 - 1 && p.final_state) store_state(p.final_state, q.n, w.D, w.d, w.nd, h);
             }
@@ -487,21 +483,27 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? 2 : 1) gated_bwd
         __syncwarp();
         const T* v = &tile.v[round & 1][0][w.sub * KS][(w.lane & 15) * 2];
         const auto at = [&](int which, int k) { return pair_at(v + (which * SPAN + k) * kChannels); };
-        // per token: a, sigmoid(r), sigmoid(i) and the state before it
-        Two a[KS], sr[KS], si[KS], hp[KS];
+        // per token: a, m, sigmoid(i) and the state before it
+        Two a[KS], mk[KS], si[KS], hp[KS];
         Map m{same(1.f), same(0.f), 0};
         if (nk > 0) {
+            with_size(small, [&](auto size) {
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+                    Two gap;
+                    decay<decltype(size)::value>(mul2(scale, sigmoid_2(at(0, k))), a[k], gap);
+                    mk[k] = root_2(gap);
+                    si[k] = sigmoid_2(at(1, k));
+                }
+            });
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
                 if (SEQS && ends && k < nk) {
                     if (t0 + k >= q.s1) q = find_seq(p, t0 + k);
                     if (t0 + k == q.s0) h = start_of(q.n);
                 }
-                Two gap;
-                sigmoids(at(0, k), at(1, k), sr[k], si[k]);
-                decay(mul2(scale, sr[k]), small, a[k], gap);
                 hp[k] = h;
-                h = fma2(a[k], h, mul2(root_2(gap), mul2(si[k], at(2, k))));
+                h = fma2(a[k], h, mul2(mk[k], mul2(si[k], at(2, k))));
             }
             if (!ends) {
 #pragma unroll
@@ -531,21 +533,18 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? 2 : 1) gated_bwd
         if (nk > 0) {
             long long o = out0 + static_cast<long long>(t0 + KS - 1) * p.D;
             const auto token = [&](int k) {
-                const Two dh = add2(at(3, k), c), L = mul2(scale, sr[k]);
-                Two again, gap;
-                decay(L, small, again, gap);
-                const Two mk = root_2(gap), gx = mul2(si[k], at(2, k));
+                const Two dh = add2(at(3, k), c), sr = sigmoid_2(at(0, k)), gx = mul2(si[k], at(2, k));
                 float m0, m1;
-                split(mk, m0, m1);
+                split(mk[k], m0, m1);
                 const Two inv = two(m0 > 0.f ? rcp(m0) : 0.f, m1 > 0.f ? rcp(m1) : 0.f);
                 // a h_{t-1} - a^2 / m gx = a (h_{t-1} - a / m gx)
                 const Two past = fma2(mul2(mul2(a[k], inv), same(-1.f)), gx, hp[k]);
                 c = mul2(a[k], dh);
-                const Two dL = mul2(c, past), dg = mul2(dh, mk);
-                dlam = fma2(dL, sr[k], dlam);
-                store_pair<T>(static_cast<T*>(p.dx) + o, w.D, w.nd, mul2(dg, si[k]));
-                store_pair<T>(static_cast<T*>(p.dr) + o, w.D, w.nd, mul2(mul2(dL, L), fma2(same(-1.f), sr[k], same(1.f))));
-                store_pair<T>(static_cast<T*>(p.di) + o, w.D, w.nd, mul2(mul2(dg, gx), fma2(same(-1.f), si[k], same(1.f))));
+                const Two dL = mul2(c, past), dg = mul2(dh, mk[k]);
+                dlam = fma2(dL, sr, dlam);
+                store_pair<T, kEven<T, PB>>(static_cast<T*>(p.dx) + o, w.nd, mul2(dg, si[k]));
+                store_pair<T, kEven<T, PB>>(static_cast<T*>(p.dr) + o, w.nd, mul2(mul2(dL, mul2(scale, sr)), fma2(same(-1.f), sr, same(1.f))));
+                store_pair<T, kEven<T, PB>>(static_cast<T*>(p.di) + o, w.nd, mul2(mul2(dg, gx), fma2(same(-1.f), si[k], same(1.f))));
             };
             if (!ends) {
 #pragma unroll
@@ -621,7 +620,7 @@ __global__ void __launch_bounds__(256) gated_step_kernel(const GatedStepArgs p) 
 #pragma unroll
     for (int e = 0; e < E; ++e) {
         Two a, gap;
-        decay(same(-p.rate * softplus(rl.get(e)) * sigmoid(rr.get(e))), false, a, gap);
+        decay<false>(same(-p.rate * softplus(rl.get(e)) * sigmoid(rr.get(e))), a, gap);
         float a0, m0, skip;
         split(a, a0, skip);
         split(gap, m0, skip);
