@@ -27,7 +27,12 @@ namespace {
 
 using namespace win;
 
-constexpr int kThreads = 320;  // warps 0-3 and 4-7: a tile's rows each; 8: copies; 9: products
+constexpr int kThreads = 384;  // warps 0-3 and 4-7: a tile's rows each; 8: copies; 9: products
+// The rows' warps hold 128 scores a thread: the registers that the third
+// warpgroup does not need go to them.  The shares add up to what the block is
+// launched with, which the launch checks.
+constexpr int kRegsLaunch = 168, kRegsRows = 224, kRegsOther = 56;
+static_assert(2 * kRegsRows + kRegsOther == 3 * kRegsLaunch, "register shares");
 constexpr float kGrow = 8.f;
 
 // mbarriers
@@ -135,202 +140,211 @@ __global__ void __launch_bounds__(kThreads, 1)
         return false;
     };
 
-    if (warp == 8) {
-        if (lane == 0) {
-            for (int x = 0; x < (second ? 2 : 1); ++x) {
-                mbar_arrive_expect_tx(bar(bQ + x), L::kTileBytes);
-                for (int s = 0; s < kSlabs; ++s)
-                    tma_load_3d(smem_u32(sm + L::q + x * L::kTileBytes + s * kSlab), &map_q, 64 * s, h0 + (two_heads ? x : 0),
-                                static_cast<int>(row0 + q0 + (two_heads ? 0 : x * kTile)), bar(bQ + x));
-            }
-        }
-        int loaded_k = 0, loaded_v = 0, tails = 0;
-        bool ok = true;
-        for (int j = 0; j < nblk; ++j) {
-            const int st = j & 1, ph = ((j >> 1) & 1) ^ 1;
-            const int row = static_cast<int>(row0 + blk.start(j));
-            ok = j < 2 || __all_sync(0xffffffffu, wait(bKFree + st, ph));
-            // K's rows behind the sequence are masked, V's have to be zeros
-            if (ok) ok = load_tile<D>(sm + L::k + st * L::kTileBytes, &map_k, hk, row, kTile, bar(bK + st), bar(bTail), tails, lane);
-            if (!ok) break;
-            loaded_k = j + 1;
-            ok = j < 2 || __all_sync(0xffffffffu, wait(bVFree + st, ph));
-            if (ok) ok = load_tile<D>(sm + L::v + st * L::kTileBytes, &map_v, hk, row, min(kTile, len - blk.start(j)), bar(bV + st),
-                                      bar(bTail), tails, lane);
-            if (!ok) break;
-            loaded_v = j + 1;
-        }
-        if (!ok) *stop = 1;
-        // every copy has landed before the block may leave
-        for (int x = 0; x < (second ? 2 : 1); ++x) mbar_wait(bar(bQ + x), 0);
-        for (int j = max(0, loaded_k - 2); j < loaded_k; ++j) mbar_wait(bar(bK + (j & 1)), (j >> 1) & 1);
-        for (int j = max(0, loaded_v - 2); j < loaded_v; ++j) mbar_wait(bar(bV + (j & 1)), (j >> 1) & 1);
-        __syncwarp();
-    } else if (warp == 9) {
-        if (elect_one()) {
-            const auto scores = [&](int j, int x) {  // S of tile x with block j
-                const uint32_t qa = smem_u32(sm + L::q + x * L::kTileBytes), ka = smem_u32(sm + L::k + (j & 1) * L::kTileBytes);
-                const uint32_t id = idesc(kFmtBf16, 0, 0, 128, blk.width(j));
-#pragma unroll
-                for (int s = 0; s < D / 16; ++s) {
-                    const uint32_t o = (s >> 2) * kSlab + (s & 3) * 32;
-                    mma_bf16(tmem + 128 * x, desc_sw128(qa + o, 0, 1024), desc_sw128(ka + o, 0, 1024), id, s > 0);
+    if (warp >= 8) {
+        registers_down<kRegsOther>();
+        if (warp == 8) {
+            if (lane == 0) {
+                for (int x = 0; x < (second ? 2 : 1); ++x) {
+                    mbar_arrive_expect_tx(bar(bQ + x), L::kTileBytes);
+                    for (int s = 0; s < kSlabs; ++s)
+                        tma_load_3d(smem_u32(sm + L::q + x * L::kTileBytes + s * kSlab), &map_q, 64 * s, h0 + (two_heads ? x : 0),
+                                    static_cast<int>(row0 + q0 + (two_heads ? 0 : x * kTile)), bar(bQ + x));
                 }
-                mma_commit(bar(bS + x));
-            };
-            const int tiles = second ? 2 : 1;
-            bool ok = true;
-            for (int x = 0; x < tiles && ok; ++x) {
-                ok = wait(bQ + x, 0) && wait(bK, 0);
-                if (!ok) break;
-                tc_fence_after();
-                scores(0, x);
             }
-            if (ok) mma_commit(bar(bKFree));
-            constexpr uint32_t id_o = idesc(kFmtBf16, 0, 1, 128, D);
-            for (int j = 0; j < nblk && ok; ++j) {
-                const int steps = blk.width(j) / 16;
+            int loaded_k = 0, loaded_v = 0, tails = 0;
+            bool ok = true;
+            for (int j = 0; j < nblk; ++j) {
+                const int st = j & 1, ph = ((j >> 1) & 1) ^ 1;
+                const int row = static_cast<int>(row0 + blk.start(j));
+                ok = j < 2 || __all_sync(0xffffffffu, wait(bKFree + st, ph));
+                // K's rows behind the sequence are masked, V's have to be zeros
+                if (ok) ok = load_tile<D>(sm + L::k + st * L::kTileBytes, &map_k, hk, row, kTile, bar(bK + st), bar(bTail), tails, lane);
+                if (!ok) break;
+                loaded_k = j + 1;
+                ok = j < 2 || __all_sync(0xffffffffu, wait(bVFree + st, ph));
+                if (ok) ok = load_tile<D>(sm + L::v + st * L::kTileBytes, &map_v, hk, row, min(kTile, len - blk.start(j)), bar(bV + st),
+                                          bar(bTail), tails, lane);
+                if (!ok) break;
+                loaded_v = j + 1;
+            }
+            if (!ok) *stop = 1;
+            // every copy has landed before the block may leave
+            for (int x = 0; x < (second ? 2 : 1); ++x) mbar_wait(bar(bQ + x), 0);
+            for (int j = max(0, loaded_k - 2); j < loaded_k; ++j) mbar_wait(bar(bK + (j & 1)), (j >> 1) & 1);
+            for (int j = max(0, loaded_v - 2); j < loaded_v; ++j) mbar_wait(bar(bV + (j & 1)), (j >> 1) & 1);
+            __syncwarp();
+        } else if (warp == 9) {
+            if (elect_one()) {
+                const auto scores = [&](int j, int x) {  // S of tile x with block j
+                    const uint32_t qa = smem_u32(sm + L::q + x * L::kTileBytes), ka = smem_u32(sm + L::k + (j & 1) * L::kTileBytes);
+                    const uint32_t id = idesc(kFmtBf16, 0, 0, 128, blk.width(j));
+#pragma unroll
+                    for (int s = 0; s < D / 16; ++s) {
+                        const uint32_t o = (s >> 2) * kSlab + (s & 3) * 32;
+                        mma_bf16(tmem + 128 * x, desc_sw128(qa + o, 0, 1024), desc_sw128(ka + o, 0, 1024), id, s > 0);
+                    }
+                    mma_commit(bar(bS + x));
+                };
+                const int tiles = second ? 2 : 1;
+                bool ok = true;
                 for (int x = 0; x < tiles && ok; ++x) {
-                    ok = wait(bV + (j & 1), (j >> 1) & 1) && wait(bP + x, j & 1);
+                    ok = wait(bQ + x, 0) && wait(bK, 0);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t va = smem_u32(sm + L::v + (j & 1) * L::kTileBytes);
-                    for (int s = 0; s < steps; ++s)
-                        mma_bf16_ts(tmem + 256 + 128 * x, tmem + 128 * x + 8 * s, desc_sw128(va + s * 2048, kSlab, 1024), id_o,
-                                    (j | s) != 0);
-                    if (j + 1 == nblk) mma_commit(bar(bO + x));
-                    if (x == tiles - 1) mma_commit(bar(bVFree + (j & 1)));
-                    if (j + 1 < nblk) {
-                        ok = wait(bK + ((j + 1) & 1), ((j + 1) >> 1) & 1);
+                    scores(0, x);
+                }
+                if (ok) mma_commit(bar(bKFree));
+                constexpr uint32_t id_o = idesc(kFmtBf16, 0, 1, 128, D);
+                for (int j = 0; j < nblk && ok; ++j) {
+                    const int steps = blk.width(j) / 16;
+                    for (int x = 0; x < tiles && ok; ++x) {
+                        ok = wait(bV + (j & 1), (j >> 1) & 1) && wait(bP + x, j & 1);
                         if (!ok) break;
                         tc_fence_after();
-                        scores(j + 1, x);
-                        if (x == tiles - 1) mma_commit(bar(bKFree + ((j + 1) & 1)));
+                        const uint32_t va = smem_u32(sm + L::v + (j & 1) * L::kTileBytes);
+                        for (int s = 0; s < steps; ++s)
+                            mma_bf16_ts(tmem + 256 + 128 * x, tmem + 128 * x + 8 * s, desc_sw128(va + s * 2048, kSlab, 1024), id_o,
+                                        (j | s) != 0);
+                        if (j + 1 == nblk) mma_commit(bar(bO + x));
+                        if (x == tiles - 1) mma_commit(bar(bVFree + (j & 1)));
+                        if (j + 1 < nblk) {
+                            ok = wait(bK + ((j + 1) & 1), ((j + 1) >> 1) & 1);
+                            if (!ok) break;
+                            tc_fence_after();
+                            scores(j + 1, x);
+                            if (x == tiles - 1) mma_commit(bar(bKFree + ((j + 1) & 1)));
+                        }
                     }
                 }
+                // every product has completed before the tensor memory is freed
+                mma_commit(bar(bDrain));
+                mbar_wait(bar(bDrain), 0);
             }
-            // every product has completed before the tensor memory is freed
-            mma_commit(bar(bDrain));
-            mbar_wait(bar(bDrain), 0);
-        }
-        __syncwarp();
-    } else if (warp < 4 || second) {
-        const int x = warp >> 2;
-        const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-        const uint32_t tS = tmem + lanes + 128 * x, tO = tmem + lanes + 256 + 128 * x;
-        const int qx = q0 + (two_heads ? 0 : x * kTile);  // this tile's first query
-        const int i = qx + 32 * (warp & 3) + lane;        // this thread's
-        const float c2 = p.scale * mix::kLog2e;
-        float m = -INFINITY, l = 0.f;
-        bool ok = true;
-        for (int j = 0; j < nblk; ++j) {
-            ok = __all_sync(0xffffffffu, wait(bS + x, j & 1));
-            if (!ok) break;
-            tc_fence_after();
-            const int j0 = blk.start(j), width = blk.width(j);
-            uint32_t s[kTile];
+            __syncwarp();
+    }
+    } else {
+        registers_up<kRegsRows>();
+        if (warp < 4 || second) {
+            const int x = warp >> 2;
+            const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+            const uint32_t tS = tmem + lanes + 128 * x, tO = tmem + lanes + 256 + 128 * x;
+            const int qx = q0 + (two_heads ? 0 : x * kTile);  // this tile's first query
+            const int i = qx + 32 * (warp & 3) + lane;        // this thread's
+            const float c2 = p.scale * mix::kLog2e;
+            float m = -INFINITY, l = 0.f;
+            bool ok = true;
+            for (int j = 0; j < nblk; ++j) {
+                ok = __all_sync(0xffffffffu, wait(bS + x, j & 1));
+                if (!ok) break;
+                tc_fence_after();
+                const int j0 = blk.start(j), width = blk.width(j);
+                uint32_t s[kTile];
 #pragma unroll
-            for (int g = 0; g < kTile; g += 32)
-                if (g < width) tmem_ld32(tS + g, s + g);
-            tmem_ld_wait();
-            if (width < kTile || !all_seen(qx, kTile, j0, width, p.window, p.sinks)) {
+                for (int g = 0; g < kTile; g += 32)
+                    if (g < width) tmem_ld32(tS + g, s + g);
+                tmem_ld_wait();
+                if (width < kTile || !all_seen(qx, kTile, j0, width, p.window, p.sinks)) {
+#pragma unroll
+                    for (int g = 0; g < kTile; g += 32) {
+                        const uint32_t see = g < width ? seen_bits(i, j0 + g, p.window, p.sinks) : 0;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) s[g + e] = (see >> e) & 1 ? s[g + e] : 0xff800000u;
+                    }
+                }
+                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int e = 0; e < kTile; ++e) top[e & 3] = fmaxf(top[e & 3], __uint_as_float(s[e]));
+                const float mb = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c2;
+                if (__any_sync(0xffffffffu, mb > m + kGrow)) {
+                    const float mn = fmaxf(m, mb);
+                    const float f = m == -INFINITY ? 0.f : mix::ex2(m - mn);
+                    m = mn;
+                    l *= f;
+                    if (j > 0) {  // the scores came behind the last product into O
+#pragma unroll
+                        for (int g = 0; g < D; g += 32) {
+                            uint32_t o[32];
+                            tmem_ld32(tO + g, o);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tmem_st32(tO + g, o);
+                        }
+                    }
+                }
+                const float ms = m == -INFINITY ? 0.f : -m;
+                const mix::Two cc = mix::two(c2, c2), mm = mix::two(ms, ms);
+                mix::Two sum[2] = {mix::two(0.f, 0.f), mix::two(0.f, 0.f)};
 #pragma unroll
                 for (int g = 0; g < kTile; g += 32) {
-                    const uint32_t see = g < width ? seen_bits(i, j0 + g, p.window, p.sinks) : 0;
+                    uint32_t pk[16];
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) s[g + e] = (see >> e) & 1 ? s[g + e] : 0xff800000u;
-                }
-            }
-            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int e = 0; e < kTile; ++e) top[e & 3] = fmaxf(top[e & 3], __uint_as_float(s[e]));
-            const float mb = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c2;
-            if (__any_sync(0xffffffffu, mb > m + kGrow)) {
-                const float mn = fmaxf(m, mb);
-                const float f = m == -INFINITY ? 0.f : mix::ex2(m - mn);
-                m = mn;
-                l *= f;
-                if (j > 0) {  // the scores came behind the last product into O
-#pragma unroll
-                    for (int g = 0; g < D; g += 32) {
-                        uint32_t o[32];
-                        tmem_ld32(tO + g, o);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                        tmem_st32(tO + g, o);
+                    for (int e = 0; e < 32; e += 2) {
+                        float a, bb;
+                        const mix::Two y =
+                            mix::ex2_2(mix::fma2(mix::two(__uint_as_float(s[g + e]), __uint_as_float(s[g + e + 1])), cc, mm));
+                        sum[(e >> 1) & 1] = mix::add2(sum[(e >> 1) & 1], y);
+                        mix::split(y, a, bb);
+                        pk[e / 2] = cvt_bf16x2(a, bb);
                     }
+                    if (g < width) tmem_st16(tS + g / 2, pk);
                 }
-            }
-            const float ms = m == -INFINITY ? 0.f : -m;
-            const mix::Two cc = mix::two(c2, c2), mm = mix::two(ms, ms);
-            mix::Two sum[2] = {mix::two(0.f, 0.f), mix::two(0.f, 0.f)};
-            uint32_t pk[kTile / 2];
-#pragma unroll
-            for (int e = 0; e < kTile; e += 2) {
                 float a, bb;
-                const mix::Two y = mix::ex2_2(mix::fma2(mix::two(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), cc, mm));
-                sum[(e >> 1) & 1] = mix::add2(sum[(e >> 1) & 1], y);
-                mix::split(y, a, bb);
-                pk[e / 2] = cvt_bf16x2(a, bb);
+                mix::split(mix::add2(sum[0], sum[1]), a, bb);
+                l += a + bb;
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(bP + x));
             }
-            float a, bb;
-            mix::split(mix::add2(sum[0], sum[1]), a, bb);
-            l += a + bb;
-            tmem_st32(tS, pk);
-            if (width == kTile || width > 64) tmem_st32(tS + 32, pk + 32);
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(bP + x));
-        }
-        if (ok && __all_sync(0xffffffffu, wait(bO + x, 0))) {
-            tc_fence_after();
-            const int h = h0 + (two_heads ? x : 0);
-            const float r = 1.f / l;
-            float lse = (m + log2f(l)) * 0.6931471805599453f;
-            // through this warp's own 32 rows of Q's buffer (its products are done):
-            // 16-byte chunks, permuted so that neither side meets a bank twice
-            uint8_t* mine = sm + L::q + x * L::kTileBytes + (warp & 3) * 32 * (D * 2);
-            float bad = 0.f;
+            if (ok && __all_sync(0xffffffffu, wait(bO + x, 0))) {
+                tc_fence_after();
+                const int h = h0 + (two_heads ? x : 0);
+                const float r = 1.f / l;
+                float lse = (m + log2f(l)) * 0.6931471805599453f;
+                // through this warp's own 32 rows of Q's buffer (its products are done):
+                // 16-byte chunks, permuted so that neither side meets a bank twice
+                uint8_t* mine = sm + L::q + x * L::kTileBytes + (warp & 3) * 32 * (D * 2);
+                float bad = 0.f;
 #pragma unroll
-            for (int g = 0; g < D; g += 32) {
-                uint32_t o[32];
-                tmem_ld32(tO + g, o);
-                tmem_ld_wait();
+                for (int g = 0; g < D; g += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(tO + g, o);
+                    tmem_ld_wait();
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t w[4];
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t w[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float u = __uint_as_float(o[8 * q + 2 * e]) * r, v = __uint_as_float(o[8 * q + 2 * e + 1]) * r;
-                        bad = fmaf(u, 0.f, fmaf(v, 0.f, bad));
-                        w[e] = cvt_bf16x2(u, v);
+                        for (int e = 0; e < 4; ++e) {
+                            const float u = __uint_as_float(o[8 * q + 2 * e]) * r, v = __uint_as_float(o[8 * q + 2 * e + 1]) * r;
+                            bad = fmaf(u, 0.f, fmaf(v, 0.f, bad));
+                            w[e] = cvt_bf16x2(u, v);
+                        }
+                        *reinterpret_cast<uint4*>(mine + lane * (D * 2) + (((g / 8 + q) ^ (lane & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
                     }
-                    *reinterpret_cast<uint4*>(mine + lane * (D * 2) + (((g / 8 + q) ^ (lane & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
-            }
-            __syncwarp();
-            constexpr int kChunks = D / 8;  // of 16 bytes in a row
+                __syncwarp();
+                constexpr int kChunks = D / 8;  // of 16 bytes in a row
 #pragma unroll 4
-            for (int k = 0; k < kChunks; ++k) {
-                const int r2 = (k * 32 + lane) / kChunks, ch = (k * 32 + lane) % kChunks;
-                const int t = qx + 32 * (warp & 3) + r2;
-                const uint4 w = *reinterpret_cast<const uint4*>(mine + r2 * (D * 2) + ((ch ^ (r2 & 7)) * 16));
-                if (t < len)
-                    *reinterpret_cast<uint4*>(p.out + (row0 + t) * (static_cast<long long>(p.H) * D) + h * D + ch * 8) = w;
+                for (int k = 0; k < kChunks; ++k) {
+                    const int r2 = (k * 32 + lane) / kChunks, ch = (k * 32 + lane) % kChunks;
+                    const int t = qx + 32 * (warp & 3) + r2;
+                    const uint4 w = *reinterpret_cast<const uint4*>(mine + r2 * (D * 2) + ((ch ^ (r2 & 7)) * 16));
+                    if (t < len)
+                        *reinterpret_cast<uint4*>(p.out + (row0 + t) * (static_cast<long long>(p.H) * D) + h * D + ch * 8) = w;
+                }
+                __syncwarp();
+                uint32_t again = __ballot_sync(0xffffffffu, bad != 0.f && i < len);
+                while (again) {
+                    const int src = __ffs(again) - 1;
+                    again &= again - 1;
+                    float v;
+                    one_row<D>(p, row0, qx + 32 * (warp & 3) + src, h, v);
+                    if (lane == src) lse = v;
+                }
+                if (p.lse && i < len)  // (row of the batch, head, token)
+                    p.lse[(static_cast<long long>(b) * p.H + h) * p.T + t0 + i] = lse;
             }
-            __syncwarp();
-            uint32_t again = __ballot_sync(0xffffffffu, bad != 0.f && i < len);
-            while (again) {
-                const int src = __ffs(again) - 1;
-                again &= again - 1;
-                float v;
-                one_row<D>(p, row0, qx + 32 * (warp & 3) + src, h, v);
-                if (lane == src) lse = v;
-            }
-            if (p.lse && i < len)  // (row of the batch, head, token)
-                p.lse[(static_cast<long long>(b) * p.H + h) * p.T + t0 + i] = lse;
         }
     }
     tc_fence_before();
@@ -350,6 +364,10 @@ cudaError_t launch(const WindowArgs& a, cudaStream_t stream) {
         return cudaErrorInvalidValue;
     cudaError_t e = cudaFuncSetAttribute(window_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::total);
     if (e != cudaSuccess) return e;
+    cudaFuncAttributes at;
+    e = cudaFuncGetAttributes(&at, window_fwd_kernel<D>);
+    if (e != cudaSuccess) return e;
+    if (at.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;  // the shares would wait for registers that are not there
     const int units = (a.H / a.Hk) % 2 == 0 ? a.H / 2 : a.H;
     window_fwd_kernel<D><<<static_cast<unsigned>(a.slots * units), kThreads, Smem<D>::total, stream>>>(mq, mk, mv, a);
     return cudaGetLastError();
