@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tslot;
-    constexpr uint32_t cS = 0, cDP = 128, cDQ = 256;
+    constexpr uint32_t cS = 0, cDP = 128, cDQ = 384;  // dP alternates between 128 and 256
     const auto wait = [&](int i, int parity) {
         if (*stop) return false;
         if (mbar_wait(bar(i), parity)) return true;
@@ -489,45 +489,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mma_bf16(tmem + d, desc_sw128(ua + o, 0, 1024), desc_sw128(ub + o, 0, 1024), id, s > 0);
                 }
             };
-            bool ok = wait(qIn, 0) && wait(qK, 0);
-            if (ok) {
+            // S and dP of block j: while the others turn one block's into dS, the next
+            // block's are on their way
+            const auto forms = [&](int j) {
+                const int st = j & 1, ph = (j >> 1) & 1;
+                if (j > 0 && !wait(qRead, (j - 1) & 1)) return false;
+                if (!wait(qK + st, ph)) return false;
                 tc_fence_after();
-                outer(cS, L::q, L::k, blk.width(0));
+                outer(cS, L::q, L::k + st * L::kTileBytes, blk.width(j));
                 mma_commit(bar(qS));
-                ok = wait(qV, 0);
-            }
-            if (ok) {
+                if (!wait(qV + st, ph)) return false;
                 tc_fence_after();
-                outer(cDP, L::g, L::v, blk.width(0));
+                outer(cDP + 128 * st, L::g, L::v + st * L::kTileBytes, blk.width(j));
                 mma_commit(bar(qDP));
-                mma_commit(bar(qVFree));
-            }
+                mma_commit(bar(qVFree + st));
+                return true;
+            };
+            bool ok = wait(qIn, 0) && forms(0);
             for (int j = 0; j < nblk && ok; ++j) {
-                const int st = j & 1, nx = (j + 1) & 1, nph = ((j + 1) >> 1) & 1;
-                if (j + 1 < nblk) {
-                    ok = wait(qRead, j & 1) && wait(qK + nx, nph);
-                    if (!ok) break;
-                    tc_fence_after();
-                    outer(cS, L::q, L::k + nx * L::kTileBytes, blk.width(j + 1));
-                    mma_commit(bar(qS));
-                }
-                ok = wait(qDS, j & 1);
+                const int st = j & 1;
+                if (j + 1 < nblk) ok = forms(j + 1);
+                ok = ok && wait(qDS, j & 1);
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t ub = smem_u32(sm + L::k + st * L::kTileBytes);
                 const int steps = blk.width(j) / 16;
                 for (int s = 0; s < steps; ++s)
-                    mma_bf16_ts(tmem + cDQ, tmem + cDP + (s >> 2) * 64 + (s & 3) * 8, desc_sw128(ub + s * 2048, kSlab, 1024), id_o,
-                                (j | s) != 0);
+                    mma_bf16_ts(tmem + cDQ, tmem + cDP + 128 * st + (s >> 2) * 64 + (s & 3) * 8, desc_sw128(ub + s * 2048, kSlab, 1024),
+                                id_o, (j | s) != 0);
                 mma_commit(bar(qKFree + st));
-                if (j + 1 < nblk) {
-                    ok = wait(qV + nx, nph);
-                    if (!ok) break;
-                    tc_fence_after();
-                    outer(cDP, L::g, L::v + nx * L::kTileBytes, blk.width(j + 1));
-                    mma_commit(bar(qDP));
-                    mma_commit(bar(qVFree + nx));
-                }
             }
             mma_commit(bar(qDone));
             mbar_wait(bar(qDone), 0);
@@ -536,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         const int half = warp >> 2;  // which 64 keys of the block
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-        const uint32_t tS = tmem + lanes + cS + 64 * half, tDP = tmem + lanes + cDP + 64 * half;
+        const uint32_t tS = tmem + lanes + cS + 64 * half;
         const int i = q0 + 32 * (warp & 3) + lane;  // this thread's query
         const float c2 = p.scale * mix::kLog2e;
         float lse = 0.f, delta = 0.f;
@@ -551,6 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = __all_sync(0xffffffffu, wait(qS, j & 1));
             if (!ok) break;
             tc_fence_after();
+            const uint32_t tDP = tmem + lanes + cDP + 128 * (j & 1) + 64 * half;
             const int j0 = blk.start(j) + 64 * half, width = blk.width(j) - 64 * half;  // of this half, 0 or less: none
             uint32_t s[64], pk[32];
             float pr[64];

@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_wait(bar(bDrain), 0);
             }
             __syncwarp();
-    }
+        }
     } else {
         registers_up<kRegsRows>();
         if (warp < 4 || second) {
