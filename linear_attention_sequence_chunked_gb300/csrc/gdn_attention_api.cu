@@ -25,7 +25,7 @@ gdn_status check_rope(int B, int T, int H, int Hk, int d, int pairs, int dtype) 
 gdn_status rope_args(gdn::RopeArgs& a, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
                      const float* q_weight, const float* k_weight, const float* inv_freq, const int32_t* positions,
                      const int32_t* cu_seqlens, int B, int T, int H, int Hk, int d, int pairs, int interleaved,
-                     float eps, int dtype, bool backward) {
+                     float eps, int dtype) {
     GDN_TRY(check_rope(B, T, H, Hk, d, pairs, dtype));
     if (pairs > 0 && !inv_freq) return GDN_ERR_INVALID_ARG;
     a.tokens = cu_seqlens ? T : static_cast<long long>(B) * T;
@@ -40,8 +40,8 @@ gdn_status rope_args(gdn::RopeArgs& a, const void* q, int64_t q_stride, const vo
     a.inv_freq = inv_freq; a.positions = positions; a.cu_seqlens = cu_seqlens;
     a.nseq = B; a.T = T; a.H = H; a.Hk = Hk; a.d = d; a.pairs = pairs; a.interleaved = interleaved != 0;
     a.dtype = dtype; a.eps = eps;
-    a.tile = gdn::rope_tile(a.tokens, H + Hk);
-    a.blocks = static_cast<unsigned>(gdn::rope_blocks(a.tokens, H + Hk, backward));
+    a.share = gdn::rope_share(a.tokens, std::max(H, Hk), d);
+    a.blocks = static_cast<unsigned>(gdn::rope_blocks(a.tokens, std::max(H, Hk), d));
     if (a.tokens > 0 && !(a.err = gdn::device_error_word())) return GDN_ERR_CUDA;
     return GDN_OK;
 }
@@ -115,7 +115,7 @@ gdn_status gdn_rope_fwd(const void* q, int64_t q_stride, const void* k, int64_t 
                         int pairs, int interleaved, float eps, int dtype, cudaStream_t stream) {
     gdn::RopeArgs a{};
     GDN_TRY(rope_args(a, q, q_stride, k, k_stride, q_weight, k_weight, inv_freq, positions, cu_seqlens, B, T, H, Hk, d,
-                      pairs, interleaved, eps, dtype, false));
+                      pairs, interleaved, eps, dtype));
     GDN_TRY(check_dense({q_out, k_out}));
     if (a.tokens == 0) return GDN_OK;
     if (!q_out || !k_out) return GDN_ERR_INVALID_ARG;
@@ -126,7 +126,7 @@ gdn_status gdn_rope_fwd(const void* q, int64_t q_stride, const void* k, int64_t 
 size_t gdn_rope_bwd_workspace_size(int B, int T, int H, int Hk, int d, int varlen) {
     if (check_rope(B, T, H, Hk, d, 0, 0) != GDN_OK) return 0;
     const long long tokens = varlen ? T : static_cast<long long>(B) * T;
-    return round_up(sizeof(float) * 2 * gdn::rope_blocks(tokens, H + Hk, true) * d);
+    return round_up(sizeof(float) * 2 * gdn::rope_blocks(tokens, std::max(H, Hk), d) * d);
 }
 
 gdn_status gdn_rope_bwd(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const float* q_weight,
@@ -137,7 +137,7 @@ gdn_status gdn_rope_bwd(const void* q, int64_t q_stride, const void* k, int64_t 
                         cudaStream_t stream) {
     gdn::RopeArgs a{};
     GDN_TRY(rope_args(a, q, q_stride, k, k_stride, q_weight, k_weight, inv_freq, positions, cu_seqlens, B, T, H, Hk, d,
-                      pairs, interleaved, eps, dtype, true));
+                      pairs, interleaved, eps, dtype));
     if ((q_weight != nullptr) != (dq_weight != nullptr) || (k_weight != nullptr) != (dk_weight != nullptr))
         return GDN_ERR_INVALID_ARG;
     GDN_TRY(check_dense({dq_out, dk_out, dq, dk, dq_weight, dk_weight}));

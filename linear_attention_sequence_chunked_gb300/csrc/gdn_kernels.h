@@ -543,12 +543,12 @@ struct RopeArgs {
     int nseq, T, H, Hk, d, pairs;
     int interleaved, dtype;
     float eps;
-    int tile;                     // tokens per block
+    int share;                    // teams that share a token's heads
     unsigned blocks;
     int* err;
 };
-int rope_tile(long long tokens, int heads);
-long long rope_blocks(long long tokens, int heads, bool backward);
+int rope_share(long long tokens, int heads, int d);
+long long rope_blocks(long long tokens, int heads, int d);
 cudaError_t launch_rope_fwd(const RopeArgs& a, cudaStream_t stream);
 cudaError_t launch_rope_bwd(const RopeArgs& a, cudaStream_t stream);
 

@@ -253,7 +253,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int e = 0; e < kTile; ++e) top[e & 3] = fmaxf(top[e & 3], __uint_as_float(s[e]));
+                for (int e = 0; e < kTile; e += 8)
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) top[g] = max3(top[g], __uint_as_float(s[e + 2 * g]), __uint_as_float(s[e + 2 * g + 1]));
                 const float mb = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c2;
                 if (__any_sync(0xffffffffu, mb > m + kGrow)) {
                     const float mn = fmaxf(m, mb);
