@@ -219,7 +219,7 @@ gdn_status gdn_window_step(const gdn_bf16* q, int64_t q_stride, const gdn_bf16* 
     a.k_cache = k_cache; a.v_cache = v_cache; a.lengths = lengths; a.slots = slots; a.out = out;
     a.B = B; a.S = S; a.H = H; a.Hk = Hk; a.d = d; a.rows = sinks + window; a.window = window; a.sinks = sinks;
     a.scale = scale;
-    a.cluster = gdn::window_step_cluster(B, Hk, (H / Hk + 15) / 16, a.rows);
+    gdn::window_step_shape(a);
     return gdn::count_launch(gdn::launch_window_step(a, stream)) ? GDN_OK : GDN_ERR_CUDA;
 }
 

@@ -593,10 +593,10 @@ struct WindowStepArgs {
     int B, S, H, Hk, d;
     int rows, window, sinks;
     float scale;
-    int cluster;
+    int warps, cluster;
     int* err;
 };
-int window_step_cluster(int B, int Hk, int sets, int rows);
+void window_step_shape(WindowStepArgs& a);  // sets warps and cluster
 cudaError_t launch_window_step(const WindowStepArgs& a, cudaStream_t stream);
 struct WindowFillArgs {
     const uint16_t* k;            // (tokens, Hk, d), tokens k_stride apart; v likewise

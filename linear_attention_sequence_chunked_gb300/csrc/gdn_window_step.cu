@@ -28,8 +28,11 @@ namespace {
 
 using namespace mix;
 
-constexpr int kWarps = 4;
 constexpr int kKeys = 16;  // of a warp's step
+// Warps of a block: six, two blocks to an SM (64 rows of 1028 keys, 4 key heads: 25
+// us; four warps and three blocks 29, twelve and one 31), or twelve where the rows
+// and heads of a call are too few for that.
+constexpr int kFew = 6, kMany = 12;
 
 __device__ __forceinline__ void mma_16x8x16(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -47,33 +50,44 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// Stores to the same shared variable of block `rank` of the cluster.
+__device__ __forceinline__ uint32_t remote(const void* p, uint32_t rank) {
+    uint32_t to;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(rank));
+    return to;
 }
-__device__ __forceinline__ float load_remote(const float* p, uint32_t rank) {
-    const uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p));
-    uint32_t from;
-    float v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(from) : "r"(a), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(from) : "memory");
-    return v;
+__device__ __forceinline__ void store_remote(float2* p, uint32_t rank, float2 v) {
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(remote(p, rank)), "f"(v.x), "f"(v.y) : "memory");
+}
+__device__ __forceinline__ void store_remote(float4* p, uint32_t rank, float4 v) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(remote(p, rank)), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
 }
 
-template <int D>
+constexpr int kMaxCluster = 16;
+
+template <int D, int kWarps>
 struct Joined {
+    uint4 q[D / 32][2][32];  // Q as the first product's operand, a lane's four registers together
     float o[kWarps][16][D + 4];
-    float m[kWarps][16], l[kWarps][16];
-    float jo[16][D], jm[16], jl[16];  // the block's
+    float m[kWarps][16], l[kWarps][16], f[kWarps][16];
+    float2 ml[16];                         // the block's maximum and sum
+    // what the blocks of the cluster send: everyone's maxima and sums, and their
+    // sums of the part of the output that is this block's
+    float2 sent_ml[kMaxCluster][16];
+    float4 sent[16 * D / 4 + kMaxCluster];
 };
 
-template <int D>
-__global__ void __launch_bounds__(32 * kWarps) window_step_kernel(const WindowStepArgs p) {
+template <int D, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps, 12 / kWarps) window_step_kernel(const WindowStepArgs p) {
     constexpr int CH = D / 32;  // 16-byte chunks of a row per lane
     extern __shared__ __align__(16) unsigned char smem[];
-    Joined<D>& sm = *reinterpret_cast<Joined<D>*>(smem);
+    Joined<D, kWarps>& sm = *reinterpret_cast<Joined<D, kWarps>*>(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int C = p.cluster;
     const uint32_t rank = C > 1 ? cluster_rank() : 0;
+    if (C > 1) cluster_arrive();
     const int G = p.H / p.Hk, sets = (G + 15) / 16;
     long long unit = blockIdx.x / C;
     const int set = static_cast<int>(unit % sets);
@@ -103,13 +117,14 @@ __global__ void __launch_bounds__(32 * kWarps) window_step_kernel(const WindowSt
     }
 
     // Q: rows g and g + 8 of the product, this lane's chunks t, t + 4, ...
-    uint32_t q[2 * CH][4];
     const uint16_t* qp = p.q + b * p.q_stride + static_cast<long long>(h0) * D;
+    if (warp == 0) {
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-        const uint4 lo = load_16(qp + g * D + (c * 4 + t) * 8, g < heads), hi = load_16(qp + (g + 8) * D + (c * 4 + t) * 8, g + 8 < heads);
-        q[2 * c][0] = lo.x; q[2 * c][1] = hi.x; q[2 * c][2] = lo.y; q[2 * c][3] = hi.y;
-        q[2 * c + 1][0] = lo.z; q[2 * c + 1][1] = hi.z; q[2 * c + 1][2] = lo.w; q[2 * c + 1][3] = hi.w;
+        for (int c = 0; c < CH; ++c) {
+            const uint4 lo = load_16(qp + g * D + (c * 4 + t) * 8, g < heads), hi = load_16(qp + (g + 8) * D + (c * 4 + t) * 8, g + 8 < heads);
+            sm.q[c][0][lane] = make_uint4(lo.x, hi.x, lo.y, hi.y);
+            sm.q[c][1][lane] = make_uint4(lo.z, hi.z, lo.w, hi.w);
+        }
     }
     float o[D / 8][4];
 #pragma unroll
@@ -121,31 +136,45 @@ __global__ void __launch_bounds__(32 * kWarps) window_step_kernel(const WindowSt
 
     const int strips = (rows + kKeys - 1) / kKeys, per = (strips + C - 1) / C;
     const int s1 = min(strips, static_cast<int>(rank + 1) * per);
-    for (int s = static_cast<int>(rank) * per + warp; s < s1; s += kWarps) {
-        const int r0 = s * kKeys;
-        uint4 kr[2][CH], vr[4][CH / 2];
+    // the next strip's keys are on their way from the first product on, its
+    // values from the second on
+    uint4 kr[2][CH], vr[4][CH / 2];
+    const auto load_keys = [&](int s) {
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {  // keys r0 + 8 n + g
-            const int r = r0 + 8 * n + g;
+        for (int n = 0; n < 2; ++n) {  // keys 8 n + g of the strip
+            const int r = s * kKeys + 8 * n + g;
             const uint16_t* k = r == at ? kn : kc + r * stride;
 #pragma unroll
-            for (int c = 0; c < CH; ++c) kr[n][c] = load_16(k + (c * 4 + t) * 8, r < rows);
+            for (int c = 0; c < CH; ++c) kr[n][c] = load_16(k + (c * 4 + t) * 8, s < s1 && r < rows);
         }
+    };
+    const auto load_values = [&](int s) {
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {  // keys r0 + 2 t, + 1, + 8, + 9
-            const int r = r0 + 2 * t + (n & 1) + (n >> 1) * 8;
+        for (int n = 0; n < 4; ++n) {  // keys 2 t, + 1, + 8, + 9
+            const int r = s * kKeys + 2 * t + (n & 1) + (n >> 1) * 8;
             const uint16_t* v = r == at ? vn : vc + r * stride;
 #pragma unroll
-            for (int c = 0; c < CH / 2; ++c) vr[n][c] = load_16(v + c * 64 + g * 8, r < rows);
+            for (int c = 0; c < CH / 2; ++c) vr[n][c] = load_16(v + c * 64 + g * 8, s < s1 && r < rows);
         }
+    };
+    int s = static_cast<int>(rank) * per + warp;
+    load_keys(s);
+    load_values(s);
+    __syncthreads();  // Q is there
+    for (; s < s1; s += kWarps) {
+        const int r0 = s * kKeys;
         float sc[2][4] = {};
 #pragma unroll
-        for (int c = 0; c < CH; ++c)
+        for (int c = 0; c < CH; ++c) {
+            const uint4 q0 = sm.q[c][0][lane], q1 = sm.q[c][1][lane];
+            const uint32_t a0[4] = {q0.x, q0.y, q0.z, q0.w}, a1[4] = {q1.x, q1.y, q1.z, q1.w};
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
-                mma_16x8x16(sc[n], q[2 * c], kr[n][c].x, kr[n][c].y);
-                mma_16x8x16(sc[n], q[2 * c + 1], kr[n][c].z, kr[n][c].w);
+                mma_16x8x16(sc[n], a0, kr[n][c].x, kr[n][c].y);
+                mma_16x8x16(sc[n], a1, kr[n][c].z, kr[n][c].w);
             }
+        }
+        load_keys(s + kWarps);
         // sc[n][e]: query row g + 8 (e / 2), key r0 + 8 n + 2 t + e % 2
         uint32_t pa[4];
 #pragma unroll
@@ -189,6 +218,7 @@ __global__ void __launch_bounds__(32 * kWarps) window_step_kernel(const WindowSt
                 mma_16x8x16(o[8 * c + j], pa, __byte_perm(w[0][j / 2], w[1][j / 2], sel), __byte_perm(w[2][j / 2], w[3][j / 2], sel));
             }
         }
+        load_values(s + kWarps);
     }
     // a row's sum lies across its four lanes
 #pragma unroll
@@ -205,47 +235,69 @@ __global__ void __launch_bounds__(32 * kWarps) window_step_kernel(const WindowSt
 #pragma unroll
         for (int e = 0; e < 4; ++e) sm.o[warp][g + 8 * (e >> 1)][(i / 8) * 64 + (2 * t + (e & 1)) * 8 + i % 8] = o[i][e];
     __syncthreads();
-    // the block's warps
-    for (int i = threadIdx.x; i < heads * D; i += 32 * kWarps) {
-        const int r = i / D, d = i % D;
+    // the block's warps: each one's weight against the largest maximum
+    if (threadIdx.x < 16 * kWarps) {
+        const int w = threadIdx.x / 16, r = threadIdx.x % 16;
         float mx = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sm.m[w][r]);
+        for (int i = 0; i < kWarps; ++i) mx = fmaxf(mx, sm.m[i][r]);
         const float ms = mx == -INFINITY ? 0.f : mx;
-        float sum = 0.f, acc = 0.f;
+        sm.f[w][r] = ex2(sm.m[w][r] - ms);
+        if (w == 0) {
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) sum = fmaf(sm.l[i][r], ex2(sm.m[i][r] - ms), sum);
+            sm.ml[r] = make_float2(mx, sum);
+        }
+    }
+    __syncthreads();
+    const auto write = [&](int r, int d, const float4& o, float sum) {
+        const float inv = on ? 1.f / sum : 0.f;
+        *reinterpret_cast<uint2*>(p.out + (b * p.H + h0 + r) * D + d) =
+            on ? make_uint2(pair_of(o.x * inv, o.y * inv), pair_of(o.z * inv, o.w * inv)) : make_uint2(0, 0);
+    };
+    const int quads = heads * D / 4, share = (quads + C - 1) / C;  // of the output's 4 channels each
+    if (C > 1) cluster_wait();  // every block of the cluster is there
+    for (int i = threadIdx.x; i < quads; i += 32 * kWarps) {
+        const int r = i / (D / 4), d = i % (D / 4) * 4;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            const float f = ex2(sm.m[w][r] - ms);
-            sum = fmaf(sm.l[w][r], f, sum);
-            acc = fmaf(sm.o[w][r][d], f, acc);
+            const float f = sm.f[w][r];
+            const float4 v = *reinterpret_cast<const float4*>(&sm.o[w][r][d]);
+            acc.x = fmaf(v.x, f, acc.x);
+            acc.y = fmaf(v.y, f, acc.y);
+            acc.z = fmaf(v.z, f, acc.z);
+            acc.w = fmaf(v.w, f, acc.w);
         }
-        if (C > 1) {
-            sm.jo[r][d] = acc;
-            if (d == 0) {
-                sm.jm[r] = mx;
-                sm.jl[r] = sum;
-            }
-        } else {
-            p.out[(b * p.H + h0 + r) * D + d] = f32_to_bf16(on ? acc / sum : 0.f);
-        }
+        if (C == 1)
+            write(r, d, acc, sm.ml[r].y);
+        else
+            store_remote(&sm.sent[rank * share + i % share], i / share, acc);
     }
     if (C == 1) return;
-    cluster_sync();
-    const int share = (heads * D + C - 1) / C, last = min(heads * D, static_cast<int>(rank + 1) * share);
-    for (int i = static_cast<int>(rank) * share + threadIdx.x; i < last; i += 32 * kWarps) {
-        const int r = i / D, d = i % D;
+    for (int i = threadIdx.x; i < 16 * C; i += 32 * kWarps) store_remote(&sm.sent_ml[rank][i % 16], i / 16, sm.ml[i % 16]);
+    cluster_arrive();
+    cluster_wait();
+    for (int i = threadIdx.x; i < share && static_cast<int>(rank) * share + i < quads; i += 32 * kWarps) {
+        const int at4 = static_cast<int>(rank) * share + i, r = at4 / (D / 4), d = at4 % (D / 4) * 4;
         float mx = -INFINITY;
-        for (int c = 0; c < C; ++c) mx = fmaxf(mx, load_remote(&sm.jm[r], c));
+        for (int c = 0; c < C; ++c) mx = fmaxf(mx, sm.sent_ml[c][r].x);
         const float ms = mx == -INFINITY ? 0.f : mx;
-        float sum = 0.f, acc = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float sum = 0.f;
         for (int c = 0; c < C; ++c) {
-            const float f = ex2(load_remote(&sm.jm[r], c) - ms);
-            sum = fmaf(load_remote(&sm.jl[r], c), f, sum);
-            acc = fmaf(load_remote(&sm.jo[r][d], c), f, acc);
+            const float2 ml = sm.sent_ml[c][r];
+            const float f = ex2(ml.x - ms);
+            const float4 v = sm.sent[c * share + i];
+            sum = fmaf(ml.y, f, sum);
+            acc.x = fmaf(v.x, f, acc.x);
+            acc.y = fmaf(v.y, f, acc.y);
+            acc.z = fmaf(v.z, f, acc.z);
+            acc.w = fmaf(v.w, f, acc.w);
         }
-        p.out[(b * p.H + h0 + r) * D + d] = f32_to_bf16(on ? acc / sum : 0.f);
+        write(r, d, acc, sum);
     }
-    cluster_sync();  // the others may still read here
 }
 
 // The rows of a cache that a prompt leaves behind, 16 bytes per thread.
@@ -273,19 +325,20 @@ __global__ void __launch_bounds__(256) window_fill_kernel(const WindowFillArgs p
     }
 }
 
-template <int D>
+template <int D, int kWarps>
 cudaError_t launch(const WindowStepArgs& a, cudaStream_t stream) {
     const int sets = (a.H / a.Hk + 15) / 16;
-    cudaError_t e = cudaFuncSetAttribute(window_step_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Joined<D>));
+    constexpr size_t smem = sizeof(Joined<D, kWarps>);
+    cudaError_t e = cudaFuncSetAttribute(window_step_kernel<D, kWarps>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     if (a.cluster > 8) {
-        e = cudaFuncSetAttribute(window_step_kernel<D>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        e = cudaFuncSetAttribute(window_step_kernel<D, kWarps>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(static_cast<long long>(a.B) * a.Hk * sets * a.cluster));
     cfg.blockDim = dim3(32 * kWarps);
-    cfg.dynamicSmemBytes = sizeof(Joined<D>);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -294,21 +347,26 @@ cudaError_t launch(const WindowStepArgs& a, cudaStream_t stream) {
     attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = a.cluster > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, window_step_kernel<D>, a);
+    return cudaLaunchKernelEx(&cfg, window_step_kernel<D, kWarps>, a);
+}
+template <int D>
+cudaError_t launch_warps(const WindowStepArgs& a, cudaStream_t stream) {
+    return a.warps == kMany ? launch<D, kMany>(a, stream) : launch<D, kFew>(a, stream);
 }
 
 }  // namespace
 
-// Blocks per row, group and set of heads: enough of them for the GPU, none
-// with less than a step per warp.
-int window_step_cluster(int B, int Hk, int sets, int rows) {
-    int c = 1;
-    while (c < 16 && static_cast<long long>(B) * Hk * sets * c < 3 * 152 && rows > c * kWarps * kKeys) c *= 2;
-    return c;
+// Blocks per row, group and set of heads, and their warps: enough for the GPU,
+// none with less than a step per warp.
+void window_step_shape(WindowStepArgs& a) {
+    const long long units = static_cast<long long>(a.B) * a.Hk * ((a.H / a.Hk + 15) / 16);
+    a.warps = units * 16 < 2 * 152 && a.rows > 16 * kFew * kKeys ? kMany : kFew;
+    a.cluster = 1;
+    while (a.cluster < kMaxCluster && units * a.cluster * a.warps < 12 * 152 / 2 && a.rows > a.cluster * a.warps * kKeys) a.cluster *= 2;
 }
 
 cudaError_t launch_window_step(const WindowStepArgs& a, cudaStream_t stream) {
-    return a.d == 64 ? launch<64>(a, stream) : launch<128>(a, stream);
+    return a.d == 64 ? launch_warps<64>(a, stream) : launch_warps<128>(a, stream);
 }
 
 cudaError_t launch_window_fill(const WindowFillArgs& a, cudaStream_t stream) {
