@@ -17,8 +17,9 @@ import torch
 
 from ._first_order import first_order
 from .gdn import _check, _on_stream, _workspace, load
-from .mixer import _aligned, _current, _dense, _dtype, _is, _on_gpu, _out, _rows, _sequences
+from .mixer import _aligned, _current, _dense, _dtype, _is, _new, _on_gpu, _out, _rows, _sequences
 
+_BF16 = torch.bfloat16
 HEAD_SIZES = (32, 64, 128, 256)
 WINDOW_HEAD_SIZES = (64, 128)
 MAX_SINKS = 128
@@ -29,21 +30,22 @@ MAX_SINKS = 128
 # ----------------------------------------------------------------------------
 
 def _rope_args(q, k, q_weight, k_weight, inv_freq, positions, cu_seqlens, interleaved, eps):
-    if q.dim() != 4 or k.dim() != 4:
-        raise ValueError(f"q and k must be (B, T, heads, d), got shapes {tuple(q.shape)} and {tuple(k.shape)}")
+    qs, ks = q.shape, k.shape
+    if len(qs) != 4 or len(ks) != 4:
+        raise ValueError(f"q and k must be (B, T, heads, d), got shapes {tuple(qs)} and {tuple(ks)}")
     dtype, dev = _dtype(q, "q"), q.get_device()
-    B, T, H, d = q.shape
-    Hk = k.shape[2]
+    B, T, H, d = qs
+    Hk = ks[2]
     _is("k", k, (B, T, Hk, d), q.dtype, dev)
     if d not in HEAD_SIZES:
         raise ValueError(f"the head size must be one of {HEAD_SIZES}, got {d}")
     pairs = 0
     if inv_freq is not None:
-        if inv_freq.dim() != 1 or inv_freq.numel() % 4 or 2 * inv_freq.numel() > d:
+        if inv_freq.dim() != 1 or inv_freq.shape[0] % 4 or 2 * inv_freq.shape[0] > d:
             raise ValueError(f"inv_freq must hold a multiple of 4 frequencies, at most {d // 2}, "
                              f"got shape {tuple(inv_freq.shape)}")
-        pairs = inv_freq.numel()
-    n, cu = _sequences(q, cu_seqlens, dev, "q")
+        pairs = inv_freq.shape[0]
+    n, cu = (B, None) if cu_seqlens is None else _sequences(q, cu_seqlens, dev, "q")
     args = (*_rows(q, H * d, 2), *_rows(k, Hk * d, 2), _dense("q_weight", q_weight, (d,), torch.float32, dev),
             _dense("k_weight", k_weight, (d,), torch.float32, dev),
             _dense("inv_freq", inv_freq, (pairs,), torch.float32, dev),
@@ -64,7 +66,7 @@ def qk_norm_rope_fwd(q, k, q_weight=None, k_weight=None, inv_freq=None, position
         return _on_stream(qk_norm_rope_fwd, locals())
     q_weight, k_weight, inv_freq = _aligned(q_weight, k_weight, inv_freq)
     dev, args, dims = _rope_args(q, k, q_weight, k_weight, inv_freq, positions, cu_seqlens, interleaved, eps)
-    qo, ko = q.new_empty(q.shape), k.new_empty(k.shape)
+    qo, ko = _new(q), _new(k)
     _check(load().gdn_rope_fwd(*args, qo.data_ptr(), ko.data_ptr(), *dims, _current(dev)), "gdn_rope_fwd")
     return qo, ko
 
@@ -80,7 +82,7 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight=None, k_weight=None, inv_fre
     dev, args, dims = _rope_args(q, k, q_weight, k_weight, inv_freq, positions, cu_seqlens, interleaved, eps)
     gq = _dense("dq_out", dq_out, q.shape, q.dtype, dev)
     gk = _dense("dk_out", dk_out, k.shape, k.dtype, dev)
-    res = {"dq": q.new_empty(q.shape), "dk": k.new_empty(k.shape)}
+    res = {"dq": _new(q), "dk": _new(k)}
     if q_weight is not None:
         res["dq_weight"] = torch.empty_like(q_weight)
     if k_weight is not None:
@@ -100,29 +102,32 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight=None, k_weight=None, inv_fre
 # attention with a sliding window and first tokens that stay visible
 # ----------------------------------------------------------------------------
 
-def _pieces(x, width):
-    """(tensor, address, row stride) of rows of heads that the kernels copy in
-    16-byte pieces; as a copy where they lie elsewhere."""
-    at, stride = _rows(x, width, 2)
+def _pieces(x, width, held):
+    """(address, row stride) of rows of heads that the kernels copy in 16-byte
+    pieces; of a copy, which the caller holds until its launch, where they lie
+    elsewhere."""
+    at, stride = (x.data_ptr(), width) if x.is_contiguous() else _rows(x, width, 2)
     if at & 15 or stride & 7:
-        x = x.contiguous() if not x.is_contiguous() else x.clone()
-        at, stride = x.data_ptr(), width
-    return x, at, stride
+        held.append(x.clone(memory_format=torch.contiguous_format))
+        at, stride = held[-1].data_ptr(), width
+    return at, stride
 
 
 def _window_args(q, k, v, window, sinks, scale, dims):
     """Checks shared by the attention and its step (q of 4 or 3 dimensions).
-    The tensors of the answer are held until the launch."""
-    if q.dim() != dims or k.dim() != dims:
+    The copies of the answer are held until the launch."""
+    shape, kv, dev = q.shape, k.shape, q.get_device()
+    if len(shape) != dims or len(kv) != dims:
         raise ValueError(f"q and k must be {'(B, T, heads, d)' if dims == 4 else '(B, heads, d)'}, "
-                         f"got shapes {tuple(q.shape)} and {tuple(k.shape)}")
-    if q.dtype is not torch.bfloat16:
-        raise ValueError(f"q must be {torch.bfloat16}, got {q.dtype}")
-    dev, shape = q.get_device(), q.shape
-    H, d, Hk = shape[-2], shape[-1], k.shape[-2]
-    kv = shape[:-2] + (Hk, d)
-    _is("k", k, kv, q.dtype, dev)
-    _is("v", v, kv, q.dtype, dev)
+                         f"got shapes {tuple(shape)} and {tuple(kv)}")
+    if q.dtype is not _BF16:
+        raise ValueError(f"q must be {_BF16}, got {q.dtype}")
+    H, d = shape[-2:]
+    Hk = kv[-2]
+    if kv[-1] != d or kv[0] != shape[0] or kv[1] != (shape[1] if dims == 4 else Hk) or k.dtype is not _BF16 or k.get_device() != dev:
+        _is("k", k, shape[:-2] + (Hk, d), _BF16, dev)
+    if v.shape != kv or v.dtype is not _BF16 or v.get_device() != dev:
+        _is("v", v, kv, _BF16, dev)
     if d not in WINDOW_HEAD_SIZES:
         raise ValueError(f"the head size must be one of {WINDOW_HEAD_SIZES}, got {d}")
     if Hk < 1 or H % Hk or H < 1:
@@ -132,8 +137,8 @@ def _window_args(q, k, v, window, sinks, scale, dims):
     if not scale > 0:
         raise ValueError(f"scale must be positive, got {scale}")
     _on_gpu(dev, q)
-    held = [_pieces(q, H * d), _pieces(k, Hk * d), _pieces(v, Hk * d)]
-    return dev, held, [a for _, *at in held for a in at], H, Hk, d, scale
+    held = []
+    return dev, held, (*_pieces(q, H * d, held), *_pieces(k, Hk * d, held), *_pieces(v, Hk * d, held)), H, Hk, d, scale
 
 
 def _window_sizes(window, sinks):
@@ -154,7 +159,7 @@ def window_attention_fwd(q, k, v, window, sinks=0, scale=None, cu_seqlens=None, 
     dev, held, args, H, Hk, d, scale = _window_args(q, k, v, window, sinks, scale, 4)
     n, cu = _sequences(q, cu_seqlens, dev, "q")
     B, T = q.shape[:2]
-    out = q.new_empty(q.shape)
+    out = _new(q)
     lse = torch.empty((B, H, T), dtype=torch.float32, device=q.device) if save_for_backward else None
     _check(load().gdn_window_fwd(*args, cu, out.data_ptr(), None if lse is None else lse.data_ptr(), n, T, H, Hk, d,
                                  min(window, max(T, 1)), sinks, scale, _current(dev)), "gdn_window_fwd")
@@ -173,7 +178,7 @@ def window_attention_bwd(q, k, v, out, lse, d_out, window, sinks=0, scale=None, 
     o = _dense("out", out, q.shape, q.dtype, dev)
     s = _dense("lse", lse, (B, H, T), torch.float32, dev)
     g = _dense("d_out", d_out, q.shape, q.dtype, dev)
-    res = {"dq": q.new_empty(q.shape), "dk": k.new_empty(k.shape), "dv": v.new_empty(v.shape)}
+    res = {"dq": _new(q), "dk": _new(k), "dv": _new(v)}
     window = min(window, max(T, 1))
     lib = load()
     nbytes = lib.gdn_window_bwd_workspace_size(n, T, H, Hk, d, window, sinks, int(cu_seqlens is not None))
@@ -184,13 +189,18 @@ def window_attention_bwd(q, k, v, out, lse, d_out, window, sinks=0, scale=None, 
     return res
 
 
-def _cache(name, t, like, Hk, d, sinks, dev):
-    if t.dim() != 4 or t.shape[1] <= sinks or (like is not None and t.shape != like.shape):
-        raise ValueError(f"the caches must be (S, sinks + window, {Hk}, {d}) alike, got {name} of shape {tuple(t.shape)}")
-    at = _dense(name, t, (t.shape[0], t.shape[1], Hk, d), torch.bfloat16, dev)
-    if at & 15:
-        raise ValueError(f"{name} must start at a 16-byte boundary: it is updated in place")
-    return at
+def _caches(k_cache, v_cache, Hk, d, sinks, dev):
+    """Addresses of the two caches, and how many there are of how many rows."""
+    shape = k_cache.shape
+    if len(shape) != 4 or shape[1] <= sinks or v_cache.shape != shape:
+        raise ValueError(f"the caches must be (S, sinks + window, {Hk}, {d}) alike, got shapes {tuple(shape)} and "
+                         f"{tuple(v_cache.shape)}")
+    S, rows = shape[:2]
+    kc = _dense("k_cache", k_cache, (S, rows, Hk, d), _BF16, dev)
+    vc = _dense("v_cache", v_cache, (S, rows, Hk, d), _BF16, dev)
+    if (kc | vc) & 15:
+        raise ValueError("the caches must start at 16-byte boundaries: they are updated in place")
+    return kc, vc, S, rows
 
 
 def window_attention_step(q, k, v, k_cache, v_cache, lengths, sinks=0, scale=None, slots=None, stream=None):
@@ -204,14 +214,12 @@ def window_attention_step(q, k, v, k_cache, v_cache, lengths, sinks=0, scale=Non
         return _on_stream(window_attention_step, locals())
     dev, held, args, H, Hk, d, scale = _window_args(q, k, v, 1, sinks, scale, 3)
     B = q.shape[0]
-    kc = _cache("k_cache", k_cache, None, Hk, d, sinks, dev)
-    vc = _cache("v_cache", v_cache, k_cache, Hk, d, sinks, dev)
-    S, rows = k_cache.shape[:2]
+    kc, vc, S, rows = _caches(k_cache, v_cache, Hk, d, sinks, dev)
     if slots is None and S < B:
         raise ValueError(f"the caches hold {S} rows for a batch of {B}")
     ln = _dense("lengths", lengths, (B,), torch.int32, dev)
     sl = _dense("slots", slots, (B,), torch.int32, dev)
-    out = q.new_empty(q.shape)
+    out = _new(q)
     _check(load().gdn_window_step(*args, kc, vc, ln, sl, out.data_ptr(), B, S, H, Hk, d, rows - sinks, sinks, scale,
                                   _current(dev)), "gdn_window_step")
     return out
@@ -227,9 +235,7 @@ def window_cache_fill(k, v, k_cache, v_cache, sinks=0, cu_seqlens=None, slots=No
         raise ValueError(f"k must be (B, T, heads, d), got shape {tuple(k.shape)}")
     dev, held, args, _, Hk, d, _ = _window_args(k, k, v, 1, sinks, None, 4)
     n, cu = _sequences(k, cu_seqlens, dev, "k")
-    kc = _cache("k_cache", k_cache, None, Hk, d, sinks, dev)
-    vc = _cache("v_cache", v_cache, k_cache, Hk, d, sinks, dev)
-    S, rows = k_cache.shape[:2]
+    kc, vc, S, rows = _caches(k_cache, v_cache, Hk, d, sinks, dev)
     if slots is None and S < n:
         raise ValueError(f"the caches hold {S} rows for {n} sequences")
     sl = _dense("slots", slots, (n,), torch.int32, dev)

@@ -22,6 +22,7 @@
 #include <type_traits>
 
 #include "gdn_kernels.h"
+#include "gdn_launch.h"
 #include "gdn_mix_common.cuh"
 
 namespace gdn {
@@ -644,9 +645,10 @@ bool fits(int bytes, int D, std::initializer_list<const void*> ptrs, std::initia
     return true;
 }
 
-template <typename K>
-cudaError_t launch_clusters(K kernel, size_t smem, const GatedArgs& a, cudaStream_t stream) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+template <auto kernel>
+cudaError_t launch_clusters(size_t smem, const GatedArgs& a, cudaStream_t stream) {
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_once(kernel, smem, false, done);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>((a.D + kChannels - 1) / kChannels * a.cluster), a.rows);
@@ -667,10 +669,10 @@ template <typename T, int PB>
 cudaError_t launch_pieces(const GatedArgs& a, bool backward, cudaStream_t stream) {
     constexpr size_t bwd = sizeof(Tiles<T, 4, 2 * kStripBwd>) * kWarps, fwd = sizeof(Tiles<T, 3, 2 * kStripFwd>) * kWarps;
     if (a.cu_seqlens)
-        return backward ? launch_clusters(gated_bwd_kernel<T, PB, true>, bwd, a, stream)
-                        : launch_clusters(gated_fwd_kernel<T, PB, true>, fwd, a, stream);
-    return backward ? launch_clusters(gated_bwd_kernel<T, PB, false>, bwd, a, stream)
-                    : launch_clusters(gated_fwd_kernel<T, PB, false>, fwd, a, stream);
+        return backward ? launch_clusters<gated_bwd_kernel<T, PB, true>>(bwd, a, stream)
+                        : launch_clusters<gated_fwd_kernel<T, PB, true>>(fwd, a, stream);
+    return backward ? launch_clusters<gated_bwd_kernel<T, PB, false>>(bwd, a, stream)
+                    : launch_clusters<gated_fwd_kernel<T, PB, false>>(fwd, a, stream);
 }
 template <typename T>
 cudaError_t launch(const GatedArgs& a, bool backward, cudaStream_t stream) {

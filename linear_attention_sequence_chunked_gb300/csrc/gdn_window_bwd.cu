@@ -16,6 +16,7 @@
 // queries, one block each, whose fp32 sums a last kernel adds in order.
 #include <cmath>
 
+#include "gdn_launch.h"
 #include "gdn_window_common.cuh"
 
 namespace gdn {
@@ -606,9 +607,10 @@ cudaError_t launch(const WindowArgs& a, cudaStream_t stream) {
         !make_heads_map(&mv, a.v, a.tokens, a.v_stride, a.Hk, D, kTile) ||
         !make_heads_map(&mg, a.d_out, a.tokens, static_cast<long long>(a.H) * D, a.H, D, kTile))
         return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(window_dkv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, KvSmem<D>::total);
+    static std::atomic<uint64_t> done_kv{0}, done_q{0};
+    cudaError_t e = allow_once(window_dkv_kernel<D>, KvSmem<D>::total, false, done_kv);
     if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(window_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, QSmem<D>::total);
+    e = allow_once(window_dq_kernel<D>, QSmem<D>::total, false, done_q);
     if (e != cudaSuccess) return e;
     const long long rows = a.tokens * a.H * (D / 8);
     window_delta_kernel<D><<<static_cast<unsigned>((rows + 255) / 256), 256, 0, stream>>>(a);

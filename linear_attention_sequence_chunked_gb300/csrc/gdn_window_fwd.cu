@@ -19,6 +19,7 @@
 // non-finite are computed again from the keys they see.
 #include <cmath>
 
+#include "gdn_launch.h"
 #include "gdn_window_common.cuh"
 
 namespace gdn {
@@ -364,12 +365,15 @@ cudaError_t launch(const WindowArgs& a, cudaStream_t stream) {
         !make_heads_map(&mk, a.k, tokens, a.k_stride, a.Hk, D, kTile) ||
         !make_heads_map(&mv, a.v, tokens, a.v_stride, a.Hk, D, kTile))
         return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(window_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::total);
+    static std::atomic<uint64_t> done{0};
+    if (!done.load(std::memory_order_acquire)) {
+        cudaFuncAttributes at;
+        const cudaError_t e = cudaFuncGetAttributes(&at, window_fwd_kernel<D>);
+        if (e != cudaSuccess) return e;
+        if (at.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;  // the shares would wait for registers that are not there
+    }
+    const cudaError_t e = allow_once(window_fwd_kernel<D>, Smem<D>::total, false, done);
     if (e != cudaSuccess) return e;
-    cudaFuncAttributes at;
-    e = cudaFuncGetAttributes(&at, window_fwd_kernel<D>);
-    if (e != cudaSuccess) return e;
-    if (at.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;  // the shares would wait for registers that are not there
     const int units = (a.H / a.Hk) % 2 == 0 ? a.H / 2 : a.H;
     window_fwd_kernel<D><<<static_cast<unsigned>(a.slots * units), kThreads, Smem<D>::total, stream>>>(mq, mk, mv, a);
     return cudaGetLastError();

@@ -20,6 +20,7 @@
 #include <cmath>
 
 #include "gdn_kernels.h"
+#include "gdn_launch.h"
 #include "gdn_mix_common.cuh"
 
 namespace gdn {
@@ -329,12 +330,9 @@ template <int D, int kWarps>
 cudaError_t launch(const WindowStepArgs& a, cudaStream_t stream) {
     const int sets = (a.H / a.Hk + 15) / 16;
     constexpr size_t smem = sizeof(Joined<D, kWarps>);
-    cudaError_t e = cudaFuncSetAttribute(window_step_kernel<D, kWarps>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_once(window_step_kernel<D, kWarps>, smem, true, done);
     if (e != cudaSuccess) return e;
-    if (a.cluster > 8) {
-        e = cudaFuncSetAttribute(window_step_kernel<D, kWarps>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e != cudaSuccess) return e;
-    }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(static_cast<long long>(a.B) * a.Hk * sets * a.cluster));
     cfg.blockDim = dim3(32 * kWarps);

@@ -98,6 +98,11 @@ def _rows(x, width, inner=1):
     shape, strides = x.shape, x.stride()
     if inner == 1 and len(shape) == 2 and strides[1] == 1 and strides[0] >= width:
         return x.data_ptr(), strides[0]
+    if inner == 2 and strides[-1] == 1 and strides[-2] == shape[-1]:  # heads side by side, the usual two cases
+        if len(shape) == 3 and strides[0] >= width:
+            return x.data_ptr(), strides[0]
+        if len(shape) == 4 and strides[1] >= width and (shape[0] == 1 or strides[0] == strides[1] * shape[1]):
+            return x.data_ptr(), strides[1]
     dense = width
     for k in range(len(shape) - inner, len(shape)):
         dense //= max(shape[k], 1)
