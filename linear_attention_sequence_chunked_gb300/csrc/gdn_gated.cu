@@ -92,10 +92,10 @@ __device__ __forceinline__ void decay(Two L, Two& a, Two& gap) {
     a = add2(same(1.f), u);
     gap = mul2(u, fma2(same(-1.f), u, same(-2.f)));
 }
-// f(std::true_type) where `small`, else f(std::false_type): one branch around a loop
+// f(std::true_type) where `yes`, else f(std::false_type): one branch around a loop
 template <typename F>
-__device__ __forceinline__ void with_size(bool small, F&& f) {
-    if (small)
+__device__ __forceinline__ void with_flag(bool yes, F&& f) {
+    if (yes)
         f(std::true_type{});
     else
         f(std::false_type{});
@@ -129,6 +129,39 @@ __device__ __forceinline__ Seq find_seq(const GatedArgs& p, int t) {
     return Seq{lo, p.cu_seqlens[lo], p.cu_seqlens[lo + 1]};
 }
 
+// The next and the previous sequence that has tokens (malformed offsets stay in bounds).
+__device__ __forceinline__ int next_seq(const GatedArgs& p, int n) {
+    do ++n;
+    while (n < p.nseq - 1 && p.cu_seqlens[n] == p.cu_seqlens[n + 1]);
+    return min(n, p.nseq - 1);
+}
+__device__ __forceinline__ int previous_seq(const GatedArgs& p, int n) {
+    do --n;
+    while (n > 0 && p.cu_seqlens[n] == p.cu_seqlens[n + 1]);
+    return max(n, 0);
+}
+// Where sequences begin and end among a strip's nk tokens from t0 on, as bits, and
+// the sequences of the first and the last beginning and of the last end.
+struct Marks {
+    uint32_t starts, ends;
+    int first, begun, last;
+};
+__device__ __forceinline__ Marks marks_of(const GatedArgs& p, const Seq& q, int t0, int nk) {
+    Marks m{q.s0 == t0 ? 1u : 0u, 0, q.n, q.n, q.n};
+    int e = q.s1, n = q.n;
+    for (int i = 0; i < nk && e > t0 && e <= t0 + nk; ++i) {
+        m.ends |= 1u << (e - 1 - t0);
+        m.last = n;
+        if (e == t0 + nk) break;
+        n = next_seq(p, n);
+        if (m.starts == 0) m.first = n;
+        m.starts |= 1u << (e - t0);
+        m.begun = n;
+        e = p.cu_seqlens[n + 1];
+    }
+    return m;
+}
+
 // ---------------------------------------------------------------- exchange
 
 // A map of two channels: h -> P h + H, or h -> H where `cut`.
@@ -159,7 +192,6 @@ template <bool CUTS>
 __device__ __forceinline__ Two exchange(Exchange& sm, int parity, int warp, int lane, uint32_t rank, int C, const Map& own,
                                         bool later, Two& carry) {
     const int pr = lane & 15;
-    const auto strip = [&](int w) { return map_of(sm.warp[parity][w][pr], CUTS ? sm.cut[parity][w] : 0); };
     Map far;
     far.P.v = __shfl_xor_sync(0xffffffffu, own.P.v, 16);
     far.H.v = __shfl_xor_sync(0xffffffffu, own.H.v, 16);
@@ -169,24 +201,30 @@ __device__ __forceinline__ Two exchange(Exchange& sm, int parity, int warp, int 
     } else {
         if (lane < 16) sm.warp[parity][warp][pr] = packed(mul2(own.P, far.P), pass(own, far.H));
     }
-    if (CUTS && lane == 0) sm.cut[parity][warp] = own.cut | far.cut;
-    __syncthreads();
+    bool cuts = false;  // some map of the block ignores what comes in
+    if constexpr (CUTS) {
+        if (lane == 0) sm.cut[parity][warp] = own.cut | far.cut;
+        cuts = __syncthreads_or(own.cut) != 0;
+    } else {
+        __syncthreads();
+    }
+    const auto strip = [&](int w, auto some) { return map_of(sm.warp[parity][w][pr], decltype(some)::value ? sm.cut[parity][w] : 0); };
     Two mine = carry;
     if (C > 1) {
         if (threadIdx.x < 16) {  // the whole block's map
             Two P = same(1.f), H = same(0.f);
-            int any = 0;
+            with_flag(cuts, [&](auto some) {
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const Map m = strip(w);
-                H = pass(m, H);
-                P = mul2(P, m.P);
-                any |= m.cut;
-            }
+                for (int w = 0; w < kWarps; ++w) {
+                    const Map m = strip(w, some);
+                    H = pass(m, H);
+                    P = mul2(P, m.P);
+                }
+            });
             const float4 v = packed(P, H);
             for (int c = 0; c < C; ++c) {
                 store_remote(&sm.block[parity][rank][pr], c, v);
-                if (CUTS && lane == 0) store_remote(&sm.block_cut[parity][rank], c, any);
+                if (CUTS && lane == 0) store_remote(&sm.block_cut[parity][rank], c, cuts);
             }
         }
         cluster_sync();
@@ -194,15 +232,19 @@ __device__ __forceinline__ Two exchange(Exchange& sm, int parity, int warp, int 
             if (c == static_cast<int>(rank)) mine = carry;
             carry = pass(map_of(sm.block[parity][c][pr], CUTS ? sm.block_cut[parity][c] : 0), carry);
         }
+        with_flag(cuts, [&](auto some) {
 #pragma unroll
-        for (int w = 0; w < kWarps - 1; ++w)
-            if (w < warp) mine = pass(strip(w), mine);
+            for (int w = 0; w < kWarps - 1; ++w)
+                if (w < warp) mine = pass(strip(w, some), mine);
+        });
     } else {
+        with_flag(cuts, [&](auto some) {
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            if (w == warp) mine = carry;
-            carry = pass(strip(w), carry);
-        }
+            for (int w = 0; w < kWarps; ++w) {
+                if (w == warp) mine = carry;
+                carry = pass(strip(w, some), carry);
+            }
+        });
     }
     return later ? pass(far, mine) : mine;
 }
@@ -343,22 +385,24 @@ __global__ void __launch_bounds__(32 * kWarps, 2) gated_fwd_kernel(const GatedAr
     fetch(mine0, 0);
     if (w.C > 1) cluster_sync();  // every block of the cluster is there
     Two carry = SEQS ? same(0.f) : start_of(w.row);
+    Seq q{w.row, 0, SEQS ? 0 : p.T};  // that of the strip's first token
     for (int b0 = 0, round = 0; b0 < spans; b0 += step, ++round) {
         const int s = b0 + mine0;
         const int t0 = s * SPAN + w.sub * KS;  // this lane's first token: below 2^30 + 2^13
         const int nk = max(0, min(KS, p.T - t0));
         fetch(s + step, (round + 1) & 1);
-        Seq q{w.row, 0, p.T};
-        if (SEQS && nk > 0) q = find_seq(p, t0);
+        if (SEQS && nk > 0 && t0 >= q.s1) q = find_seq(p, t0);
         // the strip holds a sequence's end, or (packed) its beginning
         const bool ends = q.s1 <= t0 + KS || (SEQS && q.s0 == t0);
+        Marks mk{0, q.s1 - 1 - t0 < KS && nk > 0 ? 1u << (q.s1 - 1 - t0) : 0u, w.row, w.row, w.row};
+        if (SEQS && ends) mk = marks_of(p, q, t0, nk);
         wait_copies<1>();
         __syncwarp();
         Two a[KS], b[KS];
         Map m{same(1.f), same(0.f), 0};
         if (s < spans) {
             const T* v = &tile.v[round & 1][0][w.sub * KS][(w.lane & 15) * 2];
-            with_size(small, [&](auto size) {
+            with_flag(small, [&](auto size) {
 #pragma unroll
                 for (int k = 0; k < KS; ++k) {
                     Two gap;
@@ -375,18 +419,23 @@ __global__ void __launch_bounds__(32 * kWarps, 2) gated_fwd_kernel(const GatedAr
                 }
             }
             if (ends) {
-                Seq e = q;
+                if (SEQS) {
+                    // an initial state joins its first token's input, and nothing else comes in
+                    int n = mk.first;
+                    for (uint32_t left = mk.starts; left; left &= left - 1) {
+                        const int at = __ffs(left) - 1;
+                        const Two h0 = start_of(n);
+#pragma unroll
+                        for (int k = 0; k < KS; ++k)
+                            if (k == at) b[k] = fma2(a[k], h0, b[k]);
+                        n = next_seq(p, n);
+                    }
+                    m.cut = mk.starts != 0;
+                }
 #pragma unroll
                 for (int k = 0; k < KS; ++k) {
-                    if (k >= nk) continue;
-                    if (SEQS) {
-                        if (t0 + k >= e.s1) e = find_seq(p, t0 + k);
-                        if (t0 + k == e.s0) {
-                            m.cut = 1;
-                            m.H = start_of(e.n);
-                        }
-                    }
-                    m.H = fma2(a[k], m.H, b[k]);
+                    if (SEQS && (mk.starts >> k) & 1) m.H = same(0.f);
+                    if (k < nk) m.H = fma2(a[k], m.H, b[k]);
                     m.P = mul2(m.P, a[k]);
                 }
             }
@@ -403,18 +452,19 @@ __global__ void __launch_bounds__(32 * kWarps, 2) gated_fwd_kernel(const GatedAr
                 to += p.D;
             }
         } else {
+            int n = SEQS ? q.n : w.row;
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
                 if (k >= nk) continue;
                 if (k % kGatedStrip == 0 && keep) store_state(keep, k / kGatedStrip, w.D, w.d, w.nd, h);
-                if (SEQS) {
-                    if (t0 + k >= q.s1) q = find_seq(p, t0 + k);
-                    if (t0 + k == q.s0) h = start_of(q.n);
-                }
+                if (SEQS && (mk.starts >> k) & 1) h = same(0.f);
                 h = fma2(a[k], h, b[k]);
                 store_pair<T, kEven<T, PB>>(to, w.nd, h);
                 to += p.D;
-                if (t0 + k == q.s1 - 1 && p.final_state) store_state(p.final_state, q.n, w.D, w.d, w.nd, h);
+                if ((mk.ends >> k) & 1) {
+                    if (p.final_state) store_state(p.final_state, n, w.D, w.d, w.nd, h);
+                    if (SEQS) n = next_seq(p, n);
+                }
             }
         }
     }
@@ -468,6 +518,7 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? 2 : 1) gated_bwd
     fetch(spans - 1 - mine0, 0);
     if (w.C > 1) cluster_sync();  // every block of the cluster is there
     Two carry = SEQS ? same(0.f) : end_of(w.row), dlam = same(0.f);
+    Seq q{w.row, SEQS ? p.T : 0, p.T};  // that of the strip's first token
     for (int b0 = 0, round = 0; b0 < spans; b0 += step, ++round) {
         const int s = spans - 1 - (b0 + mine0);  // from the last span on
         const int t0 = s * SPAN + w.sub * KS;
@@ -476,35 +527,37 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? 2 : 1) gated_bwd
         fetch(s - step, (round + 1) & 1);
         Two h = same(0.f);
         if (nk > 0) h = load_state(p.saved, static_cast<long long>(w.row) * strips + 2 * s + w.sub, w.D, w.d, w.nd);
-        Seq q{w.row, 0, p.T};
-        if (SEQS && nk > 0) q = find_seq(p, t0);
+        if (SEQS && nk > 0 && t0 < q.s0) q = find_seq(p, t0);
         // the strip holds a sequence's beginning, or (packed) its end, or is not full
         const bool ends = q.s0 == t0 || nk < KS || (SEQS && q.s1 <= t0 + KS);
+        Marks mk{t0 == 0 ? 1u : 0u, 0, w.row, w.row, w.row};
+        if (SEQS && ends) mk = marks_of(p, q, t0, nk);
         wait_copies<1>();
         __syncwarp();
         const T* v = &tile.v[round & 1][0][w.sub * KS][(w.lane & 15) * 2];
         const auto at = [&](int which, int k) { return pair_at(v + (which * SPAN + k) * kChannels); };
         // per token: a, m, sigmoid(i) and the state before it
-        Two a[KS], mk[KS], si[KS], hp[KS];
+        Two a[KS], mt[KS], si[KS], hp[KS];
         Map m{same(1.f), same(0.f), 0};
         if (nk > 0) {
-            with_size(small, [&](auto size) {
+            with_flag(small, [&](auto size) {
 #pragma unroll
                 for (int k = 0; k < KS; ++k) {
                     Two gap;
                     decay<decltype(size)::value>(mul2(scale, sigmoid_2(at(0, k))), a[k], gap);
-                    mk[k] = root_2(gap);
+                    mt[k] = root_2(gap);
                     si[k] = sigmoid_2(at(1, k));
                 }
             });
+            int n = mk.first;
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
-                if (SEQS && ends && k < nk) {
-                    if (t0 + k >= q.s1) q = find_seq(p, t0 + k);
-                    if (t0 + k == q.s0) h = start_of(q.n);
+                if (SEQS && (mk.starts >> k) & 1) {
+                    h = start_of(n);
+                    n = next_seq(p, n);
                 }
                 hp[k] = h;
-                h = fma2(a[k], h, mul2(mk[k], mul2(si[k], at(2, k))));
+                h = fma2(a[k], h, mul2(mt[k], mul2(si[k], at(2, k))));
             }
             if (!ends) {
 #pragma unroll
@@ -513,16 +566,14 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? 2 : 1) gated_bwd
                     m.P = mul2(m.P, a[k]);
                 }
             } else {
-                Seq e = q;
+                n = mk.last;
+                m.cut = SEQS && mk.ends != 0;
 #pragma unroll
                 for (int k = KS - 1; k >= 0; --k) {
                     if (k >= nk) continue;  // the row's last strip may be short: its other tokens are not there
-                    if (SEQS) {
-                        if (t0 + k < e.s0) e = find_seq(p, t0 + k);
-                        if (t0 + k == e.s1 - 1) {  // nothing comes from the next sequence
-                            m.cut = 1;
-                            m.H = end_of(e.n);
-                        }
+                    if (SEQS && (mk.ends >> k) & 1) {  // nothing comes from the next sequence
+                        m.H = end_of(n);
+                        n = previous_seq(p, n);
                     }
                     m.H = mul2(a[k], add2(at(3, k), m.H));
                     m.P = mul2(m.P, a[k]);
@@ -536,12 +587,12 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? 2 : 1) gated_bwd
             const auto token = [&](int k) {
                 const Two dh = add2(at(3, k), c), sr = sigmoid_2(at(0, k)), gx = mul2(si[k], at(2, k));
                 float m0, m1;
-                split(mk[k], m0, m1);
+                split(mt[k], m0, m1);
                 const Two inv = two(m0 > 0.f ? rcp(m0) : 0.f, m1 > 0.f ? rcp(m1) : 0.f);
                 // a h_{t-1} - a^2 / m gx = a (h_{t-1} - a / m gx)
                 const Two past = fma2(mul2(mul2(a[k], inv), same(-1.f)), gx, hp[k]);
                 c = mul2(a[k], dh);
-                const Two dL = mul2(c, past), dg = mul2(dh, mk[k]);
+                const Two dL = mul2(c, past), dg = mul2(dh, mt[k]);
                 dlam = fma2(dL, sr, dlam);
                 store_pair<T, kEven<T, PB>>(static_cast<T*>(p.dx) + o, w.nd, mul2(dg, si[k]));
                 store_pair<T, kEven<T, PB>>(static_cast<T*>(p.dr) + o, w.nd, mul2(mul2(dL, mul2(scale, sr)), fma2(same(-1.f), sr, same(1.f))));
@@ -551,15 +602,19 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? 2 : 1) gated_bwd
 #pragma unroll
                 for (int k = KS - 1; k >= 0; --k, o -= p.D) token(k);
             } else {
+                int end = mk.last, start = mk.begun;
 #pragma unroll
                 for (int k = KS - 1; k >= 0; --k, o -= p.D) {
                     if (k >= nk) continue;
-                    if (SEQS) {
-                        if (t0 + k < q.s0) q = find_seq(p, t0 + k);
-                        if (t0 + k == q.s1 - 1) c = end_of(q.n);
+                    if (SEQS && (mk.ends >> k) & 1) {
+                        c = end_of(end);
+                        end = previous_seq(p, end);
                     }
                     token(k);
-                    if (t0 + k == q.s0 && p.d_initial_state) store_state(p.d_initial_state, q.n, w.D, w.d, w.nd, c);
+                    if ((mk.starts >> k) & 1) {
+                        if (p.d_initial_state) store_state(p.d_initial_state, start, w.D, w.d, w.nd, c);
+                        if (SEQS) start = previous_seq(p, start);
+                    }
                 }
             }
         }
