@@ -185,68 +185,68 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = max(0, lg - 2); i < lg; ++i) mbar_wait(bar(kvG + (i & 1)), (i >> 1) & 1);
         __syncwarp();
     } else if (warp == 9) {
-        if (elect_one()) {
-            constexpr uint32_t id_s = idesc(kFmtBf16, 0, 0, 128, kTile), id_o = idesc(kFmtBf16, 0, 1, 128, D);
-            // D[tmem] = rows (K-major) of `a` times rows of `b`
-            const auto outer = [&](uint32_t d, int a, int bb) {
-                const uint32_t ua = smem_u32(sm + a), ub = smem_u32(sm + bb);
+        const Issuer issue;
+        const uint32_t base = uniform(smem_u32(sm)), tm = uniform(tmem), bar0 = base + L::bars;
+        const int ns = uniform(steps);
+        const auto ready = [&](int i, int parity) { return __all_sync(0xffffffffu, wait(i, parity)) != 0; };
+        constexpr uint32_t id_s = idesc(kFmtBf16, 0, 0, 128, kTile), id_o = idesc(kFmtBf16, 0, 1, 128, D);
+        // D[tmem] = rows (K-major) of `a` times rows of `b`
+        const auto outer = [&](uint32_t d, uint32_t a, uint32_t b) {
+            const uint64_t da = desc_sw128(base + a, 0, 1024), db = desc_sw128(base + b, 0, 1024);
 #pragma unroll
-                for (int s = 0; s < D / 16; ++s) {
-                    const uint32_t o = (s >> 2) * kSlab + (s & 3) * 32;
-                    mma_bf16(tmem + d, desc_sw128(ua + o, 0, 1024), desc_sw128(ub + o, 0, 1024), id_s, s > 0);
-                }
-            };
-            // D[tmem] += bf16 pairs at `a` (two halves of 32 columns, 64 apart) times rows of `b`
-            const auto inner = [&](uint32_t d, uint32_t a, int bb, bool more) {
-                const uint32_t ub = smem_u32(sm + bb);
+            for (int s = 0; s < D / 16; ++s) {
+                const uint32_t o = ((s >> 2) * kSlab + (s & 3) * 32) >> 4;
+                issue.ss(tm + d, da + o, db + o, id_s, s > 0);
+            }
+        };
+        // D[tmem] += bf16 pairs at `a` (two halves of 32 columns, 64 apart) times rows of `b`
+        const auto inner = [&](uint32_t d, uint32_t a, uint32_t b, bool more) {
+            const uint64_t db = desc_sw128(base + b, kSlab, 1024);
 #pragma unroll
-                for (int s = 0; s < kTile / 16; ++s)
-                    mma_bf16_ts(tmem + d, tmem + a + (s >> 2) * 64 + (s & 3) * 8, desc_sw128(ub + s * 2048, kSlab, 1024), id_o,
-                                more || s > 0);
-            };
-            bool ok = wait(kvIn, 0) && wait(kvQ, 0);
-            if (ok) {
-                tc_fence_after();
-                outer(cS, L::k, L::q);
-                mma_commit(bar(kvS));
-                ok = wait(kvG, 0);
-            }
-            if (ok) {
-                tc_fence_after();
-                outer(cDP, L::v, L::g);
-                mma_commit(bar(kvDP));
-            }
-            for (int i = 0; i < steps && ok; ++i) {
-                const int st = i & 1, nx = (i + 1) & 1, nph = ((i + 1) >> 1) & 1;
-                ok = wait(kvP, i & 1);
-                if (!ok) break;
-                tc_fence_after();
-                inner(cDV, cS, L::g + st * L::kTileBytes, i > 0);
-                mma_commit(bar(kvGFree + st));
-                if (i + 1 < steps) {
-                    ok = wait(kvQ + nx, nph);
-                    if (!ok) break;
-                    tc_fence_after();
-                    outer(cS, L::k, L::q + nx * L::kTileBytes);
-                    mma_commit(bar(kvS));
-                }
-                ok = wait(kvDS, i & 1);
-                if (!ok) break;
-                tc_fence_after();
-                inner(cDK, cDP, L::q + st * L::kTileBytes, i > 0);
-                mma_commit(bar(kvQFree + st));
-                if (i + 1 < steps) {
-                    ok = wait(kvG + nx, nph);
-                    if (!ok) break;
-                    tc_fence_after();
-                    outer(cDP, L::v, L::g + nx * L::kTileBytes);
-                    mma_commit(bar(kvDP));
-                }
-            }
-            // every product has completed before the tensor memory is read or freed
-            mma_commit(bar(kvDone));
-            mbar_wait(bar(kvDone), 0);
+            for (int s = 0; s < kTile / 16; ++s) issue.ts(tm + d, tm + a + (s >> 2) * 64 + (s & 3) * 8, db + s * 128, id_o, more || s > 0);
+        };
+        bool ok = ready(kvIn, 0) && ready(kvQ, 0);
+        if (ok) {
+            tc_fence_after();
+            outer(cS, L::k, L::q);
+            issue.commit(bar0 + 8 * kvS);
+            ok = ready(kvG, 0);
         }
+        if (ok) {
+            tc_fence_after();
+            outer(cDP, L::v, L::g);
+            issue.commit(bar0 + 8 * kvDP);
+        }
+        for (int i = 0; i < ns && ok; ++i) {
+            const int st = i & 1, nx = (i + 1) & 1, nph = ((i + 1) >> 1) & 1;
+            ok = ready(kvP, i & 1);
+            if (!ok) break;
+            tc_fence_after();
+            inner(cDV, cS, L::g + st * L::kTileBytes, i > 0);
+            issue.commit(bar0 + 8 * (kvGFree + st));
+            if (i + 1 < ns) {
+                ok = ready(kvQ + nx, nph);
+                if (!ok) break;
+                tc_fence_after();
+                outer(cS, L::k, L::q + nx * L::kTileBytes);
+                issue.commit(bar0 + 8 * kvS);
+            }
+            ok = ready(kvDS, i & 1);
+            if (!ok) break;
+            tc_fence_after();
+            inner(cDK, cDP, L::q + st * L::kTileBytes, i > 0);
+            issue.commit(bar0 + 8 * (kvQFree + st));
+            if (i + 1 < ns) {
+                ok = ready(kvG + nx, nph);
+                if (!ok) break;
+                tc_fence_after();
+                outer(cDP, L::v, L::g + nx * L::kTileBytes);
+                issue.commit(bar0 + 8 * kvDP);
+            }
+        }
+        // every product has completed before the tensor memory is read or freed
+        issue.commit(bar0 + 8 * kvDone);
+        mbar_wait(bar(kvDone), 0);
         __syncwarp();
     } else {
         const int half = warp >> 2;  // which 64 queries of the tile
@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(256) window_join_kernel(const WindowArgs p) {
 
 // ------------------------------------------------------------------ dQ
 
-enum { qIn = 0, qK = 1, qKFree = 3, qV = 5, qVFree = 7, qS = 9, qRead = 10, qDP = 11, qDS = 12, qDone = 13, qTail = 14, qBars = 15 };
+enum { qIn = 0, qK = 1, qKFree = 3, qV = 5, qVFree = 7, qS = 9, qRead = 10, qDP = 11, qDS = 13, qDone = 14, qTail = 15, qBars = 16 };
 
 template <int D>
 struct QSmem {
@@ -480,49 +480,56 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = max(0, lv - 2); j < lv; ++j) mbar_wait(bar(qV + (j & 1)), (j >> 1) & 1);
         __syncwarp();
     } else if (warp == 9) {
-        if (elect_one()) {
-            constexpr uint32_t id_o = idesc(kFmtBf16, 0, 1, 128, D);
-            const auto outer = [&](uint32_t d, int a, int bb, int width) {
-                const uint32_t ua = smem_u32(sm + a), ub = smem_u32(sm + bb), id = idesc(kFmtBf16, 0, 0, 128, width);
+        const Issuer issue;
+        const uint32_t base = uniform(smem_u32(sm)), tm = uniform(tmem), bar0 = base + L::bars;
+        Blocks ub;
+        ub.first = uniform(blk.first);
+        ub.lo = uniform(blk.lo);
+        ub.hi = uniform(blk.hi);
+        const int nb = ub.count();
+        const auto ready = [&](int i, int parity) { return __all_sync(0xffffffffu, wait(i, parity)) != 0; };
+        constexpr uint32_t id_o = idesc(kFmtBf16, 0, 1, 128, D);
+        const auto outer = [&](uint32_t d, uint32_t a, uint32_t b, int width) {
+            const uint64_t da = desc_sw128(base + a, 0, 1024), db = desc_sw128(base + b, 0, 1024);
+            const uint32_t id = idesc(kFmtBf16, 0, 0, 128, width);
 #pragma unroll
-                for (int s = 0; s < D / 16; ++s) {
-                    const uint32_t o = (s >> 2) * kSlab + (s & 3) * 32;
-                    mma_bf16(tmem + d, desc_sw128(ua + o, 0, 1024), desc_sw128(ub + o, 0, 1024), id, s > 0);
-                }
-            };
-            // S and dP of block j: while the others turn one block's into dS, the next
-            // block's are on their way
-            const auto forms = [&](int j) {
-                const int st = j & 1, ph = (j >> 1) & 1;
-                if (j > 0 && !wait(qRead, (j - 1) & 1)) return false;
-                if (!wait(qK + st, ph)) return false;
-                tc_fence_after();
-                outer(cS, L::q, L::k + st * L::kTileBytes, blk.width(j));
-                mma_commit(bar(qS));
-                if (!wait(qV + st, ph)) return false;
-                tc_fence_after();
-                outer(cDP + 128 * st, L::g, L::v + st * L::kTileBytes, blk.width(j));
-                mma_commit(bar(qDP));
-                mma_commit(bar(qVFree + st));
-                return true;
-            };
-            bool ok = wait(qIn, 0) && forms(0);
-            for (int j = 0; j < nblk && ok; ++j) {
-                const int st = j & 1;
-                if (j + 1 < nblk) ok = forms(j + 1);
-                ok = ok && wait(qDS, j & 1);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t ub = smem_u32(sm + L::k + st * L::kTileBytes);
-                const int steps = blk.width(j) / 16;
-                for (int s = 0; s < steps; ++s)
-                    mma_bf16_ts(tmem + cDQ, tmem + cDP + 128 * st + (s >> 2) * 64 + (s & 3) * 8, desc_sw128(ub + s * 2048, kSlab, 1024),
-                                id_o, (j | s) != 0);
-                mma_commit(bar(qKFree + st));
+            for (int s = 0; s < D / 16; ++s) {
+                const uint32_t o = ((s >> 2) * kSlab + (s & 3) * 32) >> 4;
+                issue.ss(tm + d, da + o, db + o, id, s > 0);
             }
-            mma_commit(bar(qDone));
-            mbar_wait(bar(qDone), 0);
+        };
+        // S and dP of block j: while the others turn one block's into dS, the next
+        // block's are on their way
+        const auto forms = [&](int j) {
+            const int st = j & 1, ph = (j >> 1) & 1;
+            if (j > 0 && !ready(qRead, (j - 1) & 1)) return false;
+            if (!ready(qK + st, ph)) return false;
+            tc_fence_after();
+            outer(cS, L::q, L::k + st * L::kTileBytes, ub.width(j));
+            issue.commit(bar0 + 8 * qS);
+            if (!ready(qV + st, ph)) return false;
+            tc_fence_after();
+            outer(cDP + 128 * st, L::g, L::v + st * L::kTileBytes, ub.width(j));
+            issue.commit(bar0 + 8 * (qDP + st));  // (a barrier per buffer: the next block's may follow before this one is looked at)
+            issue.commit(bar0 + 8 * (qVFree + st));
+            return true;
+        };
+        bool ok = ready(qIn, 0) && forms(0);
+        for (int j = 0; j < nb && ok; ++j) {
+            const int st = j & 1;
+            if (j + 1 < nb) ok = forms(j + 1);
+            ok = ok && ready(qDS, j & 1);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t k = desc_sw128(base + L::k + st * L::kTileBytes, kSlab, 1024);
+            const int steps = ub.width(j) / 16;
+#pragma unroll
+            for (int s = 0; s < kTile / 16; ++s)
+                if (s < steps) issue.ts(tm + cDQ, tm + cDP + 128 * st + (s >> 2) * 64 + (s & 3) * 8, k + s * 128, id_o, (j | s) != 0);
+            issue.commit(bar0 + 8 * (qKFree + st));
         }
+        issue.commit(bar0 + 8 * qDone);
+        mbar_wait(bar(qDone), 0);
         __syncwarp();
     } else {
         const int half = warp >> 2;  // which 64 keys of the block
@@ -561,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int e = 0; e < 64; e += 2)
                 mix::split(mix::ex2_2(mix::fma2(mix::two(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), cc, ll)), pr[e], pr[e + 1]);
-            ok = __all_sync(0xffffffffu, wait(qDP, j & 1));
+            ok = __all_sync(0xffffffffu, wait(qDP + (j & 1), (j >> 1) & 1));
             if (!ok) break;
             tc_fence_after();
             if (width > 0) tmem_ld32(tDP, s);

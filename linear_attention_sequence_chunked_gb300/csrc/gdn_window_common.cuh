@@ -22,14 +22,41 @@ using tc::smem_align_pad;
 constexpr int kTile = 128;
 constexpr int kSlab = kTile * 128;  // bytes of 128 rows of 64 channels, swizzled
 
-// D[tmem] (+)= A[tmem] * B[smem]: A holds two bf16 of a row per column.
-__device__ __forceinline__ void mma_bf16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t accum) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(id), "r"(accum)
-        : "memory");
-}
+// Products are issued by one lane (`on`) of a warp whose other lanes run along:
+// what an instruction names (descriptors, columns) then stays in uniform registers
+// from the start.  In a branch that only one lane takes every operand is moved
+// there first, which took longer than the product (100 clocks for 128 x 128 x 16).
+struct Issuer {
+    uint32_t on;
+    __device__ __forceinline__ Issuer() : on(elect_one() ? 1u : 0u) {}
+    // D[tmem] (+)= A[smem] * B[smem]
+    __device__ __forceinline__ void ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool more) const {
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(id), "r"(static_cast<uint32_t>(more)), "r"(on)
+            : "memory");
+    }
+    // D[tmem] (+)= A[tmem] * B[smem]: A holds two bf16 of a row per column
+    __device__ __forceinline__ void ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool more) const {
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+            "r"(a), "l"(b), "r"(id), "r"(static_cast<uint32_t>(more)), "r"(on)
+            : "memory");
+    }
+    // arrives on `bar` when everything issued so far has completed
+    __device__ __forceinline__ void commit(uint32_t bar) const {
+        asm volatile(
+            "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+            "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+            "r"(on)
+            : "memory");
+    }
+};
+// The warp's value of x, which all its lanes have
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
 // 32 lanes x 32 bits, 32 consecutive columns per thread.
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
@@ -41,6 +68,16 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
           "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
           "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(taddr));
+}
+// Holds every use of r behind the wait before it (a load's registers are only
+// there after tcgen05.wait::ld, which names none).
+__device__ __forceinline__ void after_wait32(uint32_t* r) {
+    asm volatile(""
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
+                   "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                   "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]));
+    asm volatile("" : "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
 }
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
     asm volatile(
@@ -139,6 +176,44 @@ __device__ __forceinline__ bool load_tile(uint8_t* tile, const CUtensorMap* map,
         if (lane == 0) mbar_arrive(full);
     }
     return true;
+}
+
+// A warp's 32 rows of W columns of an accumulator, times `mul`, as bf16 into rows
+// of `out` (the column's place, `stride` elements apart): rows [first, rows) of
+// them.  Through `mine`, 64 W bytes of the warp's own shared memory, in 16-byte
+// chunks permuted so that neither side meets a bank twice.  Returns NaN for a row
+// with a value that is not finite, else 0.
+template <int W>
+__device__ __forceinline__ float store_columns(uint32_t t, float mul, uint8_t* mine, uint16_t* out, long long stride, int first,
+                                               int rows, int lane) {
+    constexpr int kChunks = W / 8, kMask = kChunks - 1;
+    float bad = 0.f;
+#pragma unroll
+    for (int g = 0; g < W; g += 32) {
+        uint32_t o[32];
+        tmem_ld32(t + g, o);
+        tmem_ld_wait();
+        after_wait32(o);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float u = __uint_as_float(o[8 * q + 2 * e]) * mul, v = __uint_as_float(o[8 * q + 2 * e + 1]) * mul;
+                bad = fmaf(u, 0.f, fmaf(v, 0.f, bad));
+                w[e] = cvt_bf16x2(u, v);
+            }
+            *reinterpret_cast<uint4*>(mine + lane * (W * 2) + (((g / 8 + q) ^ (lane & kMask)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+    __syncwarp();
+#pragma unroll 4
+    for (int k = 0; k < kChunks; ++k) {
+        const int r = (k * 32 + lane) / kChunks, ch = (k * 32 + lane) % kChunks;
+        const uint4 w = *reinterpret_cast<const uint4*>(mine + r * (W * 2) + ((ch ^ (r & kMask)) * 16));
+        if (r >= first && r < rows) *reinterpret_cast<uint4*>(out + r * stride + ch * 8) = w;
+    }
+    return bad;
 }
 
 // {64 channels, 1 head, `box` tokens} of (tokens, heads, d) bf16, tokens `stride`

@@ -175,52 +175,57 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = max(0, loaded_v - 2); j < loaded_v; ++j) mbar_wait(bar(bV + (j & 1)), (j >> 1) & 1);
             __syncwarp();
         } else if (warp == 9) {
-            if (elect_one()) {
-                const auto scores = [&](int j, int x) {  // S of tile x with block j
-                    const uint32_t qa = smem_u32(sm + L::q + x * L::kTileBytes), ka = smem_u32(sm + L::k + (j & 1) * L::kTileBytes);
-                    const uint32_t id = idesc(kFmtBf16, 0, 0, 128, blk.width(j));
+            const Issuer issue;
+            const uint32_t base = uniform(smem_u32(sm)), tm = uniform(tmem), bar0 = base + L::bars;
+            Blocks ub;
+            ub.first = uniform(blk.first);
+            ub.lo = uniform(blk.lo);
+            ub.hi = uniform(blk.hi);
+            const int nb = ub.count(), tiles = uniform(second ? 2 : 1);
+            const auto ready = [&](int i, int parity) { return __all_sync(0xffffffffu, wait(i, parity)) != 0; };
+            const auto scores = [&](int j, int x) {  // S of tile x with block j
+                const uint64_t q = desc_sw128(base + L::q + x * L::kTileBytes, 0, 1024), k = desc_sw128(base + L::k + (j & 1) * L::kTileBytes, 0, 1024);
+                const uint32_t id = idesc(kFmtBf16, 0, 0, 128, ub.width(j));
 #pragma unroll
-                    for (int s = 0; s < D / 16; ++s) {
-                        const uint32_t o = (s >> 2) * kSlab + (s & 3) * 32;
-                        mma_bf16(tmem + 128 * x, desc_sw128(qa + o, 0, 1024), desc_sw128(ka + o, 0, 1024), id, s > 0);
-                    }
-                    mma_commit(bar(bS + x));
-                };
-                const int tiles = second ? 2 : 1;
-                bool ok = true;
+                for (int s = 0; s < D / 16; ++s) {
+                    const uint32_t o = ((s >> 2) * kSlab + (s & 3) * 32) >> 4;
+                    issue.ss(tm + 128 * x, q + o, k + o, id, s > 0);
+                }
+                issue.commit(bar0 + 8 * (bS + x));
+            };
+            bool ok = true;
+            for (int x = 0; x < tiles && ok; ++x) {
+                ok = ready(bQ + x, 0) && ready(bK, 0);
+                if (!ok) break;
+                tc_fence_after();
+                scores(0, x);
+            }
+            if (ok) issue.commit(bar0 + 8 * bKFree);
+            constexpr uint32_t id_o = idesc(kFmtBf16, 0, 1, 128, D);
+            for (int j = 0; j < nb && ok; ++j) {
+                const int steps = ub.width(j) / 16;
                 for (int x = 0; x < tiles && ok; ++x) {
-                    ok = wait(bQ + x, 0) && wait(bK, 0);
+                    ok = ready(bV + (j & 1), (j >> 1) & 1) && ready(bP + x, j & 1);
                     if (!ok) break;
                     tc_fence_after();
-                    scores(0, x);
-                }
-                if (ok) mma_commit(bar(bKFree));
-                constexpr uint32_t id_o = idesc(kFmtBf16, 0, 1, 128, D);
-                for (int j = 0; j < nblk && ok; ++j) {
-                    const int steps = blk.width(j) / 16;
-                    for (int x = 0; x < tiles && ok; ++x) {
-                        ok = wait(bV + (j & 1), (j >> 1) & 1) && wait(bP + x, j & 1);
+                    const uint64_t v = desc_sw128(base + L::v + (j & 1) * L::kTileBytes, kSlab, 1024);
+#pragma unroll
+                    for (int s = 0; s < kTile / 16; ++s)
+                        if (s < steps) issue.ts(tm + 256 + 128 * x, tm + 128 * x + 8 * s, v + s * 128, id_o, (j | s) != 0);
+                    if (j + 1 == nb) issue.commit(bar0 + 8 * (bO + x));
+                    if (x == tiles - 1) issue.commit(bar0 + 8 * (bVFree + (j & 1)));
+                    if (j + 1 < nb) {
+                        ok = ready(bK + ((j + 1) & 1), ((j + 1) >> 1) & 1);
                         if (!ok) break;
                         tc_fence_after();
-                        const uint32_t va = smem_u32(sm + L::v + (j & 1) * L::kTileBytes);
-                        for (int s = 0; s < steps; ++s)
-                            mma_bf16_ts(tmem + 256 + 128 * x, tmem + 128 * x + 8 * s, desc_sw128(va + s * 2048, kSlab, 1024), id_o,
-                                        (j | s) != 0);
-                        if (j + 1 == nblk) mma_commit(bar(bO + x));
-                        if (x == tiles - 1) mma_commit(bar(bVFree + (j & 1)));
-                        if (j + 1 < nblk) {
-                            ok = wait(bK + ((j + 1) & 1), ((j + 1) >> 1) & 1);
-                            if (!ok) break;
-                            tc_fence_after();
-                            scores(j + 1, x);
-                            if (x == tiles - 1) mma_commit(bar(bKFree + ((j + 1) & 1)));
-                        }
+                        scores(j + 1, x);
+                        if (x == tiles - 1) issue.commit(bar0 + 8 * (bKFree + ((j + 1) & 1)));
                     }
                 }
-                // every product has completed before the tensor memory is freed
-                mma_commit(bar(bDrain));
-                mbar_wait(bar(bDrain), 0);
             }
+            // every product has completed before the tensor memory is freed
+            issue.commit(bar0 + 8 * bDrain);
+            mbar_wait(bar(bDrain), 0);
             __syncwarp();
         }
     } else {
