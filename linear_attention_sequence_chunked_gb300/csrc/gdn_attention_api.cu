@@ -42,7 +42,6 @@ gdn_status rope_args(gdn::RopeArgs& a, const void* q, int64_t q_stride, const vo
     a.dtype = dtype; a.eps = eps;
     a.share = gdn::rope_share(a.tokens, std::max(H, Hk), d);
     a.blocks = static_cast<unsigned>(gdn::rope_blocks(a.tokens, std::max(H, Hk), d));
-    if (a.tokens > 0 && !(a.err = gdn::device_error_word())) return GDN_ERR_CUDA;
     return GDN_OK;
 }
 
@@ -101,7 +100,6 @@ gdn_status window_args(gdn::WindowArgs& a, const WindowLayout& L, const gdn_bf16
     a.cu_seqlens = cu_seqlens; a.tokens = varlen ? T : static_cast<long long>(B) * T;
     a.nseq = B; a.T = T; a.H = H; a.Hk = Hk; a.d = d; a.window = L.window; a.sinks = L.sinks; a.scale = scale;
     a.far_tokens = L.far_tokens; a.far_slots = L.far_slots;
-    if (T > 0 && !(a.err = gdn::device_error_word())) return GDN_ERR_CUDA;
     return GDN_OK;
 }
 
@@ -119,6 +117,7 @@ gdn_status gdn_rope_fwd(const void* q, int64_t q_stride, const void* k, int64_t 
     GDN_TRY(check_dense({q_out, k_out}));
     if (a.tokens == 0) return GDN_OK;
     if (!q_out || !k_out) return GDN_ERR_INVALID_ARG;
+    if (!(a.err = gdn::device_error_word())) return GDN_ERR_CUDA;
     a.q_out = q_out; a.k_out = k_out;
     return gdn::count_launch(gdn::launch_rope_fwd(a, stream)) ? GDN_OK : GDN_ERR_CUDA;
 }
@@ -145,6 +144,7 @@ gdn_status gdn_rope_bwd(const void* q, int64_t q_stride, const void* k, int64_t 
     if (par) GDN_TRY(check_ws(workspace, workspace_bytes, gdn_rope_bwd_workspace_size(B, T, H, Hk, d, cu_seqlens != nullptr)));
     if (a.tokens > 0) {
         if (!dq_out || !dk_out || !dq || !dk) return GDN_ERR_INVALID_ARG;
+        if (!(a.err = gdn::device_error_word())) return GDN_ERR_CUDA;
         a.dq_out = dq_out; a.dk_out = dk_out; a.dq = dq; a.dk = dk;
         a.partial = par ? static_cast<float*>(workspace) : nullptr;
         if (!gdn::count_launch(gdn::launch_rope_bwd(a, stream))) return GDN_ERR_CUDA;
@@ -168,6 +168,7 @@ gdn_status gdn_window_fwd(const gdn_bf16* q, int64_t q_stride, const gdn_bf16* k
     GDN_TRY(check_dense({out, lse}));
     if (T == 0) return GDN_OK;
     if (!out) return GDN_ERR_INVALID_ARG;
+    if (!(a.err = gdn::device_error_word())) return GDN_ERR_CUDA;
     a.out = out; a.lse = lse;
     a.slots = tile_slots(B, T, gdn::window_fwd_rows(H, Hk), varlen);
     return gdn::count_launch(gdn::launch_window_fwd(a, stream)) ? GDN_OK : GDN_ERR_CUDA;
@@ -192,6 +193,7 @@ gdn_status gdn_window_bwd(const gdn_bf16* q, int64_t q_stride, const gdn_bf16* k
     if (T == 0) return GDN_OK;
     if (!out || !lse || !d_out || !dq || !dk || !dv) return GDN_ERR_INVALID_ARG;
     GDN_TRY(check_ws(workspace, workspace_bytes, L.total));
+    if (!(a.err = gdn::device_error_word())) return GDN_ERR_CUDA;
     a.out = const_cast<gdn_bf16*>(out); a.lse = const_cast<float*>(lse); a.d_out = d_out;
     a.dq = dq; a.dk = dk; a.dv = dv;
     a.delta = static_cast<float*>(workspace);
