@@ -107,6 +107,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (blockIdx.x == 0) mix::check_offsets(p.cu_seqlens, p.nseq, p.T, p.err);
 
+    if (threadIdx.x == 256) {
+        tma_prefetch_desc(&map_q);
+        tma_prefetch_desc(&map_k);
+        tma_prefetch_desc(&map_v);
+        tma_prefetch_desc(&map_g);
+    }
     // a tile of keys and the tiles of queries [qa, qb) that its block looks at:
     // those in reach of the tile's own window, or a stretch that sees only the
     // first tokens of block 0
@@ -418,6 +424,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+    if (threadIdx.x == 256) {
+        tma_prefetch_desc(&map_q);
+        tma_prefetch_desc(&map_k);
+        tma_prefetch_desc(&map_v);
+        tma_prefetch_desc(&map_g);
+    }
     const int h = blockIdx.x % p.H, hk = h / (p.H / p.Hk);
     const long long slot = p.slots - 1 - blockIdx.x / p.H;  // late tiles, with the most keys, first
     int n, b, t0, t1;

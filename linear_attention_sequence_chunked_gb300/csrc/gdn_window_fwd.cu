@@ -98,6 +98,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (blockIdx.x == 0) mix::check_offsets(p.cu_seqlens, p.nseq, p.T, p.err);
 
+    if (threadIdx.x == 256) {
+        tma_prefetch_desc(&map_q);
+        tma_prefetch_desc(&map_k);
+        tma_prefetch_desc(&map_v);
+    }
+
     // the two tiles: heads h and h + 1 of one tile, or two tiles of head h
     const int G = p.H / p.Hk, two_heads = G % 2 == 0;
     const int units = two_heads ? p.H / 2 : p.H;
