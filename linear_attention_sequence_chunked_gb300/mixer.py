@@ -87,7 +87,7 @@ _current = torch._C._cuda_getCurrentRawStream
 
 def _new(x):
     """A contiguous tensor of x's shape and type (the quickest call that gives one)."""
-    return torch.empty_like(x) if x.is_contiguous() else x.new_empty(x.shape)
+    return torch.empty_like(x) if x.is_contiguous() else torch.empty(x.shape, dtype=x.dtype, device=x.device)
 
 
 def _rows(x, width, inner=1):
