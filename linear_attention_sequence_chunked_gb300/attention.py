@@ -134,8 +134,8 @@ def _window_args(q, k, v, window, sinks, scale, dims):
         raise ValueError(f"the {H} query heads must divide into the {Hk} key heads")
     _window_sizes(window, sinks)
     scale = d ** -0.5 if scale is None else float(scale)
-    if not scale > 0:
-        raise ValueError(f"scale must be positive, got {scale}")
+    if not 0 < scale < 3e38:
+        raise ValueError(f"scale must be positive and finite, got {scale}")
     _on_gpu(dev, q)
     held = []
     return dev, held, (*_pieces(q, H * d, held), *_pieces(k, Hk * d, held), *_pieces(v, Hk * d, held)), H, Hk, d, scale

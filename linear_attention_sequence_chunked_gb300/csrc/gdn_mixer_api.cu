@@ -377,7 +377,7 @@ gdn_status gdn_gated_fwd(const void* x, int64_t x_stride, const void* r, int64_t
                          const int32_t* cu_seqlens, void* y, float* final_state, void* saved, size_t saved_bytes,
                          int B, int T, int D, int dtype, cudaStream_t stream) {
     GDN_TRY(check_sizes(B, T, D, dtype));
-    if (!lam || !(rate > 0.f) || (T > 0 && !y)) return GDN_ERR_INVALID_ARG;
+    if (!lam || !(rate > 0.f && rate < 3e38f) || (T > 0 && !y)) return GDN_ERR_INVALID_ARG;
     if (T > 0) {
         GDN_TRY(check_rows(x, x_stride, D, dtype));
         GDN_TRY(check_rows(r, r_stride, D, dtype));
@@ -411,7 +411,7 @@ gdn_status gdn_gated_bwd(const void* x, int64_t x_stride, const void* r, int64_t
                          size_t saved_bytes, void* dx, void* dr, void* di, float* dlam, float* d_initial_state, int B,
                          int T, int D, int dtype, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
     GDN_TRY(check_sizes(B, T, D, dtype));
-    if (!lam || !dlam || !(rate > 0.f)) return GDN_ERR_INVALID_ARG;
+    if (!lam || !dlam || !(rate > 0.f && rate < 3e38f)) return GDN_ERR_INVALID_ARG;
     if (T > 0) {
         if (!d_out || !dx || !dr || !di) return GDN_ERR_INVALID_ARG;
         GDN_TRY(check_rows(x, x_stride, D, dtype));
@@ -445,7 +445,7 @@ gdn_status gdn_gated_step(const void* x, int64_t x_stride, const void* r, int64_
                           int64_t i_stride, const float* lam, float rate, const float* state, float* out_state,
                           const int32_t* slots, void* y, int B, int S, int D, int dtype, cudaStream_t stream) {
     GDN_TRY(check_sizes(B, 1, D, dtype));
-    if (!lam || !state || !out_state || !y || !(rate > 0.f) || S < 1 || (!slots && S < B)) return GDN_ERR_INVALID_ARG;
+    if (!lam || !state || !out_state || !y || !(rate > 0.f && rate < 3e38f) || S < 1 || (!slots && S < B)) return GDN_ERR_INVALID_ARG;
     GDN_TRY(check_rows(x, x_stride, D, dtype));
     GDN_TRY(check_rows(r, r_stride, D, dtype));
     GDN_TRY(check_rows(i, i_stride, D, dtype));

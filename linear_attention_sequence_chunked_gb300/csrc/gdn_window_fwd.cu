@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int g = 0; g < 4; ++g) top[g] = max3(top[g], __uint_as_float(s[e + 2 * g]), __uint_as_float(s[e + 2 * g + 1]));
                 const float mb = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c2;
-                if (__any_sync(0xffffffffu, mb > m + kGrow)) {
+                if (__any_sync(0xffffffffu, mb > m + kGrow && i < len)) {  // (rows behind the sequence move nobody's maximum)
                     const float mn = fmaxf(m, mb);
                     const float f = m == -INFINITY ? 0.f : mix::ex2(m - mn);
                     m = mn;
@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         *reinterpret_cast<uint4*>(p.out + (row0 + t) * (static_cast<long long>(p.H) * D) + h * D + ch * 8) = w;
                 }
                 __syncwarp();
-                uint32_t again = __ballot_sync(0xffffffffu, bad != 0.f && i < len);
+                uint32_t again = __ballot_sync(0xffffffffu, bad != 0.f && l < INFINITY && i < len);  // (a sum that is not finite: its own scores)
                 while (again) {
                     const int src = __ffs(again) - 1;
                     again &= again - 1;

@@ -390,8 +390,8 @@ def _gated_args(x, r, i, lam, rate):
     D = shape[-1]
     _is("r", r, shape, x.dtype, dev)
     _is("i", i, shape, x.dtype, dev)
-    if not rate > 0:
-        raise ValueError(f"rate must be positive, got {rate}")
+    if not 0 < rate < 3e38:
+        raise ValueError(f"rate must be positive and finite, got {rate}")
     return dev, dtype, D, (*_rows(x, D), *_rows(r, D), *_rows(i, D), _dense("lam", lam, (D,), torch.float32, dev), rate)
 
 

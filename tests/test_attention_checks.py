@@ -34,7 +34,7 @@ def _gated(**over):
     (dict(x=_z(2, 8, 12, dtype=torch.float16)), "x must be"), (dict(x=_z(8, 12)), "x must be"),
     (dict(r=_z(2, 8, 12, dtype=F32)), "r must be"), (dict(i=_z(2, 8, 11)), "i must have shape"),
     (dict(lam=torch.zeros(11)), "lam must have shape"), (dict(lam=_z(12)), "lam must be"), (dict(rate=0.0), "rate"),
-    (dict(rate=float("nan")), "rate"), (dict(initial_state=torch.zeros(2, 11)), "initial_state"),
+    (dict(rate=float("nan")), "rate"), (dict(rate=float("inf")), "rate"), (dict(initial_state=torch.zeros(2, 11)), "initial_state"),
     (dict(initial_state=_z(2, 12)), "initial_state"), (dict(cu_seqlens=torch.tensor([0, 8], dtype=torch.int32)), "batch extent 1"),
     ({}, "CUDA"),
 ])
@@ -91,7 +91,7 @@ def _window(**over):
     (dict(v=_z(2, 8, 1, 64)), "v must have shape"), (dict(v=_z(2, 8, 2, 64, dtype=F32)), "v must be"),
     (dict(q=_z(2, 8, 4, 96), k=_z(2, 8, 2, 96), v=_z(2, 8, 2, 96)), "head size"),
     (dict(k=_z(2, 8, 3, 64), v=_z(2, 8, 3, 64)), "divide into"), (dict(window=0), "window"), (dict(window=-1), "window"),
-    (dict(sinks=-1), "sinks"), (dict(sinks=129), "sinks"), (dict(scale=0.0), "scale"), (dict(scale=float("nan")), "scale"),
+    (dict(sinks=-1), "sinks"), (dict(sinks=129), "sinks"), (dict(scale=0.0), "scale"), (dict(scale=float("nan")), "scale"), (dict(scale=float("inf")), "scale"),
     ({}, "CUDA"),
 ])
 def test_window_refusals(over, msg):
@@ -280,7 +280,7 @@ def test_gated_host_validation(lib):
         return lib.gdn_gated_fwd(x, xs, r, rs, i, i_s, lam, rate, h, cu, y, fs, saved, n, B, T, D, dtype, None)
     assert call(B=0) == 1 and call(T=-1) == 1 and call(D=0) == 1 and call(dtype=2) == 1 and call(B=70000) == 2 and call(D=70000) == 2
     assert call(x=None) == 1 and call(r=None) == 1 and call(i=None) == 1 and call(lam=None) == 1 and call(y=None) == 1
-    assert call(xs=63) == 1 and call(rs=63) == 1 and call(i_s=63) == 1 and call(rate=0.0) == 1 and call(rate=float("nan")) == 1
+    assert call(xs=63) == 1 and call(rs=63) == 1 and call(i_s=63) == 1 and call(rate=0.0) == 1 and call(rate=float("nan")) == 1 and call(rate=float("inf")) == 1
     assert call(x=FAKE + 1) == 3 and call(r=FAKE + 2, dtype=1) == 3 and call(lam=FAKE + 4) == 3 and call(y=FAKE + 2) == 3
     assert call(cu=FAKE + 2) == 3 and call(h=FAKE, fs=FAKE) == 1 and call(T=0) == 0
     need = lib.gdn_gated_saved_size(1, 20, 64, 0)

@@ -206,3 +206,44 @@ def test_calls_side_by_side_repeat_bit_for_bit():
         torch.cuda.synchronize()
         for got in made:
             assert all(torch.equal(x1, x2) for x1, x2 in zip(got, want))
+
+
+def test_sequences_do_not_touch_each_other():
+    """A neighbour's values, however large, change no bit of a packed sequence:
+    of its outputs, its states or its gradients."""
+    cu, T = [0, 100, 250, 411], 411
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    n = lambda *s: torch.randn(*s, generator=gen, device="cuda").to(BF)  # noqa: E731
+    ins = [n(1, T, 4, 64), n(1, T, 2, 64), n(1, T, 2, 64), n(1, T, 4, 64)]
+    seq = [n(1, T, 66) for _ in range(4)]
+    lam, f = -torch.rand(66, device="cuda") * 3 - 2, 10000.0 ** (-torch.arange(32, device="cuda") / 32)
+
+    def everything(q, k, v, g, x, r, i, dy):
+        q, k = attention.qk_norm_rope_fwd(q, k, inv_freq=f, cu_seqlens=_ints(cu))
+        q, k = q * big, k * big
+        out, lse = attention.window_attention_fwd(q, k, v, 70, 3, cu_seqlens=_ints(cu), save_for_backward=True)
+        b = attention.window_attention_bwd(q, k, v, out, lse, g, 70, 3, cu_seqlens=_ints(cu))
+        y, fs, saved = mixer.gated_scan_fwd(x, r, i, lam, cu_seqlens=_ints(cu), save_for_backward=True)
+        c = mixer.gated_scan_bwd(x, r, i, lam, dy, saved, cu_seqlens=_ints(cu))
+        return [out, lse.transpose(1, 2), *b.values(), y, c["dx"], c["dr"], c["di"]], fs
+
+    big = torch.ones(1, T, 1, 1, device="cuda", dtype=BF)
+    want, states = everything(*ins, *seq)
+    big[0, 100:250] = 64
+    other = [t.clone() for t in (*ins, *seq)]
+    for t in other:
+        t[0, 100:250] *= 100
+    got, new = everything(*other)
+    for a, b in zip(got, want):
+        assert torch.equal(a[0, :100], b[0, :100]) and torch.equal(a[0, 250:], b[0, 250:])
+    assert torch.equal(new[0], states[0]) and torch.equal(new[2], states[2])
+
+
+def test_queries_that_are_not_finite():
+    """Their own outputs are NaN, and nobody else's."""
+    q, k, v = (torch.randn(1, 4096, h, 64, device="cuda").to(BF) for h in (2, 2, 2))
+    good = attention.window_attention_fwd(q, k, v, 4096)
+    q[0, 1000:3000] = float("nan")
+    out = attention.window_attention_fwd(q, k, v, 4096)
+    assert torch.isnan(out[0, 1000:3000]).all()
+    assert torch.equal(out[0, :1000], good[0, :1000]) and torch.equal(out[0, 3000:], good[0, 3000:])
