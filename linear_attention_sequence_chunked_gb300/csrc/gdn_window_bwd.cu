@@ -7,9 +7,13 @@
 // in two kernels, one that owns a tile of keys and one that owns a tile of
 // queries, each of which forms S and dP for itself: seven products instead of
 // five, but every gradient is summed by one block in one order, without atomics.
-// All products run on the tensor cores; P and dS are rounded to bf16 as operands
-// (half a step of 2^-8 each, in random directions) and stay in tensor memory,
-// written over the S and dP that they come from.
+// All products run on the tensor cores, with operands that stay in tensor memory,
+// written over the S and dP that they come from.  P is rounded to bf16 for dV, as
+// in the forward.  dS goes in as two bf16 parts, what it rounds to and what is
+// left: it is a difference that carries delta's error already, and one part alone
+// left dQ and dK at 2.5e-3 to 2.7e-3 of L2, 1.6 times the rounding of the outputs
+// themselves (2.0e-3 so; 1213 us instead of 1060 for a training step of 16384
+// tokens, 16 / 4 heads of 128, window 2048).
 //
 // The first tokens that stay visible are seen by every later query.  Their
 // share beyond the reach of their own tile's window is cut into stretches of
@@ -54,6 +58,19 @@ __device__ __forceinline__ void store_rows(uint32_t t, float mul, uint8_t* mine,
         const int r = (k * 32 + lane) / kChunks, ch = (k * 32 + lane) % kChunks;
         const uint4 w = *reinterpret_cast<const uint4*>(mine + r * (D * 2) + ((ch ^ (r & 7)) * 16));
         if (r >= first && r < rows) *reinterpret_cast<uint4*>(out + r * stride + ch * 8) = w;
+    }
+}
+
+// A row's 64 values as bf16 pairs: 32 columns of the rounded values and 32 of what
+// rounding left over.
+__device__ __forceinline__ void store_split(uint32_t t, const float* x) {
+#pragma unroll
+    for (int c = 0; c < 64; c += 32) {
+        uint32_t hi[16], lo[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) tc::split_bf16x2(x[c + 2 * e], x[c + 2 * e + 1], hi[e], lo[e]);
+        tmem_st16(t + c / 2, hi);
+        tmem_st16(t + 32 + c / 2, lo);
     }
 }
 
@@ -241,6 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             tc_fence_after();
             inner(cDK, cDP, L::q + st * L::kTileBytes, i > 0);
+            inner(cDK, cDP + 32, L::q + st * L::kTileBytes, true);
             issue.commit(bar0 + 8 * (kvQFree + st));
             if (i + 1 < ns) {
                 ok = ready(kvG + nx, nph);
@@ -334,9 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int e = 0; e < 64; ++e) pr[e] = (see[e >> 5] >> (e & 31)) & 1 ? pr[e] : 0.f;
             }
-#pragma unroll
-            for (int e = 0; e < 32; ++e) pk[e] = cvt_bf16x2(pr[2 * e], pr[2 * e + 1]);
-            tmem_st32(tDP, pk);
+            store_split(tDP, pr);
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
@@ -546,6 +562,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int s = 0; s < kTile / 16; ++s)
                 if (s < steps) issue.ts(tm + cDQ, tm + cDP + 128 * st + (s >> 2) * 64 + (s & 3) * 8, k + s * 128, id_o, (j | s) != 0);
+#pragma unroll
+            for (int s = 0; s < kTile / 16; ++s)
+                if (s < steps) issue.ts(tm + cDQ, tm + cDP + 128 * st + (s >> 2) * 64 + 32 + (s & 3) * 8, k + s * 128, id_o, true);
             issue.commit(bar0 + 8 * (qKFree + st));
         }
         issue.commit(bar0 + 8 * qDone);
@@ -571,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             const uint32_t tDP = tmem + lanes + cDP + 128 * (j & 1) + 64 * half;
             const int j0 = blk.start(j) + 64 * half, width = blk.width(j) - 64 * half;  // of this half, 0 or less: none
-            uint32_t s[64], pk[32];
+            uint32_t s[64];
             float pr[64];
             if (width > 0) tmem_ld32(tS, s);
             if (width > 32) tmem_ld32(tS + 32, s + 32);
@@ -604,9 +623,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int e = 0; e < 64; ++e) pr[e] = (see[e >> 5] >> (e & 31)) & 1 ? pr[e] : 0.f;
             }
-#pragma unroll
-            for (int e = 0; e < 32; ++e) pk[e] = cvt_bf16x2(pr[2 * e], pr[2 * e + 1]);
-            if (width > 0) tmem_st32(tDP, pk);
+            if (width > 0) store_split(tDP, pr);
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
