@@ -67,12 +67,14 @@ long long tile_slots(int B, int T, int rows, bool varlen) {
     return static_cast<long long>(B) * (T > rows ? (T + rows - 1) / rows : 1);
 }
 
-// What the backward keeps beside its outputs: delta, and the first tokens' partial sums.
+// What the backward keeps beside its outputs: delta, the first tokens' partial
+// sums, and those of heads in pieces.
 struct WindowLayout {
     int window, sinks;  // no longer than the row; no first tokens where the window leaves none out
     int far_tokens;
     long long far_slots;
-    size_t far, total;
+    int pieces;
+    size_t far, heads, total;
 };
 WindowLayout window_layout(int B, int T, int H, int Hk, int d, int window, int sinks, bool varlen) {
     WindowLayout L{};
@@ -82,7 +84,10 @@ WindowLayout window_layout(int B, int T, int H, int Hk, int d, int window, int s
     L.far_tokens = static_cast<int>(std::min<long long>(reach * gdn::kWindowTile, 1 << 30));
     L.far_slots = L.sinks > 0 ? tile_slots(B, T, L.far_tokens, varlen) : 0;
     L.far = round_up(sizeof(float) * (varlen ? 1 : B) * static_cast<size_t>(H) * T);
-    L.total = L.far + round_up(sizeof(float) * L.far_slots * Hk * 2 * L.sinks * d);
+    L.pieces = gdn::window_pieces(tile_slots(B, T, gdn::kWindowTile, varlen) + L.far_slots, H, Hk);
+    L.heads = L.far + round_up(sizeof(float) * L.far_slots * L.pieces * Hk * 2 * L.sinks * d);
+    const long long tokens = varlen ? T : static_cast<long long>(B) * T;
+    L.total = L.heads + (L.pieces > 1 ? round_up(sizeof(float) * L.pieces * tokens * Hk * 2 * d) : 0);
     return L;
 }
 
@@ -99,7 +104,7 @@ gdn_status window_args(gdn::WindowArgs& a, const WindowLayout& L, const gdn_bf16
     a.q = q; a.k = k; a.v = v; a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride;
     a.cu_seqlens = cu_seqlens; a.tokens = varlen ? T : static_cast<long long>(B) * T;
     a.nseq = B; a.T = T; a.H = H; a.Hk = Hk; a.d = d; a.window = L.window; a.sinks = L.sinks; a.scale = scale;
-    a.far_tokens = L.far_tokens; a.far_slots = L.far_slots;
+    a.far_tokens = L.far_tokens; a.far_slots = L.far_slots; a.pieces = L.pieces;
     return GDN_OK;
 }
 
@@ -198,8 +203,9 @@ gdn_status gdn_window_bwd(const gdn_bf16* q, int64_t q_stride, const gdn_bf16* k
     a.dq = dq; a.dk = dk; a.dv = dv;
     a.delta = static_cast<float*>(workspace);
     a.far_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + L.far);
+    a.head_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + L.heads);
     a.slots = tile_slots(B, T, gdn::kWindowTile, varlen);
-    return gdn::count_launch(gdn::launch_window_bwd(a, stream), L.sinks > 0 ? 4 : 3) ? GDN_OK : GDN_ERR_CUDA;
+    return gdn::count_launch(gdn::launch_window_bwd(a, stream), L.sinks > 0 || L.pieces > 1 ? 4 : 3) ? GDN_OK : GDN_ERR_CUDA;
 }
 
 gdn_status gdn_window_step(const gdn_bf16* q, int64_t q_stride, const gdn_bf16* k, int64_t k_stride, const gdn_bf16* v,

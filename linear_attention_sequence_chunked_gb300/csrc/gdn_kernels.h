@@ -566,16 +566,19 @@ struct WindowArgs {
     uint16_t* dk;
     uint16_t* dv;
     float* delta;                 // (batch rows, H, T)
-    float* far_part;              // [far_slots][Hk][2][sinks][d]: dV and dK of the first tokens
+    float* far_part;              // [far_slots][pieces][Hk][2][sinks][d]: dV and dK of the first tokens
+    float* head_part;             // [pieces][tokens][Hk][2][d], where there is more than one piece
     long long tokens, slots;      // slots: tiles of queries (backward: of keys), as find_block counts them
     long long far_slots;          // stretches of far_tokens queries, likewise
     int far_tokens;
+    int pieces;                   // of a key head's query heads, a block of the backward each
     int nseq, T, H, Hk, d;
     int window, sinks;
     float scale;
     int* err;
 };
 int window_fwd_rows(int H, int Hk);  // queries per block of the forward
+int window_pieces(long long slots, int H, int Hk);
 constexpr int kWindowTile = 128;
 constexpr int kWindowMaxSinks = 128;
 cudaError_t launch_window_fwd(const WindowArgs& a, cudaStream_t stream);

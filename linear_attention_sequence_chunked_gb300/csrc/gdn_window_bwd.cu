@@ -5,8 +5,8 @@
 //   dV = P^T dout,  dK = scale dS^T Q,  dQ = scale dS K
 //
 // in two kernels, one that owns a tile of keys and one that owns a tile of
-// queries, each of which forms S and dP for itself: seven products instead of
-// five, but every gradient is summed by one block in one order, without atomics.
+// queries, each of which forms S and dP for itself: two products more, but every
+// gradient is summed by one block in one order, without atomics.
 // All products run on the tensor cores, with operands that stay in tensor memory,
 // written over the S and dP that they come from.  P is rounded to bf16 for dV, as
 // in the forward.  dS goes in as two bf16 parts, what it rounds to and what is
@@ -17,7 +17,9 @@
 //
 // The first tokens that stay visible are seen by every later query.  Their
 // share beyond the reach of their own tile's window is cut into stretches of
-// queries, one block each, whose fp32 sums a last kernel adds in order.
+// queries, one block each, whose fp32 sums a last kernel adds in order.  So are
+// the shares of a key head's query heads where the keys alone leave SMs idle.
+#include <algorithm>
 #include <cmath>
 
 #include "gdn_launch.h"
@@ -32,8 +34,9 @@ using namespace win;
 constexpr int kThreads = 320;  // warps 0-7: elementwise work; 8: copies; 9: products
 
 // A warp's 32 rows of an accumulator (D columns), times `mul`, as bf16 rows of
-// `out`, rows `stride` elements apart, the first `rows` of them; through `mine`,
-// the warp's own shared memory.
+// `out`, rows `stride` elements apart, rows [first, rows) of them; through `mine`,
+// the warp's own shared memory, in 16-byte chunks permuted so that neither side
+// meets a bank twice.
 template <int D>
 __device__ __forceinline__ void store_rows(uint32_t t, float mul, uint8_t* mine, uint16_t* out, long long stride, int first,
                                            int rows, int lane) {
@@ -42,6 +45,7 @@ __device__ __forceinline__ void store_rows(uint32_t t, float mul, uint8_t* mine,
         uint32_t o[32];
         tmem_ld32(t + g, o);
         tmem_ld_wait();
+        after_wait32(o);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             uint32_t w[4];
@@ -133,9 +137,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // a tile of keys and the tiles of queries [qa, qb) that its block looks at:
     // those in reach of the tile's own window, or a stretch that sees only the
     // first tokens of block 0
-    const int G = p.H / p.Hk;
-    const int hk = blockIdx.x % p.Hk;
-    long long slot = blockIdx.x / p.Hk;
+    const int hk = blockIdx.x % p.Hk, piece = blockIdx.x / p.Hk % p.pieces;
+    const int H0 = p.H / p.Hk * hk;  // the first of the key head's query heads
+    const int g0 = p.H / p.Hk * piece / p.pieces, G = p.H / p.Hk * (piece + 1) / p.pieces - g0;  // this block's, from there
+    long long slot = blockIdx.x / p.Hk / p.pieces;
     const int reach = (kTile - 1 + p.window - 1) / kTile + 1;  // tiles that a tile's keys reach, its own included
     const bool far = slot >= p.slots;
     int n, b, t0, t1;
@@ -149,13 +154,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int qb = min(tiles, qa + reach), nq = qb - qa;
     const int steps = nq * G;
     const long long row0 = static_cast<long long>(b) * p.T + t0;
-    // first tokens, to be joined: where the sums of this block go
-    const int joined = j0 == 0 ? min(p.sinks, len) : 0;
+    // rows whose sums are joined by a later kernel, and where they go (row j at j
+    // times `pitch`, dV before dK `apart`): all where the heads are in pieces, else
+    // the first tokens' of block 0
+    int joined = 0;
+    long long pitch = D, apart = static_cast<long long>(p.sinks) * D;
     float* part = nullptr;
-    if (joined > 0) {
+    if (!far && p.pieces > 1) {
+        joined = min(len, j0 + kTile);
+        pitch = static_cast<long long>(p.Hk) * 2 * D;
+        apart = D;
+        part = p.head_part + ((piece * p.tokens + row0) * p.Hk + hk) * 2 * D;
+    } else if (j0 == 0 && p.sinks > 0) {
+        joined = min(p.sinks, len);
         const long long base = p.cu_seqlens ? static_cast<long long>(t0 / p.far_tokens) + n
                                             : static_cast<long long>(n) * (p.T > p.far_tokens ? (p.T + p.far_tokens - 1) / p.far_tokens : 1);
-        part = p.far_part + ((base + (far ? c : 0)) * p.Hk + hk) * 2 * p.sinks * D;
+        part = p.far_part + (((base + (far ? c : 0)) * p.pieces + piece) * p.Hk + hk) * 2 * p.sinks * D;
     }
 
     if (warp == 9) {
@@ -190,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         bool ok = true;
         for (int i = 0; i < steps && ok; ++i) {
-            const int h = hk * G + i / nq, i0 = (qa + i % nq) * kTile, st = i & 1, ph = ((i >> 1) & 1) ^ 1;
+            const int h = H0 + g0 + i / nq, i0 = (qa + i % nq) * kTile, st = i & 1, ph = ((i >> 1) & 1) ^ 1;
             const int row = static_cast<int>(row0 + i0), valid = min(kTile, len - i0);
             ok = i < 2 || __all_sync(0xffffffffu, wait(kvQFree + st, ph));
             if (ok) ok = load_tile<D>(sm + L::q + st * L::kTileBytes, &map_q, h, row, valid, bar(kvQ + st), bar(kvTail), tails, lane);
@@ -282,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const auto stat = [&](int i) {  // the tile's lse, in powers of two, and delta: one value a thread
             const int e = threadIdx.x & (kTile - 1), t = (qa + i % nq) * kTile + e;
             if (i >= steps || t >= len) return 0.f;
-            const long long o = (static_cast<long long>(b) * p.H + hk * G + i / nq) * p.T + t0 + t;
+            const long long o = (static_cast<long long>(b) * p.H + H0 + g0 + i / nq) * p.T + t0 + t;
             return half ? p.delta[o] : p.lse[o] * mix::kLog2e;
         };
         float next = stat(0);
@@ -313,6 +327,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld32(tS, s);
             tmem_ld32(tS + 32, s + 32);
             tmem_ld_wait();
+            after_wait32(s);
+            after_wait32(s + 32);
 #pragma unroll
             for (int e = 0; e < 64; e += 4) {
                 const float4 l4 = lse4[e / 4];
@@ -338,6 +354,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld32(tDP, s);
             tmem_ld32(tDP + 32, s + 32);
             tmem_ld_wait();
+            after_wait32(s);
+            after_wait32(s + 32);
 #pragma unroll
             for (int e = 0; e < 64; e += 4) {
                 const float4 d4 = del4[e / 4];
@@ -365,13 +383,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float mul = half ? p.scale : 1.f;
             const int r0 = 32 * (warp & 3);
             uint8_t* mine = sm + L::q + warp * 32 * (D * 2);
-            if (part && r0 < joined) {
-                float* to = part + static_cast<long long>(half) * p.sinks * D + static_cast<long long>(j) * D;
+            if (part && j0 + r0 < joined) {
+                float* to = part + half * apart + j * pitch;
 #pragma unroll
                 for (int g = 0; g < D; g += 32) {
                     uint32_t o[32];
                     tmem_ld32(t + g, o);
                     tmem_ld_wait();
+                    after_wait32(o);
                     if (j < joined) {
 #pragma unroll
                         for (int e = 0; e < 32; e += 4)
@@ -380,9 +399,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            if (!far)
+            if (!far && joined < j0 + kTile)
                 store_rows<D>(t, mul, mine, (half ? p.dk : p.dv) + ((row0 + j0 + r0) * p.Hk + hk) * D, static_cast<long long>(p.Hk) * D,
-                              joined - r0, min(32, len - j0 - r0), lane);
+                              joined - j0 - r0, min(32, len - j0 - r0), lane);
         }
     }
     tc_fence_before();
@@ -421,6 +440,48 @@ __global__ void __launch_bounds__(256) window_join_kernel(const WindowArgs p) {
         for (int k = 0; k < 8; ++k) s += v[k];
     }
     (which ? p.dk : p.dv)[((static_cast<long long>(b) * p.T + t0 + j) * p.Hk + hk) * p.d + d] = f32_to_bf16(s);
+}
+
+// Every row's dK and dV where the heads are in pieces: the sums of the pieces and,
+// for a first token, of its stretches, in order.  Four channels per thread.
+__global__ void __launch_bounds__(256) window_sum_kernel(const WindowArgs p) {
+    const long long id = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) * 4;
+    const long long row = static_cast<long long>(p.Hk) * 2 * p.d;
+    const long long tok = id / row;
+    if (tok >= p.tokens) return;
+    const int rest = static_cast<int>(id % row), d = rest % p.d, which = rest / p.d % 2, hk = rest / p.d / 2;
+    int n = static_cast<int>(tok / p.T), b, t0, t1;
+    if (p.cu_seqlens) {  // the last sequence that starts at or before the token
+        int end = p.nseq - 1;
+        n = 0;
+        while (n < end) {
+            const int mid = (n + end + 1) >> 1;
+            if (p.cu_seqlens[mid] <= tok)
+                n = mid;
+            else
+                end = mid - 1;
+        }
+    }
+    if (!mix::token_range(p.cu_seqlens, n, p.nseq, p.T, p.err, b, t0, t1)) return;
+    const long long j = tok - static_cast<long long>(b) * p.T - t0;
+    if (j < 0 || j >= t1 - t0) return;  // a row of no sequence
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    const auto add = [&](const float* from) {
+        const float4 v = *reinterpret_cast<const float4*>(from);
+        s.x += v.x;
+        s.y += v.y;
+        s.z += v.z;
+        s.w += v.w;
+    };
+    for (int k = 0; k < p.pieces; ++k) add(p.head_part + k * p.tokens * row + id);
+    if (j < p.sinks) {
+        const long long base = p.cu_seqlens ? static_cast<long long>(t0 / p.far_tokens) + n
+                                            : static_cast<long long>(n) * (p.T > p.far_tokens ? (p.T + p.far_tokens - 1) / p.far_tokens : 1);
+        const int parts = (t1 - t0 + p.far_tokens - 1) / p.far_tokens;
+        for (int c = 1; c < parts; ++c)
+            for (int k = 0; k < p.pieces; ++k) add(p.far_part + (((((base + c) * p.pieces + k) * p.Hk + hk) * 2 + which) * p.sinks + j) * p.d + d);
+    }
+    *reinterpret_cast<uint2*>((which ? p.dk : p.dv) + (tok * p.Hk + hk) * p.d + d) = make_uint2(cvt_bf16x2(s.x, s.y), cvt_bf16x2(s.z, s.w));
 }
 
 // ------------------------------------------------------------------ dQ
@@ -595,6 +656,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (width > 0) tmem_ld32(tS, s);
             if (width > 32) tmem_ld32(tS + 32, s + 32);
             tmem_ld_wait();
+            after_wait32(s);
+            after_wait32(s + 32);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(qRead));
@@ -613,6 +676,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (width > 0) tmem_ld32(tDP, s);
             if (width > 32) tmem_ld32(tDP + 32, s + 32);
             tmem_ld_wait();
+            after_wait32(s);
+            after_wait32(s + 32);
 #pragma unroll
             for (int e = 0; e < 64; e += 2) {
                 const mix::Two a = mix::mul2(mix::two(pr[e], pr[e + 1]),
@@ -658,8 +723,11 @@ cudaError_t launch(const WindowArgs& a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     const long long rows = a.tokens * a.H * (D / 8);
     window_delta_kernel<D><<<static_cast<unsigned>((rows + 255) / 256), 256, 0, stream>>>(a);
-    window_dkv_kernel<D><<<static_cast<unsigned>((a.slots + a.far_slots) * a.Hk), kThreads, KvSmem<D>::total, stream>>>(mq, mk, mv, mg, a);
-    if (a.sinks > 0) {
+    window_dkv_kernel<D><<<static_cast<unsigned>((a.slots + a.far_slots) * a.Hk * a.pieces), kThreads, KvSmem<D>::total, stream>>>(mq, mk, mv, mg, a);
+    if (a.pieces > 1) {
+        const long long ids = a.tokens * a.Hk * 2 * D / 4;
+        window_sum_kernel<<<static_cast<unsigned>((ids + 255) / 256), 256, 0, stream>>>(a);
+    } else if (a.sinks > 0) {
         const long long ids = static_cast<long long>(a.nseq) * a.Hk * 2 * a.sinks * D;
         window_join_kernel<<<static_cast<unsigned>((ids + 255) / 256), 256, 0, stream>>>(a);
     }
@@ -668,6 +736,18 @@ cudaError_t launch(const WindowArgs& a, cudaStream_t stream) {
 }
 
 }  // namespace
+
+// Pieces of a key head's query heads, each a block of its own: as many as find an
+// SM.  More than one costs a pass over fp32 sums and reads the keys once a piece.
+// Gradients in us, one piece and as the rule has it, of 16 query heads of 128:
+// 1 x 512 tokens, 4 key heads (16 blocks in one piece) 46.1 and 33.3; 1 x 2048, 2
+// key heads (32) 249 and 103; 1 x 4096, 2 key heads, window 1024 (64) 213 and 154,
+// where four pieces take 163.  Beyond the SMs pieces lose: 1 x 4096, 4 key heads
+// (128 blocks) 149 in one, 168 in two.
+int window_pieces(long long slots, int H, int Hk) {
+    const long long blocks = slots * Hk;
+    return static_cast<int>(std::min<long long>(H / Hk, std::max(1ll, 152 / std::max(blocks, 1ll))));
+}
 
 cudaError_t launch_window_bwd(const WindowArgs& a, cudaStream_t stream) {
     return a.d == 64 ? launch<64>(a, stream) : launch<128>(a, stream);

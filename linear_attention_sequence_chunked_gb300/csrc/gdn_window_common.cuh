@@ -178,44 +178,6 @@ __device__ __forceinline__ bool load_tile(uint8_t* tile, const CUtensorMap* map,
     return true;
 }
 
-// A warp's 32 rows of W columns of an accumulator, times `mul`, as bf16 into rows
-// of `out` (the column's place, `stride` elements apart): rows [first, rows) of
-// them.  Through `mine`, 64 W bytes of the warp's own shared memory, in 16-byte
-// chunks permuted so that neither side meets a bank twice.  Returns NaN for a row
-// with a value that is not finite, else 0.
-template <int W>
-__device__ __forceinline__ float store_columns(uint32_t t, float mul, uint8_t* mine, uint16_t* out, long long stride, int first,
-                                               int rows, int lane) {
-    constexpr int kChunks = W / 8, kMask = kChunks - 1;
-    float bad = 0.f;
-#pragma unroll
-    for (int g = 0; g < W; g += 32) {
-        uint32_t o[32];
-        tmem_ld32(t + g, o);
-        tmem_ld_wait();
-        after_wait32(o);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float u = __uint_as_float(o[8 * q + 2 * e]) * mul, v = __uint_as_float(o[8 * q + 2 * e + 1]) * mul;
-                bad = fmaf(u, 0.f, fmaf(v, 0.f, bad));
-                w[e] = cvt_bf16x2(u, v);
-            }
-            *reinterpret_cast<uint4*>(mine + lane * (W * 2) + (((g / 8 + q) ^ (lane & kMask)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-    }
-    __syncwarp();
-#pragma unroll 4
-    for (int k = 0; k < kChunks; ++k) {
-        const int r = (k * 32 + lane) / kChunks, ch = (k * 32 + lane) % kChunks;
-        const uint4 w = *reinterpret_cast<const uint4*>(mine + r * (W * 2) + ((ch ^ (r & kMask)) * 16));
-        if (r >= first && r < rows) *reinterpret_cast<uint4*>(out + r * stride + ch * 8) = w;
-    }
-    return bad;
-}
-
 // {64 channels, 1 head, `box` tokens} of (tokens, heads, d) bf16, tokens `stride`
 // elements apart: 128-byte swizzled rows.
 inline bool make_heads_map(CUtensorMap* m, const void* base, long long tokens, long long stride, int heads, int d, int box_rows) {

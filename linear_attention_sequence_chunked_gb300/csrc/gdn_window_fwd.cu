@@ -255,6 +255,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int g = 0; g < kTile; g += 32)
                     if (g < width) tmem_ld32(tS + g, s + g);
                 tmem_ld_wait();
+#pragma unroll
+                for (int g = 0; g < kTile; g += 32) after_wait32(s + g);
                 if (width < kTile || !all_seen(qx, kTile, j0, width, p.window, p.sinks)) {
 #pragma unroll
                     for (int g = 0; g < kTile; g += 32) {
@@ -280,6 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             uint32_t o[32];
                             tmem_ld32(tO + g, o);
                             tmem_ld_wait();
+                            after_wait32(o);
 #pragma unroll
                             for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
                             tmem_st32(tO + g, o);
@@ -325,6 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint32_t o[32];
                     tmem_ld32(tO + g, o);
                     tmem_ld_wait();
+                    after_wait32(o);
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         uint32_t w[4];

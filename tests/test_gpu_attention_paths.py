@@ -97,6 +97,28 @@ def test_many_ragged_sequences(n, most):
     assert gdn.gdn_get_last_device_error() == 0
 
 
+@pytest.mark.parametrize("B,T,H,Hk,d,W,S,ends", [
+    (1, 1200, 4, 2, 64, 30, 3, list(range(0, 1200, 20)) + [1200]),                                   # a block for both heads
+    (1, 900, 6, 2, 64, 40, 5, [0, 300, 301, 420, 420, 500, 557, 600, 640, 700, 760, 800, 900]),      # of three, one and two
+    (3, 900, 5, 1, 128, 100, 3, None),                                                               # of five, four pieces
+    (2, 1300, 8, 1, 64, 1300, 0, None),
+], ids=str)
+def test_gradients_of_shared_heads(B, T, H, Hk, d, W, S, ends):
+    """A key head's query heads in one block and spread over several, evenly or
+    not, with and without first tokens."""
+    rng = np.random.default_rng(B + T + H)
+    a = {n: _round(rng.standard_normal((B, T, h, d)), BF) for n, h in (("q", H), ("k", Hk), ("v", Hk), ("g", H))}
+    t = {n: _dev(x, BF) for n, x in a.items()}
+    kw = dict(window=W, sinks=S, cu_seqlens=_ints(ends))
+    out, lse = attention.window_attention_fwd(t["q"], t["k"], t["v"], save_for_backward=True, **kw)
+    r = attention.window_attention_bwd(t["q"], t["k"], t["v"], out, lse, t["g"], **kw)
+    for n, want in A.window_bwd(a["q"], a["k"], a["v"], a["g"], W, S, cu=ends).items():
+        _close(r[n], want, TOL_GRAD, n)
+    again = attention.window_attention_bwd(t["q"], t["k"], t["v"], out, lse, t["g"], **kw)
+    assert all(torch.equal(r[n], again[n]) for n in r)
+    assert gdn.gdn_get_last_device_error() == 0
+
+
 def test_malformed_offsets_are_recorded():
     """Out of order, beyond the row, not from zero: an error, and nothing outside the tensors is touched."""
     T = 300
