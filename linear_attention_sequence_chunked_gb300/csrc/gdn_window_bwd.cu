@@ -31,17 +31,21 @@ namespace {
 
 using namespace win;
 
-constexpr int kThreads = 320;  // warps 0-7: elementwise work; 8: copies; 9: products
+// Warps 0-15: elementwise work, 32 rows and a quarter of the columns each; 16:
+// copies; 17 and 18: products.  Two warps issue them, so that what waits for one
+// operand does not hold up the others.
+constexpr int kElem = 16, kCopies = kElem, kProducts = kElem + 1, kThreads = 32 * (kElem + 3);
 
-// A warp's 32 rows of an accumulator (D columns), times `mul`, as bf16 rows of
+// A warp's 32 rows of W columns of an accumulator, times `mul`, as bf16 rows of
 // `out`, rows `stride` elements apart, rows [first, rows) of them; through `mine`,
 // the warp's own shared memory, in 16-byte chunks permuted so that neither side
 // meets a bank twice.
-template <int D>
+template <int W>
 __device__ __forceinline__ void store_rows(uint32_t t, float mul, uint8_t* mine, uint16_t* out, long long stride, int first,
                                            int rows, int lane) {
+    constexpr int kChunks = W / 8, kMask = kChunks < 8 ? kChunks - 1 : 7;
 #pragma unroll
-    for (int g = 0; g < D; g += 32) {
+    for (int g = 0; g < W; g += 32) {
         uint32_t o[32];
         tmem_ld32(t + g, o);
         tmem_ld_wait();
@@ -52,30 +56,25 @@ __device__ __forceinline__ void store_rows(uint32_t t, float mul, uint8_t* mine,
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 w[e] = cvt_bf16x2(__uint_as_float(o[8 * q + 2 * e]) * mul, __uint_as_float(o[8 * q + 2 * e + 1]) * mul);
-            *reinterpret_cast<uint4*>(mine + lane * (D * 2) + (((g / 8 + q) ^ (lane & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(mine + lane * (W * 2) + (((g / 8 + q) ^ (lane & kMask)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
     }
     __syncwarp();
-    constexpr int kChunks = D / 8;
 #pragma unroll 4
     for (int k = 0; k < kChunks; ++k) {
         const int r = (k * 32 + lane) / kChunks, ch = (k * 32 + lane) % kChunks;
-        const uint4 w = *reinterpret_cast<const uint4*>(mine + r * (D * 2) + ((ch ^ (r & 7)) * 16));
+        const uint4 w = *reinterpret_cast<const uint4*>(mine + r * (W * 2) + ((ch ^ (r & kMask)) * 16));
         if (r >= first && r < rows) *reinterpret_cast<uint4*>(out + r * stride + ch * 8) = w;
     }
 }
 
-// A row's 64 values as bf16 pairs: 32 columns of the rounded values and 32 of what
+// A row's 32 values as bf16 pairs: 16 columns of the rounded values and 16 of what
 // rounding left over.
 __device__ __forceinline__ void store_split(uint32_t t, const float* x) {
+    uint32_t w[32];
 #pragma unroll
-    for (int c = 0; c < 64; c += 32) {
-        uint32_t hi[16], lo[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) tc::split_bf16x2(x[c + 2 * e], x[c + 2 * e + 1], hi[e], lo[e]);
-        tmem_st16(t + c / 2, hi);
-        tmem_st16(t + 32 + c / 2, lo);
-    }
+    for (int e = 0; e < 16; ++e) tc::split_bf16x2(x[2 * e], x[2 * e + 1], w[e], w[16 + e]);
+    tmem_st32(t, w);
 }
 
 // ------------------------------------------------------------------ delta
@@ -128,7 +127,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (blockIdx.x == 0) mix::check_offsets(p.cu_seqlens, p.nseq, p.T, p.err);
 
-    if (threadIdx.x == 256) {
+    if (threadIdx.x == 32 * kCopies) {
         tma_prefetch_desc(&map_q);
         tma_prefetch_desc(&map_k);
         tma_prefetch_desc(&map_v);
@@ -172,12 +171,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         part = p.far_part + (((base + (far ? c : 0)) * p.pieces + piece) * p.Hk + hk) * 2 * p.sinks * D;
     }
 
-    if (warp == 9) {
+    if (warp == kProducts) {
         tmem_alloc(smem_u32(tslot), 512);
         tmem_relinquish();
     }
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kvBars; ++i) mbar_init(bar(i), i == kvP || i == kvDS ? 8 : 1);
+        for (int i = 0; i < kvBars; ++i) mbar_init(bar(i), i == kvP || i == kvDS ? kElem : i == kvGFree || i == kvGFree + 1 || i == kvDone ? 2 : 1);
         fence_mbar_init();
         *stop = 0;
     }
@@ -186,14 +185,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *tslot;
     constexpr uint32_t cS = 0, cDP = 128, cDV = 256, cDK = 384;
-    const auto wait = [&](int i, int parity) {
-        if (*stop) return false;
-        if (mbar_wait(bar(i), parity)) return true;
-        *stop = 1;
-        return false;
-    };
+    const auto wait = [&](int i, int parity) { return warp_wait(bar(i), parity, stop); };
 
-    if (warp == 8) {
+    if (warp == kCopies) {
         int tails = 0, lq = 0, lg = 0;
         if (lane == 0) {
             mbar_arrive_expect_tx(bar(kvIn), 2 * L::kTileBytes);
@@ -206,11 +200,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < steps && ok; ++i) {
             const int h = H0 + g0 + i / nq, i0 = (qa + i % nq) * kTile, st = i & 1, ph = ((i >> 1) & 1) ^ 1;
             const int row = static_cast<int>(row0 + i0), valid = min(kTile, len - i0);
-            ok = i < 2 || __all_sync(0xffffffffu, wait(kvQFree + st, ph));
+            ok = i < 2 || wait(kvQFree + st, ph);
             if (ok) ok = load_tile<D>(sm + L::q + st * L::kTileBytes, &map_q, h, row, valid, bar(kvQ + st), bar(kvTail), tails, lane);
             if (!ok) break;
             lq = i + 1;
-            ok = i < 2 || __all_sync(0xffffffffu, wait(kvGFree + st, ph));
+            ok = i < 2 || wait(kvGFree + st, ph);
             if (ok) ok = load_tile<D>(sm + L::g + st * L::kTileBytes, &map_g, h, row, valid, bar(kvG + st), bar(kvTail), tails, lane);
             if (!ok) break;
             lg = i + 1;
@@ -221,11 +215,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = max(0, lq - 2); i < lq; ++i) mbar_wait(bar(kvQ + (i & 1)), (i >> 1) & 1);
         for (int i = max(0, lg - 2); i < lg; ++i) mbar_wait(bar(kvG + (i & 1)), (i >> 1) & 1);
         __syncwarp();
-    } else if (warp == 9) {
+    } else if (warp >= kProducts) {
         const Issuer issue;
         const uint32_t base = uniform(smem_u32(sm)), tm = uniform(tmem), bar0 = base + L::bars;
         const int ns = uniform(steps);
-        const auto ready = [&](int i, int parity) { return __all_sync(0xffffffffu, wait(i, parity)) != 0; };
         constexpr uint32_t id_s = idesc(kFmtBf16, 0, 0, 128, kTile), id_o = idesc(kFmtBf16, 0, 1, 128, D);
         // D[tmem] = rows (K-major) of `a` times rows of `b`
         const auto outer = [&](uint32_t d, uint32_t a, uint32_t b) {
@@ -236,50 +229,42 @@ __global__ void __launch_bounds__(kThreads, 1)
                 issue.ss(tm + d, da + o, db + o, id_s, s > 0);
             }
         };
-        // D[tmem] += bf16 pairs at `a` (two halves of 32 columns, 64 apart) times rows of `b`
+        // D[tmem] += bf16 pairs at `a` (four times 16 columns, 32 apart) times rows of `b`
         const auto inner = [&](uint32_t d, uint32_t a, uint32_t b, bool more) {
             const uint64_t db = desc_sw128(base + b, kSlab, 1024);
 #pragma unroll
-            for (int s = 0; s < kTile / 16; ++s) issue.ts(tm + d, tm + a + (s >> 2) * 64 + (s & 3) * 8, db + s * 128, id_o, more || s > 0);
+            for (int s = 0; s < kTile / 16; ++s) issue.ts(tm + d, tm + a + (s >> 1) * 32 + (s & 1) * 8, db + s * 128, id_o, more || s > 0);
         };
-        bool ok = ready(kvIn, 0) && ready(kvQ, 0);
-        if (ok) {
-            tc_fence_after();
-            outer(cS, L::k, L::q);
-            issue.commit(bar0 + 8 * kvS);
-            ok = ready(kvG, 0);
-        }
-        if (ok) {
-            tc_fence_after();
-            outer(cDP, L::v, L::g);
-            issue.commit(bar0 + 8 * kvDP);
-        }
-        for (int i = 0; i < ns && ok; ++i) {
-            const int st = i & 1, nx = (i + 1) & 1, nph = ((i + 1) >> 1) & 1;
-            ok = ready(kvP, i & 1);
-            if (!ok) break;
-            tc_fence_after();
-            inner(cDV, cS, L::g + st * L::kTileBytes, i > 0);
-            issue.commit(bar0 + 8 * (kvGFree + st));
-            if (i + 1 < ns) {
-                ok = ready(kvQ + nx, nph);
+        bool ok = wait(kvIn, 0);
+        if (warp == kProducts) {  // S, and dV from P, which lies over it
+            for (int i = 0; i < ns && ok; ++i) {
+                const int st = i & 1, ph = (i >> 1) & 1;
+                ok = wait(kvQ + st, ph);
                 if (!ok) break;
                 tc_fence_after();
-                outer(cS, L::k, L::q + nx * L::kTileBytes);
+                outer(cS, L::k, L::q + st * L::kTileBytes);
                 issue.commit(bar0 + 8 * kvS);
-            }
-            ok = ready(kvDS, i & 1);
-            if (!ok) break;
-            tc_fence_after();
-            inner(cDK, cDP, L::q + st * L::kTileBytes, i > 0);
-            inner(cDK, cDP + 32, L::q + st * L::kTileBytes, true);
-            issue.commit(bar0 + 8 * (kvQFree + st));
-            if (i + 1 < ns) {
-                ok = ready(kvG + nx, nph);
+                ok = wait(kvG + st, ph) && wait(kvP, i & 1);
                 if (!ok) break;
                 tc_fence_after();
-                outer(cDP, L::v, L::g + nx * L::kTileBytes);
+                inner(cDV, cS, L::g + st * L::kTileBytes, i > 0);
+                issue.commit(bar0 + 8 * (kvGFree + st));
+            }
+        } else {  // dP, and dK from dS, which lies over it
+            for (int i = 0; i < ns && ok; ++i) {
+                const int st = i & 1;
+                ok = wait(kvG + st, (i >> 1) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                outer(cDP, L::v, L::g + st * L::kTileBytes);
                 issue.commit(bar0 + 8 * kvDP);
+                issue.commit(bar0 + 8 * (kvGFree + st));
+                ok = wait(kvDS, i & 1);
+                if (!ok) break;
+                tc_fence_after();
+                inner(cDK, cDP, L::q + st * L::kTileBytes, i > 0);
+                inner(cDK, cDP + 16, L::q + st * L::kTileBytes, true);
+                issue.commit(bar0 + 8 * (kvQFree + st));
             }
         }
         // every product has completed before the tensor memory is read or freed
@@ -287,50 +272,47 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait(bar(kvDone), 0);
         __syncwarp();
     } else {
-        const int half = warp >> 2;  // which 64 queries of the tile
+        const int quarter = warp >> 2;  // which 32 queries of the tile
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-        const uint32_t tS = tmem + lanes + cS + 64 * half, tDP = tmem + lanes + cDP + 64 * half;
+        const uint32_t tS = tmem + lanes + cS + 32 * quarter, tDP = tmem + lanes + cDP + 32 * quarter;
         const int j = j0 + 32 * (warp & 3) + lane;  // this thread's key
         const float c2 = p.scale * mix::kLog2e;
         const mix::Two cc = mix::two(c2, c2);
-        const auto stat = [&](int i) {  // the tile's lse, in powers of two, and delta: one value a thread
+        const auto stat = [&](int i) {  // the tile's lse, in powers of two, and delta: a value each of 256 threads
             const int e = threadIdx.x & (kTile - 1), t = (qa + i % nq) * kTile + e;
-            if (i >= steps || t >= len) return 0.f;
+            if (i >= steps || t >= len || quarter > 1) return 0.f;
             const long long o = (static_cast<long long>(b) * p.H + H0 + g0 + i / nq) * p.T + t0 + t;
-            return half ? p.delta[o] : p.lse[o] * mix::kLog2e;
+            return quarter ? p.delta[o] : p.lse[o] * mix::kLog2e;
         };
         float next = stat(0);
         bool ok = true;
         for (int i = 0; i < steps; ++i) {
             float* ls = stats + (i & 1) * 2 * kTile;
-            ls[threadIdx.x] = next;
-            tc::named_bar(1, 256);
+            if (quarter < 2) ls[threadIdx.x] = next;
+            tc::named_bar(1, 32 * kElem);
             next = stat(i + 1);
-            const float4* lse4 = reinterpret_cast<const float4*>(ls + 64 * half);
-            const float4* del4 = reinterpret_cast<const float4*>(ls + kTile + 64 * half);
+            const float4* lse4 = reinterpret_cast<const float4*>(ls + 32 * quarter);
+            const float4* del4 = reinterpret_cast<const float4*>(ls + kTile + 32 * quarter);
             const int i0 = (qa + i % nq) * kTile;  // the tile's first query
             // queries that see the key: from it on, up to its window's end or, a first token, the sequence's
-            uint32_t see[2] = {0xffffffffu, 0xffffffffu};
+            uint32_t see = 0xffffffffu;
             const bool masked = i0 < j0 + kTile || (i0 + kTile - 1 - j0 >= p.window) || i0 + kTile > len;
             if (masked) {
-                const int from = j - i0 - 64 * half;
-                const int to = (j < p.sinks ? len : static_cast<int>(min(static_cast<long long>(len), static_cast<long long>(j) + p.window))) - i0 - 64 * half;
+                const int from = j - i0 - 32 * quarter;
+                const int to = (j < p.sinks ? len : static_cast<int>(min(static_cast<long long>(len), static_cast<long long>(j) + p.window))) - i0 - 32 * quarter;
                 const auto below = [](int k) { return k <= 0 ? 0u : k >= 32 ? 0xffffffffu : (1u << k) - 1u; };
-#pragma unroll
-                for (int g = 0; g < 2; ++g) see[g] = below(to - 32 * g) & ~below(from - 32 * g);
+                see = below(to) & ~below(from);
             }
-            ok = ok && __all_sync(0xffffffffu, wait(kvS, i & 1));
+            ok = ok && wait(kvS, i & 1);
             if (!ok) continue;  // (the named barrier above stays in step)
             tc_fence_after();
-            uint32_t s[64], pk[32];
-            float pr[64];
+            uint32_t s[32], pk[16];
+            float pr[32];
             tmem_ld32(tS, s);
-            tmem_ld32(tS + 32, s + 32);
             tmem_ld_wait();
             after_wait32(s);
-            after_wait32(s + 32);
 #pragma unroll
-            for (int e = 0; e < 64; e += 4) {
+            for (int e = 0; e < 32; e += 4) {
                 const float4 l4 = lse4[e / 4];
                 mix::split(mix::ex2_2(mix::fma2(mix::two(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), cc, mix::two(-l4.x, -l4.y))),
                            pr[e], pr[e + 1]);
@@ -339,25 +321,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (masked) {
 #pragma unroll
-                for (int e = 0; e < 64; ++e) pr[e] = (see[e >> 5] >> (e & 31)) & 1 ? pr[e] : 0.f;
+                for (int e = 0; e < 32; ++e) pr[e] = (see >> e) & 1 ? pr[e] : 0.f;
             }
 #pragma unroll
-            for (int e = 0; e < 32; ++e) pk[e] = cvt_bf16x2(pr[2 * e], pr[2 * e + 1]);
-            tmem_st32(tS, pk);
+            for (int e = 0; e < 16; ++e) pk[e] = cvt_bf16x2(pr[2 * e], pr[2 * e + 1]);
+            tmem_st16(tS, pk);
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(kvP));
-            ok = __all_sync(0xffffffffu, wait(kvDP, i & 1));
+            ok = wait(kvDP, i & 1);
             if (!ok) continue;
             tc_fence_after();
             tmem_ld32(tDP, s);
-            tmem_ld32(tDP + 32, s + 32);
             tmem_ld_wait();
             after_wait32(s);
-            after_wait32(s + 32);
 #pragma unroll
-            for (int e = 0; e < 64; e += 4) {
+            for (int e = 0; e < 32; e += 4) {
                 const float4 d4 = del4[e / 4];
                 const mix::Two a = mix::mul2(mix::two(pr[e], pr[e + 1]),
                                              mix::add2(mix::two(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), mix::two(-d4.x, -d4.y)));
@@ -368,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (masked) {
 #pragma unroll
-                for (int e = 0; e < 64; ++e) pr[e] = (see[e >> 5] >> (e & 31)) & 1 ? pr[e] : 0.f;
+                for (int e = 0; e < 32; ++e) pr[e] = (see >> e) & 1 ? pr[e] : 0.f;
             }
             store_split(tDP, pr);
             tmem_st_wait();
@@ -376,17 +356,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(kvDS));
         }
-        if (ok && __all_sync(0xffffffffu, wait(kvDone, 0))) {
+        if (ok && wait(kvDone, 0)) {
             tc_fence_after();
-            // the first four warps store dV, the others dK
-            const uint32_t t = tmem + lanes + (half ? cDK : cDV);
-            const float mul = half ? p.scale : 1.f;
+            // the first eight warps store dV, half of the channels each, the others dK
+            constexpr int W = D / 2;
+            const int to_k = quarter >> 1, ch = (quarter & 1) * W;
+            const uint32_t t = tmem + lanes + (to_k ? cDK : cDV) + ch;
+            const float mul = to_k ? p.scale : 1.f;
             const int r0 = 32 * (warp & 3);
-            uint8_t* mine = sm + L::q + warp * 32 * (D * 2);
+            uint8_t* mine = sm + L::q + warp * 32 * (W * 2);
             if (part && j0 + r0 < joined) {
-                float* to = part + half * apart + j * pitch;
+                float* to = part + to_k * apart + j * pitch + ch;
 #pragma unroll
-                for (int g = 0; g < D; g += 32) {
+                for (int g = 0; g < W; g += 32) {
                     uint32_t o[32];
                     tmem_ld32(t + g, o);
                     tmem_ld_wait();
@@ -400,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (!far && joined < j0 + kTile)
-                store_rows<D>(t, mul, mine, (half ? p.dk : p.dv) + ((row0 + j0 + r0) * p.Hk + hk) * D, static_cast<long long>(p.Hk) * D,
+                store_rows<W>(t, mul, mine, (to_k ? p.dk : p.dv) + ((row0 + j0 + r0) * p.Hk + hk) * D + ch, static_cast<long long>(p.Hk) * D,
                               joined - j0 - r0, min(32, len - j0 - r0), lane);
         }
     }
@@ -408,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     if (*stop && threadIdx.x == 0) record_error(p.err, kErrTimeout);
-    if (warp == 9) tmem_dealloc(tmem, 512);
+    if (warp == kProducts) tmem_dealloc(tmem, 512);
 }
 
 // The first tokens' dK and dV: the sums of their stretches, in order.
@@ -486,12 +468,13 @@ __global__ void __launch_bounds__(256) window_sum_kernel(const WindowArgs p) {
 
 // ------------------------------------------------------------------ dQ
 
-enum { qIn = 0, qK = 1, qKFree = 3, qV = 5, qVFree = 7, qS = 9, qRead = 10, qDP = 11, qDS = 13, qDone = 14, qTail = 15, qBars = 16 };
+// K has three places: the next block's is loaded while dQ still reads the last one's.
+enum { qIn = 0, qK = 1, qKFree = 4, qV = 7, qVFree = 9, qS = 11, qRead = 12, qDP = 13, qDS = 15, qDone = 17, qTail = 18, qBars = 19 };
 
 template <int D>
 struct QSmem {
     static constexpr int kTileBytes = kSlab * (D / 64);
-    static constexpr int q = 0, g = kTileBytes, k = 2 * kTileBytes, v = 4 * kTileBytes, bars = 6 * kTileBytes;
+    static constexpr int q = 0, g = kTileBytes, k = 2 * kTileBytes, v = 5 * kTileBytes, bars = 7 * kTileBytes;
     static constexpr int misc = bars + qBars * 8;
     static constexpr int total = misc + 32 + 1024;
 };
@@ -509,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    if (threadIdx.x == 256) {
+    if (threadIdx.x == 32 * kCopies) {
         tma_prefetch_desc(&map_q);
         tma_prefetch_desc(&map_k);
         tma_prefetch_desc(&map_v);
@@ -528,12 +511,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int nblk = blk.count();
     const long long row0 = static_cast<long long>(b) * p.T + t0;
 
-    if (warp == 9) {
+    if (warp == kProducts) {
         tmem_alloc(smem_u32(tslot), 512);
         tmem_relinquish();
     }
     if (threadIdx.x == 0) {
-        for (int i = 0; i < qBars; ++i) mbar_init(bar(i), i == qRead || i == qDS ? 8 : 1);
+        for (int i = 0; i < qBars; ++i) mbar_init(bar(i), i == qRead || i == qDS || i == qDS + 1 ? kElem : i == qDone ? 2 : 1);
         fence_mbar_init();
         *stop = 0;
     }
@@ -542,14 +525,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *tslot;
     constexpr uint32_t cS = 0, cDP = 128, cDQ = 384;  // dP alternates between 128 and 256
-    const auto wait = [&](int i, int parity) {
-        if (*stop) return false;
-        if (mbar_wait(bar(i), parity)) return true;
-        *stop = 1;
-        return false;
-    };
+    const auto wait = [&](int i, int parity) { return warp_wait(bar(i), parity, stop); };
 
-    if (warp == 8) {
+    if (warp == kCopies) {
         int tails = 0, lk = 0, lv = 0;
         if (lane == 0) {
             mbar_arrive_expect_tx(bar(qIn), 2 * L::kTileBytes);
@@ -562,21 +540,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j < nblk && ok; ++j) {
             const int j0 = blk.start(j), st = j & 1, ph = ((j >> 1) & 1) ^ 1;
             const int row = static_cast<int>(row0 + j0);
-            ok = j < 2 || __all_sync(0xffffffffu, wait(qKFree + st, ph));
-            if (ok) ok = load_tile<D>(sm + L::k + st * L::kTileBytes, &map_k, hk, row, min(kTile, len - j0), bar(qK + st), bar(qTail), tails, lane);
+            ok = j < 3 || wait(qKFree + j % 3, (j / 3 & 1) ^ 1);
+            if (ok) ok = load_tile<D>(sm + L::k + j % 3 * L::kTileBytes, &map_k, hk, row, min(kTile, len - j0), bar(qK + j % 3), bar(qTail), tails, lane);
             if (!ok) break;
             lk = j + 1;
-            ok = j < 2 || __all_sync(0xffffffffu, wait(qVFree + st, ph));
+            ok = j < 2 || wait(qVFree + st, ph);
             if (ok) ok = load_tile<D>(sm + L::v + st * L::kTileBytes, &map_v, hk, row, kTile, bar(qV + st), bar(qTail), tails, lane);
             if (!ok) break;
             lv = j + 1;
         }
         if (!ok) *stop = 1;
         mbar_wait(bar(qIn), 0);
-        for (int j = max(0, lk - 2); j < lk; ++j) mbar_wait(bar(qK + (j & 1)), (j >> 1) & 1);
+        for (int j = max(0, lk - 3); j < lk; ++j) mbar_wait(bar(qK + j % 3), j / 3 & 1);
         for (int j = max(0, lv - 2); j < lv; ++j) mbar_wait(bar(qV + (j & 1)), (j >> 1) & 1);
         __syncwarp();
-    } else if (warp == 9) {
+    } else if (warp >= kProducts) {
         const Issuer issue;
         const uint32_t base = uniform(smem_u32(sm)), tm = uniform(tmem), bar0 = base + L::bars;
         Blocks ub;
@@ -584,8 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ub.lo = uniform(blk.lo);
         ub.hi = uniform(blk.hi);
         const int nb = ub.count();
-        const auto ready = [&](int i, int parity) { return __all_sync(0xffffffffu, wait(i, parity)) != 0; };
-        constexpr uint32_t id_o = idesc(kFmtBf16, 0, 1, 128, D);
+                constexpr uint32_t id_o = idesc(kFmtBf16, 0, 1, 128, D);
         const auto outer = [&](uint32_t d, uint32_t a, uint32_t b, int width) {
             const uint64_t da = desc_sw128(base + a, 0, 1024), db = desc_sw128(base + b, 0, 1024);
             const uint32_t id = idesc(kFmtBf16, 0, 0, 128, width);
@@ -595,46 +572,48 @@ __global__ void __launch_bounds__(kThreads, 1)
                 issue.ss(tm + d, da + o, db + o, id, s > 0);
             }
         };
-        // S and dP of block j: while the others turn one block's into dS, the next
-        // block's are on their way
-        const auto forms = [&](int j) {
-            const int st = j & 1, ph = (j >> 1) & 1;
-            if (j > 0 && !ready(qRead, (j - 1) & 1)) return false;
-            if (!ready(qK + st, ph)) return false;
-            tc_fence_after();
-            outer(cS, L::q, L::k + st * L::kTileBytes, ub.width(j));
-            issue.commit(bar0 + 8 * qS);
-            if (!ready(qV + st, ph)) return false;
-            tc_fence_after();
-            outer(cDP + 128 * st, L::g, L::v + st * L::kTileBytes, ub.width(j));
-            issue.commit(bar0 + 8 * (qDP + st));  // (a barrier per buffer: the next block's may follow before this one is looked at)
-            issue.commit(bar0 + 8 * (qVFree + st));
-            return true;
-        };
-        bool ok = ready(qIn, 0) && forms(0);
-        for (int j = 0; j < nb && ok; ++j) {
-            const int st = j & 1;
-            if (j + 1 < nb) ok = forms(j + 1);
-            ok = ok && ready(qDS, j & 1);
-            if (!ok) break;
-            tc_fence_after();
-            const uint64_t k = desc_sw128(base + L::k + st * L::kTileBytes, kSlab, 1024);
-            const int steps = ub.width(j) / 16;
+        bool ok = wait(qIn, 0);
+        if (warp == kProducts) {
+            // S and dP: while one block's are turned into dS, the next block's are on their way
+            for (int j = 0; j < nb && ok; ++j) {
+                const int st = j & 1, ph = (j >> 1) & 1;
+                ok = (j == 0 || wait(qRead, (j - 1) & 1)) && wait(qK + j % 3, j / 3 & 1);
+                if (!ok) break;
+                tc_fence_after();
+                outer(cS, L::q, L::k + j % 3 * L::kTileBytes, ub.width(j));
+                issue.commit(bar0 + 8 * qS);
+                // (dP goes over dS of the last block but one)
+                ok = wait(qV + st, ph) && (j < 2 || wait(qKFree + (j - 2) % 3, (j - 2) / 3 & 1));
+                if (!ok) break;
+                tc_fence_after();
+                outer(cDP + 128 * st, L::g, L::v + st * L::kTileBytes, ub.width(j));
+                issue.commit(bar0 + 8 * (qDP + st));  // (a barrier per buffer, for dS too: the next block's may follow before this one is looked at)
+                issue.commit(bar0 + 8 * (qVFree + st));
+            }
+        } else {
+            for (int j = 0; j < nb && ok; ++j) {
+                const int st = j & 1;
+                ok = wait(qDS + st, (j >> 1) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t k = desc_sw128(base + L::k + j % 3 * L::kTileBytes, kSlab, 1024);
+                const int steps = ub.width(j) / 16;
 #pragma unroll
-            for (int s = 0; s < kTile / 16; ++s)
-                if (s < steps) issue.ts(tm + cDQ, tm + cDP + 128 * st + (s >> 2) * 64 + (s & 3) * 8, k + s * 128, id_o, (j | s) != 0);
+                for (int s = 0; s < kTile / 16; ++s)
+                    if (s < steps) issue.ts(tm + cDQ, tm + cDP + 128 * st + (s >> 1) * 32 + (s & 1) * 8, k + s * 128, id_o, (j | s) != 0);
 #pragma unroll
-            for (int s = 0; s < kTile / 16; ++s)
-                if (s < steps) issue.ts(tm + cDQ, tm + cDP + 128 * st + (s >> 2) * 64 + 32 + (s & 3) * 8, k + s * 128, id_o, true);
-            issue.commit(bar0 + 8 * (qKFree + st));
+                for (int s = 0; s < kTile / 16; ++s)
+                    if (s < steps) issue.ts(tm + cDQ, tm + cDP + 128 * st + (s >> 1) * 32 + 16 + (s & 1) * 8, k + s * 128, id_o, true);
+                issue.commit(bar0 + 8 * (qKFree + j % 3));
+            }
         }
         issue.commit(bar0 + 8 * qDone);
         mbar_wait(bar(qDone), 0);
         __syncwarp();
     } else {
-        const int half = warp >> 2;  // which 64 keys of the block
+        const int quarter = warp >> 2;  // which 32 keys of the block
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-        const uint32_t tS = tmem + lanes + cS + 64 * half;
+        const uint32_t tS = tmem + lanes + cS + 32 * quarter;
         const int i = q0 + 32 * (warp & 3) + lane;  // this thread's query
         const float c2 = p.scale * mix::kLog2e;
         float lse = 0.f, delta = 0.f;
@@ -646,58 +625,52 @@ __global__ void __launch_bounds__(kThreads, 1)
         const mix::Two cc = mix::two(c2, c2), ll = mix::two(-lse, -lse), dd = mix::two(-delta, -delta);
         bool ok = true;
         for (int j = 0; j < nblk; ++j) {
-            ok = __all_sync(0xffffffffu, wait(qS, j & 1));
+            ok = wait(qS, j & 1);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t tDP = tmem + lanes + cDP + 128 * (j & 1) + 64 * half;
-            const int j0 = blk.start(j) + 64 * half, width = blk.width(j) - 64 * half;  // of this half, 0 or less: none
-            uint32_t s[64];
-            float pr[64];
-            if (width > 0) tmem_ld32(tS, s);
-            if (width > 32) tmem_ld32(tS + 32, s + 32);
+            const uint32_t tDP = tmem + lanes + cDP + 128 * (j & 1) + 32 * quarter;
+            const int j0 = blk.start(j) + 32 * quarter;
+            const bool any = blk.width(j) > 32 * quarter;  // a block of first tokens may be narrower
+            uint32_t s[32];
+            float pr[32];
+            if (any) tmem_ld32(tS, s);
             tmem_ld_wait();
             after_wait32(s);
-            after_wait32(s + 32);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(qRead));
             const bool masked = blk.width(j) < kTile || !all_seen(q0, kTile, blk.start(j), kTile, p.window, p.sinks);
-            uint32_t see[2] = {0xffffffffu, 0xffffffffu};
-            if (masked) {
-                see[0] = width > 0 ? seen_bits(i, j0, p.window, p.sinks) : 0;
-                see[1] = width > 32 ? seen_bits(i, j0 + 32, p.window, p.sinks) : 0;
-            }
+            const uint32_t see = masked && any ? seen_bits(i, j0, p.window, p.sinks) : 0xffffffffu;
 #pragma unroll
-            for (int e = 0; e < 64; e += 2)
+            for (int e = 0; e < 32; e += 2)
                 mix::split(mix::ex2_2(mix::fma2(mix::two(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), cc, ll)), pr[e], pr[e + 1]);
-            ok = __all_sync(0xffffffffu, wait(qDP + (j & 1), (j >> 1) & 1));
+            ok = wait(qDP + (j & 1), (j >> 1) & 1);
             if (!ok) break;
             tc_fence_after();
-            if (width > 0) tmem_ld32(tDP, s);
-            if (width > 32) tmem_ld32(tDP + 32, s + 32);
+            if (any) tmem_ld32(tDP, s);
             tmem_ld_wait();
             after_wait32(s);
-            after_wait32(s + 32);
 #pragma unroll
-            for (int e = 0; e < 64; e += 2) {
+            for (int e = 0; e < 32; e += 2) {
                 const mix::Two a = mix::mul2(mix::two(pr[e], pr[e + 1]),
                                              mix::add2(mix::two(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), dd));
                 mix::split(a, pr[e], pr[e + 1]);
             }
             if (masked) {
 #pragma unroll
-                for (int e = 0; e < 64; ++e) pr[e] = (see[e >> 5] >> (e & 31)) & 1 ? pr[e] : 0.f;
+                for (int e = 0; e < 32; ++e) pr[e] = (see >> e) & 1 ? pr[e] : 0.f;
             }
-            if (width > 0) store_split(tDP, pr);
+            if (any) store_split(tDP, pr);
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(qDS));
+            if (lane == 0) mbar_arrive(bar(qDS + (j & 1)));
         }
-        if (ok && half == 0 && __all_sync(0xffffffffu, wait(qDone, 0))) {
+        if (ok && quarter < 2 && wait(qDone, 0)) {
             tc_fence_after();
-            const int r0 = 32 * warp;
-            store_rows<D>(tmem + lanes + cDQ, p.scale, sm + L::q + warp * 32 * (D * 2), p.dq + ((row0 + q0 + r0) * p.H + h) * D,
+            constexpr int W = D / 2;
+            const int r0 = 32 * (warp & 3), ch = quarter * W;
+            store_rows<W>(tmem + lanes + cDQ + ch, p.scale, sm + L::q + warp * 32 * (W * 2), p.dq + ((row0 + q0 + r0) * p.H + h) * D + ch,
                           static_cast<long long>(p.H) * D, 0, min(32, len - q0 - r0), lane);
         }
     }
@@ -705,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     if (*stop && threadIdx.x == 0) record_error(p.err, kErrTimeout);
-    if (warp == 9) tmem_dealloc(tmem, 512);
+    if (warp == kProducts) tmem_dealloc(tmem, 512);
 }
 
 template <int D>

@@ -55,8 +55,8 @@ struct Issuer {
     }
 };
 // The warp's value of x, which all its lanes have
-__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
-__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __reduce_or_sync(0xffffffffu, x); }
+__device__ __forceinline__ int uniform(int x) { return static_cast<int>(__reduce_or_sync(0xffffffffu, static_cast<uint32_t>(x))); }
 
 // 32 lanes x 32 bits, 32 consecutive columns per thread.
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
@@ -143,6 +143,19 @@ __device__ __forceinline__ uint32_t seen_bits(int i, int j0, int window, int sin
 // Whether every row of the tile sees every key of [j0, j0 + width).
 __device__ __forceinline__ bool all_seen(int q0, int rows, int j0, int width, int window, int sinks) {
     return j0 + width - 1 <= q0 && (q0 + rows - 1 - j0 < window || j0 + width <= sinks);
+}
+
+// A warp's wait, false where it ran out here or in another warp of the block.  Every
+// branch hangs on a vote: what follows is uniform to the compiler, as the products'
+// operands and the instructions that a whole warp issues need it, and a phase that
+// is over costs 65 clocks (200 with each lane in a loop of its own).
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* stop) {
+    for (uint32_t k = 0; k < 4000000u; ++k) {
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        if (__any_sync(0xffffffffu, *stop != 0)) return false;
+    }
+    *stop = 1;
+    return false;
 }
 
 // Zeros in the rows of a swizzled tile from `from` on: they belong to another

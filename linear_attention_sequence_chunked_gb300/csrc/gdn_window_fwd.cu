@@ -146,12 +146,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *tslot;
     // S (then P) of tile x at column 128 x, O at 256 + 128 x
-    const auto wait = [&](int i, int parity) {
-        if (*stop) return false;
-        if (mbar_wait(bar(i), parity)) return true;
-        *stop = 1;
-        return false;
-    };
+    const auto wait = [&](int i, int parity) { return warp_wait(bar(i), parity, stop); };
 
     if (warp >= 8) {
         registers_down<kRegsOther>();
@@ -169,12 +164,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < nblk; ++j) {
                 const int st = j & 1, ph = ((j >> 1) & 1) ^ 1;
                 const int row = static_cast<int>(row0 + blk.start(j));
-                ok = j < 2 || __all_sync(0xffffffffu, wait(bKFree + st, ph));
+                ok = j < 2 || wait(bKFree + st, ph);
                 // K's rows behind the sequence are masked, V's have to be zeros
                 if (ok) ok = load_tile<D>(sm + L::k + st * L::kTileBytes, &map_k, hk, row, kTile, bar(bK + st), bar(bTail), tails, lane);
                 if (!ok) break;
                 loaded_k = j + 1;
-                ok = j < 2 || __all_sync(0xffffffffu, wait(bVFree + st, ph));
+                ok = j < 2 || wait(bVFree + st, ph);
                 if (ok) ok = load_tile<D>(sm + L::v + st * L::kTileBytes, &map_v, hk, row, min(kTile, len - blk.start(j)), bar(bV + st),
                                           bar(bTail), tails, lane);
                 if (!ok) break;
@@ -194,7 +189,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             ub.lo = uniform(blk.lo);
             ub.hi = uniform(blk.hi);
             const int nb = ub.count(), tiles = uniform(second ? 2 : 1);
-            const auto ready = [&](int i, int parity) { return __all_sync(0xffffffffu, wait(i, parity)) != 0; };
             const auto scores = [&](int j, int x) {  // S of tile x with block j
                 const uint64_t q = desc_sw128(base + L::q + x * L::kTileBytes, 0, 1024), k = desc_sw128(base + L::k + (j & 1) * L::kTileBytes, 0, 1024);
                 const uint32_t id = idesc(kFmtBf16, 0, 0, 128, ub.width(j));
@@ -207,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             bool ok = true;
             for (int x = 0; x < tiles && ok; ++x) {
-                ok = ready(bQ + x, 0) && ready(bK, 0);
+                ok = wait(bQ + x, 0) && wait(bK, 0);
                 if (!ok) break;
                 tc_fence_after();
                 scores(0, x);
@@ -217,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < nb && ok; ++j) {
                 const int steps = ub.width(j) / 16;
                 for (int x = 0; x < tiles && ok; ++x) {
-                    ok = ready(bV + (j & 1), (j >> 1) & 1) && ready(bP + x, j & 1);
+                    ok = wait(bV + (j & 1), (j >> 1) & 1) && wait(bP + x, j & 1);
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t v = desc_sw128(base + L::v + (j & 1) * L::kTileBytes, kSlab, 1024);
@@ -227,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (j + 1 == nb) issue.commit(bar0 + 8 * (bO + x));
                     if (x == tiles - 1) issue.commit(bar0 + 8 * (bVFree + (j & 1)));
                     if (j + 1 < nb) {
-                        ok = ready(bK + ((j + 1) & 1), ((j + 1) >> 1) & 1);
+                        ok = wait(bK + ((j + 1) & 1), ((j + 1) >> 1) & 1);
                         if (!ok) break;
                         tc_fence_after();
                         scores(j + 1, x);
@@ -252,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float m = -INFINITY, l = 0.f;
             bool ok = true;
             for (int j = 0; j < nblk; ++j) {
-                ok = __all_sync(0xffffffffu, wait(bS + x, j & 1));
+                ok = wait(bS + x, j & 1);
                 if (!ok) break;
                 tc_fence_after();
                 const int j0 = blk.start(j), width = blk.width(j);
@@ -320,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(bP + x));
             }
-            if (ok && __all_sync(0xffffffffu, wait(bO + x, 0))) {
+            if (ok && wait(bO + x, 0)) {
                 tc_fence_after();
                 const int h = h0 + (two_heads ? x : 0);
                 const float r = 1.f / l;
