@@ -210,8 +210,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             constexpr uint32_t id_o = idesc(kFmtBf16, 0, 1, 128, D);
             for (int j = 0; j < nb && ok; ++j) {
                 const int steps = ub.width(j) / 16;
+                // the copies first: they were there before P
+                ok = wait(bV + (j & 1), (j >> 1) & 1) && (j + 1 == nb || wait(bK + ((j + 1) & 1), ((j + 1) >> 1) & 1));
                 for (int x = 0; x < tiles && ok; ++x) {
-                    ok = wait(bV + (j & 1), (j >> 1) & 1) && wait(bP + x, j & 1);
+                    ok = wait(bP + x, j & 1);
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t v = desc_sw128(base + L::v + (j & 1) * L::kTileBytes, kSlab, 1024);
@@ -219,14 +221,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int s = 0; s < kTile / 16; ++s)
                         if (s < steps) issue.ts(tm + 256 + 128 * x, tm + 128 * x + 8 * s, v + s * 128, id_o, (j | s) != 0);
                     if (j + 1 == nb) issue.commit(bar0 + 8 * (bO + x));
-                    if (x == tiles - 1) issue.commit(bar0 + 8 * (bVFree + (j & 1)));
                     if (j + 1 < nb) {
-                        ok = wait(bK + ((j + 1) & 1), ((j + 1) >> 1) & 1);
-                        if (!ok) break;
-                        tc_fence_after();
                         scores(j + 1, x);
                         if (x == tiles - 1) issue.commit(bar0 + 8 * (bKFree + ((j + 1) & 1)));
                     }
+                    if (x == tiles - 1) issue.commit(bar0 + 8 * (bVFree + (j & 1)));
                 }
             }
             // every product has completed before the tensor memory is freed
