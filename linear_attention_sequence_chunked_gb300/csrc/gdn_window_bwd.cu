@@ -200,14 +200,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < steps && ok; ++i) {
             const int h = H0 + g0 + i / nq, i0 = (qa + i % nq) * kTile, st = i & 1, ph = ((i >> 1) & 1) ^ 1;
             const int row = static_cast<int>(row0 + i0), valid = min(kTile, len - i0);
-            ok = i < 2 || wait(kvQFree + st, ph);
-            if (ok) ok = load_tile<D>(sm + L::q + st * L::kTileBytes, &map_q, h, row, valid, bar(kvQ + st), bar(kvTail), tails, lane);
-            if (!ok) break;
-            lq = i + 1;
+            // (dout before Q, whose place is free later)
             ok = i < 2 || wait(kvGFree + st, ph);
             if (ok) ok = load_tile<D>(sm + L::g + st * L::kTileBytes, &map_g, h, row, valid, bar(kvG + st), bar(kvTail), tails, lane);
             if (!ok) break;
             lg = i + 1;
+            ok = i < 2 || wait(kvQFree + st, ph);
+            if (ok) ok = load_tile<D>(sm + L::q + st * L::kTileBytes, &map_q, h, row, valid, bar(kvQ + st), bar(kvTail), tails, lane);
+            if (!ok) break;
+            lq = i + 1;
         }
         if (!ok) *stop = 1;
         // every copy has landed before the block may leave
@@ -251,20 +252,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 issue.commit(bar0 + 8 * (kvGFree + st));
             }
         } else {  // dP, and dK from dS, which lies over it
-            for (int i = 0; i < ns && ok; ++i) {
-                const int st = i & 1;
-                ok = wait(kvG + st, (i >> 1) & 1);
-                if (!ok) break;
+            const auto forms = [&](int i) {
                 tc_fence_after();
-                outer(cDP, L::v, L::g + st * L::kTileBytes);
+                outer(cDP, L::v, L::g + (i & 1) * L::kTileBytes);
                 issue.commit(bar0 + 8 * kvDP);
-                issue.commit(bar0 + 8 * (kvGFree + st));
-                ok = wait(kvDS, i & 1);
+                issue.commit(bar0 + 8 * (kvGFree + (i & 1)));
+            };
+            ok = ok && wait(kvG, 0);
+            if (ok) forms(0);
+            for (int i = 0; i < ns && ok; ++i) {
+                const int st = i & 1, nx = i + 1;
+                ok = (nx == ns || wait(kvG + (nx & 1), (nx >> 1) & 1)) && wait(kvDS, i & 1);
                 if (!ok) break;
                 tc_fence_after();
                 inner(cDK, cDP, L::q + st * L::kTileBytes, i > 0);
                 inner(cDK, cDP + 16, L::q + st * L::kTileBytes, true);
                 issue.commit(bar0 + 8 * (kvQFree + st));
+                if (nx < ns) forms(nx);
             }
         }
         // every product has completed before the tensor memory is read or freed
@@ -278,22 +282,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int j = j0 + 32 * (warp & 3) + lane;  // this thread's key
         const float c2 = p.scale * mix::kLog2e;
         const mix::Two cc = mix::two(c2, c2);
-        const auto stat = [&](int i) {  // the tile's lse, in powers of two, and delta: a value each of 256 threads
-            const int e = threadIdx.x & (kTile - 1), t = (qa + i % nq) * kTile + e;
-            if (i >= steps || t >= len || quarter > 1) return 0.f;
-            const long long o = (static_cast<long long>(b) * p.H + H0 + g0 + i / nq) * p.T + t0 + t;
+        // the tile's lse, in powers of two, and delta: a value each of 256 threads
+        const auto stat = [&](int g, int x) {
+            const int t = (qa + x) * kTile + static_cast<int>(threadIdx.x & (kTile - 1));
+            if (g >= G || t >= len || quarter > 1) return 0.f;
+            const long long o = (static_cast<long long>(b) * p.H + H0 + g0 + g) * p.T + t0 + t;
             return quarter ? p.delta[o] : p.lse[o] * mix::kLog2e;
         };
-        float next = stat(0);
+        int g = 0, x = 0;  // this step's head and tile
+        float next = stat(0, 0);
+        if (quarter < 2) stats[threadIdx.x] = next;
         bool ok = true;
         for (int i = 0; i < steps; ++i) {
-            float* ls = stats + (i & 1) * 2 * kTile;
-            if (quarter < 2) ls[threadIdx.x] = next;
+            const float* ls = stats + (i & 1) * 2 * kTile;
+            const int i0 = (qa + x) * kTile;  // the tile's first query
+            if (++x == nq) x = 0, ++g;
             tc::named_bar(1, 32 * kElem);
-            next = stat(i + 1);
+            next = stat(g, x);
             const float4* lse4 = reinterpret_cast<const float4*>(ls + 32 * quarter);
             const float4* del4 = reinterpret_cast<const float4*>(ls + kTile + 32 * quarter);
-            const int i0 = (qa + i % nq) * kTile;  // the tile's first query
             // queries that see the key: from it on, up to its window's end or, a first token, the sequence's
             uint32_t see = 0xffffffffu;
             const bool masked = i0 < j0 + kTile || (i0 + kTile - 1 - j0 >= p.window) || i0 + kTile > len;
@@ -330,6 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(kvP));
+            if (quarter < 2) stats[((i + 1) & 1) * 2 * kTile + threadIdx.x] = next;
             ok = wait(kvDP, i & 1);
             if (!ok) continue;
             tc_fence_after();
@@ -577,13 +585,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             // S and dP: while one block's are turned into dS, the next block's are on their way
             for (int j = 0; j < nb && ok; ++j) {
                 const int st = j & 1, ph = (j >> 1) & 1;
-                ok = (j == 0 || wait(qRead, (j - 1) & 1)) && wait(qK + j % 3, j / 3 & 1);
+                ok = wait(qK + j % 3, j / 3 & 1) && wait(qV + st, ph) && (j == 0 || wait(qRead, (j - 1) & 1));
                 if (!ok) break;
                 tc_fence_after();
                 outer(cS, L::q, L::k + j % 3 * L::kTileBytes, ub.width(j));
                 issue.commit(bar0 + 8 * qS);
                 // (dP goes over dS of the last block but one)
-                ok = wait(qV + st, ph) && (j < 2 || wait(qKFree + (j - 2) % 3, (j - 2) / 3 & 1));
+                ok = j < 2 || wait(qKFree + (j - 2) % 3, (j - 2) / 3 & 1);
                 if (!ok) break;
                 tc_fence_after();
                 outer(cDP + 128 * st, L::g, L::v + st * L::kTileBytes, ub.width(j));
