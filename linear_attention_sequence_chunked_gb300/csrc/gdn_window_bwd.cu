@@ -12,8 +12,16 @@
 // in the forward.  dS goes in as two bf16 parts, what it rounds to and what is
 // left: it is a difference that carries delta's error already, and one part alone
 // left dQ and dK at 2.5e-3 to 2.7e-3 of L2, 1.6 times the rounding of the outputs
-// themselves (2.0e-3 so; 1213 us instead of 1060 for a training step of 16384
-// tokens, 16 / 4 heads of 128, window 2048).
+// themselves (2.0e-3 so, for two more products of nine).
+//
+// 16384 tokens, 16 / 4 heads of 128, window 2048 take 496 us for dK and dV, 357 for
+// dQ, 25 for delta and 4 for the join.  A tile of dK and dV is 2560 clocks of
+// products in some 3300: dS, dK over it, dP in its place and dS again are a chain
+// (tensor memory holds S, dP and two accumulators, no second dP), and 544 equal
+// blocks leave a tenth of the last round's SMs idle.  A tile of dQ is 2048 in some
+// 2950: dP has two places and K three, so that nothing waits but the elementwise
+// work's own chain.  With eight warps for that work, one that issues all products
+// and two places of K the two kernels took 519 and 439 us.
 //
 // The first tokens that stay visible are seen by every later query.  Their
 // share beyond the reach of their own tile's window is cut into stretches of
@@ -721,10 +729,11 @@ cudaError_t launch(const WindowArgs& a, cudaStream_t stream) {
 // Pieces of a key head's query heads, each a block of its own: as many as find an
 // SM.  More than one costs a pass over fp32 sums and reads the keys once a piece.
 // Gradients in us, one piece and as the rule has it, of 16 query heads of 128:
-// 1 x 512 tokens, 4 key heads (16 blocks in one piece) 46.1 and 33.3; 1 x 2048, 2
-// key heads (32) 249 and 103; 1 x 4096, 2 key heads, window 1024 (64) 213 and 154,
-// where four pieces take 163.  Beyond the SMs pieces lose: 1 x 4096, 4 key heads
-// (128 blocks) 149 in one, 168 in two.
+// 1 x 512 tokens, 4 key heads (16 blocks in one piece) 44 and 34; 1 x 2048, 2 key
+// heads (32) 237 and 99; 1 x 4096, 2 key heads, window 1024 (64) 195 and 144, where
+// four pieces take 155.  Beyond the SMs pieces lose: 1 x 4096, 4 key heads (128
+// blocks) 136 in one, 161 in two.  What they cost where there is little to share:
+// 1 x 128 tokens, 4 key heads 21.6 and 24.
 int window_pieces(long long slots, int H, int Hk) {
     const long long blocks = slots * Hk;
     return static_cast<int>(std::min<long long>(H / Hk, std::max(1ll, 152 / std::max(blocks, 1ll))));

@@ -14,8 +14,8 @@
 // O is rescaled only when a row's maximum has grown by more than 2^8, so most
 // blocks leave it where it is; until then P is at most 2^8.
 //
-// 4 x 4096 tokens, 16 / 4 heads of 128, window 1024 take 141 us, 858 TFLOP/s.  What
-// bounds it is one tile's chain: 128 keys of both tiles take 3430 clocks, in which
+// 4 x 4096 tokens, 16 / 4 heads of 128, window 1024 take 136 us, 890 TFLOP/s.  What
+// bounds it is one tile's chain: 128 keys of both tiles take 3300 clocks, in which
 // the products need 2048 and a warpgroup some 1700 from the scores' arrival to P's.
 // The chain cannot start on the next scores before P V is done, since P lies over
 // them: tensor memory holds two tiles' S and O and no third.
@@ -396,9 +396,10 @@ cudaError_t launch(const WindowArgs& a, cudaStream_t stream) {
 }  // namespace
 
 // Two heads read their keys once for both and end at the same one.  In us against
-// two tiles of a head: 4 x 4096 tokens, 16 / 4 heads, window 1024 138 and 152; 8 x
+// two tiles of a head: 4 x 4096 tokens, 16 / 4 heads, window 1024 134 and 148; 8 x
 // 512, 16 / 2 heads 23 and 26; one tile of 16 / 4 heads 8.2 and 7.2, where twice the
-// blocks run.
+// blocks run.  One warp issues the products of both: two that do make every product
+// of one tile wait for half of the other's (177 us instead of 138).
 int window_fwd_rows(int H, int Hk) { return (H / Hk) % 2 == 0 ? win::kTile : 2 * win::kTile; }
 
 cudaError_t launch_window_fwd(const WindowArgs& a, cudaStream_t stream) {
