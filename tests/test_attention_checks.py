@@ -331,8 +331,13 @@ def test_window_host_validation(lib):
     assert call(q=FAKE + 8) == 3 and call(v=FAKE + 2) == 3 and call(out=FAKE + 8) == 3 and call(lse=FAKE + 4) == 3 and call(cu=FAKE + 2) == 3
     # delta alone where the window is everything, the first tokens' partial sums where it is not
     size = lib.gdn_window_bwd_workspace_size
-    assert size(1, 1024, 4, 2, 64, 1024, 4, 0) == 4 * 4 * 1024 and size(1, 1024, 4, 2, 64, 100, 0, 0) == 4 * 4 * 1024
-    assert size(1, 1024, 4, 2, 64, 128, 4, 0) == 4 * 4 * 1024 + 4 * 4 * 2 * 2 * 4 * 64  # stretches of two tiles: four
+    assert size(1, 1024, 4, 4, 64, 1024, 4, 0) == 4 * 4 * 1024 and size(1, 1024, 4, 4, 64, 100, 0, 0) == 4 * 4 * 1024
+    assert size(1, 1024, 4, 4, 64, 128, 4, 0) == 4 * 4 * 1024 + 4 * 4 * 4 * 2 * 4 * 64  # stretches of two tiles: four
+    # and those of a key head's two query heads, where they go to two blocks, but not where one is enough for the GPU
+    heads = 4 * 2 * 1024 * 2 * 2 * 64
+    assert size(1, 1024, 4, 2, 64, 1024, 4, 0) == 4 * 4 * 1024 + heads and size(1, 1024, 4, 2, 64, 100, 0, 0) == 4 * 4 * 1024 + heads
+    assert size(1, 1024, 4, 2, 64, 128, 4, 0) == 4 * 4 * 1024 + 2 * 4 * 4 * 2 * 2 * 4 * 64 + heads
+    assert size(8, 1024, 4, 2, 64, 100, 0, 0) == 8 * 4 * 4 * 1024
     assert size(1, 1000, 4, 3, 64, 100, 0, 0) == 0
     need = size(1, 8, 4, 2, 64, 4, 2, 0)
 
