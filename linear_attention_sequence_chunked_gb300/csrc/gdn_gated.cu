@@ -120,31 +120,45 @@ __device__ __forceinline__ Two root_2(Two x) {
 
 // ---------------------------------------------------------------- sequences
 
+// The offsets of packed sequences, from shared memory where they fit: looked up
+// where a strip crosses one, while the whole cluster waits.
+constexpr int kOffsets = 512;
+struct Offsets {
+    const int32_t* at;
+    int nseq;
+};
+// (whole block; the copies are there after its next barrier)
+__device__ __forceinline__ Offsets offsets_of(const GatedArgs& p, int32_t* held) {
+    if (p.nseq >= kOffsets) return Offsets{p.cu_seqlens, p.nseq};
+    for (int n = threadIdx.x; n <= p.nseq; n += 32 * kWarps) held[n] = p.cu_seqlens[n];
+    return Offsets{held, p.nseq};
+}
+
 // The sequence that holds a token of the row, and its ends.
 struct Seq {
     int n, s0, s1;
 };
-__device__ __forceinline__ Seq find_seq(const GatedArgs& p, int t) {
+__device__ __forceinline__ Seq find_seq(const Offsets& p, int t) {
     int lo = 0, hi = p.nseq - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (p.cu_seqlens[mid] <= t)
+        if (p.at[mid] <= t)
             lo = mid;
         else
             hi = mid - 1;
     }
-    return Seq{lo, p.cu_seqlens[lo], p.cu_seqlens[lo + 1]};
+    return Seq{lo, p.at[lo], p.at[lo + 1]};
 }
 
 // The next and the previous sequence that has tokens (malformed offsets stay in bounds).
-__device__ __forceinline__ int next_seq(const GatedArgs& p, int n) {
+__device__ __forceinline__ int next_seq(const Offsets& p, int n) {
     do ++n;
-    while (n < p.nseq - 1 && p.cu_seqlens[n] == p.cu_seqlens[n + 1]);
+    while (n < p.nseq - 1 && p.at[n] == p.at[n + 1]);
     return min(n, p.nseq - 1);
 }
-__device__ __forceinline__ int previous_seq(const GatedArgs& p, int n) {
+__device__ __forceinline__ int previous_seq(const Offsets& p, int n) {
     do --n;
-    while (n > 0 && p.cu_seqlens[n] == p.cu_seqlens[n + 1]);
+    while (n > 0 && p.at[n] == p.at[n + 1]);
     return max(n, 0);
 }
 // Where sequences begin and end among a strip's nk tokens from t0 on, as bits, and
@@ -153,7 +167,7 @@ struct Marks {
     uint32_t starts, ends;
     int first, begun, last;
 };
-__device__ __forceinline__ Marks marks_of(const GatedArgs& p, const Seq& q, int t0, int nk) {
+__device__ __forceinline__ Marks marks_of(const Offsets& p, const Seq& q, int t0, int nk) {
     Marks m{q.s0 == t0 ? 1u : 0u, 0, q.n, q.n, q.n};
     int e = q.s1, n = q.n;
     for (int i = 0; i < nk && e > t0 && e <= t0 + nk; ++i) {
@@ -164,7 +178,7 @@ __device__ __forceinline__ Marks marks_of(const GatedArgs& p, const Seq& q, int 
         if (m.starts == 0) m.first = n;
         m.starts |= 1u << (e - t0);
         m.begun = n;
-        e = p.cu_seqlens[n + 1];
+        e = p.at[n + 1];
     }
     return m;
 }
@@ -361,9 +375,12 @@ __global__ void __launch_bounds__(32 * kWarps, 2) gated_fwd_kernel(const GatedAr
     constexpr int KS = kStripFwd, SPAN = 2 * KS;
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ Exchange sm;
+    __shared__ int32_t held[SEQS ? kOffsets : 1];
     const Place<T> w(p);
     Tiles<T, 3, SPAN>& tile = reinterpret_cast<Tiles<T, 3, SPAN>*>(smem)[w.warp];
     if (SEQS && blockIdx.x == 0 && w.row == 0) check_offsets(p.cu_seqlens, p.nseq, p.T, p.err);
+    const Offsets cu = SEQS ? offsets_of(p, held) : Offsets{nullptr, 1};
+    if (SEQS) __syncthreads();
     const float s0 = w.nd > 0 ? -p.rate * softplus(p.lam[w.d]) : 0.f, s1 = w.nd > 1 ? -p.rate * softplus(p.lam[w.d + 1]) : 0.f;
     const Two scale = two(s0, s1);
     const bool small = __all_sync(0xffffffffu, s0 >= -0.5f && s1 >= -0.5f);
@@ -376,7 +393,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) gated_fwd_kernel(const GatedAr
     if (p.final_state && w.rank == 0 && w.sub == 0) {  // sequences without tokens
         const int first = SEQS ? 0 : w.row, last = SEQS ? p.nseq : w.row + 1;
         for (int n = first + w.warp; n < last; n += kWarps) {
-            if (SEQS ? p.cu_seqlens[n] < p.cu_seqlens[n + 1] : p.T > 0) continue;
+            if (SEQS ? cu.at[n] < cu.at[n + 1] : p.T > 0) continue;
             store_state(p.final_state, n, w.D, w.d, w.nd, start_of(n));
         }
     }
@@ -398,11 +415,11 @@ __global__ void __launch_bounds__(32 * kWarps, 2) gated_fwd_kernel(const GatedAr
         const int t0 = s * SPAN + w.sub * KS;  // this lane's first token: below 2^30 + 2^13
         const int nk = max(0, min(KS, p.T - t0));
         fetch(s + step, (round + 1) & 1);
-        if (SEQS && nk > 0 && t0 >= q.s1) q = find_seq(p, t0);
+        if (SEQS && nk > 0 && t0 >= q.s1) q = find_seq(cu, t0);
         // the strip holds a sequence's end, or (packed) its beginning
         const bool ends = q.s1 <= t0 + KS || (SEQS && q.s0 == t0);
         Marks mk{0, q.s1 - 1 - t0 < KS && nk > 0 ? 1u << (q.s1 - 1 - t0) : 0u, w.row, w.row, w.row};
-        if (SEQS && ends) mk = marks_of(p, q, t0, nk);
+        if (SEQS && ends) mk = marks_of(cu, q, t0, nk);
         wait_copies<1>();
         __syncwarp();
         Two a[KS], b[KS];
@@ -435,7 +452,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) gated_fwd_kernel(const GatedAr
 #pragma unroll
                         for (int k = 0; k < KS; ++k)
                             if (k == at) b[k] = fma2(a[k], h0, b[k]);
-                        n = next_seq(p, n);
+                        n = next_seq(cu, n);
                     }
                     m.cut = mk.starts != 0;
                 }
@@ -470,7 +487,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) gated_fwd_kernel(const GatedAr
                 to += p.D;
                 if ((mk.ends >> k) & 1) {
                     if (p.final_state) store_state(p.final_state, n, w.D, w.d, w.nd, h);
-                    if (SEQS) n = next_seq(p, n);
+                    if (SEQS) n = next_seq(cu, n);
                 }
             }
         }
@@ -491,10 +508,13 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? 2 : 1) gated_bwd
     constexpr int KS = kStripBwd, SPAN = 2 * KS;
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ Exchange sm;
+    __shared__ int32_t held[SEQS ? kOffsets : 1];
     __shared__ float2 part[kWarps][32];
     const Place<T> w(p);
     Tiles<T, 4, SPAN>& tile = reinterpret_cast<Tiles<T, 4, SPAN>*>(smem)[w.warp];
     if (SEQS && blockIdx.x == 0 && w.row == 0) check_offsets(p.cu_seqlens, p.nseq, p.T, p.err);
+    const Offsets cu = SEQS ? offsets_of(p, held) : Offsets{nullptr, 1};
+    if (SEQS) __syncthreads();
     const float s0 = w.nd > 0 ? -p.rate * softplus(p.lam[w.d]) : 0.f, s1 = w.nd > 1 ? -p.rate * softplus(p.lam[w.d + 1]) : 0.f;
     const Two scale = two(s0, s1);
     const bool small = __all_sync(0xffffffffu, s0 >= -0.5f && s1 >= -0.5f);
@@ -508,7 +528,7 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? 2 : 1) gated_bwd
     if (p.d_initial_state && w.rank == 0 && w.sub == 0) {  // sequences without tokens pass the final state's gradient on
         const int first = SEQS ? 0 : w.row, last = SEQS ? p.nseq : w.row + 1;
         for (int n = first + w.warp; n < last; n += kWarps) {
-            if (SEQS ? p.cu_seqlens[n] < p.cu_seqlens[n + 1] : p.T > 0) continue;
+            if (SEQS ? cu.at[n] < cu.at[n + 1] : p.T > 0) continue;
             store_state(p.d_initial_state, n, w.D, w.d, w.nd, end_of(n));
         }
     }
@@ -534,11 +554,11 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? 2 : 1) gated_bwd
         fetch(s - step, (round + 1) & 1);
         Two h = same(0.f);
         if (nk > 0) h = load_state(p.saved, static_cast<long long>(w.row) * strips + 2 * s + w.sub, w.D, w.d, w.nd);
-        if (SEQS && nk > 0 && t0 < q.s0) q = find_seq(p, t0);
+        if (SEQS && nk > 0 && t0 < q.s0) q = find_seq(cu, t0);
         // the strip holds a sequence's beginning, or (packed) its end, or is not full
         const bool ends = q.s0 == t0 || nk < KS || (SEQS && q.s1 <= t0 + KS);
         Marks mk{t0 == 0 ? 1u : 0u, 0, w.row, w.row, w.row};
-        if (SEQS && ends) mk = marks_of(p, q, t0, nk);
+        if (SEQS && ends) mk = marks_of(cu, q, t0, nk);
         wait_copies<1>();
         __syncwarp();
         const T* v = &tile.v[round & 1][0][w.sub * KS][(w.lane & 15) * 2];
@@ -561,7 +581,7 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? 2 : 1) gated_bwd
             for (int k = 0; k < KS; ++k) {
                 if (SEQS && (mk.starts >> k) & 1) {
                     h = start_of(n);
-                    n = next_seq(p, n);
+                    n = next_seq(cu, n);
                 }
                 hp[k] = h;
                 h = fma2(a[k], h, mul2(mt[k], mul2(si[k], at(2, k))));
@@ -580,7 +600,7 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? 2 : 1) gated_bwd
                     if (k >= nk) continue;  // the row's last strip may be short: its other tokens are not there
                     if (SEQS && (mk.ends >> k) & 1) {  // nothing comes from the next sequence
                         m.H = end_of(n);
-                        n = previous_seq(p, n);
+                        n = previous_seq(cu, n);
                     }
                     m.H = mul2(a[k], add2(at(3, k), m.H));
                     m.P = mul2(m.P, a[k]);
@@ -615,12 +635,12 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? 2 : 1) gated_bwd
                     if (k >= nk) continue;
                     if (SEQS && (mk.ends >> k) & 1) {
                         c = end_of(end);
-                        end = previous_seq(p, end);
+                        end = previous_seq(cu, end);
                     }
                     token(k);
                     if ((mk.starts >> k) & 1) {
                         if (p.d_initial_state) store_state(p.d_initial_state, start, w.D, w.d, w.nd, c);
-                        if (SEQS) start = previous_seq(p, start);
+                        if (SEQS) start = previous_seq(cu, start);
                     }
                 }
             }
