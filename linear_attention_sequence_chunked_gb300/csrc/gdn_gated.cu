@@ -419,7 +419,11 @@ __global__ void __launch_bounds__(32 * kWarps, 2) gated_fwd_kernel(const GatedAr
         // the strip holds a sequence's end, or (packed) its beginning
         const bool ends = q.s1 <= t0 + KS || (SEQS && q.s0 == t0);
         Marks mk{0, q.s1 - 1 - t0 < KS && nk > 0 ? 1u << (q.s1 - 1 - t0) : 0u, w.row, w.row, w.row};
-        if (SEQS && ends) mk = marks_of(cu, q, t0, nk);
+        Two h0 = same(0.f);  // the first's initial state, on its way with the copies
+        if (SEQS && ends) {
+            mk = marks_of(cu, q, t0, nk);
+            if (mk.starts) h0 = start_of(mk.first);
+        }
         wait_copies<1>();
         __syncwarp();
         Two a[KS], b[KS];
@@ -448,11 +452,11 @@ __global__ void __launch_bounds__(32 * kWarps, 2) gated_fwd_kernel(const GatedAr
                     int n = mk.first;
                     for (uint32_t left = mk.starts; left; left &= left - 1) {
                         const int at = __ffs(left) - 1;
-                        const Two h0 = start_of(n);
 #pragma unroll
                         for (int k = 0; k < KS; ++k)
                             if (k == at) b[k] = fma2(a[k], h0, b[k]);
                         n = next_seq(cu, n);
+                        if (left & (left - 1)) h0 = start_of(n);
                     }
                     m.cut = mk.starts != 0;
                 }
