@@ -278,6 +278,9 @@ __device__ __forceinline__ Two load_state(const float* base, long long n, int D,
     const float* q = base + n * D + d;
     return two(nd > 0 ? q[0] : 0.f, nd > 1 ? q[1] : 0.f);
 }
+__device__ __forceinline__ void touch_state(const float* base, long long n, int D, int d) {
+    if (base) asm volatile("prefetch.global.L1 [%0];" ::"l"(base + n * D + d));
+}
 __device__ __forceinline__ void store_state(float* base, long long n, int D, int d, int nd, Two h) {
     float a, b;
     split(h, a, b);
@@ -562,7 +565,12 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? 2 : 1) gated_bwd
         // the strip holds a sequence's beginning, or (packed) its end, or is not full
         const bool ends = q.s0 == t0 || nk < KS || (SEQS && q.s1 <= t0 + KS);
         Marks mk{t0 == 0 ? 1u : 0u, 0, w.row, w.row, w.row};
-        if (SEQS && ends) mk = marks_of(cu, q, t0, nk);
+        if (SEQS && ends) {
+            mk = marks_of(cu, q, t0, nk);
+            // (no registers to hold them: they come as far as the cache)
+            if (mk.starts && w.nd > 0) touch_state(p.initial_state, mk.first, w.D, w.d);
+            if (mk.ends && w.nd > 0) touch_state(p.d_final_state, mk.last, w.D, w.d);
+        }
         wait_copies<1>();
         __syncwarp();
         const T* v = &tile.v[round & 1][0][w.sub * KS][(w.lane & 15) * 2];
