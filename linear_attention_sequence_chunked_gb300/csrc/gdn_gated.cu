@@ -60,11 +60,6 @@ __device__ __forceinline__ void store_remote(float4* p, uint32_t rank, float4 v)
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(a), "r"(rank));
     asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
 }
-__device__ __forceinline__ void store_remote(int* p, uint32_t rank, int v) {
-    uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p)), to;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(a), "r"(rank));
-    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to), "r"(v) : "memory");
-}
 
 // ---------------------------------------------------------------- the gates
 
@@ -196,13 +191,18 @@ __device__ __forceinline__ Two pass(const Map& m, Two h) {
 struct Exchange {
     float4 warp[2][kWarps][kChannels / 2];  // (P, H) of a channel pair: P0, P1, H0, H1
     float4 block[2][kGatedMaxCluster][kChannels / 2];
-    int cut[2][kWarps], block_cut[2][kGatedMaxCluster];
 };
-__device__ __forceinline__ Map map_of(const float4& v, int cut) { return Map{two(v.x, v.y), two(v.z, v.w), cut}; }
-__device__ __forceinline__ float4 packed(Two P, Two H) {
+// A product of decays is never negative, so P0 = -1 says that the map is cut.
+template <bool CUTS>
+__device__ __forceinline__ Map map_of(const float4& v) {
+    return Map{two(v.x, v.y), two(v.z, v.w), CUTS && v.x == -1.f};
+}
+template <bool CUTS>
+__device__ __forceinline__ float4 packed(Two P, Two H, int cut) {
     float4 v;
     split(P, v.x, v.y);
     split(H, v.z, v.w);
+    if (CUTS && cut) v.x = -1.f;
     return v;
 }
 
@@ -217,55 +217,39 @@ __device__ __forceinline__ Two exchange(Exchange& sm, int parity, int warp, int 
     far.P.v = __shfl_xor_sync(0xffffffffu, own.P.v, 16);
     far.H.v = __shfl_xor_sync(0xffffffffu, own.H.v, 16);
     far.cut = CUTS ? __shfl_xor_sync(0xffffffffu, own.cut, 16) : 0;
-    if (later == (lane >= 16)) {  // the half that stores holds the pair in order
-        if (lane < 16) sm.warp[parity][warp][pr] = packed(mul2(own.P, far.P), pass(far, own.H));
-    } else {
-        if (lane < 16) sm.warp[parity][warp][pr] = packed(mul2(own.P, far.P), pass(own, far.H));
-    }
-    bool cuts = false;  // some map of the block ignores what comes in
-    if constexpr (CUTS) {
-        if (lane == 0) sm.cut[parity][warp] = own.cut | far.cut;
-        cuts = __syncthreads_or(own.cut) != 0;
-    } else {
-        __syncthreads();
-    }
-    const auto strip = [&](int w, auto some) { return map_of(sm.warp[parity][w][pr], decltype(some)::value ? sm.cut[parity][w] : 0); };
+    if (lane < 16)  // the pair in order
+        sm.warp[parity][warp][pr] = packed<CUTS>(mul2(own.P, far.P), later ? pass(own, far.H) : pass(far, own.H), own.cut | far.cut);
+    __syncthreads();
+    const auto strip = [&](int w) { return map_of<CUTS>(sm.warp[parity][w][pr]); };
     Two mine = carry;
     if (C > 1) {
         if (threadIdx.x < 16) {  // the whole block's map
             Two P = same(1.f), H = same(0.f);
-            with_flag(cuts, [&](auto some) {
+            int cut = 0;
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    const Map m = strip(w, some);
-                    H = pass(m, H);
-                    P = mul2(P, m.P);
-                }
-            });
-            const float4 v = packed(P, H);
-            for (int c = 0; c < C; ++c) {
-                store_remote(&sm.block[parity][rank][pr], c, v);
-                if (CUTS && lane == 0) store_remote(&sm.block_cut[parity][rank], c, cuts);
+            for (int w = 0; w < kWarps; ++w) {
+                const Map m = strip(w);
+                H = pass(m, H);
+                P = mul2(P, m.P);
+                cut |= m.cut;
             }
+            const float4 v = packed<CUTS>(P, H, cut);
+            for (int c = 0; c < C; ++c) store_remote(&sm.block[parity][rank][pr], c, v);
         }
         cluster_sync();
         for (int c = 0; c < C; ++c) {
             if (c == static_cast<int>(rank)) mine = carry;
-            carry = pass(map_of(sm.block[parity][c][pr], CUTS ? sm.block_cut[parity][c] : 0), carry);
+            carry = pass(map_of<CUTS>(sm.block[parity][c][pr]), carry);
         }
-        with_flag(cuts, [&](auto some) {
 #pragma unroll
-            for (int w = 0; w < kWarps - 1; ++w)
-                if (w < warp) mine = pass(strip(w, some), mine);
-        });
+        for (int w = 0; w < kWarps - 1; ++w)
+            if (w < warp) mine = pass(strip(w), mine);
     } else {
-        with_flag(cuts, [&](auto some) {
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                if (w == warp) mine = carry;
-                carry = pass(strip(w, some), carry);
-            }
-        });
+        for (int w = 0; w < kWarps; ++w) {
+            if (w == warp) mine = carry;
+            carry = pass(strip(w), carry);
+        }
     }
     return later ? pass(far, mine) : mine;
 }
