@@ -24,7 +24,11 @@
 // where eight took 71.
 //
 // Packed sequences are one row: a sequence's first token starts from its own
-// initial state, and a strip that holds such a token ignores what comes in.
+// initial state, and a strip that holds such a token ignores what comes in.  The
+// whole cluster waits in a round in which a warp goes through such a strip with
+// its states and offsets: 1 x 16384 x 2048 bf16 take 74 us forward and 158 in
+// reverse, in 12 sequences 86 and 194, in 64 94 and 235.  (Offsets in global
+// memory: 94 and 197, 110 and 245.)
 #include <algorithm>
 #include <type_traits>
 

@@ -104,6 +104,28 @@ def test_forward_and_gradients(case, dtype):
     assert gdn.gdn_get_last_device_error() == 0
 
 
+@pytest.mark.parametrize("n", [510, 511, 512, 513, 900])
+def test_more_sequences_than_a_block_holds_offsets_of(n):
+    """Offsets in shared and in global memory, empty sequences at both ends and between."""
+    rng = np.random.default_rng(n)
+    lengths = rng.integers(0, 4, n)
+    lengths[[0, n // 2, n - 1]] = 0
+    lengths[[n // 3, n - 2]] = 90, 300
+    cu = np.concatenate([[0], np.cumsum(lengths)]).tolist()
+    case = (1, cu[-1], 36, cu, True, False)
+    a, t = _inputs(case, F32)
+    kw = dict(initial_state=t["h0"], cu_seqlens=t["cu"])
+    y, fs, saved = mixer.gated_scan_fwd(t["x"], t["r"], t["i"], t["lam"], save_for_backward=True, **kw)
+    y_ref, fs_ref = M.gated_fwd(a["x"], a["r"], a["i"], a["lam"], h0=a["h0"], cu=cu)
+    _close(y, y_ref, TOL_F32, "y")
+    _close(fs, fs_ref, TOL_F32, "final state")
+    g = mixer.gated_scan_bwd(t["x"], t["r"], t["i"], t["lam"], t["dy"], saved, d_final_state=t["dfs"], **kw)
+    ref = M.gated_bwd(a["x"], a["r"], a["i"], a["lam"], a["dy"], h0=a["h0"], cu=cu, dfs=a["dfs"])
+    for k, v in g.items():
+        _close(v, ref[k], {"dlam": TOL_PAR}.get(k, TOL_F32), k)
+    assert gdn.gdn_get_last_device_error() == 0
+
+
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("D,strided", [(64, False), (33, False), (48, True)])
 def test_steps_continue_a_prompt(dtype, D, strided):
