@@ -32,6 +32,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "gdn_cluster.cuh"
 #include "gdn_kernels.h"
 #include "gdn_launch.h"
 #include "gdn_mix_common.cuh"
@@ -47,23 +48,6 @@ constexpr int kChannels = 32;  // of a block
 // Tokens of a lane's strip: what a round costs beside its tokens' own arithmetic
 // is shared by more of them, as far as the registers go.
 constexpr int kStripFwd = 2 * kGatedStrip, kStripBwd = kGatedStrip;
-
-// ---------------------------------------------------------------- clusters
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// A store to the same shared variable of block `rank` of the cluster.
-__device__ __forceinline__ void store_remote(float4* p, uint32_t rank, float4 v) {
-    uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p)), to;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(a), "r"(rank));
-    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
-}
 
 // ---------------------------------------------------------------- the gates
 
@@ -238,9 +222,9 @@ __device__ __forceinline__ Two exchange(Exchange& sm, int parity, int warp, int 
                 cut |= m.cut;
             }
             const float4 v = packed<CUTS>(P, H, cut);
-            for (int c = 0; c < C; ++c) store_remote(&sm.block[parity][rank][pr], c, v);
+            for (int c = 0; c < C; ++c) cluster::store(&sm.block[parity][rank][pr], c, v);
         }
-        cluster_sync();
+        cluster::sync();
         for (int c = 0; c < C; ++c) {
             if (c == static_cast<int>(rank)) mine = carry;
             carry = pass(map_of<CUTS>(sm.block[parity][c][pr]), carry);
@@ -348,7 +332,7 @@ struct Place {
         sub = lane >> 4;
         C = p.cluster;
         row = blockIdx.y;
-        rank = C > 1 ? cluster_rank() : 0;
+        rank = C > 1 ? cluster::rank() : 0;
         D = p.D;
         d0 = blockIdx.x / C * kChannels;
         nc = min(kChannels, D - d0);
@@ -398,7 +382,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) gated_fwd_kernel(const GatedAr
         commit_copies();
     };
     fetch(mine0, 0);
-    if (w.C > 1) cluster_sync();  // every block of the cluster is there
+    if (w.C > 1) cluster::sync();  // every block of the cluster is there
     Two carry = SEQS ? same(0.f) : start_of(w.row);
     Seq q{w.row, 0, SEQS ? 0 : p.T};  // that of the strip's first token
     for (int b0 = 0, round = 0; b0 < spans; b0 += step, ++round) {
@@ -487,7 +471,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) gated_fwd_kernel(const GatedAr
             }
         }
     }
-    if (w.C > 1) cluster_sync();  // the others may still write here
+    if (w.C > 1) cluster::sync();  // the others may still write here
 }
 
 // ---------------------------------------------------------------- reverse mode
@@ -538,7 +522,7 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? 2 : 1) gated_bwd
         commit_copies();
     };
     fetch(spans - 1 - mine0, 0);
-    if (w.C > 1) cluster_sync();  // every block of the cluster is there
+    if (w.C > 1) cluster::sync();  // every block of the cluster is there
     Two carry = SEQS ? same(0.f) : end_of(w.row), dlam = same(0.f);
     Seq q{w.row, SEQS ? p.T : 0, p.T};  // that of the strip's first token
     for (int b0 = 0, round = 0; b0 < spans; b0 += step, ++round) {
@@ -660,7 +644,7 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? 2 : 1) gated_bwd
         }
         if (d < p.D) p.partial[(static_cast<long long>(w.row) * w.C + w.rank) * p.D + d] = -p.rate * sigmoid(p.lam[d]) * sum;
     }
-    if (w.C > 1) cluster_sync();
+    if (w.C > 1) cluster::sync();
 }
 
 // ---------------------------------------------------------------- one token

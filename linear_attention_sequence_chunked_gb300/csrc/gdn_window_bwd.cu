@@ -180,6 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 
     if (warp == kProducts) {
+        __syncwarp();  // (the checks before may have parted its lanes)
         tmem_alloc(smem_u32(tslot), 512);
         tmem_relinquish();
     }
@@ -305,6 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float* ls = stats + (i & 1) * 2 * kTile;
             const int i0 = (qa + x) * kTile;  // the tile's first query
             if (++x == nq) x = 0, ++g;
+            __syncwarp();  // (one lane arrived on the last step's barrier)
             tc::named_bar(1, 32 * kElem);
             next = stat(g, x);
             const float4* lse4 = reinterpret_cast<const float4*>(ls + 32 * quarter);
@@ -395,6 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             *reinterpret_cast<float4*>(to + g + e) = make_float4(__uint_as_float(o[e]) * mul, __uint_as_float(o[e + 1]) * mul,
                                                                                  __uint_as_float(o[e + 2]) * mul, __uint_as_float(o[e + 3]) * mul);
                     }
+                    __syncwarp();  // (the next loads take the whole warp)
                 }
             }
             if (!far && joined < j0 + kTile)
@@ -528,6 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const long long row0 = static_cast<long long>(b) * p.T + t0;
 
     if (warp == kProducts) {
+        __syncwarp();  // (the checks before may have parted its lanes)
         tmem_alloc(smem_u32(tslot), 512);
         tmem_relinquish();
     }

@@ -133,6 +133,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const long long row0 = static_cast<long long>(b) * p.T + t0;  // the sequence's first row
 
     if (warp == 9) {
+        __syncwarp();  // (the checks before may have parted its lanes)
         tmem_alloc(smem_u32(tslot), 512);
         tmem_relinquish();
     }

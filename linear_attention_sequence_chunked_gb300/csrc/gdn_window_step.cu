@@ -22,6 +22,7 @@
 #include <algorithm>
 #include <cmath>
 
+#include "gdn_cluster.cuh"
 #include "gdn_kernels.h"
 #include "gdn_launch.h"
 #include "gdn_mix_common.cuh"
@@ -49,26 +50,6 @@ __device__ __forceinline__ uint32_t pair_of(float a, float b) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
     return r;
 }
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-// Stores to the same shared variable of block `rank` of the cluster.
-__device__ __forceinline__ uint32_t remote(const void* p, uint32_t rank) {
-    uint32_t to;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(rank));
-    return to;
-}
-__device__ __forceinline__ void store_remote(float2* p, uint32_t rank, float2 v) {
-    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(remote(p, rank)), "f"(v.x), "f"(v.y) : "memory");
-}
-__device__ __forceinline__ void store_remote(float4* p, uint32_t rank, float4 v) {
-    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(remote(p, rank)), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
-}
-
 constexpr int kMaxCluster = 16;
 
 template <int D, int kWarps>
@@ -90,8 +71,8 @@ __global__ void __launch_bounds__(32 * kWarps, 12 / kWarps) window_step_kernel(c
     Joined<D, kWarps>& sm = *reinterpret_cast<Joined<D, kWarps>*>(smem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int C = p.cluster;
-    const uint32_t rank = C > 1 ? cluster_rank() : 0;
-    if (C > 1) cluster_arrive();
+    const uint32_t rank = C > 1 ? cluster::rank() : 0;
+    if (C > 1) cluster::arrive();
     const int G = p.H / p.Hk, sets = (G + 15) / 16;
     long long unit = blockIdx.x / C;
     const int set = static_cast<int>(unit % sets);
@@ -204,7 +185,7 @@ __global__ void __launch_bounds__(32 * kWarps, 12 / kWarps) window_step_kernel(c
             }
             pa[x] = pair_of(v[0], v[1]);
             pa[x + 2] = pair_of(v[2], v[3]);
-            if (f != 1.f) {
+            if (__any_sync(0xffffffffu, f != 1.f)) {  // (the products behind it take the whole warp)
 #pragma unroll
                 for (int i = 0; i < D / 8; ++i) {
                     o[i][2 * x] *= f;
@@ -261,7 +242,7 @@ __global__ void __launch_bounds__(32 * kWarps, 12 / kWarps) window_step_kernel(c
             on ? make_uint2(pair_of(o.x * inv, o.y * inv), pair_of(o.z * inv, o.w * inv)) : make_uint2(0, 0);
     };
     const int quads = heads * D / 4, share = (quads + C - 1) / C;  // of the output's 4 channels each
-    if (C > 1) cluster_wait();  // every block of the cluster is there
+    if (C > 1) cluster::wait();  // every block of the cluster is there
     for (int i = threadIdx.x; i < quads; i += 32 * kWarps) {
         const int r = i / (D / 4), d = i % (D / 4) * 4;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -277,12 +258,12 @@ __global__ void __launch_bounds__(32 * kWarps, 12 / kWarps) window_step_kernel(c
         if (C == 1)
             write(r, d, acc, sm.ml[r].y);
         else
-            store_remote(&sm.sent[rank * share + i % share], i / share, acc);
+            cluster::store(&sm.sent[rank * share + i % share], i / share, acc);
     }
     if (C == 1) return;
-    for (int i = threadIdx.x; i < 16 * C; i += 32 * kWarps) store_remote(&sm.sent_ml[rank][i % 16], i / 16, sm.ml[i % 16]);
-    cluster_arrive();
-    cluster_wait();
+    for (int i = threadIdx.x; i < 16 * C; i += 32 * kWarps) cluster::store(&sm.sent_ml[rank][i % 16], i / 16, sm.ml[i % 16]);
+    cluster::arrive();
+    cluster::wait();
     for (int i = threadIdx.x; i < share && static_cast<int>(rank) * share + i < quads; i += 32 * kWarps) {
         const int at4 = static_cast<int>(rank) * share + i, r = at4 / (D / 4), d = at4 % (D / 4) * 4;
         float mx = -INFINITY;
