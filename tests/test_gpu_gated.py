@@ -250,3 +250,58 @@ def test_runs_on_a_graph_and_another_stream():
     t["x"].copy_(t["x"].flip(1))
     graph.replay()
     assert torch.equal(yg, want) and all(torch.equal(g[k], first[k]) for k in g)
+
+
+# Strong decays, channel by channel: a relative L2 norm over a tensor is ruled by the
+# weak ones in it.  Per channel of decay L, by the roundings of an fp32 path: softplus
+# 2^-22, the gate's sigmoid 2^-21 (an exponential, a sum, a reciprocal), two products
+# 2^-23 and the change of base 1.5 x 2^-24, so L is off by 9.3e-7 of itself and a =
+# exp(L) by 9.3e-7 |L| + 2^-22.  dr, dlam and d_initial_state are products of a with
+# at most eight more factors and sums of some 2^-22 each, and L once more: 4e-6.
+DECAYS = np.array([-0.45, -0.52, -0.7, -1.0, -2.0, -4.0, -6.0, -8.0, -10.0, -12.0, -14.0, -16.0, -17.0, -18.0, -25.0, -40.0])
+
+
+def _tol_of(L):
+    return 4e-6 + 1e-6 * np.abs(L)
+
+
+def _decaying(B, T, seed):
+    """Gates about 1/2 and lam by channel, so that its L is about DECAYS."""
+    rng = np.random.default_rng(seed)
+    D = len(DECAYS)
+    lam = _round(np.log(np.expm1(-DECAYS / 4)), F32)
+    a = {k: _round(rng.standard_normal((B, T, D)), F32) for k in ("x", "i", "dy")}
+    a["r"] = _round(rng.uniform(-0.05, 0.05, (B, T, D)), F32)
+    a["h0"] = _round(rng.standard_normal((B, D)), F32)
+    gate = 1 / (1 + np.exp(-a["r"]))
+    return a, lam, -8 * np.log1p(np.exp(lam)) * gate, gate
+
+
+@pytest.mark.parametrize("T", [1, 3, 40, 700])
+def test_gradients_through_strong_decays(T):
+    a, lam, L, gate = _decaying(24, T, T)
+    t = {k: _dev(v) for k, v in a.items()}
+    args = (t["x"], t["r"], t["i"], _dev(lam))
+    _, _, saved = mixer.gated_scan_fwd(*args, initial_state=t["h0"], save_for_backward=True)
+    g = mixer.gated_scan_bwd(*args, t["dy"], saved, initial_state=t["h0"])
+    ref = M.gated_bwd(a["x"], a["r"], a["i"], lam, a["dy"], h0=a["h0"])
+    tol = _tol_of(np.abs(L).max((0, 1)))
+    for k, axes in (("dr", (0, 1)), ("d_initial_state", 0)):
+        err = np.sqrt(((_np(g[k]) - ref[k]) ** 2).sum(axes) / (ref[k] ** 2).sum(axes))
+        assert np.all(err <= tol), (k, err)
+    # dlam sums over the rows and may cancel: against the sum of its terms' sizes
+    size = (np.abs(ref["dr"] / (L * (1 - gate))) * gate).sum((0, 1)) * 8 / (1 + np.exp(-lam))
+    err = np.abs(_np(g["dlam"]) - ref["dlam"]) / size
+    assert np.all(err <= tol), err
+
+
+def test_a_state_through_strong_decays():
+    """One token without input: what is left of the state, value by value."""
+    a, lam, L, _ = _decaying(24, 1, 3)
+    t = {k: _dev(v) for k, v in a.items()}
+    want, tol = np.exp(L[:, 0]) * a["h0"], _tol_of(L[:, 0])
+    zero = torch.zeros_like(t["x"])
+    y, fs = mixer.gated_scan_fwd(zero, t["r"], t["i"], _dev(lam), initial_state=t["h0"])
+    step = mixer.gated_scan_step(zero[:, 0], t["r"][:, 0], t["i"][:, 0], _dev(lam), t["h0"].clone())
+    for got in (y[:, 0], fs, step):
+        assert np.all(np.abs(_np(got) - want) <= tol * np.abs(want))
