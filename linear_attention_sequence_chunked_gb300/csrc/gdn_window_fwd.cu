@@ -76,7 +76,7 @@ __device__ __noinline__ void one_row(const WindowArgs& p, long long row0, int i,
 #pragma unroll
         for (int x = 16; x > 0; x /= 2) s += __shfl_xor_sync(0xffffffffu, s, x);
         const float mn = s > m || s != s ? s : m;
-        const float f = m == mn ? 1.f : mix::ex2(m - mn), w = mix::ex2(s - mn);
+        const float f = m == mn ? 1.f : mix::ex2(m - mn), w = mn == -INFINITY ? 0.f : mix::ex2(s - mn);
         m = mn;
         l = fmaf(l, f, w);
         const uint16_t* v = p.v + j * p.v_stride + hk * D + lane * E;

@@ -405,3 +405,23 @@ def test_window_misaligned_slices_and_streams():
         graph.replay()
         assert torch.equal(og, want) and all(torch.equal(rg[n], grads[n]) for n in rg)
     assert gdn.gdn_get_last_device_error() == 0
+
+
+def test_a_score_of_minus_infinity_has_no_weight():
+    """A key that a token sees with a score of -inf weighs nothing, also where the
+    row is computed again because of a NaN that it does not see."""
+    case = (1, 300, 4, 2, 64, 60, 2, None)
+    a, t, kw = _window_inputs(case)
+    a["q"][..., 3] = np.abs(a["q"][..., 3]) + 0.5
+    a["q"] = _round(a["q"], BF)
+    a["k"][0, 0, :, 3] = -np.inf
+    with np.errstate(invalid="ignore"):
+        want, want_lse = A.window_fwd(a["q"], a["k"], a["v"], 60, 2)
+    assert np.isfinite(want[0, 1:]).all()
+    v = t["v"].clone()
+    v[0, 150] = float("nan")
+    out, lse = attention.window_attention_fwd(_dev(a["q"], BF), _dev(a["k"], BF), v, save_for_backward=True, **kw)
+    rows = np.r_[1:150, 210:300]  # the first token sees that key alone, and 150 to 209 the NaN
+    _close(out[0, rows], want[0, rows], TOL_BF16, "out")
+    _close(lse[0][:, rows], want_lse[0][:, rows], TOL_PAR, "lse")
+    assert torch.isnan(out[0, 0]).all()
