@@ -7,9 +7,12 @@
 // that a softmax does not care about.
 //
 // The step is bound by reading the cache once.  A warp takes 16 rows at a time
-// for up to 16 query heads of a group: S = Q K^T and O += P V are 16 x 8 x 16
-// register products (mma.sync: one query per head leaves the 128 rows of a
-// tensor-memory product empty, and nothing here waits for arithmetic).  The
+// for up to 16 query heads of a group: S = Q K^T (bf16, 16 x 8 x 16) and O += P V
+// (tf32, 16 x 8 x 8) are register products (mma.sync: one query per head leaves the
+// 128 rows of a tensor-memory product empty, and nothing here waits for arithmetic).
+// P keeps eleven bits there: as bf16 its rounding was as large as the output's own
+// (2.0e-3 of L2 together, 1.7e-3 so), and a second bf16 part, which may be zero,
+// would make a NaN of an infinite value.  The
 // channels are numbered so that both operands are what 16-byte loads of the
 // rows bring, without shared memory: in the first product a channel's place
 // does not matter as long as Q and K agree, in the second a lane's 16 bytes of V
@@ -44,6 +47,17 @@ __device__ __forceinline__ void mma_16x8x16(float* d, const uint32_t* a, uint32_
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_16x8x8(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t tf32_of(float x) {
+    uint32_t r;
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
+    return r;
 }
 __device__ __forceinline__ uint32_t pair_of(float a, float b) {
     uint32_t r;
@@ -161,7 +175,7 @@ __global__ void __launch_bounds__(32 * kWarps, 12 / kWarps) window_step_kernel(c
         }
         load_keys(s + kWarps);
         // sc[n][e]: query row g + 8 (e / 2), key r0 + 8 n + 2 t + e % 2
-        uint32_t pa[4];
+        uint32_t pa[2][4];  // P of keys 2 t and 2 t + 1, and of 8 and 9 + 2 t, as the second product's operand
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             float v[4], top = -INFINITY;
@@ -183,8 +197,8 @@ __global__ void __launch_bounds__(32 * kWarps, 12 / kWarps) window_step_kernel(c
                 v[e] = ex2(v[e] - ms);
                 l[x] += v[e];
             }
-            pa[x] = pair_of(v[0], v[1]);
-            pa[x + 2] = pair_of(v[2], v[3]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) pa[e >> 1][x + 2 * (e & 1)] = tf32_of(v[e]);
             if (__any_sync(0xffffffffu, f != 1.f)) {  // (the products behind it take the whole warp)
 #pragma unroll
                 for (int i = 0; i < D / 8; ++i) {
@@ -199,8 +213,9 @@ __global__ void __launch_bounds__(32 * kWarps, 12 / kWarps) window_step_kernel(c
                                       {vr[2][c].x, vr[2][c].y, vr[2][c].z, vr[2][c].w}, {vr[3][c].x, vr[3][c].y, vr[3][c].z, vr[3][c].w}};
 #pragma unroll
             for (int j = 0; j < 8; ++j) {  // column g is channel 64 c + 8 g + j
-                const uint32_t sel = j & 1 ? 0x7632u : 0x5410u;
-                mma_16x8x16(o[8 * c + j], pa, __byte_perm(w[0][j / 2], w[1][j / 2], sel), __byte_perm(w[2][j / 2], w[3][j / 2], sel));
+                const auto channel = [&](int n) { return j & 1 ? w[n][j / 2] & 0xffff0000u : w[n][j / 2] << 16; };
+                mma_16x8x8(o[8 * c + j], pa[0], channel(0), channel(1));
+                mma_16x8x8(o[8 * c + j], pa[1], channel(2), channel(3));
             }
         }
         load_values(s + kWarps);

@@ -425,3 +425,31 @@ def test_a_score_of_minus_infinity_has_no_weight():
     _close(out[0, rows], want[0, rows], TOL_BF16, "out")
     _close(lse[0][:, rows], want_lse[0][:, rows], TOL_PAR, "lse")
     assert torch.isnan(out[0, 0]).all()
+
+
+@pytest.mark.parametrize("case", [(8, 16, 4, 128, 1024, 4, [1100] * 8), (16, 8, 8, 64, 300, 0, [299] * 16),
+                                  (1, 40, 1, 128, 9000, 0, [9500])], ids=lambda c: "-".join(map(str, c[:6])))
+def test_a_step_is_off_by_its_outputs_rounding(case):
+    """The weights of the second product keep eleven bits or more, so beside the
+    rounding of the output there is at most 2^-11 of a weight, in random directions:
+    2^-11 / sqrt(3) x 0.72 = 2.1e-4 of L2, which adds in squares (a root mean square
+    over 5000 values and more varies by a hundredth or two)."""
+    a, t, lengths = _step_inputs(case)
+    out = attention.window_attention_step(t["q"], t["k"], t["v"], t["kc"], t["vc"], lengths, sinks=case[5])
+    ref, _, _ = A.window_step(a["q"], a["k"], a["v"], a["kc"], a["vc"], case[6], case[5])
+    rounding = metrics.rel_l2(_round(ref, BF), ref)
+    err = metrics.rel_l2(_np(out), ref)
+    assert err ** 2 <= (1.03 * rounding) ** 2 + 2.1e-4 ** 2, (err, rounding)
+
+
+def test_an_infinite_value_stays_one_in_a_step():
+    case = (2, 4, 2, 128, 50, 0, [70, 70])
+    a, t, lengths = _step_inputs(case)
+    t["vc"][0, 7, 1, 5], t["vc"][1, 9, 0, 100] = float("inf"), float("-inf")
+    out = attention.window_attention_step(t["q"], t["k"], t["v"], t["kc"], t["vc"], lengths)
+    ref, _, _ = A.window_step(a["q"], a["k"], a["v"], a["kc"], a["vc"], case[6], 0)
+    bad = np.zeros(ref.shape, bool)
+    bad[0, 2:, 5] = bad[1, :2, 100] = True
+    got = _np(out)
+    assert np.all(got[0, 2:, 5] == np.inf) and np.all(got[1, :2, 100] == -np.inf)
+    _close(np.where(bad, 0, got), np.where(bad, 0, ref), TOL_BF16, "the others")
