@@ -492,7 +492,8 @@ GDN_API gdn_status gdn_chunk_bwd_saved_wait_limit(const gdn_bf16* q, const gdn_b
  * else is dense and 16-byte aligned.  Widths and strides that 16-byte accesses
  * cannot take are read in narrower ones.  All arithmetic is fp32, rounded once
  * on output; sums run in a fixed order (no atomics).  T <= 2^30, D <= 65536,
- * B <= 65535; outputs must not overlap inputs except where said.
+ * B <= 65535 and fewer than 2^40 / D tokens: B T of them, T where packed;
+ * outputs must not overlap inputs except where said.
  * ------------------------------------------------------------------------ */
 typedef enum { GDN_BF16 = 0, GDN_F32 = 1 } gdn_dtype;
 typedef enum { GDN_ACT_NONE = 0, GDN_ACT_SILU = 1, GDN_ACT_SIGMOID = 2 } gdn_activation;
@@ -672,7 +673,7 @@ GDN_API gdn_status gdn_gated_step(const void* x, int64_t x_stride, const void* r
  *   positions (B,T) int32 or NULL: a token's place in its sequence
  *   q_out (B,T,H,d), k_out (B,T,Hk,d), dense
  *   d in {32, 64, 128, 256}; pairs a multiple of 4, at most d / 2; H, Hk <= 1024;
- *   B T < 2^31
+ *   fewer than 2^31 tokens
  * The angle is exact to about 2^-26 turns at any position: p inv_freq is formed
  * from the fp32 frequency in 64-bit fixed point.
  */
@@ -705,7 +706,7 @@ GDN_API gdn_status gdn_rope_bwd(const void* q, int64_t q_stride, const void* k, 
  *   lse       NULL, or fp32 (B,H,T) (packed: (1,H,T)): the log of the sum of
  *             exp(scale q_i . k_j) over the keys that token i sees
  *   window >= 1, scale > 0, 0 <= sinks <= 128, H a multiple of Hk, H <= 1024,
- *   d in {64, 128}, B T < 2^31 - 256
+ *   d in {64, 128}, fewer than 2^31 - 256 tokens
  * A token that another does not see has no part in that one's output, whatever
  * it holds (NaN and infinities included).
  */

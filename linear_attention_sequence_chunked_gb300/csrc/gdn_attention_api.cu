@@ -13,12 +13,12 @@ namespace {
 
 using namespace gdn::checks;
 
-gdn_status check_rope(int B, int T, int H, int Hk, int d, int pairs, int dtype) {
+gdn_status check_rope(int B, int T, int H, int Hk, int d, int pairs, int dtype, bool varlen) {
     if (H < 1 || Hk < 1 || pairs < 0) return GDN_ERR_INVALID_ARG;
     if (H > 1024 || Hk > 1024 || (d != 32 && d != 64 && d != 128 && d != 256) || pairs % 4 != 0) return GDN_ERR_UNSUPPORTED;
     if (2 * pairs > d) return GDN_ERR_INVALID_ARG;
-    GDN_TRY(check_sizes(B, T, 1, dtype));
-    if (static_cast<long long>(B) * T > INT32_MAX) return GDN_ERR_UNSUPPORTED;  // a grid's blocks
+    GDN_TRY(check_sizes(B, T, 1, dtype, varlen));
+    if (token_count(B, T, varlen) > INT32_MAX) return GDN_ERR_UNSUPPORTED;  // a grid's blocks
     return GDN_OK;
 }
 
@@ -26,9 +26,9 @@ gdn_status rope_args(gdn::RopeArgs& a, const void* q, int64_t q_stride, const vo
                      const float* q_weight, const float* k_weight, const float* inv_freq, const int32_t* positions,
                      const int32_t* cu_seqlens, int B, int T, int H, int Hk, int d, int pairs, int interleaved,
                      float eps, int dtype) {
-    GDN_TRY(check_rope(B, T, H, Hk, d, pairs, dtype));
+    GDN_TRY(check_rope(B, T, H, Hk, d, pairs, dtype, cu_seqlens != nullptr));
     if (pairs > 0 && !inv_freq) return GDN_ERR_INVALID_ARG;
-    a.tokens = cu_seqlens ? T : static_cast<long long>(B) * T;
+    a.tokens = token_count(B, T, cu_seqlens != nullptr);
     if (a.tokens > 0) {
         GDN_TRY(check_rows(q, q_stride, static_cast<int64_t>(H) * d, dtype));
         GDN_TRY(check_rows(k, k_stride, static_cast<int64_t>(Hk) * d, dtype));
@@ -45,13 +45,13 @@ gdn_status rope_args(gdn::RopeArgs& a, const void* q, int64_t q_stride, const vo
     return GDN_OK;
 }
 
-gdn_status check_window(int B, int T, int H, int Hk, int d, int window, int sinks, float scale) {
+gdn_status check_window(int B, int T, int H, int Hk, int d, int window, int sinks, float scale, bool varlen) {
     if (H < 1 || Hk < 1 || H % Hk != 0 || window < 1 || sinks < 0) return GDN_ERR_INVALID_ARG;
     if (!(scale > 0.f) || scale > 3e38f) return GDN_ERR_INVALID_ARG;
     if ((d != 64 && d != 128) || H > 1024 || sinks > gdn::kWindowMaxSinks) return GDN_ERR_UNSUPPORTED;
-    GDN_TRY(check_sizes(B, T, H * d, GDN_BF16));
+    GDN_TRY(check_sizes(B, T, H * d, GDN_BF16, varlen));
     // blocks of a grid, and the copies' row coordinates
-    const long long tokens = static_cast<long long>(B) * T;
+    const long long tokens = token_count(B, T, varlen);
     if (tokens >= (1LL << 31) - 256 || (tokens / 32 + B) * H * (d / 8) >= (1LL << 31) * 8) return GDN_ERR_UNSUPPORTED;
     return GDN_OK;
 }
@@ -86,7 +86,7 @@ WindowLayout window_layout(int B, int T, int H, int Hk, int d, int window, int s
     L.far = round_up(sizeof(float) * (varlen ? 1 : B) * static_cast<size_t>(H) * T);
     L.pieces = gdn::window_pieces(tile_slots(B, T, gdn::kWindowTile, varlen) + L.far_slots, H, Hk);
     L.heads = L.far + round_up(sizeof(float) * L.far_slots * L.pieces * Hk * 2 * L.sinks * d);
-    const long long tokens = varlen ? T : static_cast<long long>(B) * T;
+    const long long tokens = token_count(B, T, varlen);
     L.total = L.heads + (L.pieces > 1 ? round_up(sizeof(float) * L.pieces * tokens * Hk * 2 * d) : 0);
     return L;
 }
@@ -102,7 +102,7 @@ gdn_status window_args(gdn::WindowArgs& a, const WindowLayout& L, const gdn_bf16
         GDN_TRY(check_pieces(v, v_stride, static_cast<int64_t>(Hk) * d));
     }
     a.q = q; a.k = k; a.v = v; a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride;
-    a.cu_seqlens = cu_seqlens; a.tokens = varlen ? T : static_cast<long long>(B) * T;
+    a.cu_seqlens = cu_seqlens; a.tokens = token_count(B, T, varlen);
     a.nseq = B; a.T = T; a.H = H; a.Hk = Hk; a.d = d; a.window = L.window; a.sinks = L.sinks; a.scale = scale;
     a.far_tokens = L.far_tokens; a.far_slots = L.far_slots; a.pieces = L.pieces;
     return GDN_OK;
@@ -128,8 +128,8 @@ gdn_status gdn_rope_fwd(const void* q, int64_t q_stride, const void* k, int64_t 
 }
 
 size_t gdn_rope_bwd_workspace_size(int B, int T, int H, int Hk, int d, int varlen) {
-    if (check_rope(B, T, H, Hk, d, 0, 0) != GDN_OK) return 0;
-    const long long tokens = varlen ? T : static_cast<long long>(B) * T;
+    if (check_rope(B, T, H, Hk, d, 0, 0, varlen != 0) != GDN_OK) return 0;
+    const long long tokens = token_count(B, T, varlen != 0);
     return round_up(sizeof(float) * 2 * gdn::rope_blocks(tokens, std::max(H, Hk), d) * d);
 }
 
@@ -165,7 +165,7 @@ gdn_status gdn_rope_bwd(const void* q, int64_t q_stride, const void* k, int64_t 
 gdn_status gdn_window_fwd(const gdn_bf16* q, int64_t q_stride, const gdn_bf16* k, int64_t k_stride, const gdn_bf16* v,
                           int64_t v_stride, const int32_t* cu_seqlens, gdn_bf16* out, float* lse, int B, int T, int H,
                           int Hk, int d, int window, int sinks, float scale, cudaStream_t stream) {
-    GDN_TRY(check_window(B, T, H, Hk, d, window, sinks, scale));
+    GDN_TRY(check_window(B, T, H, Hk, d, window, sinks, scale, cu_seqlens != nullptr));
     gdn::WindowArgs a{};
     const bool varlen = cu_seqlens != nullptr;
     GDN_TRY(window_args(a, window_layout(B, T, H, Hk, d, window, sinks, varlen), q, q_stride, k, k_stride, v, v_stride,
@@ -180,7 +180,7 @@ gdn_status gdn_window_fwd(const gdn_bf16* q, int64_t q_stride, const gdn_bf16* k
 }
 
 size_t gdn_window_bwd_workspace_size(int B, int T, int H, int Hk, int d, int window, int sinks, int varlen) {
-    if (check_window(B, T, H, Hk, d, window, sinks, 1.f) != GDN_OK) return 0;
+    if (check_window(B, T, H, Hk, d, window, sinks, 1.f, varlen != 0) != GDN_OK) return 0;
     return window_layout(B, T, H, Hk, d, window, sinks, varlen != 0).total;
 }
 
@@ -189,7 +189,7 @@ gdn_status gdn_window_bwd(const gdn_bf16* q, int64_t q_stride, const gdn_bf16* k
                           const gdn_bf16* d_out, gdn_bf16* dq, gdn_bf16* dk, gdn_bf16* dv, int B, int T, int H, int Hk,
                           int d, int window, int sinks, float scale, void* workspace, size_t workspace_bytes,
                           cudaStream_t stream) {
-    GDN_TRY(check_window(B, T, H, Hk, d, window, sinks, scale));
+    GDN_TRY(check_window(B, T, H, Hk, d, window, sinks, scale, cu_seqlens != nullptr));
     gdn::WindowArgs a{};
     const bool varlen = cu_seqlens != nullptr;
     const WindowLayout L = window_layout(B, T, H, Hk, d, window, sinks, varlen);
@@ -212,7 +212,7 @@ gdn_status gdn_window_step(const gdn_bf16* q, int64_t q_stride, const gdn_bf16* 
                            int64_t v_stride, gdn_bf16* k_cache, gdn_bf16* v_cache, const int32_t* lengths,
                            const int32_t* slots, gdn_bf16* out, int B, int S, int H, int Hk, int d, int window,
                            int sinks, float scale, cudaStream_t stream) {
-    GDN_TRY(check_window(B, 1, H, Hk, d, window, sinks, scale));
+    GDN_TRY(check_window(B, 1, H, Hk, d, window, sinks, scale, false));
     if (window > gdn::checks::kMaxT) return GDN_ERR_UNSUPPORTED;
     if (!k_cache || !v_cache || !lengths || !out || S < 1 || (!slots && S < B)) return GDN_ERR_INVALID_ARG;
     GDN_TRY(check_pieces(q, q_stride, static_cast<int64_t>(H) * d));
@@ -234,7 +234,7 @@ gdn_status gdn_window_step(const gdn_bf16* q, int64_t q_stride, const gdn_bf16* 
 gdn_status gdn_window_fill(const gdn_bf16* k, int64_t k_stride, const gdn_bf16* v, int64_t v_stride,
                            const int32_t* cu_seqlens, const int32_t* slots, gdn_bf16* k_cache, gdn_bf16* v_cache, int B,
                            int T, int S, int Hk, int d, int window, int sinks, cudaStream_t stream) {
-    GDN_TRY(check_window(B, T, Hk, Hk, d, window, sinks, 1.f));
+    GDN_TRY(check_window(B, T, Hk, Hk, d, window, sinks, 1.f, cu_seqlens != nullptr));
     if (window > gdn::checks::kMaxT) return GDN_ERR_UNSUPPORTED;
     if (!k_cache || !v_cache || S < 1 || (!slots && S < B)) return GDN_ERR_INVALID_ARG;
     if (T > 0) {

@@ -37,11 +37,14 @@ inline gdn_status check_ws(const void* p, size_t bytes, size_t need) {
     return reinterpret_cast<uintptr_t>(p) & (kAlign - 1) ? GDN_ERR_MISALIGNED : GDN_OK;
 }
 
-inline gdn_status check_sizes(int B, int T, int D, int dtype) {
+// Tokens of a call: B rows of T, or (packed: B sequences) T in all.
+inline long long token_count(int B, int T, bool varlen) { return varlen ? T : static_cast<long long>(B) * T; }
+
+inline gdn_status check_sizes(int B, int T, int D, int dtype, bool varlen) {
     if (B < 1 || T < 0 || D < 1) return GDN_ERR_INVALID_ARG;
     if (dtype != GDN_BF16 && dtype != GDN_F32) return GDN_ERR_INVALID_ARG;
     if (B > 65535 || T > kMaxT || D > 65536) return GDN_ERR_UNSUPPORTED;
-    if (static_cast<long long>(B) * T >= (1LL << 40) / D) return GDN_ERR_UNSUPPORTED;
+    if (token_count(B, T, varlen) >= (1LL << 40) / D) return GDN_ERR_UNSUPPORTED;
     return GDN_OK;
 }
 

@@ -13,16 +13,16 @@ namespace {
 
 using namespace gdn::checks;
 
-gdn_status check_conv(int B, int T, int D, int W, int activation, int dtype) {
-    const gdn_status st = check_sizes(B, T, D, dtype);
+gdn_status check_conv(int B, int T, int D, int W, int activation, int dtype, bool varlen) {
+    const gdn_status st = check_sizes(B, T, D, dtype, varlen);
     if (st != GDN_OK) return st;
     if (W < 2 || W > 4) return GDN_ERR_UNSUPPORTED;
     if (activation != GDN_ACT_NONE && activation != GDN_ACT_SILU) return GDN_ERR_INVALID_ARG;
     return GDN_OK;
 }
 
-gdn_status check_ssm(int B, int T, int D, int G, int N, int dtype) {
-    const gdn_status st = check_sizes(B, T, D, dtype);
+gdn_status check_ssm(int B, int T, int D, int G, int N, int dtype, bool varlen) {
+    const gdn_status st = check_sizes(B, T, D, dtype, varlen);
     if (st != GDN_OK) return st;
     if (G < 1 || D % G != 0) return GDN_ERR_INVALID_ARG;
     if (N != 8 && N != 16 && N != 32 && N != 64 && N != 128) return GDN_ERR_UNSUPPORTED;
@@ -126,7 +126,7 @@ extern "C" {
 gdn_status gdn_conv_fwd(const void* x, int64_t x_stride, const float* weight, const float* bias,
                         const void* initial_state, const int32_t* cu_seqlens, void* y, void* final_state, int B, int T,
                         int D, int W, int activation, int dtype, cudaStream_t stream) {
-    GDN_TRY(check_conv(B, T, D, W, activation, dtype));
+    GDN_TRY(check_conv(B, T, D, W, activation, dtype, cu_seqlens != nullptr));
     if (!weight || (T > 0 && !y)) return GDN_ERR_INVALID_ARG;
     if (T > 0) GDN_TRY(check_rows(x, x_stride, D, dtype));
     GDN_TRY(check_dense({weight, bias, initial_state, y, final_state}));
@@ -145,7 +145,7 @@ gdn_status gdn_conv_fwd(const void* x, int64_t x_stride, const float* weight, co
 }
 
 size_t gdn_conv_bwd_workspace_size(int B, int T, int D, int W, int varlen) {
-    if (check_conv(B, T, D, W, 0, 0) != GDN_OK) return 0;
+    if (check_conv(B, T, D, W, 0, 0, varlen != 0) != GDN_OK) return 0;
     return conv_ws(B, T, D, W, varlen != 0);
 }
 
@@ -154,7 +154,7 @@ gdn_status gdn_conv_bwd(const void* x, int64_t x_stride, const float* weight, co
                         const void* d_final_state, void* dx, float* dweight, float* dbias, void* d_initial_state,
                         int B, int T, int D, int W, int activation, int dtype, void* workspace, size_t workspace_bytes,
                         cudaStream_t stream) {
-    GDN_TRY(check_conv(B, T, D, W, activation, dtype));
+    GDN_TRY(check_conv(B, T, D, W, activation, dtype, cu_seqlens != nullptr));
     if (!weight || !dweight || (T > 0 && (!d_out || !dx))) return GDN_ERR_INVALID_ARG;
     if (T > 0) GDN_TRY(check_rows(x, x_stride, D, dtype));
     GDN_TRY(check_dense({weight, bias, initial_state, d_out, d_final_state, dx, dweight, dbias, d_initial_state}));
@@ -180,7 +180,7 @@ gdn_status gdn_conv_bwd(const void* x, int64_t x_stride, const float* weight, co
 gdn_status gdn_conv_step(const void* x, int64_t x_stride, const float* weight, const float* bias, const void* state,
                          void* out_state, const int32_t* slots, void* y, int B, int S, int D, int W, int activation,
                          int dtype, cudaStream_t stream) {
-    GDN_TRY(check_conv(B, 1, D, W, activation, dtype));
+    GDN_TRY(check_conv(B, 1, D, W, activation, dtype, false));
     if (!weight || !state || !out_state || !y || S < 1 || (!slots && S < B)) return GDN_ERR_INVALID_ARG;
     GDN_TRY(check_rows(x, x_stride, D, dtype));
     GDN_TRY(check_dense({weight, bias, state, out_state, y}));
@@ -195,12 +195,12 @@ gdn_status gdn_conv_step(const void* x, int64_t x_stride, const float* weight, c
 }
 
 size_t gdn_ssm_saved_size(int B, int T, int D, int N, int varlen) {
-    if (check_ssm(B, T, D, 1, N, 0) != GDN_OK) return 0;
+    if (check_ssm(B, T, D, 1, N, 0, varlen != 0) != GDN_OK) return 0;
     return ssm_saved(B, T, D, N, varlen != 0);
 }
 
 size_t gdn_ssm_fwd_workspace_size(int B, int T, int D, int G, int N, int varlen) {
-    if (check_ssm(B, T, D, G, N, 0) != GDN_OK) return 0;
+    if (check_ssm(B, T, D, G, N, 0, varlen != 0) != GDN_OK) return 0;
     return ssm_split(B, T, D, G, N, varlen != 0, false).total;
 }
 
@@ -210,7 +210,7 @@ gdn_status gdn_ssm_fwd(const void* u, int64_t u_stride, const void* dt, int64_t 
                        const float* initial_state, const int32_t* cu_seqlens, void* out, float* final_state,
                        void* saved, size_t saved_bytes, int B, int T, int D, int G, int N, int dtype, void* workspace,
                        size_t workspace_bytes, cudaStream_t stream) {
-    GDN_TRY(check_ssm(B, T, D, G, N, dtype));
+    GDN_TRY(check_ssm(B, T, D, G, N, dtype, cu_seqlens != nullptr));
     if (!A || (T > 0 && !out)) return GDN_ERR_INVALID_ARG;
     if (T > 0) {
         GDN_TRY(check_rows(u, u_stride, D, dtype));
@@ -240,7 +240,7 @@ gdn_status gdn_ssm_fwd(const void* u, int64_t u_stride, const void* dt, int64_t 
 }
 
 size_t gdn_ssm_bwd_workspace_size(int B, int T, int D, int G, int N, int varlen) {
-    if (check_ssm(B, T, D, G, N, 0) != GDN_OK) return 0;
+    if (check_ssm(B, T, D, G, N, 0, varlen != 0) != GDN_OK) return 0;
     return ssm_bwd_layout(B, T, D, G, N, varlen != 0).total;
 }
 
@@ -251,7 +251,7 @@ gdn_status gdn_ssm_bwd(const void* u, int64_t u_stride, const void* dt, int64_t 
                        size_t saved_bytes, void* du, void* ddt, void* dz, void* dB, void* dC, float* dA, float* dD,
                        float* ddt_bias, float* d_initial_state, int B, int T, int D, int G, int N, int dtype,
                        void* workspace, size_t workspace_bytes, cudaStream_t stream) {
-    GDN_TRY(check_ssm(B, T, D, G, N, dtype));
+    GDN_TRY(check_ssm(B, T, D, G, N, dtype, cu_seqlens != nullptr));
     if (!A || !dA) return GDN_ERR_INVALID_ARG;
     if (T > 0) {
         if (!d_out || !du || !ddt || !dB || !dC || (z != nullptr) != (dz != nullptr)) return GDN_ERR_INVALID_ARG;
@@ -298,7 +298,7 @@ gdn_status gdn_ssm_step(const void* u, int64_t u_stride, const void* dt, int64_t
                         const void* z, int64_t z_stride, const float* dt_bias, int dt_softplus, const float* state,
                         float* out_state, const int32_t* slots, void* out, int B, int S, int D, int G, int N, int dtype,
                         cudaStream_t stream) {
-    GDN_TRY(check_ssm(B, 1, D, G, N, dtype));
+    GDN_TRY(check_ssm(B, 1, D, G, N, dtype, false));
     if (!A || !state || !out_state || !out || S < 1 || (!slots && S < B)) return GDN_ERR_INVALID_ARG;
     GDN_TRY(check_rows(u, u_stride, D, dtype));
     GDN_TRY(check_rows(dt, dt_stride, D, dtype));
@@ -368,7 +368,7 @@ gdn_status gdn_norm_bwd(const void* x, int64_t x_stride, const void* gate, int64
 }
 
 size_t gdn_gated_saved_size(int B, int T, int D, int varlen) {
-    if (check_sizes(B, T, D, 0) != GDN_OK) return 0;
+    if (check_sizes(B, T, D, 0, varlen != 0) != GDN_OK) return 0;
     return gated_saved(B, T, D, varlen != 0);
 }
 
@@ -376,7 +376,7 @@ gdn_status gdn_gated_fwd(const void* x, int64_t x_stride, const void* r, int64_t
                          int64_t i_stride, const float* lam, float rate, const float* initial_state,
                          const int32_t* cu_seqlens, void* y, float* final_state, void* saved, size_t saved_bytes,
                          int B, int T, int D, int dtype, cudaStream_t stream) {
-    GDN_TRY(check_sizes(B, T, D, dtype));
+    GDN_TRY(check_sizes(B, T, D, dtype, cu_seqlens != nullptr));
     if (!lam || !(rate > 0.f && rate < 3e38f) || (T > 0 && !y)) return GDN_ERR_INVALID_ARG;
     if (T > 0) {
         GDN_TRY(check_rows(x, x_stride, D, dtype));
@@ -401,7 +401,7 @@ gdn_status gdn_gated_fwd(const void* x, int64_t x_stride, const void* r, int64_t
 }
 
 size_t gdn_gated_bwd_workspace_size(int B, int T, int D, int varlen) {
-    if (check_sizes(B, T, D, 0) != GDN_OK) return 0;
+    if (check_sizes(B, T, D, 0, varlen != 0) != GDN_OK) return 0;
     return gated_ws(varlen ? 1 : B, T, D);
 }
 
@@ -410,7 +410,7 @@ gdn_status gdn_gated_bwd(const void* x, int64_t x_stride, const void* r, int64_t
                          const int32_t* cu_seqlens, const void* d_out, const float* d_final_state, const void* saved,
                          size_t saved_bytes, void* dx, void* dr, void* di, float* dlam, float* d_initial_state, int B,
                          int T, int D, int dtype, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
-    GDN_TRY(check_sizes(B, T, D, dtype));
+    GDN_TRY(check_sizes(B, T, D, dtype, cu_seqlens != nullptr));
     if (!lam || !dlam || !(rate > 0.f && rate < 3e38f)) return GDN_ERR_INVALID_ARG;
     if (T > 0) {
         if (!d_out || !dx || !dr || !di) return GDN_ERR_INVALID_ARG;
@@ -444,7 +444,7 @@ gdn_status gdn_gated_bwd(const void* x, int64_t x_stride, const void* r, int64_t
 gdn_status gdn_gated_step(const void* x, int64_t x_stride, const void* r, int64_t r_stride, const void* i,
                           int64_t i_stride, const float* lam, float rate, const float* state, float* out_state,
                           const int32_t* slots, void* y, int B, int S, int D, int dtype, cudaStream_t stream) {
-    GDN_TRY(check_sizes(B, 1, D, dtype));
+    GDN_TRY(check_sizes(B, 1, D, dtype, false));
     if (!lam || !state || !out_state || !y || !(rate > 0.f && rate < 3e38f) || S < 1 || (!slots && S < B)) return GDN_ERR_INVALID_ARG;
     GDN_TRY(check_rows(x, x_stride, D, dtype));
     GDN_TRY(check_rows(r, r_stride, D, dtype));

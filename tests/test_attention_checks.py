@@ -362,3 +362,26 @@ def test_workspaces_of_long_rows(lib):
     assert lib.gdn_gated_saved_size(1, 1 << 28, 1024, 0) == (1 << 25) * 1024 * 4
     assert lib.gdn_window_bwd_workspace_size(1, 1 << 29, 16, 1, 64, 1 << 29, 0, 0) == 4 * 16 << 29
     assert ctypes.sizeof(ctypes.c_size_t) == 8
+
+
+def test_packs_of_many_sequences(lib):
+    """A packed call has N sequences in T tokens altogether: what limits a call is T,
+    not N times T."""
+    window, rope = lib.gdn_window_bwd_workspace_size, lib.gdn_rope_bwd_workspace_size
+    for n, T in ((512, 1 << 20), (2048, 1 << 18), (4096, 1 << 17), (2048, 1 << 20), (65535, 1 << 20)):
+        assert window(n, T, 16, 4, 128, 1024, 4, 1) > 0 and rope(n, T, 16, 4, 128, 1) > 0, (n, T)
+        assert lib.gdn_gated_saved_size(n, T, 2048, 1) == T // 8 * 2048 * 4 and lib.gdn_gated_bwd_workspace_size(n, T, 2048, 1) > 0
+        assert lib.gdn_conv_bwd_workspace_size(n, T, 2048, 4, 1) > 0 and lib.gdn_ssm_saved_size(n, T, 2048, 16, 1) > 0
+        assert lib.gdn_ssm_bwd_workspace_size(n, T, 2048, 1, 16, 1) > 0
+    # dense rows of as many tokens each are too many
+    assert window(4096, 1 << 17, 16, 4, 128, 1024, 4, 0) == 0 and rope(2048, 1 << 20, 16, 4, 128, 0) == 0
+    assert lib.gdn_gated_saved_size(4096, 1 << 17, 2048, 0) == 0 and lib.gdn_conv_bwd_workspace_size(4096, 1 << 17, 2048, 4, 0) == 0
+    # and so is a pack that is too long by itself
+    assert lib.gdn_gated_saved_size(1, 1 << 29, 65536, 1) == 0 and window(1, (1 << 30) + 1, 1, 1, 64, 9, 0, 1) == 0
+    # the calls look at the same limit: a missing input is what they name
+    N, T, cu = 4096, 1 << 17, FAKE
+    assert lib.gdn_gated_fwd(None, 2048, FAKE, 2048, FAKE, 2048, FAKE, 8.0, None, cu, FAKE, None, None, 0, N, T, 2048, 0, None) == 1
+    assert lib.gdn_rope_fwd(None, 2048, FAKE, 512, None, None, FAKE, None, cu, FAKE, FAKE, 2048, 1 << 20, 16, 4, 128, 64, 0, 1e-6, 0, None) == 1
+    assert lib.gdn_window_fwd(None, 2048, FAKE, 512, FAKE, 512, cu, FAKE, None, N, T, 16, 4, 128, 1024, 4, 0.1, None) == 1
+    assert lib.gdn_window_fill(None, 512, FAKE, 512, cu, None, FAKE, FAKE, N, T, N, 4, 128, 1024, 4, None) == 1
+    assert lib.gdn_conv_fwd(FAKE, 2048, None, None, None, cu, FAKE, None, N, T, 2048, 4, 1, 0, None) == 1

@@ -269,3 +269,39 @@ def test_queries_that_are_not_finite():
     out = attention.window_attention_fwd(q, k, v, 4096)
     assert torch.isnan(out[0, 1000:3000]).all()
     assert torch.equal(out[0, :1000], good[0, :1000]) and torch.equal(out[0, 3000:], good[0, 3000:])
+
+
+def test_many_sequences_in_a_long_pack():
+    """4096 sequences in 2^17 tokens: every operator that packs them, and of its
+    results the sequences at the ends and some in between."""
+    n, T, D = 4096, 1 << 17, 2048
+    rng = np.random.default_rng(9)
+    cu = np.concatenate([[0], np.sort(rng.choice(np.arange(1, T), n - 1, replace=False)), [T]])
+    some = [0, 1, 1000, 2047, 3500, 4094, 4095]
+    rows = np.concatenate([np.arange(cu[s], cu[s + 1]) for s in some])
+    few = np.concatenate([[0], np.cumsum([cu[s + 1] - cu[s] for s in some])]).tolist()
+    pick = lambda t: _np(t[:, torch.from_numpy(rows).cuda()])  # noqa: E731
+    tc = _ints(cu)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    x, r, i = (torch.randn(1, T, D, device="cuda", generator=gen).to(BF) for _ in range(3))
+    lam = _round(rng.uniform(-4, -1, D), F32)
+    h0, w = torch.randn(n, D, device="cuda", generator=gen), torch.randn(D, 4, device="cuda", generator=gen)
+    y, fs = mixer.gated_scan_fwd(x, r, i, _dev(lam), initial_state=h0, cu_seqlens=tc)
+    want, end = M.gated_fwd(pick(x), pick(r), pick(i), lam, h0=_np(h0[some]), cu=few)
+    _close(torch.from_numpy(pick(y)), want, TOL_BF16, "recurrence")
+    _close(fs[some], end, TOL_F32, "state")
+    y, _ = mixer.short_conv_fwd(x, w, cu_seqlens=tc)
+    alone, _ = mixer.short_conv_fwd(x[:, torch.from_numpy(rows).cuda()].contiguous(), w, cu_seqlens=_ints(few))
+    assert np.array_equal(pick(y), _np(alone))
+    q = x.view(1, T, 16, 128)
+    k, v = (t.view(1, T, 16, 128)[:, :, :4].contiguous() for t in (r, i))
+    out, lse = attention.window_attention_fwd(q, k, v, 20, 2, cu_seqlens=tc, save_for_backward=True)
+    g = attention.window_attention_bwd(q, k, v, out, lse, q, 20, 2, cu_seqlens=tc)
+    a = [pick(t) for t in (q, k, v)]
+    _close(torch.from_numpy(pick(out)), A.window_fwd(*a, 20, 2, cu=few)[0], TOL_BF16, "attention")
+    for name, want in A.window_bwd(*a, a[0], 20, 2, cu=few).items():
+        _close(torch.from_numpy(pick(g[name])), want, TOL_GRAD, name)
+    f = np.float32(10000.0) ** (-np.arange(64, dtype=np.float32) / 64)
+    tq, _ = attention.qk_norm_rope_fwd(q, k, inv_freq=_dev(f), cu_seqlens=tc)
+    _close(torch.from_numpy(pick(tq)), A.rope_fwd(a[0], None, f, A.positions_of(a[0], few)), TOL_BF16, "rotation")
+    assert gdn.gdn_get_last_device_error() == 0
