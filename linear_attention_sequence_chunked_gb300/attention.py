@@ -7,8 +7,8 @@ As in mixer.py, nothing is computed here: arguments are checked and handed to
 the CUDA kernels of ``_build/libgdn.so`` (include/gdn.h has the formulas and
 layouts), without a CPU fallback.  ``*_fwd`` / ``*_bwd`` are the explicit forms
 and take `stream=`, in place of the current stream; the others are the same
-behind torch.autograd (first derivatives only).  All tensors are on the current
-device.
+behind torch.autograd (first derivatives in reverse mode only).  All tensors are
+on the current device.
 """
 
 from __future__ import annotations
@@ -17,7 +17,7 @@ import torch
 
 from ._first_order import first_order
 from .gdn import _check, _on_stream, _workspace, load
-from .mixer import _aligned, _current, _dense, _dtype, _is, _new, _on_gpu, _out, _rows, _sequences
+from .mixer import _aligned, _current, _dense, _differentiated, _dtype, _is, _new, _on_gpu, _out, _rows, _sequences
 
 _BF16 = torch.bfloat16
 HEAD_SIZES = (32, 64, 128, 256)
@@ -304,6 +304,6 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, inv_freq=None, positions=No
 def window_attention(q, k, v, window, sinks=0, scale=None, cu_seqlens=None):
     """window_attention_fwd with autograd (q, k, v).  The rows' sums are kept
     where a backward can follow."""
-    if not (torch.is_grad_enabled() and any(t.requires_grad for t in (q, k, v))):
+    if not _differentiated(q, k, v):
         return window_attention_fwd(q, k, v, window, sinks, scale, cu_seqlens)
     return _functions()["window"].apply(q, k, v, window, sinks, scale, cu_seqlens)

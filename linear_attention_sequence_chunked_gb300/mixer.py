@@ -6,8 +6,8 @@ As in gdn.py, nothing is computed here: arguments are checked and handed to
 the CUDA kernels of ``_build/libgdn.so`` (include/gdn.h has the formulas and
 layouts), without a CPU fallback.  ``*_fwd`` / ``*_bwd`` / ``*_step`` allocate
 their outputs and workspaces with torch; short_conv, ssm_scan, gated_scan and group_norm
-are the same forwards and backwards behind torch.autograd (first derivatives
-only: a second one raises).  The former also
+are the same forwards and backwards behind torch.autograd (first derivatives in
+reverse mode only: a second one and forward mode raise).  The former also
 take `stream=`, in place of the current stream; as with any stream, the caller
 has it wait for what produces the inputs.  All tensors are on the current device.
 
@@ -21,6 +21,7 @@ start at a 16-byte boundary; a state cache that a step updates does.
 from __future__ import annotations
 
 import torch
+from torch.autograd import forward_ad
 
 from ._first_order import first_order
 from .gdn import _check, _on_stream, _workspace, load
@@ -637,6 +638,17 @@ def _functions():
     return _FUNCTIONS
 
 
+def _differentiated(*tensors):
+    """Whether a call on these takes its autograd function: a backward can follow it,
+    or one is a dual tensor, which carries its tangent without requires_grad and
+    under no_grad too (the functions have no forward mode, and say so)."""
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+        return True
+    # (outside of a dual level, -1, nothing is dual; a torch without the number looks at each tensor)
+    return getattr(forward_ad, "_current_level", 0) >= 0 and any(
+        t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors)
+
+
 def short_conv(x, weight, bias=None, activation="silu", initial_state=None, cu_seqlens=None):
     """short_conv_fwd with autograd (x, weight, bias, initial_state).  Returns
     (y, final_state)."""
@@ -647,8 +659,7 @@ def ssm_scan(u, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=True, ini
     """ssm_scan_fwd with autograd (every tensor but cu_seqlens).  Returns
     (out, final_state).  The states for the backward are kept where one can
     follow: some input needs a gradient and grad mode is on."""
-    if not (torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in
-                                            (u, dt, A, B, C, D, z, dt_bias, initial_state))):
+    if not _differentiated(u, dt, A, B, C, D, z, dt_bias, initial_state):
         return ssm_scan_fwd(u, dt, A, B, C, D, z, dt_bias, dt_softplus, initial_state, cu_seqlens)
     return _functions()["scan"].apply(u, dt, A, B, C, D, z, dt_bias, initial_state, dt_softplus, cu_seqlens)
 
@@ -656,7 +667,7 @@ def ssm_scan(u, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=True, ini
 def gated_scan(x, r, i, lam, rate=8.0, initial_state=None, cu_seqlens=None):
     """gated_scan_fwd with autograd (x, r, i, lam, initial_state).  Returns (h,
     final_state).  The states for the backward are kept where one can follow."""
-    if not (torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, r, i, lam, initial_state))):
+    if not _differentiated(x, r, i, lam, initial_state):
         return gated_scan_fwd(x, r, i, lam, rate, initial_state, cu_seqlens)
     return _functions()["gated"].apply(x, r, i, lam, initial_state, rate, cu_seqlens)
 

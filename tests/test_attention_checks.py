@@ -385,3 +385,29 @@ def test_packs_of_many_sequences(lib):
     assert lib.gdn_window_fwd(None, 2048, FAKE, 512, FAKE, 512, cu, FAKE, None, N, T, 16, 4, 128, 1024, 4, 0.1, None) == 1
     assert lib.gdn_window_fill(None, 512, FAKE, 512, cu, None, FAKE, FAKE, N, T, N, 4, 128, 1024, 4, None) == 1
     assert lib.gdn_conv_fwd(FAKE, 2048, None, None, None, cu, FAKE, None, N, T, 2048, 4, 1, 0, None) == 1
+
+
+FORWARD_MODE = {
+    "gated": (lambda x, r, i, lam, h: mixer.gated_scan(x, r, i, lam, initial_state=h),
+              dict(x=_z(2, 4, 8), r=_z(2, 4, 8), i=_z(2, 4, 8), lam=torch.zeros(8), h=torch.zeros(2, 8))),
+    "ssm": (lambda u, dt, A, B, C, D, z, b, h: mixer.ssm_scan(u, dt, A, B, C, D, z, b, initial_state=h),
+            dict(u=_z(2, 4, 8), dt=_z(2, 4, 8), A=torch.zeros(8, 8), B=_z(2, 4, 1, 8), C=_z(2, 4, 1, 8), D=torch.zeros(8), z=_z(2, 4, 8),
+                 b=torch.zeros(8), h=torch.zeros(2, 8, 8))),
+    "rope": (lambda q, k, w: attention.qk_norm_rope(q, k, w), dict(q=_z(2, 4, 2, 64), k=_z(2, 4, 1, 64), w=torch.zeros(64))),
+    "window": (lambda q, k, v: attention.window_attention(q, k, v, 3), dict(q=_z(2, 4, 2, 64), k=_z(2, 4, 1, 64), v=_z(2, 4, 1, 64))),
+}
+
+
+@pytest.mark.parametrize("grad", [True, False], ids=["grad", "no_grad"])
+@pytest.mark.parametrize("name", list(FORWARD_MODE))
+def test_forward_mode_is_refused(fake, name, grad):
+    """A dual tensor carries a derivative without requires_grad, under no_grad too: a
+    result without a tangent would count as constant."""
+    from torch.autograd import forward_ad
+    f, inputs = FORWARD_MODE[name]
+    with torch.set_grad_enabled(grad), forward_ad.dual_level():
+        f(**inputs)  # (nothing asks for a derivative)
+        for k, t in inputs.items():
+            with pytest.raises(NotImplementedError, match="forward mode"):
+                f(**{**inputs, k: forward_ad.make_dual(t, torch.ones_like(t))})
+    f(**inputs)
