@@ -221,7 +221,7 @@ def short_conv_bwd(x, weight, d_out, bias=None, activation="silu", initial_state
     nbytes = lib.gdn_conv_bwd_workspace_size(N, T, D, W, int(cu_seqlens is not None))
     ws = _workspace(nbytes, x.device)
     _check(lib.gdn_conv_bwd(*args, dout, dfs, res["dx"].data_ptr(), res["dweight"].data_ptr(), _out(res, "dbias"),
-                            _out(res, "d_initial_state"), *dims, ws.data_ptr(), nbytes, _current(dev)),
+                            _out(res, "d_initial_state"), *dims, None if ws is None else ws.data_ptr(), nbytes, _current(dev)),
            "gdn_conv_bwd")
     return res
 
@@ -358,7 +358,7 @@ def ssm_scan_bwd(u, dt, A, B, C, d_out, saved, D=None, z=None, dt_bias=None, dt_
     ws = _workspace(nbytes, u.device)
     out = [_out(res, k) for k in ("du", "ddt", "dz", "dB", "dC", "dA", "dD", "ddt_bias", "d_initial_state")]
     _check(lib.gdn_ssm_bwd(*args, cu, dout, dfs, saved.data_ptr(), saved.numel(), *out, nseq, T, *dims,
-                           ws.data_ptr(), nbytes, _current(dev)), "gdn_ssm_bwd")
+                           None if ws is None else ws.data_ptr(), nbytes, _current(dev)), "gdn_ssm_bwd")
     return res
 
 
@@ -455,7 +455,7 @@ def gated_scan_bwd(x, r, i, lam, d_out, saved, rate=8.0, initial_state=None, cu_
     ws = _workspace(nbytes, x.device)
     _check(lib.gdn_gated_bwd(*args, h0, cu, dout, dfs, saved.data_ptr(), saved.numel(), res["dx"].data_ptr(),
                              res["dr"].data_ptr(), res["di"].data_ptr(), res["dlam"].data_ptr(),
-                             _out(res, "d_initial_state"), nseq, T, D, dtype, ws.data_ptr(), nbytes, _current(dev)),
+                             _out(res, "d_initial_state"), nseq, T, D, dtype, None if ws is None else ws.data_ptr(), nbytes, _current(dev)),
            "gdn_gated_bwd")
     return res
 

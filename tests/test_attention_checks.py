@@ -411,3 +411,24 @@ def test_forward_mode_is_refused(fake, name, grad):
             with pytest.raises(NotImplementedError, match="forward mode"):
                 f(**{**inputs, k: forward_ad.make_dual(t, torch.ones_like(t))})
     f(**inputs)
+
+
+def test_an_empty_batch_is_the_librarys_refusal(monkeypatch, lib):
+    """Every form names the argument, none trips over the workspace that sizes like
+    these do not have."""
+    for m in (mixer, attention):
+        monkeypatch.setattr(m, "_on_gpu", lambda dev, x: None)
+        monkeypatch.setattr(m, "_current", lambda dev: 0)
+    x, lam, byte = _z(0, 4, 8), torch.zeros(8), torch.zeros(0, dtype=torch.uint8)
+    q, k, w = _z(0, 4, 2, 64), _z(0, 4, 1, 64), torch.zeros(64)
+    lse = torch.zeros(0, 2, 4)
+    for call in (lambda: mixer.gated_scan_fwd(x, x, x, lam), lambda: mixer.gated_scan_bwd(x, x, x, lam, x, byte),
+                 lambda: mixer.gated_scan_step(x[:, 0], x[:, 0], x[:, 0], lam, torch.zeros(2, 8)),
+                 lambda: mixer.short_conv_bwd(x, torch.zeros(8, 4), x),
+                 lambda: mixer.ssm_scan_bwd(x, x, torch.zeros(8, 8), _z(0, 4, 1, 8), _z(0, 4, 1, 8), x, byte),
+                 lambda: attention.qk_norm_rope_fwd(q, k, w), lambda: attention.qk_norm_rope_bwd(q, k, q, k, w),
+                 lambda: attention.window_attention_fwd(q, k, k, 3), lambda: attention.window_attention_bwd(q, k, k, q, lse, q, 3),
+                 lambda: attention.window_attention_step(q[:, 0], k[:, 0], k[:, 0], _z(2, 5, 1, 64), _z(2, 5, 1, 64), torch.zeros(0, dtype=torch.int32)),
+                 lambda: attention.window_cache_fill(k, k, _z(2, 5, 1, 64), _z(2, 5, 1, 64))):
+        with pytest.raises(gdn.GdnError, match="INVALID_ARG"):
+            call()
