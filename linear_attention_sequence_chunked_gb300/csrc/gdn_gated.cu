@@ -660,40 +660,38 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 ? 2 : 1) gated_bwd
 
 // ---------------------------------------------------------------- one token
 
-// Four channels a thread, each input and state once through registers; bound by the
-// launch (64 x 2048 bf16: 2.7 us inside a graph, 0.3 of bytes).
-template <typename T, int E, bool VEC>
+// Four channels a thread in accesses of all four, or, where widths, strides or
+// addresses do not allow it, one; each input and state once through registers.  Bound
+// by the launch (64 x 2048 bf16: 2.7 us inside a graph, 0.3 of bytes).
+template <typename T, int E>
 __global__ void __launch_bounds__(256) gated_step_kernel(const GatedStepArgs p) {
-    const int per = (p.D + E - 1) / E;
+    const int per = p.D / E;  // (E is one where it does not divide the width)
     const long long id = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
     const long long b = id / per;
     if (b >= p.B) return;
     const int d = static_cast<int>(id % per) * E;
-    const int nd = min(E, p.D - d);
     long long slot = b;
     if (p.slots) {
         slot = p.slots[b];
         if (slot >= p.S) record_error(p.err, kErrBadSlot);
     }
     const bool on = slot >= 0 && slot < p.S;
-    const int n = on ? nd : 0;
-    const Raw<float, E> rl = load_raw<float, E, VEC>(p.lam + d, nd);
-    const Raw<T, E> rr = load_raw<T, E, VEC>(static_cast<const T*>(p.r) + b * p.r_stride + d, n);
-    const Raw<T, E> ri = load_raw<T, E, VEC>(static_cast<const T*>(p.i) + b * p.i_stride + d, n);
-    const Raw<T, E> rx = load_raw<T, E, VEC>(static_cast<const T*>(p.x) + b * p.x_stride + d, n);
+    const int n = on ? E : 0;
+    const Raw<float, E> rl = load_raw<float, E>(p.lam + d, E);
+    const Raw<T, E> rr = load_raw<T, E>(static_cast<const T*>(p.r) + b * p.r_stride + d, n);
+    const Raw<T, E> ri = load_raw<T, E>(static_cast<const T*>(p.i) + b * p.i_stride + d, n);
+    const Raw<T, E> rx = load_raw<T, E>(static_cast<const T*>(p.x) + b * p.x_stride + d, n);
     Raw<float, E> h;  // not load_raw: the cache may be written in place
     const long long so = (on ? slot : 0) * p.D + d;
 #pragma unroll
     for (int e = 0; e < E; ++e) h.w[e] = 0;
     if (on) {
-        if constexpr (VEC && E == 4) {
+        if constexpr (E == 4) {
             const float4 v = *reinterpret_cast<const float4*>(p.state + so);
             h.w[0] = __float_as_uint(v.x); h.w[1] = __float_as_uint(v.y);
             h.w[2] = __float_as_uint(v.z); h.w[3] = __float_as_uint(v.w);
         } else {
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                if (e < nd) h.w[e] = __float_as_uint(p.state[so + e]);
+            h.w[0] = __float_as_uint(p.state[so]);
         }
     }
     float out[E];
@@ -706,8 +704,8 @@ __global__ void __launch_bounds__(256) gated_step_kernel(const GatedStepArgs p) 
         split(gap, m0, skip);
         out[e] = on ? fmaf(a0, h.get(e), root(m0) * (sigmoid(ri.get(e)) * rx.get(e))) : 0.f;
     }
-    if (on) store_raw<float, E, VEC>(p.out_state + so, pack<float, E>(out), nd);
-    store_raw<T, E, VEC>(static_cast<T*>(p.y) + b * p.D + d, pack<T, E>(out), nd);
+    if (on) store_raw<float, E>(p.out_state + so, pack<float, E>(out), E);
+    store_raw<T, E>(static_cast<T*>(p.y) + b * p.D + d, pack<T, E>(out), E);
 }
 
 // ---------------------------------------------------------------- launches
@@ -796,9 +794,9 @@ cudaError_t launch_step(const GatedStepArgs& a, cudaStream_t stream) {
     const long long n = static_cast<long long>(a.B) * (vec ? a.D / 4 : a.D);
     const unsigned blocks = static_cast<unsigned>((n + 255) / 256);
     if (vec)
-        gated_step_kernel<T, 4, true><<<blocks, 256, 0, stream>>>(a);
+        gated_step_kernel<T, 4><<<blocks, 256, 0, stream>>>(a);
     else
-        gated_step_kernel<T, 1, true><<<blocks, 256, 0, stream>>>(a);
+        gated_step_kernel<T, 1><<<blocks, 256, 0, stream>>>(a);
     return cudaGetLastError();
 }
 }  // namespace
