@@ -719,8 +719,9 @@ GDN_API gdn_status gdn_window_fwd(const gdn_bf16* q, int64_t q_stride, const gdn
  * Reverse mode of gdn_window_fwd from its inputs, its out and its lse: d_out
  * (B,T,H,d) in; dq (B,T,H,d), dk and dv (B,T,Hk,d) out, dense.  The gradients
  * of a key head are summed over its query heads in a fixed order.  A NaN or an
- * infinity stays in its sequence, but may reach tokens of it up to 128 away
- * that do not see it.
+ * infinity stays in its sequence, but may reach gradients there that its token
+ * has no part in, by places of the same tiles of 128: of tokens up to 127 away, or
+ * up to 254 beyond the window's distance.
  */
 GDN_API size_t gdn_window_bwd_workspace_size(int B, int T, int H, int Hk, int d, int window, int sinks, int varlen);
 GDN_API gdn_status gdn_window_bwd(const gdn_bf16* q, int64_t q_stride, const gdn_bf16* k, int64_t k_stride,

@@ -501,7 +501,8 @@ struct QSmem {
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     window_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-                     const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_g, const WindowArgs p) {
+                     const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_g, const __grid_constant__ CUtensorMap map_k_first,
+                     const WindowArgs p) {
     using L = QSmem<D>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = smem_raw + smem_align_pad(smem_raw);
@@ -516,6 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_prefetch_desc(&map_k);
         tma_prefetch_desc(&map_v);
         tma_prefetch_desc(&map_g);
+        tma_prefetch_desc(&map_k_first);
     }
     const int h = blockIdx.x % p.H, hk = h / (p.H / p.Hk);
     const long long slot = p.slots - 1 - blockIdx.x / p.H;  // late tiles, with the most keys, first
@@ -561,7 +563,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int j0 = blk.start(j), st = j & 1, ph = ((j >> 1) & 1) ^ 1;
             const int row = static_cast<int>(row0 + j0);
             ok = j < 3 || wait(qKFree + j % 3, (j / 3 & 1) ^ 1);
-            if (ok) ok = load_tile<D>(sm + L::k + j % 3 * L::kTileBytes, &map_k, hk, row, min(kTile, len - j0), bar(qK + j % 3), bar(qTail), tails, lane);
+            if (ok && blk.first > 0 && j == 0)  // of the first tokens' block they alone
+                load_first<D>(sm + L::k, &map_k_first, hk, row, p.sinks, blk.first, bar(qK), lane);
+            else if (ok)
+                ok = load_tile<D>(sm + L::k + j % 3 * L::kTileBytes, &map_k, hk, row, min(kTile, len - j0), bar(qK + j % 3), bar(qTail), tails, lane);
             if (!ok) break;
             lk = j + 1;
             ok = j < 2 || wait(qVFree + st, ph);
@@ -703,11 +708,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int D>
 cudaError_t launch(const WindowArgs& a, cudaStream_t stream) {
-    CUtensorMap mq, mk, mv, mg;
+    CUtensorMap mq, mk, mv, mg, mf;
     if (!make_heads_map(&mq, a.q, a.tokens, a.q_stride, a.H, D, kTile) ||
         !make_heads_map(&mk, a.k, a.tokens, a.k_stride, a.Hk, D, kTile) ||
         !make_heads_map(&mv, a.v, a.tokens, a.v_stride, a.Hk, D, kTile) ||
-        !make_heads_map(&mg, a.d_out, a.tokens, static_cast<long long>(a.H) * D, a.H, D, kTile))
+        !make_heads_map(&mg, a.d_out, a.tokens, static_cast<long long>(a.H) * D, a.H, D, kTile) ||
+        !make_heads_map(&mf, a.k, a.tokens, a.k_stride, a.Hk, D, a.sinks > 0 ? a.sinks : kTile))
         return cudaErrorInvalidValue;
     static std::atomic<uint64_t> done_kv{0}, done_q{0};
     cudaError_t e = allow_once(window_dkv_kernel<D>, KvSmem<D>::total, false, done_kv);
@@ -724,7 +730,7 @@ cudaError_t launch(const WindowArgs& a, cudaStream_t stream) {
         const long long ids = static_cast<long long>(a.nseq) * a.Hk * 2 * a.sinks * D;
         window_join_kernel<<<static_cast<unsigned>((ids + 255) / 256), 256, 0, stream>>>(a);
     }
-    window_dq_kernel<D><<<static_cast<unsigned>(a.slots * a.H), kThreads, QSmem<D>::total, stream>>>(mq, mk, mv, mg, a);
+    window_dq_kernel<D><<<static_cast<unsigned>(a.slots * a.H), kThreads, QSmem<D>::total, stream>>>(mq, mk, mv, mg, mf, a);
     return cudaGetLastError();
 }
 

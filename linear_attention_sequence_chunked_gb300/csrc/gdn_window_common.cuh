@@ -158,13 +158,13 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
     return false;
 }
 
-// Zeros in the rows of a swizzled tile from `from` on: they belong to another
-// sequence (or to nobody), and 0 times what they hold need not be zero.
+// Zeros in the rows [from, to) of a swizzled tile: they belong to another sequence
+// (or to nobody), and 0 times what they hold need not be zero.
 template <int D>
-__device__ __forceinline__ void clear_rows(uint8_t* tile, int from, int lane) {
+__device__ __forceinline__ void clear_rows(uint8_t* tile, int from, int to, int lane) {
 #pragma unroll
     for (int s = 0; s < D / 64; ++s)
-        for (int o = from * 128 + lane * 16; o < kSlab; o += 512) *reinterpret_cast<uint4*>(tile + s * kSlab + o) = make_uint4(0, 0, 0, 0);
+        for (int o = from * 128 + lane * 16; o < to * 128; o += 512) *reinterpret_cast<uint4*>(tile + s * kSlab + o) = make_uint4(0, 0, 0, 0);
 }
 
 // A tile of one head by TMA, onto barrier `full`; one that ends behind its
@@ -183,12 +183,29 @@ __device__ __forceinline__ bool load_tile(uint8_t* tile, const CUtensorMap* map,
     if (valid < kTile) {
         if (!__all_sync(0xffffffffu, mbar_wait(tail, tails & 1))) return false;
         ++tails;
-        clear_rows<D>(tile, valid, lane);
+        clear_rows<D>(tile, valid, kTile, lane);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(full);
     }
     return true;
+}
+
+// The first tokens alone (`map` has boxes of that many), zeros behind them up to the
+// block's width: nobody who looks at this block sees what lies there.  Into a place that
+// nothing has used yet.  Whole warp.
+template <int D>
+__device__ __forceinline__ void load_first(uint8_t* tile, const CUtensorMap* map, int head, int row, int sinks, int width, uint32_t full,
+                                           int lane) {
+    clear_rows<D>(tile, sinks, width, lane);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+        mbar_arrive_expect_tx(full, sinks * 128 * (D / 64));
+#pragma unroll
+        for (int s = 0; s < D / 64; ++s) tma_load_3d(smem_u32(tile + s * kSlab), map, 64 * s, head, row, full);
+    }
+    __syncwarp();
 }
 
 // {64 channels, 1 head, `box` tokens} of (tokens, heads, d) bf16, tokens `stride`

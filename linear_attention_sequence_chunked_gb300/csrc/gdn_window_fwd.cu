@@ -21,7 +21,7 @@
 // them: tensor memory holds two tiles' S and O and no third.
 //
 // A masked place has P = 0, and 0 times a NaN or an infinity in V would not be
-// zero: rows behind the sequence are cleared in V's tiles, and queries that end up
+// zero: rows behind the sequence and behind the first tokens are cleared in V's tiles, and queries that end up
 // non-finite are computed again from the keys they see.
 #include <cmath>
 
@@ -92,7 +92,7 @@ __device__ __noinline__ void one_row(const WindowArgs& p, long long row0, int i,
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     window_fwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-                      const __grid_constant__ CUtensorMap map_v, const WindowArgs p) {
+                      const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_v_first, const WindowArgs p) {
     using L = Smem<D>;
     constexpr int kSlabs = D / 64;
     extern __shared__ uint8_t smem_raw[];
@@ -108,6 +108,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_prefetch_desc(&map_q);
         tma_prefetch_desc(&map_k);
         tma_prefetch_desc(&map_v);
+        tma_prefetch_desc(&map_v_first);
     }
 
     // the two tiles: heads h and h + 1 of one tile, or two tiles of head h
@@ -171,8 +172,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 loaded_k = j + 1;
                 ok = j < 2 || wait(bVFree + st, ph);
-                if (ok) ok = load_tile<D>(sm + L::v + st * L::kTileBytes, &map_v, hk, row, min(kTile, len - blk.start(j)), bar(bV + st),
-                                          bar(bTail), tails, lane);
+                if (ok && blk.first > 0 && j == 0)  // of the first tokens' block they alone
+                    load_first<D>(sm + L::v + st * L::kTileBytes, &map_v_first, hk, row, p.sinks, blk.first, bar(bV + st), lane);
+                else if (ok)
+                    ok = load_tile<D>(sm + L::v + st * L::kTileBytes, &map_v, hk, row, min(kTile, len - blk.start(j)), bar(bV + st),
+                                      bar(bTail), tails, lane);
                 if (!ok) break;
                 loaded_v = j + 1;
             }
@@ -374,11 +378,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int D>
 cudaError_t launch(const WindowArgs& a, cudaStream_t stream) {
-    CUtensorMap mq, mk, mv;
+    CUtensorMap mq, mk, mv, mf;
     const long long tokens = a.cu_seqlens ? a.T : static_cast<long long>(a.nseq) * a.T;
     if (!make_heads_map(&mq, a.q, tokens, a.q_stride, a.H, D, kTile) ||
         !make_heads_map(&mk, a.k, tokens, a.k_stride, a.Hk, D, kTile) ||
-        !make_heads_map(&mv, a.v, tokens, a.v_stride, a.Hk, D, kTile))
+        !make_heads_map(&mv, a.v, tokens, a.v_stride, a.Hk, D, kTile) ||
+        !make_heads_map(&mf, a.v, tokens, a.v_stride, a.Hk, D, a.sinks > 0 ? a.sinks : kTile))
         return cudaErrorInvalidValue;
     static std::atomic<uint64_t> done{0};
     if (!done.load(std::memory_order_acquire)) {
@@ -390,7 +395,7 @@ cudaError_t launch(const WindowArgs& a, cudaStream_t stream) {
     const cudaError_t e = allow_once(window_fwd_kernel<D>, Smem<D>::total, false, done);
     if (e != cudaSuccess) return e;
     const int units = (a.H / a.Hk) % 2 == 0 ? a.H / 2 : a.H;
-    window_fwd_kernel<D><<<static_cast<unsigned>(a.slots * units), kThreads, Smem<D>::total, stream>>>(mq, mk, mv, a);
+    window_fwd_kernel<D><<<static_cast<unsigned>(a.slots * units), kThreads, Smem<D>::total, stream>>>(mq, mk, mv, mf, a);
     return cudaGetLastError();
 }
 

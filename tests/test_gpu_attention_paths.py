@@ -305,3 +305,20 @@ def test_many_sequences_in_a_long_pack():
     tq, _ = attention.qk_norm_rope_fwd(q, k, inv_freq=_dev(f), cu_seqlens=tc)
     _close(torch.from_numpy(pick(tq)), A.rope_fwd(a[0], None, f, A.positions_of(a[0], few)), TOL_BF16, "rotation")
     assert gdn.gdn_get_last_device_error() == 0
+
+
+def test_a_nan_behind_the_first_tokens_stays_near():
+    """The block of first tokens is as wide as a multiple of 32: what else lies in it
+    has no part in the gradients of queries that are far away, nor in their outputs."""
+    rng = np.random.default_rng(5)
+    W, S, T = 100, 4, 900
+    a = {n: _round(rng.standard_normal((1, T, h, 64)), BF) for n, h in (("q", 4), ("k", 2), ("v", 2), ("g", 4))}
+    t = {n: _dev(x, BF) for n, x in a.items()}
+    for n in "kv":
+        t[n][0, S:32] = float("nan")
+    out, lse = attention.window_attention_fwd(t["q"], t["k"], t["v"], W, S, save_for_backward=True)
+    r = attention.window_attention_bwd(t["q"], t["k"], t["v"], out, lse, t["g"], W, S)
+    far = slice(31 + W + 254, None)
+    _close(out[:, far], A.window_fwd(a["q"], a["k"], a["v"], W, S)[0][:, far], TOL_BF16, "out")
+    _close(r["dq"][:, far], A.window_bwd(a["q"], a["k"], a["v"], a["g"], W, S)["dq"][:, far], TOL_GRAD, "dq")
+    assert gdn.gdn_get_last_device_error() == 0
