@@ -29,6 +29,7 @@
 #include "gdn_kernels.h"
 #include "gdn_launch.h"
 #include "gdn_mix_common.cuh"
+#include "gdn_mma.cuh"
 
 namespace gdn {
 
@@ -42,23 +43,6 @@ constexpr int kKeys = 16;  // of a warp's step
 // and heads of a call are too few for that.
 constexpr int kFew = 6, kMany = 12;
 
-__device__ __forceinline__ void mma_16x8x16(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void mma_16x8x8(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint32_t tf32_of(float x) {
-    uint32_t r;
-    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
-    return r;
-}
 __device__ __forceinline__ uint32_t pair_of(float a, float b) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
@@ -169,8 +153,8 @@ __global__ void __launch_bounds__(32 * kWarps, 12 / kWarps) window_step_kernel(c
             const uint32_t a0[4] = {q0.x, q0.y, q0.z, q0.w}, a1[4] = {q1.x, q1.y, q1.z, q1.w};
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
-                mma_16x8x16(sc[n], a0, kr[n][c].x, kr[n][c].y);
-                mma_16x8x16(sc[n], a1, kr[n][c].z, kr[n][c].w);
+                mma::bf16_16x8x16(sc[n], a0, kr[n][c].x, kr[n][c].y);
+                mma::bf16_16x8x16(sc[n], a1, kr[n][c].z, kr[n][c].w);
             }
         }
         load_keys(s + kWarps);
@@ -198,7 +182,7 @@ __global__ void __launch_bounds__(32 * kWarps, 12 / kWarps) window_step_kernel(c
                 l[x] += v[e];
             }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) pa[e >> 1][x + 2 * (e & 1)] = tf32_of(v[e]);
+            for (int e = 0; e < 4; ++e) pa[e >> 1][x + 2 * (e & 1)] = mma::tf32(v[e]);
             if (__any_sync(0xffffffffu, f != 1.f)) {  // (the products behind it take the whole warp)
 #pragma unroll
                 for (int i = 0; i < D / 8; ++i) {
@@ -209,13 +193,11 @@ __global__ void __launch_bounds__(32 * kWarps, 12 / kWarps) window_step_kernel(c
         }
 #pragma unroll
         for (int c = 0; c < CH / 2; ++c) {
-            const uint32_t w[4][4] = {{vr[0][c].x, vr[0][c].y, vr[0][c].z, vr[0][c].w}, {vr[1][c].x, vr[1][c].y, vr[1][c].z, vr[1][c].w},
-                                      {vr[2][c].x, vr[2][c].y, vr[2][c].z, vr[2][c].w}, {vr[3][c].x, vr[3][c].y, vr[3][c].z, vr[3][c].w}};
 #pragma unroll
             for (int j = 0; j < 8; ++j) {  // column g is channel 64 c + 8 g + j
-                const auto channel = [&](int n) { return j & 1 ? w[n][j / 2] & 0xffff0000u : w[n][j / 2] << 16; };
-                mma_16x8x8(o[8 * c + j], pa[0], channel(0), channel(1));
-                mma_16x8x8(o[8 * c + j], pa[1], channel(2), channel(3));
+                const auto channel = [&](int n) { return mma::widen(mma::word(vr[n][c], j / 2), j & 1); };
+                mma::tf32_16x8x8(o[8 * c + j], pa[0], channel(0), channel(1));
+                mma::tf32_16x8x8(o[8 * c + j], pa[1], channel(2), channel(3));
             }
         }
         load_values(s + kWarps);

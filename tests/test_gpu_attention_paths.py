@@ -307,6 +307,68 @@ def test_many_sequences_in_a_long_pack():
     assert gdn.gdn_get_last_device_error() == 0
 
 
+@pytest.mark.parametrize("B,T,H,Hk,d,W,S,cu", [
+    (1, 700, 4, 2, 128, 200, 5, None),
+    (2, 520, 3, 1, 64, 129, 33, None),   # two tiles of a head
+    (1, 900, 2, 1, 64, 900, 0, None),    # the window is everything
+    (1, 640, 2, 2, 128, 1, 3, None),     # itself and the first tokens
+    (1, 800, 5, 1, 128, 70, 128, [0, 3, 300, 300, 431, 800]),
+], ids=str)
+def test_what_is_not_finite_reaches_its_readers_alone(B, T, H, Hk, d, W, S, cu):
+    """Value by value: NaN and infinities of either sign at random places, each in a
+    channel of its own or shared, and in whole rows.  An output is NaN, an infinity or
+    its definition's number by what its token sees of that channel."""
+    rng = np.random.default_rng(T + W)
+    q, k, v = (_round(rng.standard_normal((B, T, h, d)), BF) for h in (H, Hk, Hk))
+    bad = v.copy()
+    for x in (np.nan, np.inf, -np.inf):
+        for c in (0, 7, d - 1, *rng.integers(0, d, 3)):
+            for n in range(3):
+                bad[rng.integers(B), rng.integers(T), rng.integers(Hk), c] = x
+    bad[0, -40] = np.nan
+    bad[B - 1, T - 60, 0] = np.inf
+    out, lse = attention.window_attention_fwd(_dev(q, BF), _dev(k, BF), _dev(bad, BF), W, S, cu_seqlens=_ints(cu), save_for_backward=True)
+    want, want_lse = A.window_fwd(q, k, v, W, S, cu=cu)
+    got, kind = _np(out), np.zeros(want.shape, int)  # 1: inf, 2: -inf, 3: both or a NaN
+    for b, t0, t1 in A.rows_of(q, cu):
+        i, j = np.arange(t1 - t0)[:, None], np.arange(t1 - t0)[None]
+        see = ((j <= i) & ((i - j < W) | (j < S))).astype(float)
+        for h in range(H):
+            x = bad[b, t0:t1, h // (H // Hk)]
+            nan, up, down = (see @ f.astype(float) > 0 for f in (np.isnan(x), x == np.inf, x == -np.inf))
+            kind[b, t0:t1, h] = np.where(nan | (up & down), 3, np.where(up, 1, np.where(down, 2, 0)))
+    assert np.array_equal(np.isnan(got), kind == 3) and np.array_equal(got == np.inf, kind == 1) and np.array_equal(got == -np.inf, kind == 2)
+    assert (kind == 0).mean() > 0.2 and all((kind == x).any() for x in (1, 2, 3))
+    fine = kind == 0
+    _close(np.where(fine, got, 0), np.where(fine, want, 0), TOL_BF16, "the finite ones")
+    _close(lse, want_lse, TOL_PAR, "lse")
+    assert gdn.gdn_get_last_device_error() == 0
+
+
+@pytest.mark.parametrize("W,S,places", [(4096, 0, [0]), (4096, 0, [5, 2000]), (512, 4, [5]), (4096, 0, slice(None)), (4096, 0, slice(0, None, 300))],
+                         ids=str)
+def test_a_nan_does_not_slow_its_readers(W, S, places):
+    """Outputs are formed again where a value that is not seen spoils them, not where
+    one that is seen does: well below ten times the time of finite values, where
+    walking over every reader's keys took a thousand times it."""
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    q, k, v = (torch.randn(1, 8192, h, 128, device="cuda", generator=gen).to(BF) for h in (16, 4, 4))
+    bad = v.clone()
+    bad[0, places, :, 3] = float("nan")
+
+    def ms(x):
+        best = float("inf")
+        for _ in range(3):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            attention.window_attention_fwd(q, k, x, W, S)
+            b.record()
+            b.synchronize()
+            best = min(best, a.elapsed_time(b))
+        return best
+    assert ms(bad) < 10 * ms(v)
+
+
 def test_a_nan_behind_the_first_tokens_stays_near():
     """The block of first tokens is as wide as a multiple of 32: what else lies in it
     has no part in the gradients of queries that are far away, nor in their outputs."""
