@@ -674,8 +674,8 @@ GDN_API gdn_status gdn_gated_step(const void* x, int64_t x_stride, const void* r
  *   q_out (B,T,H,d), k_out (B,T,Hk,d), dense
  *   d in {32, 64, 128, 256}; pairs a multiple of 4, at most d / 2; H, Hk <= 1024;
  *   fewer than 2^31 tokens
- * The angle is exact to about 2^-26 turns at any position: p inv_freq is formed
- * from the fp32 frequency in 64-bit fixed point.
+ * The angle is exact to about 2^-26 turns at any position for frequencies up to
+ * 128: p inv_freq is formed from the fp32 frequency in 64-bit fixed point.
  */
 GDN_API gdn_status gdn_rope_fwd(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
                                 const float* q_weight, const float* k_weight, const float* inv_freq,
@@ -706,7 +706,7 @@ GDN_API gdn_status gdn_rope_bwd(const void* q, int64_t q_stride, const void* k, 
  *   lse       NULL, or fp32 (B,H,T) (packed: (1,H,T)): the log of the sum of
  *             exp(scale q_i . k_j) over the keys that token i sees
  *   window >= 1, scale > 0, 0 <= sinks <= 128, H a multiple of Hk, H <= 1024,
- *   d in {64, 128}, fewer than 2^31 - 256 tokens
+ *   H d <= 65536, d in {64, 128}, fewer than 2^31 - 256 tokens
  * A token that another does not see has no part in that one's output, whatever
  * it holds (NaN and infinities included).
  */
@@ -750,7 +750,7 @@ GDN_API gdn_status gdn_window_step(const gdn_bf16* q, int64_t q_stride, const gd
  * What prompts leave in such caches: of each sequence's keys and values (B,T,
  * Hk,d) (strided, on 16-byte boundaries) the rows that its next token looks at.
  * Rows that hold no token keep what they have.  slots (B or, packed, N): the
- * cache of each sequence, negative for none; NULL: cache n.
+ * cache of each sequence, negative for none, no two the same; NULL: cache n.
  */
 GDN_API gdn_status gdn_window_fill(const gdn_bf16* k, int64_t k_stride, const gdn_bf16* v, int64_t v_stride,
                                    const int32_t* cu_seqlens, const int32_t* slots, gdn_bf16* k_cache,

@@ -16,12 +16,16 @@
 // memory.  The cluster then takes the next stretch, with the state it ended in.
 // All compositions run in a fixed order.
 //
-// Bound by instruction issue, not by HBM, which would move the bytes in 40 us: 4 x
-// 4096 x 2048 bf16 take 65 us forward (4.1 TB/s; 35 instructions per element and
-// lane pair, 26 of them the formulas' own) and 136 reverse (3.4 TB/s), 1 x 65536 x
-// 1024 152 and 321.  Sixteen tokens a strip forward and eight in reverse are what
-// fits 128 registers, two blocks an SM; four warps a block took 106 us and sixteen 83
-// where eight took 71.
+// HBM would move the bytes in 40 us; 4 x 4096 x 2048 bf16 take 66 us forward (4.1
+// TB/s) and 136 reverse (3.4 TB/s), 1 x 65536 x 1024 152 and 321.  What bounds them is
+// latency at few warps: 12.6 active an SM forward, with 53 % of the issue slots used
+// (35 instructions per element and lane pair, 26 of them the formulas' own), 46 % of
+// HBM's rate and 30 % of the exponential unit's; 13.8, 39 %, 28 % and 15 % in the
+// packed reverse.  Each round ends in the block's and the cluster's barrier with
+// nothing between arriving and waiting, and 256 blocks on 304 places leave 48 SMs with
+// one.  Sixteen tokens a strip forward and eight in reverse are what fits 128
+// registers, two blocks an SM; four warps a block took 106 us and sixteen 83 where
+// eight took 71.
 //
 // Packed sequences are one row: a sequence's first token starts from its own
 // initial state, and a strip that holds such a token ignores what comes in.  The

@@ -10,9 +10,10 @@
 // lanes takes a token, forms its angles and walks its heads; where tokens are
 // few, several teams share a token's heads.  Each row is read once and written
 // once: 4 x 4096 tokens of 20 heads of 128 bf16 take 36 us, 4.7 TB/s or 70 % of a
-// copy, and the gradients of 8191 tokens of 12 heads of 64 fp32 17, 4.4 TB/s.  What
-// is left is instruction issue and latency, 126 instructions per two rows: angles
-// kept in shared memory for a block's teams took 43 us.
+// copy, and the gradients of 8191 tokens of 12 heads of 64 fp32 18, 4.2 TB/s.  What
+// bounds it is latency: 15 warps an SM (128 registers) use 53 % of the issue slots
+// (126 instructions per two rows) and 39 % of HBM's rate.  Angles kept in shared
+// memory for a block's teams took 43 us.
 //
 // The angle p f is formed in turns, in fixed point: f / 2 pi as a 64-bit
 // fraction (24 bits of f times 64 bits of 1 / 2 pi), multiplied by the integer

@@ -17,8 +17,10 @@
 // 16384 tokens, 16 / 4 heads of 128, window 2048 take 496 us for dK and dV, 357 for
 // dQ, 25 for delta and 4 for the join.  A tile of dK and dV is 2560 clocks of
 // products in some 3300: dS, dK over it, dP in its place and dS again are a chain
-// (tensor memory holds S, dP and two accumulators, no second dP), and 544 equal
-// blocks leave a tenth of the last round's SMs idle.  A tile of dQ is 2048 in some
+// (tensor memory holds S, dP and two accumulators, no second dP), and 544 blocks, the
+// last tiles' of less work, in 3.6 rounds leave a fifth of the SMs' time idle: the
+// tensor pipe is active in 76 % of the cycles in which an SM is, in 61 % of the
+// kernel's.  A tile of dQ is 2048 in some
 // 2950: dP has two places and K three, so that nothing waits but the elementwise
 // work's own chain.  With eight warps for that work, one that issues all products
 // and two places of K the two kernels took 519 and 439 us.
@@ -741,9 +743,10 @@ cudaError_t launch(const WindowArgs& a, cudaStream_t stream) {
 // Gradients in us, one piece and as the rule has it, of 16 query heads of 128:
 // 1 x 512 tokens, 4 key heads (16 blocks in one piece) 44 and 34; 1 x 2048, 2 key
 // heads (32) 237 and 99; 1 x 4096, 2 key heads, window 1024 (64) 195 and 144, where
-// four pieces take 155.  Beyond the SMs pieces lose: 1 x 4096, 4 key heads (128
-// blocks) 136 in one, 161 in two.  What they cost where there is little to share:
-// 1 x 128 tokens, 4 key heads 21.6 and 24.
+// four pieces take 155.  With more blocks than half of the SMs it is one: 1 x 4096, 4
+// key heads (128 blocks) take 136 in one, 161 in two.  (The rule does not look at how a
+// last round of several fills: no other size beyond one round was measured.)  What
+// pieces cost where there is little to share: 1 x 128 tokens, 4 key heads 21.6 and 24.
 int window_pieces(long long slots, int H, int Hk) {
     const long long blocks = slots * Hk;
     return static_cast<int>(std::min<long long>(H / Hk, std::max(1ll, 152 / std::max(blocks, 1ll))));

@@ -19,9 +19,10 @@
 // are its column in eight products.  The warps of a block, and the blocks of a
 // cluster where the rows alone leave SMs idle, join their (maximum, sum, O) in a
 // fixed order through (distributed) shared memory.  64 rows of 1028 keys, 16 / 4
-// heads of 128, take 25 us, 4.8 TB/s: the latency of HBM with as many loads on
-// their way as the registers hold, 71 % of a copy.  One row of 16388 keys takes 13
-// on the sixteen blocks that a cluster may have.
+// heads of 128, take 26 us, 4.6 TB/s: the latency of HBM with as many loads on
+// their way as the registers hold, 69 % of a copy (the tensor pipe is active in 20 %
+// of the cycles).  One row of 16388 keys takes 14 on the sixteen blocks that a cluster
+// may have.
 #include <algorithm>
 #include <cmath>
 
@@ -38,9 +39,9 @@ namespace {
 using namespace mix;
 
 constexpr int kKeys = 16;  // of a warp's step
-// Warps of a block: six, two blocks to an SM (64 rows of 1028 keys, 4 key heads: 25
-// us; four warps and three blocks 29, twelve and one 31), or twelve where the rows
-// and heads of a call are too few for that.
+// Warps of a block: six, two blocks to an SM (64 rows of 1028 keys, 4 key heads, with
+// P in bf16: 25 us; four warps and three blocks 29, twelve and one 31), or twelve where
+// the rows and heads of a call are too few for that.
 constexpr int kFew = 6, kMany = 12;
 
 __device__ __forceinline__ uint32_t pair_of(float a, float b) {
